@@ -27,6 +27,15 @@
  *   moe_backward_kept   the backward that reads them instead of rerunning that GEMM
  *   moe_router_backward the router's backward: dlogits, dW_router, d bias
  *
+ * and, on either side of the layer in the same training or serving step (the last section):
+ *
+ *   moe_embed, moe_embed_backward            token embedding, its gradient by sorted tokens
+ *   moe_block_norm, moe_block_norm_backward  the norms before and after a block, with its
+ *                                            gates and the scaled residual
+ *   moe_head_loss, moe_head_loss_backward    softmax cross entropy over the vocabulary without
+ *                                            keeping the logits, and its gradients
+ *   moe_grad_norm, moe_grad_clip             the global norm of many gradients, and clipping
+ *
  * Conventions shared by every call:
  *  - Every data pointer is DEVICE memory owned by the caller; the library allocates
  *    nothing and frees nothing. Pointers must be 16-byte aligned.
@@ -466,6 +475,134 @@ moe_status_t moe_route_static_scratch(const moe_config_t* cfg, const float* logi
  * timeout_ns (0 < timeout_ns <= 10 s) and returns, and the context stays usable. */
 moe_status_t moe_selftest_bounded_wait(int64_t timeout_ns, int32_t* device_status,
                                        moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Around the layer: the other operators of a training or serving step. The conventions above
+ * hold (dense row-major matrices, 16-byte aligned device pointers unless stated otherwise,
+ * caller-owned buffers, no host sync, capturable). A workspace of these calls is initialised
+ * once with moe_workspace_init; moe_read_status reads its status word.
+ * --------------------------------------------------------------------------------------- */
+
+/* Block norms. T tokens of H channels (1 <= H <= 16384). */
+typedef struct {
+  int32_t T, H;
+  int32_t act_dtype; /* MOE_DTYPE_F32 or MOE_DTYPE_BF16: x, y, r, n and their gradients */
+  float eps;         /* > 0 */
+  float res_scale;   /* the residual's scale */
+} moe_norm_config_t;
+
+/* With rho(v) = 1 / sqrt(mean_c v_c^2 + eps) of a row:
+ *     u = y rho(y) w_post                              (w_post NULL: u = y)
+ *     r[t,c] = res_scale x[t,c] + token_gate[t] gate[c] u[t,c]
+ *     n = r rho(r) w_next
+ * x the residual stream, y the output of the block that ends here (NULL: no block yet, r =
+ * res_scale x; w_post and the gates must then be NULL), r the new residual, n the next
+ * block's input. gate [H] and token_gate [T] default to 1 (NULL). r or n may be NULL (not
+ * formed), not both; n needs w_next. Weights and gates are fp32; sums are fp32, and n is
+ * formed from r before its rounding. r may be x, n may be y; other outputs must not overlap
+ * inputs. x, y, r, n [T, H] act. Any H; multiples of 16 bytes move as such. */
+moe_status_t moe_block_norm(const moe_norm_config_t* cfg, const void* x, const void* y, const float* w_post,
+                            const float* w_next, const float* gate, const float* token_gate, void* r, void* n,
+                            moe_stream_t stream);
+
+/* Gradients of the parameters of moe_block_norm (fp32, overwritten; each may be NULL). */
+typedef struct {
+  float* dw_post;     /* [H], with w_post */
+  float* dw_next;     /* [H], with w_next */
+  float* dgate;       /* [H]: also without a gate (the gradient at gate = 1) */
+  float* dtoken_gate; /* [T] */
+} moe_norm_grads_t;
+
+/* The backward, from the stored residual r and block output y (the row statistics are formed
+ * again): dr and dn are the gradients that reach r and n (either may be NULL: zero; dn needs
+ * w_next and w_next needs dn), dx [T, H] and dy [T, H] those of x and y (either may be NULL;
+ * dy and the gradients of w_post and the gates need y). dx may be dr, dy may be dn. The column
+ * sums of the parameter gradients are added in a fixed order. ws:
+ * moe_block_norm_workspace_size bytes (may be NULL when no [H] gradient is asked for). */
+moe_status_t moe_block_norm_workspace_size(const moe_norm_config_t* cfg, size_t* bytes);
+moe_status_t moe_block_norm_backward(const moe_norm_config_t* cfg, const void* r, const void* y, const float* w_post,
+                                     const float* w_next, const float* gate, const float* token_gate, const void* dr,
+                                     const void* dn, void* dx, void* dy, const moe_norm_grads_t* grads, void* ws,
+                                     moe_stream_t stream);
+
+/* Vocabulary head. T tokens, width H, V vocabulary rows. */
+typedef struct {
+  int32_t T, H, V;
+  int32_t act_dtype;  /* MOE_DTYPE_F32 or MOE_DTYPE_BF16: x, w and dx */
+  int32_t grad_dtype; /* the same choice for dw */
+  int32_t piece;      /* vocabulary rows per piece of the backward; 0: as many as 256 MB of
+                         logit gradients hold, at least 4096 */
+} moe_head_config_t;
+
+/* Softmax cross entropy of x [T, H] against the vocabulary rows w [V, H], without keeping the
+ * logits z = x w^T (accumulated in fp32):
+ *     lse[t] = log sum_v exp z[t,v];   loss[t] = lse[t] - z[t, target[t]]
+ * A negative target is left out: its loss is 0 and it has no gradient (its lse is still
+ * given). A target >= V sets MOE_ERR_DEVICE_BAD_INPUT and is left out too. mean (NULL to skip):
+ * two floats, the mean loss of the tokens that count and 1 / their number (0, 0 if none).
+ * target [T] int32; loss, lse [T] fp32. bf16 with H % 8 == 0 runs on the tensor cores, all
+ * else on exact fp32 products. ws: moe_head_workspace_size bytes, used by both calls (they
+ * need not share it). Deterministic. */
+moe_status_t moe_head_workspace_size(const moe_head_config_t* cfg, size_t* bytes);
+moe_status_t moe_head_loss(const moe_head_config_t* cfg, const void* x, const void* w, const int32_t* target,
+                           float* loss, float* lse, float* mean, void* ws, moe_stream_t stream);
+
+/* Its gradients, piece after piece of the vocabulary, the logits formed again:
+ *     dz[t,v] = (exp(z[t,v] - lse[t]) - [v = target[t]]) dloss[t];  dx = dz w;  dw = dz^T x
+ * dloss [T] fp32: the gradient of every token's loss; or NULL, and mean (from moe_head_loss)
+ * makes it the gradient of the mean loss. Exactly one of the two is given. dx [T, H] act and
+ * dw [V, H] grad_dtype are overwritten (either may be NULL). On the tensor cores dz is rounded
+ * to bf16, the operand type of its two products, which accumulate in fp32. */
+moe_status_t moe_head_loss_backward(const moe_head_config_t* cfg, const void* x, const void* w, const int32_t* target,
+                                    const float* lse, const float* dloss, const float* mean, void* dx, void* dw,
+                                    void* ws, moe_stream_t stream);
+
+/* Token embedding. T tokens, rows of H channels, V <= 2^21 - 1 vocabulary rows. */
+typedef struct {
+  int32_t T, H, V;
+  int32_t act_dtype;  /* MOE_DTYPE_F32 or MOE_DTYPE_BF16: table, out and dout */
+  int32_t grad_dtype; /* the same choice for dtable */
+  float scale;        /* multiplies every row */
+} moe_embed_config_t;
+
+/* out[t] = scale * table[token[t]]. A negative token is padding: a zero row, no gradient; a
+ * token >= V sets MOE_ERR_DEVICE_BAD_INPUT and is treated as padding. table [V, H], out
+ * [T, H] act, token [T] int32. ws: at least the status head (4096 bytes) of a workspace. */
+moe_status_t moe_embed(const moe_embed_config_t* cfg, const void* table, const int32_t* token, void* out, void* ws,
+                       moe_stream_t stream);
+
+/* dtable[v] = scale * sum of dout[t] over the positions t with token[t] = v, in fp32, split at
+ * fixed places of the positions sorted by (token, position): no atomics on the sums, the same
+ * bits on every run. accumulate = 0: every row of dtable [V, H] is written (zeros where no
+ * token occurs); 1: the sums are added to the rows of the tokens that occur and the others
+ * are not touched (a table shared with the head, whose gradient is already there). ws:
+ * moe_embed_workspace_size bytes. */
+moe_status_t moe_embed_workspace_size(const moe_embed_config_t* cfg, size_t* bytes);
+moe_status_t moe_embed_backward(const moe_embed_config_t* cfg, const int32_t* token, const void* dout, void* dtable,
+                                int32_t accumulate, void* ws, moe_stream_t stream);
+
+/* One gradient of a list: n elements at grad, dtype MOE_DTYPE_F32 or MOE_DTYPE_BF16, aligned
+ * to its element size only (a view into a flat buffer will do). out: where moe_grad_clip
+ * writes it, of the same dtype; NULL: in place. Tensors must not overlap. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+} moe_grad_t;
+
+/* norm[0] = sqrt(sum over every element of every gradient of its square), summed in fp64
+ * from fp32 sums of at most 64 elements (elements whose squares overflow or underflow fp32
+ * are squared in fp64). `grads` is a host array, read during the call. A non-finite norm sets
+ * MOE_ERR_DEVICE_BAD_INPUT. ws: moe_grad_clip_workspace_size bytes. Deterministic. */
+moe_status_t moe_grad_clip_workspace_size(int32_t count, size_t* bytes);
+moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t count, float* norm, void* ws, moe_stream_t stream);
+
+/* moe_grad_norm, then out = grad * min(1, max_norm / norm) for every gradient (max_norm > 0).
+ * A gradient in place is not touched when the factor is 1. With a non-finite norm the factor
+ * is 1: the caller sees the norm (or the status) and drops the step. */
+moe_status_t moe_grad_clip(const moe_grad_t* grads, int32_t count, float max_norm, float* norm, void* ws,
+                           moe_stream_t stream);
 
 /* Synchronises `stream`, returns the device status word of `ws` in *device_status
  * (MOE_OK or a moe_status_t code) and clears it. The only call that blocks the host. */

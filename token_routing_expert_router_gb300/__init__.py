@@ -1,4 +1,4 @@
-"""GB300-native single-GPU Mixture-of-Experts layer forward.
+"""GB300-native single-GPU Mixture-of-Experts layer, and the operators around it in a step.
 
 Thin ctypes binding over the C ABI in ``include/moe.h`` (``libmoe_gb300.so``): every
 function below has the name of the C entry point it calls and does argument marshalling
@@ -77,6 +77,84 @@ class MoEWeightGrads(ctypes.Structure):
         return g
 
 
+class _PlainConfig(ctypes.Structure):
+    """A C configuration struct made from keywords; _defaults_ fills the fields left out."""
+
+    @classmethod
+    def make(cls, **kw):
+        c = cls()
+        d = {**cls._defaults_, **kw}
+        for name, _ in cls._fields_:
+            setattr(c, name, d.pop(name))
+        if d:
+            raise TypeError(f"{cls.__name__} has no field {', '.join(d)}")
+        return c
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class MoENormConfig(_PlainConfig):
+    _fields_ = [("T", c_int32), ("H", c_int32), ("act_dtype", c_int32), ("eps", c_float), ("res_scale", c_float)]
+    _defaults_ = dict(act_dtype=BF16, eps=1e-6, res_scale=1.0)
+
+
+class MoENormGrads(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("dw_post", "dw_next", "dgate", "dtoken_gate")]
+
+    @classmethod
+    def from_tensors(cls, d: dict) -> "MoENormGrads":
+        g = cls()
+        for name, _ in cls._fields_:
+            setattr(g, name, _ptr(d.get(name)))
+        return g
+
+
+class MoEHeadConfig(_PlainConfig):
+    _fields_ = [("T", c_int32), ("H", c_int32), ("V", c_int32), ("act_dtype", c_int32), ("grad_dtype", c_int32),
+                ("piece", c_int32)]
+    _defaults_ = dict(act_dtype=BF16, grad_dtype=F32, piece=0)
+
+
+class MoEEmbedConfig(_PlainConfig):
+    _fields_ = [("T", c_int32), ("H", c_int32), ("V", c_int32), ("act_dtype", c_int32), ("grad_dtype", c_int32),
+                ("scale", c_float)]
+    _defaults_ = dict(act_dtype=BF16, grad_dtype=F32, scale=1.0)
+
+
+class MoEGrad(ctypes.Structure):
+    _fields_ = [("grad", c_void_p), ("out", c_void_p), ("n", c_int64), ("dtype", c_int32)]
+
+
+class MoEGradList:
+    """The gradients of one model as the C array that moe_grad_norm and moe_grad_clip read.
+    Keeps the tensors alive; make it once and use it every step."""
+
+    def __init__(self, tensors, outs=None):
+        import torch
+        self.tensors = list(tensors)
+        self.outs = None if outs is None else list(outs)
+        if self.outs is not None and len(self.outs) != len(self.tensors):
+            raise ValueError("as many outputs as gradients, or none")
+        code = {torch.float32: F32, torch.bfloat16: BF16}
+        self.array = (MoEGrad * max(1, len(self.tensors)))()
+        for i, t in enumerate(self.tensors):
+            o = None if self.outs is None else self.outs[i]
+            if t.dtype not in code:
+                raise ValueError(f"gradients are fp32 or bf16, not {t.dtype}")
+            if o is not None and (o.dtype != t.dtype or o.numel() != t.numel()):
+                raise ValueError("an output has its gradient's type and number of elements")
+            self.array[i] = MoEGrad(_ptr(t), _ptr(o), t.numel(), code[t.dtype])
+
+    @classmethod
+    def from_tensors(cls, tensors, outs=None) -> "MoEGradList":
+        """outs: where the clipped gradients go (None: in place)."""
+        return cls(tensors, outs)
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+
 _lib = None
 
 
@@ -128,6 +206,19 @@ def lib():
             "moe_read_status": [P, P, POINTER(c_int32)],
             "moe_route_static_scratch": [cfg, P, P, P, P, P, P, P, P, P],
             "moe_selftest_bounded_wait": [c_int64, P, P],
+            "moe_block_norm": [POINTER(MoENormConfig), P, P, P, P, P, P, P, P, P],
+            "moe_block_norm_workspace_size": [POINTER(MoENormConfig), POINTER(c_size_t)],
+            "moe_block_norm_backward": [POINTER(MoENormConfig), P, P, P, P, P, P, P, P, P, P, POINTER(MoENormGrads),
+                                        P, P],
+            "moe_head_workspace_size": [POINTER(MoEHeadConfig), POINTER(c_size_t)],
+            "moe_head_loss": [POINTER(MoEHeadConfig), P, P, P, P, P, P, P, P],
+            "moe_head_loss_backward": [POINTER(MoEHeadConfig), P, P, P, P, P, P, P, P, P, P],
+            "moe_embed": [POINTER(MoEEmbedConfig), P, P, P, P, P],
+            "moe_embed_workspace_size": [POINTER(MoEEmbedConfig), POINTER(c_size_t)],
+            "moe_embed_backward": [POINTER(MoEEmbedConfig), P, P, P, c_int32, P, P],
+            "moe_grad_clip_workspace_size": [c_int32, POINTER(c_size_t)],
+            "moe_grad_norm": [POINTER(MoEGrad), c_int32, P, P, P],
+            "moe_grad_clip": [POINTER(MoEGrad), c_int32, ctypes.c_float, P, P, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -150,6 +241,10 @@ def exported_symbols() -> list:
             "moe_dispatch_backward", "moe_backward", "moe_forward_train", "moe_backward_kept",
             "moe_router_backward_workspace_size",
             "moe_router_backward", "moe_dispatch_router_backward",
+            "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
+            "moe_head_workspace_size", "moe_head_loss", "moe_head_loss_backward",
+            "moe_embed", "moe_embed_workspace_size", "moe_embed_backward",
+            "moe_grad_clip_workspace_size", "moe_grad_norm", "moe_grad_clip",
             "moe_read_status", "moe_status_string", "moe_route_static_scratch",
             "moe_selftest_bounded_wait"]
 
@@ -377,6 +472,81 @@ def moe_route_static_scratch(cfg, logits, topk_idx, topk_w, counts, offsets, row
                                           _ptr(counts), _ptr(offsets), _ptr(row_token),
                                           _ptr(tok_row), _ptr(device_status), _stream(stream)),
            "moe_route_static_scratch")
+
+
+def moe_block_norm(cfg, x, y, w_post, w_next, r, n, gate=None, token_gate=None, stream=None):
+    """r = res_scale x + gates * norm(y) and n = norm(r) in one pass (y None: no block yet;
+    r or n None: not formed)."""
+    _check(lib().moe_block_norm(byref(cfg), _ptr(x), _ptr(y), _ptr(w_post), _ptr(w_next), _ptr(gate),
+                                _ptr(token_gate), _ptr(r), _ptr(n), _stream(stream)), "moe_block_norm")
+
+
+def moe_block_norm_workspace_size(cfg: MoENormConfig) -> int:
+    n = c_size_t()
+    _check(lib().moe_block_norm_workspace_size(byref(cfg), byref(n)), "moe_block_norm_workspace_size")
+    return n.value
+
+
+def moe_block_norm_backward(cfg, r, y, w_post, w_next, dr, dn, dx, dy, grads: dict, ws, gate=None, token_gate=None,
+                            stream=None):
+    """grads: fp32 tensors by field name (dw_post, dw_next, dgate, dtoken_gate; absent: not formed)."""
+    g = MoENormGrads.from_tensors(grads)
+    _check(lib().moe_block_norm_backward(byref(cfg), _ptr(r), _ptr(y), _ptr(w_post), _ptr(w_next), _ptr(gate),
+                                         _ptr(token_gate), _ptr(dr), _ptr(dn), _ptr(dx), _ptr(dy), byref(g), _ptr(ws),
+                                         _stream(stream)), "moe_block_norm_backward")
+
+
+def moe_head_workspace_size(cfg: MoEHeadConfig) -> int:
+    n = c_size_t()
+    _check(lib().moe_head_workspace_size(byref(cfg), byref(n)), "moe_head_workspace_size")
+    return n.value
+
+
+def moe_head_loss(cfg, x, w, target, loss, lse, mean, ws, stream=None):
+    """Every token's loss and log sum, and (mean: 2 fp32 values, or None) the mean loss of the
+    tokens that count and 1 / their number."""
+    _check(lib().moe_head_loss(byref(cfg), _ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), _ptr(mean),
+                               _ptr(ws), _stream(stream)), "moe_head_loss")
+
+
+def moe_head_loss_backward(cfg, x, w, target, lse, dx, dw, ws, dloss=None, mean=None, stream=None):
+    """dx and dw (either may be None) for the tokens' loss gradients dloss, or for the mean
+    loss (mean: moe_head_loss's)."""
+    _check(lib().moe_head_loss_backward(byref(cfg), _ptr(x), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss),
+                                        _ptr(mean), _ptr(dx), _ptr(dw), _ptr(ws), _stream(stream)),
+           "moe_head_loss_backward")
+
+
+def moe_embed(cfg, table, token, out, ws, stream=None):
+    _check(lib().moe_embed(byref(cfg), _ptr(table), _ptr(token), _ptr(out), _ptr(ws), _stream(stream)), "moe_embed")
+
+
+def moe_embed_workspace_size(cfg: MoEEmbedConfig) -> int:
+    n = c_size_t()
+    _check(lib().moe_embed_workspace_size(byref(cfg), byref(n)), "moe_embed_workspace_size")
+    return n.value
+
+
+def moe_embed_backward(cfg, token, dout, dtable, ws, accumulate=False, stream=None):
+    """accumulate: added to the rows of the tokens that occur, the others left alone."""
+    _check(lib().moe_embed_backward(byref(cfg), _ptr(token), _ptr(dout), _ptr(dtable), int(accumulate), _ptr(ws),
+                                    _stream(stream)), "moe_embed_backward")
+
+
+def moe_grad_clip_workspace_size(grads: MoEGradList) -> int:
+    n = c_size_t()
+    _check(lib().moe_grad_clip_workspace_size(len(grads), byref(n)), "moe_grad_clip_workspace_size")
+    return n.value
+
+
+def moe_grad_norm(grads: MoEGradList, norm, ws, stream=None):
+    _check(lib().moe_grad_norm(grads.array, len(grads), _ptr(norm), _ptr(ws), _stream(stream)), "moe_grad_norm")
+
+
+def moe_grad_clip(grads: MoEGradList, max_norm: float, norm, ws, stream=None):
+    """Scales every gradient by min(1, max_norm / norm); norm (1 fp32 value) is left for the caller."""
+    _check(lib().moe_grad_clip(grads.array, len(grads), float(max_norm), _ptr(norm), _ptr(ws), _stream(stream)),
+           "moe_grad_clip")
 
 
 def moe_selftest_bounded_wait(timeout_ns: int, device_status, stream=None):

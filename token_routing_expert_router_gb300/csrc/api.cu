@@ -754,7 +754,7 @@ const char* moe_status_string(moe_status_t s) {
     case MOE_ERR_INVALID_ARG: return "invalid argument";
     case MOE_ERR_UNSUPPORTED: return "unsupported configuration";
     case MOE_ERR_CUDA: return "CUDA error";
-    case MOE_ERR_DEVICE_BAD_INPUT: return "device: bad input (expert id out of range, repeated id or non-finite score)";
+    case MOE_ERR_DEVICE_BAD_INPUT: return "device: bad input (expert id, token or target out of range, repeated id, or non-finite score or norm)";
     case MOE_ERR_TIMEOUT: return "device: bounded wait expired";
   }
   return "unknown status";

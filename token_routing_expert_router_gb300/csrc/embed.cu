@@ -1,0 +1,425 @@
+// Token embedding and its gradient.
+//   out[t] = scale * table[token[t]]                          (a negative token: a zero row)
+//   dtable[v] = scale * sum over t with token[t] = v of dout[t], positions ascending
+//
+// The gradient has no atomics, so its bits do not depend on timing. The positions are sorted
+// by (token, position), in two launches: blocks sort 2048 tokens each in shared memory as one
+// 32-bit key (token << 11 | position in the block), then every element finds its place as its
+// own index plus, by binary search, the number of smaller keys in each other block. Work grows
+// with T^2 / 2048 there; at 131072 tokens that is 64 searches of 11 steps an element.
+// The sums then go over equal chunks of the sorted positions, whatever the tokens' frequencies:
+// a token whose run lies inside a chunk is written at once, one that crosses chunks leaves one
+// partial sum per chunk, and join_kernel adds those in order. Rows of tokens that do not occur
+// are zeroed by further blocks of the same launch. Everything is bound by DRAM: dout is read
+// once, dtable written once.
+#include <algorithm>
+
+#include "step.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kSortBlock = 2048;  // tokens sorted by one block
+constexpr int kSortThreads = 1024;
+constexpr int kPosBits = 11;
+constexpr uint32_t kNoKey = 0xffffffffu;
+
+template <typename T, int VEC>
+struct Vec;
+template <>
+struct Vec<float, 8> {
+  uint4 a, b;
+  __device__ void add_to(float (&f)[8]) const {
+    f[0] += __uint_as_float(a.x), f[1] += __uint_as_float(a.y), f[2] += __uint_as_float(a.z), f[3] += __uint_as_float(a.w);
+    f[4] += __uint_as_float(b.x), f[5] += __uint_as_float(b.y), f[6] += __uint_as_float(b.z), f[7] += __uint_as_float(b.w);
+  }
+  __device__ static Vec of(const float (&f)[8]) {
+    return {make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])),
+            make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]))};
+  }
+};
+template <>
+struct Vec<__nv_bfloat16, 8> {
+  uint4 a;
+  __device__ void add_to(float (&f)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] += __uint_as_float(w[i] << 16);
+      f[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ static Vec of(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return {make_uint4(w[0], w[1], w[2], w[3])};
+  }
+};
+template <>
+struct Vec<float, 1> {
+  float a;
+  __device__ void add_to(float (&f)[1]) const { f[0] += a; }
+  __device__ static Vec of(const float (&f)[1]) { return {f[0]}; }
+};
+template <>
+struct Vec<__nv_bfloat16, 1> {
+  __nv_bfloat16 a;
+  __device__ void add_to(float (&f)[1]) const { f[0] += __bfloat162float(a); }
+  __device__ static Vec of(const float (&f)[1]) { return {__float2bfloat16_rn(f[0])}; }
+};
+
+// blockIdx.x: token, blockIdx.y: slab of blockDim.x pieces of its row.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256)
+    embed_kernel(const T* table, const int32_t* token, T* out, int H, int V, float scale, DeviceStatus* st) {
+  using P = Vec<T, VEC>;
+  const int nvec = H / VEC, c = blockIdx.y * blockDim.x + threadIdx.x;
+  const int64_t t = blockIdx.x;
+  const int32_t v = __ldg(token + t);
+  if (v >= V && threadIdx.x == 0 && blockIdx.y == 0) set_status(st, MOE_ERR_DEVICE_BAD_INPUT, (int32_t)t);
+  if (c >= nvec) return;
+  float f[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) f[e] = 0.0f;
+  if (v >= 0 && v < V) {
+    reinterpret_cast<const P*>(table)[(int64_t)v * nvec + c].add_to(f);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] *= scale;
+  }
+  reinterpret_cast<P*>(out)[t * nvec + c] = P::of(f);
+}
+
+// Sorts block b's tokens [2048 b, 2048 b + 2048): keys [T rounded up to 2048] (tokens that do
+// not count, and the places past T, become kNoKey and sort last). With one block the order is
+// final: stoken and spos are written. The number of tokens that count goes to block_count[b],
+// or to *count.
+__global__ void __launch_bounds__(kSortThreads)
+    sort_blocks_kernel(const int32_t* token, int T, int V, uint32_t* keys, int32_t* block_count,
+                       int32_t* stoken, int32_t* spos, int32_t* count, DeviceStatus* st) {
+  __shared__ uint32_t k[kSortBlock];
+  const int64_t base = (int64_t)blockIdx.x * kSortBlock;
+  const bool single = gridDim.x == 1;
+  for (int i = threadIdx.x; i < kSortBlock; i += kSortThreads) {
+    uint32_t key = kNoKey;
+    if (base + i < T) {
+      const int32_t v = token[base + i];
+      if (v >= V) set_status(st, MOE_ERR_DEVICE_BAD_INPUT, (int32_t)(base + i));
+      if (v >= 0 && v < V) key = (uint32_t)v << kPosBits | (uint32_t)i;
+    }
+    k[i] = key;
+  }
+  const int live = (int)min((int64_t)kSortBlock, T - base);
+  int n = 32;  // sorted length: a power of two that holds every live element
+  while (n < live) n <<= 1;
+  __syncthreads();
+  for (int size = 2; size <= n; size <<= 1) {  // bitonic network
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      const int i = threadIdx.x;
+      if (i < n / 2) {
+        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
+        const uint32_t a = k[lo], b = k[hi];
+        const bool up = (lo & size) == 0;
+        if ((a > b) == up) k[lo] = b, k[hi] = a;
+      }
+      // with stride < 32 a warp's pairs stay inside its own 64 elements
+      if (stride > 32) __syncthreads();
+      else __syncwarp();
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < kSortBlock; i += kSortThreads) {
+    const uint32_t key = k[i];
+    int32_t* here = single ? count : block_count + blockIdx.x;
+    if (!single) {
+      keys[base + i] = key;
+    } else if (key != kNoKey) {
+      stoken[i] = (int32_t)(key >> kPosBits);
+      spos[i] = (int32_t)(key & (kSortBlock - 1));
+    }
+    if (key == kNoKey) {
+      if (i == 0) *here = 0;
+    } else if (i + 1 == kSortBlock || k[i + 1] == kNoKey) {
+      *here = i + 1;
+    }
+  }
+}
+
+// The place of every key among all blocks: the number of smaller keys in its own block (its
+// index there), of keys of the same or a smaller token in the blocks before, and of a smaller
+// token in those after. One thread per key; block 0 also adds up the blocks' counts.
+__global__ void __launch_bounds__(256)
+    rank_kernel(const uint32_t* keys, const int32_t* block_count, int blocks, int32_t* stoken, int32_t* spos,
+                int32_t* count) {
+  if (blockIdx.x == 0) {
+    __shared__ int32_t total;
+    if (threadIdx.x == 0) total = 0;
+    __syncthreads();
+    int32_t mine = 0;
+    for (int b = threadIdx.x; b < blocks; b += 256) mine += block_count[b];
+    if (mine) atomicAdd(&total, mine);
+    __syncthreads();
+    if (threadIdx.x == 0) *count = total;
+  }
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int own = (int)(i / kSortBlock);
+  const uint32_t key = keys[i];
+  if (key == kNoKey) return;
+  const uint32_t token = key >> kPosBits;
+  int64_t rank = 0;
+#pragma unroll 4
+  for (int b = 0; b < blocks; ++b) {
+    const uint32_t bound = b == own ? key : (b < own ? token + 1 : token) << kPosBits;
+    const uint32_t* kb = keys + (int64_t)b * kSortBlock;
+    int at = 0;  // number of keys below bound
+#pragma unroll
+    for (int s = kSortBlock / 2; s > 0; s >>= 1)
+      if (__ldg(kb + at + s - 1) < bound) at += s;
+    if (at == kSortBlock - 1 && __ldg(kb + at) < bound) ++at;
+    rank += at;
+  }
+  stoken[rank] = (int32_t)token;
+  spos[rank] = own * kSortBlock + (int)(key & (kSortBlock - 1));
+}
+
+struct EmbedBwd {
+  const int32_t *stoken, *spos, *count;
+  const void* dout;
+  void* dtable;
+  float* part;  // [chunks][2][H]: the sums of a run that came from the chunk before, and of one that goes on
+  int H, V, chunk, chunks, zero_rows, accumulate;
+  float scale;
+};
+
+template <typename G, int VEC>
+__device__ __forceinline__ void write_row(const EmbedBwd& p, int32_t v, int c, const float (&acc)[VEC]) {
+  using Q = Vec<G, VEC>;
+  Q* dst = static_cast<Q*>(p.dtable) + (int64_t)v * (p.H / VEC) + c;
+  float f[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) f[e] = acc[e] * p.scale;
+  if (p.accumulate) dst->add_to(f);
+  *dst = Q::of(f);
+}
+
+// blockIdx.x < chunks: the sums of one chunk of sorted positions; the further blocks zero the
+// rows of tokens that do not occur, zero_rows tokens each. blockIdx.y: slab of 256 pieces.
+constexpr int kMaxChunk = 256;
+template <typename T, typename G, int VEC>
+__global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedBwd p) {
+  using P = Vec<T, VEC>;
+  __shared__ int32_t ids[kMaxChunk + 2];  // ids[i + 1] = token of the chunk's place i, with both neighbours
+  __shared__ int32_t pos[kMaxChunk];
+  const int nvec = p.H / VEC, c = blockIdx.y * 256 + threadIdx.x;
+  const int n = *p.count;
+  if ((int)blockIdx.x < p.chunks) {
+    const int64_t s = (int64_t)blockIdx.x * p.chunk;
+    if (s >= n) return;
+    const int len = (int)min((int64_t)p.chunk, n - s);
+    for (int i = threadIdx.x; i < len + 2; i += 256) {
+      const int64_t at = s + i - 1;
+      ids[i] = at >= 0 && at < n ? p.stoken[at] : -1;
+      if (i >= 1 && i <= len) pos[i - 1] = p.spos[at];
+    }
+    __syncthreads();
+    if (c >= nvec) return;
+    const P* dout = static_cast<const P*>(p.dout) + c;
+    float acc[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
+    bool started = ids[0] != ids[1];  // the current run begins inside this chunk
+    constexpr int kAhead = 8;  // loads in flight
+    P buf[kAhead];
+    for (int i0 = 0; i0 < len; i0 += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (i0 + u < len) buf[u] = dout[(int64_t)pos[i0 + u] * nvec];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u;
+        if (i >= len) break;
+        buf[u].add_to(acc);
+        const bool ends = ids[i + 2] != ids[i + 1];
+        if (ends || i + 1 == len) {
+          if (started && ends) {
+            write_row<G, VEC>(p, ids[i + 1], c, acc);
+          } else {
+            float* q = p.part + ((int64_t)blockIdx.x * 2 + (started ? 1 : 0)) * p.H + (int64_t)c * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) q[e] = acc[e];
+          }
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
+          started = true;
+        }
+      }
+    }
+  } else {
+    // the tokens [v0, v1) that do not occur: walk the sorted tokens from the first >= v0
+    const int v0 = ((int)blockIdx.x - p.chunks) * p.zero_rows, v1 = min(p.V, v0 + p.zero_rows);
+    __shared__ uint32_t seen[kMaxChunk / 32];
+    for (int i = threadIdx.x; i < kMaxChunk / 32; i += 256) seen[i] = 0;
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      if (__ldg(p.stoken + mid) < v0) lo = mid + 1;
+      else hi = mid;
+    }
+    __syncthreads();
+    for (int i = lo + threadIdx.x; i < n; i += 256) {
+      const int v = p.stoken[i];
+      if (v >= v1) break;
+      atomicOr(&seen[(v - v0) >> 5], 1u << ((v - v0) & 31));
+    }
+    __syncthreads();
+    if (c >= nvec) return;
+    float zero[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) zero[e] = 0.0f;
+    for (int v = v0; v < v1; ++v)
+      if (!(seen[(v - v0) >> 5] >> ((v - v0) & 31) & 1))
+        static_cast<Vec<G, VEC>*>(p.dtable)[(int64_t)v * nvec + c] = Vec<G, VEC>::of(zero);
+  }
+}
+
+// One block per chunk whose last run goes on: the run's partial sums in order of the chunks,
+// 32 pieces wide (blockIdx.y), 8 lanes of chunks, then the lanes in order.
+template <typename G, int VEC>
+__global__ void __launch_bounds__(256) embed_join_kernel(const EmbedBwd p) {
+  __shared__ float lanes[8][32 * VEC];
+  const int n = *p.count;
+  const int64_t e = ((int64_t)blockIdx.x + 1) * p.chunk;  // the place after this chunk
+  if (e >= n) return;
+  const int32_t v = p.stoken[e - 1];
+  if (p.stoken[e] != v) return;
+  const int64_t s = e - p.chunk;
+  if (s > 0 && p.stoken[s - 1] == v && p.stoken[s] == v) return;  // it began in an earlier chunk
+  // first place past the run, by binary search
+  int lo = (int)e, hi = n;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (__ldg(p.stoken + mid) <= v) lo = mid + 1;
+    else hi = mid;
+  }
+  const int last = (lo - 1) / p.chunk;  // chunk of the run's last place
+  const int nvec = p.H / VEC, lane = threadIdx.x >> 5, x = threadIdx.x & 31, c = blockIdx.y * 32 + x;
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  if (c < nvec) {
+    for (int k = (int)blockIdx.x + lane; k <= last; k += 8) {
+      const float* q = p.part + ((int64_t)k * 2 + (k == (int)blockIdx.x ? 1 : 0)) * p.H + (int64_t)c * VEC;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += q[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) lanes[lane][i * 32 + x] = acc[i];
+  __syncthreads();
+  if (lane != 0 || c >= nvec) return;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    float t = 0.0f;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) t += lanes[l][i * 32 + x];
+    acc[i] = t;
+  }
+  write_row<G, VEC>(p, v, c, acc);
+}
+
+int chunk_of(int64_t T) {
+  int chunk = 32;  // about a thousand chunks, of 32 to 256 places
+  while (chunk < kMaxChunk && T > (int64_t)chunk * 1024) chunk *= 2;
+  return chunk;
+}
+
+template <typename T, typename G, int VEC>
+cudaError_t sums(const moe_embed_config_t& c, EmbedBwd p, cudaStream_t s) {
+  const int nvec = c.H / VEC;
+  const int zero_blocks = p.accumulate ? 0 : (int)ceil_div(c.V, p.zero_rows);
+  embed_sum_kernel<T, G, VEC><<<dim3((unsigned)(p.chunks + zero_blocks), (unsigned)ceil_div(nvec, 256)), 256, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.chunks < 2) return e;
+  embed_join_kernel<G, VEC><<<dim3((unsigned)(p.chunks - 1), (unsigned)ceil_div(nvec, 32)), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+EmbedScratch embed_scratch(const moe_embed_config_t& c) {
+  EmbedScratch L;
+  size_t o = kWsHead;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  const size_t T = align_up((size_t)c.T, kSortBlock);
+  L.count = take(4);
+  L.block_count = take(T / kSortBlock * 4);
+  L.keys = take(T * 4);
+  L.stoken = take(T * 4);
+  L.spos = take(T * 4);
+  L.part = take((size_t)ceil_div(c.T, chunk_of(c.T)) * 2 * c.H * 4);
+  L.total = o;
+  return L;
+}
+
+cudaError_t launch_embed(const moe_embed_config_t& c, const void* table, const int32_t* token, void* out,
+                         DeviceStatus* st, cudaStream_t s) {
+  if (c.T == 0) return cudaSuccess;
+  const bool bf = c.act_dtype == MOE_DTYPE_BF16, wide = c.H % 8 == 0;
+  const int nvec = wide ? c.H / 8 : c.H, threads = (int)std::min<int64_t>(256, ceil_div(nvec, 32) * 32);
+  const dim3 grid((unsigned)c.T, (unsigned)ceil_div(nvec, threads));
+  auto run = [&](auto kern, auto* t, auto* o) { kern<<<grid, threads, 0, s>>>(t, token, o, c.H, c.V, c.scale, st); };
+  const auto* tb = static_cast<const __nv_bfloat16*>(table);
+  const auto* tf = static_cast<const float*>(table);
+  auto* ob = static_cast<__nv_bfloat16*>(out);
+  auto* of = static_cast<float*>(out);
+  if (bf && wide) run(embed_kernel<__nv_bfloat16, 8>, tb, ob);
+  else if (bf) run(embed_kernel<__nv_bfloat16, 1>, tb, ob);
+  else if (wide) run(embed_kernel<float, 8>, tf, of);
+  else run(embed_kernel<float, 1>, tf, of);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_embed_backward(const moe_embed_config_t& c, const int32_t* token, const void* dout, void* dtable,
+                                  int accumulate, void* ws, DeviceStatus* st, cudaStream_t s) {
+  const bool gbf = c.grad_dtype == MOE_DTYPE_BF16, bf = c.act_dtype == MOE_DTYPE_BF16, wide = c.H % 8 == 0;
+  if (c.T == 0)
+    return accumulate ? cudaSuccess : cudaMemsetAsync(dtable, 0, (size_t)c.V * c.H * (gbf ? 2 : 4), s);
+  const EmbedScratch L = embed_scratch(c);
+  char* w = static_cast<char*>(ws);
+  auto* keys = reinterpret_cast<uint32_t*>(w + L.keys);
+  auto* stoken = reinterpret_cast<int32_t*>(w + L.stoken);
+  auto* spos = reinterpret_cast<int32_t*>(w + L.spos);
+  auto* count = reinterpret_cast<int32_t*>(w + L.count);
+  auto* bcount = reinterpret_cast<int32_t*>(w + L.block_count);
+  const int blocks = (int)ceil_div(c.T, kSortBlock);
+  sort_blocks_kernel<<<blocks, kSortThreads, 0, s>>>(token, c.T, c.V, keys, bcount, stoken, spos, count, st);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (blocks > 1) {
+    rank_kernel<<<blocks * (kSortBlock / 256), 256, 0, s>>>(keys, bcount, blocks, stoken, spos, count);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  EmbedBwd p{stoken, spos, count, dout, dtable, reinterpret_cast<float*>(w + L.part)};
+  p.H = c.H;
+  p.V = c.V;
+  p.chunk = chunk_of(c.T);
+  p.chunks = (int)ceil_div(c.T, p.chunk);
+  p.zero_rows = 64;
+  p.accumulate = accumulate;
+  p.scale = c.scale;
+  if (wide) {
+    if (bf) return gbf ? sums<__nv_bfloat16, __nv_bfloat16, 8>(c, p, s) : sums<__nv_bfloat16, float, 8>(c, p, s);
+    return gbf ? sums<float, __nv_bfloat16, 8>(c, p, s) : sums<float, float, 8>(c, p, s);
+  }
+  if (bf) return gbf ? sums<__nv_bfloat16, __nv_bfloat16, 1>(c, p, s) : sums<__nv_bfloat16, float, 1>(c, p, s);
+  return gbf ? sums<float, __nv_bfloat16, 1>(c, p, s) : sums<float, float, 1>(c, p, s);
+}
+
+}  // namespace moe
