@@ -270,9 +270,11 @@ def _host_ptr(t):
 
 
 def _stream(stream=None):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # the raw handle: a Stream object would cost about as much as a kernel launch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(code: int, where: str):

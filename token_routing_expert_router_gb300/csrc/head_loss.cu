@@ -37,13 +37,16 @@ constexpr int kEpiWarps = 8;
 constexpr int kABytes = BM * BK * 2;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kRun = 16;  // K stages (1024 elements) added by the tensor core in one go
 
 enum Mode { STATS = 0, DLOGITS = 1, DX = 2, DW = 3 };
 
 struct HeadParams {
   int M, N;            // rows and columns of the product that exist
   int m_tiles, n_tiles, kblocks;
-  int splits;          // DX: K splits, each with its own slice of out
+  int direct;          // DX: the first `direct` tiles are whole; the K of each further one is
+  int splits;          //   split over `splits` units, which write fp32 tiles to `slices`
+  float* slices;       //   [tile - direct][split][TM][BN]
   int b_row0;          // first vocabulary row of the piece (STATS: 0)
   int V;
   const int32_t* target;
@@ -51,12 +54,13 @@ struct HeadParams {
   float2* part;
   float* target_logit;
   // DLOGITS
-  const float *lse, *dloss, *mean;
+  const float *lse, *dloss;
   // outputs of the other modes, and their row length in elements
   void* out;
   int64_t ldo;
   int out_f32;         // DX, DW: fp32 output (else bf16)
   int add;             // DX: added to what out holds (a later piece of the vocabulary)
+  const float* factor; // DX, DW: every value is multiplied by it (the mean's 1 / count), or NULL
   DeviceStatus* status;
   uint64_t timeout_ns;
 };
@@ -79,9 +83,30 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
   return d;
 }
 
+// 2^x (the PTX instruction, relative error 2^-22).
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// A row's next 64 bytes into the staging buffer: 32 columns as bf16, or 16 as fp32.
+__device__ __forceinline__ void stage_bf16(uint8_t* stage, int lane, const float* v) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    stage_piece(stage, lane, q, make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                                           pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7])));
+}
+__device__ __forceinline__ void stage_f32(uint8_t* stage, int lane, const float* v) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    stage_piece(stage, lane, q, make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                           __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
 }
 
 // flush_rows_64B with a column bound: the 16-byte pieces c >= pieces are left out.
@@ -109,20 +134,40 @@ __device__ __forceinline__ void flush_edge(uint8_t* stage, int lane, uint8_t* ba
 }
 
 struct HeadTile {
-  int mb, nb, split, kb0, kb1;
+  int mb, nb, slice, kb0, kb1;  // slice: -1, or the tile's place in `slices`
 };
 
-// m tiles run fastest: they share a tile of w (or of x) through L2.
-__device__ __forceinline__ HeadTile head_tile(int tile, const HeadParams& p) {
+// Which tiles run side by side, and so share operands through L2. Logits and dx: the m tiles
+// (a tile of w is read once, x or a K slice of dz stays in L2). dw: the n tiles (the columns of
+// dz are read once, x stays in L2; with the m tiles first, dz came from DRAM once per n tile,
+// 4.2 GB for 4096 x 4096 x 32000, and the product took 700 us).
+template <int MODE>
+__device__ __forceinline__ HeadTile head_tile(int unit_index, const HeadParams& p) {
   HeadTile t;
-  const int per = p.m_tiles * p.n_tiles;
-  t.split = tile / per;
-  const int local = tile - t.split * per;
-  t.nb = local / p.m_tiles;
-  t.mb = local - t.nb * p.m_tiles;
-  t.kb0 = (int)((int64_t)p.kblocks * t.split / p.splits);
-  t.kb1 = (int)((int64_t)p.kblocks * (t.split + 1) / p.splits);
+  int tile = unit_index;
+  t.slice = -1;
+  t.kb0 = 0;
+  t.kb1 = p.kblocks;
+  if (MODE == DX && unit_index >= p.direct) {
+    t.slice = unit_index - p.direct;
+    const int split = t.slice % p.splits;
+    tile = p.direct + t.slice / p.splits;
+    t.kb0 = (int)((int64_t)p.kblocks * split / p.splits);
+    t.kb1 = (int)((int64_t)p.kblocks * (split + 1) / p.splits);
+  }
+  if (MODE == DW) {
+    t.mb = tile / p.n_tiles;
+    t.nb = tile - t.mb * p.n_tiles;
+  } else {
+    t.nb = tile / p.m_tiles;
+    t.mb = tile - t.nb * p.m_tiles;
+  }
   return t;
+}
+
+// Work units of a launch.
+__host__ __device__ __forceinline__ int head_units(const HeadParams& p) {
+  return p.direct + (p.m_tiles * p.n_tiles - p.direct) * p.splits;
 }
 
 template <int MODE, int CG, int BN>
@@ -177,7 +222,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total_tiles = p.m_tiles * p.n_tiles * p.splits;
+  const int total_tiles = head_units(p);
+  // The loss's logits are added up in runs of kRun K stages: each run has its own accumulator,
+  // and the epilogue adds the runs in fp32. The tensor core's own additions truncate: over 4096
+  // elements in one go the loss was off by 3.4e-6 of its size, in runs of 1024 by 6e-7. dz is
+  // rounded to bf16, where one go is good enough.
+  constexpr bool kRuns = MODE == STATS;
+  auto runs_of = [&](const HeadTile& t) { return kRuns ? (t.kb1 - t.kb0 + kRun - 1) / kRun : 1; };
+  auto run_end = [&](const HeadTile& t, int run) { return kRuns ? min(t.kb1, (run + 1) * kRun) : t.kb1; };
 
   if (warp == 0) {
     // ======================= TMA producer (each CTA loads its own rows of A and its part of B)
@@ -187,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t issued = 0;
       bool ok = true;
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
-        const HeadTile t = head_tile(tile, p);
+        const HeadTile t = head_tile<MODE>(tile, p);
         const int am = t.mb * TM + (int)rank * BM, bn = t.nb * BN + (int)rank * (BN / CG);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort, p.timeout_ns, p.status)) { ok = false; break; }
@@ -239,31 +291,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t acc_phase = 0;
       bool ok = true;
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
-        const HeadTile t = head_tile(tile, p);
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort, p.timeout_ns, p.status)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!mbar_wait(&full[stage], phase, abort, p.timeout_ns, p.status)) { ok = false; break; }
+        const HeadTile t = head_tile<MODE>(tile, p);
+        int kb = t.kb0;
+        for (int run = 0; run < runs_of(t) && ok; ++run) {
+          if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort, p.timeout_ns, p.status)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_addr = smem_addr(sA + stage * kABytes);
-          const uint32_t b_addr = smem_addr(sB + stage * kBBytes);
+          const uint32_t d_tmem = tmem_base + acc * BN;
+          const int first = kb, end = run_end(t, run);
+          for (; kb < end; ++kb) {
+            if (!mbar_wait(&full[stage], phase, abort, p.timeout_ns, p.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a_addr = smem_addr(sA + stage * kABytes);
+            const uint32_t b_addr = smem_addr(sB + stage * kBBytes);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) {
-            const uint64_t ad = kAmn ? desc_mn(a_addr + k * 2048) : desc_k_sw128(a_addr + k * 32);
-            const uint64_t bd = kBmn ? desc_mn(b_addr + k * 2048) : desc_k_sw128(b_addr + k * 32);
-            const uint32_t accumulate = kb > t.kb0 || k > 0;
-            if constexpr (CG == 1) mma_bf16(d_tmem, ad, bd, idesc, accumulate);
-            else mma_bf16_pair(d_tmem, ad, bd, idesc, accumulate);
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint64_t ad = kAmn ? desc_mn(a_addr + k * 2048) : desc_k_sw128(a_addr + k * 32);
+              const uint64_t bd = kBmn ? desc_mn(b_addr + k * 2048) : desc_k_sw128(b_addr + k * 32);
+              const uint32_t accumulate = kb > first || k > 0;
+              if constexpr (CG == 1) mma_bf16(d_tmem, ad, bd, idesc, accumulate);
+              else mma_bf16_pair(d_tmem, ad, bd, idesc, accumulate);
+            }
+            if constexpr (CG == 1) mma_commit(&empty[stage]);
+            else mma_commit_pair(&empty[stage], 0x3);
+            if (++stage == kStages) { stage = 0; phase ^= 1; }
           }
-          if constexpr (CG == 1) mma_commit(&empty[stage]);
-          else mma_commit_pair(&empty[stage], 0x3);
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
+          if (!ok) break;
+          if constexpr (CG == 1) mma_commit(&tfull[acc]);
+          else mma_commit_pair(&tfull[acc], 0x3);
+          if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
-        if (!ok) break;
-        if constexpr (CG == 1) mma_commit(&tfull[acc]);
-        else mma_commit_pair(&tfull[acc], 0x3);
-        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
       if constexpr (CG == 1) mma_commit(drain);
       else mma_commit_pair(drain, 0x3);
@@ -283,114 +339,146 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = unit; tile < total_tiles; tile += nunits) {
-      const HeadTile t = head_tile(tile, p);
+      const HeadTile t = head_tile<MODE>(tile, p);
       const int row0 = t.mb * TM + wrow, row = row0 + lane;  // the thread's row of the product
       const int col0 = t.nb * BN + cbase;                    // the warp's first column
       const bool live = row < p.M;
-      int tgt = -1;
-      float lse2 = 0.0f, g = 0.0f;
-      if constexpr (MODE == STATS || MODE == DLOGITS) {
-        if (live) tgt = __ldg(p.target + row);
-        if constexpr (MODE == DLOGITS) {
-          if (live) {
-            lse2 = __ldg(p.lse + row) * kLog2e;
-            g = p.dloss ? __ldg(p.dloss + row) : __ldg(p.mean + 1);
-          }
-          if (tgt < 0 || tgt >= p.V) tgt = -1;
-          else tgt -= p.b_row0;  // column of this piece
+      auto wait_full = [&] {
+        const bool ok = mbar_wait(&tfull[acc], acc_phase, abort, p.timeout_ns, p.status);
+        tc_fence_after();
+        return __all_sync(0xffffffffu, ok);
+      };
+      auto release = [&] {  // this accumulator may be written again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2 && !leader) mbar_arrive_cluster_relaxed(tempty_leader + acc * 8);
+          else mbar_arrive_relaxed(&tempty[acc]);
         }
-      }
-      const bool counts = MODE == DLOGITS && live && __ldg(p.target + row) >= 0 && __ldg(p.target + row) < p.V;
-      bool ok = mbar_wait(&tfull[acc], acc_phase, abort, p.timeout_ns, p.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN + cbase;
-      uint32_t nxt[32];
-      tmem_ld32(t_row, nxt);
-      float mx = -INFINITY, sum = 0.0f;  // STATS: running maximum (of z log2 e) and sum
-#pragma unroll 1
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
-        uint32_t v[32];
-        tmem_ld_wait();
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+      };
+      const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16) + cbase;
+
+      if constexpr (MODE == STATS) {
+        // this row's half of the tile's columns, out of TMEM before anything is made of it
+        uint32_t zr[kCols / 32][32];
+        auto z = [&](int i) { return __uint_as_float(zr[i / 32][i % 32]); };
+        const int runs = runs_of(t);
+        bool ok = true;
+        for (int run = 0; run < runs; ++run) {
+          if (!(ok = wait_full())) break;
+          const uint32_t t_row = t_lane + acc * BN;
+          if (run == 0) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = MODE == DX && t.kb0 == t.kb1 ? 0u : nxt[i];  // a split without K stages
-        if (c0 + 32 < kCols) tmem_ld32(t_row + c0 + 32, nxt);
-        const int cc = col0 + c0;            // first column of the chunk
-        const int cols = p.N - cc;           // columns from there on that exist
-        if constexpr (MODE == STATS) {
-          if (__any_sync(0xffffffffu, (uint32_t)(tgt - cc) < 32u) && tgt < p.N) {
+            for (int c = 0; c < kCols / 32; ++c) tmem_ld32(t_row + 32 * c, zr[c]);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (cc + i == tgt) p.target_logit[row] = __uint_as_float(v[i]);
-          }
-          float z[32], m = mx;
+            for (int c = 0; c < kCols; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(t_row + c, v);
+              tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            z[i] = __uint_as_float(v[i]) * kLog2e;
-            if (cols < 32 && i >= cols) z[i] = -INFINITY;
-            m = fmaxf(m, z[i]);
-          }
-          const float base = m == -INFINITY ? 0.0f : m;
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            s0 += exp2f(z[i] - base);
-            s1 += exp2f(z[i + 1] - base);
-          }
-          sum = fmaf(sum, exp2f(mx - base), s0 + s1);
-          mx = m;
-        } else if constexpr (MODE == DLOGITS) {
-          uint32_t w[16];
-          const int at = tgt - cc;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float d[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float pr = exp2f(fmaf(__uint_as_float(v[i + e]), kLog2e, -lse2));
-              if (tgt >= 0 && i + e == at) pr -= 1.0f;
-              d[e] = counts && i + e < cols ? pr * g : 0.0f;
+              for (int i = 0; i < 16; ++i)
+                zr[c / 32][c % 32 + i] = __float_as_uint(__uint_as_float(zr[c / 32][c % 32 + i]) + __uint_as_float(v[i]));
             }
-            w[i / 2] = pack2(d[0], d[1]);
           }
+          release();
+        }
+        if (!ok) break;
+        const int cols = p.N - col0;  // columns from here on that exist
+        const int tgt = live ? __ldg(p.target + row) : -1;
+        if (tgt >= col0 && tgt < min(col0 + kCols, p.N)) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            stage_piece(stage, lane, q, make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
-          // columns past the vocabulary are written too, as zeros: they are K rows of the next products
-          flush_rows_64B(stage, lane, static_cast<uint8_t*>(p.out) + ((int64_t)row0 * p.ldo + cc) * 2, p.ldo * 2,
-                         p.M - row0);
-        } else if (p.out_f32) {
-          uint8_t* out = static_cast<uint8_t*>(p.out) +
-                         (((int64_t)t.split * p.M + row0) * p.ldo + cc) * 4;
+          for (int i = 0; i < kCols; ++i)
+            if (col0 + i == tgt) p.target_logit[row] = z(i);
+        }
+        float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
+        for (int i = 0; i < kCols; i += 2) {
+          if (cols < kCols) {
+            if (i >= cols) zr[i / 32][i % 32] = __float_as_uint(-INFINITY);
+            if (i + 1 >= cols) zr[i / 32][i % 32 + 1] = __float_as_uint(-INFINITY);
+          }
+          m0 = fmaxf(m0, z(i));
+          m1 = fmaxf(m1, z(i + 1));
+        }
+        const float mx = fmaxf(m0, m1) * kLog2e;
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              stage_piece(stage, lane, q, make_uint4(v[16 * h2 + 4 * q], v[16 * h2 + 4 * q + 1], v[16 * h2 + 4 * q + 2],
-                                                     v[16 * h2 + 4 * q + 3]));
-            flush_edge(stage, lane, out + 64 * h2, p.ldo * 4, p.M - row0, (cols - 16 * h2) / 4, MODE == DX && p.add);
+        for (int i = 0; i < kCols; i += 2) {
+          s0 += ex2(fmaf(z(i), kLog2e, -base));
+          s1 += ex2(fmaf(z(i + 1), kLog2e, -base));
+        }
+        if (live) p.part[(int64_t)(2 * t.nb + half) * p.M + row] = make_float2(mx, s0 + s1);
+      } else {
+        int tgt = -1;
+        bool counts = false;
+        float lse2 = 0.0f, g = 0.0f;
+        if constexpr (MODE == DLOGITS) {
+          if (live) tgt = __ldg(p.target + row);
+          counts = tgt >= 0 && tgt < p.V;
+          if (counts) {
+            lse2 = __ldg(p.lse + row) * kLog2e;
+            // the gradient of the mean: its factor 1 / count is left to the two products
+            g = p.dloss ? __ldg(p.dloss + row) : 1.0f;
           }
         } else {
-          uint8_t* out = static_cast<uint8_t*>(p.out) + ((int64_t)row0 * p.ldo + cc) * 2;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            stage_piece(stage, lane, q,
-                        make_uint4(pack2(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1])),
-                                   pack2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3])),
-                                   pack2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5])),
-                                   pack2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]))));
-          flush_edge(stage, lane, out, p.ldo * 2, p.M - row0, cols / 8, false);
+          g = p.factor ? __ldg(p.factor) : 1.0f;
         }
+        if (!wait_full()) break;
+        const bool none = MODE == DX && t.kb0 == t.kb1;  // a split without K stages: nothing in the accumulator
+        const uint32_t t_row = t_lane + acc * BN;
+        uint32_t nxt[32];
+        tmem_ld32(t_row, nxt);
+#pragma unroll 1
+        for (int c0 = 0; c0 < kCols; c0 += 32) {
+          float v[32];
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(nxt[i]);
+          if (c0 + 32 < kCols) tmem_ld32(t_row + c0 + 32, nxt);  // next chunk in flight
+          const int cc = col0 + c0;   // first column of the chunk
+          const int cols = p.N - cc;  // columns from there on that exist
+          if constexpr (MODE == DLOGITS) {
+            const int at = tgt - p.b_row0 - cc;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[i] = ex2(fmaf(v[i], kLog2e, -lse2));
+              if (i == at) v[i] -= 1.0f;
+              v[i] = counts && i < cols ? v[i] * g : 0.0f;
+            }
+            stage_bf16(stage, lane, v);
+            // columns past the vocabulary are written too, as zeros: they are K rows of the next products
+            flush_rows_64B(stage, lane, static_cast<uint8_t*>(p.out) + ((int64_t)row0 * p.ldo + cc) * 2, p.ldo * 2,
+                           p.M - row0);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = none ? 0.0f : v[i] * g;
+            if (MODE == DX && t.slice >= 0) {
+              uint8_t* out = reinterpret_cast<uint8_t*>(p.slices + ((int64_t)t.slice * TM + wrow) * BN + cbase + c0);
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                stage_f32(stage, lane, v + h);
+                flush_rows_64B(stage, lane, out + 4 * h, BN * 4, 32);
+              }
+            } else if (p.out_f32) {
+              uint8_t* out = static_cast<uint8_t*>(p.out) + ((int64_t)row0 * p.ldo + cc) * 4;
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                stage_f32(stage, lane, v + h);
+                flush_edge(stage, lane, out + 4 * h, p.ldo * 4, p.M - row0, (cols - h) / 4, MODE == DX && p.add);
+              }
+            } else {
+              stage_bf16(stage, lane, v);
+              flush_edge(stage, lane, static_cast<uint8_t*>(p.out) + ((int64_t)row0 * p.ldo + cc) * 2, p.ldo * 2,
+                         p.M - row0, cols / 8, false);
+            }
+          }
+        }
+        release();
       }
-      if (MODE == STATS && live) p.part[(int64_t)(2 * t.nb + half) * p.M + row] = make_float2(mx, sum);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 2 && !leader) mbar_arrive_cluster_relaxed(tempty_leader + acc * 8);
-        else mbar_arrive_relaxed(&tempty[acc]);
-      }
-      if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
   }
 
@@ -418,7 +506,7 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+  const int64_t tiles = head_units(p);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(CG * (num_sms() / CG));
   cfg.blockDim = dim3(kThreads);
@@ -448,12 +536,45 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
 // Up to 128 tokens: one 128-row tile, single CTAs. Else 256-row tiles on CTA pairs.
 bool small_tokens(int T) { return T <= BM; }
 
-HeadParams base_params(DeviceStatus* st) {
+HeadParams base_params(int64_t M, int64_t N, int64_t K, int tm, int tn, DeviceStatus* st) {
   HeadParams p{};
+  p.M = (int)M;
+  p.N = (int)N;
+  p.m_tiles = (int)ceil_div(M, tm);
+  p.n_tiles = (int)ceil_div(N, tn);
+  p.kblocks = (int)ceil_div(K, BK);
+  p.direct = p.m_tiles * p.n_tiles;
   p.splits = 1;
   p.status = st;
   p.timeout_ns = kTimeoutNs;
   return p;
+}
+
+// dx of the tiles whose K was split: the sum of a tile's slices in order, written or added.
+template <typename T>
+__global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, int tm, int tn, T* out) {
+  const int tile = p.direct + blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;  // 4 columns each
+  const int nb = tile / p.m_tiles, mb = tile - nb * p.m_tiles;
+  const int row = mb * tm + e / tn, col = nb * tn + e % tn;
+  if (row >= p.M || col >= p.N) return;
+  const float* s = p.slices + (int64_t)blockIdx.y * p.splits * tm * tn + e;
+  float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int k = 0; k < p.splits; ++k) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(s + (int64_t)k * tm * tn));
+    v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+  }
+  T* o = out + (int64_t)row * p.ldo + col;
+  if constexpr (sizeof(T) == 4) {
+    float4* d = reinterpret_cast<float4*>(o);
+    if (p.add) {
+      const float4 a = *d;
+      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+    }
+    *d = v;
+  } else {
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+  }
 }
 
 }  // namespace
@@ -461,17 +582,30 @@ HeadParams base_params(DeviceStatus* st) {
 // Columns of a tile of the logits, for the number of (max, sum) halves.
 int head_tile_cols(int T) { return small_tokens(T) ? 128 : 256; }
 
+// The input gradient's tiles rarely fill whole rounds of the SMs (4096 x 4096 is 256 tiles of
+// 256 x 256 on 76 CTA pairs: 3.37 rounds, so 4). The tiles of the last round are therefore
+// split along K, by the number of ways that takes least time: rounds of stages of 64 at 0.14 us
+// each against the slices' traffic at 0.08 us a tile, and the launch that adds them.
+HeadSplit head_split(int64_t T, int64_t H, int64_t rows) {
+  const bool small = small_tokens((int)std::min<int64_t>(T, INT32_MAX));
+  const int tm = small ? BM : 2 * BM, tn = small ? 128 : 256, units = small ? 152 : 76;
+  const int64_t tiles = ceil_div(T, tm) * ceil_div(H, tn), kblocks = ceil_div(rows, BK);
+  HeadSplit best{tiles, 1, 0};
+  const int64_t tail = tiles % units;
+  double least = (tail ? 1.0 : 0.0) * kblocks * 0.14;
+  for (int s = 2; s <= 32 && tail && s * 4 <= kblocks; ++s) {
+    const double t = (double)ceil_div(tail * s, units) * ceil_div(kblocks, s) * 0.14 +
+                     tail * s * 0.08 * (small ? 0.25 : 1.0) + 4.0;
+    if (t < least) least = t, best = {tiles - tail, s, (size_t)(tail * s) * tm * tn * 4};
+  }
+  return best;
+}
+
 cudaError_t launch_head_stats(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
                               float2* part, float* target_logit, DeviceStatus* st, cudaStream_t s) {
-  HeadParams p = base_params(st);
   const bool small = small_tokens(c.T);
-  const int bn = head_tile_cols(c.T);
-  p.M = c.T;
-  p.N = c.V;
+  HeadParams p = base_params(c.T, c.V, c.H, small ? BM : 2 * BM, head_tile_cols(c.T), st);
   p.V = c.V;
-  p.m_tiles = (int)ceil_div(c.T, small ? BM : 2 * BM);
-  p.n_tiles = (int)ceil_div(c.V, bn);
-  p.kblocks = (int)ceil_div(c.H, BK);
   p.target = target;
   p.part = part;
   p.target_logit = target_logit;
@@ -483,55 +617,49 @@ cudaError_t launch_head_stats(const moe_head_config_t& c, const void* x, const v
 // dz of the vocabulary rows [v0, v0 + rows) -> dl [T, ld] bf16; then dx and dw of the piece.
 cudaError_t launch_head_piece(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
                               const float* lse, const float* dloss, const float* mean, int64_t v0, int rows, void* dl,
-                              int ld, void* dx, int splits, bool dx_f32, bool add, void* dw, DeviceStatus* st,
-                              cudaStream_t s) {
+                              int ld, void* dx, const HeadSplit& split, float* slices, bool dx_f32, bool add, void* dw,
+                              DeviceStatus* st, cudaStream_t s) {
   const bool small = small_tokens(c.T);
+  const int tm = small ? BM : 2 * BM, tn = head_tile_cols(c.T);
   CUtensorMap a, b;
-  HeadParams p = base_params(st);
-  const int bn = head_tile_cols(c.T);
-  p.M = c.T;
-  p.N = rows;
+  HeadParams p = base_params(c.T, rows, c.H, tm, tn, st);
   p.V = c.V;
   p.b_row0 = (int)v0;
-  p.m_tiles = (int)ceil_div(c.T, small ? BM : 2 * BM);
-  p.n_tiles = (int)ceil_div(rows, bn);
-  p.kblocks = (int)ceil_div(c.H, BK);
   p.target = target;
   p.lse = lse;
   p.dloss = dloss;
-  p.mean = mean;
   p.out = dl;
   p.ldo = ld;
   if (!bf16_box(&a, x, c.T, c.H, BM) || !bf16_box(&b, w, c.V, c.H, 128)) return cudaErrorInvalidValue;
   cudaError_t e = small ? launch_gemm<DLOGITS, 1, 128>(a, b, p, s) : launch_gemm<DLOGITS, 2, 256>(a, b, p, s);
   if (e != cudaSuccess) return e;
   if (dx) {  // M = T, N = H, K = the piece's vocabulary rows
-    p = base_params(st);
-    p.M = c.T;
-    p.N = c.H;
+    p = base_params(c.T, c.H, rows, tm, tn, st);
     p.b_row0 = (int)v0;
-    p.m_tiles = (int)ceil_div(c.T, small ? BM : 2 * BM);
-    p.n_tiles = (int)ceil_div(c.H, small ? 128 : 256);
-    p.kblocks = (int)ceil_div(rows, BK);
-    p.splits = splits;
+    p.direct = (int)split.direct;
+    p.splits = split.splits;
+    p.slices = slices;
     p.out = dx;
     p.ldo = c.H;
     p.out_f32 = dx_f32;
     p.add = add;
+    p.factor = mean ? mean + 1 : nullptr;
     if (!bf16_box(&a, dl, c.T, ld, BM) || !bf16_box(&b, w, c.V, c.H, 64)) return cudaErrorInvalidValue;
     e = small ? launch_gemm<DX, 1, 128>(a, b, p, s) : launch_gemm<DX, 2, 256>(a, b, p, s);
     if (e != cudaSuccess) return e;
+    if (split.splits > 1) {
+      const dim3 grid((unsigned)(tm * tn / 1024), (unsigned)(p.m_tiles * p.n_tiles - p.direct));
+      if (dx_f32) join_slices_kernel<float><<<grid, 256, 0, s>>>(p, tm, tn, static_cast<float*>(dx));
+      else join_slices_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p, tm, tn, static_cast<__nv_bfloat16*>(dx));
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
   }
   if (dw) {  // M = the piece's vocabulary rows, N = H, K = T
-    p = base_params(st);
-    p.M = rows;
-    p.N = c.H;
-    p.m_tiles = (int)ceil_div(rows, 2 * BM);
-    p.n_tiles = (int)ceil_div(c.H, 256);
-    p.kblocks = (int)ceil_div(c.T, BK);
+    p = base_params(rows, c.H, c.T, 2 * BM, 256, st);
     p.out_f32 = c.grad_dtype == MOE_DTYPE_F32;
     p.out = static_cast<uint8_t*>(dw) + v0 * c.H * (p.out_f32 ? 4 : 2);
     p.ldo = c.H;
+    p.factor = mean ? mean + 1 : nullptr;
     if (!bf16_box(&a, dl, c.T, ld, 64) || !bf16_box(&b, x, c.T, c.H, 64)) return cudaErrorInvalidValue;
     e = launch_gemm<DW, 2, 256>(a, b, p, s);
   }
@@ -670,16 +798,19 @@ cudaError_t launch_simt(const SimtParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Four tokens per block, 256 lanes of halves each: lse = max + log(sum), the loss, and in the
-// block that finishes last their mean over the tokens that count and its reciprocal count.
-constexpr int kJoinTokens = 4;
+// TOK tokens per block of 1024 threads, the other lanes over the halves: lse = max + log(sum),
+// the loss, and in the block that finishes last their mean over the tokens that count and its
+// reciprocal count. Few tokens take TOK = 4 (a token's 2000 halves of a large vocabulary in 8
+// steps), many TOK = 32 (256 bytes of a row of halves per step).
+template <int TOK>
 __global__ void __launch_bounds__(1024)
     join_kernel(const float2* part, int parts, int T, int V, const int32_t* target, const float* target_logit,
                 float* loss, float* lse, float* mean, uint32_t* ticket, DeviceStatus* st) {
-  __shared__ float sm[32][kJoinTokens], ss[32][kJoinTokens];
+  constexpr int kLanes = 1024 / TOK, kAhead = 4;
+  __shared__ float sm[32][TOK], ss[32][TOK];
   __shared__ bool finish;
-  const int tok = threadIdx.x & 3, lane = threadIdx.x >> 2, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * kJoinTokens + tok;
+  const int tok = threadIdx.x % TOK, lane = threadIdx.x / TOK, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * TOK + tok;
   float m = -INFINITY, s = 0.0f;
   auto merge = [&](float m2, float s2) {
     const float n = fmaxf(m, m2), base = n == -INFINITY ? 0.0f : n;
@@ -687,23 +818,35 @@ __global__ void __launch_bounds__(1024)
     m = n;
   };
   if (t < T) {
-#pragma unroll 4
-    for (int i = lane; i < parts; i += 256) {
-      const float2 v = __ldg(part + (int64_t)i * T + t);
-      merge(v.x, v.y);
+    for (int i0 = lane; i0 < parts; i0 += kLanes * kAhead) {
+      float2 v[kAhead];
+      float m2 = m;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kLanes;
+        v[u] = i < parts ? __ldg(part + (int64_t)i * T + t) : make_float2(-INFINITY, 0.0f);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) m2 = fmaxf(m2, v[u].x);
+      const float base = m2 == -INFINITY ? 0.0f : m2;
+      s *= exp2f(m - base);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) s = fmaf(v[u].y, exp2f(v[u].x - base), s);
+      m = m2;
     }
   }
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) merge(__shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, s, off));
-  if ((threadIdx.x & 31) < kJoinTokens) sm[warp][tok] = m, ss[warp][tok] = s;
+  for (int off = TOK; off < 32; off <<= 1)
+    merge(__shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, s, off));
+  if ((threadIdx.x & 31) < TOK) sm[warp][tok] = m, ss[warp][tok] = s;
   __syncthreads();
   if (warp == 0) {
     m = -INFINITY, s = 0.0f;
-    for (int i = lane; i < 32; i += 8) merge(sm[i][tok], ss[i][tok]);
+    for (int i = lane; i < 32; i += 32 / TOK) merge(sm[i][tok], ss[i][tok]);
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1)
+    for (int off = TOK; off < 32; off <<= 1)
       merge(__shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, s, off));
-    if (threadIdx.x < kJoinTokens && t < T) {
+    if (threadIdx.x < TOK && t < T) {
       const float l = (m + log2f(s)) * 0.6931471805599453f;
       const int32_t tgt = target[t];
       if (tgt >= V) set_status(st, MOE_ERR_DEVICE_BAD_INPUT, (int32_t)t);
@@ -760,7 +903,8 @@ bool head_tc(const moe_head_config_t& c) { return c.act_dtype == MOE_DTYPE_BF16 
 }  // namespace
 
 // A piece holds at most 256 MB of dz unless the caller names its length; whole 256-column
-// tiles. The input gradient's K is split where its tiles alone would not fill the SMs.
+// tiles. The SIMT input gradient splits K where its tiles alone would not fill the SMs, into
+// slices [splits][T, H]; the tensor cores' split is head_split's.
 HeadScratch head_scratch(const moe_head_config_t& c) {
   HeadScratch L{};
   const bool tc = head_tc(c);
@@ -771,18 +915,16 @@ HeadScratch head_scratch(const moe_head_config_t& c) {
   L.piece = piece;
   L.ld = (int)piece;
   const int64_t rows = std::min<int64_t>(piece, c.V);
-  int64_t tiles, units, most;
+  const bool one = piece >= c.V;
+  size_t dx_bytes;
   if (tc) {
-    const bool small = c.T <= 128;
-    tiles = small ? ceil_div(c.H, 128) : ceil_div(T, 256) * ceil_div(c.H, 256);
-    units = small ? 152 : 76;
-    most = ceil_div(rows, 64) / 8;  // at least 8 K stages a split
+    L.split = tc::head_split(T, c.H, rows);
+    dx_bytes = one ? 0 : (size_t)T * c.H * 4;
   } else {
-    tiles = ceil_div(T, ST) * ceil_div(c.H, ST);
-    units = 152 * 2;
-    most = rows / 64;
+    const int64_t tiles = ceil_div(T, ST) * ceil_div(c.H, ST);
+    L.split = {0, (int)std::max<int64_t>(1, std::min<int64_t>({152 * 2 / tiles, rows / 64, 64})), 0};
+    dx_bytes = one && L.split.splits == 1 ? 0 : (size_t)L.split.splits * T * c.H * 4;
   }
-  L.splits = (int)std::max<int64_t>(1, std::min<int64_t>({units / tiles, most, 64}));
   size_t o = kWsHead;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -793,7 +935,8 @@ HeadScratch head_scratch(const moe_head_config_t& c) {
   L.part = take((size_t)ceil_div(c.V, 128) * 2 * T * 8);
   L.target_logit = take((size_t)T * 4);
   L.dlogits = take((size_t)T * piece * esize);
-  L.dx = take((size_t)L.splits * T * c.H * 4);
+  L.dx = take(dx_bytes);
+  L.slices = take(L.split.bytes);
   L.total = o;
   return L;
 }
@@ -823,8 +966,11 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
   }
   if (e != cudaSuccess) return e;
   // the ticket lives in the head, which moe_workspace_init clears
-  join_kernel<<<(unsigned)ceil_div(c.T, kJoinTokens), 1024, 0, s>>>(part, parts, c.T, c.V, target, tl, loss, lse, mean,
-                                                                   reinterpret_cast<uint32_t*>(b + 320), st);
+  auto* ticket = reinterpret_cast<uint32_t*>(b + 320);
+  if (c.T >= 1024)
+    join_kernel<32><<<(unsigned)ceil_div(c.T, 32), 1024, 0, s>>>(part, parts, c.T, c.V, target, tl, loss, lse, mean, ticket, st);
+  else
+    join_kernel<4><<<(unsigned)ceil_div(c.T, 4), 1024, 0, s>>>(part, parts, c.T, c.V, target, tl, loss, lse, mean, ticket, st);
   return cudaGetLastError();
 }
 
@@ -834,7 +980,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   if (c.T == 0)
     return dw ? cudaMemsetAsync(dw, 0, (size_t)c.V * c.H * (c.grad_dtype == MOE_DTYPE_F32 ? 4 : 2), s) : cudaSuccess;
   const HeadScratch L = head_scratch(c);
-  const bool tc = head_tc(c), one = L.piece >= c.V && L.splits == 1;
+  const bool tc = head_tc(c), one = L.piece >= c.V && (tc || L.split.splits == 1);
   char* b = static_cast<char*>(ws);
   float* slices = reinterpret_cast<float*>(b + L.dx);
   const int f32 = c.act_dtype == MOE_DTYPE_F32;
@@ -843,7 +989,8 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     cudaError_t e;
     if (tc) {
       e = tc::launch_head_piece(c, x, w, target, lse, dloss, mean, v0, rows, b + L.dlogits, L.ld,
-                                dx ? (one ? dx : slices) : nullptr, L.splits, !one, v0 > 0, dw, st, s);
+                                dx ? (one ? dx : slices) : nullptr, L.split, reinterpret_cast<float*>(b + L.slices),
+                                !one, v0 > 0, dw, st, s);
       if (e != cudaSuccess) return e;
       continue;
     }
@@ -857,7 +1004,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     SimtParams q{};
     q.A = b + L.dlogits, q.a_f32 = 1, q.splits = 1;
     if (dx) {
-      q.M = c.T, q.N = c.H, q.K = rows, q.splits = L.splits;
+      q.M = c.T, q.N = c.H, q.K = rows, q.splits = L.split.splits;
       q.a_row = L.ld, q.a_k = 1;
       q.B = p.B, q.b_row = 1, q.b_k = c.H, q.b_f32 = f32;
       q.out = one ? dx : slices, q.ldo = c.H, q.out_f32 = one ? f32 : 1, q.add = v0 > 0;
@@ -874,9 +1021,10 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   }
   if (!dx || one) return cudaSuccess;
   const int64_t n = (int64_t)c.T * c.H;
+  const int splits = tc ? 1 : L.split.splits;
   const unsigned grid = (unsigned)ceil_div(n, 256);
-  if (f32) join_dx_kernel<float><<<grid, 256, 0, s>>>(slices, L.splits, n, static_cast<float*>(dx));
-  else join_dx_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(slices, L.splits, n, static_cast<__nv_bfloat16*>(dx));
+  if (f32) join_dx_kernel<float><<<grid, 256, 0, s>>>(slices, splits, n, static_cast<float*>(dx));
+  else join_dx_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(slices, splits, n, static_cast<__nv_bfloat16*>(dx));
   return cudaGetLastError();
 }
 

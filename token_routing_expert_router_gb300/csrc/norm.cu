@@ -13,6 +13,7 @@
 // it keeps several rows in flight per CTA while the row sums of the current one are formed.
 // Widths that are not a multiple of 16 bytes take plain element loads (VEC = 1).
 #include <algorithm>
+#include <atomic>
 
 #include "step.cuh"
 
@@ -448,15 +449,23 @@ Shape shape_of(int nvec, int vpt) {
   return s;
 }
 
+// Persistent grid of an instantiation. What fits on an SM depends on the threads of a row only;
+// the last answer is kept (one word, so that concurrent callers see a whole one).
 template <typename K>
-cudaError_t grid_of(K kern, const Shape& sh, size_t smem, int64_t T, int* grid) {
-  cudaError_t e = cudaSuccess;
-  if (smem > 32 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, sh.tpr * sh.groups, smem);
-  if (e != cudaSuccess) return e;
-  *grid = (int)std::min<int64_t>(ceil_div(T, sh.groups), (int64_t)std::min(tc::num_sms(), kNormMaxSms) * std::max(1, per_sm));
+cudaError_t grid_of(K kern, std::atomic<uint32_t>& last, const Shape& sh, size_t smem, int64_t T, int* grid) {
+  uint32_t known = last.load(std::memory_order_relaxed);  // tpr << 8 | blocks per SM
+  if (known >> 8 != (uint32_t)sh.tpr) {
+    cudaError_t e = cudaSuccess;
+    if (smem > 32 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, sh.tpr * sh.groups, smem);
+    if (e != cudaSuccess) return e;
+    known = (uint32_t)sh.tpr << 8 | (uint32_t)std::max(1, per_sm);
+    last.store(known, std::memory_order_relaxed);
+  }
+  *grid = (int)std::min<int64_t>(ceil_div(T, sh.groups),
+                                 (int64_t)std::min(tc::num_sms(), kNormMaxSms) * (known & 255));
   return cudaSuccess;
 }
 
@@ -466,7 +475,8 @@ cudaError_t fwd(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, 
   const size_t smem = (size_t)STAGES * 2 * VPT * sh.tpr * sh.groups * 16;
   auto kern = block_norm_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES>;
   int grid = 0;
-  cudaError_t e = grid_of(kern, sh, smem, c.T, &grid);
+  static std::atomic<uint32_t> last{0};
+  cudaError_t e = grid_of(kern, last, sh, smem, c.T, &grid);
   if (e != cudaSuccess) return e;
   kern<<<grid, dim3(sh.tpr, sh.groups), smem, s>>>(in, r, n, c.T, c.H, c.eps, c.res_scale);
   return cudaGetLastError();
@@ -478,7 +488,8 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
   const size_t smem = (size_t)STAGES * 4 * VPT * sh.tpr * sh.groups * 16;
   auto kern = block_norm_bwd_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES>;
   int grid = 0;
-  cudaError_t e = grid_of(kern, sh, smem, c.T, &grid);
+  static std::atomic<uint32_t> last{0};
+  cudaError_t e = grid_of(kern, last, sh, smem, c.T, &grid);
   if (e != cudaSuccess) return e;
   kern<<<grid, dim3(sh.tpr, sh.groups), smem, s>>>(b, part, c.T, c.H, c.eps, c.res_scale);
   e = cudaGetLastError();
