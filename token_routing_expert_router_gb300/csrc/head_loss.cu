@@ -670,15 +670,18 @@ cudaError_t launch_head_piece(const moe_head_config_t& c, const void* x, const v
 
 namespace {
 
-// ---- exact fp32 tiles: 128 x 128 outputs per block, 8 x 8 per thread, K steps of 16
-constexpr int ST = 128, SK = 16;
+// ---- exact fp32 tiles, K steps of 16. ST = 128: 8 x 8 outputs per thread of 256; ST = 64: 8 x 4
+// of 128, for products whose 128-tiles would leave SMs without a block (256 x 128 x 5003: 35 us
+// for 80 blocks of 128 x 128).
+constexpr int SK = 16;
 
 struct SimtParams {
   int M, N, K;
-  int splits;                  // DX: K splits
+  int splits, k_split;         // DX: K splits of k_split (a multiple of SK) each
   const void *A, *B;           // operand element (row, k) at row * r + k * k
   int64_t a_row, a_k, b_row, b_k;
   int a_f32, b_f32;            // element types (else bf16)
+  int vec;                     // rows of both operands begin on multiples of 4 elements
   const int32_t* target;
   float2* part;
   float* target_logit;
@@ -692,61 +695,113 @@ struct SimtParams {
 __device__ __forceinline__ float load_elem(const void* p, int64_t at, int f32) {
   return f32 ? static_cast<const float*>(p)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
 }
+__device__ __forceinline__ float4 load_elem4(const void* p, int64_t at, int f32) {
+  if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+  const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
 
 enum { S_STATS = 0, S_DLOGITS = 1, S_STORE = 2 };
 
-template <int MODE>
-__global__ void __launch_bounds__(256) simt_kernel(const SimtParams p) {
-  __shared__ float sa[SK][ST + 4], sb[SK][ST + 4];
+template <int MODE, int ST>
+__global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
+  constexpr int TN = ST / 16, NT = ST * 2, LD = ST + 4;
+  __shared__ __align__(16) float sa[2][SK][LD], sb[2][SK][LD];
   const int m0 = blockIdx.x * ST, n0 = blockIdx.y * ST;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int k_lo = (int)((int64_t)p.K * blockIdx.z / p.splits), k_hi = (int)((int64_t)p.K * (blockIdx.z + 1) / p.splits);
-  float acc[8][8];
+  const int k_lo = blockIdx.z * p.k_split, k_hi = min(p.K, k_lo + p.k_split);
+  float acc[8][TN];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-  // consecutive threads read along the operand's contiguous direction
-  auto fill = [&](float (*dst)[ST + 4], const void* src, int64_t rstep, int64_t kstep, int f32, int r0, int rows, int k0) {
+    for (int j = 0; j < TN; ++j) acc[i][j] = 0.0f;
+  // Four elements per thread and step, along the operand's contiguous direction: ST * SK / 4 / NT = 2 steps.
+  auto place = [&](int64_t kstep, int i, int* r, int* k) {
+    const int e = threadIdx.x + i * NT;
+    if (kstep == 1) *r = e / (SK / 4), *k = e % (SK / 4) * 4;
+    else *r = e % (ST / 4) * 4, *k = e / (ST / 4);
+  };
+  auto fetch = [&](float4 (&v)[2], const void* src, int64_t rstep, int64_t kstep, int f32, int r0, int rows, int k0) {
 #pragma unroll
-    for (int i = 0; i < ST * SK / 256; ++i) {
-      const int e = threadIdx.x + i * 256;
-      const int r = kstep == 1 ? e / SK : e % ST, k = kstep == 1 ? e % SK : e / ST;
-      float v = 0.0f;
-      if (r0 + r < rows && k0 + k < k_hi) v = load_elem(src, (int64_t)(r0 + r) * rstep + (int64_t)(k0 + k) * kstep, f32);
-      dst[k][r] = v;
+    for (int i = 0; i < 2; ++i) {
+      int r, k;
+      place(kstep, i, &r, &k);
+      const int64_t at = (int64_t)(r0 + r) * rstep + (int64_t)(k0 + k) * kstep;
+      const bool along_k = kstep == 1;
+      const int left = along_k ? (r0 + r < rows ? k_hi - (k0 + k) : 0) : (k0 + k < k_hi ? rows - (r0 + r) : 0);
+      if (p.vec && left >= 4) {
+        v[i] = load_elem4(src, at, f32);
+      } else {
+        const int64_t step = along_k ? kstep : rstep;
+        v[i].x = left > 0 ? load_elem(src, at, f32) : 0.0f;
+        v[i].y = left > 1 ? load_elem(src, at + step, f32) : 0.0f;
+        v[i].z = left > 2 ? load_elem(src, at + 2 * step, f32) : 0.0f;
+        v[i].w = left > 3 ? load_elem(src, at + 3 * step, f32) : 0.0f;
+      }
     }
   };
+  auto keep = [&](float (*dst)[LD], const float4 (&v)[2], int64_t kstep) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int r, k;
+      place(kstep, i, &r, &k);
+      if (kstep == 1) {
+        dst[k][r] = v[i].x, dst[k + 1][r] = v[i].y, dst[k + 2][r] = v[i].z, dst[k + 3][r] = v[i].w;
+      } else {
+        *reinterpret_cast<float4*>(&dst[k][r]) = v[i];
+      }
+    }
+  };
+  float4 va[2], vb[2];
+  if (k_lo < k_hi) {
+    fetch(va, p.A, p.a_row, p.a_k, p.a_f32, m0, p.M, k_lo);
+    fetch(vb, p.B, p.b_row, p.b_k, p.b_f32, n0, p.N, k_lo);
+    keep(sa[0], va, p.a_k);
+    keep(sb[0], vb, p.b_k);
+  }
+  __syncthreads();
+  int buf = 0;
   for (int k0 = k_lo; k0 < k_hi; k0 += SK) {
-    fill(sa, p.A, p.a_row, p.a_k, p.a_f32, m0, p.M, k0);
-    fill(sb, p.B, p.b_row, p.b_k, p.b_f32, n0, p.N, k0);
-    __syncthreads();
+    const bool more = k0 + SK < k_hi;
+    if (more) {  // the next step's loads fly while this one is multiplied
+      fetch(va, p.A, p.a_row, p.a_k, p.a_f32, m0, p.M, k0 + SK);
+      fetch(vb, p.B, p.b_row, p.b_k, p.b_f32, n0, p.N, k0 + SK);
+    }
 #pragma unroll
     for (int k = 0; k < SK; ++k) {
-      float a[8], b[8];
+      float a[8], b[TN];
+      *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 8]);
+      *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 8 + 4]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = sa[k][ty * 8 + i], b[i] = sb[k][tx + 16 * i];
+      for (int j = 0; j < TN; j += 4)
+        *reinterpret_cast<float4*>(b + j) = *reinterpret_cast<const float4*>(&sb[buf][k][j * 16 + tx * 4]);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+    if (more) {
+      keep(sa[buf ^ 1], va, p.a_k);
+      keep(sb[buf ^ 1], vb, p.b_k);
     }
     __syncthreads();
+    buf ^= 1;
   }
-  // the thread's rows m0 + 8 ty + i, columns n0 + tx + 16 j
+  // the thread's rows m0 + 8 ty + i, columns n0 + 64 (j / 4) + 4 tx + j % 4
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = m0 + ty * 8 + i;
     const bool live = row < p.M;
+    auto col_of = [&](int j) { return n0 + j / 4 * 64 + tx * 4 + j % 4; };
     if constexpr (MODE == S_STATS) {
       constexpr float kLog2e = 1.4426950408889634f;
       const int tgt = live ? p.target[row] : -1;
       float m = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int col = n0 + tx + 16 * j;
-        if (col < p.N) {
-          if (col == tgt) p.target_logit[row] = acc[i][j];
+      for (int j = 0; j < TN; ++j) {
+        if (col_of(j) < p.N) {
+          if (col_of(j) == tgt) p.target_logit[row] = acc[i][j];
           m = fmaxf(m, acc[i][j] * kLog2e);
         }
       }
@@ -755,46 +810,71 @@ __global__ void __launch_bounds__(256) simt_kernel(const SimtParams p) {
       const float base = m == -INFINITY ? 0.0f : m;
       float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (n0 + tx + 16 * j < p.N) s += exp2f(fmaf(acc[i][j], kLog2e, -base));
+      for (int j = 0; j < TN; ++j)
+        if (col_of(j) < p.N) s += exp2f(fmaf(acc[i][j], kLog2e, -base));
 #pragma unroll
       for (int off = 8; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       if (tx == 0 && live) p.part[(int64_t)blockIdx.y * p.M + row] = make_float2(m, s);
-    } else if constexpr (MODE == S_DLOGITS) {
-      if (live) {
-        const int tgt = p.target[row];
-        const bool counts = tgt >= 0 && tgt < p.V;
-        const float lse = p.lse[row], g = p.dloss ? p.dloss[row] : p.mean[1];
+    } else if (live) {
+      float lse = 0.0f, g = 0.0f;
+      int tgt = -1;
+      bool counts = false;
+      if constexpr (MODE == S_DLOGITS) {
+        tgt = p.target[row];
+        counts = tgt >= 0 && tgt < p.V;
+        lse = p.lse[row];
+        g = p.dloss ? p.dloss[row] : p.mean[1];
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int col = n0 + tx + 16 * j;
-          if (col < p.N) {
-            float pr = expf(acc[i][j] - lse);
-            if (col + p.v0 == tgt) pr -= 1.0f;
-            static_cast<float*>(p.out)[(int64_t)row * p.ldo + col] = counts ? pr * g : 0.0f;
+      for (int j0 = 0; j0 < TN; j0 += 4) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] = acc[i][j0 + j];
+          if constexpr (MODE == S_DLOGITS) {
+            v[j] = expf(v[j] - lse);
+            if (col_of(j0 + j) + p.v0 == tgt) v[j] -= 1.0f;
+            v[j] = counts ? v[j] * g : 0.0f;
           }
         }
-      }
-    } else if (live) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int col = n0 + tx + 16 * j;
-        if (col >= p.N) continue;
+        const int col = col_of(j0);
         const int64_t at = ((int64_t)blockIdx.z * p.M + row) * p.ldo + col;
-        if (p.out_f32) {
-          float* o = static_cast<float*>(p.out) + at;
-          *o = p.add ? *o + acc[i][j] : acc[i][j];
-        } else {
-          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc[i][j]);
+        if (p.out_f32 && p.ldo % 4 == 0 && col + 3 < p.N) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+          if (p.add) {
+            const float4 w = *o;
+            v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+          }
+          *o = make_float4(v[0], v[1], v[2], v[3]);
+          continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (col + j >= p.N) break;
+          if (p.out_f32) {
+            float* o = static_cast<float*>(p.out) + at + j;
+            *o = p.add ? *o + v[j] : v[j];
+          } else {
+            static_cast<__nv_bfloat16*>(p.out)[at + j] = __float2bfloat16_rn(v[j]);
+          }
         }
       }
     }
   }
 }
 
+// The tile of a product: 64 while the 128-tiles do not give every SM two blocks.
+int simt_tile(int64_t M, int64_t N, int splits) {
+  return ceil_div(M, 128) * ceil_div(N, 128) * splits >= 2 * 152 ? 128 : 64;
+}
+
 template <int MODE>
-cudaError_t launch_simt(const SimtParams& p, cudaStream_t s) {
-  simt_kernel<MODE><<<dim3((unsigned)ceil_div(p.M, ST), (unsigned)ceil_div(p.N, ST), (unsigned)p.splits), 256, 0, s>>>(p);
+cudaError_t launch_simt(SimtParams p, cudaStream_t s) {
+  p.k_split = (int)(ceil_div(ceil_div(p.K, p.splits), SK) * SK);
+  const int st = simt_tile(p.M, p.N, p.splits);
+  const dim3 grid((unsigned)ceil_div(p.M, st), (unsigned)ceil_div(p.N, st), (unsigned)p.splits);
+  if (st == 128) simt_kernel<MODE, 128><<<grid, 256, 0, s>>>(p);
+  else simt_kernel<MODE, 64><<<grid, 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -893,7 +973,8 @@ __global__ void __launch_bounds__(256) join_dx_kernel(const float* slices, int s
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float v = 0.0f;
-  for (int k = 0; k < splits; ++k) v += slices[k * n + i];
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k) v += __ldg(slices + k * n + i);
   if constexpr (sizeof(T) == 4) dx[i] = v;
   else dx[i] = __float2bfloat16_rn(v);
 }
@@ -921,7 +1002,7 @@ HeadScratch head_scratch(const moe_head_config_t& c) {
     L.split = tc::head_split(T, c.H, rows);
     dx_bytes = one ? 0 : (size_t)T * c.H * 4;
   } else {
-    const int64_t tiles = ceil_div(T, ST) * ceil_div(c.H, ST);
+    const int64_t tiles = ceil_div(T, 64) * ceil_div(c.H, 64);
     L.split = {0, (int)std::max<int64_t>(1, std::min<int64_t>({152 * 2 / tiles, rows / 64, 64})), 0};
     dx_bytes = one && L.split.splits == 1 ? 0 : (size_t)L.split.splits * T * c.H * 4;
   }
@@ -954,13 +1035,13 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
     parts = 2 * (int)ceil_div(c.V, tc::head_tile_cols(c.T));
     e = tc::launch_head_stats(c, x, w, target, part, tl, st, s);
   } else {
-    parts = (int)ceil_div(c.V, ST);
+    parts = (int)ceil_div(c.V, simt_tile(c.T, c.V, 1));
     const int f32 = c.act_dtype == MOE_DTYPE_F32;
     SimtParams p{};
     p.M = c.T, p.N = c.V, p.K = c.H, p.splits = 1;
     p.A = x, p.B = w;
     p.a_row = p.b_row = c.H, p.a_k = p.b_k = 1;
-    p.a_f32 = p.b_f32 = f32;
+    p.a_f32 = p.b_f32 = f32, p.vec = c.H % 4 == 0;
     p.target = target, p.part = part, p.target_logit = tl;
     e = launch_simt<S_STATS>(p, s);
   }
@@ -999,10 +1080,10 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     p.A = x, p.a_row = c.H, p.a_k = 1, p.a_f32 = f32;
     p.B = static_cast<const char*>(w) + v0 * c.H * (f32 ? 4 : 2), p.b_row = c.H, p.b_k = 1, p.b_f32 = f32;
     p.target = target, p.lse = lse, p.dloss = dloss, p.mean = mean, p.v0 = (int)v0, p.V = c.V;
-    p.out = b + L.dlogits, p.ldo = L.ld, p.out_f32 = 1;
+    p.out = b + L.dlogits, p.ldo = L.ld, p.out_f32 = 1, p.vec = c.H % 4 == 0;
     if ((e = launch_simt<S_DLOGITS>(p, s)) != cudaSuccess) return e;
     SimtParams q{};
-    q.A = b + L.dlogits, q.a_f32 = 1, q.splits = 1;
+    q.A = b + L.dlogits, q.a_f32 = 1, q.splits = 1, q.vec = c.H % 4 == 0;
     if (dx) {
       q.M = c.T, q.N = c.H, q.K = rows, q.splits = L.split.splits;
       q.a_row = L.ld, q.a_k = 1;

@@ -2,15 +2,17 @@
 //   u = y rho(y) w_post            (u = y without w_post)
 //   r = res_scale x + g_t G_c u    (token gate g, channel gate G; 1 where absent)
 //   n = r rho(r) w_next
-// with rho(v) = 1 / sqrt(mean_c v_c^2 + eps). One pass: x and y are read once, r and n
-// written once; the two row sums are taken from registers.
+// with rho(v) = 1 / sqrt(mean_c v_c^2 + eps). x and y are read once, r and n written once.
 //
-// What bounds it: DRAM. A row group of TPR threads owns a row at a time and every thread the
-// same channels of each row, so the per-channel weights stay in registers over the rows of a
-// persistent CTA (w_post G is one product; read per row they would be more L2 traffic than
-// the row itself). Rows arrive through a ring of cp.async stages in shared memory: a thread
-// reads back only the 16-byte pieces it asked for itself, so the ring needs no barrier, and
-// it keeps several rows in flight per CTA while the row sums of the current one are formed.
+// What bounds it: DRAM, once the row sums are out of the way. A row group of TPR threads owns a
+// row at a time and every thread the same channels of each row, so the per-channel weights stay
+// in registers over the rows of a persistent CTA (w_post G is one product; read per row they
+// would be more L2 traffic than the row itself). Rows arrive through a ring of cp.async stages
+// in shared memory: a thread reads back only the 16-byte pieces it asked for itself, so the
+// ring needs no barrier. The row sums do need one each, and a CTA that does nothing else
+// meanwhile is bound by them; so the forward takes two rows through its two sums together, and
+// the backward adds up one row while it finishes the row before. Products go two at a time
+// (fma.f32x2): with the weights and conversions a row is otherwise near the issue limit.
 // Widths that are not a multiple of 16 bytes take plain element loads (VEC = 1).
 #include <algorithm>
 #include <atomic>
@@ -21,34 +23,46 @@ namespace moe {
 
 namespace {
 
+// Values in pairs where a piece holds more than one.
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float fold(float2 a) { return a.x + a.y; }
+__device__ __forceinline__ float fold(float a) { return a; }
+__device__ __forceinline__ void splat(float v, float2* o) { *o = make_float2(v, v); }
+__device__ __forceinline__ void splat(float v, float* o) { *o = v; }
+
 template <typename T, int VEC>
-struct Piece;  // VEC consecutive elements of a row, as loaded
+struct Piece;  // VEC consecutive elements of a row, as loaded; N values of type E in fp32
 template <>
 struct Piece<float, 4> {
+  using E = float2;
+  static constexpr int N = 2;
   uint4 v;
-  __device__ void to(float (&f)[4]) const {
-    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  __device__ __forceinline__ void to(E (&f)[N]) const {
+    f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  __device__ static Piece of(const float (&f)[4]) {
-    return {make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]))};
+  __device__ __forceinline__ static Piece of(const E (&f)[N]) {
+    return {make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y))};
   }
 };
 template <>
 struct Piece<__nv_bfloat16, 8> {
+  using E = float2;
+  static constexpr int N = 4;
   uint4 v;
-  __device__ void to(float (&f)[8]) const {
+  __device__ __forceinline__ void to(E (&f)[N]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  __device__ static Piece of(const float (&f)[8]) {
+  __device__ __forceinline__ static Piece of(const E (&f)[N]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(f[i].x, f[i].y);
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
     return {make_uint4(w[0], w[1], w[2], w[3])};
@@ -56,15 +70,19 @@ struct Piece<__nv_bfloat16, 8> {
 };
 template <>
 struct Piece<float, 1> {
+  using E = float;
+  static constexpr int N = 1;
   float v;
-  __device__ void to(float (&f)[1]) const { f[0] = v; }
-  __device__ static Piece of(const float (&f)[1]) { return {f[0]}; }
+  __device__ __forceinline__ void to(E (&f)[N]) const { f[0] = v; }
+  __device__ __forceinline__ static Piece of(const E (&f)[N]) { return {f[0]}; }
 };
 template <>
 struct Piece<__nv_bfloat16, 1> {
+  using E = float;
+  static constexpr int N = 1;
   __nv_bfloat16 v;
-  __device__ void to(float (&f)[1]) const { f[0] = __bfloat162float(v); }
-  __device__ static Piece of(const float (&f)[1]) { return {__float2bfloat16_rn(f[0])}; }
+  __device__ __forceinline__ void to(E (&f)[N]) const { f[0] = __bfloat162float(v); }
+  __device__ __forceinline__ static Piece of(const E (&f)[N]) { return {__float2bfloat16_rn(f[0])}; }
 };
 
 __device__ __forceinline__ void cp16(void* dst, const void* src) {
@@ -77,335 +95,388 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Sums NV values over the TPR threads of each row group (blockDim = (TPR, groups), TPR a
-// multiple of 32) in a fixed order; every thread gets the sums. `buf` holds NV floats per
-// warp; the caller alternates two buffers, so one barrier per call is enough.
-template <int NV>
-__device__ __forceinline__ void row_sum(float (&v)[NV], float* buf) {
-#pragma unroll
-  for (int off = 16; off; off >>= 1)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return;
-  float* b = buf + threadIdx.y * warps * NV;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) b[(threadIdx.x >> 5) * NV + i] = v[i];
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float t = lane < warps ? b[lane * NV + i] : 0.0f;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    v[i] = t;
-  }
-}
-
+// Row sums of NV values over the TPR threads of a row group (blockDim = (TPR, groups), TPR a
+// multiple of 32), in a fixed order, in two halves so that a barrier of the caller's stands
+// between them. Both work on kP values at once (NV rounded up to a power of two): a lane ends
+// up with the value lane / (32 / kP), which takes 9 shuffles for 8 values instead of 40.
 constexpr int kMaxWarps = 32;
 constexpr int kNormMaxSms = 152;  // bounds the grid, and so the backward's column partial sums
+template <int NV>
+struct RowSums {
+  static constexpr int kP = NV <= 1 ? 1 : NV <= 2 ? 2 : NV <= 4 ? 4 : 8;
+  static constexpr int kLanes = 32 / kP;
+  float buf[2][kP * kMaxWarps];  // [parity][group][value][warp]
 
-// The ring of row stages: A arrays per row, VPT pieces per thread and array. Slot of
-// (stage, array, piece) for this thread: consecutive threads are 16 bytes apart.
-template <typename P, int A, int VPT, int STAGES>
-struct Ring {
-  P* base;
-  int threads, tid;
-  __device__ P* slot(int stage, int a, int j) const {
-    return base + ((stage * A + a) * VPT + j) * threads + tid;
+  __device__ __forceinline__ void publish(const float (&in)[NV], int parity) {
+    float v[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) v[i] = i < NV ? in[i < NV ? i : 0] : 0.0f;
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int n = kP / 2, off = 16; off; off >>= 1, n >>= 1) {
+      if (n >= 1) {
+        const bool upper = lane & off;
+#pragma unroll
+        for (int i = 0; i < kP / 2; ++i) {
+          if (i < n) {
+            const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+          }
+        }
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+      }
+    }
+    if (lane % kLanes == 0)
+      buf[parity][(threadIdx.y * kP + lane / kLanes) * warps + (threadIdx.x >> 5)] = v[0];
+  }
+  // The sums that were published with this parity, in every thread.
+  __device__ __forceinline__ void total(float (&out)[NV], int parity) const {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const float* b = buf[parity] + (threadIdx.y * kP + lane / kLanes) * warps;
+    float t = 0.0f;
+    for (int w = lane % kLanes; w < warps; w += kLanes) t += b[w];
+#pragma unroll
+    for (int off = kLanes / 2; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) out[i] = __shfl_sync(0xffffffffu, t, i * kLanes);
   }
 };
 
-template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
-__global__ void __launch_bounds__(MAXT)
-    block_norm_kernel(NormIn in, void* r_out, void* n_out, int T_, int H, float eps, float res_scale) {
-  using P = Piece<T, VEC>;
-  constexpr bool kAsync = STAGES > 0;
-  constexpr int kStages = kAsync ? STAGES : 1;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float sums[2][kMaxWarps];
-  int flip = 0;
-  const int tpr = blockDim.x, groups = blockDim.y;
-  const Ring<P, 2, VPT, kStages> ring{reinterpret_cast<P*>(smem), tpr * groups, (int)(threadIdx.y * tpr + threadIdx.x)};
-  const int nvec = H / VEC;
-  const P* x = static_cast<const P*>(in.x);
-  const P* y = static_cast<const P*>(in.y);
-  const float inv_h = 1.0f / (float)H;
+// A warp per row needs no barrier of the block.
+__device__ __forceinline__ void row_barrier() {
+  if (blockDim.x == 32) __syncwarp();
+  else __syncthreads();
+}
 
-  float wu[CACHE_W ? VPT : 1][VEC], wn[CACHE_W ? VPT : 1][VEC];
-  auto channel_weights = [&](int c, float (&a)[VEC], float (&b)[VEC]) {
+// A thread's pieces c = threadIdx.x + j TPR of a row's A arrays, from a ring of stages in shared
+// memory (MAXT threads wide, so that a piece's place is a constant away from the stage's), or,
+// with STAGES = 0, from global memory whenever they are asked for. An array that is not there
+// (src NULL) and pieces past the row read as zeros: their places in the ring are zeroed once.
+template <typename P, int A, int VPT, int MAXT, int STAGES>
+struct Rows {
+  static constexpr int kStage = A * VPT * MAXT;
+  P* ring;
+  const P* src[A];
+  int T, nvec;
+
+  __device__ __forceinline__ bool on(int j) const { return (int)(threadIdx.x + j * blockDim.x) < nvec; }
+  __device__ __forceinline__ void zero_ring() const {
+    P z{};
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int h = c * VEC + e;
-      float v = in.w_post ? __ldg(in.w_post + h) : 1.0f;
-      if (in.gate) v *= __ldg(in.gate + h);
-      a[e] = v;
-      b[e] = n_out ? __ldg(in.w_next + h) : 0.0f;
-    }
-  };
-  if constexpr (CACHE_W) {
+    for (int s = 0; s < STAGES; ++s)
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = threadIdx.x + j * tpr;
-      if (c < nvec) channel_weights(c, wu[j], wn[j]);
+      for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+          if (!src[a] || !on(j)) ring[s * kStage + (a * VPT + j) * MAXT] = z;
+  }
+  __device__ __forceinline__ void fetch(int64_t row, int stage) const {
+    if (row >= T) return;
+    const int64_t at = row * nvec + threadIdx.x;
+#pragma unroll
+    for (int a = 0; a < A; ++a)
+      if (src[a])
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+          if (on(j)) cp16(ring + stage * kStage + (a * VPT + j) * MAXT, src[a] + at + j * blockDim.x);
+  }
+  __device__ __forceinline__ void get(int64_t row, int stage, int a, int j, typename P::E (&f)[P::N]) const {
+    if constexpr (STAGES > 0) {
+      ring[stage * kStage + (a * VPT + j) * MAXT].to(f);
+    } else {
+      if (src[a] && row < T && on(j)) {
+        src[a][row * nvec + threadIdx.x + j * blockDim.x].to(f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < P::N; ++e) splat(0.0f, &f[e]);
+      }
     }
   }
+};
 
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row = (int64_t)blockIdx.x * groups + threadIdx.y;
-  const int64_t iters = ceil_div(T_ - (int64_t)blockIdx.x * groups, step);  // the same for every group of the CTA
-  auto fetch = [&](int64_t rw, int stage) {
-    if constexpr (kAsync) {
-      if (rw < T_) {
+// Per-channel weights of a thread's pieces: a = w_post G, b = w_next (0 past the row and where
+// there is no next norm).
+template <typename P, int VEC>
+__device__ __forceinline__ void channel_weights(const float* w_post, const float* gate, const float* w_next, int j, int H,
+                                                typename P::E (&a)[P::N], typename P::E (&b)[P::N]) {
+  const int h0 = (threadIdx.x + j * blockDim.x) * VEC;
+  float* fa = reinterpret_cast<float*>(a);
+  float* fb = reinterpret_cast<float*>(b);
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          const int c = threadIdx.x + j * tpr;
-          if (c < nvec) {
-            cp16(ring.slot(stage, 0, j), x + rw * nvec + c);
-            if (y) cp16(ring.slot(stage, 1, j), y + rw * nvec + c);
-          }
-        }
-      }
+  for (int e = 0; e < VEC; ++e) {
+    const bool in = h0 + e < H;
+    float v = !in ? 0.0f : w_post ? __ldg(w_post + h0 + e) : 1.0f;
+    if (in && gate) v *= __ldg(gate + h0 + e);
+    fa[e] = v;
+    fb[e] = in && w_next ? __ldg(w_next + h0 + e) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ float inv_rms(float sum, float inv_h, float eps) { return rsqrtf(fmaf(sum, inv_h, eps)); }
+
+// ROWS rows per iteration: i ROWS + k is row (first + (i ROWS + k) step) of the group.
+template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
+    block_norm_kernel(NormIn in, void* r_out, void* n_out, int T_, int H, float eps, float res_scale) {
+  using P = Piece<T, VEC>;
+  using E = typename P::E;
+  constexpr int N = P::N, ROWS = STAGES > 0 ? 2 : 1;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ RowSums<ROWS> sums;
+  const int groups = blockDim.y, nvec = H / VEC;
+  const float inv_h = 1.0f / (float)H;
+  using R = Rows<P, 2, VPT, MAXT, STAGES * ROWS>;
+  const R rows{reinterpret_cast<P*>(smem) + threadIdx.y * blockDim.x + threadIdx.x,
+               {static_cast<const P*>(in.x), static_cast<const P*>(in.y)}, T_, nvec};
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row0 = (int64_t)blockIdx.x * groups + threadIdx.y;
+  // the same for every group of the CTA: the rows of its first one
+  const int iters = (int)ceil_div(ceil_div(T_ - (int64_t)blockIdx.x * groups, step), ROWS);
+  rows.zero_ring();
+  auto fetch = [&](int64_t row, int stage) {
+    if constexpr (STAGES > 0) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) rows.fetch(row + k * step, stage * ROWS + k);
       cp_commit();
     }
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(row + i * step, i);
+  for (int i = 0; i < STAGES; ++i) fetch(row0 + i * ROWS * step, i);
+
+  E wu[CACHE_W ? VPT : 1][N], wn[CACHE_W ? VPT : 1][N];
+  auto weights = [&](int j) {
+    channel_weights<P, VEC>(in.w_post, in.gate, n_out ? in.w_next : nullptr, j, H, wu[CACHE_W ? j : 0], wn[CACHE_W ? j : 0]);
+  };
+  if constexpr (CACHE_W) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) weights(j);
+  }
+  E scale;
+  splat(res_scale, &scale);
+
   int stage = 0;
-  for (int64_t it = 0; it < iters; ++it, row += step) {
-    if constexpr (kAsync) {
-      // the stage asked for now was read one iteration ago, by this thread alone
-      fetch(row + (kStages - 1) * step, (stage + kStages - 1) % kStages);
-      cp_wait<kStages - 1>();
-    }
-    const bool live = row < T_;
-    float v[VPT][VEC], s1[1] = {0.0f};
-    float yv[VPT][VEC];
+  for (int it = 0; it < iters; ++it, row0 += ROWS * step) {
+    if constexpr (STAGES > 0) cp_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
+    float su[ROWS], s[ROWS];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = threadIdx.x + j * tpr;
-      const bool on = live && c < nvec;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[j][e] = yv[j][e] = 0.0f;
-      if (on) {
-        if constexpr (kAsync) {
-          ring.slot(stage, 0, j)->to(v[j]);
-          if (y) ring.slot(stage, 1, j)->to(yv[j]);
-        } else {
-          x[row * nvec + c].to(v[j]);
-          if (y) y[row * nvec + c].to(yv[j]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s1[0] = fmaf(yv[j][e], yv[j][e], s1[0]);
-    }
-    float su = 1.0f;
+    for (int k = 0; k < ROWS; ++k) su[k] = 1.0f;
     if (in.w_post) {
-      row_sum(s1, sums[flip ^= 1]);
-      su = 1.0f / sqrtf(fmaf(s1[0], inv_h, eps));
-    }
-    if (in.token_gate && live) su *= __ldg(in.token_gate + row);
-    float s2[1] = {0.0f};
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = threadIdx.x + j * tpr;
-      float a[VEC], b[VEC];
-      if constexpr (!CACHE_W)
-        if (c < nvec) channel_weights(c, a, b);
+      for (int k = 0; k < ROWS; ++k) {
+        E t;
+        splat(0.0f, &t);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        v[j][e] *= res_scale;
-        if (y && c < nvec) v[j][e] = fmaf(yv[j][e] * su, CACHE_W ? wu[CACHE_W ? j : 0][e] : a[e], v[j][e]);
-        s2[0] = fmaf(v[j][e], v[j][e], s2[0]);
+        for (int j = 0; j < VPT; ++j) {
+          E y[N];
+          rows.get(row0 + k * step, stage * ROWS + k, 1, j, y);
+#pragma unroll
+          for (int e = 0; e < N; ++e) t = fma(y[e], y[e], t);
+        }
+        s[k] = fold(t);
       }
-      if (r_out && live && c < nvec) static_cast<P*>(r_out)[row * nvec + c] = P::of(v[j]);
+      sums.publish(s, 0);
+      row_barrier();
+      sums.total(s, 0);
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) su[k] = inv_rms(s[k], inv_h, eps);
     }
-    if (n_out) {
-      row_sum(s2, sums[flip ^= 1]);
-      // n is formed from r before its rounding to the activation type
-      const float rho = 1.0f / sqrtf(fmaf(s2[0], inv_h, eps));
+    E v[ROWS][VPT][N];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t row = row0 + k * step;
+      if (in.token_gate && row < T_) su[k] *= __ldg(in.token_gate + row);
+      E f, t;
+      splat(su[k], &f);
+      splat(0.0f, &t);
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int c = threadIdx.x + j * tpr;
-        if (live && c < nvec) {
-          float a[VEC], b[VEC], o[VEC];
-          if constexpr (!CACHE_W) channel_weights(c, a, b);
+        E y[N];
+        rows.get(row, stage * ROWS + k, 0, j, v[k][j]);
+        rows.get(row, stage * ROWS + k, 1, j, y);
+        if constexpr (!CACHE_W) weights(j);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) o[e] = v[j][e] * rho * (CACHE_W ? wn[CACHE_W ? j : 0][e] : b[e]);
-          static_cast<P*>(n_out)[row * nvec + c] = P::of(o);
+        for (int e = 0; e < N; ++e) {
+          v[k][j][e] = fma(mul(y[e], f), wu[CACHE_W ? j : 0][e], mul(v[k][j][e], scale));
+          t = fma(v[k][j][e], v[k][j][e], t);
+        }
+        if (r_out && row < T_ && rows.on(j))
+          static_cast<P*>(r_out)[row * nvec + threadIdx.x + j * blockDim.x] = P::of(v[k][j]);
+      }
+      s[k] = fold(t);
+    }
+    // the stage has been read; its next rows are asked for
+    fetch(row0 + STAGES * ROWS * step, stage);
+    if (STAGES > 0 && ++stage == STAGES) stage = 0;
+    if (n_out) {
+      sums.publish(s, 1);
+      row_barrier();
+      sums.total(s, 1);
+      // n is formed from r before its rounding to the activation type
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        const int64_t row = row0 + k * step;
+        E f;
+        splat(inv_rms(s[k], inv_h, eps), &f);
+        if (row < T_) {
+#pragma unroll
+          for (int j = 0; j < VPT; ++j) {
+            if constexpr (!CACHE_W) weights(j);
+            if (!rows.on(j)) continue;
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[k][j][e] = mul(mul(v[k][j][e], f), wn[CACHE_W ? j : 0][e]);
+            static_cast<P*>(n_out)[row * nvec + threadIdx.x + j * blockDim.x] = P::of(v[k][j]);
+          }
         }
       }
     }
-    if constexpr (kAsync) stage = (stage + 1) % kStages;
+    if (in.w_post && !n_out) row_barrier();  // sums' one buffer in use is free again
+    if (n_out && !in.w_post) row_barrier();
   }
 }
 
 // Backward, per row, from the stored residual r and block output y (both statistics are
 // formed again from them, so nothing else is kept from the forward):
-//   a = dn w_next;  dr' = dr + rho_r a - rho_r^3 r (sum_c a r) / H;   dx = res_scale dr'
-//   b = G w_post dr';  q = sum_c b y;  dy = g (rho_y b - rho_y^3 y q / H)
+//   a = dn w_next;  dr' = dr + rho_r a - k r,  k = rho_r^3 (sum_c a r) / H;   dx = res_scale dr'
+//   w = G w_post;  q = sum_c w dr' y;  dy = g (rho_y w dr' - rho_y^3 y q / H)
 //   dtoken_gate = rho_y q
 //   column sums over the rows: N = sum dn r rho_r = dw_next, S = sum g dr' y rho_y, from which
-//   dw_post = G S and dgate = w_post S (without w_post: rho_y = 1, dy = g b, dgate = S).
+//   dw_post = G S and dgate = w_post S (without w_post: rho_y = 1, dy = g w dr', dgate = S).
+// q is linear in dr', so q = sum w dr y + rho_r sum w a y - k sum w r y, and all six sums of a
+// row are formed in one go; row i's sums are added while row i - 1 is finished. Each term of q
+// is rounded relative to its own size, as the terms of dr' would be.
 // Each CTA keeps the column sums of its rows in registers and writes them once; colsum_kernel
 // adds the CTAs' sums in a fixed order.
 template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
-__global__ void __launch_bounds__(MAXT)
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
     block_norm_bwd_kernel(NormBwd b, float* part, int T_, int H, float eps, float res_scale) {
   using P = Piece<T, VEC>;
-  constexpr bool kAsync = STAGES > 0;
-  constexpr int kStages = kAsync ? STAGES : 1;
+  using E = typename P::E;
+  constexpr int N = P::N;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float sums[2][3 * kMaxWarps];
-  int flip = 0;
-  const int tpr = blockDim.x, groups = blockDim.y;
-  const Ring<P, 4, VPT, kStages> ring{reinterpret_cast<P*>(smem), tpr * groups, (int)(threadIdx.y * tpr + threadIdx.x)};
-  const int nvec = H / VEC;
-  const P* src[4] = {b.w_next ? static_cast<const P*>(b.r) : nullptr, static_cast<const P*>(b.y),
-                     static_cast<const P*>(b.dr), static_cast<const P*>(b.dn)};
+  __shared__ RowSums<6> sums;
+  const int groups = blockDim.y, nvec = H / VEC;
   const float inv_h = 1.0f / (float)H;
   const bool need_s = b.dgate || b.dw_post;
-
-  float wu[CACHE_W ? VPT : 1][VEC], wn[CACHE_W ? VPT : 1][VEC];
-  float colS[VPT][VEC], colN[VPT][VEC];
-  auto channel_weights = [&](int c, float (&wa)[VEC], float (&wb)[VEC]) {
+  enum { R = 0, Y = 1, DR = 2, DN = 3 };
+  using Ring = Rows<P, 4, VPT, MAXT, STAGES>;
+  const Ring rows{reinterpret_cast<P*>(smem) + threadIdx.y * blockDim.x + threadIdx.x,
+                  {b.w_next ? static_cast<const P*>(b.r) : nullptr, static_cast<const P*>(b.y),
+                   static_cast<const P*>(b.dr), static_cast<const P*>(b.dn)},
+                  T_, nvec};
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + threadIdx.y - step;  // the row that is finished, one behind the sums
+  const int iters = (int)ceil_div(T_ - (int64_t)blockIdx.x * groups, step);
+  rows.zero_ring();
+  if constexpr (STAGES > 0) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int h = c * VEC + e;
-      float v = b.w_post ? __ldg(b.w_post + h) : 1.0f;
-      if (b.gate) v *= __ldg(b.gate + h);
-      wa[e] = v;
-      wb[e] = b.w_next ? __ldg(b.w_next + h) : 0.0f;
+    for (int i = 0; i < STAGES - 1; ++i) {
+      rows.fetch(row + (i + 1) * step, i);
+      cp_commit();
     }
+  }
+
+  E wu[CACHE_W ? VPT : 1][N], wn[CACHE_W ? VPT : 1][N], colS[VPT][N], colN[VPT][N];
+  auto weights = [&](int j) {
+    channel_weights<P, VEC>(b.w_post, b.gate, b.w_next, j, H, wu[CACHE_W ? j : 0], wn[CACHE_W ? j : 0]);
   };
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    if constexpr (CACHE_W) {
-      const int c = threadIdx.x + j * tpr;
-      if (c < nvec) channel_weights(c, wu[j], wn[j]);
-    }
+    if constexpr (CACHE_W) weights(j);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) colS[j][e] = colN[j][e] = 0.0f;
+    for (int e = 0; e < N; ++e) splat(0.0f, &colS[j][e]), splat(0.0f, &colN[j][e]);
   }
 
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row = (int64_t)blockIdx.x * groups + threadIdx.y;
-  const int64_t iters = ceil_div(T_ - (int64_t)blockIdx.x * groups, step);
-  auto fetch = [&](int64_t rw, int stage) {
-    if constexpr (kAsync) {
-      if (rw < T_) {
+  int stage = 0, prev = STAGES > 0 ? STAGES - 1 : 0;  // of row + step, whose sums are formed, and of row
+  for (int it = 0; it <= iters; ++it, row += step) {
+    const int parity = it & 1;
+    if constexpr (STAGES > 0) cp_wait<(STAGES > 2 ? STAGES - 2 : 0)>();
+    float tot[6] = {0, 0, 0, 0, 0, 0};
+    if (it > 0) sums.total(tot, parity ^ 1);
+    if (it < iters) {
+      E s[6];
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          const int c = threadIdx.x + j * tpr;
-          if (c < nvec) {
+      for (int i = 0; i < 6; ++i) splat(0.0f, &s[i]);
 #pragma unroll
-            for (int a = 0; a < 4; ++a)
-              if (src[a]) cp16(ring.slot(stage, a, j), src[a] + rw * nvec + c);
-          }
+      for (int j = 0; j < VPT; ++j) {
+        E r[N], y[N], dr[N], dn[N];
+        rows.get(row + step, stage, R, j, r);
+        rows.get(row + step, stage, Y, j, y);
+        rows.get(row + step, stage, DR, j, dr);
+        rows.get(row + step, stage, DN, j, dn);
+        if constexpr (!CACHE_W) weights(j);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const E a = mul(dn[e], wn[CACHE_W ? j : 0][e]), wy = mul(y[e], wu[CACHE_W ? j : 0][e]);
+          s[0] = fma(r[e], r[e], s[0]);
+          s[1] = fma(a, r[e], s[1]);
+          s[2] = fma(y[e], y[e], s[2]);
+          s[3] = fma(dr[e], wy, s[3]);
+          s[4] = fma(a, wy, s[4]);
+          s[5] = fma(r[e], wy, s[5]);
         }
       }
+      const float f[6] = {fold(s[0]), fold(s[1]), fold(s[2]), fold(s[3]), fold(s[4]), fold(s[5])};
+      sums.publish(f, parity);
+    }
+    if (it > 0 && row < T_) {
+      const float rho = b.w_next ? inv_rms(tot[0], inv_h, eps) : 0.0f;
+      const float k = rho * rho * rho * tot[1] * inv_h;
+      const float rho_y = b.w_post ? inv_rms(tot[2], inv_h, eps) : 1.0f;
+      const float g = b.token_gate ? __ldg(b.token_gate + row) : 1.0f;
+      const float q = fmaf(rho, tot[4], fmaf(-k, tot[5], tot[3]));
+      if (b.dtoken_gate && threadIdx.x == 0) b.dtoken_gate[row] = rho_y * q;
+      E e_rho, e_k, e_g, e_ky, e_res;
+      splat(rho, &e_rho);
+      splat(-k, &e_k);
+      splat(g * rho_y, &e_g);
+      splat(b.w_post ? -g * rho_y * rho_y * rho_y * q * inv_h : 0.0f, &e_ky);
+      splat(res_scale, &e_res);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        E r[N], y[N], d[N], dn[N], o[N];
+        rows.get(row, prev, R, j, r);
+        rows.get(row, prev, Y, j, y);
+        rows.get(row, prev, DR, j, d);
+        rows.get(row, prev, DN, j, dn);
+        if constexpr (!CACHE_W) weights(j);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const E p = mul(dn[e], e_rho);  // rho dn
+          d[e] = fma(p, wn[CACHE_W ? j : 0][e], fma(e_k, r[e], d[e]));
+          colN[j][e] = fma(p, r[e], colN[j][e]);
+          const E gd = mul(e_g, d[e]);
+          colS[j][e] = fma(gd, y[e], colS[j][e]);
+          o[e] = fma(gd, wu[CACHE_W ? j : 0][e], mul(e_ky, y[e]));
+          d[e] = mul(d[e], e_res);
+        }
+        if (rows.on(j)) {
+          const int64_t at = row * nvec + threadIdx.x + j * blockDim.x;
+          if (b.dx) static_cast<P*>(b.dx)[at] = P::of(d);
+          if (b.dy) static_cast<P*>(b.dy)[at] = P::of(o);
+        }
+      }
+    }
+    if constexpr (STAGES > 0) {  // row's stage has been read (in iteration 0: was never filled)
+      rows.fetch(row + (int64_t)STAGES * step, prev);
       cp_commit();
+      prev = stage;
+      if (++stage == STAGES) stage = 0;
     }
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(row + i * step, i);
-  int stage = 0;
-  for (int64_t it = 0; it < iters; ++it, row += step) {
-    if constexpr (kAsync) {
-      fetch(row + (kStages - 1) * step, (stage + kStages - 1) % kStages);
-      cp_wait<kStages - 1>();
-    }
-    const bool live = row < T_;
-    auto piece = [&](int a, int j, float (&f)[VEC]) {  // zeros where there is nothing to read
-      const int c = threadIdx.x + j * tpr;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) f[e] = 0.0f;
-      if (src[a] && live && c < nvec) {
-        if constexpr (kAsync) ring.slot(stage, a, j)->to(f);
-        else src[a][row * nvec + c].to(f);
-      }
-    };
-    float d[VPT][VEC], yv[VPT][VEC], rv[VPT][VEC];
-    float s[3] = {0.0f, 0.0f, 0.0f};  // sum r^2, sum a r, sum y^2
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = threadIdx.x + j * tpr;
-      float dn[VEC], wa[VEC], wb[VEC];
-      piece(0, j, rv[j]);
-      piece(1, j, yv[j]);
-      piece(3, j, dn);
-      if constexpr (!CACHE_W)
-        if (c < nvec) channel_weights(c, wa, wb);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float a = c < nvec ? dn[e] * (CACHE_W ? wn[CACHE_W ? j : 0][e] : wb[e]) : 0.0f;
-        s[0] = fmaf(rv[j][e], rv[j][e], s[0]);
-        s[1] = fmaf(a, rv[j][e], s[1]);
-        s[2] = fmaf(yv[j][e], yv[j][e], s[2]);
-      }
-    }
-    row_sum(s, sums[flip ^= 1]);
-    const float rho = 1.0f / sqrtf(fmaf(s[0], inv_h, eps));
-    const float k = b.w_next ? rho * rho * rho * s[1] * inv_h : 0.0f;
-    const float rho_y = b.w_post ? 1.0f / sqrtf(fmaf(s[2], inv_h, eps)) : 1.0f;
-    const float g = b.token_gate && live ? __ldg(b.token_gate + row) : 1.0f;
-    float q[1] = {0.0f};
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = threadIdx.x + j * tpr;
-      const bool on = live && c < nvec;
-      float dn[VEC], wa[VEC], wb[VEC], o[VEC];
-      piece(2, j, d[j]);
-      piece(3, j, dn);
-      if constexpr (!CACHE_W)
-        if (c < nvec) channel_weights(c, wa, wb);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (on) {
-          const float w_n = CACHE_W ? wn[CACHE_W ? j : 0][e] : wb[e], w_u = CACHE_W ? wu[CACHE_W ? j : 0][e] : wa[e];
-          if (b.w_next) {
-            d[j][e] = fmaf(rho, dn[e] * w_n, fmaf(-k, rv[j][e], d[j][e]));
-            colN[j][e] = fmaf(dn[e], rv[j][e] * rho, colN[j][e]);
-          }
-          if (need_s) colS[j][e] = fmaf(g * d[j][e], yv[j][e] * rho_y, colS[j][e]);
-          q[0] = fmaf(w_u * d[j][e], yv[j][e], q[0]);
-        }
-        o[e] = res_scale * d[j][e];
-      }
-      if (b.dx && on) static_cast<P*>(b.dx)[row * nvec + c] = P::of(o);
-    }
-    if (b.y) {
-      if (b.w_post || b.dtoken_gate) row_sum(q, sums[flip ^= 1]);
-      const float ky = b.w_post ? g * rho_y * rho_y * rho_y * q[0] * inv_h : 0.0f;
-      if (b.dtoken_gate && live && threadIdx.x == 0) b.dtoken_gate[row] = rho_y * q[0];
-      if (b.dy) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          const int c = threadIdx.x + j * tpr;
-          if (live && c < nvec) {
-            float wa[VEC], wb[VEC], o[VEC];
-            if constexpr (!CACHE_W) channel_weights(c, wa, wb);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-              o[e] = fmaf(g * rho_y * (CACHE_W ? wu[CACHE_W ? j : 0][e] : wa[e]), d[j][e], -ky * yv[j][e]);
-            static_cast<P*>(b.dy)[row * nvec + c] = P::of(o);
-          }
-        }
-      }
-    }
-    if constexpr (kAsync) stage = (stage + 1) % kStages;
+    row_barrier();
   }
   if (need_s || b.dw_next) {  // [2][gridDim.x * groups][H]
     const int64_t p = (int64_t)blockIdx.x * groups + threadIdx.y, np = (int64_t)gridDim.x * groups;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = threadIdx.x + j * tpr;
+      const int c = threadIdx.x + j * blockDim.x;
       if (c < nvec) {
+        E* ps = reinterpret_cast<E*>(part + p * H + c * VEC);
+        E* pn = reinterpret_cast<E*>(part + (np + p) * H + c * VEC);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (need_s) part[p * H + c * VEC + e] = colS[j][e];
-          if (b.dw_next) part[(np + p) * H + c * VEC + e] = colN[j][e];
+        for (int e = 0; e < N; ++e) {
+          if (need_s) ps[e] = colS[j][e];
+          if (b.dw_next) pn[e] = colN[j][e];
         }
       }
     }
@@ -445,7 +516,7 @@ Shape shape_of(int nvec, int vpt) {
   Shape s;
   s.vpt = vpt;
   s.tpr = (int)(ceil_div(ceil_div(nvec, vpt), 32) * 32);
-  s.groups = std::max(1, 128 / s.tpr);
+  s.groups = std::max(1, 256 / s.tpr);
   return s;
 }
 
@@ -472,7 +543,7 @@ cudaError_t grid_of(K kern, std::atomic<uint32_t>& last, const Shape& sh, size_t
 template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
 cudaError_t fwd(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
   const Shape sh = shape_of(c.H / VEC, VPT);
-  const size_t smem = (size_t)STAGES * 2 * VPT * sh.tpr * sh.groups * 16;
+  const size_t smem = (size_t)STAGES * 2 * 2 * VPT * MAXT * 16;
   auto kern = block_norm_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES>;
   int grid = 0;
   static std::atomic<uint32_t> last{0};
@@ -485,7 +556,7 @@ cudaError_t fwd(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, 
 template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
 cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
   const Shape sh = shape_of(c.H / VEC, VPT);
-  const size_t smem = (size_t)STAGES * 4 * VPT * sh.tpr * sh.groups * 16;
+  const size_t smem = (size_t)STAGES * 4 * VPT * MAXT * 16;
   auto kern = block_norm_bwd_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES>;
   int grid = 0;
   static std::atomic<uint32_t> last{0};
@@ -501,20 +572,21 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
 }  // namespace
 
 // A row's pieces are spread over at most 1024 threads: bf16 rows have up to 2048 16-byte
-// pieces (H = 16384), fp32 rows up to 4096, rows of odd width up to 16384 elements. STAGES:
-// rows of the cp.async ring (FS with one piece per thread, BS with two).
-// Rows of more than 1024 pieces and odd widths do without the ring (0).
-#define NORM_DISPATCH(FN, FS, BS, ...)                                                         \
+// pieces (H = 16384), fp32 rows up to 4096, rows of odd width up to 16384 elements. S1 / S2:
+// stages of the ring with one / two pieces per thread (forward: stages of two rows), as many as
+// leave room for several CTAs (S1) or one (S2) on an SM. Rows of more than 1024 pieces and odd
+// widths do without the ring.
+#define NORM_DISPATCH(FN, S1, S2, ...)                                                         \
   if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0) {                                         \
     const int nvec = c.H / 8;                                                                  \
-    if (nvec <= 256) return FN<__nv_bfloat16, 8, 1, true, 256, FS>(__VA_ARGS__);               \
-    if (nvec <= 1024) return FN<__nv_bfloat16, 8, 2, true, 512, BS>(__VA_ARGS__);              \
+    if (nvec <= 256) return FN<__nv_bfloat16, 8, 1, true, 256, S1>(__VA_ARGS__);               \
+    if (nvec <= 1024) return FN<__nv_bfloat16, 8, 2, true, 512, S2>(__VA_ARGS__);              \
     return FN<__nv_bfloat16, 8, 4, false, 512, 0>(__VA_ARGS__);                                \
   }                                                                                            \
   if (c.act_dtype == MOE_DTYPE_F32 && c.H % 4 == 0) {                                          \
     const int nvec = c.H / 4;                                                                  \
-    if (nvec <= 512) return FN<float, 4, 1, true, 512, FS>(__VA_ARGS__);                       \
-    if (nvec <= 1024) return FN<float, 4, 2, true, 512, BS>(__VA_ARGS__);                      \
+    if (nvec <= 256) return FN<float, 4, 1, true, 256, S1>(__VA_ARGS__);                       \
+    if (nvec <= 1024) return FN<float, 4, 2, true, 512, S2>(__VA_ARGS__);                      \
     if (nvec <= 2048) return FN<float, 4, 4, false, 512, 0>(__VA_ARGS__);                      \
     return FN<float, 4, 4, false, 1024, 0>(__VA_ARGS__);                                       \
   }                                                                                            \
@@ -527,7 +599,7 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
 
 cudaError_t launch_block_norm(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  NORM_DISPATCH(fwd, 4, 3, c, in, r, n, s)
+  NORM_DISPATCH(fwd, 3, 3, c, in, r, n, s)
 }
 
 cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
@@ -537,7 +609,7 @@ cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd
       if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)c.H * 4, s);
     return e;
   }
-  NORM_DISPATCH(bwd, 3, 2, c, b, part, s)
+  NORM_DISPATCH(bwd, 4, 3, c, b, part, s)
 }
 
 // Two sets of column sums for every row group of the largest grid: at most 2048 / (threads of
@@ -545,7 +617,7 @@ cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd
 size_t norm_part_bytes(const moe_norm_config_t& c) {
   const int vec = c.act_dtype == MOE_DTYPE_BF16 ? (c.H % 8 ? 1 : 8) : (c.H % 4 ? 1 : 4);
   const int nvec = c.H / vec;
-  const int vpt = vec == 1 ? (c.H <= 2048 ? 8 : 16) : nvec <= (vec == 8 ? 256 : 512) ? 1 : nvec <= 1024 ? 2 : 4;
+  const int vpt = vec == 1 ? (c.H <= 2048 ? 8 : 16) : nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
   const Shape sh = shape_of(nvec, vpt);
   const int64_t groups = std::min<int64_t>(align_up(c.T, sh.groups), (int64_t)kNormMaxSms * (2048 / sh.tpr));
   return (size_t)(2 * groups * c.H * 4);
