@@ -60,7 +60,8 @@ NORM_CASES = [
     (700, 2048, BF, 1, 1, 1, 1), (641, 264, BF, 0, 1, 1, 0), (333, 1001, FP, 1, 1, 1, 1), (130, 999, BF, 1, 1, 0, 1),
     (65, 512, FP, 1, 0, 0, 1), (97, 4096, FP, 1, 1, 1, 0), (40, 4100, FP, 1, 1, 1, 1), (20, 8200, BF, 1, 1, 1, 1),
     (9, 16384, BF, 1, 1, 1, 1), (9, 16384, FP, 1, 1, 1, 1), (7, 16383, FP, 0, 1, 0, 0), (6, 5001, BF, 1, 1, 1, 1),
-    (2000, 64, BF, 1, 1, 1, 1), (50, 96, BF, 0, 0, 0, 0), (400, 7168, BF, 1, 1, 0, 0)]
+    (2000, 64, BF, 1, 1, 1, 1), (50, 96, BF, 0, 0, 0, 0), (400, 7168, BF, 1, 1, 0, 0), (700, 1002, BF, 1, 1, 1, 1),
+    (30, 5002, BF, 1, 1, 1, 1), (500, 7168, FP, 1, 1, 1, 1), (300, 12296, BF, 1, 1, 1, 1), (1100, 1500, FP, 0, 1, 0, 1)]
 
 
 def norm_inputs(T, H, dt, post, nxt, gate, tgate, seed=0):

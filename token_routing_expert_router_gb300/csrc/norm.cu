@@ -69,6 +69,19 @@ struct Piece<__nv_bfloat16, 8> {
   }
 };
 template <>
+struct Piece<__nv_bfloat16, 2> {
+  using E = float2;
+  static constexpr int N = 1;
+  uint32_t v;
+  __device__ __forceinline__ void to(E (&f)[N]) const {
+    f[0] = make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+  __device__ __forceinline__ static Piece of(const E (&f)[N]) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[0].x, f[0].y);
+    return {*reinterpret_cast<const uint32_t*>(&p)};
+  }
+};
+template <>
 struct Piece<float, 1> {
   using E = float;
   static constexpr int N = 1;
@@ -85,9 +98,12 @@ struct Piece<__nv_bfloat16, 1> {
   __device__ __forceinline__ static Piece of(const E (&f)[N]) { return {__float2bfloat16_rn(f[0])}; }
 };
 
-__device__ __forceinline__ void cp16(void* dst, const void* src) {
+// One piece (16 or 4 bytes) from global to shared memory, asynchronously.
+template <typename P>
+__device__ __forceinline__ void cp_piece(P* dst, const P* src) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  if constexpr (sizeof(P) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -99,9 +115,11 @@ __device__ __forceinline__ void cp_wait() {
 // multiple of 32), in a fixed order, in two halves so that a barrier of the caller's stands
 // between them. Both work on kP values at once (NV rounded up to a power of two): a lane ends
 // up with the value lane / (32 / kP), which takes 9 shuffles for 8 values instead of 40.
+// With CL > 1 a row's channels are spread over a cluster of CL CTAs, and the totals are taken
+// from all of them.
 constexpr int kMaxWarps = 32;
 constexpr int kNormMaxSms = 152;  // bounds the grid, and so the backward's column partial sums
-template <int NV>
+template <int NV, int CL>
 struct RowSums {
   static constexpr int kP = NV <= 1 ? 1 : NV <= 2 ? 2 : NV <= 4 ? 4 : 8;
   static constexpr int kLanes = 32 / kP;
@@ -135,7 +153,18 @@ struct RowSums {
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const float* b = buf[parity] + (threadIdx.y * kP + lane / kLanes) * warps;
     float t = 0.0f;
-    for (int w = lane % kLanes; w < warps; w += kLanes) t += b[w];
+    if constexpr (CL == 1) {
+      for (int w = lane % kLanes; w < warps; w += kLanes) t += b[w];
+    } else {
+      const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(b));
+      for (int w = lane % kLanes; w < warps * CL; w += kLanes) {
+        uint32_t at;
+        float v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(here + w / CL * 4), "r"(w % CL));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+        t += v;
+      }
+    }
 #pragma unroll
     for (int off = kLanes / 2; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
 #pragma unroll
@@ -143,13 +172,16 @@ struct RowSums {
   }
 };
 
-// A warp per row needs no barrier of the block.
+template <int CL>
 __device__ __forceinline__ void row_barrier() {
-  if (blockDim.x == 32) __syncwarp();
+  if constexpr (CL > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else if (blockDim.x == 32) __syncwarp();  // a warp per row needs no barrier of the block
   else __syncthreads();
 }
 
-// A thread's pieces c = threadIdx.x + j TPR of a row's A arrays, from a ring of stages in shared
+// A thread's pieces c = threadIdx.x + j TPR of a row's A arrays (of this CTA's share of the row,
+// which begins at piece c0), from a ring of stages in shared
 // memory (MAXT threads wide, so that a piece's place is a constant away from the stage's), or,
 // with STAGES = 0, from global memory whenever they are asked for. An array that is not there
 // (src NULL) and pieces past the row read as zeros: their places in the ring are zeroed once.
@@ -158,9 +190,10 @@ struct Rows {
   static constexpr int kStage = A * VPT * MAXT;
   P* ring;
   const P* src[A];
-  int T, nvec;
+  int T, nvec, c0;
 
-  __device__ __forceinline__ bool on(int j) const { return (int)(threadIdx.x + j * blockDim.x) < nvec; }
+  __device__ __forceinline__ int piece(int j) const { return c0 + threadIdx.x + j * blockDim.x; }
+  __device__ __forceinline__ bool on(int j) const { return piece(j) < nvec; }
   __device__ __forceinline__ void zero_ring() const {
     P z{};
 #pragma unroll
@@ -173,20 +206,20 @@ struct Rows {
   }
   __device__ __forceinline__ void fetch(int64_t row, int stage) const {
     if (row >= T) return;
-    const int64_t at = row * nvec + threadIdx.x;
+    const int64_t at = row * nvec + piece(0);
 #pragma unroll
     for (int a = 0; a < A; ++a)
       if (src[a])
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
-          if (on(j)) cp16(ring + stage * kStage + (a * VPT + j) * MAXT, src[a] + at + j * blockDim.x);
+          if (on(j)) cp_piece(ring + stage * kStage + (a * VPT + j) * MAXT, src[a] + at + j * blockDim.x);
   }
   __device__ __forceinline__ void get(int64_t row, int stage, int a, int j, typename P::E (&f)[P::N]) const {
     if constexpr (STAGES > 0) {
       ring[stage * kStage + (a * VPT + j) * MAXT].to(f);
     } else {
       if (src[a] && row < T && on(j)) {
-        src[a][row * nvec + threadIdx.x + j * blockDim.x].to(f);
+        src[a][row * nvec + piece(j)].to(f);
       } else {
 #pragma unroll
         for (int e = 0; e < P::N; ++e) splat(0.0f, &f[e]);
@@ -195,44 +228,64 @@ struct Rows {
   }
 };
 
-// Per-channel weights of a thread's pieces: a = w_post G, b = w_next (0 past the row and where
+// Per-channel weights of a thread's piece c: a = w_post G, b = w_next (0 past the row and where
 // there is no next norm).
 template <typename P, int VEC>
-__device__ __forceinline__ void channel_weights(const float* w_post, const float* gate, const float* w_next, int j, int H,
+__device__ __forceinline__ void channel_weights(const float* w_post, const float* gate, const float* w_next, int c, int nvec,
                                                 typename P::E (&a)[P::N], typename P::E (&b)[P::N]) {
-  const int h0 = (threadIdx.x + j * blockDim.x) * VEC;
   float* fa = reinterpret_cast<float*>(a);
   float* fb = reinterpret_cast<float*>(b);
+  if constexpr (VEC >= 4) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    const bool in = h0 + e < H;
-    float v = !in ? 0.0f : w_post ? __ldg(w_post + h0 + e) : 1.0f;
-    if (in && gate) v *= __ldg(gate + h0 + e);
-    fa[e] = v;
-    fb[e] = in && w_next ? __ldg(w_next + h0 + e) : 0.0f;
+    for (int e = 0; e < VEC; e += 4) {
+      float4 u = make_float4(0, 0, 0, 0), n = u;
+      if (c < nvec) {
+        const int64_t at = ((int64_t)c * VEC + e) / 4;
+        u = w_post ? __ldg(reinterpret_cast<const float4*>(w_post) + at) : make_float4(1, 1, 1, 1);
+        if (gate) {
+          const float4 g = __ldg(reinterpret_cast<const float4*>(gate) + at);
+          u.x *= g.x, u.y *= g.y, u.z *= g.z, u.w *= g.w;
+        }
+        if (w_next) n = __ldg(reinterpret_cast<const float4*>(w_next) + at);
+      }
+      fa[e] = u.x, fa[e + 1] = u.y, fa[e + 2] = u.z, fa[e + 3] = u.w;
+      fb[e] = n.x, fb[e + 1] = n.y, fb[e + 2] = n.z, fb[e + 3] = n.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const bool in = c < nvec;
+      float v = !in ? 0.0f : w_post ? __ldg(w_post + c * VEC + e) : 1.0f;
+      if (in && gate) v *= __ldg(gate + c * VEC + e);
+      fa[e] = v;
+      fb[e] = in && w_next ? __ldg(w_next + c * VEC + e) : 0.0f;
+    }
   }
 }
 
 __device__ __forceinline__ float inv_rms(float sum, float inv_h, float eps) { return rsqrtf(fmaf(sum, inv_h, eps)); }
 
 // ROWS rows per iteration: i ROWS + k is row (first + (i ROWS + k) step) of the group.
-template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
+template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
     block_norm_kernel(NormIn in, void* r_out, void* n_out, int T_, int H, float eps, float res_scale) {
   using P = Piece<T, VEC>;
   using E = typename P::E;
-  constexpr int N = P::N, ROWS = STAGES > 0 ? 2 : 1;
+  constexpr int N = P::N, ROWS = STAGES > 0 ? 2 : 1;  // without the ring there are no registers for two
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ RowSums<ROWS> sums;
+  __shared__ RowSums<ROWS, CL> sums;
   const int groups = blockDim.y, nvec = H / VEC;
   const float inv_h = 1.0f / (float)H;
+  const int cta = blockIdx.x / CL;  // of the row groups' walkers
+  // this CTA's share of a row's pieces: VPT per thread
+  const int share0 = CL > 1 ? (int)(blockIdx.x % CL * blockDim.x) * VPT : 0;
   using R = Rows<P, 2, VPT, MAXT, STAGES * ROWS>;
   const R rows{reinterpret_cast<P*>(smem) + threadIdx.y * blockDim.x + threadIdx.x,
-               {static_cast<const P*>(in.x), static_cast<const P*>(in.y)}, T_, nvec};
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row0 = (int64_t)blockIdx.x * groups + threadIdx.y;
+               {static_cast<const P*>(in.x), static_cast<const P*>(in.y)}, T_, nvec, share0};
+  const int64_t step = (int64_t)gridDim.x / CL * groups;
+  int64_t row0 = (int64_t)cta * groups + threadIdx.y;
   // the same for every group of the CTA: the rows of its first one
-  const int iters = (int)ceil_div(ceil_div(T_ - (int64_t)blockIdx.x * groups, step), ROWS);
+  const int iters = (int)ceil_div(ceil_div(T_ - (int64_t)cta * groups, step), ROWS);
   rows.zero_ring();
   auto fetch = [&](int64_t row, int stage) {
     if constexpr (STAGES > 0) {
@@ -246,7 +299,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
 
   E wu[CACHE_W ? VPT : 1][N], wn[CACHE_W ? VPT : 1][N];
   auto weights = [&](int j) {
-    channel_weights<P, VEC>(in.w_post, in.gate, n_out ? in.w_next : nullptr, j, H, wu[CACHE_W ? j : 0], wn[CACHE_W ? j : 0]);
+    channel_weights<P, VEC>(in.w_post, in.gate, n_out ? in.w_next : nullptr, rows.piece(j), nvec, wu[CACHE_W ? j : 0], wn[CACHE_W ? j : 0]);
   };
   if constexpr (CACHE_W) {
 #pragma unroll
@@ -276,7 +329,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
         s[k] = fold(t);
       }
       sums.publish(s, 0);
-      row_barrier();
+      row_barrier<CL>();
       sums.total(s, 0);
 #pragma unroll
       for (int k = 0; k < ROWS; ++k) su[k] = inv_rms(s[k], inv_h, eps);
@@ -301,7 +354,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
           t = fma(v[k][j][e], v[k][j][e], t);
         }
         if (r_out && row < T_ && rows.on(j))
-          static_cast<P*>(r_out)[row * nvec + threadIdx.x + j * blockDim.x] = P::of(v[k][j]);
+          static_cast<P*>(r_out)[row * nvec + rows.piece(j)] = P::of(v[k][j]);
       }
       s[k] = fold(t);
     }
@@ -310,7 +363,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
     if (STAGES > 0 && ++stage == STAGES) stage = 0;
     if (n_out) {
       sums.publish(s, 1);
-      row_barrier();
+      row_barrier<CL>();
       sums.total(s, 1);
       // n is formed from r before its rounding to the activation type
 #pragma unroll
@@ -325,14 +378,15 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
             if (!rows.on(j)) continue;
 #pragma unroll
             for (int e = 0; e < N; ++e) v[k][j][e] = mul(mul(v[k][j][e], f), wn[CACHE_W ? j : 0][e]);
-            static_cast<P*>(n_out)[row * nvec + threadIdx.x + j * blockDim.x] = P::of(v[k][j]);
+            static_cast<P*>(n_out)[row * nvec + rows.piece(j)] = P::of(v[k][j]);
           }
         }
       }
     }
-    if (in.w_post && !n_out) row_barrier();  // sums' one buffer in use is free again
-    if (n_out && !in.w_post) row_barrier();
+    // with one sum in use, its buffer is free again only after a second barrier
+    if ((in.w_post != nullptr) != (n_out != nullptr)) row_barrier<CL>();
   }
+  if constexpr (CL > 1) row_barrier<CL>();  // the cluster may still be reading this CTA's sums
 }
 
 // Backward, per row, from the stored residual r and block output y (both statistics are
@@ -347,26 +401,29 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
 // is rounded relative to its own size, as the terms of dr' would be.
 // Each CTA keeps the column sums of its rows in registers and writes them once; colsum_kernel
 // adds the CTAs' sums in a fixed order.
-template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
+template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
     block_norm_bwd_kernel(NormBwd b, float* part, int T_, int H, float eps, float res_scale) {
   using P = Piece<T, VEC>;
   using E = typename P::E;
   constexpr int N = P::N;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ RowSums<6> sums;
+  __shared__ RowSums<6, CL> sums;
   const int groups = blockDim.y, nvec = H / VEC;
   const float inv_h = 1.0f / (float)H;
+  const int cta = blockIdx.x / CL;  // of the row groups' walkers
+  // this CTA's share of a row's pieces: VPT per thread
+  const int share0 = CL > 1 ? (int)(blockIdx.x % CL * blockDim.x) * VPT : 0;
   const bool need_s = b.dgate || b.dw_post;
   enum { R = 0, Y = 1, DR = 2, DN = 3 };
   using Ring = Rows<P, 4, VPT, MAXT, STAGES>;
   const Ring rows{reinterpret_cast<P*>(smem) + threadIdx.y * blockDim.x + threadIdx.x,
                   {b.w_next ? static_cast<const P*>(b.r) : nullptr, static_cast<const P*>(b.y),
                    static_cast<const P*>(b.dr), static_cast<const P*>(b.dn)},
-                  T_, nvec};
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row = (int64_t)blockIdx.x * groups + threadIdx.y - step;  // the row that is finished, one behind the sums
-  const int iters = (int)ceil_div(T_ - (int64_t)blockIdx.x * groups, step);
+                  T_, nvec, share0};
+  const int64_t step = (int64_t)gridDim.x / CL * groups;
+  int64_t row = (int64_t)cta * groups + threadIdx.y - step;  // the row that is finished, one behind the sums
+  const int iters = (int)ceil_div(T_ - (int64_t)cta * groups, step);
   rows.zero_ring();
   if constexpr (STAGES > 0) {
 #pragma unroll
@@ -378,7 +435,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
 
   E wu[CACHE_W ? VPT : 1][N], wn[CACHE_W ? VPT : 1][N], colS[VPT][N], colN[VPT][N];
   auto weights = [&](int j) {
-    channel_weights<P, VEC>(b.w_post, b.gate, b.w_next, j, H, wu[CACHE_W ? j : 0], wn[CACHE_W ? j : 0]);
+    channel_weights<P, VEC>(b.w_post, b.gate, b.w_next, rows.piece(j), nvec, wu[CACHE_W ? j : 0], wn[CACHE_W ? j : 0]);
   };
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -425,7 +482,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
       const float rho_y = b.w_post ? inv_rms(tot[2], inv_h, eps) : 1.0f;
       const float g = b.token_gate ? __ldg(b.token_gate + row) : 1.0f;
       const float q = fmaf(rho, tot[4], fmaf(-k, tot[5], tot[3]));
-      if (b.dtoken_gate && threadIdx.x == 0) b.dtoken_gate[row] = rho_y * q;
+      if (b.dtoken_gate && threadIdx.x == 0 && share0 == 0) b.dtoken_gate[row] = rho_y * q;
       E e_rho, e_k, e_g, e_ky, e_res;
       splat(rho, &e_rho);
       splat(-k, &e_k);
@@ -451,7 +508,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
           d[e] = mul(d[e], e_res);
         }
         if (rows.on(j)) {
-          const int64_t at = row * nvec + threadIdx.x + j * blockDim.x;
+          const int64_t at = row * nvec + rows.piece(j);
           if (b.dx) static_cast<P*>(b.dx)[at] = P::of(d);
           if (b.dy) static_cast<P*>(b.dy)[at] = P::of(o);
         }
@@ -463,13 +520,13 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
       prev = stage;
       if (++stage == STAGES) stage = 0;
     }
-    row_barrier();
+    row_barrier<CL>();
   }
   if (need_s || b.dw_next) {  // [2][gridDim.x * groups][H]
-    const int64_t p = (int64_t)blockIdx.x * groups + threadIdx.y, np = (int64_t)gridDim.x * groups;
+    const int64_t p = (int64_t)cta * groups + threadIdx.y, np = (int64_t)gridDim.x / CL * groups;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = threadIdx.x + j * blockDim.x;
+      const int c = rows.piece(j);
       if (c < nvec) {
         E* ps = reinterpret_cast<E*>(part + p * H + c * VEC);
         E* pn = reinterpret_cast<E*>(part + (np + p) * H + c * VEC);
@@ -508,98 +565,116 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* part, int np,
   }
 }
 
-// Threads per row, rows per CTA and pieces per thread for a row of `nvec` pieces.
+// Threads per row (of one CTA of its cluster) and rows per CTA.
 struct Shape {
-  int vpt, tpr, groups;
+  int tpr, groups;
 };
-Shape shape_of(int nvec, int vpt) {
+Shape shape_of(int nvec, int vpt, int cl) {
   Shape s;
-  s.vpt = vpt;
-  s.tpr = (int)(ceil_div(ceil_div(nvec, vpt), 32) * 32);
-  s.groups = std::max(1, 256 / s.tpr);
+  s.tpr = (int)(ceil_div(ceil_div(nvec, vpt * cl), 32) * 32);
+  s.groups = cl > 1 ? 1 : std::max(1, 256 / s.tpr);
   return s;
 }
 
-// Persistent grid of an instantiation. What fits on an SM depends on the threads of a row only;
-// the last answer is kept (one word, so that concurrent callers see a whole one).
-template <typename K>
-cudaError_t grid_of(K kern, std::atomic<uint32_t>& last, const Shape& sh, size_t smem, int64_t T, int* grid) {
-  uint32_t known = last.load(std::memory_order_relaxed);  // tpr << 8 | blocks per SM
-  if (known >> 8 != (uint32_t)sh.tpr) {
+// Persistent launch of an instantiation. What fits on an SM depends on the threads of a row
+// only; the last answer is kept (one word, so that concurrent callers see a whole one).
+template <int CL, typename K, typename... Args>
+cudaError_t launch_rows(K kern, std::atomic<uint32_t>& last, const Shape& sh, size_t smem, int64_t T, cudaStream_t s,
+                        int* walkers, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(sh.tpr, sh.groups);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL > 1 ? 1 : 0;
+  const int sms = std::min(tc::num_sms(), kNormMaxSms);
+  uint32_t known = last.load(std::memory_order_relaxed);  // tpr << 16 | row walkers that are resident together
+  if (known >> 16 != (uint32_t)sh.tpr) {
     cudaError_t e = cudaSuccess;
     if (smem > 32 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, sh.tpr * sh.groups, smem);
+    int fit = 0;
+    if constexpr (CL > 1) {
+      cfg.gridDim = dim3(CL * (sms / CL));
+      e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
+    } else {
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, sh.tpr * sh.groups, smem);
+      fit *= sms;
+    }
     if (e != cudaSuccess) return e;
-    known = (uint32_t)sh.tpr << 8 | (uint32_t)std::max(1, per_sm);
+    known = (uint32_t)sh.tpr << 16 | (uint32_t)std::max(1, std::min(fit, sms * (2048 / (sh.tpr * sh.groups)) / CL));
     last.store(known, std::memory_order_relaxed);
   }
-  *grid = (int)std::min<int64_t>(ceil_div(T, sh.groups),
-                                 (int64_t)std::min(tc::num_sms(), kNormMaxSms) * (known & 255));
-  return cudaSuccess;
+  *walkers = (int)std::min<int64_t>(ceil_div(T, sh.groups), known & 0xffff);
+  cfg.gridDim = dim3((unsigned)(*walkers * CL));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
+template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
 cudaError_t fwd(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
-  const Shape sh = shape_of(c.H / VEC, VPT);
-  const size_t smem = (size_t)STAGES * 2 * 2 * VPT * MAXT * 16;
-  auto kern = block_norm_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES>;
-  int grid = 0;
+  const size_t smem = (size_t)STAGES * 2 * 2 * VPT * MAXT * sizeof(Piece<T, VEC>);
   static std::atomic<uint32_t> last{0};
-  cudaError_t e = grid_of(kern, last, sh, smem, c.T, &grid);
-  if (e != cudaSuccess) return e;
-  kern<<<grid, dim3(sh.tpr, sh.groups), smem, s>>>(in, r, n, c.T, c.H, c.eps, c.res_scale);
-  return cudaGetLastError();
+  int walkers = 0;
+  return launch_rows<CL>(block_norm_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES, CL>, last, shape_of(c.H / VEC, VPT, CL),
+                         smem, c.T, s, &walkers, in, r, n, c.T, c.H, c.eps, c.res_scale);
 }
 
-template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES>
+template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
 cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
-  const Shape sh = shape_of(c.H / VEC, VPT);
-  const size_t smem = (size_t)STAGES * 4 * VPT * MAXT * 16;
-  auto kern = block_norm_bwd_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES>;
-  int grid = 0;
+  const Shape sh = shape_of(c.H / VEC, VPT, CL);
+  const size_t smem = (size_t)STAGES * 4 * VPT * MAXT * sizeof(Piece<T, VEC>);
   static std::atomic<uint32_t> last{0};
-  cudaError_t e = grid_of(kern, last, sh, smem, c.T, &grid);
-  if (e != cudaSuccess) return e;
-  kern<<<grid, dim3(sh.tpr, sh.groups), smem, s>>>(b, part, c.T, c.H, c.eps, c.res_scale);
-  e = cudaGetLastError();
+  int walkers = 0;
+  cudaError_t e = launch_rows<CL>(block_norm_bwd_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES, CL>, last, sh, smem, c.T, s,
+                                  &walkers, b, part, c.T, c.H, c.eps, c.res_scale);
   if (e != cudaSuccess || !(b.dgate || b.dw_post || b.dw_next)) return e;
-  colsum_kernel<<<dim3((unsigned)ceil_div(c.H, 32), 2), dim3(32, 32), 0, s>>>(part, grid * sh.groups, c.H, b);
+  colsum_kernel<<<dim3((unsigned)ceil_div(c.H, 32), 2), dim3(32, 32), 0, s>>>(part, walkers * sh.groups, c.H, b);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// A row's pieces are spread over at most 1024 threads: bf16 rows have up to 2048 16-byte
-// pieces (H = 16384), fp32 rows up to 4096, rows of odd width up to 16384 elements. S1 / S2:
-// stages of the ring with one / two pieces per thread (forward: stages of two rows), as many as
-// leave room for several CTAs (S1) or one (S2) on an SM. Rows of more than 1024 pieces and odd
-// widths do without the ring.
-#define NORM_DISPATCH(FN, S1, S2, ...)                                                         \
-  if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0) {                                         \
-    const int nvec = c.H / 8;                                                                  \
-    if (nvec <= 256) return FN<__nv_bfloat16, 8, 1, true, 256, S1>(__VA_ARGS__);               \
-    if (nvec <= 1024) return FN<__nv_bfloat16, 8, 2, true, 512, S2>(__VA_ARGS__);              \
-    return FN<__nv_bfloat16, 8, 4, false, 512, 0>(__VA_ARGS__);                                \
-  }                                                                                            \
-  if (c.act_dtype == MOE_DTYPE_F32 && c.H % 4 == 0) {                                          \
-    const int nvec = c.H / 4;                                                                  \
-    if (nvec <= 256) return FN<float, 4, 1, true, 256, S1>(__VA_ARGS__);                       \
-    if (nvec <= 1024) return FN<float, 4, 2, true, 512, S2>(__VA_ARGS__);                      \
-    if (nvec <= 2048) return FN<float, 4, 4, false, 512, 0>(__VA_ARGS__);                      \
-    return FN<float, 4, 4, false, 1024, 0>(__VA_ARGS__);                                       \
-  }                                                                                            \
-  if (c.act_dtype == MOE_DTYPE_BF16) {                                                         \
-    if (c.H <= 2048) return FN<__nv_bfloat16, 1, 8, true, 256, 0>(__VA_ARGS__);                \
-    return FN<__nv_bfloat16, 1, 16, false, 1024, 0>(__VA_ARGS__);                              \
-  }                                                                                            \
-  if (c.H <= 2048) return FN<float, 1, 8, true, 256, 0>(__VA_ARGS__);                          \
-  return FN<float, 1, 16, false, 1024, 0>(__VA_ARGS__);
+// How a row is spread: pieces of VEC elements, at most 1024 pieces per CTA (two per thread), so
+// a cluster of 2 or 4 CTAs for wider rows. Rows of H not a multiple of 16 bytes have pieces of
+// 4 bytes (4 to 16 per thread); an odd number of bf16 channels leaves nothing for cp.async to
+// copy, and takes single elements without the ring. S1 / S2: stages of the ring with one / two
+// pieces per thread (forward: stages of two rows), as many as leave room for several CTAs (S1)
+// or one (S2) on an SM; S4: with four pieces of 4 bytes.
+#define NORM_DISPATCH(FN, S1, S2, S4, ...)                                                        \
+  if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0) {                                            \
+    const int nvec = c.H / 8;                                                                     \
+    if (nvec <= 256) return FN<__nv_bfloat16, 8, 1, true, 256, S1, 1>(__VA_ARGS__);               \
+    if (nvec <= 1024) return FN<__nv_bfloat16, 8, 2, true, 512, S2, 1>(__VA_ARGS__);              \
+    return FN<__nv_bfloat16, 8, 2, true, 512, S2, 2>(__VA_ARGS__);                                \
+  }                                                                                               \
+  if (c.act_dtype == MOE_DTYPE_F32 && c.H % 4 == 0) {                                             \
+    const int nvec = c.H / 4;                                                                     \
+    if (nvec <= 256) return FN<float, 4, 1, true, 256, S1, 1>(__VA_ARGS__);                       \
+    if (nvec <= 1024) return FN<float, 4, 2, true, 512, S2, 1>(__VA_ARGS__);                      \
+    if (nvec <= 2048) return FN<float, 4, 2, true, 512, S2, 2>(__VA_ARGS__);                      \
+    return FN<float, 4, 2, true, 512, S2, 4>(__VA_ARGS__);                                        \
+  }                                                                                               \
+  if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 2 == 0) {                                            \
+    if (c.H <= 2048) return FN<__nv_bfloat16, 2, 4, true, 256, S4, 1>(__VA_ARGS__);               \
+    return FN<__nv_bfloat16, 2, 8, false, 1024, 0, 1>(__VA_ARGS__);                               \
+  }                                                                                               \
+  if (c.act_dtype == MOE_DTYPE_BF16) {                                                            \
+    if (c.H <= 2048) return FN<__nv_bfloat16, 1, 8, true, 256, 0, 1>(__VA_ARGS__);                \
+    return FN<__nv_bfloat16, 1, 16, false, 1024, 0, 1>(__VA_ARGS__);                              \
+  }                                                                                               \
+  if (c.H <= 1024) return FN<float, 1, 4, true, 256, S4, 1>(__VA_ARGS__);                         \
+  if (c.H <= 2048) return FN<float, 1, 8, true, 256, 0, 1>(__VA_ARGS__);                          \
+  return FN<float, 1, 16, false, 1024, 0, 1>(__VA_ARGS__);
 
 cudaError_t launch_block_norm(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  NORM_DISPATCH(fwd, 3, 3, c, in, r, n, s)
+  NORM_DISPATCH(fwd, 3, 3, 3, c, in, r, n, s)
 }
 
 cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
@@ -609,17 +684,15 @@ cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd
       if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)c.H * 4, s);
     return e;
   }
-  NORM_DISPATCH(bwd, 4, 3, c, b, part, s)
+  NORM_DISPATCH(bwd, 4, 3, 4, c, b, part, s)
 }
 
-// Two sets of column sums for every row group of the largest grid: at most 2048 / (threads of
-// a row) row groups on each of 152 SMs, and never more than one per row.
+// Two sets of column sums for every row group of the largest grid: never more than one row
+// group per row, nor than 2048 threads of them on each of 152 SMs. A row has at least H / 16
+// threads.
 size_t norm_part_bytes(const moe_norm_config_t& c) {
-  const int vec = c.act_dtype == MOE_DTYPE_BF16 ? (c.H % 8 ? 1 : 8) : (c.H % 4 ? 1 : 4);
-  const int nvec = c.H / vec;
-  const int vpt = vec == 1 ? (c.H <= 2048 ? 8 : 16) : nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
-  const Shape sh = shape_of(nvec, vpt);
-  const int64_t groups = std::min<int64_t>(align_up(c.T, sh.groups), (int64_t)kNormMaxSms * (2048 / sh.tpr));
+  const int64_t threads = align_up((size_t)ceil_div(c.H, 16), 32);
+  const int64_t groups = std::min<int64_t>((int64_t)c.T + 8, (int64_t)kNormMaxSms * 2048 / threads);
   return (size_t)(2 * groups * c.H * 4);
 }
 
