@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kSortThreads)
                        int32_t* stoken, int32_t* spos, int32_t* count, DeviceStatus* st) {
   __shared__ __align__(16) uint32_t other[2][kSortBlock];
   __shared__ int32_t counted;
+  let_next_begin();
   const int64_t base = (int64_t)blockIdx.x * kSortBlock;
   const int first = threadIdx.x * kKeys;  // this thread's first place in the block
   if (threadIdx.x == 0) counted = 0;
@@ -193,6 +194,8 @@ __global__ void __launch_bounds__(256)
     rank_kernel(const uint32_t* keys, const int32_t* block_count, int blocks, int32_t* stoken, int32_t* spos,
                 int32_t* count) {
   __shared__ __align__(16) uint32_t sk[kRankBlocks][kSortBlock];
+  let_next_begin();
+  after_previous();
   if (blockIdx.x == 0) {
     __shared__ int32_t total;
     if (threadIdx.x == 0) total = 0;
@@ -269,6 +272,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedBwd p) {
   using P = Vec<T, VEC>;
   __shared__ int32_t ids[kMaxChunk + 2];  // ids[i + 1] = token of the chunk's place i, with both neighbours
   __shared__ int32_t pos[kMaxChunk];
+  let_next_begin();
+  after_previous();
   const int nvec = p.H / VEC, c = blockIdx.y * 256 + threadIdx.x;
   const int n = *p.count;
   if ((int)blockIdx.x < p.chunks) {
@@ -353,6 +358,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedBwd p) {
 template <typename G, int VEC>
 __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedBwd p) {
   const int chunk = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  after_previous();
   const int n = *p.count;
   const int64_t e = ((int64_t)chunk + 1) * p.chunk, s = e - p.chunk;  // the chunk's places [s, e)
   if (e >= n) return;
@@ -373,14 +379,21 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedBwd p) {
   const int nvec = p.H / VEC, c = blockIdx.y * 32 + lane;
   if (c >= nvec) return;
   float acc[VEC];
-  const float* q = p.part + ((int64_t)chunk * 2 + 1) * p.H + (int64_t)c * VEC;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] = q[i];
-#pragma unroll 4
-  for (int k = chunk + 1; k <= last; ++k) {
-    const float* r = p.part + (int64_t)k * 2 * p.H + (int64_t)c * VEC;
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  // slot 1 of the first chunk, slot 0 of the further ones
+  using P = Vec<float, VEC>;
+  const P* part = reinterpret_cast<const P*>(p.part) + c;
+  part[((int64_t)chunk * 2 + 1) * nvec].add_to(acc);
+  constexpr int kAhead = 8;
+  for (int k0 = chunk + 1; k0 <= last; k0 += kAhead) {
+    P buf[kAhead];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] += __ldg(r + i);
+    for (int u = 0; u < kAhead; ++u)
+      if (k0 + u <= last) buf[u] = part[(int64_t)(k0 + u) * 2 * nvec];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (k0 + u <= last) buf[u].add_to(acc);
   }
   write_row<G, VEC>(p, v, c, acc);
 }
@@ -395,11 +408,11 @@ template <typename T, typename G, int VEC>
 cudaError_t sums(const moe_embed_config_t& c, EmbedBwd p, cudaStream_t s) {
   const int nvec = c.H / VEC;
   const int zero_blocks = p.accumulate ? 0 : (int)ceil_div(c.V, p.zero_rows);
-  embed_sum_kernel<T, G, VEC><<<dim3((unsigned)(p.chunks + zero_blocks), (unsigned)ceil_div(nvec, 256)), 256, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(embed_sum_kernel<T, G, VEC>,
+                                     dim3((unsigned)(p.chunks + zero_blocks), (unsigned)ceil_div(nvec, 256)), 256, s, p);
   if (e != cudaSuccess || p.chunks < 2) return e;
-  embed_join_kernel<G, VEC><<<dim3((unsigned)ceil_div(p.chunks - 1, 8), (unsigned)ceil_div(nvec, 32)), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(embed_join_kernel<G, VEC>, dim3((unsigned)ceil_div(p.chunks - 1, 8), (unsigned)ceil_div(nvec, 32)),
+                      256, s, p);
 }
 
 }  // namespace
@@ -458,8 +471,8 @@ cudaError_t launch_embed_backward(const moe_embed_config_t& c, const int32_t* to
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (blocks > 1) {
-    rank_kernel<<<blocks * (kSortBlock / 256), 256, 0, s>>>(keys, bcount, blocks, stoken, spos, count);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(rank_kernel, blocks * (kSortBlock / 256), 256, s, keys, bcount, blocks, stoken, spos, count);
+    if (e != cudaSuccess) return e;
   }
   EmbedBwd p{stoken, spos, count, dout, dtable, reinterpret_cast<float*>(w + L.part)};
   p.H = c.H;

@@ -98,6 +98,8 @@ __device__ __forceinline__ void values(const uint4& p, bool bf, float (&f)[8]) {
 __global__ void __launch_bounds__(kThreads)
     sum_squares_kernel(const __grid_constant__ ClipList list, double* sums, int slot0, int last, float max_norm,
                        float* norm, ClipState* state, DeviceStatus* st) {
+  let_next_begin();
+  if (slot0 > 0) after_previous();  // an earlier launch of the same call
   const int64_t tiles = list.tile0[list.count];
   double total = 0.0;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -169,13 +171,12 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ ClipList list, const ClipState* state) {
-  const float scale = *reinterpret_cast<const volatile float*>(&state->scale);
   const int64_t tiles = list.tile0[list.count];
+  float scale = 0.0f;  // read once the norm is there; the first tile is on its way by then
   for (int64_t back = blockIdx.x; back < tiles; back += gridDim.x) {
     const int64_t tile = tiles - 1 - back;
     const int k = tensor_of(list, tile);
     const ClipTensor t = list.t[k];
-    if (scale == 1.0f && t.in == t.out) continue;
     const View v = view_of(t);
     const bool bf = t.n2 & 1;
     uint8_t* out0 = static_cast<uint8_t*>(t.out) - v.lo * (bf ? 2 : 4);  // the place of element 0 of piece 0
@@ -186,6 +187,13 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     for (int j = 0; j < kShare; ++j) {
       const int64_t i = p0 + j * kThreads;
       if (i < v.pieces) p[j] = load_piece(v, i, bf);
+    }
+    if (back == blockIdx.x) {
+      after_previous();
+      scale = *reinterpret_cast<const volatile float*>(&state->scale);
+    }
+    if (scale == 1.0f) {
+      if (t.in == t.out) continue;
     }
 #pragma unroll
     for (int j = 0; j < kShare; ++j) {
@@ -258,9 +266,14 @@ cudaError_t launch_grad_clip(const moe_grad_t* grads, int32_t count, float max_n
     while (rest < count && grads[rest].n == 0) ++rest;
     at = rest;
     const int grid = grid_of(l);
-    sum_squares_kernel<<<grid, kThreads, 0, s>>>(l, sums, slot, at >= count, max_norm, norm, state, st);
+    cudaError_t e;
+    if (slot == 0) {
+      sum_squares_kernel<<<grid, kThreads, 0, s>>>(l, sums, slot, at >= count, max_norm, norm, state, st);
+      e = cudaGetLastError();
+    } else {
+      e = launch_after(sum_squares_kernel, grid, kThreads, s, l, sums, slot, at >= count, max_norm, norm, state, st);
+    }
     slot += grid;
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   } while (at < count);
   if (max_norm < 0.0f) return cudaSuccess;
@@ -268,8 +281,7 @@ cudaError_t launch_grad_clip(const moe_grad_t* grads, int32_t count, float max_n
   while (at < count) {
     fill(&l, grads, count, &at);
     if (l.count == 0) break;
-    scale_kernel<<<grid_of(l), kThreads, 0, s>>>(l, state);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(scale_kernel, grid_of(l), kThreads, s, l, static_cast<const ClipState*>(state));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kBmn = MODE == DX || MODE == DW;   // the same for B
   constexpr int kBoxes = (BN / CG) / 64;
   extern __shared__ uint8_t smem_raw[];
+  let_next_begin();  // the small kernel that joins the tiles' results
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kABytes;
@@ -553,6 +554,7 @@ HeadParams base_params(int64_t M, int64_t N, int64_t K, int tm, int tn, DeviceSt
 // dx of the tiles whose K was split: the sum of a tile's slices in order, written or added.
 template <typename T>
 __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, int tm, int tn, T* out) {
+  after_previous();
   const int tile = p.direct + blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;  // 4 columns each
   const int nb = tile / p.m_tiles, mb = tile - nb * p.m_tiles;
   const int row = mb * tm + e / tn, col = nb * tn + e % tn;
@@ -649,9 +651,9 @@ cudaError_t launch_head_piece(const moe_head_config_t& c, const void* x, const v
     if (e != cudaSuccess) return e;
     if (split.splits > 1) {
       const dim3 grid((unsigned)(tm * tn / 1024), (unsigned)(p.m_tiles * p.n_tiles - p.direct));
-      if (dx_f32) join_slices_kernel<float><<<grid, 256, 0, s>>>(p, tm, tn, static_cast<float*>(dx));
-      else join_slices_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p, tm, tn, static_cast<__nv_bfloat16*>(dx));
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = dx_f32 ? launch_after(join_slices_kernel<float>, grid, 256, s, p, tm, tn, static_cast<float*>(dx))
+                 : launch_after(join_slices_kernel<__nv_bfloat16>, grid, 256, s, p, tm, tn, static_cast<__nv_bfloat16*>(dx));
+      if (e != cudaSuccess) return e;
     }
   }
   if (dw) {  // M = the piece's vocabulary rows, N = H, K = T
@@ -707,6 +709,8 @@ enum { S_STATS = 0, S_DLOGITS = 1, S_STORE = 2 };
 template <int MODE, int ST>
 __global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
   constexpr int TN = ST / 16, NT = ST * 2, LD = ST + 4;
+  let_next_begin();
+  after_previous();
   __shared__ __align__(16) float sa[2][SK][LD], sb[2][SK][LD];
   const int m0 = blockIdx.x * ST, n0 = blockIdx.y * ST;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -873,6 +877,9 @@ cudaError_t launch_simt(SimtParams p, cudaStream_t s) {
   p.k_split = (int)(ceil_div(ceil_div(p.K, p.splits), SK) * SK);
   const int st = simt_tile(p.M, p.N, p.splits);
   const dim3 grid((unsigned)ceil_div(p.M, st), (unsigned)ceil_div(p.N, st), (unsigned)p.splits);
+  // a call begins with a plain launch (the logits), the products after it follow closely
+  if (MODE == S_STORE)
+    return st == 128 ? launch_after(simt_kernel<MODE, 128>, grid, 256, s, p) : launch_after(simt_kernel<MODE, 64>, grid, 128, s, p);
   if (st == 128) simt_kernel<MODE, 128><<<grid, 256, 0, s>>>(p);
   else simt_kernel<MODE, 64><<<grid, 128, 0, s>>>(p);
   return cudaGetLastError();
@@ -889,6 +896,7 @@ __global__ void __launch_bounds__(1024)
   constexpr int kLanes = 1024 / TOK, kAhead = 4;
   __shared__ float sm[32][TOK], ss[32][TOK];
   __shared__ bool finish;
+  after_previous();
   const int tok = threadIdx.x % TOK, lane = threadIdx.x / TOK, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * TOK + tok;
   float m = -INFINITY, s = 0.0f;
@@ -970,6 +978,7 @@ __global__ void __launch_bounds__(1024)
 // dx = the sum of the K splits' slices [splits][T H], in order.
 template <typename T>
 __global__ void __launch_bounds__(256) join_dx_kernel(const float* slices, int splits, int64_t n, T* dx) {
+  after_previous();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float v = 0.0f;
@@ -1049,10 +1058,10 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
   // the ticket lives in the head, which moe_workspace_init clears
   auto* ticket = reinterpret_cast<uint32_t*>(b + 320);
   if (c.T >= 1024)
-    join_kernel<32><<<(unsigned)ceil_div(c.T, 32), 1024, 0, s>>>(part, parts, c.T, c.V, target, tl, loss, lse, mean, ticket, st);
-  else
-    join_kernel<4><<<(unsigned)ceil_div(c.T, 4), 1024, 0, s>>>(part, parts, c.T, c.V, target, tl, loss, lse, mean, ticket, st);
-  return cudaGetLastError();
+    return launch_after(join_kernel<32>, (unsigned)ceil_div(c.T, 32), 1024, s, part, parts, c.T, c.V, target, tl, loss, lse,
+                        mean, ticket, st);
+  return launch_after(join_kernel<4>, (unsigned)ceil_div(c.T, 4), 1024, s, part, parts, c.T, c.V, target, tl, loss, lse, mean,
+                      ticket, st);
 }
 
 cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
@@ -1104,9 +1113,9 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   const int64_t n = (int64_t)c.T * c.H;
   const int splits = tc ? 1 : L.split.splits;
   const unsigned grid = (unsigned)ceil_div(n, 256);
-  if (f32) join_dx_kernel<float><<<grid, 256, 0, s>>>(slices, splits, n, static_cast<float*>(dx));
-  else join_dx_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(slices, splits, n, static_cast<__nv_bfloat16*>(dx));
-  return cudaGetLastError();
+  const float* from = slices;
+  return f32 ? launch_after(join_dx_kernel<float>, grid, 256, s, from, splits, n, static_cast<float*>(dx))
+             : launch_after(join_dx_kernel<__nv_bfloat16>, grid, 256, s, from, splits, n, static_cast<__nv_bfloat16*>(dx));
 }
 
 }  // namespace moe

@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
 template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
     block_norm_bwd_kernel(NormBwd b, float* part, int T_, int H, float eps, float res_scale) {
+  let_next_begin();
   using P = Piece<T, VEC>;
   using E = typename P::E;
   constexpr int N = P::N;
@@ -546,6 +547,7 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* part, int np,
   __shared__ float acc[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
   const bool second = blockIdx.y == 1;
+  after_previous();
   if (second ? !b.dw_next : !(b.dgate || b.dw_post)) return;
   const float* p = part + (second ? (int64_t)np * H : 0);
   float v = 0.0f;
@@ -634,8 +636,7 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
   cudaError_t e = launch_rows<CL>(block_norm_bwd_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES, CL>, last, sh, smem, c.T, s,
                                   &walkers, b, part, c.T, c.H, c.eps, c.res_scale);
   if (e != cudaSuccess || !(b.dgate || b.dw_post || b.dw_next)) return e;
-  colsum_kernel<<<dim3((unsigned)ceil_div(c.H, 32), 2), dim3(32, 32), 0, s>>>(part, walkers * sh.groups, c.H, b);
-  return cudaGetLastError();
+  return launch_after(colsum_kernel, dim3((unsigned)ceil_div(c.H, 32), 2), dim3(32, 32), s, part, walkers * sh.groups, c.H, b);
 }
 
 }  // namespace
