@@ -4,9 +4,12 @@
 // writes them once. The list of tensors travels in the kernel parameters, kPerLaunch tensors a
 // launch, so a call needs no device table and captures into a graph. Each tensor is cut into
 // tiles of kTile 16-byte pieces between 16-byte boundaries, so a view that starts at any
-// element still moves as whole pieces but for its two ends; the blocks of a persistent grid
-// take the tiles in turn. The scaling walks them in the opposite order: what the norm read
-// last is still in L2.
+// element still moves as whole pieces but for its two ends. The grids are many blocks of few
+// tiles: a persistent grid of what is resident keeps its blocks in step, with the reads and the
+// writes of all of them on the same DRAM pages (604 M fp32 elements: scaling 1336 us with 4
+// blocks per SM, 870 with 8, 767 with 64, 759 with a block per tile, of 712 for the bytes; the
+// sum 395, 407, 354). The scaling walks the tiles in the opposite order: of a list the size of
+// L2, what the norm read last is still there.
 //
 // Squares are added in fp32 over the 8 pieces of one thread's share of a tile and in fp64
 // from there on (one fp64 add per 32 or 64 elements; every element in fp64 would be bound by
@@ -21,10 +24,11 @@ namespace moe {
 namespace {
 
 constexpr int kPerLaunch = 120;   // 24 bytes each: the parameters stay below 4 KB
-constexpr int kThreads = 256;
 constexpr int kShare = 8;         // pieces of a tile per thread
-constexpr int kTile = kThreads * kShare;
-constexpr int kMaxBlocks = 152 * 8;
+constexpr int kMaxBlocks = 152 * 64;  // of the sum: its blocks' sums are added by one block
+// Threads of a block: 256, or 128 for lists that would give an SM fewer than four tiles of 256
+// (48 views, 3 M elements: sum 8.4 -> 7.7, scaling 7.6 -> 5.9 us; 604 M: scaling 759 -> 788 us).
+constexpr int kThreadsLarge = 256, kThreadsSmall = 128;
 
 struct ClipTensor {
   const void* in;
@@ -33,7 +37,7 @@ struct ClipTensor {
 };
 struct ClipList {
   ClipTensor t[kPerLaunch];
-  int64_t tile0[kPerLaunch + 1];  // first tile of each tensor
+  int64_t tile0[kPerLaunch + 1];  // first tile (kShare pieces per thread) of each tensor
   int count;
 };
 static_assert(sizeof(ClipList) <= 4096 - 64, "kernel parameters");
@@ -95,9 +99,11 @@ __device__ __forceinline__ void values(const uint4& p, bool bf, float (&f)[8]) {
   }
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads)
     sum_squares_kernel(const __grid_constant__ ClipList list, double* sums, int slot0, int last, float max_norm,
                        float* norm, ClipState* state, DeviceStatus* st) {
+  constexpr int kTile = kThreads * kShare;
   let_next_begin();
   if (slot0 > 0) after_previous();  // an earlier launch of the same call
   const int64_t tiles = list.tile0[list.count];
@@ -170,7 +176,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ ClipList list, const ClipState* state) {
+  constexpr int kTile = kThreads * kShare;
   const int64_t tiles = list.tile0[list.count];
   float scale = 0.0f;  // read once the norm is there; the first tile is on its way by then
   for (int64_t back = blockIdx.x; back < tiles; back += gridDim.x) {
@@ -225,66 +233,72 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
   }
 }
 
+// The pieces a gradient spans, from the 16-byte boundary before it.
+int64_t pieces_of(const moe_grad_t& g) {
+  const bool bf = g.dtype == MOE_DTYPE_BF16;
+  return ceil_div((int64_t)((uintptr_t)g.grad & 15) / (bf ? 2 : 4) + g.n, bf ? 8 : 4);
+}
+
 // The next launch's tensors, from grads[*at] on (empty ones are left out).
-void fill(ClipList* l, const moe_grad_t* grads, int32_t count, int32_t* at) {
+void fill(ClipList* l, const moe_grad_t* grads, int32_t count, int tile, int32_t* at) {
   l->count = 0;
   l->tile0[0] = 0;
-  for (; *at < count && l->count < kPerLaunch; ++*at) {
+  for (; *at < count && (l->count < kPerLaunch || grads[*at].n == 0); ++*at) {
     const moe_grad_t& g = grads[*at];
     if (g.n == 0) continue;
-    const bool bf = g.dtype == MOE_DTYPE_BF16;
-    const int64_t lead = (int64_t)((uintptr_t)g.grad & 15) / (bf ? 2 : 4);
-    const int64_t pieces = ceil_div(lead + g.n, bf ? 8 : 4);
-    l->t[l->count] = {g.grad, g.out ? g.out : const_cast<void*>(g.grad), g.n * 2 + (bf ? 1 : 0)};
-    l->tile0[l->count + 1] = l->tile0[l->count] + ceil_div(pieces, kTile);
+    l->t[l->count] = {g.grad, g.out ? g.out : const_cast<void*>(g.grad), g.n * 2 + (g.dtype == MOE_DTYPE_BF16 ? 1 : 0)};
+    l->tile0[l->count + 1] = l->tile0[l->count] + ceil_div(pieces_of(g), tile);
     ++l->count;
   }
 }
 
-int grid_of(const ClipList& l) {
-  return (int)std::min<int64_t>(std::max<int64_t>(l.tile0[l.count], 1), std::min(tc::num_sms() * 8, kMaxBlocks));
+template <int kThreads>
+cudaError_t clip_launches(const moe_grad_t* grads, int32_t count, float max_norm, float* norm, char* w, DeviceStatus* st,
+                          cudaStream_t s) {
+  // the ticket lives in the head, which moe_workspace_init clears
+  ClipState* state = reinterpret_cast<ClipState*>(w + 256);
+  double* sums = reinterpret_cast<double*>(w + kWsHead);
+  ClipList l;
+  int slot = 0;
+  int32_t at = 0;
+  do {
+    fill(&l, grads, count, kThreads * kShare, &at);
+    const int grid = (int)std::min<int64_t>(std::max<int64_t>(l.tile0[l.count], 1), kMaxBlocks);
+    cudaError_t e;
+    if (slot == 0) {
+      sum_squares_kernel<kThreads><<<grid, kThreads, 0, s>>>(l, sums, slot, at >= count, max_norm, norm, state, st);
+      e = cudaGetLastError();
+    } else {
+      e = launch_after(sum_squares_kernel<kThreads>, grid, kThreads, s, l, sums, slot, at >= count, max_norm, norm, state, st);
+    }
+    if (e != cudaSuccess) return e;
+    slot += grid;
+  } while (at < count);
+  if (max_norm < 0.0f) return cudaSuccess;
+  at = 0;
+  while (at < count) {
+    fill(&l, grads, count, kThreads * kShare, &at);
+    if (l.count == 0) break;
+    const unsigned grid = (unsigned)std::min<int64_t>(l.tile0[l.count], INT32_MAX);
+    const cudaError_t e = launch_after(scale_kernel<kThreads>, grid, kThreads, s, l, static_cast<const ClipState*>(state));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
 size_t grad_clip_ws_bytes(int32_t count) {
-  return kWsHead + 256 + align_up((size_t)std::max<int64_t>(1, ceil_div(count, kPerLaunch)) * kMaxBlocks * 8, 256);
+  return kWsHead + (size_t)std::max<int64_t>(1, ceil_div(count, kPerLaunch)) * kMaxBlocks * 8;
 }
 
 cudaError_t launch_grad_clip(const moe_grad_t* grads, int32_t count, float max_norm, float* norm, void* ws,
                              DeviceStatus* st, cudaStream_t s) {
-  char* w = static_cast<char*>(ws);
-  // the ticket lives in the head, which moe_workspace_init clears
-  ClipState* state = reinterpret_cast<ClipState*>(w + 256);
-  double* sums = reinterpret_cast<double*>(w + kWsHead + 256);
-  ClipList l;
-  int slot = 0;
-  int32_t at = 0;
-  do {
-    fill(&l, grads, count, &at);
-    int32_t rest = at;
-    while (rest < count && grads[rest].n == 0) ++rest;
-    at = rest;
-    const int grid = grid_of(l);
-    cudaError_t e;
-    if (slot == 0) {
-      sum_squares_kernel<<<grid, kThreads, 0, s>>>(l, sums, slot, at >= count, max_norm, norm, state, st);
-      e = cudaGetLastError();
-    } else {
-      e = launch_after(sum_squares_kernel, grid, kThreads, s, l, sums, slot, at >= count, max_norm, norm, state, st);
-    }
-    slot += grid;
-    if (e != cudaSuccess) return e;
-  } while (at < count);
-  if (max_norm < 0.0f) return cudaSuccess;
-  at = 0;
-  while (at < count) {
-    fill(&l, grads, count, &at);
-    if (l.count == 0) break;
-    const cudaError_t e = launch_after(scale_kernel, grid_of(l), kThreads, s, l, static_cast<const ClipState*>(state));
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  int64_t pieces = 0;
+  for (int32_t i = 0; i < count; ++i) pieces += grads[i].n ? pieces_of(grads[i]) : 0;
+  return pieces < (int64_t)4 * 152 * kThreadsLarge * kShare
+             ? clip_launches<kThreadsSmall>(grads, count, max_norm, norm, static_cast<char*>(ws), st, s)
+             : clip_launches<kThreadsLarge>(grads, count, max_norm, norm, static_cast<char*>(ws), st, s);
 }
 
 }  // namespace moe
