@@ -115,15 +115,15 @@ __device__ __forceinline__ void cp_wait() {
 // multiple of 32), in a fixed order, in two halves so that a barrier of the caller's stands
 // between them. Both work on kP values at once (NV rounded up to a power of two): a lane ends
 // up with the value lane / (32 / kP), which takes 9 shuffles for 8 values instead of 40.
-// With CL > 1 a row's channels are spread over a cluster of CL CTAs, and the totals are taken
-// from all of them.
+// With CL > 1 a row's channels are spread over a cluster of CL CTAs, and every warp's sums are
+// written to all of them (read from there, 28 loads of 250 cycles each came one after another).
 constexpr int kMaxWarps = 32;
 constexpr int kNormMaxSms = 152;  // bounds the grid, and so the backward's column partial sums
 template <int NV, int CL>
 struct RowSums {
   static constexpr int kP = NV <= 1 ? 1 : NV <= 2 ? 2 : NV <= 4 ? 4 : 8;
   static constexpr int kLanes = 32 / kP;
-  float buf[2][kP * kMaxWarps];  // [parity][group][value][warp]
+  float buf[2][kP * kMaxWarps * CL];  // [parity][group][value][CTA][warp]
 
   __device__ __forceinline__ void publish(const float (&in)[NV], int parity) {
     float v[kP];
@@ -145,26 +145,28 @@ struct RowSums {
         v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
       }
     }
-    if (lane % kLanes == 0)
-      buf[parity][(threadIdx.y * kP + lane / kLanes) * warps + (threadIdx.x >> 5)] = v[0];
+    if (lane % kLanes == 0) {
+      const int rank = CL > 1 ? blockIdx.x % CL : 0;
+      float* mine = buf[parity] + ((threadIdx.y * kP + lane / kLanes) * CL + rank) * warps + (threadIdx.x >> 5);
+      if constexpr (CL == 1) {
+        *mine = v[0];
+      } else {
+        const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+#pragma unroll
+        for (int r = 0; r < CL; ++r) {
+          uint32_t at;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(here), "r"(r));
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[0]) : "memory");
+        }
+      }
+    }
   }
   // The sums that were published with this parity, in every thread.
   __device__ __forceinline__ void total(float (&out)[NV], int parity) const {
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warps = (blockDim.x >> 5) * CL;
     const float* b = buf[parity] + (threadIdx.y * kP + lane / kLanes) * warps;
     float t = 0.0f;
-    if constexpr (CL == 1) {
-      for (int w = lane % kLanes; w < warps; w += kLanes) t += b[w];
-    } else {
-      const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(b));
-      for (int w = lane % kLanes; w < warps * CL; w += kLanes) {
-        uint32_t at;
-        float v;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(here + w / CL * 4), "r"(w % CL));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-        t += v;
-      }
-    }
+    for (int w = lane % kLanes; w < warps; w += kLanes) t += b[w];
 #pragma unroll
     for (int off = kLanes / 2; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
 #pragma unroll
@@ -267,7 +269,7 @@ __device__ __forceinline__ float inv_rms(float sum, float inv_h, float eps) { re
 
 // ROWS rows per iteration: i ROWS + k is row (first + (i ROWS + k) step) of the group.
 template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
+__global__ void __launch_bounds__(MAXT, MAXT <= 128 ? 4 : MAXT <= 256 || (MAXT <= 512 && STAGES == 0) ? 2 : 1)
     block_norm_kernel(NormIn in, void* r_out, void* n_out, int T_, int H, float eps, float res_scale) {
   using P = Piece<T, VEC>;
   using E = typename P::E;
@@ -287,6 +289,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
   // the same for every group of the CTA: the rows of its first one
   const int iters = (int)ceil_div(ceil_div(T_ - (int64_t)cta * groups, step), ROWS);
   rows.zero_ring();
+  if constexpr (CL > 1) row_barrier<CL>();  // the whole cluster runs before its shared memory is written
   auto fetch = [&](int64_t row, int stage) {
     if constexpr (STAGES > 0) {
 #pragma unroll
@@ -386,7 +389,6 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
     // with one sum in use, its buffer is free again only after a second barrier
     if ((in.w_post != nullptr) != (n_out != nullptr)) row_barrier<CL>();
   }
-  if constexpr (CL > 1) row_barrier<CL>();  // the cluster may still be reading this CTA's sums
 }
 
 // Backward, per row, from the stored residual r and block output y (both statistics are
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
 // Each CTA keeps the column sums of its rows in registers and writes them once; colsum_kernel
 // adds the CTAs' sums in a fixed order.
 template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
+__global__ void __launch_bounds__(MAXT, MAXT <= 128 ? 4 : MAXT <= 256 || (MAXT <= 512 && STAGES == 0) ? 2 : 1)
     block_norm_bwd_kernel(NormBwd b, float* part, int T_, int H, float eps, float res_scale) {
   let_next_begin();
   using P = Piece<T, VEC>;
@@ -426,6 +428,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? (VEC > 1 ? 3 : 2) : 1)
   int64_t row = (int64_t)cta * groups + threadIdx.y - step;  // the row that is finished, one behind the sums
   const int iters = (int)ceil_div(T_ - (int64_t)cta * groups, step);
   rows.zero_ring();
+  if constexpr (CL > 1) row_barrier<CL>();  // the whole cluster runs before its shared memory is written
   if constexpr (STAGES > 0) {
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) {
@@ -571,10 +574,10 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* part, int np,
 struct Shape {
   int tpr, groups;
 };
-Shape shape_of(int nvec, int vpt, int cl) {
+Shape shape_of(int nvec, int vpt, int maxt, int cl) {
   Shape s;
   s.tpr = (int)(ceil_div(ceil_div(nvec, vpt * cl), 32) * 32);
-  s.groups = cl > 1 ? 1 : std::max(1, 256 / s.tpr);
+  s.groups = cl > 1 ? 1 : std::max(1, std::min(maxt, 256) / s.tpr);
   return s;
 }
 
@@ -623,13 +626,13 @@ cudaError_t fwd(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, 
   const size_t smem = (size_t)STAGES * 2 * 2 * VPT * MAXT * sizeof(Piece<T, VEC>);
   static std::atomic<uint32_t> last{0};
   int walkers = 0;
-  return launch_rows<CL>(block_norm_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES, CL>, last, shape_of(c.H / VEC, VPT, CL),
+  return launch_rows<CL>(block_norm_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES, CL>, last, shape_of(c.H / VEC, VPT, MAXT, CL),
                          smem, c.T, s, &walkers, in, r, n, c.T, c.H, c.eps, c.res_scale);
 }
 
 template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
 cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
-  const Shape sh = shape_of(c.H / VEC, VPT, CL);
+  const Shape sh = shape_of(c.H / VEC, VPT, MAXT, CL);
   const size_t smem = (size_t)STAGES * 4 * VPT * MAXT * sizeof(Piece<T, VEC>);
   static std::atomic<uint32_t> last{0};
   int walkers = 0;
@@ -644,19 +647,25 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
 // How a row is spread: pieces of VEC elements, at most 1024 pieces per CTA (two per thread), so
 // a cluster of 2 or 4 CTAs for wider rows. Rows of H not a multiple of 16 bytes have pieces of
 // 4 bytes (4 to 16 per thread); an odd number of bf16 channels leaves nothing for cp.async to
-// copy, and takes single elements without the ring. S1 / S2: stages of the ring with one / two
-// pieces per thread (forward: stages of two rows), as many as leave room for several CTAs (S1)
-// or one (S2) on an SM; S4: with four pieces of 4 bytes.
-#define NORM_DISPATCH(FN, S1, S2, S4, ...)                                                        \
+// copy, and takes single elements without the ring. V1: pieces per thread of rows of up to 256
+// pieces: 1 in the forward, 2 in the backward, whose bookkeeping per row and thread is near half
+// of its instructions (16384 x 2048: 88 -> 80 us; the forward is better with more threads, 49
+// against 51 us). S1, S2, S4: stages of the ring (forward: of two rows each) for those rows, for
+// wider ones and for pieces of 4 bytes, as many as leave room for several CTAs on an SM.
+#define NORM_DISPATCH(FN, V1, S1, S2, S4, ...)                                                    \
   if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0) {                                            \
     const int nvec = c.H / 8;                                                                     \
-    if (nvec <= 256) return FN<__nv_bfloat16, 8, 1, true, 256, S1, 1>(__VA_ARGS__);               \
+    if (nvec <= 32) return FN<__nv_bfloat16, 8, 1, true, 128, S1, 1>(__VA_ARGS__);                \
+    if (nvec <= 256) return FN<__nv_bfloat16, 8, V1, true, 256 / V1, S1, 1>(__VA_ARGS__);         \
+    if (nvec <= 512) return FN<__nv_bfloat16, 8, 2, true, 256, S2, 1>(__VA_ARGS__);               \
     if (nvec <= 1024) return FN<__nv_bfloat16, 8, 2, true, 512, S2, 1>(__VA_ARGS__);              \
     return FN<__nv_bfloat16, 8, 2, true, 512, S2, 2>(__VA_ARGS__);                                \
   }                                                                                               \
   if (c.act_dtype == MOE_DTYPE_F32 && c.H % 4 == 0) {                                             \
     const int nvec = c.H / 4;                                                                     \
-    if (nvec <= 256) return FN<float, 4, 1, true, 256, S1, 1>(__VA_ARGS__);                       \
+    if (nvec <= 32) return FN<float, 4, 1, true, 128, S1, 1>(__VA_ARGS__);                        \
+    if (nvec <= 256) return FN<float, 4, V1, true, 256 / V1, S1, 1>(__VA_ARGS__);                 \
+    if (nvec <= 512) return FN<float, 4, 2, true, 256, S2, 1>(__VA_ARGS__);                       \
     if (nvec <= 1024) return FN<float, 4, 2, true, 512, S2, 1>(__VA_ARGS__);                      \
     if (nvec <= 2048) return FN<float, 4, 2, true, 512, S2, 2>(__VA_ARGS__);                      \
     return FN<float, 4, 2, true, 512, S2, 4>(__VA_ARGS__);                                        \
@@ -666,16 +675,16 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
     return FN<__nv_bfloat16, 2, 8, false, 1024, 0, 1>(__VA_ARGS__);                               \
   }                                                                                               \
   if (c.act_dtype == MOE_DTYPE_BF16) {                                                            \
-    if (c.H <= 2048) return FN<__nv_bfloat16, 1, 8, true, 256, 0, 1>(__VA_ARGS__);                \
+    if (c.H <= 2048) return FN<__nv_bfloat16, 1, 4, true, 512, 0, 1>(__VA_ARGS__);                \
     return FN<__nv_bfloat16, 1, 16, false, 1024, 0, 1>(__VA_ARGS__);                              \
   }                                                                                               \
   if (c.H <= 1024) return FN<float, 1, 4, true, 256, S4, 1>(__VA_ARGS__);                         \
-  if (c.H <= 2048) return FN<float, 1, 8, true, 256, 0, 1>(__VA_ARGS__);                          \
+  if (c.H <= 2048) return FN<float, 1, 4, true, 512, 0, 1>(__VA_ARGS__);                          \
   return FN<float, 1, 16, false, 1024, 0, 1>(__VA_ARGS__);
 
 cudaError_t launch_block_norm(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  NORM_DISPATCH(fwd, 3, 3, 3, c, in, r, n, s)
+  NORM_DISPATCH(fwd, 1, 3, 3, 3, c, in, r, n, s)
 }
 
 cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
@@ -685,7 +694,7 @@ cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd
       if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)c.H * 4, s);
     return e;
   }
-  NORM_DISPATCH(bwd, 4, 3, 4, c, b, part, s)
+  NORM_DISPATCH(bwd, 2, 4, 3, 4, c, b, part, s)
 }
 
 // Two sets of column sums for every row group of the largest grid: never more than one row
