@@ -60,6 +60,28 @@ struct Vec<__nv_bfloat16, 8> {
   }
 };
 template <>
+struct Vec<float, 4> {
+  uint4 a;
+  __device__ void add_to(float (&f)[4]) const {
+    f[0] += __uint_as_float(a.x), f[1] += __uint_as_float(a.y), f[2] += __uint_as_float(a.z), f[3] += __uint_as_float(a.w);
+  }
+  __device__ static Vec of(const float (&f)[4]) {
+    return {make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]))};
+  }
+};
+template <>
+struct Vec<__nv_bfloat16, 4> {
+  uint2 a;
+  __device__ void add_to(float (&f)[4]) const {
+    f[0] += __uint_as_float(a.x << 16), f[1] += __uint_as_float(a.x & 0xffff0000u);
+    f[2] += __uint_as_float(a.y << 16), f[3] += __uint_as_float(a.y & 0xffff0000u);
+  }
+  __device__ static Vec of(const float (&f)[4]) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[0], f[1]), q = __floats2bfloat162_rn(f[2], f[3]);
+    return {make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q))};
+  }
+};
+template <>
 struct Vec<float, 1> {
   float a;
   __device__ void add_to(float (&f)[1]) const { f[0] += a; }
@@ -323,12 +345,16 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedBwd p) {
     const int v0 = ((int)blockIdx.x - p.chunks) * p.zero_rows, v1 = min(p.V, v0 + p.zero_rows);
     __shared__ uint32_t seen[kMaxChunk / 32];
     for (int i = threadIdx.x; i < kMaxChunk / 32; i += 256) seen[i] = 0;
-    int lo = 0, hi = n;
-    while (lo < hi) {
-      const int mid = lo + (hi - lo) / 2;
-      if (__ldg(p.stoken + mid) < v0) lo = mid + 1;
-      else hi = mid;
+    // every warp: the lanes try a place each, 32 times closer per step
+    int lo = -1, hi = n;  // the first place with a token >= v0 is in (lo, hi]
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + (int)(threadIdx.x % 32 + 1) * step;
+      const bool less = at < hi && __ldg(p.stoken + at) < v0;
+      const int k = __popc(__ballot_sync(0xffffffffu, less));  // sorted: the places below v0 are the first k
+      hi = min(hi, lo + (k + 1) * step);
+      lo += k * step;
     }
+    lo = hi;
     __syncthreads();
     for (int i = lo + threadIdx.x; i < n; i += 256) {
       const int v = p.stoken[i];
@@ -385,7 +411,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedBwd p) {
   using P = Vec<float, VEC>;
   const P* part = reinterpret_cast<const P*>(p.part) + c;
   part[((int64_t)chunk * 2 + 1) * nvec].add_to(acc);
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   for (int k0 = chunk + 1; k0 <= last; k0 += kAhead) {
     P buf[kAhead];
 #pragma unroll
@@ -411,8 +437,9 @@ cudaError_t sums(const moe_embed_config_t& c, EmbedBwd p, cudaStream_t s) {
   const cudaError_t e = launch_after(embed_sum_kernel<T, G, VEC>,
                                      dim3((unsigned)(p.chunks + zero_blocks), (unsigned)ceil_div(nvec, 256)), 256, s, p);
   if (e != cudaSuccess || p.chunks < 2) return e;
-  return launch_after(embed_join_kernel<G, VEC>, dim3((unsigned)ceil_div(p.chunks - 1, 8), (unsigned)ceil_div(nvec, 32)),
-                      256, s, p);
+  constexpr int JV = VEC > 4 ? 4 : VEC;  // fewer columns per lane, more partial sums in flight
+  return launch_after(embed_join_kernel<G, JV>,
+                      dim3((unsigned)ceil_div(p.chunks - 1, 8), (unsigned)ceil_div(c.H / JV, 32)), 256, s, p);
 }
 
 }  // namespace
@@ -479,7 +506,7 @@ cudaError_t launch_embed_backward(const moe_embed_config_t& c, const int32_t* to
   p.V = c.V;
   p.chunk = chunk_of(c.T);
   p.chunks = (int)ceil_div(c.T, p.chunk);
-  p.zero_rows = 64;
+  p.zero_rows = 32;
   p.accumulate = accumulate;
   p.scale = c.scale;
   if (wide) {

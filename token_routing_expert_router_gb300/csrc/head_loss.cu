@@ -363,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (MODE == STATS) {
         // this row's half of the tile's columns, out of TMEM before anything is made of it
         uint32_t zr[kCols / 32][32];
-        auto z = [&](int i) { return __uint_as_float(zr[i / 32][i % 32]); };
         const int runs = runs_of(t);
         bool ok = true;
         for (int run = 0; run < runs; ++run) {
@@ -387,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           release();
         }
         if (!ok) break;
+        auto z = [&](int i) { return __uint_as_float(zr[i / 32][i % 32]); };
         const int cols = p.N - col0;  // columns from here on that exist
         const int tgt = live ? __ldg(p.target + row) : -1;
         if (tgt >= col0 && tgt < min(col0 + kCols, p.N)) {
@@ -672,9 +672,11 @@ cudaError_t launch_head_piece(const moe_head_config_t& c, const void* x, const v
 
 namespace {
 
-// ---- exact fp32 tiles, K steps of 16. ST = 128: 8 x 8 outputs per thread of 256; ST = 64: 8 x 4
-// of 128, for products whose 128-tiles would leave SMs without a block (256 x 128 x 5003: 35 us
-// for 80 blocks of 128 x 128).
+// ---- exact fp32 tiles of ST x ST outputs, K steps of 16, 256 threads with (ST / 16)^2 outputs
+// each. ST = 64 is for products whose 128-tiles would leave SMs without two blocks (256 x 128 x
+// 5003: 35 us for 80 blocks of 128 x 128). Rows go in pairs through fma.f32x2 (each half rounded
+// on its own, as fmaf): with one FMA per instruction and two warps per scheduler the tiles were
+// bound by issue (64 x 64 by 128 threads: 17 us).
 constexpr int SK = 16;
 
 struct SimtParams {
@@ -707,28 +709,29 @@ __device__ __forceinline__ float4 load_elem4(const void* p, int64_t at, int f32)
 enum { S_STATS = 0, S_DLOGITS = 1, S_STORE = 2 };
 
 template <int MODE, int ST>
-__global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
-  constexpr int TN = ST / 16, NT = ST * 2, LD = ST + 4;
+__global__ void __launch_bounds__(256) simt_kernel(const SimtParams p) {
+  constexpr int TM = ST / 16, TN = ST / 16, LD = ST + 4;
+  constexpr int kLoads = ST * SK / 4 / 256;  // of four elements per thread, operand and step
   let_next_begin();
   after_previous();
   __shared__ __align__(16) float sa[2][SK][LD], sb[2][SK][LD];
   const int m0 = blockIdx.x * ST, n0 = blockIdx.y * ST;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int k_lo = blockIdx.z * p.k_split, k_hi = min(p.K, k_lo + p.k_split);
-  float acc[8][TN];
+  float2 acc2[TM / 2][TN];  // rows 2 i and 2 i + 1
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < TM / 2; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = 0.0f;
-  // Four elements per thread and step, along the operand's contiguous direction: ST * SK / 4 / NT = 2 steps.
+    for (int j = 0; j < TN; ++j) acc2[i][j] = make_float2(0.0f, 0.0f);
+  // Four elements per thread and load, along the operand's contiguous direction.
   auto place = [&](int64_t kstep, int i, int* r, int* k) {
-    const int e = threadIdx.x + i * NT;
+    const int e = threadIdx.x + i * 256;
     if (kstep == 1) *r = e / (SK / 4), *k = e % (SK / 4) * 4;
     else *r = e % (ST / 4) * 4, *k = e / (ST / 4);
   };
-  auto fetch = [&](float4 (&v)[2], const void* src, int64_t rstep, int64_t kstep, int f32, int r0, int rows, int k0) {
+  auto fetch = [&](float4 (&v)[kLoads], const void* src, int64_t rstep, int64_t kstep, int f32, int r0, int rows, int k0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       int r, k;
       place(kstep, i, &r, &k);
       const int64_t at = (int64_t)(r0 + r) * rstep + (int64_t)(k0 + k) * kstep;
@@ -745,9 +748,9 @@ __global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
       }
     }
   };
-  auto keep = [&](float (*dst)[LD], const float4 (&v)[2], int64_t kstep) {
+  auto keep = [&](float (*dst)[LD], const float4 (&v)[kLoads], int64_t kstep) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       int r, k;
       place(kstep, i, &r, &k);
       if (kstep == 1) {
@@ -757,7 +760,7 @@ __global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
       }
     }
   };
-  float4 va[2], vb[2];
+  float4 va[kLoads], vb[kLoads];
   if (k_lo < k_hi) {
     fetch(va, p.A, p.a_row, p.a_k, p.a_f32, m0, p.M, k_lo);
     fetch(vb, p.B, p.b_row, p.b_k, p.b_f32, n0, p.N, k_lo);
@@ -774,16 +777,23 @@ __global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
     }
 #pragma unroll
     for (int k = 0; k < SK; ++k) {
-      float a[8], b[TN];
-      *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 8]);
-      *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 8 + 4]);
+      float2 a[TM / 2];
+      float b[TN];
+#pragma unroll
+      for (int i = 0; i < TM; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(&sa[buf][k][ty * TM + i]);
+        a[i / 2] = make_float2(v.x, v.y);
+        a[i / 2 + 1] = make_float2(v.z, v.w);
+      }
 #pragma unroll
       for (int j = 0; j < TN; j += 4)
         *reinterpret_cast<float4*>(b + j) = *reinterpret_cast<const float4*>(&sb[buf][k][j * 16 + tx * 4]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int j = 0; j < TN; ++j) {
+        const float2 bb = make_float2(b[j], b[j]);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        for (int i = 0; i < TM / 2; ++i) acc2[i][j] = __ffma2_rn(a[i], bb, acc2[i][j]);
+      }
     }
     if (more) {
       keep(sa[buf ^ 1], va, p.a_k);
@@ -792,10 +802,11 @@ __global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
     __syncthreads();
     buf ^= 1;
   }
-  // the thread's rows m0 + 8 ty + i, columns n0 + 64 (j / 4) + 4 tx + j % 4
+  auto acc = [&](int i, int j) { return i & 1 ? acc2[i / 2][j].y : acc2[i / 2][j].x; };
+  // the thread's rows m0 + TM ty + i, columns n0 + 64 (j / 4) + 4 tx + j % 4
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = m0 + ty * 8 + i;
+  for (int i = 0; i < TM; ++i) {
+    const int row = m0 + ty * TM + i;
     const bool live = row < p.M;
     auto col_of = [&](int j) { return n0 + j / 4 * 64 + tx * 4 + j % 4; };
     if constexpr (MODE == S_STATS) {
@@ -805,8 +816,8 @@ __global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         if (col_of(j) < p.N) {
-          if (col_of(j) == tgt) p.target_logit[row] = acc[i][j];
-          m = fmaxf(m, acc[i][j] * kLog2e);
+          if (col_of(j) == tgt) p.target_logit[row] = acc(i, j);
+          m = fmaxf(m, acc(i, j) * kLog2e);
         }
       }
 #pragma unroll
@@ -815,7 +826,7 @@ __global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
       float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        if (col_of(j) < p.N) s += exp2f(fmaf(acc[i][j], kLog2e, -base));
+        if (col_of(j) < p.N) s += exp2f(fmaf(acc(i, j), kLog2e, -base));
 #pragma unroll
       for (int off = 8; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       if (tx == 0 && live) p.part[(int64_t)blockIdx.y * p.M + row] = make_float2(m, s);
@@ -834,7 +845,7 @@ __global__ void __launch_bounds__(ST * 2) simt_kernel(const SimtParams p) {
         float v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v[j] = acc[i][j0 + j];
+          v[j] = acc(i, j0 + j);
           if constexpr (MODE == S_DLOGITS) {
             v[j] = expf(v[j] - lse);
             if (col_of(j0 + j) + p.v0 == tgt) v[j] -= 1.0f;
@@ -879,32 +890,28 @@ cudaError_t launch_simt(SimtParams p, cudaStream_t s) {
   const dim3 grid((unsigned)ceil_div(p.M, st), (unsigned)ceil_div(p.N, st), (unsigned)p.splits);
   // a call begins with a plain launch (the logits), the products after it follow closely
   if (MODE == S_STORE)
-    return st == 128 ? launch_after(simt_kernel<MODE, 128>, grid, 256, s, p) : launch_after(simt_kernel<MODE, 64>, grid, 128, s, p);
+    return st == 128 ? launch_after(simt_kernel<MODE, 128>, grid, 256, s, p) : launch_after(simt_kernel<MODE, 64>, grid, 256, s, p);
   if (st == 128) simt_kernel<MODE, 128><<<grid, 256, 0, s>>>(p);
-  else simt_kernel<MODE, 64><<<grid, 128, 0, s>>>(p);
+  else simt_kernel<MODE, 64><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 // TOK tokens per block of 1024 threads, the other lanes over the halves: lse = max + log(sum),
 // the loss, and in the block that finishes last their mean over the tokens that count and its
 // reciprocal count. Few tokens take TOK = 4 (a token's 2000 halves of a large vocabulary in 8
-// steps), many TOK = 32 (256 bytes of a row of halves per step).
+// steps), many TOK = 32 (256 bytes of a row of halves per step). Every lane's running (max, sum)
+// goes to shared memory, and one warp per token takes the maximum, then the sum.
 template <int TOK>
 __global__ void __launch_bounds__(1024)
     join_kernel(const float2* part, int parts, int T, int V, const int32_t* target, const float* target_logit,
                 float* loss, float* lse, float* mean, uint32_t* ticket, DeviceStatus* st) {
   constexpr int kLanes = 1024 / TOK, kAhead = 4;
-  __shared__ float sm[32][TOK], ss[32][TOK];
+  __shared__ float2 lanes[TOK][kLanes + 1];
   __shared__ bool finish;
   after_previous();
-  const int tok = threadIdx.x % TOK, lane = threadIdx.x / TOK, warp = threadIdx.x >> 5;
+  const int tok = threadIdx.x % TOK, lane = threadIdx.x / TOK, warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * TOK + tok;
   float m = -INFINITY, s = 0.0f;
-  auto merge = [&](float m2, float s2) {
-    const float n = fmaxf(m, m2), base = n == -INFINITY ? 0.0f : n;
-    s = fmaf(s, exp2f(m - base), s2 * exp2f(m2 - base));
-    m = n;
-  };
   if (t < T) {
     for (int i0 = lane; i0 < parts; i0 += kLanes * kAhead) {
       float2 v[kAhead];
@@ -923,23 +930,30 @@ __global__ void __launch_bounds__(1024)
       m = m2;
     }
   }
-#pragma unroll
-  for (int off = TOK; off < 32; off <<= 1)
-    merge(__shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, s, off));
-  if ((threadIdx.x & 31) < TOK) sm[warp][tok] = m, ss[warp][tok] = s;
+  lanes[tok][lane] = make_float2(m, s);
   __syncthreads();
-  if (warp == 0) {
+  const int64_t tw = (int64_t)blockIdx.x * TOK + warp;  // the warp's token
+  if (warp < TOK && tw < T) {
+    float2 v[kLanes / 32];
     m = -INFINITY, s = 0.0f;
-    for (int i = lane; i < 32; i += 32 / TOK) merge(sm[i][tok], ss[i][tok]);
 #pragma unroll
-    for (int off = TOK; off < 32; off <<= 1)
-      merge(__shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, s, off));
-    if (threadIdx.x < TOK && t < T) {
+    for (int u = 0; u < kLanes / 32; ++u) {
+      v[u] = lanes[warp][wl + 32 * u];
+      m = fmaxf(m, v[u].x);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int u = 0; u < kLanes / 32; ++u) s = fmaf(v[u].y, exp2f(v[u].x - base), s);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (wl == 0) {
       const float l = (m + log2f(s)) * 0.6931471805599453f;
-      const int32_t tgt = target[t];
-      if (tgt >= V) set_status(st, MOE_ERR_DEVICE_BAD_INPUT, (int32_t)t);
-      lse[t] = l;
-      loss[t] = tgt >= 0 && tgt < V ? l - target_logit[t] : 0.0f;
+      const int32_t tgt = target[tw];
+      if (tgt >= V) set_status(st, MOE_ERR_DEVICE_BAD_INPUT, (int32_t)tw);
+      lse[tw] = l;
+      loss[tw] = tgt >= 0 && tgt < V ? l - target_logit[tw] : 0.0f;
       __threadfence();
     }
   }
@@ -949,6 +963,8 @@ __global__ void __launch_bounds__(1024)
   __syncthreads();
   if (!finish) return;
   __threadfence();
+  __shared__ float sums[32];
+  __shared__ int counts[32];
   float sum = 0.0f;
   int count = 0;
   for (int i = threadIdx.x; i < T; i += 1024) {
@@ -963,15 +979,20 @@ __global__ void __launch_bounds__(1024)
     sum += __shfl_xor_sync(0xffffffffu, sum, off);
     count += __shfl_xor_sync(0xffffffffu, count, off);
   }
-  __shared__ int counts[32];
-  if ((threadIdx.x & 31) == 0) sm[warp][0] = sum, counts[warp] = count;
+  if (wl == 0) sums[warp] = sum, counts[warp] = count;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double total = 0.0;
-    int n = 0;
-    for (int i = 0; i < 32; ++i) total += (double)sm[i][0], n += counts[i];
-    mean[0] = n ? (float)(total / n) : 0.0f;
-    mean[1] = n ? 1.0f / (float)n : 0.0f;
+  if (warp == 0) {
+    double total = (double)sums[wl];
+    int n = counts[wl];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, off);
+      n += __shfl_xor_sync(0xffffffffu, n, off);
+    }
+    if (wl == 0) {
+      mean[0] = n ? (float)total / (float)n : 0.0f;
+      mean[1] = n ? 1.0f / (float)n : 0.0f;
+    }
   }
 }
 
@@ -982,7 +1003,7 @@ __global__ void __launch_bounds__(256) join_dx_kernel(const float* slices, int s
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float v = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
   for (int k = 0; k < splits; ++k) v += __ldg(slices + k * n + i);
   if constexpr (sizeof(T) == 4) dx[i] = v;
   else dx[i] = __float2bfloat16_rn(v);
