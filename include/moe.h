@@ -530,8 +530,8 @@ typedef struct {
   int32_t T, H, V;
   int32_t act_dtype;  /* MOE_DTYPE_F32 or MOE_DTYPE_BF16: x, w and dx */
   int32_t grad_dtype; /* the same choice for dw */
-  int32_t piece;      /* vocabulary rows per piece of the backward; 0: as many as 256 MB of
-                         logit gradients hold, at least 4096 */
+  int32_t piece;      /* vocabulary rows per piece; 0: as many as 256 MB of logit gradients
+                         (and laid-out rows of w, below) hold, at least 4096 */
 } moe_head_config_t;
 
 /* Softmax cross entropy of x [T, H] against the vocabulary rows w [V, H], without keeping the
@@ -540,9 +540,12 @@ typedef struct {
  * A negative target is left out: its loss is 0 and it has no gradient (its lse is still
  * given). A target >= V sets MOE_ERR_DEVICE_BAD_INPUT and is left out too. mean (NULL to skip):
  * two floats, the mean loss of the tokens that count and 1 / their number (0, 0 if none).
- * target [T] int32; loss, lse [T] fp32. bf16 with H % 8 == 0 runs on the tensor cores, all
- * else on exact fp32 products. ws: moe_head_workspace_size bytes, used by both calls (they
- * need not share it). Deterministic. */
+ * target [T] int32; loss, lse [T] fp32. The products run on the tensor cores: bf16 as it is,
+ * fp32 as three bf16 planes per operand and the six products of planes above 2^-24 of the
+ * whole (fp32 accuracy for finite operands; planes of a value beyond bf16's largest finite one,
+ * 3.39e38, are not finite). fp32 operands, and bf16 ones with H % 8 != 0, are laid out in the
+ * workspace first, w piece by piece. ws: moe_head_workspace_size bytes, used by both calls
+ * (they need not share it). Deterministic. */
 moe_status_t moe_head_workspace_size(const moe_head_config_t* cfg, size_t* bytes);
 moe_status_t moe_head_loss(const moe_head_config_t* cfg, const void* x, const void* w, const int32_t* target,
                            float* loss, float* lse, float* mean, void* ws, moe_stream_t stream);
@@ -551,8 +554,9 @@ moe_status_t moe_head_loss(const moe_head_config_t* cfg, const void* x, const vo
  *     dz[t,v] = (exp(z[t,v] - lse[t]) - [v = target[t]]) dloss[t];  dx = dz w;  dw = dz^T x
  * dloss [T] fp32: the gradient of every token's loss; or NULL, and mean (from moe_head_loss)
  * makes it the gradient of the mean loss. Exactly one of the two is given. dx [T, H] act and
- * dw [V, H] grad_dtype are overwritten (either may be NULL). On the tensor cores dz is rounded
- * to bf16, the operand type of its two products, which accumulate in fp32. */
+ * dw [V, H] grad_dtype are overwritten (either may be NULL). For bf16 operands in place
+ * dz is rounded to bf16, the operand type of its two products, which accumulate in fp32; with
+ * laid-out operands it has three planes as well. */
 moe_status_t moe_head_loss_backward(const moe_head_config_t* cfg, const void* x, const void* w, const int32_t* target,
                                     const float* lse, const float* dloss, const float* mean, void* dx, void* dw,
                                     void* ws, moe_stream_t stream);

@@ -9,13 +9,20 @@
 // dx += dz w_piece and dw_piece = dz^T x. Memory beside the inputs and outputs: one piece of dz
 // and 16 bytes per token and tile.
 //
-// bf16 with H a multiple of 8 runs on the tensor cores (tcgen05): warp 0 feeds a ring of
-// shared-memory stages by TMA, warp 1 issues the MMAs into two TMEM accumulators, warps 2-9
-// are the epilogue of one accumulator while the other fills. Tiles are 256 x 256 on a CTA pair,
-// or 128 x 128 on one CTA for up to 128 tokens, where reading w is all the time there is and
-// smaller tiles spread it more evenly over the SMs. Edges need no special case in the operands:
-// the TMA fills zeros past the last row and column. fp32, and widths of other multiples, take
-// exact fp32 FMA tiles (simt_kernel), with dz kept in fp32.
+// All products run on the tensor cores (tcgen05): warp 0 feeds a ring of shared-memory stages
+// by TMA, warp 1 issues the MMAs into two TMEM accumulators, warps 2-9 are the epilogue of one
+// accumulator while the other fills. Tiles are 256 x 256 on a CTA pair, or 128 x 128 on one CTA
+// for up to 128 tokens, where reading w is all the time there is and smaller tiles spread it
+// more evenly over the SMs. Edges need no special case in the operands: the TMA fills zeros
+// past the last row and column.
+//
+// fp32 operands are split into three bf16 planes, v = v0 + v1 + v2 with 8 bits of the mantissa
+// each, and a product takes the six plane products above 2^-24 of it: x0 w0, x0 w1, x1 w0,
+// x0 w2, x1 w1, x2 w0, added in fp32 runs of 1024 elements. That is fp32 accuracy at a sixth of
+// the bf16 rate; exact fp32 FMA tiles reached 23 to 36 TFLOP/s (1024 x 1024 x 8192, forward and
+// backward: 2401 us). The planes of x and of one piece of w are laid out in the workspace, rows
+// padded to a multiple of 16 bytes; bf16 operands of a width that is not a multiple of 8 are
+// copied there too, as one plane (their dz has three).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -37,7 +44,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kABytes = BM * BK * 2;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kRun = 16;  // K stages (1024 elements) added by the tensor core in one go
+constexpr int kRun = 16;  // K stages (of 64 elements) added by the tensor core in one go
+
+constexpr int kNowhere = -(1 << 30);  // no column: far below the first of any tile
 
 enum Mode { STATS = 0, DLOGITS = 1, DX = 2, DW = 3 };
 
@@ -47,8 +56,12 @@ struct HeadParams {
   int direct;          // DX: the first `direct` tiles are whole; the K of each further one is
   int splits;          //   split over `splits` units, which write fp32 tiles to `slices`
   float* slices;       //   [tile - direct][split][TM][BN]
-  int b_row0;          // first vocabulary row of the piece (STATS: 0)
+  int v0;              // first vocabulary row of the piece
+  int w_row0;          // its row in the map of w (0 where the piece was laid out by itself)
   int V;
+  int terms;           // plane products per K stage of 64 elements, and the planes of A and B in
+  uint32_t a_code, b_code;  //   each of them, four bits a term from the first on
+  int a_plane, b_plane;  // rows from one plane of A and B to the next
   const int32_t* target;
   // STATS: (max, sum) per token and half tile [2 n_tiles][T], and the target's logit [T]
   float2* part;
@@ -58,7 +71,10 @@ struct HeadParams {
   // outputs of the other modes, and their row length in elements
   void* out;
   int64_t ldo;
+  int m_out;           // DLOGITS: rows that are stored (those past M as zeros)
+  int64_t out_plane;   // DLOGITS: elements from one plane of dz to the next
   int out_f32;         // DX, DW: fp32 output (else bf16)
+  int scalar;          // DX, DW: the output's rows do not begin on 16-byte boundaries
   int add;             // DX: added to what out holds (a later piece of the vocabulary)
   const float* factor; // DX, DW: every value is multiplied by it (the mean's 1 / count), or NULL
   DeviceStatus* status;
@@ -133,6 +149,25 @@ __device__ __forceinline__ void flush_edge(uint8_t* stage, int lane, uint8_t* ba
   __syncwarp();
 }
 
+// The same for rows that do not begin on 16-byte boundaries: element by element, cols of them.
+template <typename T>
+__device__ __forceinline__ void flush_scalar(const uint8_t* stage, int lane, T* base, int64_t ldo, int live, int cols,
+                                             bool add) {
+  __syncwarp();
+  constexpr int kPer = 64 / sizeof(T);
+#pragma unroll 4
+  for (int j = 0; j < kPer; ++j) {
+    const int e = lane + 32 * j, row = e / kPer, col = e % kPer, c = col * (int)sizeof(T) / 16;
+    const T v = *reinterpret_cast<const T*>(stage + row * 64 + 16 * (c ^ ((row >> 1) & 3)) + col * sizeof(T) % 16);
+    if (row < live && col < cols) {
+      T* dst = base + row * ldo + col;
+      if constexpr (sizeof(T) == 4) *dst = add ? *dst + v : v;
+      else *dst = v;
+    }
+  }
+  __syncwarp();
+}
+
 struct HeadTile {
   int mb, nb, slice, kb0, kb1;  // slice: -1, or the tile's place in `slices`
 };
@@ -170,7 +205,8 @@ __host__ __device__ __forceinline__ int head_units(const HeadParams& p) {
   return p.direct + (p.m_tiles * p.n_tiles - p.direct) * p.splits;
 }
 
-template <int MODE, int CG, int BN>
+// NP planes: 1, or up to 3 per operand with p.terms products per K stage (the smallest first).
+template <int MODE, int CG, int BN, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const HeadParams p) {
   using S = HeadSmem<CG, BN>;
@@ -224,13 +260,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total_tiles = head_units(p);
-  // The loss's logits are added up in runs of kRun K stages: each run has its own accumulator,
-  // and the epilogue adds the runs in fp32. The tensor core's own additions truncate: over 4096
-  // elements in one go the loss was off by 3.4e-6 of its size, in runs of 1024 by 6e-7. dz is
-  // rounded to bf16, where one go is good enough.
-  constexpr bool kRuns = MODE == STATS;
-  auto runs_of = [&](const HeadTile& t) { return kRuns ? (t.kb1 - t.kb0 + kRun - 1) / kRun : 1; };
-  auto run_end = [&](const HeadTile& t, int run) { return kRuns ? min(t.kb1, (run + 1) * kRun) : t.kb1; };
+  // The loss's logits and all sums of planes are added up in runs of kRun K stages: each run has
+  // its own accumulator, and the epilogue adds the runs in fp32. The tensor core's own additions
+  // truncate: over 4096 elements in one go the loss was off by 3.4e-6 of its size, in runs of
+  // 1024 by 6e-7. Where dz or the output is rounded to bf16, one go is good enough.
+  constexpr bool kRuns = MODE == STATS || NP == 3;
+  const int terms = NP == 3 ? p.terms : 1;  // K stages per 64 elements
+  auto runs_of = [&](const HeadTile& t) { return kRuns ? ((t.kb1 - t.kb0) * terms + kRun - 1) / kRun : 1; };
+  auto run_end = [&](const HeadTile& t, int run) {
+    return kRuns ? min(t.kb1 * terms, t.kb0 * terms + (run + 1) * kRun) : t.kb1;
+  };
 
   if (warp == 0) {
     // ======================= TMA producer (each CTA loads its own rows of A and its part of B)
@@ -242,7 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
         const HeadTile t = head_tile<MODE>(tile, p);
         const int am = t.mb * TM + (int)rank * BM, bn = t.nb * BN + (int)rank * (BN / CG);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        int kb = t.kb0, term = 0;
+        for (int ks = t.kb0 * terms; ks < t.kb1 * terms; ++ks) {
+          const int pa = NP == 3 ? (int)(p.a_code >> (4 * term) & 3) * p.a_plane : 0;
+          const int pb = NP == 3 ? (int)(p.b_code >> (4 * term) & 3) * p.b_plane : 0;
           if (!mbar_wait(&empty[stage], phase ^ 1, abort, p.timeout_ns, p.status)) { ok = false; break; }
           uint8_t* a_dst = sA + stage * kABytes;
           uint8_t* b_dst = sB + stage * kBBytes;
@@ -258,18 +300,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tma_load_2d_pair(m, dst, bar, x, y);
           };
           if constexpr (kAmn) {
-            load(&tmA, a_dst, am, kb * BK);
-            load(&tmA, a_dst + 8192, am + 64, kb * BK);
+            load(&tmA, a_dst, am, pa + kb * BK);
+            load(&tmA, a_dst + 8192, am + 64, pa + kb * BK);
           } else {
-            load(&tmA, a_dst, kb * BK, am);
+            load(&tmA, a_dst, kb * BK, pa + am);
           }
           if constexpr (kBmn) {
-            const int y = (MODE == DX ? p.b_row0 : 0) + kb * BK;
+            const int y = pb + (MODE == DX ? p.w_row0 : 0) + kb * BK;
 #pragma unroll
             for (int j = 0; j < kBoxes; ++j) load(&tmB, b_dst + 8192 * j, bn + 64 * j, y);
           } else {
-            load(&tmB, b_dst, kb * BK, p.b_row0 + bn);
+            load(&tmB, b_dst, kb * BK, pb + p.w_row0 + bn);
           }
+          if (++term == terms) { term = 0; ++kb; }
           ++issued;
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
@@ -293,13 +336,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
         const HeadTile t = head_tile<MODE>(tile, p);
-        int kb = t.kb0;
+        int ks = t.kb0 * terms;
         for (int run = 0; run < runs_of(t) && ok; ++run) {
           if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort, p.timeout_ns, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * BN;
-          const int first = kb, end = run_end(t, run);
-          for (; kb < end; ++kb) {
+          const int first = ks, end = run_end(t, run);
+          for (; ks < end; ++ks) {
             if (!mbar_wait(&full[stage], phase, abort, p.timeout_ns, p.status)) { ok = false; break; }
             tc_fence_after();
             const uint32_t a_addr = smem_addr(sA + stage * kABytes);
@@ -308,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < BK / 16; ++k) {
               const uint64_t ad = kAmn ? desc_mn(a_addr + k * 2048) : desc_k_sw128(a_addr + k * 32);
               const uint64_t bd = kBmn ? desc_mn(b_addr + k * 2048) : desc_k_sw128(b_addr + k * 32);
-              const uint32_t accumulate = kb > first || k > 0;
+              const uint32_t accumulate = ks > first || k > 0;
               if constexpr (CG == 1) mma_bf16(d_tmem, ad, bd, idesc, accumulate);
               else mma_bf16_pair(d_tmem, ad, bd, idesc, accumulate);
             }
@@ -360,11 +403,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16) + cbase;
 
-      if constexpr (MODE == STATS) {
+      // dz or output values of the 32 columns from c0 of this warp's share on
+      int tgt = -1;
+      bool counts = false;
+      float lse2 = 0.0f, g = 0.0f;
+      if constexpr (MODE == STATS || MODE == DLOGITS) {
+        if (live) tgt = __ldg(p.target + row);
+        counts = tgt >= 0 && tgt < p.V;
+        tgt = counts ? tgt - p.v0 : kNowhere;  // the target's column of this piece, or outside it
+        if (MODE == DLOGITS && counts) {
+          lse2 = __ldg(p.lse + row) * kLog2e;
+          // the gradient of the mean: its factor 1 / count is left to the two products
+          g = p.dloss ? __ldg(p.dloss + row) : 1.0f;
+        }
+      } else {
+        g = p.factor ? __ldg(p.factor) : 1.0f;
+      }
+      auto finish = [&](float (&v)[32], int c0) {
+        const int cc = col0 + c0;   // first column of the chunk
+        const int cols = p.N - cc;  // columns from there on that exist
+        if constexpr (MODE == DLOGITS) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = ex2(fmaf(v[i], kLog2e, -lse2));
+            if (i == tgt - cc) v[i] -= 1.0f;
+            v[i] = counts && i < cols ? v[i] * g : 0.0f;
+          }
+          // columns past the vocabulary are written too, as zeros: they are K rows of the next products
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)row0 * p.ldo + cc;
+#pragma unroll
+          for (int pl = 0; pl < NP; ++pl) {
+            stage_bf16(stage, lane, v);
+            flush_rows_64B(stage, lane, reinterpret_cast<uint8_t*>(out + pl * p.out_plane), p.ldo * 2, p.m_out - row0);
+            if (pl + 1 < NP)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= g;
+          if (MODE == DX && t.slice >= 0) {
+            uint8_t* out = reinterpret_cast<uint8_t*>(p.slices + ((int64_t)t.slice * TM + wrow) * BN + cbase + c0);
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              stage_f32(stage, lane, v + h);
+              flush_rows_64B(stage, lane, out + 4 * h, BN * 4, 32);
+            }
+          } else if (p.out_f32) {
+            float* out = static_cast<float*>(p.out) + (int64_t)row0 * p.ldo + cc;
+            const bool add = MODE == DX && p.add;
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              stage_f32(stage, lane, v + h);
+              if (p.scalar) flush_scalar(stage, lane, out + h, p.ldo, p.M - row0, cols - h, add);
+              else flush_edge(stage, lane, reinterpret_cast<uint8_t*>(out + h), p.ldo * 4, p.M - row0, (cols - h) / 4, add);
+            }
+          } else {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)row0 * p.ldo + cc;
+            stage_bf16(stage, lane, v);
+            if (p.scalar) flush_scalar(stage, lane, out, p.ldo, p.M - row0, cols, false);
+            else flush_edge(stage, lane, reinterpret_cast<uint8_t*>(out), p.ldo * 2, p.M - row0, cols / 8, false);
+          }
+        }
+      };
+
+      if constexpr (kRuns) {
         // this row's half of the tile's columns, out of TMEM before anything is made of it
         uint32_t zr[kCols / 32][32];
         const int runs = runs_of(t);
         bool ok = true;
+        if (runs == 0) {  // a split without K stages
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) zr[i / 32][i % 32] = 0u;
+        }
         for (int run = 0; run < runs; ++run) {
           if (!(ok = wait_full())) break;
           const uint32_t t_row = t_lane + acc * BN;
@@ -387,47 +498,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         auto z = [&](int i) { return __uint_as_float(zr[i / 32][i % 32]); };
-        const int cols = p.N - col0;  // columns from here on that exist
-        const int tgt = live ? __ldg(p.target + row) : -1;
-        if (tgt >= col0 && tgt < min(col0 + kCols, p.N)) {
+        if constexpr (MODE == STATS) {
+          const int cols = p.N - col0;  // columns from here on that exist
+          if (tgt >= col0 && tgt < min(col0 + kCols, p.N)) {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i)
-            if (col0 + i == tgt) p.target_logit[row] = z(i);
-        }
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kCols; i += 2) {
-          if (cols < kCols) {
-            if (i >= cols) zr[i / 32][i % 32] = __float_as_uint(-INFINITY);
-            if (i + 1 >= cols) zr[i / 32][i % 32 + 1] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < kCols; ++i)
+              if (col0 + i == tgt) p.target_logit[row] = z(i);
           }
-          m0 = fmaxf(m0, z(i));
-          m1 = fmaxf(m1, z(i + 1));
-        }
-        const float mx = fmaxf(m0, m1) * kLog2e;
-        const float base = mx == -INFINITY ? 0.0f : mx;
-        float s0 = 0.0f, s1 = 0.0f;
+          float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kCols; i += 2) {
-          s0 += ex2(fmaf(z(i), kLog2e, -base));
-          s1 += ex2(fmaf(z(i + 1), kLog2e, -base));
-        }
-        if (live) p.part[(int64_t)(2 * t.nb + half) * p.M + row] = make_float2(mx, s0 + s1);
-      } else {
-        int tgt = -1;
-        bool counts = false;
-        float lse2 = 0.0f, g = 0.0f;
-        if constexpr (MODE == DLOGITS) {
-          if (live) tgt = __ldg(p.target + row);
-          counts = tgt >= 0 && tgt < p.V;
-          if (counts) {
-            lse2 = __ldg(p.lse + row) * kLog2e;
-            // the gradient of the mean: its factor 1 / count is left to the two products
-            g = p.dloss ? __ldg(p.dloss + row) : 1.0f;
+          for (int i = 0; i < kCols; i += 2) {
+            if (cols < kCols) {
+              if (i >= cols) zr[i / 32][i % 32] = __float_as_uint(-INFINITY);
+              if (i + 1 >= cols) zr[i / 32][i % 32 + 1] = __float_as_uint(-INFINITY);
+            }
+            m0 = fmaxf(m0, z(i));
+            m1 = fmaxf(m1, z(i + 1));
           }
+          const float mx = fmaxf(m0, m1) * kLog2e;
+          const float base = mx == -INFINITY ? 0.0f : mx;
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kCols; i += 2) {
+            s0 += ex2(fmaf(z(i), kLog2e, -base));
+            s1 += ex2(fmaf(z(i + 1), kLog2e, -base));
+          }
+          if (live) p.part[(int64_t)(2 * t.nb + half) * p.M + row] = make_float2(mx, s0 + s1);
         } else {
-          g = p.factor ? __ldg(p.factor) : 1.0f;
+#pragma unroll
+          for (int c0 = 0; c0 < kCols; c0 += 32) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = z(c0 + i);
+            finish(v, c0);
+          }
         }
+      } else {
         if (!wait_full()) break;
         const bool none = MODE == DX && t.kb0 == t.kb1;  // a split without K stages: nothing in the accumulator
         const uint32_t t_row = t_lane + acc * BN;
@@ -438,45 +544,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[32];
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(nxt[i]);
+          for (int i = 0; i < 32; ++i) v[i] = none ? 0.0f : __uint_as_float(nxt[i]);
           if (c0 + 32 < kCols) tmem_ld32(t_row + c0 + 32, nxt);  // next chunk in flight
-          const int cc = col0 + c0;   // first column of the chunk
-          const int cols = p.N - cc;  // columns from there on that exist
-          if constexpr (MODE == DLOGITS) {
-            const int at = tgt - p.b_row0 - cc;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] = ex2(fmaf(v[i], kLog2e, -lse2));
-              if (i == at) v[i] -= 1.0f;
-              v[i] = counts && i < cols ? v[i] * g : 0.0f;
-            }
-            stage_bf16(stage, lane, v);
-            // columns past the vocabulary are written too, as zeros: they are K rows of the next products
-            flush_rows_64B(stage, lane, static_cast<uint8_t*>(p.out) + ((int64_t)row0 * p.ldo + cc) * 2, p.ldo * 2,
-                           p.M - row0);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = none ? 0.0f : v[i] * g;
-            if (MODE == DX && t.slice >= 0) {
-              uint8_t* out = reinterpret_cast<uint8_t*>(p.slices + ((int64_t)t.slice * TM + wrow) * BN + cbase + c0);
-#pragma unroll
-              for (int h = 0; h < 32; h += 16) {
-                stage_f32(stage, lane, v + h);
-                flush_rows_64B(stage, lane, out + 4 * h, BN * 4, 32);
-              }
-            } else if (p.out_f32) {
-              uint8_t* out = static_cast<uint8_t*>(p.out) + ((int64_t)row0 * p.ldo + cc) * 4;
-#pragma unroll
-              for (int h = 0; h < 32; h += 16) {
-                stage_f32(stage, lane, v + h);
-                flush_edge(stage, lane, out + 4 * h, p.ldo * 4, p.M - row0, (cols - h) / 4, MODE == DX && p.add);
-              }
-            } else {
-              stage_bf16(stage, lane, v);
-              flush_edge(stage, lane, static_cast<uint8_t*>(p.out) + ((int64_t)row0 * p.ldo + cc) * 2, p.ldo * 2,
-                         p.M - row0, cols / 8, false);
-            }
-          }
+          finish(v, c0);
         }
         release();
       }
@@ -497,9 +567,9 @@ bool bf16_box(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
   return make_tmap(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, cols, box_rows, 64);
 }
 
-template <int MODE, int CG, int BN>
+template <int MODE, int CG, int BN, int NP>
 cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadParams& p, cudaStream_t s) {
-  auto kern = head_gemm_kernel<MODE, CG, BN>;
+  auto kern = head_gemm_kernel<MODE, CG, BN, NP>;
   const size_t smem = HeadSmem<CG, BN>::kBytes;
   static bool attr_set = false;  // per instantiation
   if (!attr_set) {
@@ -534,12 +604,23 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Up to 128 tokens: one 128-row tile, single CTAs. Else 256-row tiles on CTA pairs.
-bool small_tokens(int T) { return T <= BM; }
+// Up to 128 tokens: one 128-row tile, single CTAs. Else 256-row tiles on CTA pairs. Planes take
+// 128 columns a tile: the runs' sums of 64 columns per warp stay in registers.
+bool small_tokens(int64_t T) { return T <= BM; }
+int tile_rows(int64_t T) { return small_tokens(T) ? BM : 2 * BM; }
+int tile_cols(int64_t T, int planes) { return small_tokens(T) || planes == 3 ? 128 : 256; }
+
+template <int MODE>
+cudaError_t launch_mode(int T, int planes, const CUtensorMap& a, const CUtensorMap& b, const HeadParams& p, cudaStream_t s) {
+  if constexpr (MODE != DW) {
+    if (small_tokens(T)) return planes == 3 ? launch_gemm<MODE, 1, 128, 3>(a, b, p, s) : launch_gemm<MODE, 1, 128, 1>(a, b, p, s);
+  }
+  return planes == 3 ? launch_gemm<MODE, 2, 128, 3>(a, b, p, s) : launch_gemm<MODE, 2, 256, 1>(a, b, p, s);
+}
 
 HeadParams base_params(int64_t M, int64_t N, int64_t K, int tm, int tn, DeviceStatus* st) {
   HeadParams p{};
-  p.M = (int)M;
+  p.M = p.m_out = (int)M;
   p.N = (int)N;
   p.m_tiles = (int)ceil_div(M, tm);
   p.n_tiles = (int)ceil_div(N, tn);
@@ -567,7 +648,13 @@ __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, in
     v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
   }
   T* o = out + (int64_t)row * p.ldo + col;
-  if constexpr (sizeof(T) == 4) {
+  if (p.scalar) {
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < 4 && col + i < p.N; ++i) {
+      if constexpr (sizeof(T) == 4) o[i] = p.add ? o[i] + f[i] : f[i];
+      else o[i] = __float2bfloat16_rn(f[i]);
+    }
+  } else if constexpr (sizeof(T) == 4) {
     float4* d = reinterpret_cast<float4*>(o);
     if (p.add) {
       const float4 a = *d;
@@ -579,320 +666,43 @@ __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, in
   }
 }
 
-}  // namespace
-
-// Columns of a tile of the logits, for the number of (max, sum) halves.
-int head_tile_cols(int T) { return small_tokens(T) ? 128 : 256; }
-
-// The input gradient's tiles rarely fill whole rounds of the SMs (4096 x 4096 is 256 tiles of
-// 256 x 256 on 76 CTA pairs: 3.37 rounds, so 4). The tiles of the last round are therefore
-// split along K, by the number of ways that takes least time: rounds of stages of 64 at 0.14 us
-// each against the slices' traffic at 0.08 us a tile, and the launch that adds them.
-HeadSplit head_split(int64_t T, int64_t H, int64_t rows) {
-  const bool small = small_tokens((int)std::min<int64_t>(T, INT32_MAX));
-  const int tm = small ? BM : 2 * BM, tn = small ? 128 : 256, units = small ? 152 : 76;
-  const int64_t tiles = ceil_div(T, tm) * ceil_div(H, tn), kblocks = ceil_div(rows, BK);
-  HeadSplit best{tiles, 1, 0};
-  const int64_t tail = tiles % units;
-  double least = (tail ? 1.0 : 0.0) * kblocks * 0.14;
-  for (int s = 2; s <= 32 && tail && s * 4 <= kblocks; ++s) {
-    const double t = (double)ceil_div(tail * s, units) * ceil_div(kblocks, s) * 0.14 +
-                     tail * s * 0.08 * (small ? 0.25 : 1.0) + 4.0;
-    if (t < least) least = t, best = {tiles - tail, s, (size_t)(tail * s) * tm * tn * 4};
+// The planes of rows [0, rows) of src [., H] in dst [planes][rows_pad][Hp] bf16: zeros past H and
+// from `rows` to `zero_to` (the K stages of the products read that far). Eight columns a thread.
+template <typename T, int NP>
+__global__ void __launch_bounds__(256)
+    planes_kernel(const T* src, int rows, int H, __nv_bfloat16* dst, int64_t plane, int Hp, int zero_to) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = Hp / 8, row = (int)(e / per), c = (int)(e % per) * 8;
+  if (row >= zero_to) return;
+  float v[8];
+  const bool whole = H % 8 == 0;  // a thread's columns are all there, and aligned
+  if (row >= rows) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  } else if (whole && sizeof(T) == 4) {
+    const float4* q = reinterpret_cast<const float4*>(src + (int64_t)row * H + c);
+    const float4 a = __ldg(q), b = __ldg(q + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < H ? static_cast<float>(src[(int64_t)row * H + c + i]) : 0.0f;
   }
-  return best;
-}
-
-cudaError_t launch_head_stats(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
-                              float2* part, float* target_logit, DeviceStatus* st, cudaStream_t s) {
-  const bool small = small_tokens(c.T);
-  HeadParams p = base_params(c.T, c.V, c.H, small ? BM : 2 * BM, head_tile_cols(c.T), st);
-  p.V = c.V;
-  p.target = target;
-  p.part = part;
-  p.target_logit = target_logit;
-  CUtensorMap a, b;
-  if (!bf16_box(&a, x, c.T, c.H, BM) || !bf16_box(&b, w, c.V, c.H, 128)) return cudaErrorInvalidValue;
-  return small ? launch_gemm<STATS, 1, 128>(a, b, p, s) : launch_gemm<STATS, 2, 256>(a, b, p, s);
-}
-
-// dz of the vocabulary rows [v0, v0 + rows) -> dl [T, ld] bf16; then dx and dw of the piece.
-cudaError_t launch_head_piece(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
-                              const float* lse, const float* dloss, const float* mean, int64_t v0, int rows, void* dl,
-                              int ld, void* dx, const HeadSplit& split, float* slices, bool dx_f32, bool add, void* dw,
-                              DeviceStatus* st, cudaStream_t s) {
-  const bool small = small_tokens(c.T);
-  const int tm = small ? BM : 2 * BM, tn = head_tile_cols(c.T);
-  CUtensorMap a, b;
-  HeadParams p = base_params(c.T, rows, c.H, tm, tn, st);
-  p.V = c.V;
-  p.b_row0 = (int)v0;
-  p.target = target;
-  p.lse = lse;
-  p.dloss = dloss;
-  p.out = dl;
-  p.ldo = ld;
-  if (!bf16_box(&a, x, c.T, c.H, BM) || !bf16_box(&b, w, c.V, c.H, 128)) return cudaErrorInvalidValue;
-  cudaError_t e = small ? launch_gemm<DLOGITS, 1, 128>(a, b, p, s) : launch_gemm<DLOGITS, 2, 256>(a, b, p, s);
-  if (e != cudaSuccess) return e;
-  if (dx) {  // M = T, N = H, K = the piece's vocabulary rows
-    p = base_params(c.T, c.H, rows, tm, tn, st);
-    p.b_row0 = (int)v0;
-    p.direct = (int)split.direct;
-    p.splits = split.splits;
-    p.slices = slices;
-    p.out = dx;
-    p.ldo = c.H;
-    p.out_f32 = dx_f32;
-    p.add = add;
-    p.factor = mean ? mean + 1 : nullptr;
-    if (!bf16_box(&a, dl, c.T, ld, BM) || !bf16_box(&b, w, c.V, c.H, 64)) return cudaErrorInvalidValue;
-    e = small ? launch_gemm<DX, 1, 128>(a, b, p, s) : launch_gemm<DX, 2, 256>(a, b, p, s);
-    if (e != cudaSuccess) return e;
-    if (split.splits > 1) {
-      const dim3 grid((unsigned)(tm * tn / 1024), (unsigned)(p.m_tiles * p.n_tiles - p.direct));
-      e = dx_f32 ? launch_after(join_slices_kernel<float>, grid, 256, s, p, tm, tn, static_cast<float*>(dx))
-                 : launch_after(join_slices_kernel<__nv_bfloat16>, grid, 256, s, p, tm, tn, static_cast<__nv_bfloat16*>(dx));
-      if (e != cudaSuccess) return e;
-    }
-  }
-  if (dw) {  // M = the piece's vocabulary rows, N = H, K = T
-    p = base_params(rows, c.H, c.T, 2 * BM, 256, st);
-    p.out_f32 = c.grad_dtype == MOE_DTYPE_F32;
-    p.out = static_cast<uint8_t*>(dw) + v0 * c.H * (p.out_f32 ? 4 : 2);
-    p.ldo = c.H;
-    p.factor = mean ? mean + 1 : nullptr;
-    if (!bf16_box(&a, dl, c.T, ld, 64) || !bf16_box(&b, x, c.T, c.H, 64)) return cudaErrorInvalidValue;
-    e = launch_gemm<DW, 2, 256>(a, b, p, s);
-  }
-  return e;
-}
-
-}  // namespace tc
-
-namespace {
-
-// ---- exact fp32 tiles of ST x ST outputs, K steps of 16, 256 threads with (ST / 16)^2 outputs
-// each. ST = 64 is for products whose 128-tiles would leave SMs without two blocks (256 x 128 x
-// 5003: 35 us for 80 blocks of 128 x 128). Rows go in pairs through fma.f32x2 (each half rounded
-// on its own, as fmaf): with one FMA per instruction and two warps per scheduler the tiles were
-// bound by issue (64 x 64 by 128 threads: 17 us).
-constexpr int SK = 16;
-
-struct SimtParams {
-  int M, N, K;
-  int splits, k_split;         // DX: K splits of k_split (a multiple of SK) each
-  const void *A, *B;           // operand element (row, k) at row * r + k * k
-  int64_t a_row, a_k, b_row, b_k;
-  int a_f32, b_f32;            // element types (else bf16)
-  int vec;                     // rows of both operands begin on multiples of 4 elements
-  const int32_t* target;
-  float2* part;
-  float* target_logit;
-  const float *lse, *dloss, *mean;
-  int v0, V;
-  void* out;
-  int64_t ldo;
-  int out_f32, add;
-};
-
-__device__ __forceinline__ float load_elem(const void* p, int64_t at, int f32) {
-  return f32 ? static_cast<const float*>(p)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-}
-__device__ __forceinline__ float4 load_elem4(const void* p, int64_t at, int f32) {
-  if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-  const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at);
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xffff0000u));
-}
-
-enum { S_STATS = 0, S_DLOGITS = 1, S_STORE = 2 };
-
-template <int MODE, int ST>
-__global__ void __launch_bounds__(256) simt_kernel(const SimtParams p) {
-  constexpr int TM = ST / 16, TN = ST / 16, LD = ST + 4;
-  constexpr int kLoads = ST * SK / 4 / 256;  // of four elements per thread, operand and step
-  let_next_begin();
-  after_previous();
-  __shared__ __align__(16) float sa[2][SK][LD], sb[2][SK][LD];
-  const int m0 = blockIdx.x * ST, n0 = blockIdx.y * ST;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int k_lo = blockIdx.z * p.k_split, k_hi = min(p.K, k_lo + p.k_split);
-  float2 acc2[TM / 2][TN];  // rows 2 i and 2 i + 1
 #pragma unroll
-  for (int i = 0; i < TM / 2; ++i)
+  for (int p = 0; p < NP; ++p) {
+    *reinterpret_cast<uint4*>(dst + p * plane + (int64_t)row * Hp + c) =
+        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+    if (p + 1 < NP)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc2[i][j] = make_float2(0.0f, 0.0f);
-  // Four elements per thread and load, along the operand's contiguous direction.
-  auto place = [&](int64_t kstep, int i, int* r, int* k) {
-    const int e = threadIdx.x + i * 256;
-    if (kstep == 1) *r = e / (SK / 4), *k = e % (SK / 4) * 4;
-    else *r = e % (ST / 4) * 4, *k = e / (ST / 4);
-  };
-  auto fetch = [&](float4 (&v)[kLoads], const void* src, int64_t rstep, int64_t kstep, int f32, int r0, int rows, int k0) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      int r, k;
-      place(kstep, i, &r, &k);
-      const int64_t at = (int64_t)(r0 + r) * rstep + (int64_t)(k0 + k) * kstep;
-      const bool along_k = kstep == 1;
-      const int left = along_k ? (r0 + r < rows ? k_hi - (k0 + k) : 0) : (k0 + k < k_hi ? rows - (r0 + r) : 0);
-      if (p.vec && left >= 4) {
-        v[i] = load_elem4(src, at, f32);
-      } else {
-        const int64_t step = along_k ? kstep : rstep;
-        v[i].x = left > 0 ? load_elem(src, at, f32) : 0.0f;
-        v[i].y = left > 1 ? load_elem(src, at + step, f32) : 0.0f;
-        v[i].z = left > 2 ? load_elem(src, at + 2 * step, f32) : 0.0f;
-        v[i].w = left > 3 ? load_elem(src, at + 3 * step, f32) : 0.0f;
-      }
-    }
-  };
-  auto keep = [&](float (*dst)[LD], const float4 (&v)[kLoads], int64_t kstep) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      int r, k;
-      place(kstep, i, &r, &k);
-      if (kstep == 1) {
-        dst[k][r] = v[i].x, dst[k + 1][r] = v[i].y, dst[k + 2][r] = v[i].z, dst[k + 3][r] = v[i].w;
-      } else {
-        *reinterpret_cast<float4*>(&dst[k][r]) = v[i];
-      }
-    }
-  };
-  float4 va[kLoads], vb[kLoads];
-  if (k_lo < k_hi) {
-    fetch(va, p.A, p.a_row, p.a_k, p.a_f32, m0, p.M, k_lo);
-    fetch(vb, p.B, p.b_row, p.b_k, p.b_f32, n0, p.N, k_lo);
-    keep(sa[0], va, p.a_k);
-    keep(sb[0], vb, p.b_k);
-  }
-  __syncthreads();
-  int buf = 0;
-  for (int k0 = k_lo; k0 < k_hi; k0 += SK) {
-    const bool more = k0 + SK < k_hi;
-    if (more) {  // the next step's loads fly while this one is multiplied
-      fetch(va, p.A, p.a_row, p.a_k, p.a_f32, m0, p.M, k0 + SK);
-      fetch(vb, p.B, p.b_row, p.b_k, p.b_f32, n0, p.N, k0 + SK);
-    }
-#pragma unroll
-    for (int k = 0; k < SK; ++k) {
-      float2 a[TM / 2];
-      float b[TN];
-#pragma unroll
-      for (int i = 0; i < TM; i += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(&sa[buf][k][ty * TM + i]);
-        a[i / 2] = make_float2(v.x, v.y);
-        a[i / 2 + 1] = make_float2(v.z, v.w);
-      }
-#pragma unroll
-      for (int j = 0; j < TN; j += 4)
-        *reinterpret_cast<float4*>(b + j) = *reinterpret_cast<const float4*>(&sb[buf][k][j * 16 + tx * 4]);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const float2 bb = make_float2(b[j], b[j]);
-#pragma unroll
-        for (int i = 0; i < TM / 2; ++i) acc2[i][j] = __ffma2_rn(a[i], bb, acc2[i][j]);
-      }
-    }
-    if (more) {
-      keep(sa[buf ^ 1], va, p.a_k);
-      keep(sb[buf ^ 1], vb, p.b_k);
-    }
-    __syncthreads();
-    buf ^= 1;
-  }
-  auto acc = [&](int i, int j) { return i & 1 ? acc2[i / 2][j].y : acc2[i / 2][j].x; };
-  // the thread's rows m0 + TM ty + i, columns n0 + 64 (j / 4) + 4 tx + j % 4
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int row = m0 + ty * TM + i;
-    const bool live = row < p.M;
-    auto col_of = [&](int j) { return n0 + j / 4 * 64 + tx * 4 + j % 4; };
-    if constexpr (MODE == S_STATS) {
-      constexpr float kLog2e = 1.4426950408889634f;
-      const int tgt = live ? p.target[row] : -1;
-      float m = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        if (col_of(j) < p.N) {
-          if (col_of(j) == tgt) p.target_logit[row] = acc(i, j);
-          m = fmaxf(m, acc(i, j) * kLog2e);
-        }
-      }
-#pragma unroll
-      for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      const float base = m == -INFINITY ? 0.0f : m;
-      float s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        if (col_of(j) < p.N) s += exp2f(fmaf(acc(i, j), kLog2e, -base));
-#pragma unroll
-      for (int off = 8; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      if (tx == 0 && live) p.part[(int64_t)blockIdx.y * p.M + row] = make_float2(m, s);
-    } else if (live) {
-      float lse = 0.0f, g = 0.0f;
-      int tgt = -1;
-      bool counts = false;
-      if constexpr (MODE == S_DLOGITS) {
-        tgt = p.target[row];
-        counts = tgt >= 0 && tgt < p.V;
-        lse = p.lse[row];
-        g = p.dloss ? p.dloss[row] : p.mean[1];
-      }
-#pragma unroll
-      for (int j0 = 0; j0 < TN; j0 += 4) {
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = acc(i, j0 + j);
-          if constexpr (MODE == S_DLOGITS) {
-            v[j] = expf(v[j] - lse);
-            if (col_of(j0 + j) + p.v0 == tgt) v[j] -= 1.0f;
-            v[j] = counts ? v[j] * g : 0.0f;
-          }
-        }
-        const int col = col_of(j0);
-        const int64_t at = ((int64_t)blockIdx.z * p.M + row) * p.ldo + col;
-        if (p.out_f32 && p.ldo % 4 == 0 && col + 3 < p.N) {
-          float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-          if (p.add) {
-            const float4 w = *o;
-            v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
-          }
-          *o = make_float4(v[0], v[1], v[2], v[3]);
-          continue;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (col + j >= p.N) break;
-          if (p.out_f32) {
-            float* o = static_cast<float*>(p.out) + at + j;
-            *o = p.add ? *o + v[j] : v[j];
-          } else {
-            static_cast<__nv_bfloat16*>(p.out)[at + j] = __float2bfloat16_rn(v[j]);
-          }
-        }
-      }
-    }
+      for (int i = 0; i < 8; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
   }
 }
 
-// The tile of a product: 64 while the 128-tiles do not give every SM two blocks.
-int simt_tile(int64_t M, int64_t N, int splits) {
-  return ceil_div(M, 128) * ceil_div(N, 128) * splits >= 2 * 152 ? 128 : 64;
-}
-
-template <int MODE>
-cudaError_t launch_simt(SimtParams p, cudaStream_t s) {
-  p.k_split = (int)(ceil_div(ceil_div(p.K, p.splits), SK) * SK);
-  const int st = simt_tile(p.M, p.N, p.splits);
-  const dim3 grid((unsigned)ceil_div(p.M, st), (unsigned)ceil_div(p.N, st), (unsigned)p.splits);
-  // a call begins with a plain launch (the logits), the products after it follow closely
-  if (MODE == S_STORE)
-    return st == 128 ? launch_after(simt_kernel<MODE, 128>, grid, 256, s, p) : launch_after(simt_kernel<MODE, 64>, grid, 256, s, p);
-  if (st == 128) simt_kernel<MODE, 128><<<grid, 256, 0, s>>>(p);
-  else simt_kernel<MODE, 64><<<grid, 256, 0, s>>>(p);
+cudaError_t launch_planes(const void* src, int f32, int rows, int H, void* dst, int64_t plane, int Hp, int zero_to,
+                          cudaStream_t s) {
+  const unsigned grid = (unsigned)ceil_div((int64_t)zero_to * (Hp / 8), 256);
+  auto* d = static_cast<__nv_bfloat16*>(dst);
+  if (f32) planes_kernel<float, 3><<<grid, 256, 0, s>>>(static_cast<const float*>(src), rows, H, d, plane, Hp, zero_to);
+  else planes_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(src), rows, H, d, plane, Hp, zero_to);
   return cudaGetLastError();
 }
 
@@ -996,57 +806,125 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// dx = the sum of the K splits' slices [splits][T H], in order.
+// dx = the sums of the pieces, from fp32 (x of one type or the other).
 template <typename T>
-__global__ void __launch_bounds__(256) join_dx_kernel(const float* slices, int splits, int64_t n, T* dx) {
-  after_previous();
+__global__ void __launch_bounds__(256) store_dx_kernel(const float* sums, int64_t n, T* dx) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
-  float v = 0.0f;
-#pragma unroll 16
-  for (int k = 0; k < splits; ++k) v += __ldg(slices + k * n + i);
-  if constexpr (sizeof(T) == 4) dx[i] = v;
-  else dx[i] = __float2bfloat16_rn(v);
+  if constexpr (sizeof(T) == 4) dx[i] = sums[i];
+  else dx[i] = __float2bfloat16_rn(sums[i]);
 }
 
-bool head_tc(const moe_head_config_t& c) { return c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0; }
+// The input gradient's tiles rarely fill whole rounds of the SMs (4096 x 4096 is 256 tiles of
+// 256 x 256 on 76 CTA pairs: 3.37 rounds, so 4). The tiles of the last round are therefore
+// split along K, by the number of ways that takes least time: rounds of stages of 64 (0.14 us
+// with 256 columns, half of that with 128) against the slices' traffic (0.08 us for a tile of
+// 256 x 256) and the launch that adds them.
+HeadSplit head_split(int64_t T, int64_t H, int64_t rows, int planes) {
+  const int tm = tile_rows(T), tn = tile_cols(T, planes), units = small_tokens(T) ? 152 : 76;
+  const int64_t tiles = ceil_div(T, tm) * ceil_div(H, tn), kblocks = ceil_div(rows, BK);
+  HeadSplit best{tiles, 1, 0};
+  const int64_t tail = tiles % units;
+  const double stage = 0.14 * tn / 256 * (planes == 3 ? 6 : 1), slice = 0.08 * tm * tn / 65536;
+  double least = (tail ? 1.0 : 0.0) * kblocks * stage;
+  for (int s = 2; s <= 32 && tail && s * 4 <= kblocks; ++s) {
+    const double t = (double)ceil_div(tail * s, units) * ceil_div(kblocks, s) * stage + tail * s * slice + 4.0;
+    if (t < least) least = t, best = {tiles - tail, s, (size_t)(tail * s) * tm * tn * 4};
+  }
+  return best;
+}
+
+// The plane products of a GEMM: all six of fp32 operands; those of an operand of three planes (A)
+// with one of one; or one.
+void set_terms(HeadParams* p, int a_planes, int b_planes) {
+  if (a_planes == 3 && b_planes == 3) {  // (0,2) (1,1) (2,0) (0,1) (1,0) (0,0)
+    p->terms = 6;
+    p->a_code = 0x010210;
+    p->b_code = 0x001012;
+  } else if (a_planes == 3) {  // (2,0) (1,0) (0,0)
+    p->terms = 3;
+    p->a_code = 0x012;
+    p->b_code = 0;
+  } else {
+    p->terms = 1;
+    p->a_code = p->b_code = 0;
+  }
+}
+
+// x and one piece of w as the tensor maps read them: in place, or laid out in the workspace.
+struct Operands {
+  int planes;          // of dz, and the kernel's: 1 in place, 3 where laid out
+  int in_planes;       // of x and w
+  bool laid_out;
+  int64_t cols;        // of a row: H, or H padded to a multiple of 8
+  int64_t x_rows, w_rows, dl_rows;     // of the maps
+  int64_t x_plane, w_plane, dl_plane;  // rows from a plane to the next
+  const void *x, *w;
+};
+
+}  // namespace
+}  // namespace tc
+
+namespace {
+
+bool is_f32(const moe_head_config_t& c) { return c.act_dtype == MOE_DTYPE_F32; }
+bool laid_out(const moe_head_config_t& c) { return is_f32(c) || c.H % 8; }
+int planes_of(const moe_head_config_t& c) { return laid_out(c) ? 3 : 1; }  // of dz
+int64_t padded_tokens(const moe_head_config_t& c) { return align_up((size_t)c.T, 64); }
+
+tc::Operands operands(const moe_head_config_t& c, const HeadScratch& L, const void* x, const void* w, char* ws) {
+  tc::Operands o{};
+  o.planes = planes_of(c);
+  o.in_planes = is_f32(c) ? 3 : 1;
+  o.laid_out = laid_out(c);
+  o.cols = o.laid_out ? (int64_t)align_up((size_t)c.H, 8) : c.H;
+  o.x_plane = o.dl_plane = o.laid_out ? padded_tokens(c) : c.T;
+  o.w_plane = o.laid_out ? L.piece : c.V;
+  o.x_rows = o.in_planes * o.x_plane;
+  o.w_rows = o.in_planes * o.w_plane;
+  o.dl_rows = o.planes * o.dl_plane;
+  o.x = o.laid_out ? ws + L.x : x;
+  o.w = o.laid_out ? ws + L.w : w;
+  return o;
+}
+
+// Lays out x, and rows [v0, v0 + rows) of w, where the products need it.
+cudaError_t lay_out_x(const moe_head_config_t& c, const tc::Operands& o, const void* x, cudaStream_t s) {
+  if (!o.laid_out) return cudaSuccess;
+  return tc::launch_planes(x, is_f32(c), c.T, c.H, const_cast<void*>(o.x), o.x_plane * o.cols, (int)o.cols, (int)o.x_plane, s);
+}
+cudaError_t lay_out_w(const moe_head_config_t& c, const tc::Operands& o, const void* w, int64_t v0, int rows, cudaStream_t s) {
+  if (!o.laid_out) return cudaSuccess;
+  return tc::launch_planes(static_cast<const char*>(w) + v0 * c.H * (is_f32(c) ? 4 : 2), is_f32(c), rows, c.H,
+                           const_cast<void*>(o.w), o.w_plane * o.cols, (int)o.cols, (int)align_up((size_t)rows, 64), s);
+}
 
 }  // namespace
 
-// A piece holds at most 256 MB of dz unless the caller names its length; whole 256-column
-// tiles. The SIMT input gradient splits K where its tiles alone would not fill the SMs, into
-// slices [splits][T, H]; the tensor cores' split is head_split's.
+// A piece holds at most 256 MB of dz and laid-out w unless the caller names its length; whole
+// 256-column tiles.
 HeadScratch head_scratch(const moe_head_config_t& c) {
   HeadScratch L{};
-  const bool tc = head_tc(c);
-  const int64_t esize = tc ? 2 : 4;
-  const int64_t T = std::max(c.T, 1);
-  int64_t piece = c.piece > 0 ? c.piece : std::max<int64_t>(4096, (256ll << 20) / (T * esize));
+  const bool lay = laid_out(c);
+  const int64_t T = std::max<int64_t>(lay ? padded_tokens(c) : c.T, 1), Hp = align_up((size_t)c.H, 8), np = planes_of(c);
+  const int64_t row_bytes = 2 * np * (T + (lay ? Hp : 0));
+  int64_t piece = c.piece > 0 ? c.piece : std::max<int64_t>(4096, (256ll << 20) / row_bytes);
   piece = (int64_t)align_up((size_t)std::min<int64_t>(piece, c.V), 256);
   L.piece = piece;
   L.ld = (int)piece;
-  const int64_t rows = std::min<int64_t>(piece, c.V);
-  const bool one = piece >= c.V;
-  size_t dx_bytes;
-  if (tc) {
-    L.split = tc::head_split(T, c.H, rows);
-    dx_bytes = one ? 0 : (size_t)T * c.H * 4;
-  } else {
-    const int64_t tiles = ceil_div(T, 64) * ceil_div(c.H, 64);
-    L.split = {0, (int)std::max<int64_t>(1, std::min<int64_t>({152 * 2 / tiles, rows / 64, 64})), 0};
-    dx_bytes = one && L.split.splits == 1 ? 0 : (size_t)L.split.splits * T * c.H * 4;
-  }
+  L.split = tc::head_split(T, c.H, std::min<int64_t>(piece, c.V), (int)np);
   size_t o = kWsHead;
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o = align_up(o + bytes, 256);
     return at;
   };
-  // (max, sum) of the halves of 128- or 256-column tiles, or of whole SIMT tiles
-  L.part = take((size_t)ceil_div(c.V, 128) * 2 * T * 8);
+  L.part = take((size_t)ceil_div(c.V, 128) * 2 * T * 8);  // (max, sum) of the halves of 128- or 256-column tiles
   L.target_logit = take((size_t)T * 4);
-  L.dlogits = take((size_t)T * piece * esize);
-  L.dx = take(dx_bytes);
+  L.x = take(lay ? (size_t)(np * T * Hp * 2) : 0);
+  L.w = take(lay ? (size_t)(np * piece * Hp * 2) : 0);
+  L.dlogits = take((size_t)(np * T * piece * 2));
+  L.dx = take(piece >= c.V ? 0 : (size_t)T * c.H * 4);
   L.slices = take(L.split.bytes);
   L.total = o;
   return L;
@@ -1055,88 +933,130 @@ HeadScratch head_scratch(const moe_head_config_t& c) {
 cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
                              float* loss, float* lse, float* mean, void* ws, DeviceStatus* st, cudaStream_t s) {
   if (c.T == 0) return mean ? cudaMemsetAsync(mean, 0, 8, s) : cudaSuccess;
+  using namespace tc;
   const HeadScratch L = head_scratch(c);
   char* b = static_cast<char*>(ws);
   auto* part = reinterpret_cast<float2*>(b + L.part);
   auto* tl = reinterpret_cast<float*>(b + L.target_logit);
-  cudaError_t e;
-  int parts;
-  if (head_tc(c)) {
-    parts = 2 * (int)ceil_div(c.V, tc::head_tile_cols(c.T));
-    e = tc::launch_head_stats(c, x, w, target, part, tl, st, s);
-  } else {
-    parts = (int)ceil_div(c.V, simt_tile(c.T, c.V, 1));
-    const int f32 = c.act_dtype == MOE_DTYPE_F32;
-    SimtParams p{};
-    p.M = c.T, p.N = c.V, p.K = c.H, p.splits = 1;
-    p.A = x, p.B = w;
-    p.a_row = p.b_row = c.H, p.a_k = p.b_k = 1;
-    p.a_f32 = p.b_f32 = f32, p.vec = c.H % 4 == 0;
-    p.target = target, p.part = part, p.target_logit = tl;
-    e = launch_simt<S_STATS>(p, s);
+  const Operands o = operands(c, L, x, w, b);
+  const int tm = tile_rows(c.T), tn = tile_cols(c.T, o.planes);
+  cudaError_t e = lay_out_x(c, o, x, s);
+  int parts = 0;
+  const int64_t step = o.laid_out ? L.piece : c.V;  // w in place needs no pieces here
+  for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += step) {
+    const int rows = (int)std::min<int64_t>(step, c.V - v0);
+    if ((e = lay_out_w(c, o, w, v0, rows, s)) != cudaSuccess) break;
+    HeadParams p = base_params(c.T, rows, c.H, tm, tn, st);
+    p.v0 = (int)v0;
+    p.V = c.V;
+    set_terms(&p, o.in_planes, o.in_planes);
+    p.a_plane = (int)o.x_plane;
+    p.b_plane = (int)o.w_plane;
+    p.target = target;
+    p.part = part + (int64_t)parts * c.T;
+    p.target_logit = tl;
+    CUtensorMap ma, mb;
+    if (!bf16_box(&ma, o.x, o.x_rows, o.cols, BM) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
+      return cudaErrorInvalidValue;
+    e = launch_mode<STATS>(c.T, o.planes, ma, mb, p, s);
+    parts += 2 * p.n_tiles;
   }
   if (e != cudaSuccess) return e;
   // the ticket lives in the head, which moe_workspace_init clears
   auto* ticket = reinterpret_cast<uint32_t*>(b + 320);
+  const float2* from = part;
+  const float* logits = tl;
   if (c.T >= 1024)
-    return launch_after(join_kernel<32>, (unsigned)ceil_div(c.T, 32), 1024, s, part, parts, c.T, c.V, target, tl, loss, lse,
+    return launch_after(join_kernel<32>, (unsigned)ceil_div(c.T, 32), 1024, s, from, parts, c.T, c.V, target, logits, loss, lse,
                         mean, ticket, st);
-  return launch_after(join_kernel<4>, (unsigned)ceil_div(c.T, 4), 1024, s, part, parts, c.T, c.V, target, tl, loss, lse, mean,
+  return launch_after(join_kernel<4>, (unsigned)ceil_div(c.T, 4), 1024, s, from, parts, c.T, c.V, target, logits, loss, lse, mean,
                       ticket, st);
 }
 
 cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
                                       const float* lse, const float* dloss, const float* mean, void* dx, void* dw,
                                       void* ws, DeviceStatus* st, cudaStream_t s) {
-  if (c.T == 0)
-    return dw ? cudaMemsetAsync(dw, 0, (size_t)c.V * c.H * (c.grad_dtype == MOE_DTYPE_F32 ? 4 : 2), s) : cudaSuccess;
+  const int g32 = c.grad_dtype == MOE_DTYPE_F32, f32 = is_f32(c);
+  if (c.T == 0) return dw ? cudaMemsetAsync(dw, 0, (size_t)c.V * c.H * (g32 ? 4 : 2), s) : cudaSuccess;
+  using namespace tc;
   const HeadScratch L = head_scratch(c);
-  const bool tc = head_tc(c), one = L.piece >= c.V && (tc || L.split.splits == 1);
+  const bool one = L.piece >= c.V;  // dx needs no sum over pieces
   char* b = static_cast<char*>(ws);
-  float* slices = reinterpret_cast<float*>(b + L.dx);
-  const int f32 = c.act_dtype == MOE_DTYPE_F32;
-  for (int64_t v0 = 0; v0 < c.V; v0 += L.piece) {
+  const Operands o = operands(c, L, x, w, b);
+  const int tm = tile_rows(c.T), tn = tile_cols(c.T, o.planes);
+  void* dl = b + L.dlogits;
+  float* dx_sums = reinterpret_cast<float*>(b + L.dx);
+  const float* factor = mean ? mean + 1 : nullptr;
+  cudaError_t e = lay_out_x(c, o, x, s);
+  for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {
     const int rows = (int)std::min<int64_t>(L.piece, c.V - v0);
-    cudaError_t e;
-    if (tc) {
-      e = tc::launch_head_piece(c, x, w, target, lse, dloss, mean, v0, rows, b + L.dlogits, L.ld,
-                                dx ? (one ? dx : slices) : nullptr, L.split, reinterpret_cast<float*>(b + L.slices),
-                                !one, v0 > 0, dw, st, s);
-      if (e != cudaSuccess) return e;
-      continue;
+    if ((e = lay_out_w(c, o, w, v0, rows, s)) != cudaSuccess) break;
+    const int w_row0 = o.laid_out ? 0 : (int)v0;
+    CUtensorMap ma, mb;
+    // dz of the piece: M = T, N = its rows, K = H
+    HeadParams p = base_params(c.T, rows, c.H, tm, tn, st);
+    p.v0 = (int)v0;
+    p.w_row0 = w_row0;
+    p.V = c.V;
+    set_terms(&p, o.in_planes, o.in_planes);
+    p.a_plane = (int)o.x_plane;
+    p.b_plane = (int)o.w_plane;
+    p.target = target;
+    p.lse = lse;
+    p.dloss = dloss;
+    p.out = dl;
+    p.ldo = L.ld;
+    p.m_out = (int)o.dl_plane;
+    p.out_plane = o.dl_plane * L.ld;
+    if (!bf16_box(&ma, o.x, o.x_rows, o.cols, BM) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
+      return cudaErrorInvalidValue;
+    if ((e = launch_mode<DLOGITS>(c.T, o.planes, ma, mb, p, s)) != cudaSuccess) break;
+    if (dx) {  // M = T, N = H, K = the piece's rows
+      p = base_params(c.T, c.H, rows, tm, tn, st);
+      p.w_row0 = w_row0;
+      set_terms(&p, o.planes, o.in_planes);
+      p.a_plane = (int)o.dl_plane;
+      p.b_plane = (int)o.w_plane;
+      p.direct = (int)L.split.direct;
+      p.splits = L.split.splits;
+      p.slices = reinterpret_cast<float*>(b + L.slices);
+      p.out = one ? dx : dx_sums;
+      p.ldo = c.H;
+      p.out_f32 = !one || f32;
+      p.scalar = c.H * (p.out_f32 ? 4 : 2) % 16 != 0;
+      p.add = v0 > 0;
+      p.factor = factor;
+      if (!bf16_box(&ma, dl, o.dl_rows, L.ld, BM) || !bf16_box(&mb, o.w, o.w_rows, o.cols, 64)) return cudaErrorInvalidValue;
+      if ((e = launch_mode<DX>(c.T, o.planes, ma, mb, p, s)) != cudaSuccess) break;
+      if (p.splits > 1) {
+        const dim3 grid((unsigned)(tm * tn / 1024), (unsigned)(p.m_tiles * p.n_tiles - p.direct));
+        e = p.out_f32 ? launch_after(join_slices_kernel<float>, grid, 256, s, p, tm, tn, static_cast<float*>(p.out))
+                      : launch_after(join_slices_kernel<__nv_bfloat16>, grid, 256, s, p, tm, tn, static_cast<__nv_bfloat16*>(p.out));
+        if (e != cudaSuccess) break;
+      }
     }
-    SimtParams p{};
-    p.M = c.T, p.N = rows, p.K = c.H, p.splits = 1;
-    p.A = x, p.a_row = c.H, p.a_k = 1, p.a_f32 = f32;
-    p.B = static_cast<const char*>(w) + v0 * c.H * (f32 ? 4 : 2), p.b_row = c.H, p.b_k = 1, p.b_f32 = f32;
-    p.target = target, p.lse = lse, p.dloss = dloss, p.mean = mean, p.v0 = (int)v0, p.V = c.V;
-    p.out = b + L.dlogits, p.ldo = L.ld, p.out_f32 = 1, p.vec = c.H % 4 == 0;
-    if ((e = launch_simt<S_DLOGITS>(p, s)) != cudaSuccess) return e;
-    SimtParams q{};
-    q.A = b + L.dlogits, q.a_f32 = 1, q.splits = 1, q.vec = c.H % 4 == 0;
-    if (dx) {
-      q.M = c.T, q.N = c.H, q.K = rows, q.splits = L.split.splits;
-      q.a_row = L.ld, q.a_k = 1;
-      q.B = p.B, q.b_row = 1, q.b_k = c.H, q.b_f32 = f32;
-      q.out = one ? dx : slices, q.ldo = c.H, q.out_f32 = one ? f32 : 1, q.add = v0 > 0;
-      if ((e = launch_simt<S_STORE>(q, s)) != cudaSuccess) return e;
-    }
-    if (dw) {
-      const int g32 = c.grad_dtype == MOE_DTYPE_F32;
-      q.M = rows, q.N = c.H, q.K = c.T, q.splits = 1, q.add = 0;
-      q.a_row = 1, q.a_k = L.ld;
-      q.B = x, q.b_row = 1, q.b_k = c.H, q.b_f32 = f32;
-      q.out = static_cast<char*>(dw) + v0 * c.H * (g32 ? 4 : 2), q.ldo = c.H, q.out_f32 = g32;
-      if ((e = launch_simt<S_STORE>(q, s)) != cudaSuccess) return e;
+    if (dw) {  // M = the piece's rows, N = H, K = T
+      const int wn = o.planes == 3 ? 128 : 256;
+      p = base_params(rows, c.H, c.T, 2 * BM, wn, st);
+      set_terms(&p, o.planes, o.in_planes);
+      p.a_plane = (int)o.dl_plane;
+      p.b_plane = (int)o.x_plane;
+      p.out_f32 = g32;
+      p.out = static_cast<char*>(dw) + v0 * c.H * (g32 ? 4 : 2);
+      p.ldo = c.H;
+      p.scalar = c.H * (g32 ? 4 : 2) % 16 != 0;
+      p.factor = factor;
+      if (!bf16_box(&ma, dl, o.dl_rows, L.ld, 64) || !bf16_box(&mb, o.x, o.x_rows, o.cols, 64)) return cudaErrorInvalidValue;
+      e = launch_mode<DW>(c.T, o.planes, ma, mb, p, s);
     }
   }
-  if (!dx || one) return cudaSuccess;
+  if (e != cudaSuccess || !dx || one) return e;
   const int64_t n = (int64_t)c.T * c.H;
-  const int splits = tc ? 1 : L.split.splits;
   const unsigned grid = (unsigned)ceil_div(n, 256);
-  const float* from = slices;
-  return f32 ? launch_after(join_dx_kernel<float>, grid, 256, s, from, splits, n, static_cast<float*>(dx))
-             : launch_after(join_dx_kernel<__nv_bfloat16>, grid, 256, s, from, splits, n, static_cast<__nv_bfloat16*>(dx));
+  const float* from = dx_sums;
+  if (f32) store_dx_kernel<float><<<grid, 256, 0, s>>>(from, n, static_cast<float*>(dx));
+  else store_dx_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(from, n, static_cast<__nv_bfloat16*>(dx));
+  return cudaGetLastError();
 }
 
 }  // namespace moe

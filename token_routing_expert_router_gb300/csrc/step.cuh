@@ -74,7 +74,7 @@ struct HeadSplit {  // of the input gradient's product
   size_t bytes;     // fp32 tiles of the splits
 };
 struct HeadScratch {  // workspace offsets, after the status head
-  size_t part, target_logit, dlogits, dx, slices, total;
+  size_t part, target_logit, x, w, dlogits, dx, slices, total;
   int64_t piece;   // vocabulary rows whose logit gradients are held at once
   int ld;          // row length of dlogits
   HeadSplit split;

@@ -23,8 +23,9 @@ moe_status_t validate(const moe_head_config_t* c) {
   if (!c || c->T < 0 || c->H < 1 || c->V < 1 || c->piece < 0) return MOE_ERR_INVALID_ARG;
   if (!act_ok(c->act_dtype) || !act_ok(c->grad_dtype)) return MOE_ERR_INVALID_ARG;
   // tile and row numbers are 32-bit, with room for a grid's last step
-  if (c->T > (1 << 30) || c->H > (1 << 20) || c->V > (1 << 23)) return MOE_ERR_UNSUPPORTED;
-  return ceil_div(c->T, 128) * ceil_div(c->V, 128) > (1 << 30) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  if (c->T > (1 << 28) || c->H > (1 << 20) || c->V > (1 << 23)) return MOE_ERR_UNSUPPORTED;
+  if (ceil_div(c->T, 128) * ceil_div(c->V, 128) > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  return ceil_div(c->T, 128) * ceil_div(c->H, 128) > (1 << 26) ? MOE_ERR_UNSUPPORTED : MOE_OK;  // times 32 splits
 }
 
 moe_status_t validate(const moe_embed_config_t* c) {
