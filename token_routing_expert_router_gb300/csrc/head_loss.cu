@@ -423,11 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cc = col0 + c0;   // first column of the chunk
         const int cols = p.N - cc;  // columns from there on that exist
         if constexpr (MODE == DLOGITS) {
+          const int at = tgt - cc;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            v[i] = ex2(fmaf(v[i], kLog2e, -lse2));
-            if (i == tgt - cc) v[i] -= 1.0f;
-            v[i] = counts && i < cols ? v[i] * g : 0.0f;
+            const float pr = ex2(fmaf(v[i], kLog2e, -lse2)) - (i == at ? 1.0f : 0.0f);
+            v[i] = counts && i < cols ? pr * g : 0.0f;
           }
           // columns past the vocabulary are written too, as zeros: they are K rows of the next products
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)row0 * p.ldo + cc;
@@ -455,13 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 32; h += 16) {
               stage_f32(stage, lane, v + h);
-              if (p.scalar) flush_scalar(stage, lane, out + h, p.ldo, p.M - row0, cols - h, add);
+              if (NP == 3 && p.scalar) flush_scalar(stage, lane, out + h, p.ldo, p.M - row0, cols - h, add);
               else flush_edge(stage, lane, reinterpret_cast<uint8_t*>(out + h), p.ldo * 4, p.M - row0, (cols - h) / 4, add);
             }
           } else {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)row0 * p.ldo + cc;
             stage_bf16(stage, lane, v);
-            if (p.scalar) flush_scalar(stage, lane, out, p.ldo, p.M - row0, cols, false);
+            if (NP == 3 && p.scalar) flush_scalar(stage, lane, out, p.ldo, p.M - row0, cols, false);
             else flush_edge(stage, lane, reinterpret_cast<uint8_t*>(out), p.ldo * 2, p.M - row0, cols / 8, false);
           }
         }
