@@ -62,6 +62,7 @@ struct HeadParams {
   int terms;           // plane products per K stage of 64 elements, and the planes of A and B in
   uint32_t a_code, b_code;  //   each of them, four bits a term from the first on
   int a_plane, b_plane;  // rows from one plane of A and B to the next
+  int a_bytes;         // of A in a stage: its map's box may have fewer than 128 rows
   const int32_t* target;
   // STATS: (max, sum) per token and half tile [2 n_tiles][T], and the target's logit [T]
   float2* part;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* b_dst = sB + stage * kBBytes;
           uint32_t bar = 0;
           if constexpr (CG == 1) {
-            mbar_arrive_expect_tx(&full[stage], kStageBytes);
+            mbar_arrive_expect_tx(&full[stage], kBBytes + p.a_bytes);
           } else {
             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
             bar = mapa_shared(smem_addr(&full[stage]), 0);
@@ -618,6 +619,12 @@ cudaError_t launch_mode(int T, int planes, const CUtensorMap& a, const CUtensorM
   return planes == 3 ? launch_gemm<MODE, 2, 128, 3>(a, b, p, s) : launch_gemm<MODE, 2, 256, 1>(a, b, p, s);
 }
 
+// Rows of A's box, and so of a stage's A: what up to 128 tokens fill of the tile. The rest of it
+// holds whatever was there, for rows of the product that are not stored. (A box of 128 rows of
+// which 120 and more lie outside the tensor is slow to fill: the logits of 1 x 4096 x 32000 took
+// 73 us with it, 58 with a box of 16.)
+int a_box(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : BM; }
+
 HeadParams base_params(int64_t M, int64_t N, int64_t K, int tm, int tn, DeviceStatus* st) {
   HeadParams p{};
   p.M = p.m_out = (int)M;
@@ -627,6 +634,7 @@ HeadParams base_params(int64_t M, int64_t N, int64_t K, int tm, int tn, DeviceSt
   p.kblocks = (int)ceil_div(K, BK);
   p.direct = p.m_tiles * p.n_tiles;
   p.splits = 1;
+  p.a_bytes = kABytes;
   p.status = st;
   p.timeout_ns = kTimeoutNs;
   return p;
@@ -950,13 +958,14 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
     p.v0 = (int)v0;
     p.V = c.V;
     set_terms(&p, o.in_planes, o.in_planes);
+    p.a_bytes = a_box(c.T) * BK * 2;
     p.a_plane = (int)o.x_plane;
     p.b_plane = (int)o.w_plane;
     p.target = target;
     p.part = part + (int64_t)parts * c.T;
     p.target_logit = tl;
     CUtensorMap ma, mb;
-    if (!bf16_box(&ma, o.x, o.x_rows, o.cols, BM) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
+    if (!bf16_box(&ma, o.x, o.x_rows, o.cols, a_box(c.T)) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
       return cudaErrorInvalidValue;
     e = launch_mode<STATS>(c.T, o.planes, ma, mb, p, s);
     parts += 2 * p.n_tiles;
@@ -999,6 +1008,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     p.w_row0 = w_row0;
     p.V = c.V;
     set_terms(&p, o.in_planes, o.in_planes);
+    p.a_bytes = a_box(c.T) * BK * 2;
     p.a_plane = (int)o.x_plane;
     p.b_plane = (int)o.w_plane;
     p.target = target;
@@ -1008,13 +1018,14 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     p.ldo = L.ld;
     p.m_out = (int)o.dl_plane;
     p.out_plane = o.dl_plane * L.ld;
-    if (!bf16_box(&ma, o.x, o.x_rows, o.cols, BM) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
+    if (!bf16_box(&ma, o.x, o.x_rows, o.cols, a_box(c.T)) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
       return cudaErrorInvalidValue;
     if ((e = launch_mode<DLOGITS>(c.T, o.planes, ma, mb, p, s)) != cudaSuccess) break;
     if (dx) {  // M = T, N = H, K = the piece's rows
       p = base_params(c.T, c.H, rows, tm, tn, st);
       p.w_row0 = w_row0;
       set_terms(&p, o.planes, o.in_planes);
+      p.a_bytes = a_box(c.T) * BK * 2;
       p.a_plane = (int)o.dl_plane;
       p.b_plane = (int)o.w_plane;
       p.direct = (int)L.split.direct;
@@ -1026,7 +1037,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
       p.scalar = c.H * (p.out_f32 ? 4 : 2) % 16 != 0;
       p.add = v0 > 0;
       p.factor = factor;
-      if (!bf16_box(&ma, dl, o.dl_rows, L.ld, BM) || !bf16_box(&mb, o.w, o.w_rows, o.cols, 64)) return cudaErrorInvalidValue;
+      if (!bf16_box(&ma, dl, o.dl_rows, L.ld, a_box(c.T)) || !bf16_box(&mb, o.w, o.w_rows, o.cols, 64)) return cudaErrorInvalidValue;
       if ((e = launch_mode<DX>(c.T, o.planes, ma, mb, p, s)) != cudaSuccess) break;
       if (p.splits > 1) {
         const dim3 grid((unsigned)(tm * tn / 1024), (unsigned)(p.m_tiles * p.n_tiles - p.direct));
