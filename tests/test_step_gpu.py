@@ -244,7 +244,9 @@ HEAD_CASES = [
     (128, 256, 777, BF, FP, 256, 0.1), (129, 264, 1025, BF, BF, 0, 0.3), (300, 128, 5003, BF, BF, 1024, 0.1),
     (513, 1032, 2500, BF, FP, 1000, 0.0), (256, 64, 257, BF, BF, 256, 1.0), (70, 2048, 40000, BF, BF, 39936, 0.0),
     (2, 128, 33000, BF, BF, 0, 0.0), (1, 1, 1, FP, FP, 0, 0.0), (7, 33, 129, FP, FP, 0, 0.3),
-    (200, 128, 1003, FP, FP, 256, 0.1), (130, 77, 300, BF, BF, 0, 0.1), (64, 96, 20000, FP, BF, 0, 0.0)]
+    (200, 128, 1003, FP, FP, 256, 0.1), (130, 77, 300, BF, BF, 0, 0.1), (64, 96, 20000, FP, BF, 0, 0.0),
+    (150, 33, 400, FP, FP, 256, 0.1), (140, 35, 300, FP, BF, 0, 0.2), (1100, 72, 300, BF, FP, 256, 0.1),
+    (1500, 40, 700, FP, FP, 0, 0.5), (300, 101, 600, BF, FP, 256, 0.0)]
 
 
 @pytest.mark.parametrize("T,H,V,dt,gdt,piece,skip", HEAD_CASES)
@@ -456,7 +458,7 @@ def clip_views(sizes, dtypes, g, std=0.1, lead=1):
 CLIP_CASES = [
     ([1], [FP], 0), ([5], [BF], 1), ([0, 7, 0], [FP, BF, FP], 1), ([8192 * 3 + 5, 1, 2, 3], [FP, BF, FP, BF], 3),
     ([100003, 70001], [BF, FP], 1), ([33] * 130, [FP, BF] * 65, 1), ([1000] * 400, [FP] * 400, 0),
-    ([3_000_000, 17], [FP, FP], 0)]
+    ([3_000_000, 17], [FP, FP], 0), ([5_000_000, 1_000_003, 33], [FP, FP, BF], 1)]
 
 
 @pytest.mark.parametrize("sizes,dtypes,lead", CLIP_CASES)
