@@ -11,9 +11,9 @@
 //
 // All products run on the tensor cores (tcgen05): warp 0 feeds a ring of shared-memory stages
 // by TMA, warp 1 issues the MMAs into two TMEM accumulators, warps 2-9 are the epilogue of one
-// accumulator while the other fills. Tiles are 256 x 256 on a CTA pair, or 128 x 128 on one CTA
-// for up to 128 tokens, where reading w is all the time there is and smaller tiles spread it
-// more evenly over the SMs. Edges need no special case in the operands: the TMA fills zeros
+// accumulator while the other fills. Tiles are 256 x 256 on a CTA pair, or on one CTA 128 rows
+// and 64 to 256 columns for up to 128 tokens, where reading w is all the time there is and the
+// width is chosen to spread it evenly over the SMs. Edges need no special case in the operands: the TMA fills zeros
 // past the last row and column.
 //
 // fp32 operands are split into three bf16 planes, v = v0 + v1 + v2 with 8 bits of the mantissa
@@ -46,6 +46,7 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRun = 16;  // K stages (of 64 elements) added by the tensor core in one go
 
+constexpr int kMaxStages = 12;  // of a ring whose stages are sized at run time
 constexpr int kNowhere = -(1 << 30);  // no column: far below the first of any tile
 
 enum Mode { STATS = 0, DLOGITS = 1, DX = 2, DW = 3 };
@@ -64,8 +65,11 @@ struct HeadParams {
   int a_plane, b_plane;  // rows from one plane of A and B to the next
   int a_bytes;         // of A in a stage: its map's box may have fewer than 128 rows
   const int32_t* target;
-  // STATS: (max, sum) per token and half tile [2 n_tiles][T], and the target's logit [T]
+  // STATS: (max, sum) per token and half tile [2 n_tiles][T] - or, where all tiles have the same
+  // rows (one m tile), per half of a CTA's or pair's tiles [2 units][T] - and the target's logit [T]
   float2* part;
+  int bn, stages;      // STATS on single CTAs: columns of a tile, a multiple of 16, and the ring's
+                       //   stages (of a_bytes and bn rows of w)
   float* target_logit;
   // DLOGITS
   const float *lse, *dloss;
@@ -86,7 +90,7 @@ template <int CG, int BN>
 struct HeadSmem {
   static constexpr int kBBytes = (BN / CG) * BK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = kStageBytes > 32768 ? 4 : 6;  // 192 KB at most
   static constexpr size_t kBytes = 1024 + (size_t)kStages * kStageBytes + 256 + kEpiWarps * 2048;
 };
 
@@ -211,21 +215,29 @@ template <int MODE, int CG, int BN, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const HeadParams p) {
   using S = HeadSmem<CG, BN>;
-  constexpr int kStages = S::kStages, kBBytes = S::kBBytes, kStageBytes = S::kStageBytes;
+  constexpr int kBBytes = S::kBBytes, kStageBytes = S::kStageBytes;
   constexpr int TM = BM * CG;
   constexpr int kTmemCols = 2 * BN;
   constexpr bool kAmn = MODE == DW;                 // A read MN-major (its rows are the K index)
   constexpr bool kBmn = MODE == DX || MODE == DW;   // the same for B
   constexpr int kBoxes = (BN / CG) / 64;
+  // Few tokens: the tile's width is chosen so that the SMs' rounds come out even, and a stage has
+  // only the rows that there are, so that the ring is deep. The MMA reads 128 rows of A all the
+  // same: into the next stages, for rows of the product that are not stored.
+  constexpr bool kFlex = MODE == STATS && CG == 1 && NP == 1;
+  constexpr int kMostStages = kFlex ? kMaxStages : S::kStages;
+  const int bn_cols = kFlex ? p.bn : BN;
+  const int kStages = kFlex ? p.stages : S::kStages;
+  const int a_stride = kFlex ? p.a_bytes : kABytes, b_stride = kFlex ? bn_cols * BK * 2 : kBBytes;
   extern __shared__ uint8_t smem_raw[];
   let_next_begin();  // the small kernel that joins the tiles' results
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
-  uint8_t* sB = smem + kStages * kABytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint8_t* sB = smem + kStages * a_stride;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kStages * kStageBytes);
   uint64_t* full = bars;
-  uint64_t* empty = bars + kStages;
-  uint64_t* tfull = bars + 2 * kStages;
+  uint64_t* empty = bars + kMostStages;
+  uint64_t* tfull = bars + 2 * kMostStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -281,17 +293,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
         const HeadTile t = head_tile<MODE>(tile, p);
-        const int am = t.mb * TM + (int)rank * BM, bn = t.nb * BN + (int)rank * (BN / CG);
+        const int am = t.mb * TM + (int)rank * BM, bn = t.nb * bn_cols + (int)rank * (BN / CG);
         int kb = t.kb0, term = 0;
         for (int ks = t.kb0 * terms; ks < t.kb1 * terms; ++ks) {
           const int pa = NP == 3 ? (int)(p.a_code >> (4 * term) & 3) * p.a_plane : 0;
           const int pb = NP == 3 ? (int)(p.b_code >> (4 * term) & 3) * p.b_plane : 0;
           if (!mbar_wait(&empty[stage], phase ^ 1, abort, p.timeout_ns, p.status)) { ok = false; break; }
-          uint8_t* a_dst = sA + stage * kABytes;
-          uint8_t* b_dst = sB + stage * kBBytes;
+          uint8_t* a_dst = sA + stage * a_stride;
+          uint8_t* b_dst = sB + stage * b_stride;
           uint32_t bar = 0;
           if constexpr (CG == 1) {
-            mbar_arrive_expect_tx(&full[stage], kBBytes + p.a_bytes);
+            mbar_arrive_expect_tx(&full[stage], b_stride + p.a_bytes);
           } else {
             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
             bar = mapa_shared(smem_addr(&full[stage]), 0);
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ======================= MMA issuer (the leader of a pair issues for both CTAs)
     if (lane == 0 && leader) {
-      constexpr uint32_t idesc = idesc_make(1, TM, BN) | ((kAmn ? 1u : 0u) << 15) | ((kBmn ? 1u : 0u) << 16);
+      const uint32_t idesc = idesc_make(1, TM, bn_cols) | ((kAmn ? 1u : 0u) << 15) | ((kBmn ? 1u : 0u) << 16);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -346,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (; ks < end; ++ks) {
             if (!mbar_wait(&full[stage], phase, abort, p.timeout_ns, p.status)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t a_addr = smem_addr(sA + stage * kABytes);
-            const uint32_t b_addr = smem_addr(sB + stage * kBBytes);
+            const uint32_t a_addr = smem_addr(sA + stage * a_stride);
+            const uint32_t b_addr = smem_addr(sB + stage * b_stride);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
               const uint64_t ad = kAmn ? desc_mn(a_addr + k * 2048) : desc_k_sw128(a_addr + k * 32);
@@ -383,10 +395,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty_leader = CG == 2 ? mapa_shared(smem_addr(&tempty[0]), 0) : 0;
     int acc = 0;
     uint32_t acc_phase = 0;
+    float run_max = -INFINITY, run_sum = 0.0f;  // STATS with one m tile: of all tiles so far
     for (int tile = unit; tile < total_tiles; tile += nunits) {
       const HeadTile t = head_tile<MODE>(tile, p);
       const int row0 = t.mb * TM + wrow, row = row0 + lane;  // the thread's row of the product
-      const int col0 = t.nb * BN + cbase;                    // the warp's first column
+      const int col0 = t.nb * bn_cols + cbase;               // the warp's first column
       const bool live = row < p.M;
       auto wait_full = [&] {
         const bool ok = mbar_wait(&tfull[acc], acc_phase, abort, p.timeout_ns, p.status);
@@ -500,8 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         auto z = [&](int i) { return __uint_as_float(zr[i / 32][i % 32]); };
         if constexpr (MODE == STATS) {
-          const int cols = p.N - col0;  // columns from here on that exist
-          if (tgt >= col0 && tgt < min(col0 + kCols, p.N)) {
+          // columns from here on that exist, in this tile
+          const int cols = min(p.N - col0, bn_cols - cbase);
+          if (tgt >= col0 && tgt < col0 + min(kCols, cols)) {
 #pragma unroll
             for (int i = 0; i < kCols; ++i)
               if (col0 + i == tgt) p.target_logit[row] = z(i);
@@ -524,7 +538,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             s0 += ex2(fmaf(z(i), kLog2e, -base));
             s1 += ex2(fmaf(z(i + 1), kLog2e, -base));
           }
-          if (live) p.part[(int64_t)(2 * t.nb + half) * p.M + row] = make_float2(mx, s0 + s1);
+          if (p.m_tiles > 1) {
+            if (live) p.part[(int64_t)(2 * t.nb + half) * p.M + row] = make_float2(mx, s0 + s1);
+          } else {
+            const float m = fmaxf(run_max, mx), m_base = m == -INFINITY ? 0.0f : m;
+            run_sum = fmaf(run_sum, ex2(run_max - m_base), (s0 + s1) * ex2(mx - m_base));
+            run_max = m;
+          }
         } else {
 #pragma unroll
           for (int c0 = 0; c0 < kCols; c0 += 32) {
@@ -552,6 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         release();
       }
     }
+    if (MODE == STATS && p.m_tiles == 1 && wrow + lane < p.M)
+      p.part[(int64_t)(2 * unit + half) * p.M + wrow + lane] = make_float2(run_max, run_sum);
   }
 
   tc_fence_before();
@@ -568,8 +590,9 @@ bool bf16_box(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
   return make_tmap(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, cols, box_rows, 64);
 }
 
+// *walkers: the CTAs, or pairs, that walk the tiles.
 template <int MODE, int CG, int BN, int NP>
-cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadParams& p, cudaStream_t s) {
+cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadParams& p, int* walkers, cudaStream_t s) {
   auto kern = head_gemm_kernel<MODE, CG, BN, NP>;
   const size_t smem = HeadSmem<CG, BN>::kBytes;
   static bool attr_set = false;  // per instantiation
@@ -591,7 +614,7 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 1 : 0;
-  int units = num_sms() / CG;
+  int units = std::min(num_sms(), 152) / CG;  // the workspace has room for the sums of that many
   if (CG == 2) {  // a persistent grid must be resident all at once: no more pairs than fit together
     static int max_pairs = 0;
     if (!max_pairs) {
@@ -600,7 +623,9 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
     }
     units = std::min(units, max_pairs);
   }
-  cfg.gridDim = dim3((unsigned)(CG * std::min<int64_t>(units, tiles)));
+  units = (int)std::min<int64_t>(units, tiles);
+  if (walkers) *walkers = units;
+  cfg.gridDim = dim3((unsigned)(CG * units));
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, b, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -612,11 +637,29 @@ int tile_rows(int64_t T) { return small_tokens(T) ? BM : 2 * BM; }
 int tile_cols(int64_t T, int planes) { return small_tokens(T) || planes == 3 ? 128 : 256; }
 
 template <int MODE>
-cudaError_t launch_mode(int T, int planes, const CUtensorMap& a, const CUtensorMap& b, const HeadParams& p, cudaStream_t s) {
+cudaError_t launch_mode(int T, int planes, const CUtensorMap& a, const CUtensorMap& b, const HeadParams& p, cudaStream_t s,
+                        int* walkers = nullptr) {
   if constexpr (MODE != DW) {
-    if (small_tokens(T)) return planes == 3 ? launch_gemm<MODE, 1, 128, 3>(a, b, p, s) : launch_gemm<MODE, 1, 128, 1>(a, b, p, s);
+    if (small_tokens(T)) {
+      if (planes == 3) return launch_gemm<MODE, 1, 128, 3>(a, b, p, walkers, s);
+      return launch_gemm<MODE, 1, MODE == STATS ? 256 : 128, 1>(a, b, p, walkers, s);
+    }
   }
-  return planes == 3 ? launch_gemm<MODE, 2, 128, 3>(a, b, p, s) : launch_gemm<MODE, 2, 256, 1>(a, b, p, s);
+  return planes == 3 ? launch_gemm<MODE, 2, 128, 3>(a, b, p, walkers, s) : launch_gemm<MODE, 2, 256, 1>(a, b, p, walkers, s);
+}
+
+// Columns of a logits tile of the forward. Up to 128 tokens, where the time is that of reading w:
+// the width, of 64 to 256, with the fewest columns in the rounds that the SMs take together
+// (32000 vocabulary rows on 152 SMs: one round of 224 instead of two of 128).
+int stats_cols(int64_t T, int64_t V, int planes) {
+  if (!small_tokens(T) || planes == 3) return tile_cols(T, planes);
+  int best = 128;
+  int64_t least = INT64_MAX;
+  for (int bn = 256; bn >= 64; bn -= 16) {
+    const int64_t cost = ceil_div(ceil_div(V, bn), num_sms()) * (bn + 4);  // a little for every tile
+    if (cost < least) least = cost, best = bn;
+  }
+  return best;
 }
 
 // Rows of A's box, and so of a stage's A: what up to 128 tokens fill of the tile. The rest of it
@@ -927,7 +970,8 @@ HeadScratch head_scratch(const moe_head_config_t& c) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  L.part = take((size_t)ceil_div(c.V, 128) * 2 * T * 8);  // (max, sum) of the halves of 128- or 256-column tiles
+  // (max, sum) of the halves of 128- or 256-column tiles; one m tile: of the CTAs, for every piece
+  L.part = take((size_t)std::max<int64_t>(ceil_div(c.V, 128), T <= 256 ? ceil_div(c.V, lay ? piece : c.V) * 152 : 0) * 2 * T * 8);
   L.target_logit = take((size_t)T * 4);
   L.x = take(lay ? (size_t)(np * T * Hp * 2) : 0);
   L.w = take(lay ? (size_t)(np * piece * Hp * 2) : 0);
@@ -947,9 +991,9 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
   auto* part = reinterpret_cast<float2*>(b + L.part);
   auto* tl = reinterpret_cast<float*>(b + L.target_logit);
   const Operands o = operands(c, L, x, w, b);
-  const int tm = tile_rows(c.T), tn = tile_cols(c.T, o.planes);
+  const int tm = tile_rows(c.T), tn = stats_cols(c.T, c.V, o.planes);
   cudaError_t e = lay_out_x(c, o, x, s);
-  int parts = 0;
+  int parts = 0, walkers = 0;
   const int64_t step = o.laid_out ? L.piece : c.V;  // w in place needs no pieces here
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += step) {
     const int rows = (int)std::min<int64_t>(step, c.V - v0);
@@ -962,13 +1006,15 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
     p.a_plane = (int)o.x_plane;
     p.b_plane = (int)o.w_plane;
     p.target = target;
+    p.bn = tn;
+    p.stages = std::min<int>(kMaxStages, HeadSmem<1, 256>::kStages * HeadSmem<1, 256>::kStageBytes / (a_box(c.T) * BK * 2 + tn * BK * 2));
     p.part = part + (int64_t)parts * c.T;
     p.target_logit = tl;
     CUtensorMap ma, mb;
     if (!bf16_box(&ma, o.x, o.x_rows, o.cols, a_box(c.T)) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
       return cudaErrorInvalidValue;
-    e = launch_mode<STATS>(c.T, o.planes, ma, mb, p, s);
-    parts += 2 * p.n_tiles;
+    e = launch_mode<STATS>(c.T, o.planes, ma, mb, p, s, &walkers);
+    parts += 2 * (p.m_tiles > 1 ? p.n_tiles : walkers);
   }
   if (e != cudaSuccess) return e;
   // the ticket lives in the head, which moe_workspace_init clears
