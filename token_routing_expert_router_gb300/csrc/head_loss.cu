@@ -82,6 +82,7 @@ struct HeadParams {
   int scalar;          // DX, DW: the output's rows do not begin on 16-byte boundaries
   int add;             // DX: added to what out holds (a later piece of the vocabulary)
   const float* factor; // DX, DW: every value is multiplied by it (the mean's 1 / count), or NULL
+  int follows;         // launched while the kernel before it in the call may still run
   DeviceStatus* status;
   uint64_t timeout_ns;
 };
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kStages = kFlex ? p.stages : S::kStages;
   const int a_stride = kFlex ? p.a_bytes : kABytes, b_stride = kFlex ? bn_cols * BK * 2 : kBBytes;
   extern __shared__ uint8_t smem_raw[];
-  let_next_begin();  // the small kernel that joins the tiles' results
+  let_next_begin();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * a_stride;
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
+  after_previous();  // nothing of memory was touched before
   const uint32_t tmem_base = *tmem_slot;
   const int total_tiles = head_units(p);
   // The loss's logits and all sums of planes are added up in runs of kRun K stages: each run has
@@ -590,7 +592,7 @@ bool bf16_box(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
   return make_tmap(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, cols, box_rows, 64);
 }
 
-// *walkers: the CTAs, or pairs, that walk the tiles.
+// *walkers: the CTAs, or pairs, that walk the tiles. p.follows: not the first launch of its call.
 template <int MODE, int CG, int BN, int NP>
 cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadParams& p, int* walkers, cudaStream_t s) {
   auto kern = head_gemm_kernel<MODE, CG, BN, NP>;
@@ -607,13 +609,15 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
+  cfg.numAttrs = 1;
   int units = std::min(num_sms(), 152) / CG;  // the workspace has room for the sums of that many
   if (CG == 2) {  // a persistent grid must be resident all at once: no more pairs than fit together
     static int max_pairs = 0;
@@ -626,6 +630,7 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
   units = (int)std::min<int64_t>(units, tiles);
   if (walkers) *walkers = units;
   cfg.gridDim = dim3((unsigned)(CG * units));
+  cfg.numAttrs = p.follows ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, b, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -686,6 +691,7 @@ HeadParams base_params(int64_t M, int64_t N, int64_t K, int tm, int tn, DeviceSt
 // dx of the tiles whose K was split: the sum of a tile's slices in order, written or added.
 template <typename T>
 __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, int tm, int tn, T* out) {
+  let_next_begin();
   after_previous();
   const int tile = p.direct + blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;  // 4 columns each
   const int nb = tile / p.m_tiles, mb = tile - nb * p.m_tiles;
@@ -722,6 +728,8 @@ __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, in
 template <typename T, int NP>
 __global__ void __launch_bounds__(256)
     planes_kernel(const T* src, int rows, int H, __nv_bfloat16* dst, int64_t plane, int Hp, int zero_to) {
+  let_next_begin();
+  after_previous();
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = Hp / 8, row = (int)(e / per), c = (int)(e % per) * 8;
   if (row >= zero_to) return;
@@ -749,11 +757,16 @@ __global__ void __launch_bounds__(256)
 }
 
 cudaError_t launch_planes(const void* src, int f32, int rows, int H, void* dst, int64_t plane, int Hp, int zero_to,
-                          cudaStream_t s) {
-  const unsigned grid = (unsigned)ceil_div((int64_t)zero_to * (Hp / 8), 256);
+                          bool follows, cudaStream_t s) {
+  const dim3 grid((unsigned)ceil_div((int64_t)zero_to * (Hp / 8), 256));
   auto* d = static_cast<__nv_bfloat16*>(dst);
-  if (f32) planes_kernel<float, 3><<<grid, 256, 0, s>>>(static_cast<const float*>(src), rows, H, d, plane, Hp, zero_to);
-  else planes_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(src), rows, H, d, plane, Hp, zero_to);
+  const auto* xf = static_cast<const float*>(src);
+  const auto* xb = static_cast<const __nv_bfloat16*>(src);
+  if (follows)
+    return f32 ? launch_after(planes_kernel<float, 3>, grid, 256, s, xf, rows, H, d, plane, Hp, zero_to)
+               : launch_after(planes_kernel<__nv_bfloat16, 1>, grid, 256, s, xb, rows, H, d, plane, Hp, zero_to);
+  if (f32) planes_kernel<float, 3><<<grid, 256, 0, s>>>(xf, rows, H, d, plane, Hp, zero_to);
+  else planes_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(xb, rows, H, d, plane, Hp, zero_to);
   return cudaGetLastError();
 }
 
@@ -860,6 +873,7 @@ __global__ void __launch_bounds__(1024)
 // dx = the sums of the pieces, from fp32 (x of one type or the other).
 template <typename T>
 __global__ void __launch_bounds__(256) store_dx_kernel(const float* sums, int64_t n, T* dx) {
+  after_previous();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   if constexpr (sizeof(T) == 4) dx[i] = sums[i];
@@ -942,12 +956,12 @@ tc::Operands operands(const moe_head_config_t& c, const HeadScratch& L, const vo
 // Lays out x, and rows [v0, v0 + rows) of w, where the products need it.
 cudaError_t lay_out_x(const moe_head_config_t& c, const tc::Operands& o, const void* x, cudaStream_t s) {
   if (!o.laid_out) return cudaSuccess;
-  return tc::launch_planes(x, is_f32(c), c.T, c.H, const_cast<void*>(o.x), o.x_plane * o.cols, (int)o.cols, (int)o.x_plane, s);
+  return tc::launch_planes(x, is_f32(c), c.T, c.H, const_cast<void*>(o.x), o.x_plane * o.cols, (int)o.cols, (int)o.x_plane, false, s);
 }
 cudaError_t lay_out_w(const moe_head_config_t& c, const tc::Operands& o, const void* w, int64_t v0, int rows, cudaStream_t s) {
   if (!o.laid_out) return cudaSuccess;
   return tc::launch_planes(static_cast<const char*>(w) + v0 * c.H * (is_f32(c) ? 4 : 2), is_f32(c), rows, c.H,
-                           const_cast<void*>(o.w), o.w_plane * o.cols, (int)o.cols, (int)align_up((size_t)rows, 64), s);
+                           const_cast<void*>(o.w), o.w_plane * o.cols, (int)o.cols, (int)align_up((size_t)rows, 64), true, s);
 }
 
 }  // namespace
@@ -1006,6 +1020,7 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
     p.a_plane = (int)o.x_plane;
     p.b_plane = (int)o.w_plane;
     p.target = target;
+    p.follows = o.laid_out || v0 > 0;
     p.bn = tn;
     p.stages = std::min<int>(kMaxStages, HeadSmem<1, 256>::kStages * HeadSmem<1, 256>::kStageBytes / (a_box(c.T) * BK * 2 + tn * BK * 2));
     p.part = part + (int64_t)parts * c.T;
@@ -1060,6 +1075,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     p.target = target;
     p.lse = lse;
     p.dloss = dloss;
+    p.follows = o.laid_out || v0 > 0;
     p.out = dl;
     p.ldo = L.ld;
     p.m_out = (int)o.dl_plane;
@@ -1074,6 +1090,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
       p.a_bytes = a_box(c.T) * BK * 2;
       p.a_plane = (int)o.dl_plane;
       p.b_plane = (int)o.w_plane;
+      p.follows = 1;
       p.direct = (int)L.split.direct;
       p.splits = L.split.splits;
       p.slices = reinterpret_cast<float*>(b + L.slices);
@@ -1098,6 +1115,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
       set_terms(&p, o.planes, o.in_planes);
       p.a_plane = (int)o.dl_plane;
       p.b_plane = (int)o.x_plane;
+      p.follows = 1;
       p.out_f32 = g32;
       p.out = static_cast<char*>(dw) + v0 * c.H * (g32 ? 4 : 2);
       p.ldo = c.H;
@@ -1111,9 +1129,8 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   const int64_t n = (int64_t)c.T * c.H;
   const unsigned grid = (unsigned)ceil_div(n, 256);
   const float* from = dx_sums;
-  if (f32) store_dx_kernel<float><<<grid, 256, 0, s>>>(from, n, static_cast<float*>(dx));
-  else store_dx_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(from, n, static_cast<__nv_bfloat16*>(dx));
-  return cudaGetLastError();
+  return f32 ? launch_after(store_dx_kernel<float>, grid, 256, s, from, n, static_cast<float*>(dx))
+             : launch_after(store_dx_kernel<__nv_bfloat16>, grid, 256, s, from, n, static_cast<__nv_bfloat16*>(dx));
 }
 
 }  // namespace moe
