@@ -651,7 +651,9 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
 // pieces: 1 in the forward, 2 in the backward, whose bookkeeping per row and thread is near half
 // of its instructions (16384 x 2048: 88 -> 80 us; the forward is better with more threads, 49
 // against 51 us). S1, S2, S4: stages of the ring (forward: of two rows each) for those rows, for
-// wider ones and for pieces of 4 bytes, as many as leave room for several CTAs on an SM.
+// wider ones and for pieces of 4 bytes: the fewest that keep a row or two in flight, so that an
+// SM holds several CTAs (backward with 4 for those rows, which leaves room for 3 CTAs instead of
+// 4: 80 against 78 us; forward with 3: 50 against 47 us).
 #define NORM_DISPATCH(FN, V1, S1, S2, S4, ...)                                                    \
   if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0) {                                            \
     const int nvec = c.H / 8;                                                                     \
@@ -684,7 +686,7 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
 
 cudaError_t launch_block_norm(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  NORM_DISPATCH(fwd, 1, 3, 3, 3, c, in, r, n, s)
+  NORM_DISPATCH(fwd, 1, 2, 2, 2, c, in, r, n, s)
 }
 
 cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
@@ -694,7 +696,7 @@ cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd
       if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)c.H * 4, s);
     return e;
   }
-  NORM_DISPATCH(bwd, 2, 4, 3, 4, c, b, part, s)
+  NORM_DISPATCH(bwd, 2, 3, 3, 4, c, b, part, s)
 }
 
 // Two sets of column sums for every row group of the largest grid: never more than one row
