@@ -422,13 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // dz or output values of the 32 columns from c0 of this warp's share on
       int tgt = -1;
       bool counts = false;
-      float lse2 = 0.0f, g = 0.0f;
+      float lse = 0.0f, g = 0.0f;
       if constexpr (MODE == STATS || MODE == DLOGITS) {
         if (live) tgt = __ldg(p.target + row);
         counts = tgt >= 0 && tgt < p.V;
         tgt = counts ? tgt - p.v0 : kNowhere;  // the target's column of this piece, or outside it
         if (MODE == DLOGITS && counts) {
-          lse2 = __ldg(p.lse + row) * kLog2e;
+          lse = __ldg(p.lse + row);
           // the gradient of the mean: its factor 1 / count is left to the two products
           g = p.dloss ? __ldg(p.dloss + row) : 1.0f;
         }
@@ -442,7 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int at = tgt - cc;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float pr = ex2(fmaf(v[i], kLog2e, -lse2)) - (i == at ? 1.0f : 0.0f);
+            // fp32 outputs follow p to its last bits; a dz that is rounded to bf16 does not
+            const float e = NP == 3 ? expf(v[i] - lse) : ex2((v[i] - lse) * kLog2e);
+            const float pr = e - (i == at ? 1.0f : 0.0f);
             v[i] = counts && i < cols ? pr * g : 0.0f;
           }
           // columns past the vocabulary are written too, as zeros: they are K rows of the next products
@@ -532,19 +534,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             m0 = fmaxf(m0, z(i));
             m1 = fmaxf(m1, z(i + 1));
           }
-          const float mx = fmaxf(m0, m1) * kLog2e;
-          const float base = mx == -INFINITY ? 0.0f : mx;
+          // z - max is exact near the maximum; z log2 e - max log2 e would carry the rounding of the
+          // second product, several U, into every term
+          const float mx = fmaxf(m0, m1), base = mx == -INFINITY ? 0.0f : mx;
           float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
           for (int i = 0; i < kCols; i += 2) {
-            s0 += ex2(fmaf(z(i), kLog2e, -base));
-            s1 += ex2(fmaf(z(i + 1), kLog2e, -base));
+            s0 += ex2((z(i) - base) * kLog2e);
+            s1 += ex2((z(i + 1) - base) * kLog2e);
           }
           if (p.m_tiles > 1) {
             if (live) p.part[(int64_t)(2 * t.nb + half) * p.M + row] = make_float2(mx, s0 + s1);
           } else {
             const float m = fmaxf(run_max, mx), m_base = m == -INFINITY ? 0.0f : m;
-            run_sum = fmaf(run_sum, ex2(run_max - m_base), (s0 + s1) * ex2(mx - m_base));
+            run_sum = fmaf(run_sum, ex2((run_max - m_base) * kLog2e), (s0 + s1) * ex2((mx - m_base) * kLog2e));
             run_max = m;
           }
         } else {
@@ -798,9 +801,9 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) m2 = fmaxf(m2, v[u].x);
       const float base = m2 == -INFINITY ? 0.0f : m2;
-      s *= exp2f(m - base);
+      s *= expf(m - base);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) s = fmaf(v[u].y, exp2f(v[u].x - base), s);
+      for (int u = 0; u < kAhead; ++u) s = fmaf(v[u].y, expf(v[u].x - base), s);
       m = m2;
     }
   }
@@ -819,11 +822,11 @@ __global__ void __launch_bounds__(1024)
     for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-    for (int u = 0; u < kLanes / 32; ++u) s = fmaf(v[u].y, exp2f(v[u].x - base), s);
+    for (int u = 0; u < kLanes / 32; ++u) s = fmaf(v[u].y, expf(v[u].x - base), s);
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (wl == 0) {
-      const float l = (m + log2f(s)) * 0.6931471805599453f;
+      const float l = m + logf(s);
       const int32_t tgt = target[tw];
       if (tgt >= V) set_status(st, MOE_ERR_DEVICE_BAD_INPUT, (int32_t)tw);
       lse[tw] = l;
