@@ -255,8 +255,7 @@ void fill(ClipList* l, const moe_grad_t* grads, int32_t count, int tile, int32_t
 template <int kThreads>
 cudaError_t clip_launches(const moe_grad_t* grads, int32_t count, float max_norm, float* norm, char* w, DeviceStatus* st,
                           cudaStream_t s) {
-  // the ticket lives in the head, which moe_workspace_init clears
-  ClipState* state = reinterpret_cast<ClipState*>(w + 256);
+  ClipState* state = reinterpret_cast<ClipState*>(w + kClipState);
   double* sums = reinterpret_cast<double*>(w + kWsHead);
   ClipList l;
   int slot = 0;

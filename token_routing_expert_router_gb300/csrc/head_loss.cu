@@ -1035,8 +1035,7 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
     parts += 2 * (p.m_tiles > 1 ? p.n_tiles : walkers);
   }
   if (e != cudaSuccess) return e;
-  // the ticket lives in the head, which moe_workspace_init clears
-  auto* ticket = reinterpret_cast<uint32_t*>(b + 320);
+  auto* ticket = reinterpret_cast<uint32_t*>(b + kHeadTicket);
   const float2* from = part;
   const float* logits = tl;
   if (c.T >= 1024)

@@ -644,23 +644,24 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
 
 }  // namespace
 
-// How a row is spread: pieces of VEC elements, at most 1024 pieces per CTA (two per thread), so
-// a cluster of 2 or 4 CTAs for wider rows. Rows of H not a multiple of 16 bytes have pieces of
-// 4 bytes (4 to 16 per thread); an odd number of bf16 channels leaves nothing for cp.async to
-// copy, and takes single elements without the ring. V1: pieces per thread of rows of up to 256
-// pieces: 1 in the forward, 2 in the backward, whose bookkeeping per row and thread is near half
-// of its instructions (16384 x 2048: 88 -> 80 us; the forward is better with more threads, 49
-// against 51 us). S1, S2, S4: stages of the ring (forward: of two rows each) for those rows, for
-// wider ones and for pieces of 4 bytes: the fewest that keep a row or two in flight, so that an
-// SM holds several CTAs (backward with 4 for those rows, which leaves room for 3 CTAs instead of
-// 4: 80 against 78 us; forward with 3: 50 against 47 us).
-#define NORM_DISPATCH(FN, V1, S1, S2, S4, ...)                                                    \
+// How a row is spread: pieces of VEC elements, at most 1024 pieces per CTA, so a cluster of 2 or
+// 4 CTAs for wider rows. Rows of H not a multiple of 16 bytes have pieces of 4 bytes (4 to 16 per
+// thread); an odd number of bf16 channels leaves nothing for cp.async to copy, and takes single
+// elements without the ring.
+// V1, V2: pieces per thread of rows of up to 256 pieces, and of bf16 rows of 513 to 1024. The
+// backward takes two, since its bookkeeping per row and thread is near half of its instructions
+// (16384 x 2048: 80 against 88 us with one; 8192 x 7168: 141 against 203). The forward takes one:
+// more threads hide its two barriers (49 against 51 us; 77 against 79).
+// S1, S2, S4: stages of the ring (forward: of two rows each) for those rows, for wider ones and
+// for pieces of 4 bytes: the fewest that keep a row or two in flight, so that an SM holds several
+// CTAs (backward with 4 instead of 3: 80 against 78 us; forward with 3 instead of 2: 50 against 47).
+#define NORM_DISPATCH(FN, V1, V2, S1, S2, S4, ...)                                                \
   if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0) {                                            \
     const int nvec = c.H / 8;                                                                     \
     if (nvec <= 32) return FN<__nv_bfloat16, 8, 1, true, 128, S1, 1>(__VA_ARGS__);                \
     if (nvec <= 256) return FN<__nv_bfloat16, 8, V1, true, 256 / V1, S1, 1>(__VA_ARGS__);         \
     if (nvec <= 512) return FN<__nv_bfloat16, 8, 2, true, 256, S2, 1>(__VA_ARGS__);               \
-    if (nvec <= 1024) return FN<__nv_bfloat16, 8, 2, true, 512, S2, 1>(__VA_ARGS__);              \
+    if (nvec <= 1024) return FN<__nv_bfloat16, 8, V2, true, 1024 / V2, S2, 1>(__VA_ARGS__);       \
     return FN<__nv_bfloat16, 8, 2, true, 512, S2, 2>(__VA_ARGS__);                                \
   }                                                                                               \
   if (c.act_dtype == MOE_DTYPE_F32 && c.H % 4 == 0) {                                             \
@@ -686,7 +687,7 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
 
 cudaError_t launch_block_norm(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  NORM_DISPATCH(fwd, 1, 2, 2, 2, c, in, r, n, s)
+  NORM_DISPATCH(fwd, 1, 1, 2, 2, 2, c, in, r, n, s)
 }
 
 cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
@@ -696,7 +697,7 @@ cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd
       if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)c.H * 4, s);
     return e;
   }
-  NORM_DISPATCH(bwd, 2, 3, 3, 4, c, b, part, s)
+  NORM_DISPATCH(bwd, 2, 2, 3, 3, 4, c, b, part, s)
 }
 
 // Two sets of column sums for every row group of the largest grid: never more than one row

@@ -11,6 +11,11 @@ namespace tc {
 int num_sms();  // of the current device (gemm_tc.cu)
 }
 
+// Words in the workspace head, which moe_workspace_init clears, away from the routing barrier's:
+// each returns to what the next call expects, whatever call shared the workspace before.
+constexpr size_t kClipState = 1024;   // grad_clip.cu's ticket and scale
+constexpr size_t kHeadTicket = 1152;  // head_loss.cu's ticket
+
 // Programmatic dependent launch inside a call: a kernel launched with launch_after may be set
 // up while the one before it in the stream still runs, and calls after_previous() before it
 // touches anything that kernel (or one before it) wrote or read; a kernel that is followed by
