@@ -203,6 +203,24 @@ def test_block_norm_backward(T, H, dt, post, nxt, gate, tgate):
         assert (z == 0).all()
 
 
+@pytest.mark.parametrize("dt", [FP, BF])
+def test_block_norm_backward_of_zero_rows_with_a_tiny_eps(dt):
+    """rho = 1e15 there: its cube does not fit fp32, and meets sums that are 0."""
+    T, H = 6, 64
+    g = gen(3)
+    zero = torch.zeros(T, H, dtype=dt, device="cuda")
+    w_post, w_next = normal(g, H, std=0.2, mean=1.0), normal(g, H, std=0.2, mean=1.0)
+    dr, dn = normal(g, T, H, dtype=dt), normal(g, T, H, dtype=dt)
+    dx, dy = poisoned(T, H, dtype=dt), poisoned(T, H, dtype=dt)
+    cfg = moe.MoENormConfig.make(T=T, H=H, act_dtype=CODE[dt], eps=1e-30, res_scale=RES)
+    r = torch.tensor(1e-30, dtype=FP).double().item() ** -0.5
+    moe.moe_block_norm_backward(cfg, zero, zero, w_post, w_next, dr, dn, dx, dy, {}, None)
+    d = dr.double() + r * dn.double() * w_next.double()
+    # rho (2 steps of rsqrt, the mean's), three products and a sum
+    for got, want in ((dx, RES * d), (dy, r * w_post.double() * d)):
+        within(got, want, (HALF[dt] + 16 * U) * want.abs() + 16 * U * r * (r if got is dy else 1))
+
+
 def test_block_norm_backward_by_differences():
     """A small central-difference check of the kernels' own forward and backward, in fp32."""
     T, H = 3, 16
@@ -351,6 +369,37 @@ def test_head_bad_target_and_large_logits():
     moe.moe_head_loss(c0, None, w, None, None, None, mean, ws)
     moe.moe_head_loss_backward(c0, None, w, None, None, None, dw, ws)
     assert not bool(mean.any()) and not bool(dw.any())
+
+
+@pytest.mark.parametrize("T,H,V,dt", [(300, 256, 1000, BF), (40, 64, 500, BF), (200, 33, 300, BF), (70, 40, 260, FP)])
+def test_head_left_out_tokens_may_hold_anything(T, H, V, dt):
+    """Padded rows of x, and their loss gradients, may be NaN or infinite: the other tokens' losses
+    and both gradients have the bits that they have with zeros there."""
+    g = gen(T)
+    x, w = normal(g, T, H, dtype=dt), normal(g, V, H, dtype=dt, std=0.2)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda").to(torch.int32)
+    target[3::4], target[T - 1] = -1, V
+    keep = (target >= 0) & (target < V)
+    cfg = moe.MoEHeadConfig.make(T=T, H=H, V=V, act_dtype=CODE[dt])
+    ws = workspace(moe.moe_head_workspace_size(cfg))
+
+    def step(fill):
+        xf, dl = x.clone(), torch.rand(T, generator=gen(5), device="cuda")
+        xf[~keep], dl[~keep] = fill, fill
+        loss, lse, mean = poisoned(T, dtype=FP), poisoned(T, dtype=FP), poisoned(2, dtype=FP)
+        moe.moe_head_loss(cfg, xf, w, target, loss, lse, mean, ws)
+        out = [loss, lse[keep], mean]
+        for d in (None, dl):
+            dx, dw, dx2 = poisoned(T, H, dtype=dt), poisoned(V, H, dtype=FP), poisoned(T, H, dtype=dt)
+            moe.moe_head_loss_backward(cfg, xf, w, target, lse, dx, dw, ws, dloss=d, mean=mean if d is None else None)
+            moe.moe_head_loss_backward(cfg, xf, w, target, lse, dx2, None, ws, dloss=d, mean=mean if d is None else None)
+            out += [dx, dw, dx2]
+        return out
+
+    want = step(0.0)
+    assert all(torch.isfinite(v).all() for v in want)
+    for fill in (float("nan"), float("inf"), -3e38):
+        assert all(torch.equal(a, b) for a, b in zip(step(fill), want))
 
 
 # ---------------------------------------------------------------------------------- embedding
@@ -534,6 +583,17 @@ def test_grad_clip_leaves_non_finite_gradients(bad):
     empty = moe.MoEGradList.from_tensors([])
     moe.moe_grad_clip(empty, 1.0, norm, ws)
     assert norm.item() == 0.0 and moe.moe_read_status(ws) == moe.MOE_OK
+
+
+def test_grad_clip_of_a_norm_beyond_fp32():
+    """Finite elements, a norm that fp32 does not hold: as any norm that is not finite."""
+    v = torch.full((1000,), 3e38, device="cuda")
+    norm = poisoned(1, dtype=FP)
+    lst = moe.MoEGradList.from_tensors([v])
+    ws = workspace(moe.moe_grad_clip_workspace_size(lst))
+    moe.moe_grad_clip(lst, 1.0, norm, ws)
+    assert norm.item() == math.inf and bool((v == 3e38).all())
+    assert moe.moe_read_status(ws) == moe.MOE_ERR_DEVICE_BAD_INPUT
 
 
 # ---------------------------------------------------------------------------------- streams, graphs

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads)
   all = block_sum(all);
   if (threadIdx.x == 0) {
     const double nrm = sqrt(all);
-    const bool fine = all < (double)INFINITY;  // false for NaN too
+    const bool fine = (float)nrm < INFINITY;  // false for NaN too, and for a norm beyond fp32
     if (!fine) set_status(st, MOE_ERR_DEVICE_BAD_INPUT, -1);
     *norm = (float)nrm;
     state->scale = fine && max_norm >= 0.0f && nrm > (double)max_norm ? (float)((double)max_norm / nrm) : 1.0f;

@@ -727,10 +727,13 @@ __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, in
 }
 
 // The planes of rows [0, rows) of src [., H] in dst [planes][rows_pad][Hp] bf16: zeros past H and
-// from `rows` to `zero_to` (the K stages of the products read that far). Eight columns a thread.
+// from `rows` to `zero_to` (the K stages of the products read that far), and, given targets, in the
+// rows of tokens that do not count: their dz is zero, but zero times a NaN or infinity in a padded
+// row of x would reach every row of dw. Eight columns a thread.
 template <typename T, int NP>
 __global__ void __launch_bounds__(256)
-    planes_kernel(const T* src, int rows, int H, __nv_bfloat16* dst, int64_t plane, int Hp, int zero_to) {
+    planes_kernel(const T* src, int rows, int H, const int32_t* target, int V, __nv_bfloat16* dst, int64_t plane, int Hp,
+                  int zero_to) {
   let_next_begin();
   after_previous();
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -738,13 +741,23 @@ __global__ void __launch_bounds__(256)
   if (row >= zero_to) return;
   float v[8];
   const bool whole = H % 8 == 0;  // a thread's columns are all there, and aligned
-  if (row >= rows) {
+  bool there = row < rows;
+  if (there && target) {
+    const int32_t t = __ldg(target + row);
+    there = t >= 0 && t < V;
+  }
+  if (!there) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
   } else if (whole && sizeof(T) == 4) {
     const float4* q = reinterpret_cast<const float4*>(src + (int64_t)row * H + c);
     const float4 a = __ldg(q), b = __ldg(q + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else if (whole) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * H + c));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c + i < H ? static_cast<float>(src[(int64_t)row * H + c + i]) : 0.0f;
@@ -759,17 +772,17 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-cudaError_t launch_planes(const void* src, int f32, int rows, int H, void* dst, int64_t plane, int Hp, int zero_to,
-                          bool follows, cudaStream_t s) {
+cudaError_t launch_planes(const void* src, int f32, int rows, int H, const int32_t* target, int V, void* dst,
+                          int64_t plane, int Hp, int zero_to, bool follows, cudaStream_t s) {
   const dim3 grid((unsigned)ceil_div((int64_t)zero_to * (Hp / 8), 256));
   auto* d = static_cast<__nv_bfloat16*>(dst);
   const auto* xf = static_cast<const float*>(src);
   const auto* xb = static_cast<const __nv_bfloat16*>(src);
   if (follows)
-    return f32 ? launch_after(planes_kernel<float, 3>, grid, 256, s, xf, rows, H, d, plane, Hp, zero_to)
-               : launch_after(planes_kernel<__nv_bfloat16, 1>, grid, 256, s, xb, rows, H, d, plane, Hp, zero_to);
-  if (f32) planes_kernel<float, 3><<<grid, 256, 0, s>>>(xf, rows, H, d, plane, Hp, zero_to);
-  else planes_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(xb, rows, H, d, plane, Hp, zero_to);
+    return f32 ? launch_after(planes_kernel<float, 3>, grid, 256, s, xf, rows, H, target, V, d, plane, Hp, zero_to)
+               : launch_after(planes_kernel<__nv_bfloat16, 1>, grid, 256, s, xb, rows, H, target, V, d, plane, Hp, zero_to);
+  if (f32) planes_kernel<float, 3><<<grid, 256, 0, s>>>(xf, rows, H, target, V, d, plane, Hp, zero_to);
+  else planes_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(xb, rows, H, target, V, d, plane, Hp, zero_to);
   return cudaGetLastError();
 }
 
@@ -956,14 +969,16 @@ tc::Operands operands(const moe_head_config_t& c, const HeadScratch& L, const vo
   return o;
 }
 
-// Lays out x, and rows [v0, v0 + rows) of w, where the products need it.
-cudaError_t lay_out_x(const moe_head_config_t& c, const tc::Operands& o, const void* x, cudaStream_t s) {
-  if (!o.laid_out) return cudaSuccess;
-  return tc::launch_planes(x, is_f32(c), c.T, c.H, const_cast<void*>(o.x), o.x_plane * o.cols, (int)o.cols, (int)o.x_plane, false, s);
+// Lays out x (given targets, the rows that count), and rows [v0, v0 + rows) of w, where the
+// products need it.
+cudaError_t lay_out_x(const moe_head_config_t& c, const tc::Operands& o, const void* x, const int32_t* target, cudaStream_t s) {
+  if (o.x == x) return cudaSuccess;
+  return tc::launch_planes(x, is_f32(c), c.T, c.H, target, c.V, const_cast<void*>(o.x), o.x_plane * o.cols, (int)o.cols,
+                           (int)o.x_plane, false, s);
 }
 cudaError_t lay_out_w(const moe_head_config_t& c, const tc::Operands& o, const void* w, int64_t v0, int rows, cudaStream_t s) {
   if (!o.laid_out) return cudaSuccess;
-  return tc::launch_planes(static_cast<const char*>(w) + v0 * c.H * (is_f32(c) ? 4 : 2), is_f32(c), rows, c.H,
+  return tc::launch_planes(static_cast<const char*>(w) + v0 * c.H * (is_f32(c) ? 4 : 2), is_f32(c), rows, c.H, nullptr, 0,
                            const_cast<void*>(o.w), o.w_plane * o.cols, (int)o.cols, (int)align_up((size_t)rows, 64), true, s);
 }
 
@@ -990,7 +1005,7 @@ HeadScratch head_scratch(const moe_head_config_t& c) {
   // (max, sum) of the halves of 128- or 256-column tiles; one m tile: of the CTAs, for every piece
   L.part = take((size_t)std::max<int64_t>(ceil_div(c.V, 128), T <= 256 ? ceil_div(c.V, lay ? piece : c.V) * 152 : 0) * 2 * T * 8);
   L.target_logit = take((size_t)T * 4);
-  L.x = take(lay ? (size_t)(np * T * Hp * 2) : 0);
+  L.x = take((size_t)(np * T * Hp * 2));  // in place: of the rows that count, for dw
   L.w = take(lay ? (size_t)(np * piece * Hp * 2) : 0);
   L.dlogits = take((size_t)(np * T * piece * 2));
   L.dx = take(piece >= c.V ? 0 : (size_t)T * c.H * 4);
@@ -1009,7 +1024,7 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
   auto* tl = reinterpret_cast<float*>(b + L.target_logit);
   const Operands o = operands(c, L, x, w, b);
   const int tm = tile_rows(c.T), tn = stats_cols(c.T, c.V, o.planes);
-  cudaError_t e = lay_out_x(c, o, x, s);
+  cudaError_t e = lay_out_x(c, o, x, nullptr, s);
   int parts = 0, walkers = 0;
   const int64_t step = o.laid_out ? L.piece : c.V;  // w in place needs no pieces here
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += step) {
@@ -1054,12 +1069,13 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   const HeadScratch L = head_scratch(c);
   const bool one = L.piece >= c.V;  // dx needs no sum over pieces
   char* b = static_cast<char*>(ws);
-  const Operands o = operands(c, L, x, w, b);
+  Operands o = operands(c, L, x, w, b);
+  if (dw) o.x = b + L.x;
   const int tm = tile_rows(c.T), tn = tile_cols(c.T, o.planes);
   void* dl = b + L.dlogits;
   float* dx_sums = reinterpret_cast<float*>(b + L.dx);
   const float* factor = mean ? mean + 1 : nullptr;
-  cudaError_t e = lay_out_x(c, o, x, s);
+  cudaError_t e = lay_out_x(c, o, x, target, s);
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {
     const int rows = (int)std::min<int64_t>(L.piece, c.V - v0);
     if ((e = lay_out_w(c, o, w, v0, rows, s)) != cudaSuccess) break;
@@ -1077,7 +1093,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     p.target = target;
     p.lse = lse;
     p.dloss = dloss;
-    p.follows = o.laid_out || v0 > 0;
+    p.follows = o.x != x || v0 > 0;
     p.out = dl;
     p.ldo = L.ld;
     p.m_out = (int)o.dl_plane;

@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 128 ? 4 : MAXT <= 256 || (MAXT <
     }
     if (it > 0 && row < T_) {
       const float rho = b.w_next ? inv_rms(tot[0], inv_h, eps) : 0.0f;
-      const float k = rho * rho * rho * tot[1] * inv_h;
+      const float k = rho * (rho * (rho * tot[1]) * inv_h);  // rho^3 alone may overflow where the sum is 0
       const float rho_y = b.w_post ? inv_rms(tot[2], inv_h, eps) : 1.0f;
       const float g = b.token_gate ? __ldg(b.token_gate + row) : 1.0f;
       const float q = fmaf(rho, tot[4], fmaf(-k, tot[5], tot[3]));
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 128 ? 4 : MAXT <= 256 || (MAXT <
       splat(rho, &e_rho);
       splat(-k, &e_k);
       splat(g * rho_y, &e_g);
-      splat(b.w_post ? -g * rho_y * rho_y * rho_y * q * inv_h : 0.0f, &e_ky);
+      splat(b.w_post ? -g * rho_y * (rho_y * (rho_y * q) * inv_h) : 0.0f, &e_ky);
       splat(res_scale, &e_res);
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
