@@ -464,6 +464,23 @@ def test_embed_and_gradient(T, H, V, dt, gdt, kind):
     assert moe.moe_read_status(ws) == moe.MOE_OK
 
 
+@pytest.mark.parametrize("T,V,share", [(32768, 700, 0.0), (32769, 700, 0.3), (70001, 100, 0.5), (131072, 50257, 0.02),
+                                       (262145, 3, 0.1), (600000, 2000000, 0.01), (2200000, 40, 0.9), (100000, 9, 1.0)])
+def test_embed_gradient_of_long_sequences(T, V, share):
+    """Sorted in several steps, with `share` of the tokens left out. Small whole numbers: every sum is exact."""
+    H, g = 2, gen(T)
+    token = torch.randint(0, V, (T,), generator=g, device="cuda").to(torch.int32)
+    token[torch.rand(T, generator=g, device="cuda") < share] = -1
+    dout = torch.randint(-2, 3, (T, H), generator=g, device="cuda").to(BF)
+    cfg = moe.MoEEmbedConfig.make(T=T, H=H, V=V)
+    ws = workspace(moe.moe_embed_workspace_size(cfg))
+    dtable = poisoned(V, H, dtype=FP)
+    moe.moe_embed_backward(cfg, token, dout, dtable, ws)
+    keep = token >= 0
+    want = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, token[keep].long(), dout[keep].double())
+    assert torch.equal(dtable.double(), want)
+
+
 @pytest.mark.parametrize("T", [50, 5000])
 def test_embed_bad_tokens(T):
     H, V = 64, 100

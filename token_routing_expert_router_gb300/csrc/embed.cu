@@ -3,10 +3,12 @@
 //   dtable[v] = scale * sum over t with token[t] = v of dout[t], positions ascending
 //
 // The gradient has no atomics, so its bits do not depend on timing. The positions are sorted
-// by (token, position), in two launches: blocks sort 2048 tokens each in shared memory as one
-// 32-bit key (token << 11 | position in the block), then every element finds its place as its
-// own index plus, by binary search, the number of smaller keys in each other block. Work grows
-// with T^2 / 2048 there; at 131072 tokens that is 64 searches of 11 steps an element.
+// by (token, position): blocks sort 2048 tokens each in shared memory as one 32-bit key
+// (token << 11 | position in the block), then every element of a run of blocks finds its place as
+// its own index plus, by binary search, the number of smaller keys in each other block, and runs
+// of those are merged eight at a time in the same way. (Every block against every other in one
+// launch is quadratic: the whole gradient of 131072 tokens of 8 channels took 131 us, of 4 million
+// 31.9 ms.)
 // The sums then go over equal chunks of the sorted positions, whatever the tokens' frequencies:
 // a token whose run lies inside a chunk is written at once, one that crosses chunks leaves one
 // partial sum per chunk, and join_kernel adds those in order. Rows of tokens that do not occur
@@ -206,15 +208,18 @@ __global__ void __launch_bounds__(kSortThreads)
   if (threadIdx.x == 0) *(single ? count : block_count + blockIdx.x) = counted;
 }
 
-// The place of every key among all blocks: the number of smaller keys in its own block (its
-// index there), of keys of the same or a smaller token in the blocks before, and of a smaller
-// token in those after. One thread per key; the blocks' keys pass through shared memory four
-// blocks at a time (searched in L2 the 11 dependent steps took 10.6 us for 16384 tokens). Block
-// 0 also adds up the blocks' counts.
+// The place of every key among the run_blocks blocks of its run: its index in its own block, plus
+// the number of keys of the same or a smaller token in the blocks before, and of a smaller token
+// in those after. One thread per key; the blocks' keys pass through shared memory four blocks at a
+// time (searched in L2 the 11 dependent steps took 10.6 us for 16384 tokens). Block 0 also adds up
+// the blocks' counts. With more than one run the tokens that do not count are placed too, last.
+// Up to 32 blocks are one run; more are runs of 16 (the whole gradient of 65536 tokens of 8
+// channels: 82 us, and 87 with two runs to merge; of 131072: 119 with runs of 32, 108 with 16).
+int run_blocks_of(int blocks) { return blocks <= 32 ? 32 : 16; }
 constexpr int kRankBlocks = 4;
 __global__ void __launch_bounds__(256)
-    rank_kernel(const uint32_t* keys, const int32_t* block_count, int blocks, int32_t* stoken, int32_t* spos,
-                int32_t* count) {
+    rank_kernel(const uint32_t* keys, const int32_t* block_count, int blocks, int run_blocks, int32_t* stoken,
+                int32_t* spos, int32_t* count) {
   __shared__ __align__(16) uint32_t sk[kRankBlocks][kSortBlock];
   let_next_begin();
   after_previous();
@@ -230,10 +235,12 @@ __global__ void __launch_bounds__(256)
   }
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int own = (int)(i / kSortBlock);
+  const int run0 = own / run_blocks * run_blocks, run1 = min(blocks, run0 + run_blocks);
   const uint32_t key = __ldg(keys + i), token = key >> kPosBits;
-  int rank = 0;
-  for (int b0 = 0; b0 < blocks; b0 += kRankBlocks) {
-    const int here = min(kRankBlocks, blocks - b0);
+  const uint32_t own_bound = key == kNoKey ? 0 : key;
+  int rank = run0 * kSortBlock;
+  for (int b0 = run0; b0 < run1; b0 += kRankBlocks) {
+    const int here = min(kRankBlocks, run1 - b0);
     const uint4* src = reinterpret_cast<const uint4*>(keys + (int64_t)b0 * kSortBlock);
     __syncthreads();
 #pragma unroll
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int u = 0; u < kRankBlocks; ++u) {
       const int b = b0 + u;
-      bound[u] = u >= here ? 0u : b == own ? key : (b < own ? token + 1 : token) << kPosBits;
+      bound[u] = u >= here ? 0u : b == own ? own_bound : (b < own ? token + 1 : token) << kPosBits;
       at[u] = 0;
     }
 #pragma unroll
@@ -261,9 +268,44 @@ __global__ void __launch_bounds__(256)
       rank += at[u];
     }
   }
-  if (key == kNoKey) return;
+  if (key == kNoKey) {
+    if (blocks <= run_blocks) return;
+    // the bounds of the blocks before wrapped to 0: all of those, and the places before it in its own
+    rank += (own - run0) * kSortBlock + (int)(i % kSortBlock);
+  }
   stoken[rank] = (int32_t)token;
   spos[rank] = own * kSortBlock + (int)(key & (kSortBlock - 1));
+}
+
+// Merges kMerge sorted runs of `run` places (a power of two) into one, of [0, n): the place of an
+// element is its index in its own run plus the number of the same or smaller tokens in the runs
+// before and of smaller ones in those after. The tokens are in L2, and a warp's 32 neighbours walk
+// nearly the same way through them.
+constexpr int kMerge = 8;
+__global__ void __launch_bounds__(256)
+    merge_kernel(const int32_t* token, const int32_t* pos, int n, int run, int32_t* token_out, int32_t* pos_out) {
+  let_next_begin();
+  after_previous();
+  const int i = blockIdx.x * 256 + threadIdx.x;  // n is a multiple of 256
+  const int64_t base = (int64_t)i / ((int64_t)run * kMerge) * ((int64_t)run * kMerge);
+  const int own = (int)((i - base) / run);
+  const int32_t v = __ldg(token + i);
+  int at[kMerge];  // places of the run with a token below the bound
+#pragma unroll
+  for (int u = 0; u < kMerge; ++u) at[u] = 0;
+  for (int s = run; s > 0; s >>= 1)
+#pragma unroll
+    for (int u = 0; u < kMerge; ++u) {
+      const int64_t first = base + (int64_t)u * run;
+      if (u != own && at[u] + s <= run && first + at[u] + s <= n &&
+          __ldg(token + first + at[u] + s - 1) < v + (u < own ? 1 : 0))
+        at[u] += s;
+    }
+  int64_t rank = base + (i - base) % run;
+#pragma unroll
+  for (int u = 0; u < kMerge; ++u) rank += at[u];
+  token_out[rank] = v;
+  pos_out[rank] = __ldg(pos + i);
 }
 
 struct EmbedBwd {
@@ -458,6 +500,7 @@ EmbedScratch embed_scratch(const moe_embed_config_t& c) {
   L.keys = take(T * 4);
   L.stoken = take(T * 4);
   L.spos = take(T * 4);
+  L.mpos = take(T > (size_t)kSortBlock * run_blocks_of((int)(T / kSortBlock)) ? T * 4 : 0);
   L.part = take((size_t)ceil_div(c.T, chunk_of(c.T)) * 2 * c.H * 4);
   L.total = o;
   return L;
@@ -498,7 +541,15 @@ cudaError_t launch_embed_backward(const moe_embed_config_t& c, const int32_t* to
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (blocks > 1) {
-    e = launch_after(rank_kernel, blocks * (kSortBlock / 256), 256, s, keys, bcount, blocks, stoken, spos, count);
+    const int n = blocks * kSortBlock;
+    e = launch_after(rank_kernel, n / 256, 256, s, keys, bcount, blocks, run_blocks_of(blocks), stoken, spos, count);
+    // then from one pair of arrays to the other; the keys are not needed any more
+    auto *token2 = reinterpret_cast<int32_t*>(keys), *pos2 = reinterpret_cast<int32_t*>(w + L.mpos);
+    for (int64_t run = kSortBlock * run_blocks_of(blocks); run < n && e == cudaSuccess; run *= kMerge) {
+      e = launch_after(merge_kernel, n / 256, 256, s, stoken, spos, n, (int)run, token2, pos2);
+      std::swap(stoken, token2);
+      std::swap(spos, pos2);
+    }
     if (e != cudaSuccess) return e;
   }
   EmbedBwd p{stoken, spos, count, dout, dtable, reinterpret_cast<float*>(w + L.part)};

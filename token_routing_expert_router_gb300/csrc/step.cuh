@@ -57,7 +57,7 @@ cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd
 
 // ---- token embedding
 struct EmbedScratch {  // workspace offsets, after the status head
-  size_t count, block_count, keys, stoken, spos, part, total;
+  size_t count, block_count, keys, stoken, spos, mpos, part, total;
 };
 constexpr int kEmbedMaxV = (1 << 21) - 1;  // a token and its place in a block of 2048 share 32 bits
 EmbedScratch embed_scratch(const moe_embed_config_t& c);
