@@ -537,8 +537,8 @@ typedef struct {
 /* Softmax cross entropy of x [T, H] against the vocabulary rows w [V, H], without keeping the
  * logits z = x w^T (accumulated in fp32):
  *     lse[t] = log sum_v exp z[t,v];   loss[t] = lse[t] - z[t, target[t]]
- * A negative target is left out: its loss is 0 and it has no gradient (its lse is still
- * given). A target >= V sets MOE_ERR_DEVICE_BAD_INPUT and is left out too. mean (NULL to skip):
+ * A negative target is left out: its loss is 0, it has no gradient, and its row of x may hold
+ * anything (its lse is still given). A target >= V sets MOE_ERR_DEVICE_BAD_INPUT and is left out too. mean (NULL to skip):
  * two floats, the mean loss of the tokens that count and 1 / their number (0, 0 if none).
  * target [T] int32; loss, lse [T] fp32. The products run on the tensor cores: bf16 as it is,
  * fp32 as three bf16 planes per operand and the six products of planes above 2^-24 of the

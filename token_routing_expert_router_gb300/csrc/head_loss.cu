@@ -729,7 +729,9 @@ __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, in
 // The planes of rows [0, rows) of src [., H] in dst [planes][rows_pad][Hp] bf16: zeros past H and
 // from `rows` to `zero_to` (the K stages of the products read that far), and, given targets, in the
 // rows of tokens that do not count: their dz is zero, but zero times a NaN or infinity in a padded
-// row of x would reach every row of dw. Eight columns a thread.
+// row of x would reach every row of dw. (x is copied for that alone where it could be read in place:
+// 4096 x 4096 x 32000 forward and backward 2569 us, 2583 without the copy; 1500 x 2048 x 50257 743
+// and 787.) Eight columns a thread.
 template <typename T, int NP>
 __global__ void __launch_bounds__(256)
     planes_kernel(const T* src, int rows, int H, const int32_t* target, int V, __nv_bfloat16* dst, int64_t plane, int Hp,
