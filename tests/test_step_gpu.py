@@ -402,6 +402,50 @@ def test_head_left_out_tokens_may_hold_anything(T, H, V, dt):
         assert all(torch.equal(a, b) for a, b in zip(step(fill), want))
 
 
+@pytest.mark.parametrize("T,H,V,dt,share", [(1500, 64, 300, BF, 0.6), (700, 40, 260, FP, 0.9), (130, 136, 5000, BF, 0.99),
+                                           (300, 33, 700, BF, 1.0), (100, 64, 4000, BF, 1.0), (90000, 8, 40, BF, 0.5),
+                                           (70001, 16, 24, FP, 0.2)])
+def test_head_gradients_of_the_tokens_that_count(T, H, V, dt, share):
+    """Left-out tokens cost nothing and change nothing: the gradients have the bits of a call with
+    only the others (in the same pieces), at their rows of dx, zeros at the rest."""
+    g = gen(T)
+    x, w = normal(g, T, H, dtype=dt), normal(g, V, H, dtype=dt, std=0.2)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda").to(torch.int32)
+    target[torch.rand(T, generator=g, device="cuda") < share] = -1
+    keep = target >= 0
+    n = int(keep.sum())
+    dl = torch.rand(T, generator=g, device="cuda")
+
+    def step(x, target, dl):
+        T = x.shape[0]
+        cfg = moe.MoEHeadConfig.make(T=T, H=H, V=V, act_dtype=CODE[dt], piece=512)
+        ws = workspace(moe.moe_head_workspace_size(cfg))
+        loss, lse = poisoned(T, dtype=FP), poisoned(T, dtype=FP)
+        dx, dw = poisoned(T, H, dtype=dt), poisoned(V, H, dtype=FP)
+        moe.moe_head_loss(cfg, x, w, target, loss, lse, None, ws)
+        moe.moe_head_loss_backward(cfg, x, w, target, lse, dx, dw, ws, dloss=dl)
+        return lse, dx, dw
+
+    lse, dx, dw = step(x, target, dl)
+    assert not bool(dx[~keep].any())
+    if n == 0:
+        assert not bool(dw.any())
+        return
+    lse2, dx2, dw2 = step(x[keep], target[keep], dl[keep])
+    if n > 128 or T <= 128:  # up to 128 tokens the tiles are others
+        assert torch.equal(lse[keep], lse2) and torch.equal(dx[keep], dx2) and torch.equal(dw, dw2)
+    # and against the formula
+    X, W = x[keep].double(), w.double()
+    z = X @ W.t()
+    D = (torch.exp(z - lse2.double()[:, None]) - torch.zeros_like(z).scatter_(1, target[keep].long()[:, None], 1.0)) * dl[keep].double()[:, None]
+    tc = HALF[BF] if dt == BF and H % 8 == 0 else 0.0
+    # z within a truncated step per product, the exponent's own rounding, dz in bf16
+    lost = (2 * U * H * (X.abs() @ W.abs().t()) + 64 * U * (1 + z.abs())) * dl[keep].double()[:, None] + (tc + 8 * U) * D.abs() * 1.01
+    for got, want, l, k in ((dx[keep], D @ W, lost @ W.abs(), V), (dw, D.t() @ X, lost.t() @ X.abs(), n)):
+        mag = (D.abs() @ W.abs()) if k == V else (D.abs().t() @ X.abs())
+        within(got, want, l + 2 * U * (k + 64) * mag + HALF[got.dtype] * (want.abs() + l) + 1e-37)
+
+
 # ---------------------------------------------------------------------------------- embedding
 def tokens_of(kind, T, V, g):
     if kind == "uniform":

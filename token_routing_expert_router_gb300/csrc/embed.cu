@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(256)
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int own = (int)(i / kSortBlock);
   const int run0 = own / run_blocks * run_blocks, run1 = min(blocks, run0 + run_blocks);
-  const uint32_t key = __ldg(keys + i), token = key >> kPosBits;
+  const uint32_t key = keys[i], token = key >> kPosBits;
   const uint32_t own_bound = key == kNoKey ? 0 : key;
   int rank = run0 * kSortBlock;
   for (int b0 = run0; b0 < run1; b0 += kRankBlocks) {
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int j = 0; j < kRankBlocks * kSortBlock / 4 / 256; ++j) {
       const int at = threadIdx.x + j * 256;
-      if (at < here * (kSortBlock / 4)) reinterpret_cast<uint4*>(sk)[at] = __ldg(src + at);
+      if (at < here * (kSortBlock / 4)) reinterpret_cast<uint4*>(sk)[at] = src[at];
     }
     __syncthreads();
     int at[kRankBlocks];  // number of keys below the bound
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(256)
   const int i = blockIdx.x * 256 + threadIdx.x;  // n is a multiple of 256
   const int64_t base = (int64_t)i / ((int64_t)run * kMerge) * ((int64_t)run * kMerge);
   const int own = (int)((i - base) / run);
-  const int32_t v = __ldg(token + i);
+  const int32_t v = token[i];
   int at[kMerge];  // places of the run with a token below the bound
 #pragma unroll
   for (int u = 0; u < kMerge; ++u) at[u] = 0;
@@ -299,14 +299,14 @@ __global__ void __launch_bounds__(256)
     for (int u = 0; u < kMerge; ++u) {
       const int64_t first = base + (int64_t)u * run;
       if (u != own && at[u] + s <= run && first + at[u] + s <= n &&
-          __ldg(token + first + at[u] + s - 1) < v + (u < own ? 1 : 0))
+          token[first + at[u] + s - 1] < v + (u < own ? 1 : 0))
         at[u] += s;
     }
   int64_t rank = base + (i - base) % run;
 #pragma unroll
   for (int u = 0; u < kMerge; ++u) rank += at[u];
   token_out[rank] = v;
-  pos_out[rank] = __ldg(pos + i);
+  pos_out[rank] = pos[i];
 }
 
 struct EmbedBwd {
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedBwd p) {
     int lo = -1, hi = n;  // the first place with a token >= v0 is in (lo, hi]
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, at = lo + (int)(threadIdx.x % 32 + 1) * step;
-      const bool less = at < hi && __ldg(p.stoken + at) < v0;
+      const bool less = at < hi && p.stoken[at] < v0;
       const int k = __popc(__ballot_sync(0xffffffffu, less));  // sorted: the places below v0 are the first k
       hi = min(hi, lo + (k + 1) * step);
       lo += k * step;
@@ -436,14 +436,14 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedBwd p) {
   const int n = *p.count;
   const int64_t e = ((int64_t)chunk + 1) * p.chunk, s = e - p.chunk;  // the chunk's places [s, e)
   if (e >= n) return;
-  const int32_t v = __ldg(p.stoken + e - 1);
-  const int32_t next = __ldg(p.stoken + e), at_s = __ldg(p.stoken + s), before = s > 0 ? __ldg(p.stoken + s - 1) : -1;
+  const int32_t v = p.stoken[e - 1];
+  const int32_t next = p.stoken[e], at_s = p.stoken[s], before = s > 0 ? p.stoken[s - 1] : -1;
   if (next != v || (at_s == v && before == v)) return;  // it ends here, or began in an earlier chunk
   // the chunk of the run's last place: the 32 lanes try a place each, 32 times closer per step
   int64_t lo = e, hi = n;  // place lo belongs to the run, place hi does not
   while (hi - lo > 1) {
     const int64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    const bool in = at < hi && __ldg(p.stoken + at) == v;
+    const bool in = at < hi && p.stoken[at] == v;
     const int k = __popc(__ballot_sync(0xffffffffu, in));  // sorted: the places in the run are the first k
     const int64_t nhi = lo + (int64_t)(k + 1) * step;
     lo += k * step;

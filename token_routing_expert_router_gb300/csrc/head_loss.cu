@@ -6,7 +6,8 @@
 // maximum and the sum of exponentials against it, and the target's logit; join_kernel puts the
 // halves together. Backward: piece after piece of the vocabulary, the GEMM is run again and its
 // epilogue turns the logits into dz (bf16, the operand of the next products), then
-// dx += dz w_piece and dw_piece = dz^T x. Memory beside the inputs and outputs: one piece of dz
+// dx += dz w_piece and dw_piece = dz^T x; all of it over the tokens that count alone, which a first
+// kernel puts one after the other. Memory beside the inputs and outputs: one piece of dz
 // and 16 bytes per token and tile.
 //
 // All products run on the tensor cores (tcgen05): warp 0 feeds a ring of shared-memory stages
@@ -47,16 +48,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRun = 16;  // K stages (of 64 elements) added by the tensor core in one go
 
 constexpr int kMaxStages = 12;  // of a ring whose stages are sized at run time
+constexpr int kMaxSplits = 32;  // of the K of a tile of dx (a lane of a warp tries each)
 constexpr int kNowhere = -(1 << 30);  // no column: far below the first of any tile
 
 enum Mode { STATS = 0, DLOGITS = 1, DX = 2, DW = 3 };
 
+// What the backward's first kernel finds: the tokens that count, and how the tiles of dx are split.
+struct HeadPlan {
+  int rows;    // tokens that count: rows of x's copy, of dz, and of dx before they go to their places
+  int direct;  // DX: the first `direct` tiles are whole; the K of each further one is split over
+  int splits;  //   `splits` units, which write fp32 tiles to `slices`
+};
+
 struct HeadParams {
   int M, N;            // rows and columns of the product that exist
   int m_tiles, n_tiles, kblocks;
-  int direct;          // DX: the first `direct` tiles are whole; the K of each further one is
-  int splits;          //   split over `splits` units, which write fp32 tiles to `slices`
-  float* slices;       //   [tile - direct][split][TM][BN]
+  const HeadPlan* plan;  // the backward's: its rows stand for M (DLOGITS, DX) or K (DW)
+  const int32_t* index;  // DLOGITS, DX: the token of each row (NULL: its number)
+  float* slices;       // DX: of split tiles, [tile - direct][split][TM][BN]
   int v0;              // first vocabulary row of the piece
   int w_row0;          // its row in the map of w (0 where the piece was laid out by itself)
   int V;
@@ -76,7 +85,6 @@ struct HeadParams {
   // outputs of the other modes, and their row length in elements
   void* out;
   int64_t ldo;
-  int m_out;           // DLOGITS: rows that are stored (those past M as zeros)
   int64_t out_plane;   // DLOGITS: elements from one plane of dz to the next
   int out_f32;         // DX, DW: fp32 output (else bf16)
   int scalar;          // DX, DW: the output's rows do not begin on 16-byte boundaries
@@ -131,9 +139,10 @@ __device__ __forceinline__ void stage_f32(uint8_t* stage, int lane, const float*
                                            __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
 }
 
-// flush_rows_64B with a column bound: the 16-byte pieces c >= pieces are left out.
-__device__ __forceinline__ void flush_edge(uint8_t* stage, int lane, uint8_t* base, int64_t stride, int live, int pieces,
-                                           bool add) {
+// flush_rows_64B from row row0 of base on, with a column bound: the 16-byte pieces c >= pieces are
+// left out. at (or NULL): where the rows go instead.
+__device__ __forceinline__ void flush_edge(uint8_t* stage, int lane, uint8_t* base, int64_t stride, int row0,
+                                           const int32_t* at, int live, int pieces, bool add) {
   __syncwarp();
   const int c = lane & 3;
 #pragma unroll
@@ -141,7 +150,7 @@ __device__ __forceinline__ void flush_edge(uint8_t* stage, int lane, uint8_t* ba
     const int row = 8 * j + (lane >> 2);
     uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + 16 * (c ^ ((row >> 1) & 3)));
     if (row < live && c < pieces) {
-      uint4* dst = reinterpret_cast<uint4*>(base + row * stride + 16 * c);
+      uint4* dst = reinterpret_cast<uint4*>(base + (at ? at[row] : row0 + row) * stride + 16 * c);
       if (add) {
         const uint4 o = *dst;
         v = make_uint4(__float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x)),
@@ -157,8 +166,8 @@ __device__ __forceinline__ void flush_edge(uint8_t* stage, int lane, uint8_t* ba
 
 // The same for rows that do not begin on 16-byte boundaries: element by element, cols of them.
 template <typename T>
-__device__ __forceinline__ void flush_scalar(const uint8_t* stage, int lane, T* base, int64_t ldo, int live, int cols,
-                                             bool add) {
+__device__ __forceinline__ void flush_scalar(const uint8_t* stage, int lane, T* base, int64_t ldo, int row0,
+                                             const int32_t* at, int live, int cols, bool add) {
   __syncwarp();
   constexpr int kPer = 64 / sizeof(T);
 #pragma unroll 4
@@ -166,12 +175,30 @@ __device__ __forceinline__ void flush_scalar(const uint8_t* stage, int lane, T* 
     const int e = lane + 32 * j, row = e / kPer, col = e % kPer, c = col * (int)sizeof(T) / 16;
     const T v = *reinterpret_cast<const T*>(stage + row * 64 + 16 * (c ^ ((row >> 1) & 3)) + col * sizeof(T) % 16);
     if (row < live && col < cols) {
-      T* dst = base + row * ldo + col;
+      T* dst = base + (at ? at[row] : row0 + row) * ldo + col;
       if constexpr (sizeof(T) == 4) *dst = add ? *dst + v : v;
       else *dst = v;
     }
   }
   __syncwarp();
+}
+
+// The product as this launch finds it (with a plan, known on the device only).
+struct HeadShape {
+  int M, m_tiles, n_tiles, kblocks;
+  int direct, splits;
+};
+template <int MODE>
+__device__ __forceinline__ HeadShape head_shape(const HeadParams& p, int tm) {
+  HeadShape h{p.M, p.m_tiles, p.n_tiles, p.kblocks, 0, 1};
+  if (MODE != STATS) {
+    const int rows = p.plan->rows;
+    if (MODE == DW) h.kblocks = (rows + BK - 1) / BK;
+    else h.M = rows, h.m_tiles = (rows + tm - 1) / tm;
+  }
+  h.direct = h.m_tiles * h.n_tiles;
+  if (MODE == DX) h.direct = p.plan->direct, h.splits = p.plan->splits;
+  return h;
 }
 
 struct HeadTile {
@@ -183,32 +210,27 @@ struct HeadTile {
 // dz are read once, x stays in L2; with the m tiles first, dz came from DRAM once per n tile,
 // 4.2 GB for 4096 x 4096 x 32000, and the product took 700 us).
 template <int MODE>
-__device__ __forceinline__ HeadTile head_tile(int unit_index, const HeadParams& p) {
+__device__ __forceinline__ HeadTile head_tile(int unit_index, const HeadShape& h) {
   HeadTile t;
   int tile = unit_index;
   t.slice = -1;
   t.kb0 = 0;
-  t.kb1 = p.kblocks;
-  if (MODE == DX && unit_index >= p.direct) {
-    t.slice = unit_index - p.direct;
-    const int split = t.slice % p.splits;
-    tile = p.direct + t.slice / p.splits;
-    t.kb0 = (int)((int64_t)p.kblocks * split / p.splits);
-    t.kb1 = (int)((int64_t)p.kblocks * (split + 1) / p.splits);
+  t.kb1 = h.kblocks;
+  if (MODE == DX && unit_index >= h.direct) {
+    t.slice = unit_index - h.direct;
+    const int split = t.slice % h.splits;
+    tile = h.direct + t.slice / h.splits;
+    t.kb0 = (int)((int64_t)h.kblocks * split / h.splits);
+    t.kb1 = (int)((int64_t)h.kblocks * (split + 1) / h.splits);
   }
   if (MODE == DW) {
-    t.mb = tile / p.n_tiles;
-    t.nb = tile - t.mb * p.n_tiles;
+    t.mb = tile / h.n_tiles;
+    t.nb = tile - t.mb * h.n_tiles;
   } else {
-    t.nb = tile / p.m_tiles;
-    t.mb = tile - t.nb * p.m_tiles;
+    t.nb = tile / h.m_tiles;
+    t.mb = tile - t.nb * h.m_tiles;
   }
   return t;
-}
-
-// Work units of a launch.
-__host__ __device__ __forceinline__ int head_units(const HeadParams& p) {
-  return p.direct + (p.m_tiles * p.n_tiles - p.direct) * p.splits;
 }
 
 // NP planes: 1, or up to 3 per operand with p.terms products per K stage (the smallest first).
@@ -274,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   after_previous();  // nothing of memory was touched before
   const uint32_t tmem_base = *tmem_slot;
-  const int total_tiles = head_units(p);
+  const HeadShape h = head_shape<MODE>(p, TM);
+  const int total_tiles = h.direct + (h.m_tiles * h.n_tiles - h.direct) * h.splits;
   // The loss's logits and all sums of planes are added up in runs of kRun K stages: each run has
   // its own accumulator, and the epilogue adds the runs in fp32. The tensor core's own additions
   // truncate: over 4096 elements in one go the loss was off by 3.4e-6 of its size, in runs of
@@ -294,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t issued = 0;
       bool ok = true;
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
-        const HeadTile t = head_tile<MODE>(tile, p);
+        const HeadTile t = head_tile<MODE>(tile, h);
         const int am = t.mb * TM + (int)rank * BM, bn = t.nb * bn_cols + (int)rank * (BN / CG);
         int kb = t.kb0, term = 0;
         for (int ks = t.kb0 * terms; ks < t.kb1 * terms; ++ks) {
@@ -350,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t acc_phase = 0;
       bool ok = true;
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
-        const HeadTile t = head_tile<MODE>(tile, p);
+        const HeadTile t = head_tile<MODE>(tile, h);
         int ks = t.kb0 * terms;
         for (int run = 0; run < runs_of(t) && ok; ++run) {
           if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort, p.timeout_ns, p.status)) { ok = false; break; }
@@ -399,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     float run_max = -INFINITY, run_sum = 0.0f;  // STATS with one m tile: of all tiles so far
     for (int tile = unit; tile < total_tiles; tile += nunits) {
-      const HeadTile t = head_tile<MODE>(tile, p);
+      const HeadTile t = head_tile<MODE>(tile, h);
       const int row0 = t.mb * TM + wrow, row = row0 + lane;  // the thread's row of the product
       const int col0 = t.nb * bn_cols + cbase;               // the warp's first column
-      const bool live = row < p.M;
+      const bool live = row < h.M;
       auto wait_full = [&] {
         const bool ok = mbar_wait(&tfull[acc], acc_phase, abort, p.timeout_ns, p.status);
         tc_fence_after();
@@ -424,13 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool counts = false;
       float lse = 0.0f, g = 0.0f;
       if constexpr (MODE == STATS || MODE == DLOGITS) {
-        if (live) tgt = __ldg(p.target + row);
+        const int token = MODE == DLOGITS && live ? p.index[row] : row;
+        if (live) tgt = __ldg(p.target + token);
         counts = tgt >= 0 && tgt < p.V;
         tgt = counts ? tgt - p.v0 : kNowhere;  // the target's column of this piece, or outside it
         if (MODE == DLOGITS && counts) {
-          lse = __ldg(p.lse + row);
+          lse = __ldg(p.lse + token);
           // the gradient of the mean: its factor 1 / count is left to the two products
-          g = p.dloss ? __ldg(p.dloss + row) : 1.0f;
+          g = p.dloss ? __ldg(p.dloss + token) : 1.0f;
         }
       } else {
         g = p.factor ? __ldg(p.factor) : 1.0f;
@@ -447,40 +471,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float pr = e - (i == at ? 1.0f : 0.0f);
             v[i] = counts && i < cols ? pr * g : 0.0f;
           }
-          // columns past the vocabulary are written too, as zeros: they are K rows of the next products
+          // columns past the vocabulary, and rows up to a whole K stage of dw, are written too, as
+          // zeros: they are K rows of the next products
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)row0 * p.ldo + cc;
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl) {
             stage_bf16(stage, lane, v);
-            flush_rows_64B(stage, lane, reinterpret_cast<uint8_t*>(out + pl * p.out_plane), p.ldo * 2, p.m_out - row0);
+            flush_rows_64B(stage, lane, reinterpret_cast<uint8_t*>(out + pl * p.out_plane), p.ldo * 2, (h.M + BK - 1) / BK * BK - row0);
             if (pl + 1 < NP)
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
           }
         } else {
+          const int32_t* at = MODE == DX && p.index ? p.index + row0 : nullptr;  // the places of the warp's rows
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= g;
           if (MODE == DX && t.slice >= 0) {
             uint8_t* out = reinterpret_cast<uint8_t*>(p.slices + ((int64_t)t.slice * TM + wrow) * BN + cbase + c0);
 #pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-              stage_f32(stage, lane, v + h);
-              flush_rows_64B(stage, lane, out + 4 * h, BN * 4, 32);
+            for (int q = 0; q < 32; q += 16) {
+              stage_f32(stage, lane, v + q);
+              flush_rows_64B(stage, lane, out + 4 * q, BN * 4, 32);
             }
           } else if (p.out_f32) {
-            float* out = static_cast<float*>(p.out) + (int64_t)row0 * p.ldo + cc;
+            float* out = static_cast<float*>(p.out) + cc;
             const bool add = MODE == DX && p.add;
 #pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-              stage_f32(stage, lane, v + h);
-              if (NP == 3 && p.scalar) flush_scalar(stage, lane, out + h, p.ldo, p.M - row0, cols - h, add);
-              else flush_edge(stage, lane, reinterpret_cast<uint8_t*>(out + h), p.ldo * 4, p.M - row0, (cols - h) / 4, add);
+            for (int q = 0; q < 32; q += 16) {
+              stage_f32(stage, lane, v + q);
+              if (NP == 3 && p.scalar) flush_scalar(stage, lane, out + q, p.ldo, row0, at, h.M - row0, cols - q, add);
+              else flush_edge(stage, lane, reinterpret_cast<uint8_t*>(out + q), p.ldo * 4, row0, at, h.M - row0, (cols - q) / 4, add);
             }
           } else {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)row0 * p.ldo + cc;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + cc;
             stage_bf16(stage, lane, v);
-            if (NP == 3 && p.scalar) flush_scalar(stage, lane, out, p.ldo, p.M - row0, cols, false);
-            else flush_edge(stage, lane, reinterpret_cast<uint8_t*>(out), p.ldo * 2, p.M - row0, cols / 8, false);
+            if (NP == 3 && p.scalar) flush_scalar(stage, lane, out, p.ldo, row0, at, h.M - row0, cols, false);
+            else flush_edge(stage, lane, reinterpret_cast<uint8_t*>(out), p.ldo * 2, row0, at, h.M - row0, cols / 8, false);
           }
         }
       };
@@ -490,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t zr[kCols / 32][32];
         const int runs = runs_of(t);
         bool ok = true;
-        if (runs == 0) {  // a split without K stages
+        if (runs == 0) {  // no K stages: of a split, or no token counts
 #pragma unroll
           for (int i = 0; i < kCols; ++i) zr[i / 32][i % 32] = 0u;
         }
@@ -561,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         if (!wait_full()) break;
-        const bool none = MODE == DX && t.kb0 == t.kb1;  // a split without K stages: nothing in the accumulator
+        const bool none = t.kb0 == t.kb1;  // no K stages (of a split, or no token counts): nothing in the accumulator
         const uint32_t t_row = t_lane + acc * BN;
         uint32_t nxt[32];
         tmem_ld32(t_row, nxt);
@@ -606,7 +632,6 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  const int64_t tiles = head_units(p);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(CG * (num_sms() / CG));
   cfg.blockDim = dim3(kThreads);
@@ -630,7 +655,8 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
     }
     units = std::min(units, max_pairs);
   }
-  units = (int)std::min<int64_t>(units, tiles);
+  // as many as the tiles there may be (those of dx up to split 32 ways)
+  units = (int)std::min<int64_t>(units, (int64_t)p.m_tiles * p.n_tiles * (MODE == DX ? kMaxSplits : 1));
   if (walkers) *walkers = units;
   cfg.gridDim = dim3((unsigned)(CG * units));
   cfg.numAttrs = p.follows ? 2 : 1;
@@ -678,13 +704,11 @@ int a_box(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : BM; }
 
 HeadParams base_params(int64_t M, int64_t N, int64_t K, int tm, int tn, DeviceStatus* st) {
   HeadParams p{};
-  p.M = p.m_out = (int)M;
+  p.M = (int)M;
   p.N = (int)N;
   p.m_tiles = (int)ceil_div(M, tm);
   p.n_tiles = (int)ceil_div(N, tn);
   p.kblocks = (int)ceil_div(K, BK);
-  p.direct = p.m_tiles * p.n_tiles;
-  p.splits = 1;
   p.a_bytes = kABytes;
   p.status = st;
   p.timeout_ns = kTimeoutNs;
@@ -696,18 +720,20 @@ template <typename T>
 __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, int tm, int tn, T* out) {
   let_next_begin();
   after_previous();
-  const int tile = p.direct + blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;  // 4 columns each
-  const int nb = tile / p.m_tiles, mb = tile - nb * p.m_tiles;
+  const HeadShape h = head_shape<DX>(p, tm);
+  const int tile = h.direct + blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;  // 4 columns each
+  if (tile >= h.m_tiles * h.n_tiles) return;
+  const int nb = tile / h.m_tiles, mb = tile - nb * h.m_tiles;
   const int row = mb * tm + e / tn, col = nb * tn + e % tn;
-  if (row >= p.M || col >= p.N) return;
-  const float* s = p.slices + (int64_t)blockIdx.y * p.splits * tm * tn + e;
+  if (row >= h.M || col >= p.N) return;
+  const float* s = p.slices + (int64_t)blockIdx.y * h.splits * tm * tn + e;
   float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll 4
-  for (int k = 0; k < p.splits; ++k) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(s + (int64_t)k * tm * tn));
+  for (int k = 0; k < h.splits; ++k) {
+    const float4 a = *reinterpret_cast<const float4*>(s + (int64_t)k * tm * tn);
     v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
   }
-  T* o = out + (int64_t)row * p.ldo + col;
+  T* o = out + (int64_t)(p.index ? p.index[row] : row) * p.ldo + col;
   if (p.scalar) {
     const float f[4] = {v.x, v.y, v.z, v.w};
     for (int i = 0; i < 4 && col + i < p.N; ++i) {
@@ -726,47 +752,31 @@ __global__ void __launch_bounds__(256) join_slices_kernel(const HeadParams p, in
   }
 }
 
-// The planes of rows [0, rows) of src [., H] in dst [planes][rows_pad][Hp] bf16: zeros past H and
-// from `rows` to `zero_to` (the K stages of the products read that far), and, given targets, in the
-// rows of tokens that do not count: their dz is zero, but zero times a NaN or infinity in a padded
-// row of x would reach every row of dw. (x is copied for that alone where it could be read in place:
-// 4096 x 4096 x 32000 forward and backward 2569 us, 2583 without the copy; 1500 x 2048 x 50257 743
-// and 787.) Eight columns a thread.
-template <typename T, int NP>
-__global__ void __launch_bounds__(256)
-    planes_kernel(const T* src, int rows, int H, const int32_t* target, int V, __nv_bfloat16* dst, int64_t plane, int Hp,
-                  int zero_to) {
-  let_next_begin();
-  after_previous();
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int per = Hp / 8, row = (int)(e / per), c = (int)(e % per) * 8;
-  if (row >= zero_to) return;
-  float v[8];
-  const bool whole = H % 8 == 0;  // a thread's columns are all there, and aligned
-  bool there = row < rows;
-  if (there && target) {
-    const int32_t t = __ldg(target + row);
-    there = t >= 0 && t < V;
-  }
-  if (!there) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  } else if (whole && sizeof(T) == 4) {
-    const float4* q = reinterpret_cast<const float4*>(src + (int64_t)row * H + c);
+// Eight columns from c on of a row of H as fp32 (zeros past H).
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int H, float (&v)[8]) {
+  const bool whole = H % 8 == 0;  // they are all there, and aligned
+  if (whole && sizeof(T) == 4) {
+    const float4* q = reinterpret_cast<const float4*>(row + c);
     const float4 a = __ldg(q), b = __ldg(q + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else if (whole) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * H + c));
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + c));
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < H ? static_cast<float>(src[(int64_t)row * H + c + i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = c + i < H ? static_cast<float>(row[c + i]) : 0.0f;
   }
+}
+
+// Their NP planes at dst, `plane` elements apart.
+template <int NP>
+__device__ __forceinline__ void store_planes(__nv_bfloat16* dst, int64_t plane, float (&v)[8]) {
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    *reinterpret_cast<uint4*>(dst + p * plane + (int64_t)row * Hp + c) =
+    *reinterpret_cast<uint4*>(dst + p * plane) =
         make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
     if (p + 1 < NP)
 #pragma unroll
@@ -774,17 +784,164 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-cudaError_t launch_planes(const void* src, int f32, int rows, int H, const int32_t* target, int V, void* dst,
-                          int64_t plane, int Hp, int zero_to, bool follows, cudaStream_t s) {
+// The planes of rows [0, rows) of src [., H] in dst [planes][rows_pad][Hp] bf16: zeros past H and
+// from `rows` to `zero_to` (the K stages of the products read that far). Eight columns a thread.
+template <typename T, int NP>
+__global__ void __launch_bounds__(256)
+    planes_kernel(const T* src, int rows, int H, __nv_bfloat16* dst, int64_t plane, int Hp, int zero_to) {
+  let_next_begin();
+  after_previous();
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = Hp / 8, row = (int)(e / per), c = (int)(e % per) * 8;
+  if (row >= zero_to) return;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (row < rows) load8(src + (int64_t)row * H, c, H, v);
+  store_planes<NP>(dst + (int64_t)row * Hp + c, plane, v);
+}
+
+// The input gradient's tiles rarely fill whole rounds of the SMs (4096 x 4096 is 256 tiles of
+// 256 x 256 on 76 CTA pairs: 3.37 rounds, so 4). The tiles of the last round are therefore
+// split along K, by the number of ways that takes least time: rounds of stages of 64 (0.14 us
+// with 256 columns, half of that with 128) against the slices' traffic (0.08 us for a tile of
+// 256 x 256) and the launch that adds them. At most four rounds of slices.
+struct SplitRule {
+  int tm, tn, units, planes, n_tiles, kblocks;
+  __host__ __device__ float stage() const { return 0.14f * tn / 256 * (planes == 3 ? 6 : 1); }
+  __host__ __device__ float slice() const { return 0.08f * tm * tn / 65536; }
+  // Whether a split into any number could pay, for any number of rows.
+  bool may_split() const { return kblocks * stage() > 4.0f + 2.0f * sqrtf(kblocks * stage() * slice()); }
+  // By a whole warp, a number of splits per lane.
+  __device__ HeadPlan of(int rows) const {
+    const int lane = threadIdx.x & 31, s = lane + 1;
+    const int tiles = (rows + tm - 1) / tm * n_tiles, tail = tiles % units;
+    float least = INFINITY;
+    if (s == 1) least = kblocks * stage();
+    else if (tail && s * 4 <= kblocks && tail * s <= 4 * units)
+      least = (float)((tail * s + units - 1) / units) * ((kblocks + s - 1) / s) * stage() + tail * s * slice() + 4.0f;
+    int best = s;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, least, off);
+      const int at = __shfl_xor_sync(0xffffffffu, best, off);
+      if (other < least || (other == least && at < best)) least = other, best = at;
+    }
+    return {rows, best > 1 ? tiles - tail : tiles, best};
+  }
+  // Room for the slices of any number of rows up to `rows`.
+  int64_t most_slices(int64_t rows) const {
+    return std::min<int64_t>(kMaxSplits * ceil_div(rows, tm) * n_tiles, 4 * units);
+  }
+};
+SplitRule split_rule(int64_t T, int64_t H, int64_t rows, int planes) {
+  const int tm = tile_rows(T), tn = tile_cols(T, planes);
+  return {tm, tn, small_tokens(T) ? 152 : 76, planes, (int)ceil_div(H, tn), (int)ceil_div(rows, BK)};
+}
+
+// The backward's first kernel: the rows of x whose tokens count, one after the other, in dst
+// [planes][rows_pad][Hp] (with zeros up to a whole K stage), their tokens in index, the plan, and
+// zeros in the rows of dx whose tokens do not count. What is left out costs the products nothing
+// (1500 x 2048 x 50257 with 60 % left out, forward and backward: 505 us, 743 with zeros for them),
+// and a NaN or infinity in a padded row of x meets no other row. A block takes 16 tokens and 512
+// columns; it counts those of the tokens before its own by itself, from the first or, beyond 65536
+// tokens, from the last whole chunk of 4096 on and over the chunks' counts (chunk; else NULL).
+constexpr int kGather = 16, kGatherCols = 512, kItems = kGather * kGatherCols / 8 / 256;
+constexpr int kChunk = 4096, kCountFrom = 65536;
+__global__ void __launch_bounds__(256) count_kernel(const int32_t* target, int rows, int V, int32_t* chunk) {
+  let_next_begin();
+  __shared__ int32_t sum;
+  if (threadIdx.x == 0) sum = 0;
+  __syncthreads();
+  const int64_t first = (int64_t)blockIdx.x * kChunk;
+  int n = 0;
+  for (int64_t i = first + threadIdx.x; i < min((int64_t)rows, first + kChunk); i += 256) {
+    const int32_t t = __ldg(target + i);
+    n += t >= 0 && t < V;
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&sum, n);
+  __syncthreads();
+  if (threadIdx.x == 0) chunk[blockIdx.x] = sum;
+}
+
+template <typename T, int NP>
+__global__ void __launch_bounds__(256)
+    gather_kernel(const T* x, const int32_t* target, int rows, int H, int V, __nv_bfloat16* dst, int64_t plane, int Hp,
+                  const int32_t* chunk, int32_t* index, HeadPlan* plan, T* dx, SplitRule rule) {
+  let_next_begin();
+  if (chunk) after_previous();
+  __shared__ int32_t before, place[kGather];
+  const int first = blockIdx.x * kGather, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int live = min(kGather, rows - first);
+  const int c0 = blockIdx.y * kGatherCols, per = min(kGatherCols, Hp - c0) / 8;  // 8 columns an item
+  auto counts = [&](int32_t t) { return t >= 0 && t < V; };
+  // everything is on its way before the first wait: the rows, their targets and those before them
+  float v[kItems][8];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int e = threadIdx.x + i * 256, r = e / per;
+    if (r < live) load8(x + (int64_t)(first + r) * H, c0 + e % per * 8, H, v[i]);
+  }
+  const uint32_t mask = __ballot_sync(0xffffffffu, lane < live && counts(__ldg(target + first + min(lane, live - 1))));
+  if (threadIdx.x == 0) before = 0;
+  __syncthreads();
+  int n = 0;
+  const int whole = chunk ? first / kChunk : 0;
+  for (int i = threadIdx.x; i < whole; i += 256) n += chunk[i];
+  for (int i = whole * kChunk + threadIdx.x * 4; i < first; i += 1024) {
+    const int4 t = __ldg(reinterpret_cast<const int4*>(target + i));  // first is a multiple of 16
+    n += (int)counts(t.x) + (int)counts(t.y) + (int)counts(t.z) + (int)counts(t.w);
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+  if (lane == 0 && n) atomicAdd(&before, n);
+  __syncthreads();
+  if (warp == 0 && lane < kGather) {
+    const int at = before + __popc(mask & ((1u << lane) - 1));
+    const bool in = mask >> lane & 1;
+    place[lane] = in ? at : -1;
+    if (in && blockIdx.y == 0) index[at] = first + lane;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int e = threadIdx.x + i * 256, r = e / per, c = c0 + e % per * 8;
+    if (r >= live) continue;
+    if (place[r] >= 0) {
+      store_planes<NP>(dst + (int64_t)place[r] * Hp + c, plane, v[i]);
+    } else if (dx) {
+      T* o = dx + (int64_t)(first + r) * H + c;
+      if (H % 8 == 0) {
+#pragma unroll
+        for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<uint4*>(o)[q] = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int q = 0; q < 8 && c + q < H; ++q) o[q] = T(0.0f);
+      }
+    }
+  }
+  if (blockIdx.x != gridDim.x - 1) return;
+  const int total = before + __popc(mask);
+  if (blockIdx.y == 0 && warp == 7) {
+    const HeadPlan made = rule.of(total);
+    if (lane == 0) *plan = made;
+  }
+  float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const int to = (total + BK - 1) / BK * BK;
+  for (int e = threadIdx.x; e < (to - total) * per; e += 256)
+    store_planes<NP>(dst + (int64_t)(total + e / per) * Hp + c0 + e % per * 8, plane, zero);
+}
+
+cudaError_t launch_planes(const void* src, int f32, int rows, int H, void* dst, int64_t plane, int Hp, int zero_to,
+                          bool follows, cudaStream_t s) {
   const dim3 grid((unsigned)ceil_div((int64_t)zero_to * (Hp / 8), 256));
   auto* d = static_cast<__nv_bfloat16*>(dst);
   const auto* xf = static_cast<const float*>(src);
   const auto* xb = static_cast<const __nv_bfloat16*>(src);
   if (follows)
-    return f32 ? launch_after(planes_kernel<float, 3>, grid, 256, s, xf, rows, H, target, V, d, plane, Hp, zero_to)
-               : launch_after(planes_kernel<__nv_bfloat16, 1>, grid, 256, s, xb, rows, H, target, V, d, plane, Hp, zero_to);
-  if (f32) planes_kernel<float, 3><<<grid, 256, 0, s>>>(xf, rows, H, target, V, d, plane, Hp, zero_to);
-  else planes_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(xb, rows, H, target, V, d, plane, Hp, zero_to);
+    return f32 ? launch_after(planes_kernel<float, 3>, grid, 256, s, xf, rows, H, d, plane, Hp, zero_to)
+               : launch_after(planes_kernel<__nv_bfloat16, 1>, grid, 256, s, xb, rows, H, d, plane, Hp, zero_to);
+  if (f32) planes_kernel<float, 3><<<grid, 256, 0, s>>>(xf, rows, H, d, plane, Hp, zero_to);
+  else planes_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(xb, rows, H, d, plane, Hp, zero_to);
   return cudaGetLastError();
 }
 
@@ -811,7 +968,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int i = i0 + u * kLanes;
-        v[u] = i < parts ? __ldg(part + (int64_t)i * T + t) : make_float2(-INFINITY, 0.0f);
+        v[u] = i < parts ? part[(int64_t)i * T + t] : make_float2(-INFINITY, 0.0f);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) m2 = fmaxf(m2, v[u].x);
@@ -888,33 +1045,16 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// dx = the sums of the pieces, from fp32 (x of one type or the other).
+// dx = the sums of the pieces, from fp32 (x of one type or the other), at their tokens' rows.
 template <typename T>
-__global__ void __launch_bounds__(256) store_dx_kernel(const float* sums, int64_t n, T* dx) {
+__global__ void __launch_bounds__(256)
+    store_dx_kernel(const float* sums, int64_t n, int H, const int32_t* index, const HeadPlan* plan, T* dx) {
   after_previous();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  if constexpr (sizeof(T) == 4) dx[i] = sums[i];
-  else dx[i] = __float2bfloat16_rn(sums[i]);
-}
-
-// The input gradient's tiles rarely fill whole rounds of the SMs (4096 x 4096 is 256 tiles of
-// 256 x 256 on 76 CTA pairs: 3.37 rounds, so 4). The tiles of the last round are therefore
-// split along K, by the number of ways that takes least time: rounds of stages of 64 (0.14 us
-// with 256 columns, half of that with 128) against the slices' traffic (0.08 us for a tile of
-// 256 x 256) and the launch that adds them.
-HeadSplit head_split(int64_t T, int64_t H, int64_t rows, int planes) {
-  const int tm = tile_rows(T), tn = tile_cols(T, planes), units = small_tokens(T) ? 152 : 76;
-  const int64_t tiles = ceil_div(T, tm) * ceil_div(H, tn), kblocks = ceil_div(rows, BK);
-  HeadSplit best{tiles, 1, 0};
-  const int64_t tail = tiles % units;
-  const double stage = 0.14 * tn / 256 * (planes == 3 ? 6 : 1), slice = 0.08 * tm * tn / 65536;
-  double least = (tail ? 1.0 : 0.0) * kblocks * stage;
-  for (int s = 2; s <= 32 && tail && s * 4 <= kblocks; ++s) {
-    const double t = (double)ceil_div(tail * s, units) * ceil_div(kblocks, s) * stage + tail * s * slice + 4.0;
-    if (t < least) least = t, best = {tiles - tail, s, (size_t)(tail * s) * tm * tn * 4};
-  }
-  return best;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / H;
+  if (i >= n || row >= plan->rows) return;
+  T* o = dx + (int64_t)index[row] * H + i % H;
+  if constexpr (sizeof(T) == 4) *o = sums[i];
+  else *o = __float2bfloat16_rn(sums[i]);
 }
 
 // The plane products of a GEMM: all six of fp32 operands; those of an operand of three planes (A)
@@ -953,7 +1093,7 @@ namespace {
 bool is_f32(const moe_head_config_t& c) { return c.act_dtype == MOE_DTYPE_F32; }
 bool laid_out(const moe_head_config_t& c) { return is_f32(c) || c.H % 8; }
 int planes_of(const moe_head_config_t& c) { return laid_out(c) ? 3 : 1; }  // of dz
-int64_t padded_tokens(const moe_head_config_t& c) { return align_up((size_t)c.T, 64); }
+int64_t padded_tokens(const moe_head_config_t& c) { return align_up((size_t)c.T, 64); }  // whole K stages of dw
 
 tc::Operands operands(const moe_head_config_t& c, const HeadScratch& L, const void* x, const void* w, char* ws) {
   tc::Operands o{};
@@ -961,7 +1101,8 @@ tc::Operands operands(const moe_head_config_t& c, const HeadScratch& L, const vo
   o.in_planes = is_f32(c) ? 3 : 1;
   o.laid_out = laid_out(c);
   o.cols = o.laid_out ? (int64_t)align_up((size_t)c.H, 8) : c.H;
-  o.x_plane = o.dl_plane = o.laid_out ? padded_tokens(c) : c.T;
+  o.x_plane = o.laid_out ? padded_tokens(c) : c.T;
+  o.dl_plane = padded_tokens(c);
   o.w_plane = o.laid_out ? L.piece : c.V;
   o.x_rows = o.in_planes * o.x_plane;
   o.w_rows = o.in_planes * o.w_plane;
@@ -971,16 +1112,35 @@ tc::Operands operands(const moe_head_config_t& c, const HeadScratch& L, const vo
   return o;
 }
 
-// Lays out x (given targets, the rows that count), and rows [v0, v0 + rows) of w, where the
-// products need it.
-cudaError_t lay_out_x(const moe_head_config_t& c, const tc::Operands& o, const void* x, const int32_t* target, cudaStream_t s) {
-  if (o.x == x) return cudaSuccess;
-  return tc::launch_planes(x, is_f32(c), c.T, c.H, target, c.V, const_cast<void*>(o.x), o.x_plane * o.cols, (int)o.cols,
-                           (int)o.x_plane, false, s);
+// Lays out x, and rows [v0, v0 + rows) of w, where the products need it.
+cudaError_t lay_out_x(const moe_head_config_t& c, const tc::Operands& o, const void* x, cudaStream_t s) {
+  if (!o.laid_out) return cudaSuccess;
+  return tc::launch_planes(x, is_f32(c), c.T, c.H, const_cast<void*>(o.x), o.x_plane * o.cols, (int)o.cols, (int)o.x_plane, false, s);
 }
+// x's rows that count to o.x, and what else the backward's first kernel does.
+template <typename T, int NP>
+cudaError_t launch_gather(const moe_head_config_t& c, const tc::Operands& o, const void* x, const int32_t* target,
+                          int32_t* index, tc::HeadPlan* plan, void* dx, const tc::SplitRule& rule, cudaStream_t s) {
+  const dim3 grid((unsigned)ceil_div(c.T, tc::kGather), (unsigned)ceil_div(o.cols, tc::kGatherCols));
+  const auto* from = static_cast<const T*>(x);
+  auto* to = static_cast<__nv_bfloat16*>(const_cast<void*>(o.x));
+  auto* none = static_cast<T*>(dx);
+  const int64_t plane = o.x_plane * o.cols;
+  if (c.T <= tc::kCountFrom) {
+    tc::gather_kernel<T, NP><<<grid, 256, 0, s>>>(from, target, c.T, c.H, c.V, to, plane, (int)o.cols, nullptr, index, plan, none, rule);
+    return cudaGetLastError();
+  }
+  int32_t* chunk = index + padded_tokens(c);
+  tc::count_kernel<<<(unsigned)ceil_div(c.T, tc::kChunk), 256, 0, s>>>(target, c.T, c.V, chunk);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(tc::gather_kernel<T, NP>, grid, 256, s, from, target, c.T, c.H, c.V, to, plane, (int)o.cols, chunk, index,
+                      plan, none, rule);
+}
+
 cudaError_t lay_out_w(const moe_head_config_t& c, const tc::Operands& o, const void* w, int64_t v0, int rows, cudaStream_t s) {
   if (!o.laid_out) return cudaSuccess;
-  return tc::launch_planes(static_cast<const char*>(w) + v0 * c.H * (is_f32(c) ? 4 : 2), is_f32(c), rows, c.H, nullptr, 0,
+  return tc::launch_planes(static_cast<const char*>(w) + v0 * c.H * (is_f32(c) ? 4 : 2), is_f32(c), rows, c.H,
                            const_cast<void*>(o.w), o.w_plane * o.cols, (int)o.cols, (int)align_up((size_t)rows, 64), true, s);
 }
 
@@ -991,13 +1151,12 @@ cudaError_t lay_out_w(const moe_head_config_t& c, const tc::Operands& o, const v
 HeadScratch head_scratch(const moe_head_config_t& c) {
   HeadScratch L{};
   const bool lay = laid_out(c);
-  const int64_t T = std::max<int64_t>(lay ? padded_tokens(c) : c.T, 1), Hp = align_up((size_t)c.H, 8), np = planes_of(c);
+  const int64_t T = std::max<int64_t>(padded_tokens(c), 1), Hp = align_up((size_t)c.H, 8), np = planes_of(c);
   const int64_t row_bytes = 2 * np * (T + (lay ? Hp : 0));
   int64_t piece = c.piece > 0 ? c.piece : std::max<int64_t>(4096, (256ll << 20) / row_bytes);
   piece = (int64_t)align_up((size_t)std::min<int64_t>(piece, c.V), 256);
   L.piece = piece;
   L.ld = (int)piece;
-  L.split = tc::head_split(T, c.H, std::min<int64_t>(piece, c.V), (int)np);
   size_t o = kWsHead;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1007,11 +1166,14 @@ HeadScratch head_scratch(const moe_head_config_t& c) {
   // (max, sum) of the halves of 128- or 256-column tiles; one m tile: of the CTAs, for every piece
   L.part = take((size_t)std::max<int64_t>(ceil_div(c.V, 128), T <= 256 ? ceil_div(c.V, lay ? piece : c.V) * 152 : 0) * 2 * T * 8);
   L.target_logit = take((size_t)T * 4);
-  L.x = take((size_t)(np * T * Hp * 2));  // in place: of the rows that count, for dw
+  L.plan = take(sizeof(tc::HeadPlan));
+  L.index = take((size_t)(T + ceil_div(T, tc::kChunk)) * 4);  // and the chunks' counts
+  L.x = take((size_t)(np * T * Hp * 2));
   L.w = take(lay ? (size_t)(np * piece * Hp * 2) : 0);
   L.dlogits = take((size_t)(np * T * piece * 2));
   L.dx = take(piece >= c.V ? 0 : (size_t)T * c.H * 4);
-  L.slices = take(L.split.bytes);
+  const tc::SplitRule rule = tc::split_rule(T, c.H, std::min<int64_t>(piece, c.V), (int)np);
+  L.slices = take((size_t)rule.most_slices(T) * rule.tm * rule.tn * 4);
   L.total = o;
   return L;
 }
@@ -1026,7 +1188,7 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
   auto* tl = reinterpret_cast<float*>(b + L.target_logit);
   const Operands o = operands(c, L, x, w, b);
   const int tm = tile_rows(c.T), tn = stats_cols(c.T, c.V, o.planes);
-  cudaError_t e = lay_out_x(c, o, x, nullptr, s);
+  cudaError_t e = lay_out_x(c, o, x, s);
   int parts = 0, walkers = 0;
   const int64_t step = o.laid_out ? L.piece : c.V;  // w in place needs no pieces here
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += step) {
@@ -1071,13 +1233,18 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   const HeadScratch L = head_scratch(c);
   const bool one = L.piece >= c.V;  // dx needs no sum over pieces
   char* b = static_cast<char*>(ws);
-  Operands o = operands(c, L, x, w, b);
-  if (dw) o.x = b + L.x;
+  Operands o = operands(c, L, b + L.x, w, b);
+  o.x_plane = padded_tokens(c);
+  o.x_rows = o.in_planes * o.x_plane;
   const int tm = tile_rows(c.T), tn = tile_cols(c.T, o.planes);
   void* dl = b + L.dlogits;
   float* dx_sums = reinterpret_cast<float*>(b + L.dx);
   const float* factor = mean ? mean + 1 : nullptr;
-  cudaError_t e = lay_out_x(c, o, x, target, s);
+  auto* plan = reinterpret_cast<HeadPlan*>(b + L.plan);
+  auto* index = reinterpret_cast<int32_t*>(b + L.index);
+  const SplitRule rule = split_rule(c.T, c.H, std::min<int64_t>(L.piece, c.V), o.planes);
+  cudaError_t e = f32 ? launch_gather<float, 3>(c, o, x, target, index, plan, dx, rule, s)
+                      : launch_gather<__nv_bfloat16, 1>(c, o, x, target, index, plan, dx, rule, s);
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {
     const int rows = (int)std::min<int64_t>(L.piece, c.V - v0);
     if ((e = lay_out_w(c, o, w, v0, rows, s)) != cudaSuccess) break;
@@ -1095,10 +1262,11 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     p.target = target;
     p.lse = lse;
     p.dloss = dloss;
-    p.follows = o.x != x || v0 > 0;
+    p.plan = plan;
+    p.index = index;
+    p.follows = 1;
     p.out = dl;
     p.ldo = L.ld;
-    p.m_out = (int)o.dl_plane;
     p.out_plane = o.dl_plane * L.ld;
     if (!bf16_box(&ma, o.x, o.x_rows, o.cols, a_box(c.T)) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
       return cudaErrorInvalidValue;
@@ -1111,8 +1279,8 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
       p.a_plane = (int)o.dl_plane;
       p.b_plane = (int)o.w_plane;
       p.follows = 1;
-      p.direct = (int)L.split.direct;
-      p.splits = L.split.splits;
+      p.plan = plan;
+      p.index = one ? index : nullptr;  // the sums of pieces stay one row after the other
       p.slices = reinterpret_cast<float*>(b + L.slices);
       p.out = one ? dx : dx_sums;
       p.ldo = c.H;
@@ -1122,8 +1290,8 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
       p.factor = factor;
       if (!bf16_box(&ma, dl, o.dl_rows, L.ld, a_box(c.T)) || !bf16_box(&mb, o.w, o.w_rows, o.cols, 64)) return cudaErrorInvalidValue;
       if ((e = launch_mode<DX>(c.T, o.planes, ma, mb, p, s)) != cudaSuccess) break;
-      if (p.splits > 1) {
-        const dim3 grid((unsigned)(tm * tn / 1024), (unsigned)(p.m_tiles * p.n_tiles - p.direct));
+      if (rule.may_split()) {  // how many tiles are is known on the device; fewer than a round
+        const dim3 grid((unsigned)(tm * tn / 1024), (unsigned)std::min(p.m_tiles * p.n_tiles, rule.units - 1));
         e = p.out_f32 ? launch_after(join_slices_kernel<float>, grid, 256, s, p, tm, tn, static_cast<float*>(p.out))
                       : launch_after(join_slices_kernel<__nv_bfloat16>, grid, 256, s, p, tm, tn, static_cast<__nv_bfloat16*>(p.out));
         if (e != cudaSuccess) break;
@@ -1136,6 +1304,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
       p.a_plane = (int)o.dl_plane;
       p.b_plane = (int)o.x_plane;
       p.follows = 1;
+      p.plan = plan;
       p.out_f32 = g32;
       p.out = static_cast<char*>(dw) + v0 * c.H * (g32 ? 4 : 2);
       p.ldo = c.H;
@@ -1149,8 +1318,10 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   const int64_t n = (int64_t)c.T * c.H;
   const unsigned grid = (unsigned)ceil_div(n, 256);
   const float* from = dx_sums;
-  return f32 ? launch_after(store_dx_kernel<float>, grid, 256, s, from, n, static_cast<float*>(dx))
-             : launch_after(store_dx_kernel<__nv_bfloat16>, grid, 256, s, from, n, static_cast<__nv_bfloat16*>(dx));
+  const int32_t* rows_at = index;
+  const HeadPlan* from_plan = plan;
+  return f32 ? launch_after(store_dx_kernel<float>, grid, 256, s, from, n, c.H, rows_at, from_plan, static_cast<float*>(dx))
+             : launch_after(store_dx_kernel<__nv_bfloat16>, grid, 256, s, from, n, c.H, rows_at, from_plan, static_cast<__nv_bfloat16*>(dx));
 }
 
 }  // namespace moe

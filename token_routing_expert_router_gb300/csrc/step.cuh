@@ -73,16 +73,10 @@ cudaError_t launch_grad_clip(const moe_grad_t* grads, int32_t count, float max_n
                              DeviceStatus* st, cudaStream_t s);
 
 // ---- vocabulary head loss
-struct HeadSplit {  // of the input gradient's product
-  int64_t direct;   // tiles that are not split
-  int splits;       // K splits of the others
-  size_t bytes;     // fp32 tiles of the splits
-};
 struct HeadScratch {  // workspace offsets, after the status head
-  size_t part, target_logit, x, w, dlogits, dx, slices, total;
+  size_t part, target_logit, plan, index, x, w, dlogits, dx, slices, total;
   int64_t piece;   // vocabulary rows whose logit gradients are held at once
   int ld;          // row length of dlogits
-  HeadSplit split;
 };
 HeadScratch head_scratch(const moe_head_config_t& c);
 cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
