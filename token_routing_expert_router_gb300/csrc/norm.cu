@@ -268,12 +268,12 @@ __device__ __forceinline__ void channel_weights(const float* w_post, const float
 __device__ __forceinline__ float inv_rms(float sum, float inv_h, float eps) { return rsqrtf(fmaf(sum, inv_h, eps)); }
 
 // ROWS rows per iteration: i ROWS + k is row (first + (i ROWS + k) step) of the group.
-template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
+template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL, int ROWS>
 __global__ void __launch_bounds__(MAXT, MAXT <= 128 ? 4 : MAXT <= 256 || (MAXT <= 512 && STAGES == 0) ? 2 : 1)
     block_norm_kernel(NormIn in, void* r_out, void* n_out, int T_, int H, float eps, float res_scale) {
   using P = Piece<T, VEC>;
   using E = typename P::E;
-  constexpr int N = P::N, ROWS = STAGES > 0 ? 2 : 1;  // without the ring there are no registers for two
+  constexpr int N = P::N;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ RowSums<ROWS, CL> sums;
   const int groups = blockDim.y, nvec = H / VEC;
@@ -621,12 +621,13 @@ cudaError_t launch_rows(K kern, std::atomic<uint32_t>& last, const Shape& sh, si
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL>
+// Two rows an iteration, but without the ring there are no registers for them.
+template <typename T, int VEC, int VPT, bool CACHE_W, int MAXT, int STAGES, int CL, int ROWS = (STAGES > 0 ? 2 : 1)>
 cudaError_t fwd(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
-  const size_t smem = (size_t)STAGES * 2 * 2 * VPT * MAXT * sizeof(Piece<T, VEC>);
+  const size_t smem = (size_t)STAGES * ROWS * 2 * VPT * MAXT * sizeof(Piece<T, VEC>);
   static std::atomic<uint32_t> last{0};
   int walkers = 0;
-  return launch_rows<CL>(block_norm_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES, CL>, last, shape_of(c.H / VEC, VPT, MAXT, CL),
+  return launch_rows<CL>(block_norm_kernel<T, VEC, VPT, CACHE_W, MAXT, STAGES, CL, ROWS>, last, shape_of(c.H / VEC, VPT, MAXT, CL),
                          smem, c.T, s, &walkers, in, r, n, c.T, c.H, c.eps, c.res_scale);
 }
 
@@ -642,52 +643,68 @@ cudaError_t bwd(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaS
   return launch_after(colsum_kernel, dim3((unsigned)ceil_div(c.H, 32), 2), dim3(32, 32), s, part, walkers * sh.groups, c.H, b);
 }
 
+// How a row is spread, by the number of its pieces of 16 bytes. All: the fewest stages of the ring
+// that keep a row or two in flight, so that an SM holds several CTAs (backward with 4 instead of 3:
+// 80 against 78 us; forward with 3 instead of 2: 50 against 47).
+//
+// Forward: one piece per thread up to 1024 (more threads hide its two barriers: 16384 x 2048 49
+// against 51 us, 8192 x 4096 49 against 52, 8192 x 7168 77 against 79), then two, a row an iteration
+// (of two there would be no shared memory for a second stage; a cluster of two CTAs instead, with
+// its barriers of 1 us: 4096 x 16384 134 against 115 us, 4096 x 7168 fp32 123 against 85).
+template <typename T, int VEC>
+cudaError_t fwd_wide(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
+  const int nvec = c.H / VEC;
+  if (nvec <= 32) return fwd<T, VEC, 1, true, 128, 2, 1>(c, in, r, n, s);
+  if (nvec <= 256) return fwd<T, VEC, 1, true, 256, 2, 1>(c, in, r, n, s);
+  if (nvec <= 512) return fwd<T, VEC, 1, true, 512, 2, 1>(c, in, r, n, s);
+  if (nvec <= 1024) return fwd<T, VEC, 1, true, 1024, 2, 1>(c, in, r, n, s);
+  if constexpr (VEC == 4) {
+    if (nvec > 2048) return fwd<T, VEC, 2, true, 1024, 3, 2, 1>(c, in, r, n, s);  // 4096 x 16384: 257 us, 266 in four of 512 threads
+  }
+  return fwd<T, VEC, 2, true, 1024, 3, 1, 1>(c, in, r, n, s);
+}
+
+// Backward: two pieces per thread, since its bookkeeping per row and thread is near half of its
+// instructions (16384 x 2048: 80 against 88 us with one; 8192 x 7168: 141 against 203). Its columns'
+// sums leave no registers for more than 512 threads in a CTA; wider rows take a cluster of four (of
+// 512 threads, where one to an SM finds nothing to do during the cluster's barrier: 4096 x 16384 257
+// against 232 us, 4096 x 7168 fp32 191 against 175; of eight: 281, 258).
+template <typename T, int VEC>
+cudaError_t bwd_wide(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
+  const int nvec = c.H / VEC;
+  if (nvec <= 32) return bwd<T, VEC, 1, true, 128, 3, 1>(c, b, part, s);
+  if (nvec <= 256) return bwd<T, VEC, 2, true, 128, 3, 1>(c, b, part, s);
+  if (nvec <= 512) return bwd<T, VEC, 2, true, 256, 3, 1>(c, b, part, s);
+  if (nvec <= 1024) return bwd<T, VEC, 2, true, 512, 3, 1>(c, b, part, s);
+  if constexpr (VEC == 4) {
+    if (nvec > 2048) return bwd<T, VEC, 2, true, 512, 3, 4>(c, b, part, s);
+  }
+  return bwd<T, VEC, 2, true, 256, 3, 4>(c, b, part, s);
+}
+
 }  // namespace
 
-// How a row is spread: pieces of VEC elements, at most 1024 pieces per CTA, so a cluster of 2 or
-// 4 CTAs for wider rows. Rows of H not a multiple of 16 bytes have pieces of 4 bytes (4 to 16 per
-// thread); an odd number of bf16 channels leaves nothing for cp.async to copy, and takes single
-// elements without the ring.
-// V1, V2: pieces per thread of rows of up to 256 pieces, and of bf16 rows of 513 to 1024. The
-// backward takes two, since its bookkeeping per row and thread is near half of its instructions
-// (16384 x 2048: 80 against 88 us with one; 8192 x 7168: 141 against 203). The forward takes one:
-// more threads hide its two barriers (49 against 51 us; 77 against 79).
-// S1, S2, S4: stages of the ring (forward: of two rows each) for those rows, for wider ones and
-// for pieces of 4 bytes: the fewest that keep a row or two in flight, so that an SM holds several
-// CTAs (backward with 4 instead of 3: 80 against 78 us; forward with 3 instead of 2: 50 against 47).
-#define NORM_DISPATCH(FN, V1, V2, S1, S2, S4, ...)                                                \
-  if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0) {                                            \
-    const int nvec = c.H / 8;                                                                     \
-    if (nvec <= 32) return FN<__nv_bfloat16, 8, 1, true, 128, S1, 1>(__VA_ARGS__);                \
-    if (nvec <= 256) return FN<__nv_bfloat16, 8, V1, true, 256 / V1, S1, 1>(__VA_ARGS__);         \
-    if (nvec <= 512) return FN<__nv_bfloat16, 8, 2, true, 256, S2, 1>(__VA_ARGS__);               \
-    if (nvec <= 1024) return FN<__nv_bfloat16, 8, V2, true, 1024 / V2, S2, 1>(__VA_ARGS__);       \
-    return FN<__nv_bfloat16, 8, 2, true, 512, S2, 2>(__VA_ARGS__);                                \
-  }                                                                                               \
-  if (c.act_dtype == MOE_DTYPE_F32 && c.H % 4 == 0) {                                             \
-    const int nvec = c.H / 4;                                                                     \
-    if (nvec <= 32) return FN<float, 4, 1, true, 128, S1, 1>(__VA_ARGS__);                        \
-    if (nvec <= 256) return FN<float, 4, V1, true, 256 / V1, S1, 1>(__VA_ARGS__);                 \
-    if (nvec <= 512) return FN<float, 4, 2, true, 256, S2, 1>(__VA_ARGS__);                       \
-    if (nvec <= 1024) return FN<float, 4, 2, true, 512, S2, 1>(__VA_ARGS__);                      \
-    if (nvec <= 2048) return FN<float, 4, 2, true, 512, S2, 2>(__VA_ARGS__);                      \
-    return FN<float, 4, 2, true, 512, S2, 4>(__VA_ARGS__);                                        \
-  }                                                                                               \
+// Rows of H not a multiple of 16 bytes have pieces of 4 bytes (4 to 16 per thread); an odd number
+// of bf16 channels leaves nothing for cp.async to copy, and takes single elements without the ring.
+// STAGES: of the ring of 4-byte pieces.
+#define NORM_DISPATCH(FN, STAGES, ...)                                                            \
+  if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 8 == 0) return FN##_wide<__nv_bfloat16, 8>(__VA_ARGS__); \
+  if (c.act_dtype == MOE_DTYPE_F32 && c.H % 4 == 0) return FN##_wide<float, 4>(__VA_ARGS__);      \
   if (c.act_dtype == MOE_DTYPE_BF16 && c.H % 2 == 0) {                                            \
-    if (c.H <= 2048) return FN<__nv_bfloat16, 2, 4, true, 256, S4, 1>(__VA_ARGS__);               \
+    if (c.H <= 2048) return FN<__nv_bfloat16, 2, 4, true, 256, STAGES, 1>(__VA_ARGS__);           \
     return FN<__nv_bfloat16, 2, 8, false, 1024, 0, 1>(__VA_ARGS__);                               \
   }                                                                                               \
   if (c.act_dtype == MOE_DTYPE_BF16) {                                                            \
     if (c.H <= 2048) return FN<__nv_bfloat16, 1, 4, true, 512, 0, 1>(__VA_ARGS__);                \
     return FN<__nv_bfloat16, 1, 16, false, 1024, 0, 1>(__VA_ARGS__);                              \
   }                                                                                               \
-  if (c.H <= 1024) return FN<float, 1, 4, true, 256, S4, 1>(__VA_ARGS__);                         \
+  if (c.H <= 1024) return FN<float, 1, 4, true, 256, STAGES, 1>(__VA_ARGS__);                     \
   if (c.H <= 2048) return FN<float, 1, 4, true, 512, 0, 1>(__VA_ARGS__);                          \
   return FN<float, 1, 16, false, 1024, 0, 1>(__VA_ARGS__);
 
 cudaError_t launch_block_norm(const moe_norm_config_t& c, const NormIn& in, void* r, void* n, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  NORM_DISPATCH(fwd, 1, 1, 2, 2, 2, c, in, r, n, s)
+  NORM_DISPATCH(fwd, 2, c, in, r, n, s)
 }
 
 cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd& b, float* part, cudaStream_t s) {
@@ -697,7 +714,7 @@ cudaError_t launch_block_norm_backward(const moe_norm_config_t& c, const NormBwd
       if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)c.H * 4, s);
     return e;
   }
-  NORM_DISPATCH(bwd, 2, 2, 3, 3, 4, c, b, part, s)
+  NORM_DISPATCH(bwd, 4, c, b, part, s)
 }
 
 // Two sets of column sums for every row group of the largest grid: never more than one row
