@@ -21,7 +21,7 @@
 // each, and a product takes the six plane products above 2^-24 of it: x0 w0, x0 w1, x1 w0,
 // x0 w2, x1 w1, x2 w0, added in fp32 runs of 1024 elements. That is fp32 accuracy at a sixth of
 // the bf16 rate; exact fp32 FMA tiles reached 23 to 36 TFLOP/s (1024 x 1024 x 8192, forward and
-// backward: 2401 us). The planes of x and of one piece of w are laid out in the workspace, rows
+// backward: 2401 us, against 389). The planes of x and of one piece of w are laid out in the workspace, rows
 // padded to a multiple of 16 bytes; bf16 operands of a width that is not a multiple of 8 are
 // copied there too, as one plane (their dz has three).
 #include <cudaTypedefs.h>
@@ -69,16 +69,18 @@ struct HeadParams {
   int v0;              // first vocabulary row of the piece
   int w_row0;          // its row in the map of w (0 where the piece was laid out by itself)
   int V;
-  int terms;           // plane products per K stage of 64 elements, and the planes of A and B in
-  uint32_t a_code, b_code;  //   each of them, four bits a term from the first on
+  int a_planes, b_planes;  // of A and B in a K stage of 64 elements
+  int terms;           // plane products per K stage, and the planes of A and B in each of them,
+  uint32_t a_code, b_code;  //   four bits a term from the first on
   int a_plane, b_plane;  // rows from one plane of A and B to the next
   int a_bytes;         // of A in a stage: its map's box may have fewer than 128 rows
   const int32_t* target;
   // STATS: (max, sum) per token and half tile [2 n_tiles][T] - or, where all tiles have the same
   // rows (one m tile), per half of a CTA's or pair's tiles [2 units][T] - and the target's logit [T]
   float2* part;
-  int bn, stages;      // STATS on single CTAs: columns of a tile, a multiple of 16, and the ring's
-                       //   stages (of a_bytes and bn rows of w)
+  int bn;              // STATS on single CTAs: columns of a tile, a multiple of 16
+  int stages;          // of the ring, where they are sized at run time: there (a_bytes and bn rows of
+                       //   w), and with planes (all those of a K stage)
   float* target_logit;
   // DLOGITS
   const float *lse, *dloss;
@@ -95,12 +97,14 @@ struct HeadParams {
   uint64_t timeout_ns;
 };
 
+constexpr int kRingBytes = 192 * 1024;
+
 template <int CG, int BN>
 struct HeadSmem {
   static constexpr int kBBytes = (BN / CG) * BK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = kStageBytes > 32768 ? 4 : 6;  // 192 KB at most
-  static constexpr size_t kBytes = 1024 + (size_t)kStages * kStageBytes + 256 + kEpiWarps * 2048;
+  static constexpr int kStages = kRingBytes / kStageBytes;
+  static constexpr size_t kBytes = 1024 + kRingBytes + 256 + kEpiWarps * 2048;
 };
 
 // MN-major operand: 64-element MN blocks of the stage's 64 K rows (8 KB each, 128-byte swizzle).
@@ -250,14 +254,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kFlex = MODE == STATS && CG == 1 && NP == 1;
   constexpr int kMostStages = kFlex ? kMaxStages : S::kStages;
   const int bn_cols = kFlex ? p.bn : BN;
-  const int kStages = kFlex ? p.stages : S::kStages;
-  const int a_stride = kFlex ? p.a_bytes : kABytes, b_stride = kFlex ? bn_cols * BK * 2 : kBBytes;
+  const int kStages = kFlex || NP == 3 ? p.stages : S::kStages;
+  // a stage's planes lie one after the other, and a plane of A or B takes
+  const int a_bytes = kFlex ? p.a_bytes : kABytes, b_bytes = kFlex ? bn_cols * BK * 2 : kBBytes;
+  const int a_planes = NP == 3 ? p.a_planes : 1, b_planes = NP == 3 ? p.b_planes : 1;
+  const int a_stride = a_planes * a_bytes, b_stride = b_planes * b_bytes;
   extern __shared__ uint8_t smem_raw[];
   let_next_begin();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * a_stride;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kStages * kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRingBytes);
   uint64_t* full = bars;
   uint64_t* empty = bars + kMostStages;
   uint64_t* tfull = bars + 2 * kMostStages;
@@ -298,16 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const HeadShape h = head_shape<MODE>(p, TM);
   const int total_tiles = h.direct + (h.m_tiles * h.n_tiles - h.direct) * h.splits;
-  // The loss's logits and all sums of planes are added up in runs of kRun K stages: each run has
-  // its own accumulator, and the epilogue adds the runs in fp32. The tensor core's own additions
+  // The loss's logits and all sums of planes are added up in runs of kRun products of 64 elements:
+  // each run has its own accumulator, and the epilogue adds the runs in fp32. The tensor core's own additions
   // truncate: over 4096 elements in one go the loss was off by 3.4e-6 of its size, in runs of
   // 1024 by 6e-7. Where dz or the output is rounded to bf16, one go is good enough.
   constexpr bool kRuns = MODE == STATS || NP == 3;
-  const int terms = NP == 3 ? p.terms : 1;  // K stages per 64 elements
-  auto runs_of = [&](const HeadTile& t) { return kRuns ? ((t.kb1 - t.kb0) * terms + kRun - 1) / kRun : 1; };
-  auto run_end = [&](const HeadTile& t, int run) {
-    return kRuns ? min(t.kb1 * terms, t.kb0 * terms + (run + 1) * kRun) : t.kb1;
-  };
+  const int terms = NP == 3 ? p.terms : 1;
+  const int run_stages = kRun / terms;
+  auto runs_of = [&](const HeadTile& t) { return kRuns ? (t.kb1 - t.kb0 + run_stages - 1) / run_stages : 1; };
+  auto run_end = [&](const HeadTile& t, int run) { return kRuns ? min(t.kb1, t.kb0 + (run + 1) * run_stages) : t.kb1; };
 
   if (warp == 0) {
     // ======================= TMA producer (each CTA loads its own rows of A and its part of B)
@@ -319,38 +325,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
         const HeadTile t = head_tile<MODE>(tile, h);
         const int am = t.mb * TM + (int)rank * BM, bn = t.nb * bn_cols + (int)rank * (BN / CG);
-        int kb = t.kb0, term = 0;
-        for (int ks = t.kb0 * terms; ks < t.kb1 * terms; ++ks) {
-          const int pa = NP == 3 ? (int)(p.a_code >> (4 * term) & 3) * p.a_plane : 0;
-          const int pb = NP == 3 ? (int)(p.b_code >> (4 * term) & 3) * p.b_plane : 0;
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort, p.timeout_ns, p.status)) { ok = false; break; }
-          uint8_t* a_dst = sA + stage * a_stride;
-          uint8_t* b_dst = sB + stage * b_stride;
           uint32_t bar = 0;
           if constexpr (CG == 1) {
-            mbar_arrive_expect_tx(&full[stage], b_stride + p.a_bytes);
+            mbar_arrive_expect_tx(&full[stage], a_planes * p.a_bytes + b_stride);
           } else {
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (a_stride + b_stride));
             bar = mapa_shared(smem_addr(&full[stage]), 0);
           }
           auto load = [&](const CUtensorMap* m, uint8_t* dst, int x, int y) {
             if constexpr (CG == 1) tma_load_2d(m, dst, &full[stage], x, y);
             else tma_load_2d_pair(m, dst, bar, x, y);
           };
-          if constexpr (kAmn) {
-            load(&tmA, a_dst, am, pa + kb * BK);
-            load(&tmA, a_dst + 8192, am + 64, pa + kb * BK);
-          } else {
-            load(&tmA, a_dst, kb * BK, pa + am);
+          for (int pl = 0; pl < a_planes; ++pl) {
+            uint8_t* dst = sA + stage * a_stride + pl * a_bytes;
+            const int pa = NP == 3 ? pl * p.a_plane : 0;
+            if constexpr (kAmn) {
+              load(&tmA, dst, am, pa + kb * BK);
+              load(&tmA, dst + 8192, am + 64, pa + kb * BK);
+            } else {
+              load(&tmA, dst, kb * BK, pa + am);
+            }
           }
-          if constexpr (kBmn) {
-            const int y = pb + (MODE == DX ? p.w_row0 : 0) + kb * BK;
+          for (int pl = 0; pl < b_planes; ++pl) {
+            uint8_t* dst = sB + stage * b_stride + pl * b_bytes;
+            const int pb = NP == 3 ? pl * p.b_plane : 0;
+            if constexpr (kBmn) {
+              const int y = pb + (MODE == DX ? p.w_row0 : 0) + kb * BK;
 #pragma unroll
-            for (int j = 0; j < kBoxes; ++j) load(&tmB, b_dst + 8192 * j, bn + 64 * j, y);
-          } else {
-            load(&tmB, b_dst, kb * BK, pb + p.w_row0 + bn);
+              for (int j = 0; j < kBoxes; ++j) load(&tmB, dst + 8192 * j, bn + 64 * j, y);
+            } else {
+              load(&tmB, dst, kb * BK, pb + p.w_row0 + bn);
+            }
           }
-          if (++term == terms) { term = 0; ++kb; }
           ++issued;
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
@@ -374,24 +382,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = unit; tile < total_tiles && ok; tile += nunits) {
         const HeadTile t = head_tile<MODE>(tile, h);
-        int ks = t.kb0 * terms;
+        int kb = t.kb0;
         for (int run = 0; run < runs_of(t) && ok; ++run) {
           if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort, p.timeout_ns, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * BN;
-          const int first = ks, end = run_end(t, run);
-          for (; ks < end; ++ks) {
+          const int first = kb, end = run_end(t, run);
+          for (; kb < end; ++kb) {
             if (!mbar_wait(&full[stage], phase, abort, p.timeout_ns, p.status)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t a_addr = smem_addr(sA + stage * a_stride);
-            const uint32_t b_addr = smem_addr(sB + stage * b_stride);
+            const uint32_t a_stage = smem_addr(sA + stage * a_stride), b_stage = smem_addr(sB + stage * b_stride);
+            for (int term = 0; term < terms; ++term) {
+              const uint32_t a_addr = a_stage + (NP == 3 ? (p.a_code >> (4 * term) & 3) * a_bytes : 0);
+              const uint32_t b_addr = b_stage + (NP == 3 ? (p.b_code >> (4 * term) & 3) * b_bytes : 0);
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k) {
-              const uint64_t ad = kAmn ? desc_mn(a_addr + k * 2048) : desc_k_sw128(a_addr + k * 32);
-              const uint64_t bd = kBmn ? desc_mn(b_addr + k * 2048) : desc_k_sw128(b_addr + k * 32);
-              const uint32_t accumulate = ks > first || k > 0;
-              if constexpr (CG == 1) mma_bf16(d_tmem, ad, bd, idesc, accumulate);
-              else mma_bf16_pair(d_tmem, ad, bd, idesc, accumulate);
+              for (int k = 0; k < BK / 16; ++k) {
+                const uint64_t ad = kAmn ? desc_mn(a_addr + k * 2048) : desc_k_sw128(a_addr + k * 32);
+                const uint64_t bd = kBmn ? desc_mn(b_addr + k * 2048) : desc_k_sw128(b_addr + k * 32);
+                const uint32_t accumulate = kb > first || term > 0 || k > 0;
+                if constexpr (CG == 1) mma_bf16(d_tmem, ad, bd, idesc, accumulate);
+                else mma_bf16_pair(d_tmem, ad, bd, idesc, accumulate);
+              }
             }
             if constexpr (CG == 1) mma_commit(&empty[stage]);
             else mma_commit_pair(&empty[stage], 0x3);
@@ -1058,8 +1069,13 @@ __global__ void __launch_bounds__(256)
 }
 
 // The plane products of a GEMM: all six of fp32 operands; those of an operand of three planes (A)
-// with one of one; or one.
-void set_terms(HeadParams* p, int a_planes, int b_planes) {
+// with one of one; or one. A K stage brings every plane once for all of them (by itself for each
+// product, 256 x 128 tiles asked for 94 bytes a clock and SM, more than L2 gives: 1024 x 1024 x 8192
+// fp32, forward and backward, 506 us; 389 so).
+void set_terms(HeadParams* p, int a_planes, int b_planes, bool pair) {
+  p->a_planes = a_planes;
+  p->b_planes = b_planes;
+  p->stages = kRingBytes / (a_planes * kABytes + b_planes * (pair ? HeadSmem<2, 128>::kBBytes : HeadSmem<1, 128>::kBBytes));
   if (a_planes == 3 && b_planes == 3) {  // (0,2) (1,1) (2,0) (0,1) (1,0) (0,0)
     p->terms = 6;
     p->a_code = 0x010210;
@@ -1197,14 +1213,14 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
     HeadParams p = base_params(c.T, rows, c.H, tm, tn, st);
     p.v0 = (int)v0;
     p.V = c.V;
-    set_terms(&p, o.in_planes, o.in_planes);
+    set_terms(&p, o.in_planes, o.in_planes, !small_tokens(c.T));
     p.a_bytes = a_box(c.T) * BK * 2;
     p.a_plane = (int)o.x_plane;
     p.b_plane = (int)o.w_plane;
     p.target = target;
     p.follows = o.laid_out || v0 > 0;
     p.bn = tn;
-    p.stages = std::min<int>(kMaxStages, HeadSmem<1, 256>::kStages * HeadSmem<1, 256>::kStageBytes / (a_box(c.T) * BK * 2 + tn * BK * 2));
+    if (o.planes == 1) p.stages = std::min<int>(kMaxStages, kRingBytes / (a_box(c.T) * BK * 2 + tn * BK * 2));
     p.part = part + (int64_t)parts * c.T;
     p.target_logit = tl;
     CUtensorMap ma, mb;
@@ -1255,7 +1271,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     p.v0 = (int)v0;
     p.w_row0 = w_row0;
     p.V = c.V;
-    set_terms(&p, o.in_planes, o.in_planes);
+    set_terms(&p, o.in_planes, o.in_planes, !small_tokens(c.T));
     p.a_bytes = a_box(c.T) * BK * 2;
     p.a_plane = (int)o.x_plane;
     p.b_plane = (int)o.w_plane;
@@ -1274,7 +1290,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     if (dx) {  // M = T, N = H, K = the piece's rows
       p = base_params(c.T, c.H, rows, tm, tn, st);
       p.w_row0 = w_row0;
-      set_terms(&p, o.planes, o.in_planes);
+      set_terms(&p, o.planes, o.in_planes, !small_tokens(c.T));
       p.a_bytes = a_box(c.T) * BK * 2;
       p.a_plane = (int)o.dl_plane;
       p.b_plane = (int)o.w_plane;
@@ -1300,7 +1316,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     if (dw) {  // M = the piece's rows, N = H, K = T
       const int wn = o.planes == 3 ? 128 : 256;
       p = base_params(rows, c.H, c.T, 2 * BM, wn, st);
-      set_terms(&p, o.planes, o.in_planes);
+      set_terms(&p, o.planes, o.in_planes, true);
       p.a_plane = (int)o.dl_plane;
       p.b_plane = (int)o.x_plane;
       p.follows = 1;
