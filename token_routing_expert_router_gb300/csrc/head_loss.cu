@@ -19,9 +19,9 @@
 //
 // fp32 operands are split into three bf16 planes, v = v0 + v1 + v2 with 8 bits of the mantissa
 // each, and a product takes the six plane products above 2^-24 of it: x0 w0, x0 w1, x1 w0,
-// x0 w2, x1 w1, x2 w0, added in fp32 runs of 1024 elements. That is fp32 accuracy at a sixth of
+// x0 w2, x1 w1, x2 w0, and the stages of 64 elements added in fp32. That is fp32 accuracy at a sixth of
 // the bf16 rate; exact fp32 FMA tiles reached 23 to 36 TFLOP/s (1024 x 1024 x 8192, forward and
-// backward: 2401 us, against 389). The planes of x and of one piece of w are laid out in the workspace, rows
+// backward: 2401 us, against 421). The planes of x and of one piece of w are laid out in the workspace, rows
 // padded to a multiple of 16 bytes; bf16 operands of a width that is not a multiple of 8 are
 // copied there too, as one plane (their dz has three).
 #include <cudaTypedefs.h>
@@ -45,8 +45,6 @@ constexpr int kEpiWarps = 8;
 constexpr int kABytes = BM * BK * 2;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kRun = 16;  // K stages (of 64 elements) added by the tensor core in one go
-
 constexpr int kMaxStages = 12;  // of a ring whose stages are sized at run time
 constexpr int kMaxSplits = 32;  // of the K of a tile of dx (a lane of a warp tries each)
 constexpr int kNowhere = -(1 << 30);  // no column: far below the first of any tile
@@ -305,13 +303,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const HeadShape h = head_shape<MODE>(p, TM);
   const int total_tiles = h.direct + (h.m_tiles * h.n_tiles - h.direct) * h.splits;
-  // The loss's logits and all sums of planes are added up in runs of kRun products of 64 elements:
-  // each run has its own accumulator, and the epilogue adds the runs in fp32. The tensor core's own additions
-  // truncate: over 4096 elements in one go the loss was off by 3.4e-6 of its size, in runs of
-  // 1024 by 6e-7. Where dz or the output is rounded to bf16, one go is good enough.
+  // The loss's logits and all sums of planes are added up in runs: each has its own accumulator, and
+  // the epilogue adds the runs in fp32. The tensor core's own additions truncate: over 4096 elements
+  // in one go the loss was off by 3.4e-6 of its size, in runs of 1024 by 7e-7, of 512 by 3.6e-7, of
+  // 256 by 1.8e-7. 256 where reading w leaves the time (32 x 4096 x 131072: 171 us, 168 with 512),
+  // 512 from 128 tokens on (4096 x 4096 x 32000: 590 us, 566 with 1024, 645 with 256). All six
+  // products of one K stage of planes are a run, the big one last (dw of 256 x 128 x 5003: off by
+  // 4e-7, and 1.1e-6 with two stages; 1024 x 1024 x 8192 forward and backward 421 us, and 389).
+  // Where dz or the output is rounded to bf16, one go is good enough.
   constexpr bool kRuns = MODE == STATS || NP == 3;
   const int terms = NP == 3 ? p.terms : 1;
-  const int run_stages = kRun / terms;
+  const int run_stages = NP == 3 ? min(4, 6 / terms) : CG == 1 ? 4 : 8;
   auto runs_of = [&](const HeadTile& t) { return kRuns ? (t.kb1 - t.kb0 + run_stages - 1) / run_stages : 1; };
   auto run_end = [&](const HeadTile& t, int run) { return kRuns ? min(t.kb1, t.kb0 + (run + 1) * run_stages) : t.kb1; };
 
@@ -1071,7 +1073,7 @@ __global__ void __launch_bounds__(256)
 // The plane products of a GEMM: all six of fp32 operands; those of an operand of three planes (A)
 // with one of one; or one. A K stage brings every plane once for all of them (by itself for each
 // product, 256 x 128 tiles asked for 94 bytes a clock and SM, more than L2 gives: 1024 x 1024 x 8192
-// fp32, forward and backward, 506 us; 389 so).
+// fp32, forward and backward, 506 us; 421 so).
 void set_terms(HeadParams* p, int a_planes, int b_planes, bool pair) {
   p->a_planes = a_planes;
   p->b_planes = b_planes;
