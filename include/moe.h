@@ -543,7 +543,8 @@ typedef struct {
  * target [T] int32; loss, lse [T] fp32. The products run on the tensor cores: bf16 as it is,
  * fp32 as three bf16 planes per operand and the six products of planes above 2^-24 of the
  * whole (fp32 accuracy for finite operands; planes of a value beyond bf16's largest finite one,
- * 3.39e38, are not finite). fp32 operands, and bf16 ones with H % 8 != 0, are laid out in the
+ * 3.39e38, are not finite). The target's logit is a dot product in fp32 instead, here and in the
+ * backward: where the model is nearly certain, p - 1 is what is left of it and lse. fp32 operands, and bf16 ones with H % 8 != 0, are laid out in the
  * workspace first, w piece by piece. ws: moe_head_workspace_size bytes, used by both calls
  * (they need not share it). Deterministic. */
 moe_status_t moe_head_workspace_size(const moe_head_config_t* cfg, size_t* bytes);

@@ -3,12 +3,20 @@
 //   lse_t = log sum_v exp z_tv;  loss_t = lse_t - z_{t,target}
 //   dz_tv = (exp(z_tv - lse_t) - [v = target_t]) dloss_t;  dx = dz w;  dw = dz^T x
 // Forward: one GEMM whose epilogue keeps, per token and half tile of columns, the running
-// maximum and the sum of exponentials against it, and the target's logit; join_kernel puts the
-// halves together. Backward: piece after piece of the vocabulary, the GEMM is run again and its
-// epilogue turns the logits into dz (bf16, the operand of the next products), then
-// dx += dz w_piece and dw_piece = dz^T x; all of it over the tokens that count alone, which a first
-// kernel puts one after the other. Memory beside the inputs and outputs: one piece of dz
+// maximum and the sum of exponentials against it, without the target's; join_kernel puts the
+// halves and the target's logit together. Backward: piece after piece of the vocabulary, the GEMM
+// is run again and its epilogue turns the logits into dz (bf16, the operand of the next products),
+// then dx += dz w_piece and dw_piece = dz^T x; all of it over the tokens that count alone, which a
+// first kernel puts one after the other. Memory beside the inputs and outputs: one piece of dz
 // and 16 bytes per token and tile.
+//
+// The target's logit is a dot product of its own, in fp32 (target_dot), the same bits in both
+// directions. Where the model is nearly certain, the target's dz is p - 1 with p near 1, and lse is
+// the target's logit but for a small part; what is left of their difference is the error of one
+// against the other. With the tensor core's logits, which truncate (and by another amount in the
+// backward's longer runs), dx of tokens with a loss of 3e-5 was off by 164 % of itself, of 5e-3 by
+// 0.76 %; so by 1.1 % and 0.23 %, which is the rounding of lse and of dz. The dot products cost the
+// forward 3 us (in join_kernel: 32 x 4096 x 131072 174 us, 171 without), the backward a launch.
 //
 // All products run on the tensor cores (tcgen05): warp 0 feeds a ring of shared-memory stages
 // by TMA, warp 1 issues the MMAs into two TMEM accumulators, warps 2-9 are the epilogue of one
@@ -74,14 +82,14 @@ struct HeadParams {
   int a_bytes;         // of A in a stage: its map's box may have fewer than 128 rows
   const int32_t* target;
   // STATS: (max, sum) per token and half tile [2 n_tiles][T] - or, where all tiles have the same
-  // rows (one m tile), per half of a CTA's or pair's tiles [2 units][T] - and the target's logit [T]
+  // rows (one m tile), per half of a CTA's or pair's tiles [2 units][T] - without the target's logit
   float2* part;
   int bn;              // STATS on single CTAs: columns of a tile, a multiple of 16
   int stages;          // of the ring, where they are sized at run time: there (a_bytes and bn rows of
                        //   w), and with planes (all those of a K stage)
-  float* target_logit;
   // DLOGITS
   const float *lse, *dloss;
+  const float* target_logit;  // [T], from target_kernel
   // outputs of the other modes, and their row length in elements
   void* out;
   int64_t ldo;
@@ -458,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // dz or output values of the 32 columns from c0 of this warp's share on
       int tgt = -1;
       bool counts = false;
-      float lse = 0.0f, g = 0.0f;
+      float lse = 0.0f, g = 0.0f, hit = 0.0f;  // hit: DLOGITS, the target's p - 1
       if constexpr (MODE == STATS || MODE == DLOGITS) {
         const int token = MODE == DLOGITS && live ? p.index[row] : row;
         if (live) tgt = __ldg(p.target + token);
@@ -468,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lse = __ldg(p.lse + token);
           // the gradient of the mean: its factor 1 / count is left to the two products
           g = p.dloss ? __ldg(p.dloss + token) : 1.0f;
+          if (tgt >= col0 && tgt < col0 + kCols) hit = expm1f(p.target_logit[token] - lse);
         }
       } else {
         g = p.factor ? __ldg(p.factor) : 1.0f;
@@ -481,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) {
             // fp32 outputs follow p to its last bits; a dz that is rounded to bf16 does not
             const float e = NP == 3 ? expf(v[i] - lse) : ex2((v[i] - lse) * kLog2e);
-            const float pr = e - (i == at ? 1.0f : 0.0f);
+            const float pr = i == at ? hit : e;
             v[i] = counts && i < cols ? pr * g : 0.0f;
           }
           // columns past the vocabulary, and rows up to a whole K stage of dw, are written too, as
@@ -558,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (MODE == STATS) {
           // columns from here on that exist, in this tile
           const int cols = min(p.N - col0, bn_cols - cbase);
-          if (tgt >= col0 && tgt < col0 + min(kCols, cols)) {
+          if (tgt >= col0 && tgt < col0 + min(kCols, cols)) {  // its logit joins the sum later
 #pragma unroll
             for (int i = 0; i < kCols; ++i)
-              if (col0 + i == tgt) p.target_logit[row] = z(i);
+              if (col0 + i == tgt) zr[i / 32][i % 32] = __float_as_uint(-INFINITY);
           }
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
@@ -958,21 +967,59 @@ cudaError_t launch_planes(const void* src, int f32, int rows, int H, void* dst, 
   return cudaGetLastError();
 }
 
+// x . w of one row each, in fp32 by a warp: 8 sums a lane, then their tree. Every lane has the result.
+template <typename T>
+__device__ __forceinline__ float target_dot(const T* x, const T* w, int H, int lane) {
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int c = lane * 8; c < H; c += 256) {
+    float a[8], b[8];
+    load8(x, c, H, a);
+    load8(w, c, H, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = fmaf(a[i], b[i], sum[i]);
+  }
+  float r = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+#pragma unroll
+  for (int off = 16; off; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
+  return r;
+}
+
+// The backward's target logits [T], a warp per token that counts.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    target_kernel(const T* x, const T* w, const int32_t* target, int rows, int H, int V, float* logit) {
+  let_next_begin();
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (t < rows) {
+    const int32_t v = __ldg(target + t);
+    if (v >= 0 && v < V) {
+      const float z = target_dot(x + t * H, w + (int64_t)v * H, H, lane);
+      if (lane == 0) logit[t] = z;  // no kernel that may still run reads it
+    }
+  }
+  after_previous();  // this kernel's end is also that of those before it
+}
+
 // TOK tokens per block of 1024 threads, the other lanes over the halves: lse = max + log(sum),
-// the loss, and in the block that finishes last their mean over the tokens that count and its
+// the target's logit among them, the loss, and in the block that finishes last their mean over the tokens that count and its
 // reciprocal count. Few tokens take TOK = 4 (a token's 2000 halves of a large vocabulary in 8
 // steps), many TOK = 32 (256 bytes of a row of halves per step). Every lane's running (max, sum)
 // goes to shared memory, and one warp per token takes the maximum, then the sum.
-template <int TOK>
+template <int TOK, typename X>
 __global__ void __launch_bounds__(1024)
-    join_kernel(const float2* part, int parts, int T, int V, const int32_t* target, const float* target_logit,
+    join_kernel(const float2* part, int parts, int T, int H, int V, const X* x, const X* w, const int32_t* target,
                 float* loss, float* lse, float* mean, uint32_t* ticket, DeviceStatus* st) {
   constexpr int kLanes = 1024 / TOK, kAhead = 4;
   __shared__ float2 lanes[TOK][kLanes + 1];
   __shared__ bool finish;
-  after_previous();
   const int tok = threadIdx.x % TOK, lane = threadIdx.x / TOK, warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * TOK + tok;
+  const int64_t t = (int64_t)blockIdx.x * TOK + tok, tw = (int64_t)blockIdx.x * TOK + warp;  // tw: the warp's token
+  const int32_t tgt = warp < TOK && tw < T ? __ldg(target + tw) : -1;
+  const bool keep = tgt >= 0 && tgt < V;
+  const float hit = keep ? target_dot(x + tw * H, w + (int64_t)tgt * H, H, wl) : 0.0f;
+  after_previous();
   float m = -INFINITY, s = 0.0f;
   if (t < T) {
     for (int i0 = lane; i0 < parts; i0 += kLanes * kAhead) {
@@ -994,10 +1041,9 @@ __global__ void __launch_bounds__(1024)
   }
   lanes[tok][lane] = make_float2(m, s);
   __syncthreads();
-  const int64_t tw = (int64_t)blockIdx.x * TOK + warp;  // the warp's token
   if (warp < TOK && tw < T) {
     float2 v[kLanes / 32];
-    m = -INFINITY, s = 0.0f;
+    m = keep ? hit : -INFINITY, s = 0.0f;
 #pragma unroll
     for (int u = 0; u < kLanes / 32; ++u) {
       v[u] = lanes[warp][wl + 32 * u];
@@ -1010,12 +1056,12 @@ __global__ void __launch_bounds__(1024)
     for (int u = 0; u < kLanes / 32; ++u) s = fmaf(v[u].y, expf(v[u].x - base), s);
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (keep) s += expf(hit - base);
     if (wl == 0) {
       const float l = m + logf(s);
-      const int32_t tgt = target[tw];
       if (tgt >= V) set_status(st, MOE_ERR_DEVICE_BAD_INPUT, (int32_t)tw);
       lse[tw] = l;
-      loss[tw] = tgt >= 0 && tgt < V ? l - target_logit[tw] : 0.0f;
+      loss[tw] = keep ? l - hit : 0.0f;
       __threadfence();
     }
   }
@@ -1203,7 +1249,6 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
   const HeadScratch L = head_scratch(c);
   char* b = static_cast<char*>(ws);
   auto* part = reinterpret_cast<float2*>(b + L.part);
-  auto* tl = reinterpret_cast<float*>(b + L.target_logit);
   const Operands o = operands(c, L, x, w, b);
   const int tm = tile_rows(c.T), tn = stats_cols(c.T, c.V, o.planes);
   cudaError_t e = lay_out_x(c, o, x, s);
@@ -1224,7 +1269,6 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
     p.bn = tn;
     if (o.planes == 1) p.stages = std::min<int>(kMaxStages, kRingBytes / (a_box(c.T) * BK * 2 + tn * BK * 2));
     p.part = part + (int64_t)parts * c.T;
-    p.target_logit = tl;
     CUtensorMap ma, mb;
     if (!bf16_box(&ma, o.x, o.x_rows, o.cols, a_box(c.T)) || !bf16_box(&mb, o.w, o.w_rows, o.cols, tn / (tm / BM)))
       return cudaErrorInvalidValue;
@@ -1234,12 +1278,14 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
   if (e != cudaSuccess) return e;
   auto* ticket = reinterpret_cast<uint32_t*>(b + kHeadTicket);
   const float2* from = part;
-  const float* logits = tl;
-  if (c.T >= 1024)
-    return launch_after(join_kernel<32>, (unsigned)ceil_div(c.T, 32), 1024, s, from, parts, c.T, c.V, target, logits, loss, lse,
-                        mean, ticket, st);
-  return launch_after(join_kernel<4>, (unsigned)ceil_div(c.T, 4), 1024, s, from, parts, c.T, c.V, target, logits, loss, lse, mean,
-                      ticket, st);
+  auto join = [&](auto many, auto few, auto* xt) {
+    const auto* wt = static_cast<decltype(xt)>(w);
+    const int tok = c.T >= 1024 ? 32 : 4;
+    return launch_after(c.T >= 1024 ? many : few, (unsigned)ceil_div(c.T, tok), 1024, s, from, parts, c.T, c.H, c.V, xt, wt, target,
+                        loss, lse, mean, ticket, st);
+  };
+  return is_f32(c) ? join(join_kernel<32, float>, join_kernel<4, float>, static_cast<const float*>(x))
+                   : join(join_kernel<32, __nv_bfloat16>, join_kernel<4, __nv_bfloat16>, static_cast<const __nv_bfloat16*>(x));
 }
 
 cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
@@ -1260,9 +1306,17 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   const float* factor = mean ? mean + 1 : nullptr;
   auto* plan = reinterpret_cast<HeadPlan*>(b + L.plan);
   auto* index = reinterpret_cast<int32_t*>(b + L.index);
+  auto* logit = reinterpret_cast<float*>(b + L.target_logit);
   const SplitRule rule = split_rule(c.T, c.H, std::min<int64_t>(L.piece, c.V), o.planes);
   cudaError_t e = f32 ? launch_gather<float, 3>(c, o, x, target, index, plan, dx, rule, s)
                       : launch_gather<__nv_bfloat16, 1>(c, o, x, target, index, plan, dx, rule, s);
+  if (e == cudaSuccess) {
+    const dim3 grid((unsigned)ceil_div(c.T, 8));
+    e = f32 ? launch_after(target_kernel<float>, grid, 256, s, static_cast<const float*>(x), static_cast<const float*>(w), target,
+                           c.T, c.H, c.V, logit)
+            : launch_after(target_kernel<__nv_bfloat16>, grid, 256, s, static_cast<const __nv_bfloat16*>(x),
+                           static_cast<const __nv_bfloat16*>(w), target, c.T, c.H, c.V, logit);
+  }
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {
     const int rows = (int)std::min<int64_t>(L.piece, c.V - v0);
     if ((e = lay_out_w(c, o, w, v0, rows, s)) != cudaSuccess) break;
@@ -1280,6 +1334,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
     p.target = target;
     p.lse = lse;
     p.dloss = dloss;
+    p.target_logit = logit;
     p.plan = plan;
     p.index = index;
     p.follows = 1;
