@@ -596,33 +596,40 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Row-major [rows, cols] matrix, box of box_rows x box_cols, 128-byte swizzle.
-bool make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t rows, uint64_t cols,
-               uint32_t box_rows, uint32_t box_cols) {
+namespace {
+
+bool encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t rows, uint64_t cols,
+            uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle) {
   auto fn = encode_fn();
   if (!fn || rows == 0) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * (uint64_t)esize};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto run = [&] {
+    return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (run()) return true;
+  // a driver call, which needs a current context: a host thread whose first CUDA call this is has
+  // none yet (the runtime's own calls make it current)
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && run();
+}
+
+}  // namespace
+
+// Row-major [rows, cols] matrix, box of box_rows x box_cols, 128-byte swizzle.
+bool make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t rows, uint64_t cols,
+               uint32_t box_rows, uint32_t box_cols) {
+  return encode(m, base, dt, esize, rows, cols, box_rows, box_cols, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Row-major [rows, cols] matrix copied box by box without swizzle (the shared-memory copy
 // keeps the global byte order), e.g. the 512-byte MX scale atoms as rows of 128 uint32.
 bool make_tmap_linear(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t rows,
                       uint64_t cols, uint32_t box_rows, uint32_t box_cols) {
-  auto fn = encode_fn();
-  if (!fn || rows == 0) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * (uint64_t)esize};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode(m, base, dt, esize, rows, cols, box_rows, box_cols, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 namespace {
