@@ -47,6 +47,8 @@
  *    a bounded wait that expired) are written to a status word in the workspace; read it
  *    with moe_read_status.
  *  - Re-entrant as long as two calls in flight at once do not share a workspace.
+ *  - One device per process: what a launch needs of it (shared memory limits, resident blocks) is
+ *    asked for once. Only moe_route_static_scratch looks its array up for every device.
  *
  * Shapes: T tokens, H hidden, E routed experts, k experts per token, F expert FFN width.
  * R = T*k routed rows; with a shared expert the dispatch/expert buffers hold R + T rows,

@@ -35,6 +35,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "step.cuh"
 #include "tc_common.cuh"
@@ -648,11 +649,11 @@ template <int MODE, int CG, int BN, int NP>
 cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadParams& p, int* walkers, cudaStream_t s) {
   auto kern = head_gemm_kernel<MODE, CG, BN, NP>;
   const size_t smem = HeadSmem<CG, BN>::kBytes;
-  static bool attr_set = false;  // per instantiation
-  if (!attr_set) {
+  static std::atomic<bool> attr_set{false};  // per instantiation
+  if (!attr_set.load(std::memory_order_relaxed)) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    attr_set = true;
+    attr_set.store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(CG * (num_sms() / CG));
@@ -670,12 +671,14 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const HeadPa
   cfg.numAttrs = 1;
   int units = std::min(num_sms(), 152) / CG;  // the workspace has room for the sums of that many
   if (CG == 2) {  // a persistent grid must be resident all at once: no more pairs than fit together
-    static int max_pairs = 0;
-    if (!max_pairs) {
-      cudaError_t e = cudaOccupancyMaxActiveClusters(&max_pairs, kern, &cfg);
-      if (e != cudaSuccess || max_pairs <= 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
+    static std::atomic<int> max_pairs{0};
+    int pairs = max_pairs.load(std::memory_order_relaxed);
+    if (!pairs) {
+      cudaError_t e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+      if (e != cudaSuccess || pairs <= 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
+      max_pairs.store(pairs, std::memory_order_relaxed);
     }
-    units = std::min(units, max_pairs);
+    units = std::min(units, pairs);
   }
   // as many as the tiles there may be (those of dx up to split 32 ways)
   units = (int)std::min<int64_t>(units, (int64_t)p.m_tiles * p.n_tiles * (MODE == DX ? kMaxSplits : 1));
