@@ -7,8 +7,11 @@
 // halves and the target's logit together. Backward: piece after piece of the vocabulary, the GEMM
 // is run again and its epilogue turns the logits into dz (bf16, the operand of the next products),
 // then dx += dz w_piece and dw_piece = dz^T x; all of it over the tokens that count alone, which a
-// first kernel puts one after the other. Memory beside the inputs and outputs: one piece of dz
-// and 16 bytes per token and tile.
+// first kernel puts one after the other. The logits are never whole. In the workspace, besides
+// 12 bytes a token: (max, sum) of the half tiles, 16 bytes per token and 128 or 256 columns; the rows
+// of x that count; one piece of dz; with several pieces dx in fp32; where dx may be split, its
+// slices, up to 304 tiles of 256 x 256 fp32 (80 MB); of laid-out operands (below) x and a piece of w
+// in all their planes.
 //
 // The target's logit is a dot product of its own, in fp32 (target_dot), the same bits in both
 // directions. Where the model is nearly certain, the target's dz is p - 1 with p near 1, and lse is
@@ -249,7 +252,7 @@ template <int MODE, int CG, int BN, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const HeadParams p) {
   using S = HeadSmem<CG, BN>;
-  constexpr int kBBytes = S::kBBytes, kStageBytes = S::kStageBytes;
+  constexpr int kBBytes = S::kBBytes;
   constexpr int TM = BM * CG;
   constexpr int kTmemCols = 2 * BN;
   constexpr bool kAmn = MODE == DW;                 // A read MN-major (its rows are the K index)
@@ -831,17 +834,18 @@ __global__ void __launch_bounds__(256)
 // 256 x 256) and the launch that adds them. At most four rounds of slices.
 struct SplitRule {
   int tm, tn, units, planes, n_tiles, kblocks;
+  bool can;  // there is room for slices
   __host__ __device__ float stage() const { return 0.14f * tn / 256 * (planes == 3 ? 6 : 1); }
   __host__ __device__ float slice() const { return 0.08f * tm * tn / 65536; }
   // Whether a split into any number could pay, for any number of rows.
-  bool may_split() const { return kblocks * stage() > 4.0f + 2.0f * sqrtf(kblocks * stage() * slice()); }
+  bool could_pay() const { return kblocks * stage() > 4.0f + 2.0f * sqrtf(kblocks * stage() * slice()); }
   // By a whole warp, a number of splits per lane.
   __device__ HeadPlan of(int rows) const {
     const int lane = threadIdx.x & 31, s = lane + 1;
     const int tiles = (rows + tm - 1) / tm * n_tiles, tail = tiles % units;
     float least = INFINITY;
     if (s == 1) least = kblocks * stage();
-    else if (tail && s * 4 <= kblocks && tail * s <= 4 * units)
+    else if (can && tail && s * 4 <= kblocks && tail * s <= 4 * units)
       least = (float)((tail * s + units - 1) / units) * ((kblocks + s - 1) / s) * stage() + tail * s * slice() + 4.0f;
     int best = s;
 #pragma unroll
@@ -859,7 +863,9 @@ struct SplitRule {
 };
 SplitRule split_rule(int64_t T, int64_t H, int64_t rows, int planes) {
   const int tm = tile_rows(T), tn = tile_cols(T, planes);
-  return {tm, tn, small_tokens(T) ? 152 : 76, planes, (int)ceil_div(H, tn), (int)ceil_div(rows, BK)};
+  SplitRule r{tm, tn, small_tokens(T) ? 152 : 76, planes, (int)ceil_div(H, tn), (int)ceil_div(rows, BK), false};
+  r.can = r.could_pay();
+  return r;
 }
 
 // The backward's first kernel: the rows of x whose tokens count, one after the other, in dst
@@ -1160,12 +1166,13 @@ namespace {
 bool is_f32(const moe_head_config_t& c) { return c.act_dtype == MOE_DTYPE_F32; }
 bool laid_out(const moe_head_config_t& c) { return is_f32(c) || c.H % 8; }
 int planes_of(const moe_head_config_t& c) { return laid_out(c) ? 3 : 1; }  // of dz
+int in_planes_of(const moe_head_config_t& c) { return is_f32(c) ? 3 : 1; }   // of x and w
 int64_t padded_tokens(const moe_head_config_t& c) { return align_up((size_t)c.T, 64); }  // whole K stages of dw
 
 tc::Operands operands(const moe_head_config_t& c, const HeadScratch& L, const void* x, const void* w, char* ws) {
   tc::Operands o{};
   o.planes = planes_of(c);
-  o.in_planes = is_f32(c) ? 3 : 1;
+  o.in_planes = in_planes_of(c);
   o.laid_out = laid_out(c);
   o.cols = o.laid_out ? (int64_t)align_up((size_t)c.H, 8) : c.H;
   o.x_plane = o.laid_out ? padded_tokens(c) : c.T;
@@ -1218,7 +1225,7 @@ cudaError_t lay_out_w(const moe_head_config_t& c, const tc::Operands& o, const v
 HeadScratch head_scratch(const moe_head_config_t& c) {
   HeadScratch L{};
   const bool lay = laid_out(c);
-  const int64_t T = std::max<int64_t>(padded_tokens(c), 1), Hp = align_up((size_t)c.H, 8), np = planes_of(c);
+  const int64_t T = std::max<int64_t>(padded_tokens(c), 1), Hp = align_up((size_t)c.H, 8), np = planes_of(c), ip = in_planes_of(c);
   const int64_t row_bytes = 2 * np * (T + (lay ? Hp : 0));
   int64_t piece = c.piece > 0 ? c.piece : std::max<int64_t>(4096, (256ll << 20) / row_bytes);
   piece = (int64_t)align_up((size_t)std::min<int64_t>(piece, c.V), 256);
@@ -1235,12 +1242,12 @@ HeadScratch head_scratch(const moe_head_config_t& c) {
   L.target_logit = take((size_t)T * 4);
   L.plan = take(sizeof(tc::HeadPlan));
   L.index = take((size_t)(T + ceil_div(T, tc::kChunk)) * 4);  // and the chunks' counts
-  L.x = take((size_t)(np * T * Hp * 2));
-  L.w = take(lay ? (size_t)(np * piece * Hp * 2) : 0);
+  L.x = take((size_t)(ip * T * Hp * 2));
+  L.w = take(lay ? (size_t)(ip * piece * Hp * 2) : 0);
   L.dlogits = take((size_t)(np * T * piece * 2));
   L.dx = take(piece >= c.V ? 0 : (size_t)T * c.H * 4);
   const tc::SplitRule rule = tc::split_rule(T, c.H, std::min<int64_t>(piece, c.V), (int)np);
-  L.slices = take((size_t)rule.most_slices(T) * rule.tm * rule.tn * 4);
+  L.slices = take(rule.can ? (size_t)rule.most_slices(T) * rule.tm * rule.tn * 4 : 0);
   L.total = o;
   return L;
 }
@@ -1366,7 +1373,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
       p.factor = factor;
       if (!bf16_box(&ma, dl, o.dl_rows, L.ld, a_box(c.T)) || !bf16_box(&mb, o.w, o.w_rows, o.cols, 64)) return cudaErrorInvalidValue;
       if ((e = launch_mode<DX>(c.T, o.planes, ma, mb, p, s)) != cudaSuccess) break;
-      if (rule.may_split()) {  // how many tiles are is known on the device; fewer than a round
+      if (rule.can) {  // how many tiles are is known on the device; fewer than a round
         const dim3 grid((unsigned)(tm * tn / 1024), (unsigned)std::min(p.m_tiles * p.n_tiles, rule.units - 1));
         e = p.out_f32 ? launch_after(join_slices_kernel<float>, grid, 256, s, p, tm, tn, static_cast<float*>(p.out))
                       : launch_after(join_slices_kernel<__nv_bfloat16>, grid, 256, s, p, tm, tn, static_cast<__nv_bfloat16*>(p.out));

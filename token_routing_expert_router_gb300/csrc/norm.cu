@@ -13,7 +13,8 @@
 // meanwhile is bound by them; so the forward takes two rows through its two sums together, and
 // the backward adds up one row while it finishes the row before. Products go two at a time
 // (fma.f32x2): with the weights and conversions a row is otherwise near the issue limit.
-// Widths that are not a multiple of 16 bytes take plain element loads (VEC = 1).
+// Widths that are not a multiple of 16 bytes move in pieces of 4 bytes, through the ring up to 2048
+// (bf16) or 1024 (fp32) channels; odd bf16 widths in plain 2-byte loads.
 #include <algorithm>
 #include <atomic>
 
