@@ -273,8 +273,9 @@ def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
     import torch
-    # the raw handle: a Stream object would cost about as much as a kernel launch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the raw handle, where this torch has the call: a Stream object costs about as much as a kernel launch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _check(code: int, where: str):
