@@ -6,20 +6,21 @@
 // maximum and the sum of exponentials against it, without the target's; join_kernel puts the
 // halves and the target's logit together. Backward: piece after piece of the vocabulary, the GEMM
 // is run again and its epilogue turns the logits into dz (bf16, the operand of the next products),
-// then dx += dz w_piece and dw_piece = dz^T x; all of it over the tokens that count alone, which a
-// first kernel puts one after the other. The logits are never whole. In the workspace, besides
+// then dx += dz w_piece and dw_piece = dz^T x; all of it over the tokens that count alone, which
+// gather_kernel puts one after the other. The logits are never whole. In the workspace, besides
 // 12 bytes a token: (max, sum) of the half tiles, 16 bytes per token and 128 or 256 columns; the rows
 // of x that count; one piece of dz; with several pieces dx in fp32; where dx may be split, its
 // slices, up to 304 tiles of 256 x 256 fp32 (80 MB); of laid-out operands (below) x and a piece of w
 // in all their planes.
 //
-// The target's logit is a dot product of its own, in fp32 (target_dot), the same bits in both
+// The target's logit is a dot product of its own, in fp32 (target_logits), the same bits in both
 // directions. Where the model is nearly certain, the target's dz is p - 1 with p near 1, and lse is
 // the target's logit but for a small part; what is left of their difference is the error of one
 // against the other. With the tensor core's logits, which truncate (and by another amount in the
 // backward's longer runs), dx of tokens with a loss of 3e-5 was off by 164 % of itself, of 5e-3 by
-// 0.76 %; so by 1.1 % and 0.23 %, which is the rounding of lse and of dz. The dot products cost the
-// forward 3 us (in join_kernel: 32 x 4096 x 131072 174 us, 171 without), the backward a launch.
+// 0.76 %; so by 1.1 % and 0.23 %, which is the rounding of lse and of dz. The dot products run beside
+// the forward's GEMM and in the backward's first launch: nothing up to some hundred tokens, 8 us of
+// 4096 x 4096 x 32000 forward (596 us).
 //
 // All products run on the tensor cores (tcgen05): warp 0 feeds a ring of shared-memory stages
 // by TMA, warp 1 issues the MMAs into two TMEM accumulators, warps 2-9 are the epilogue of one
@@ -63,7 +64,7 @@ constexpr int kNowhere = -(1 << 30);  // no column: far below the first of any t
 
 enum Mode { STATS = 0, DLOGITS = 1, DX = 2, DW = 3 };
 
-// What the backward's first kernel finds: the tokens that count, and how the tiles of dx are split.
+// What the backward's gather_kernel finds: the tokens that count, and how the tiles of dx are split.
 struct HeadPlan {
   int rows;    // tokens that count: rows of x's copy, of dz, and of dx before they go to their places
   int direct;  // DX: the first `direct` tiles are whole; the K of each further one is split over
@@ -93,7 +94,7 @@ struct HeadParams {
                        //   w), and with planes (all those of a K stage)
   // DLOGITS
   const float *lse, *dloss;
-  const float* target_logit;  // [T], from target_kernel
+  const float* target_logit;  // [T], from gather_kernel
   // outputs of the other modes, and their row length in elements
   void* out;
   int64_t ldo;
@@ -868,13 +869,63 @@ SplitRule split_rule(int64_t T, int64_t H, int64_t rows, int planes) {
   return r;
 }
 
+// The logits of the targets, logit[t] = x_t . w_target in fp32 for the tokens that count, from token
+// `first` on: `warps` warps to a token (1, or 4 for rows of more than four pieces a lane), 8 sums a
+// lane, then their tree. By a whole block of kWarps warps; the same bits wherever a token stands.
+int target_warps(int H) { return H <= 1024 ? 1 : 4; }
+template <int kWarps, typename T>
+__device__ __forceinline__ void target_logits(const T* x, const T* w, const int32_t* target, int64_t first, int rows, int H,
+                                              int V, int warps, float* logit) {
+  __shared__ float part[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = first + warp / warps;
+  const int32_t v = t < rows ? __ldg(target + t) : -1;
+  const bool counts = v >= 0 && v < V;
+  float r = 0.0f;
+  if (counts) {
+    const T *xr = x + t * H, *wr = w + (int64_t)v * H;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+    for (int c = (warp % warps * 32 + lane) * 8; c < H; c += warps * 256) {
+      float a[8], b[8];
+      load8(xr, c, H, a);
+      load8(wr, c, H, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = fmaf(a[i], b[i], sum[i]);
+    }
+    r = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
+  if (warps > 1) {
+    if (lane == 0) part[warp] = r;
+    __syncthreads();
+    const float* p = part + warp / 4 * 4;
+    r = (p[0] + p[1]) + (p[2] + p[3]);
+  }
+  if (counts && lane == 0 && warp % warps == 0) logit[t] = r;
+}
+
+// The forward's, launched behind the GEMM, beside which its small blocks run: nothing that may still
+// run reads or writes what it touches, so it waits for the kernels before it only at its end. (In
+// join_kernel the dot products took 8 us of 64 x 4096 x 32000, which takes 55.)
+constexpr int kTargetWarps = 4;
+template <typename T>
+__global__ void __launch_bounds__(32 * kTargetWarps)
+    target_kernel(const T* x, const T* w, const int32_t* target, int rows, int H, int V, int warps, float* logit) {
+  let_next_begin();
+  target_logits<kTargetWarps>(x, w, target, (int64_t)blockIdx.x * (kTargetWarps / warps), rows, H, V, warps, logit);
+  after_previous();  // this kernel's end is also that of those before it
+}
+
 // The backward's first kernel: the rows of x whose tokens count, one after the other, in dst
 // [planes][rows_pad][Hp] (with zeros up to a whole K stage), their tokens in index, the plan, and
 // zeros in the rows of dx whose tokens do not count. What is left out costs the products nothing
 // (1500 x 2048 x 50257 with 60 % left out, forward and backward: 505 us, 743 with zeros for them),
 // and a NaN or infinity in a padded row of x meets no other row. A block takes 16 tokens and 512
 // columns; it counts those of the tokens before its own by itself, from the first or, beyond 65536
-// tokens, from the last whole chunk of 4096 on and over the chunks' counts (chunk; else NULL).
+// tokens, from the last whole chunk of 4096 on and over the chunks' counts (chunk; else NULL). The
+// blocks past the first `gathers` of a slab form the targets' logits instead, 8 or 2 tokens each.
 constexpr int kGather = 16, kGatherCols = 512, kItems = kGather * kGatherCols / 8 / 256;
 constexpr int kChunk = 4096, kCountFrom = 65536;
 __global__ void __launch_bounds__(256) count_kernel(const int32_t* target, int rows, int V, int32_t* chunk) {
@@ -897,10 +948,16 @@ __global__ void __launch_bounds__(256) count_kernel(const int32_t* target, int r
 
 template <typename T, int NP>
 __global__ void __launch_bounds__(256)
-    gather_kernel(const T* x, const int32_t* target, int rows, int H, int V, __nv_bfloat16* dst, int64_t plane, int Hp,
-                  const int32_t* chunk, int32_t* index, HeadPlan* plan, T* dx, SplitRule rule) {
+    gather_kernel(const T* x, const T* w, const int32_t* target, int rows, int H, int V, __nv_bfloat16* dst, int64_t plane, int Hp,
+                  const int32_t* chunk, int32_t* index, HeadPlan* plan, T* dx, SplitRule rule, int gathers, int warps,
+                  float* logit) {
   let_next_begin();
   if (chunk) after_previous();
+  if ((int)blockIdx.x >= gathers) {
+    const int64_t block = (int64_t)(blockIdx.x - gathers) * gridDim.y + blockIdx.y;
+    target_logits<8>(x, w, target, block * (8 / warps), rows, H, V, warps, logit);
+    return;
+  }
   __shared__ int32_t before, place[kGather];
   const int first = blockIdx.x * kGather, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int live = min(kGather, rows - first);
@@ -950,16 +1007,17 @@ __global__ void __launch_bounds__(256)
       }
     }
   }
-  if (blockIdx.x != gridDim.x - 1) return;
-  const int total = before + __popc(mask);
-  if (blockIdx.y == 0 && warp == 7) {
-    const HeadPlan made = rule.of(total);
-    if (lane == 0) *plan = made;
+  if ((int)blockIdx.x == gathers - 1) {
+    const int total = before + __popc(mask);
+    if (blockIdx.y == 0 && warp == 7) {
+      const HeadPlan made = rule.of(total);
+      if (lane == 0) *plan = made;
+    }
+    float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int to = (total + BK - 1) / BK * BK;
+    for (int e = threadIdx.x; e < (to - total) * per; e += 256)
+      store_planes<NP>(dst + (int64_t)(total + e / per) * Hp + c0 + e % per * 8, plane, zero);
   }
-  float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  const int to = (total + BK - 1) / BK * BK;
-  for (int e = threadIdx.x; e < (to - total) * per; e += 256)
-    store_planes<NP>(dst + (int64_t)(total + e / per) * Hp + c0 + e % per * 8, plane, zero);
 }
 
 cudaError_t launch_planes(const void* src, int f32, int rows, int H, void* dst, int64_t plane, int Hp, int zero_to,
@@ -976,50 +1034,14 @@ cudaError_t launch_planes(const void* src, int f32, int rows, int H, void* dst, 
   return cudaGetLastError();
 }
 
-// x . w of one row each, in fp32 by a warp: 8 sums a lane, then their tree. Every lane has the result.
-template <typename T>
-__device__ __forceinline__ float target_dot(const T* x, const T* w, int H, int lane) {
-  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-  for (int c = lane * 8; c < H; c += 256) {
-    float a[8], b[8];
-    load8(x, c, H, a);
-    load8(w, c, H, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = fmaf(a[i], b[i], sum[i]);
-  }
-  float r = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
-#pragma unroll
-  for (int off = 16; off; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
-  return r;
-}
-
-// The backward's target logits [T], a warp per token that counts.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    target_kernel(const T* x, const T* w, const int32_t* target, int rows, int H, int V, float* logit) {
-  let_next_begin();
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (t < rows) {
-    const int32_t v = __ldg(target + t);
-    if (v >= 0 && v < V) {
-      const float z = target_dot(x + t * H, w + (int64_t)v * H, H, lane);
-      if (lane == 0) logit[t] = z;  // no kernel that may still run reads it
-    }
-  }
-  after_previous();  // this kernel's end is also that of those before it
-}
-
 // TOK tokens per block of 1024 threads, the other lanes over the halves: lse = max + log(sum),
 // the target's logit among them, the loss, and in the block that finishes last their mean over the tokens that count and its
 // reciprocal count. Few tokens take TOK = 4 (a token's 2000 halves of a large vocabulary in 8
 // steps), many TOK = 32 (256 bytes of a row of halves per step). Every lane's running (max, sum)
 // goes to shared memory, and one warp per token takes the maximum, then the sum.
-template <int TOK, typename X>
+template <int TOK>
 __global__ void __launch_bounds__(1024)
-    join_kernel(const float2* part, int parts, int T, int H, int V, const X* x, const X* w, const int32_t* target,
-                float* loss, float* lse, float* mean, uint32_t* ticket, DeviceStatus* st) {
+    join_kernel(const float2* part, int parts, int T, int V, const int32_t* target, const float* target_logit, float* loss, float* lse, float* mean, uint32_t* ticket, DeviceStatus* st) {
   constexpr int kLanes = 1024 / TOK, kAhead = 4;
   __shared__ float2 lanes[TOK][kLanes + 1];
   __shared__ bool finish;
@@ -1027,8 +1049,8 @@ __global__ void __launch_bounds__(1024)
   const int64_t t = (int64_t)blockIdx.x * TOK + tok, tw = (int64_t)blockIdx.x * TOK + warp;  // tw: the warp's token
   const int32_t tgt = warp < TOK && tw < T ? __ldg(target + tw) : -1;
   const bool keep = tgt >= 0 && tgt < V;
-  const float hit = keep ? target_dot(x + tw * H, w + (int64_t)tgt * H, H, wl) : 0.0f;
   after_previous();
+  const float hit = keep ? target_logit[tw] : 0.0f;
   float m = -INFINITY, s = 0.0f;
   if (t < T) {
     for (int i0 = lane; i0 < parts; i0 += kLanes * kAhead) {
@@ -1191,25 +1213,28 @@ cudaError_t lay_out_x(const moe_head_config_t& c, const tc::Operands& o, const v
   if (!o.laid_out) return cudaSuccess;
   return tc::launch_planes(x, is_f32(c), c.T, c.H, const_cast<void*>(o.x), o.x_plane * o.cols, (int)o.cols, (int)o.x_plane, false, s);
 }
-// x's rows that count to o.x, and what else the backward's first kernel does.
+// x's rows that count to o.x, the targets' logits, and what else the backward's first kernel does.
 template <typename T, int NP>
-cudaError_t launch_gather(const moe_head_config_t& c, const tc::Operands& o, const void* x, const int32_t* target,
-                          int32_t* index, tc::HeadPlan* plan, void* dx, const tc::SplitRule& rule, cudaStream_t s) {
-  const dim3 grid((unsigned)ceil_div(c.T, tc::kGather), (unsigned)ceil_div(o.cols, tc::kGatherCols));
-  const auto* from = static_cast<const T*>(x);
+cudaError_t launch_gather(const moe_head_config_t& c, const tc::Operands& o, const void* x, const void* w, const int32_t* target,
+                          int32_t* index, tc::HeadPlan* plan, void* dx, float* logit, const tc::SplitRule& rule, cudaStream_t s) {
+  const int gathers = (int)ceil_div(c.T, tc::kGather), slabs = (int)ceil_div(o.cols, tc::kGatherCols);
+  const int warps = tc::target_warps(c.H);
+  const dim3 grid((unsigned)(gathers + ceil_div(ceil_div(c.T, 8 / warps), slabs)), (unsigned)slabs);
+  const auto *from = static_cast<const T*>(x), *wt = static_cast<const T*>(w);
   auto* to = static_cast<__nv_bfloat16*>(const_cast<void*>(o.x));
   auto* none = static_cast<T*>(dx);
   const int64_t plane = o.x_plane * o.cols;
   if (c.T <= tc::kCountFrom) {
-    tc::gather_kernel<T, NP><<<grid, 256, 0, s>>>(from, target, c.T, c.H, c.V, to, plane, (int)o.cols, nullptr, index, plan, none, rule);
+    tc::gather_kernel<T, NP><<<grid, 256, 0, s>>>(from, wt, target, c.T, c.H, c.V, to, plane, (int)o.cols, nullptr, index, plan, none,
+                                                  rule, gathers, warps, logit);
     return cudaGetLastError();
   }
   int32_t* chunk = index + padded_tokens(c);
   tc::count_kernel<<<(unsigned)ceil_div(c.T, tc::kChunk), 256, 0, s>>>(target, c.T, c.V, chunk);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_after(tc::gather_kernel<T, NP>, grid, 256, s, from, target, c.T, c.H, c.V, to, plane, (int)o.cols, chunk, index,
-                      plan, none, rule);
+  return launch_after(tc::gather_kernel<T, NP>, grid, 256, s, from, wt, target, c.T, c.H, c.V, to, plane, (int)o.cols, chunk, index,
+                      plan, none, rule, gathers, warps, logit);
 }
 
 cudaError_t lay_out_w(const moe_head_config_t& c, const tc::Operands& o, const void* w, int64_t v0, int rows, cudaStream_t s) {
@@ -1288,14 +1313,21 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
   if (e != cudaSuccess) return e;
   auto* ticket = reinterpret_cast<uint32_t*>(b + kHeadTicket);
   const float2* from = part;
-  auto join = [&](auto many, auto few, auto* xt) {
-    const auto* wt = static_cast<decltype(xt)>(w);
-    const int tok = c.T >= 1024 ? 32 : 4;
-    return launch_after(c.T >= 1024 ? many : few, (unsigned)ceil_div(c.T, tok), 1024, s, from, parts, c.T, c.H, c.V, xt, wt, target,
-                        loss, lse, mean, ticket, st);
+  auto* logit = reinterpret_cast<float*>(b + L.target_logit);
+  auto targets = [&](auto kern, auto* xt) {
+    const int warps = target_warps(c.H);
+    return launch_after(kern, (unsigned)ceil_div(c.T, kTargetWarps / warps), 32 * kTargetWarps, s, xt, static_cast<decltype(xt)>(w),
+                        target, c.T, c.H, c.V, warps, logit);
   };
-  return is_f32(c) ? join(join_kernel<32, float>, join_kernel<4, float>, static_cast<const float*>(x))
-                   : join(join_kernel<32, __nv_bfloat16>, join_kernel<4, __nv_bfloat16>, static_cast<const __nv_bfloat16*>(x));
+  e = is_f32(c) ? targets(target_kernel<float>, static_cast<const float*>(x))
+                : targets(target_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16*>(x));
+  if (e != cudaSuccess) return e;
+  const float* logits = logit;
+  if (c.T >= 1024)
+    return launch_after(join_kernel<32>, (unsigned)ceil_div(c.T, 32), 1024, s, from, parts, c.T, c.V, target, logits, loss, lse,
+                        mean, ticket, st);
+  return launch_after(join_kernel<4>, (unsigned)ceil_div(c.T, 4), 1024, s, from, parts, c.T, c.V, target, logits, loss, lse, mean,
+                      ticket, st);
 }
 
 cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
@@ -1318,15 +1350,8 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
   auto* index = reinterpret_cast<int32_t*>(b + L.index);
   auto* logit = reinterpret_cast<float*>(b + L.target_logit);
   const SplitRule rule = split_rule(c.T, c.H, std::min<int64_t>(L.piece, c.V), o.planes);
-  cudaError_t e = f32 ? launch_gather<float, 3>(c, o, x, target, index, plan, dx, rule, s)
-                      : launch_gather<__nv_bfloat16, 1>(c, o, x, target, index, plan, dx, rule, s);
-  if (e == cudaSuccess) {
-    const dim3 grid((unsigned)ceil_div(c.T, 8));
-    e = f32 ? launch_after(target_kernel<float>, grid, 256, s, static_cast<const float*>(x), static_cast<const float*>(w), target,
-                           c.T, c.H, c.V, logit)
-            : launch_after(target_kernel<__nv_bfloat16>, grid, 256, s, static_cast<const __nv_bfloat16*>(x),
-                           static_cast<const __nv_bfloat16*>(w), target, c.T, c.H, c.V, logit);
-  }
+  cudaError_t e = f32 ? launch_gather<float, 3>(c, o, x, w, target, index, plan, dx, logit, rule, s)
+                      : launch_gather<__nv_bfloat16, 1>(c, o, x, w, target, index, plan, dx, logit, rule, s);
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {
     const int rows = (int)std::min<int64_t>(L.piece, c.V - v0);
     if ((e = lay_out_w(c, o, w, v0, rows, s)) != cudaSuccess) break;
