@@ -558,8 +558,9 @@ moe_status_t moe_head_loss(const moe_head_config_t* cfg, const void* x, const vo
  * dloss [T] fp32: the gradient of every token's loss; or NULL, and mean (from moe_head_loss)
  * makes it the gradient of the mean loss. Exactly one of the two is given. dx [T, H] act and
  * dw [V, H] grad_dtype are overwritten (either may be NULL). For bf16 operands in place
- * dz is rounded to bf16, the operand type of its two products, which accumulate in fp32; with
- * laid-out operands it has three planes as well. */
+ * dz is rounded to bf16, the operand type of its two products, which accumulate in fp32 (dw is then
+ * off by up to 1.6e-3 by norm, whatever its type); with laid-out operands, as all fp32 ones are, it
+ * has three planes as well. */
 moe_status_t moe_head_loss_backward(const moe_head_config_t* cfg, const void* x, const void* w, const int32_t* target,
                                     const float* lse, const float* dloss, const float* mean, void* dx, void* dw,
                                     void* ws, moe_stream_t stream);
@@ -606,7 +607,7 @@ moe_status_t moe_grad_clip_workspace_size(int32_t count, size_t* bytes);
 moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t count, float* norm, void* ws, moe_stream_t stream);
 
 /* moe_grad_norm, then out = grad * min(1, max_norm / norm) for every gradient (max_norm > 0).
- * A gradient in place is not touched when the factor is 1. With a non-finite norm the factor
+ * A gradient in place is not written when the factor is 1. With a non-finite norm the factor
  * is 1: the caller sees the norm (or the status) and drops the step. */
 moe_status_t moe_grad_clip(const moe_grad_t* grads, int32_t count, float max_norm, float* norm, void* ws,
                            moe_stream_t stream);

@@ -8,7 +8,7 @@
 // is run again and its epilogue turns the logits into dz (bf16, the operand of the next products),
 // then dx += dz w_piece and dw_piece = dz^T x; all of it over the tokens that count alone, which
 // gather_kernel puts one after the other. The logits are never whole. In the workspace, besides
-// 12 bytes a token: (max, sum) of the half tiles, 16 bytes per token and 128 or 256 columns; the rows
+// 8 bytes a token: (max, sum) of the half tiles, 16 bytes per token and 128 or 256 columns; the rows
 // of x that count; one piece of dz; with several pieces dx in fp32; where dx may be split, its
 // slices, up to 304 tiles of 256 x 256 fp32 (80 MB); of laid-out operands (below) x and a piece of w
 // in all their planes.
@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 512 from 128 tokens on (4096 x 4096 x 32000: 590 us, 566 with 1024, 645 with 256). All six
   // products of one K stage of planes are a run, the big one last (dw of 256 x 128 x 5003: off by
   // 4e-7, and 1.1e-6 with two stages; 1024 x 1024 x 8192 forward and backward 421 us, and 389).
-  // Where dz or the output is rounded to bf16, one go is good enough.
+  // Where dz is rounded to bf16 for the next products (which leaves dw off by up to 1.6e-3 by norm,
+  // in fp32 too), one go is good enough: those 256 steps of 16 lose 0.2 half units of fp32 each, so a
+  // sum over 131072 tokens 1.1e-4. The target's dz, which could not bear it, has its own logit.
   constexpr bool kRuns = MODE == STATS || NP == 3;
   const int terms = NP == 3 ? p.terms : 1;
   const int run_stages = NP == 3 ? min(4, 6 / terms) : CG == 1 ? 4 : 8;
@@ -921,7 +923,7 @@ __global__ void __launch_bounds__(32 * kTargetWarps)
 // The backward's first kernel: the rows of x whose tokens count, one after the other, in dst
 // [planes][rows_pad][Hp] (with zeros up to a whole K stage), their tokens in index, the plan, and
 // zeros in the rows of dx whose tokens do not count. What is left out costs the products nothing
-// (1500 x 2048 x 50257 with 60 % left out, forward and backward: 505 us, 743 with zeros for them),
+// (1500 x 2048 x 50257 with 60 % left out, forward and backward: 515 us, 743 with zeros for them),
 // and a NaN or infinity in a padded row of x meets no other row. A block takes 16 tokens and 512
 // columns; it counts those of the tokens before its own by itself, from the first or, beyond 65536
 // tokens, from the last whole chunk of 4096 on and over the chunks' counts (chunk; else NULL). The
