@@ -80,7 +80,8 @@ SPLIT_CASES = [
     (1500, 512, 9000, BF, 0, 0.8, False),       # the split follows the tokens that count
     (300, 256, 11876, BF, 11776, 0.0, False),   # a last piece of two K stages: splits without any
     (256, 128, 5003, FP, 0, 0.0, False), (200, 131, 6000, FP, 0, 0.0, False), (300, 131, 6000, BF, 0, 0.2, False),
-    (200, 132, 4200, FP, 4096, 0.0, False)]
+    (200, 132, 4200, FP, 4096, 0.0, False),
+    (70, 1032, 40000, BF, 0, 0.0, False), (128, 520, 30000, BF, 0, 0.3, False), (64, 96, 20000, FP, 0, 0.0, False)]  # single CTAs
 
 
 @pytest.mark.parametrize("T,H,V,dt,piece,skip,whole", SPLIT_CASES)
