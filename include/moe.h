@@ -32,6 +32,9 @@
  *   moe_embed, moe_embed_backward            token embedding, its gradient by sorted tokens
  *   moe_block_norm, moe_block_norm_backward  the norms before and after a block, with its
  *                                            gates and the scaled residual
+ *   moe_rope, moe_rope_backward              rotary positions of queries and keys, with the store
+ *                                            into a cache's rows
+ *   moe_attn, moe_attn_backward              attention over packed prompts and over a cache
  *   moe_head_loss, moe_head_loss_backward    softmax cross entropy over the vocabulary without
  *                                            keeping the logits, and its gradients
  *   moe_grad_norm, moe_grad_clip             the global norm of many gradients, and clipping
@@ -526,6 +529,104 @@ moe_status_t moe_block_norm_backward(const moe_norm_config_t* cfg, const void* r
                                      const float* w_next, const float* gate, const float* token_gate, const void* dr,
                                      const void* dn, void* dx, void* dy, const moe_norm_grads_t* grads, void* ws,
                                      moe_stream_t stream);
+
+/* Rotary positions. The frequencies of rot / 2 pairs of channels, in radians per position:
+ * f_i = base^(-2 i / rot), i = 0 .. rot / 2 - 1, and for a context longer than the trained one
+ *   MOE_ROPE_LINEAR: f_i / factor;
+ *   MOE_ROPE_YARN: f_i k_i + f_i / factor (1 - k_i), k_i = (r_i - beta_slow) / (beta_fast - beta_slow)
+ *     held to [0, 1], r_i = trained_len f_i / (2 pi) the whole turns within the trained length. */
+enum { MOE_ROPE_UNSCALED = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_YARN = 2 };
+typedef struct {
+  int32_t rot;        /* rotated channels of a head: even */
+  int32_t scaling;
+  double base;        /* > 0, 10000 usually */
+  double factor;      /* > 0: LINEAR, YARN */
+  double trained_len; /* > 0: YARN */
+  double beta_fast, beta_slow; /* YARN: 32 and 1 usually, beta_fast > beta_slow */
+} moe_rope_freq_t;
+
+/* table [rot / 2]: turns per position, in 64-bit fixed point (2^64 is one turn; whole turns per
+ * position are dropped), so that an angle is exact modulo a turn at any position. Made once. */
+moe_status_t moe_rope_table(const moe_rope_freq_t* freq, uint64_t* table, moe_stream_t stream);
+
+/* T tokens of Hq query and Hk key heads (either may be 0) of D <= 4096 channels. */
+enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 };
+typedef struct {
+  int32_t T, Hq, Hk, D;
+  int32_t rot, first; /* channels [first, first + rot) of every head are rotated, the others copied */
+  int32_t layout;     /* HALF: channel i with i + rot / 2; INTERLEAVED: 2 i with 2 i + 1 (of those) */
+  int32_t act_dtype;  /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 */
+  int32_t slots;      /* rows of k_out and v_out, where slot is given */
+  float magnitude;    /* multiplies the rotated channels (1; YaRN's 0.1 ln(factor) + 1) */
+  int64_t ld_q, ld_k, ld_v, ld_q_out, ld_k_out, ld_v_out; /* row strides in elements; 0: dense */
+} moe_rope_config_t;
+
+/* Every pair (a, b) of token t becomes magnitude (a cos - b sin, b cos + a sin), the angle pos[t]
+ * f_i (any int32 position). q [T, Hq, D] -> q_out, k [T, Hk, D] -> k_out, and v [T, Hk, D] -> v_out
+ * as it is (both or neither NULL), in one launch. slot (or NULL) [T]: token t's rows of k_out and
+ * v_out are slot[t] instead of t (a cache with `slots` rows): a negative one stores neither (its q
+ * is rotated all the same), one >= slots neither and sets MOE_ERR_DEVICE_BAD_INPUT; of tokens with
+ * the same slot any may win, piece by piece. Other rows are not touched. Rows may be strided views
+ * (heads of a fused projection): q, k, v and the outputs are aligned to their elements only, and
+ * multiples of 16 bytes move as such. In place where the strides agree and slot is NULL; otherwise
+ * outputs must not overlap inputs. Formed in fp32, rounded once. ws: at least the status head (4096
+ * bytes) of a workspace, only needed with slot. */
+moe_status_t moe_rope(const moe_rope_config_t* cfg, const void* q, const void* k, const void* v, const int32_t* pos,
+                      const int32_t* slot, const uint64_t* table, void* q_out, void* k_out, void* v_out, void* ws,
+                      moe_stream_t stream);
+
+/* The gradients of q and k from those of q_out and k_out: the same by minus the angle. dq_out and
+ * dk_out have the row strides ld_q_out and ld_k_out (rows 0 .. T - 1: no slots), dq and dk have ld_q
+ * and ld_k. v's gradient is v_out's. */
+moe_status_t moe_rope_backward(const moe_rope_config_t* cfg, const void* dq_out, const void* dk_out, const int32_t* pos,
+                               const uint64_t* table, void* dq, void* dk, moe_stream_t stream);
+
+/* Attention of B sequences. */
+typedef struct {
+  int32_t Tq, Tk;    /* rows of q and o; rows of k and v */
+  int32_t B;         /* sequences */
+  int32_t Hq, Hkv;   /* query and key heads: query head h reads key head h / (Hq / Hkv) */
+  int32_t D;         /* channels of a head, 1 .. 128 */
+  int32_t causal;    /* 1: query i of n sees the keys j <= i + m - n of m; 0: all m */
+  int32_t max_q;     /* no sequence has more query rows than this (0: Tq); lets short ones be served as such */
+  int32_t act_dtype; /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 */
+  float scale;       /* > 0, of the scores */
+  int64_t ld_q, ld_k, ld_v, ld_o; /* row strides in elements; 0: dense */
+} moe_attn_config_t;
+
+/* With q [Tq, Hq, D], k and v [Tk, Hkv, D], for every sequence b, its query rows i and heads:
+ *     s_j = scale q_i . k_j over the keys j that i sees;  lse = log sum_j exp s_j
+ *     o_i = sum_j exp(s_j - lse) v_j
+ * Sequence b has the query rows q_start[b] .. q_start[b + 1] - 1 (q_start [B + 1], int32, device)
+ * and the key rows k_start[b] .. k_start[b] + k_len[b] - 1 (both [B]): packed anywhere, a region of a
+ * cache, or shared by several sequences. k_start and k_len NULL: the rows of its queries (Tk >= Tq).
+ * A query that sees no key (an empty sequence; fewer keys than queries) has o = 0 and lse = -inf.
+ * Rows of o and lse that are in no sequence are not touched, and key rows outside the sequences may
+ * hold anything; a value that is not finite inside a sequence's keys may reach all of its outputs.
+ * Sequences out of range (rows outside q, or more than max_q; keys outside k) set
+ * MOE_ERR_DEVICE_BAD_INPUT and have no rows, or no keys. lse [Hq, Tq] fp32. Scores, sums and
+ * outputs are held in fp32; with bf16 tensors exp(s - max) is rounded to bf16, the operand type of
+ * its product with v. Rows may be strided views, aligned to their elements; bf16 rows of multiples
+ * of 16 bytes (address, stride, D % 8 = 0) go to the tensor cores. o must not overlap an input.
+ * ws: moe_attn_workspace_size bytes. Deterministic. */
+moe_status_t moe_attn_workspace_size(const moe_attn_config_t* cfg, size_t* bytes);
+moe_status_t moe_attn(const moe_attn_config_t* cfg, const void* q, const void* k, const void* v, const int32_t* q_start,
+                      const int32_t* k_start, const int32_t* k_len, void* o, float* lse, void* ws, moe_stream_t stream);
+
+/* Its gradients, from the same inputs, moe_attn's o and lse and the gradient d_o of o:
+ *     p_ij = exp(s_ij - lse_i);  ds_ij = p_ij (d_o_i . v_j - d_o_i . o_i)
+ *     dv_j = sum_i p_ij d_o_i;  dk_j = scale sum_i ds_ij q_i;  dq_i = scale sum_j ds_ij k_j
+ * (dk and dv over every query head of their group). d_o has o's rows and stride, dq, dk and dv those
+ * of q, k and v; rows in a sequence are written (zeros for keys that nothing sees), others not
+ * touched. The keys of the sequences must lie one behind the other: a sequence whose keys begin
+ * before those of the one in front end sets MOE_ERR_DEVICE_BAD_INPUT and has no keys. With bf16
+ * tensors p and ds are rounded to bf16 for their products. Outputs must not overlap inputs or each
+ * other. ws: moe_attn_backward_workspace_size bytes. No atomics on sums: the same bits on every run. */
+moe_status_t moe_attn_backward_workspace_size(const moe_attn_config_t* cfg, size_t* bytes);
+moe_status_t moe_attn_backward(const moe_attn_config_t* cfg, const void* q, const void* k, const void* v,
+                               const int32_t* q_start, const int32_t* k_start, const int32_t* k_len, const void* o,
+                               const float* lse, const void* d_o, void* dq, void* dk, void* dv, void* ws,
+                               moe_stream_t stream);
 
 /* Vocabulary head. T tokens, width H, V vocabulary rows. */
 typedef struct {

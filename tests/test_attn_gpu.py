@@ -1,0 +1,325 @@
+"""Attention and its gradients against the formulas in 64 bits, with bounds per element on what the
+documented arithmetic may lose."""
+import math
+
+import pytest
+import torch
+
+import token_routing_expert_router_gb300 as moe
+from test_step_gpu import BF, CODE, FP, HALF, U, gen, normal, poisoned, workspace
+from test_step_gpu import within as within_all
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _built(lib):
+    pass
+
+
+def within(got, want, bound):
+    if got.numel():
+        within_all(got, want, bound)
+
+
+class Batch:
+    """q, k, v and where the sequences are. lens: (query rows, keys) of every sequence; place:
+    "self" (keys beside the queries), "cache" (a region for each, with NaN around), "shared" (all
+    on the same keys). NaN in every row that is in no sequence."""
+
+    def __init__(self, lens, Hq, Hkv, D, dt, causal=1, place="self", packed=False, tail=3, scale=None, sharp=1.0, max_q=None,
+                 seed=0):
+        g = gen(seed)
+        self.lens, self.Hq, self.Hkv, self.D, self.dt, self.causal = lens, Hq, Hkv, D, dt, causal
+        B = len(lens)
+        self.q_at, at = [], 0
+        for n, _ in lens:
+            self.q_at.append(at)
+            at += n
+        T = self.used = at
+        self.Tq = T + tail
+        self.q_start = torch.tensor(self.q_at + [T], dtype=torch.int32, device="cuda")
+        if place == "self":
+            assert all(n == m for n, m in lens)
+            self.k_at, self.k_start, self.k_len, self.Tk = self.q_at, None, None, self.Tq
+        else:
+            if place == "cache":
+                region = max([m for _, m in lens] + [0]) + 5
+                self.k_at, self.Tk = [b * region + 2 for b in range(B)], B * region + 4
+            else:
+                self.k_at, self.Tk = [1] * B, max(m for _, m in lens) + 4
+            self.k_start = torch.tensor(self.k_at, dtype=torch.int32, device="cuda")
+            self.k_len = torch.tensor([m for _, m in lens], dtype=torch.int32, device="cuda")
+        if packed:
+            assert place == "self"
+            row = poisoned(self.Tq, Hq + 2 * Hkv, D, dtype=dt)
+            row[:T] = normal(g, T, Hq + 2 * Hkv, D, dtype=dt)
+            row[:T, :Hq] *= sharp
+            self.q, self.k, self.v = row[:, :Hq], row[:, Hq:Hq + Hkv], row[:, Hq + Hkv:]
+        else:
+            self.q, self.k, self.v = (poisoned(r, h, D, dtype=dt) for r, h in ((self.Tq, Hq), (self.Tk, Hkv), (self.Tk, Hkv)))
+            self.q[:T] = normal(g, T, Hq, D, dtype=dt, std=sharp)
+            for (_, m), a in zip(lens, self.k_at):
+                self.k[a:a + m], self.v[a:a + m] = normal(g, m, Hkv, D, dtype=dt), normal(g, m, Hkv, D, dtype=dt)
+        self.do = poisoned(self.Tq, Hq, D, dtype=dt)
+        self.do[:T] = normal(g, T, Hq, D, dtype=dt)
+        self.scale = 1 / math.sqrt(D) if scale is None else scale
+        ld = (Hq + 2 * Hkv) * D if packed else 0
+        self.packed = packed
+        self.cfg = moe.MoEAttnConfig.make(Tq=self.Tq, Tk=self.Tk, B=B, Hq=Hq, Hkv=Hkv, D=D, causal=causal, act_dtype=CODE[dt],
+                                          max_q=max([n for n, _ in lens] + [0]) if max_q is None else max_q,
+                                          scale=self.scale, ld_q=ld, ld_k=ld, ld_v=ld)
+        self.scale = self.cfg.scale  # as fp32 has it
+        self.ws = workspace(moe.moe_attn_workspace_size(self.cfg))
+        self.bws = workspace(moe.moe_attn_backward_workspace_size(self.cfg))
+
+    def forward(self, stream=None):
+        o, lse = torch.full((self.Tq, self.Hq, self.D), 7.0, dtype=self.dt, device="cuda"), torch.full((self.Hq, self.Tq), 7.0,
+                                                                                                  device="cuda")
+        moe.moe_attn(self.cfg, self.q, self.k, self.v, self.q_start, self.k_start, self.k_len, o, lse, self.ws, stream=stream)
+        return o, lse
+
+    def grads(self):
+        """Buffers for the gradients, laid out as q, k and v, full of sevens."""
+        if self.packed:
+            row = torch.full((self.Tq, self.Hq + 2 * self.Hkv, self.D), 7.0, dtype=self.dt, device="cuda")
+            return row[:, :self.Hq], row[:, self.Hq:self.Hq + self.Hkv], row[:, self.Hq + self.Hkv:]
+        return tuple(torch.full_like(x, 7.0) for x in (self.q, self.k, self.v))
+
+    def backward(self, o, lse, out=None):
+        out = self.grads() if out is None else out
+        moe.moe_attn_backward(self.cfg, self.q, self.k, self.v, self.q_start, self.k_start, self.k_len, o, lse, self.do, *out,
+                              self.bws)
+        return out
+
+    def parts(self):
+        """(b, query rows, key rows, mask of visible pairs) of every sequence."""
+        for b, (n, m) in enumerate(self.lens):
+            i, j = torch.arange(n, device="cuda")[:, None], torch.arange(m, device="cuda")[None, :]
+            seen = (j <= i + m - n) if self.causal else torch.ones(n, m, dtype=torch.bool, device="cuda")
+            yield b, slice(self.q_at[b], self.q_at[b] + n), slice(self.k_at[b], self.k_at[b] + m), seen
+
+    def check_forward(self, o, lse):
+        """Against the formula. With e_s the error of a score, a probability's is e_p = p (e_s + ...);
+        o and lse follow by the sums of them."""
+        assert (o[self.used:] == 7).all() and (lse[:, self.used:] == 7).all()
+        G, bf = self.Hq // self.Hkv, self.dt == BF
+        for b, rq, rk, seen in self.parts():
+            n, m = seen.shape
+            for h in range(self.Hq):
+                q, k, v = self.q[rq, h].double(), self.k[rk, h // G].double(), self.v[rk, h // G].double()
+                s, want, wlse, p, ep, el = self._scores(q, k, v, seen)
+                empty = ~seen.any(1)
+                got = lse[h, rq]
+                assert torch.equal(got == -math.inf, empty)
+                within(got[~empty], wlse[~empty], el[~empty])
+                bound = self._o_bound(p, ep, el, v, want)
+                assert not o[rq, h][empty].any()
+                within(o[rq, h], want, bound)
+
+    def _scores(self, q, k, v, seen):
+        s = (q @ k.t()) * self.scale
+        s = s.masked_fill(~seen, -math.inf)
+        lse = torch.logsumexp(s, 1) if s.shape[1] else torch.full((s.shape[0],), -math.inf, dtype=torch.float64, device="cuda")
+        some = lse > -math.inf
+        p = torch.where(some[:, None], (s - lse[:, None]).exp(), 0.0).nan_to_num(0.0)
+        o = p @ v
+        # D fp32 products summed in any order, a tensor core's truncating additions counted twice
+        es = 2 * (self.D + 8) * U * self.scale * (q.abs() @ k.abs().t())
+        # the exponent in base 2 and the exponential: 2^-22 of it, the argument's own roundings
+        z = torch.where(seen, s, 0.0).abs() + torch.where(some, lse, 0.0).abs()[:, None] + 16
+        ep = torch.where(seen, es + 8 * U * z + 2.0 ** -21, 0.0)  # relative
+        m = s.shape[1]
+        el = (p * ep).sum(1) + (2 * m + 32) * U + 8 * U * torch.where(some, lse, 0.0).abs()
+        return s, o, lse, p, ep, el
+
+    def _o_bound(self, p, ep, el, v, want):
+        half = HALF[BF] if self.dt == BF else 0.0
+        mag = p @ v.abs()
+        lost = (p * (ep + half)) @ v.abs() + (el[:, None] + (2 * p.shape[1] + 64) * U) * mag
+        return lost + HALF[self.dt] * (want.abs() + lost) + 1e-38
+
+    def check_backward(self, dq, dk, dv):
+        outside = [torch.ones(self.Tq if i == 0 else self.Tk, dtype=torch.bool, device="cuda") for i in range(3)]
+        G = self.Hq // self.Hkv
+        half = HALF[BF] if self.dt == BF else 0.0
+        for b, rq, rk, seen in self.parts():
+            n, m = seen.shape
+            outside[0][rq] = False
+            outside[1][rk] = False
+            outside[2][rk] = False
+            acc = 2 * U * (max(n * G, m) + 64)
+            for hk in range(self.Hkv):
+                k, v = self.k[rk, hk].double(), self.v[rk, hk].double()
+                zero = torch.zeros_like(k)
+                wk, wv, bk, bv = zero.clone(), zero.clone(), zero.clone(), zero.clone()
+                for h in range(hk * G, (hk + 1) * G):
+                    q, do = self.q[rq, h].double(), self.do[rq, h].double()
+                    s, o, lse, p, ep, el = self._scores(q, k, v, seen)
+                    eo = self._o_bound(p, ep, el, v, o)
+                    ep = ep + el[:, None] + 2.0 ** -21  # exp(s - lse), lse from the forward
+                    dp, delta = do @ v.t(), (do * o).sum(1, keepdim=True)
+                    edp = 2 * (self.D + 8) * U * (do.abs() @ v.abs().t())
+                    ed = (do.abs() * eo).sum(1, keepdim=True) + 2 * (self.D + 8) * U * (do * o).abs().sum(1, keepdim=True)
+                    ds = p * (dp - delta)
+                    eds = p * (edp + ed) + ds.abs() * (ep + half + 4 * U) + p * 4 * U * (dp.abs() + delta.abs())
+                    eds = eds * (1 + half)
+                    want = self.scale * ds @ k
+                    lost = self.scale * ((eds + acc * ds.abs()) @ k.abs())
+                    within(dq[rq, h], want, lost + HALF[self.dt] * (want.abs() + lost) + 4 * U * want.abs() + 1e-38)
+                    wv += p.t() @ do
+                    bv += (p * (ep + half + acc)).t() @ do.abs()
+                    wk += self.scale * ds.t() @ q
+                    bk += self.scale * (eds + acc * ds.abs()).t() @ q.abs()
+                # fp32 scales q by the scores' scale first: one rounding more
+                bk = bk + 4 * U * (bk + wk.abs())
+                within(dk[rk, hk], wk, bk + HALF[self.dt] * (wk.abs() + bk) + 1e-38)
+                within(dv[rk, hk], wv, bv + HALF[self.dt] * (wv.abs() + bv) + 1e-38)
+        for rows, g in zip(outside, (dq, dk, dv)):
+            assert (g[rows] == 7).all()
+
+    def check_status(self, want=moe.MOE_OK):
+        assert moe.moe_read_status(self.ws) == want
+
+
+EDGES = [1, 0, 63, 64, 65, 127, 128, 129, 0, 200, 2]
+same = lambda ns: [(n, n) for n in ns]  # noqa: E731
+
+SELF = [
+    # query rows (= keys) of the sequences, Hq, Hkv, D, dtype
+    ([1], 1, 1, 1, FP), ([1], 2, 1, 8, BF), (EDGES, 4, 2, 64, BF), (EDGES, 4, 1, 128, BF), (EDGES, 2, 2, 50, FP),
+    (EDGES, 3, 1, 36, BF), ([300], 6, 2, 80, BF), ([300], 2, 2, 128, FP), ([257, 255], 8, 1, 32, BF), ([513], 2, 1, 24, BF),
+    ([700, 3, 401], 4, 4, 96, BF), ([1100], 2, 1, 128, BF), ([1100], 1, 1, 64, BF), ([5] * 300, 1, 1, 16, BF), ([], 2, 2, 64, BF),
+    ([0, 0], 2, 2, 64, BF), ([384, 640], 2, 2, 120, BF), ([260], 2, 2, 127, BF), ([2] * 600 + [150], 1, 1, 8, FP)]
+
+
+@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,dt", SELF)
+def test_packed_sequences(lens, Hq, Hkv, D, dt, packed, causal):
+    b = Batch(same(lens), Hq, Hkv, D, dt, causal=causal, packed=packed, seed=len(lens))
+    o, lse = b.forward()
+    b.check_forward(o, lse)
+    grads = b.backward(o, lse)
+    b.check_backward(*grads)
+    b.check_status()
+    assert moe.moe_read_status(b.bws) == moe.MOE_OK
+    # the same bits again
+    o2, lse2 = b.forward()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for x, y in zip(grads, b.backward(o, lse)):
+        assert torch.equal(x, y)
+
+
+OVER = [
+    # (query rows, keys) of the sequences, Hq, Hkv, D, dtype
+    ([(1, 700)], 8, 2, 128, BF), ([(1, 1)], 4, 1, 64, BF), ([(1, 0), (1, 5), (1, 64), (1, 2000), (1, 129)], 16, 2, 128, BF),
+    ([(1, 33), (1, 0), (1, 900)], 4, 4, 64, FP), ([(1, 3000)] * 3, 32, 2, 128, BF), ([(1, 500), (1, 77)], 7, 1, 80, BF),
+    ([(4, 600), (1, 9), (3, 64), (0, 50), (2, 1)], 8, 2, 128, BF), ([(5, 600), (2, 300)], 12, 1, 64, BF),
+    ([(4, 2), (2, 1), (1, 0)], 4, 2, 64, BF), ([(200, 130), (64, 64), (10, 300)], 4, 2, 64, BF),
+    ([(200, 130), (130, 0), (10, 300)], 4, 2, 128, BF), ([(150, 20), (7, 300), (3, 0)], 2, 1, 40, FP),
+    ([(130, 1000), (300, 301), (1, 800)], 4, 2, 128, BF), ([(16, 400), (0, 9)], 2, 1, 36, BF), ([(2, 130)] * 40, 2, 2, 64, BF),
+    ([(1, 40000)], 2, 1, 128, BF), ([(1, 9000), (1, 100)], 2, 2, 128, FP), ([(6, 700)], 128, 1, 64, BF),
+    ([(1, 1 + 17 * i) for i in range(70)], 4, 1, 128, BF), ([(1, 260)] * 300, 2, 1, 32, BF), ([(8, 1111)] * 2, 6, 3, 104, BF)]
+
+
+@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("place", ["cache", "shared"])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,dt", OVER)
+def test_over_a_cache(lens, Hq, Hkv, D, dt, place, causal):
+    b = Batch(lens, Hq, Hkv, D, dt, causal=causal, place=place, seed=len(lens) + D)
+    o, lse = b.forward()
+    b.check_forward(o, lse)
+    b.check_status()
+    o2, lse2 = b.forward()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    if place == "cache" and sum(n * m for n, m in lens) * Hq < 10 ** 7:
+        grads = b.backward(o, lse)
+        b.check_backward(*grads)
+        assert moe.moe_read_status(b.bws) == moe.MOE_OK
+        for x, y in zip(grads, b.backward(o, lse)):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dt,D,n", [(BF, 128, 300), (BF, 64, 200), (FP, 64, 130), (BF, 36, 130)])
+@pytest.mark.parametrize("m", [None, 2000])
+def test_sharp_and_flat_scores(dt, D, n, m):
+    """Rows whose maximum grows from tile to tile by hundreds, and rows that are all alike."""
+    lens = [(n, n)] if m is None else [(2, m)]
+    for sharp, scale in ((40.0, 1.0), (1e-3, 1e-3)):
+        b = Batch(lens, 4, 2, D, dt, place="self" if m is None else "cache", sharp=sharp, scale=scale, seed=3)
+        if sharp > 1:  # keys that lean towards the last queries, more and more
+            for (_, mm), a in zip(b.lens, b.k_at):
+                lean = b.q[b.used - 1, ::2].float() / (sharp * math.sqrt(D))
+                ramp = torch.linspace(0, 3, mm, device="cuda")[:, None, None]
+                b.k[a:a + mm] = (b.k[a:a + mm].float() * 0.2 + ramp * lean).to(dt)
+        o, lse = b.forward()
+        # scores of some hundreds are off by some 1e-4, which the bounds hold
+        b.check_forward(o, lse)
+        if m is None:
+            b.check_backward(*b.backward(o, lse))
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("lens", [[(1, 300), (1, 40)], [(200, 300), (64, 64)]])
+def test_sequences_out_of_range(dt, lens):
+    """Rows or keys that are not there: reported, and nothing of them read or written."""
+    b = Batch(lens, 4, 2, 64, dt, place="cache")
+    o, lse = b.forward()
+    for name, at, value, rows, keys in (("q_start", 0, -1, False, None), ("q_start", 2, b.Tq + 1, False, None),
+                                        ("q_start", 1, -5, False, None), ("k_start", 1, b.Tk, True, False),
+                                        ("k_start", 1, -3, True, False), ("k_len", 1, b.Tk, True, False),
+                                        ("k_len", 1, -1, True, False)):
+        t = getattr(b, name)
+        old = t[at].clone()
+        t[at] = value
+        o2, lse2 = b.forward()
+        b.check_status(moe.MOE_ERR_DEVICE_BAD_INPUT)
+        b.check_status()
+        if keys is False:  # the sequence has no keys
+            r = slice(b.q_at[1], b.q_at[1] + lens[1][0])
+            assert not o2[r].any() and (lse2[:, r] == -math.inf).all()
+            assert torch.equal(o2[:b.q_at[1]], o[:b.q_at[1]])
+        grads = b.backward(o, lse)
+        assert moe.moe_read_status(b.bws) == moe.MOE_ERR_DEVICE_BAD_INPUT
+        assert all((x[b.used if i == 0 else b.Tk - 2:] == 7).all() for i, x in enumerate(grads))
+        t[at] = old
+    # more query rows than announced
+    cfg = moe.MoEAttnConfig.make(**{**b.cfg.as_dict(), "max_q": max(n for n, _ in lens) - 1 or 1})
+    if cfg.max_q < max(n for n, _ in lens):
+        b.cfg = cfg
+        o2, _ = b.forward()
+        b.check_status(moe.MOE_ERR_DEVICE_BAD_INPUT)
+        assert (o2[:lens[0][0]] == 7).all()
+    b = Batch(lens, 4, 2, 64, dt, place="shared")  # the backward would write the keys twice
+    o, lse = b.forward()
+    b.check_status()
+    b.backward(o, lse)
+    assert moe.moe_read_status(b.bws) == moe.MOE_ERR_DEVICE_BAD_INPUT
+
+
+def test_gradients_by_differences():
+    """The 64-bit formulas behind the bounds, and the kernels, against central differences."""
+    b = Batch([(5, 9), (3, 2)], 2, 1, 8, FP, place="cache", seed=11)
+    o, lse = b.forward()
+    grads = b.backward(o, lse)
+
+    def total(q, k, v):
+        out = 0.0
+        for _, rq, rk, seen in b.parts():
+            for h in range(2):
+                s = (q[rq, h] @ k[rk, 0].t() * b.scale).masked_fill(~seen, -1e30)
+                p = torch.softmax(s, 1) * seen
+                out = out + (p @ v[rk, 0] * b.do[rq, h].double()).sum()
+        return out
+
+    x = [t.double().nan_to_num(0.0) for t in (b.q, b.k, b.v)]
+    g, h = gen(4), 1e-5
+    for i in range(3):
+        d = normal(g, *x[i].shape).double()
+        hi, lo = list(x), list(x)
+        hi[i], lo[i] = x[i] + h * d, x[i] - h * d
+        slope = (total(*hi) - total(*lo)) / (2 * h)
+        inside = torch.where(grads[i] == 7, 0.0, grads[i].double())
+        # differences lose h^2 times a third derivative of order 10; fp32 gradients 1e-5 of some dozens
+        assert abs(slope - (inside * d).sum()) < 1e-3

@@ -9,13 +9,17 @@ and a missing library raises instead of falling back.
 from __future__ import annotations
 
 import ctypes
-from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p, POINTER, byref
+import math
+from ctypes import c_double, c_float, c_int32, c_int64, c_size_t, c_void_p, POINTER, byref
 
 from ._build import build as _build_lib, LIB as _LIB_PATH
 
 F32, BF16, E4M3, MXE4M3 = 0, 1, 2, 3
 SOFTMAX, SIGMOID = 0, 1
 GROUP_TOP2_SUM, GROUP_MAX = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_UNSCALED, ROPE_LINEAR, ROPE_YARN = 0, 1, 2
+WORKSPACE_HEAD = 4096  # bytes of a workspace that only carries the status word
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA = 0, 1, 2, 3
 MOE_ERR_DEVICE_BAD_INPUT, MOE_ERR_TIMEOUT = 4, 5
@@ -122,6 +126,38 @@ class MoEEmbedConfig(_PlainConfig):
     _defaults_ = dict(act_dtype=BF16, grad_dtype=F32, scale=1.0)
 
 
+class MoERopeFreq(_PlainConfig):
+    _fields_ = [("rot", c_int32), ("scaling", c_int32), ("base", c_double), ("factor", c_double),
+                ("trained_len", c_double), ("beta_fast", c_double), ("beta_slow", c_double)]
+    _defaults_ = dict(scaling=ROPE_UNSCALED, base=10000.0, factor=1.0, trained_len=1.0, beta_fast=32.0, beta_slow=1.0)
+
+
+class MoERopeConfig(_PlainConfig):
+    _fields_ = [("T", c_int32), ("Hq", c_int32), ("Hk", c_int32), ("D", c_int32), ("rot", c_int32), ("first", c_int32),
+                ("layout", c_int32), ("act_dtype", c_int32), ("slots", c_int32), ("magnitude", c_float),
+                ("ld_q", c_int64), ("ld_k", c_int64), ("ld_v", c_int64), ("ld_q_out", c_int64), ("ld_k_out", c_int64),
+                ("ld_v_out", c_int64)]
+    _defaults_ = dict(first=0, layout=ROPE_HALF, act_dtype=BF16, slots=0, magnitude=1.0, ld_q=0, ld_k=0, ld_v=0, ld_q_out=0,
+                      ld_k_out=0, ld_v_out=0)
+
+    @classmethod
+    def make(cls, **kw):
+        """rot: every channel of a head, unless given."""
+        return super().make(**{**kw, "rot": kw.get("rot", kw.get("D"))})
+
+
+class MoEAttnConfig(_PlainConfig):
+    _fields_ = [("Tq", c_int32), ("Tk", c_int32), ("B", c_int32), ("Hq", c_int32), ("Hkv", c_int32), ("D", c_int32),
+                ("causal", c_int32), ("max_q", c_int32), ("act_dtype", c_int32), ("scale", c_float), ("ld_q", c_int64),
+                ("ld_k", c_int64), ("ld_v", c_int64), ("ld_o", c_int64)]
+    _defaults_ = dict(causal=1, max_q=0, act_dtype=BF16, ld_q=0, ld_k=0, ld_v=0, ld_o=0)
+
+    @classmethod
+    def make(cls, **kw):
+        """scale: 1 / sqrt(D), unless given."""
+        return super().make(**{**kw, "scale": kw.get("scale", 1.0 / math.sqrt(max(1, kw.get("D", 1))))})
+
+
 class MoEGrad(ctypes.Structure):
     _fields_ = [("grad", c_void_p), ("out", c_void_p), ("n", c_int64), ("dtype", c_int32)]
 
@@ -216,6 +252,13 @@ def lib():
             "moe_embed": [POINTER(MoEEmbedConfig), P, P, P, P, P],
             "moe_embed_workspace_size": [POINTER(MoEEmbedConfig), POINTER(c_size_t)],
             "moe_embed_backward": [POINTER(MoEEmbedConfig), P, P, P, c_int32, P, P],
+            "moe_rope_table": [POINTER(MoERopeFreq), P, P],
+            "moe_rope": [POINTER(MoERopeConfig), P, P, P, P, P, P, P, P, P, P, P],
+            "moe_rope_backward": [POINTER(MoERopeConfig), P, P, P, P, P, P, P],
+            "moe_attn_workspace_size": [POINTER(MoEAttnConfig), POINTER(c_size_t)],
+            "moe_attn": [POINTER(MoEAttnConfig), P, P, P, P, P, P, P, P, P, P],
+            "moe_attn_backward_workspace_size": [POINTER(MoEAttnConfig), POINTER(c_size_t)],
+            "moe_attn_backward": [POINTER(MoEAttnConfig), P, P, P, P, P, P, P, P, P, P, P, P, P, P],
             "moe_grad_clip_workspace_size": [c_int32, POINTER(c_size_t)],
             "moe_grad_norm": [POINTER(MoEGrad), c_int32, P, P, P],
             "moe_grad_clip": [POINTER(MoEGrad), c_int32, ctypes.c_float, P, P, P],
@@ -244,6 +287,8 @@ def exported_symbols() -> list:
             "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward",
             "moe_head_workspace_size", "moe_head_loss", "moe_head_loss_backward",
             "moe_embed", "moe_embed_workspace_size", "moe_embed_backward",
+            "moe_rope_table", "moe_rope", "moe_rope_backward",
+            "moe_attn_workspace_size", "moe_attn", "moe_attn_backward_workspace_size", "moe_attn_backward",
             "moe_grad_clip_workspace_size", "moe_grad_norm", "moe_grad_clip",
             "moe_read_status", "moe_status_string", "moe_route_static_scratch",
             "moe_selftest_bounded_wait"]
@@ -258,6 +303,27 @@ def _ptr(t):
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows(t, ld, width: int):
+    """Rows of `width` elements whose stride is the configuration's (ld, 0: dense): a matrix, or a
+    view of some heads of a wider row."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if 0 in t.shape:
+        return t.data_ptr()
+    inner = 1
+    for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+        if size != 1 and stride != inner:
+            raise ValueError("expected rows of neighbouring elements")
+        inner *= size
+    if t.dim() < 2 or inner != width:
+        raise ValueError(f"expected rows of {width} elements")
+    if t.shape[0] > 1 and t.stride(0) != (ld or width):
+        raise ValueError(f"rows {t.stride(0)} elements apart, {ld or width} in the configuration")
     return t.data_ptr()
 
 
@@ -534,6 +600,57 @@ def moe_embed_backward(cfg, token, dout, dtable, ws, accumulate=False, stream=No
     """accumulate: added to the rows of the tokens that occur, the others left alone."""
     _check(lib().moe_embed_backward(byref(cfg), _ptr(token), _ptr(dout), _ptr(dtable), int(accumulate), _ptr(ws),
                                     _stream(stream)), "moe_embed_backward")
+
+
+def moe_rope_table(freq: MoERopeFreq, table, stream=None):
+    """table: rot / 2 64-bit CUDA values, made once and given to every moe_rope call."""
+    _check(lib().moe_rope_table(byref(freq), _ptr(table), _stream(stream)), "moe_rope_table")
+
+
+def moe_rope(cfg, q, k, v, pos, slot, table, q_out, k_out, v_out, ws=None, stream=None):
+    """q and k rotated by their positions, v copied (or None, with v_out); slot: the rows of k_out
+    and v_out that the tokens go to (None: 0 .. T - 1; otherwise ws carries the status)."""
+    nq, nk = cfg.Hq * cfg.D, cfg.Hk * cfg.D
+    _check(lib().moe_rope(byref(cfg), _rows(q, cfg.ld_q, nq), _rows(k, cfg.ld_k, nk), _rows(v, cfg.ld_v, nk), _ptr(pos),
+                          _ptr(slot), _ptr(table), _rows(q_out, cfg.ld_q_out, nq), _rows(k_out, cfg.ld_k_out, nk),
+                          _rows(v_out, cfg.ld_v_out, nk), _ptr(ws), _stream(stream)), "moe_rope")
+
+
+def moe_rope_backward(cfg, dq_out, dk_out, pos, table, dq, dk, stream=None):
+    nq, nk = cfg.Hq * cfg.D, cfg.Hk * cfg.D
+    _check(lib().moe_rope_backward(byref(cfg), _rows(dq_out, cfg.ld_q_out, nq), _rows(dk_out, cfg.ld_k_out, nk), _ptr(pos),
+                                   _ptr(table), _rows(dq, cfg.ld_q, nq), _rows(dk, cfg.ld_k, nk), _stream(stream)),
+           "moe_rope_backward")
+
+
+def moe_attn_workspace_size(cfg: MoEAttnConfig) -> int:
+    n = c_size_t()
+    _check(lib().moe_attn_workspace_size(byref(cfg), byref(n)), "moe_attn_workspace_size")
+    return n.value
+
+
+def moe_attn(cfg, q, k, v, q_start, k_start, k_len, o, lse, ws, stream=None):
+    """o and lse of every sequence's query rows; k_start and k_len None: the keys are the rows of
+    the queries."""
+    nq, nk = cfg.Hq * cfg.D, cfg.Hkv * cfg.D
+    _check(lib().moe_attn(byref(cfg), _rows(q, cfg.ld_q, nq), _rows(k, cfg.ld_k, nk), _rows(v, cfg.ld_v, nk), _ptr(q_start),
+                          _ptr(k_start), _ptr(k_len), _rows(o, cfg.ld_o, nq), _ptr(lse), _ptr(ws), _stream(stream)),
+           "moe_attn")
+
+
+def moe_attn_backward_workspace_size(cfg: MoEAttnConfig) -> int:
+    n = c_size_t()
+    _check(lib().moe_attn_backward_workspace_size(byref(cfg), byref(n)), "moe_attn_backward_workspace_size")
+    return n.value
+
+
+def moe_attn_backward(cfg, q, k, v, q_start, k_start, k_len, o, lse, do, dq, dk, dv, ws, stream=None):
+    """dq, dk and dv, laid out as q, k and v, from moe_attn's o and lse and the gradient of o."""
+    nq, nk = cfg.Hq * cfg.D, cfg.Hkv * cfg.D
+    _check(lib().moe_attn_backward(byref(cfg), _rows(q, cfg.ld_q, nq), _rows(k, cfg.ld_k, nk), _rows(v, cfg.ld_v, nk),
+                                   _ptr(q_start), _ptr(k_start), _ptr(k_len), _rows(o, cfg.ld_o, nq), _ptr(lse),
+                                   _rows(do, cfg.ld_o, nq), _rows(dq, cfg.ld_q, nq), _rows(dk, cfg.ld_k, nk),
+                                   _rows(dv, cfg.ld_v, nk), _ptr(ws), _stream(stream)), "moe_attn_backward")
 
 
 def moe_grad_clip_workspace_size(grads: MoEGradList) -> int:

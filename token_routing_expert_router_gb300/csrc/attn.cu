@@ -1,0 +1,56 @@
+// The attention entry points' choice of variant, and their workspaces.
+#include "attn.cuh"
+
+namespace moe {
+
+namespace {
+
+attn::AttnArgs args_of(const moe_attn_config_t& c, const void* q, const void* k, const void* v, const AttnSeqs& at,
+                       const void* o, float* lse, DeviceStatus* st) {
+  attn::AttnArgs a{};
+  a.Tq = c.Tq, a.Tk = c.Tk, a.B = c.B, a.Hq = c.Hq, a.Hkv = c.Hkv, a.D = c.D, a.group = c.Hq / c.Hkv;
+  a.causal = c.causal, a.max_q = c.max_q ? c.max_q : c.Tq;
+  a.scale = c.scale;
+  a.ld_q = c.ld_q ? c.ld_q : (int64_t)c.Hq * c.D;
+  a.ld_k = c.ld_k ? c.ld_k : (int64_t)c.Hkv * c.D;
+  a.ld_v = c.ld_v ? c.ld_v : (int64_t)c.Hkv * c.D;
+  a.ld_o = c.ld_o ? c.ld_o : (int64_t)c.Hq * c.D;
+  a.q = q, a.k = k, a.v = v;
+  a.q_start = at.q_start, a.k_start = at.k_start, a.k_len = at.k_len;
+  a.o = const_cast<void*>(o);
+  a.lse = lse;
+  a.status = st;
+  return a;
+}
+
+}  // namespace
+
+AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward) {
+  AttnScratch s{};
+  size_t at = kWsHead;
+  if (backward) {
+    s.delta = at;
+    at += align_up((size_t)c.Hq * c.Tq * sizeof(float), 256);
+  }
+  s.total = at;
+  return s;
+}
+
+cudaError_t launch_attn(const moe_attn_config_t& c, const void* q, const void* k, const void* v, const AttnSeqs& at,
+                        void* o, float* lse, void* ws, DeviceStatus* st, cudaStream_t s) {
+  if (c.Tq == 0 || c.B == 0) return cudaSuccess;
+  const attn::AttnArgs a = args_of(c, q, k, v, at, o, lse, st);
+  return attn::launch_simt(a, c.act_dtype == MOE_DTYPE_BF16, s);
+}
+
+cudaError_t launch_attn_backward(const moe_attn_config_t& c, const void* q, const void* k, const void* v,
+                                 const AttnSeqs& at, const void* o, const float* lse, const void* d_o, void* dq, void* dk,
+                                 void* dv, void* ws, DeviceStatus* st, cudaStream_t s) {
+  if (c.B == 0 || (c.Tq == 0 && c.Tk == 0)) return cudaSuccess;
+  attn::AttnArgs a = args_of(c, q, k, v, at, o, const_cast<float*>(lse), st);
+  a.d_o = d_o, a.dq = dq, a.dk = dk, a.dv = dv;
+  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + attn_scratch(c, true).delta);
+  return attn::launch_simt_backward(a, c.act_dtype == MOE_DTYPE_BF16, s);
+}
+
+}  // namespace moe

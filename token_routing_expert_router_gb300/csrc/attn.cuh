@@ -1,0 +1,117 @@
+// What the attention kernels share (attn_simt.cu, attn_tc.cu, attn_decode.cu): the arguments as the
+// device sees them, a sequence's rows, and the map from a block to the tile of a ragged batch.
+#pragma once
+
+#include "step.cuh"
+
+namespace moe {
+namespace attn {
+
+struct AttnArgs {
+  int Tq, Tk, B, Hq, Hkv, D, group;  // group: query heads of a key head
+  int causal, max_q;
+  float scale;
+  int64_t ld_q, ld_k, ld_v, ld_o;
+  const void *q, *k, *v;
+  const int32_t *q_start, *k_start, *k_len;
+  void* o;
+  float* lse;
+  // backward
+  const void* d_o;
+  void *dq, *dk, *dv;
+  float* delta;  // [Hq, Tq]: do . o of every query row and head
+  DeviceStatus* status;
+};
+
+struct Seq {
+  int q0, n;  // query rows [q0, q0 + n)
+  int k0, m;  // key rows [k0, k0 + m)
+};
+
+// Sequence b, with what is out of range left out: no rows for query rows that are not inside q or
+// more than max_q, no keys for key rows that are not inside k. With `apart` a sequence whose keys
+// begin before the ones of the sequence in front of it end has no keys either (the backward writes
+// every key's gradient once).
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, bool apart, bool report) {
+  Seq s;
+  s.q0 = __ldg(a.q_start + b);
+  const int q1 = __ldg(a.q_start + b + 1);
+  bool bad = s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || q1 - s.q0 > a.max_q;
+  s.n = bad ? 0 : q1 - s.q0;
+  if (a.k_start) {
+    s.k0 = __ldg(a.k_start + b);
+    s.m = __ldg(a.k_len + b);
+    bool bad_k = s.k0 < 0 || s.m < 0 || s.k0 > a.Tk || s.m > a.Tk - s.k0;
+    if (apart && b > 0 && !bad_k)
+      bad_k = (int64_t)__ldg(a.k_start + b - 1) + __ldg(a.k_len + b - 1) > s.k0;
+    if (bad_k) s.k0 = s.m = 0;
+    bad |= bad_k;
+  } else {
+    s.k0 = s.q0;
+    s.m = s.n;
+  }
+  if (bad && report) set_status(a.status, MOE_ERR_DEVICE_BAD_INPUT, b);
+  return s;
+}
+
+struct Tile {
+  int b;      // sequence, or -1: no such tile
+  int index;  // of its tiles, from 0
+  int count;  // of the sequence's tiles
+};
+
+// The block's tile `want` of all sequences' tiles of `rows` query rows (KEYS: key rows), one after
+// the other. Every thread calls it. Each thread takes the sequences of an equal share of B, the
+// block scans the shares' tiles, and the thread whose share holds the wanted one walks it. Up to
+// 256 sequences that is one load and two exchanges; it stands in for a plan kernel in front.
+template <int THREADS, bool KEYS>
+__device__ Tile find_tile(const AttnArgs& a, int64_t want, int rows, bool apart, bool report) {
+  __shared__ int sWarp[THREADS / 32];
+  __shared__ Tile sTile;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int share = (a.B + THREADS - 1) / THREADS;
+  const int b0 = min(a.B, tid * share), b1 = min(a.B, b0 + share);
+  auto tiles = [&](int b, bool tell) {
+    const Seq s = load_seq(a, b, apart, tell);
+    return ((KEYS ? s.m : s.n) + rows - 1) / rows;
+  };
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles(b, report);
+  int inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
+  }
+  if (lane == 31) sWarp[warp] = inc;
+  if (tid == 0) sTile = Tile{-1, 0, 0};
+  __syncthreads();
+  int before = inc - mine;
+  for (int w = 0; w < warp; ++w) before += sWarp[w];
+  if (want >= before && want < before + mine) {
+    int left = (int)want - before;
+    for (int b = b0; b < b1; ++b) {
+      const int n = tiles(b, false);
+      if (left < n) {
+        sTile = Tile{b, left, n};
+        break;
+      }
+      left -= n;
+    }
+  }
+  __syncthreads();
+  return sTile;
+}
+
+// Keys that query row i of a sequence sees: [0, visible).
+__device__ __forceinline__ int visible(const AttnArgs& a, const Seq& s, int i) {
+  return a.causal ? min(s.m, i + 1 + s.m - s.n) : s.m;  // may be <= 0
+}
+
+// ---- launchers of the variants
+cudaError_t launch_simt(const AttnArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_simt_backward(const AttnArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_delta(const AttnArgs& a, bool bf16, cudaStream_t s);
+
+}  // namespace attn
+}  // namespace moe

@@ -1,0 +1,376 @@
+// Attention and its backward on the FMA units, in fp32 throughout: fp32 tensors, and bf16 ones whose
+// rows the tensor-core kernels cannot load (channels or strides that are no multiples of 16 bytes).
+//
+//   s_ij = scale q_i . k_j;  lse_i = log sum_j exp s_ij;  o_i = sum_j exp(s_ij - lse_i) v_j
+//   delta_i = do_i . o_i;  ds_ij = p_ij (do_i . v_j - delta_i) scale
+//   dv_j = sum_i p_ij do_i;  dk_j = sum_i ds_ij q_i;  dq_i = sum_j ds_ij k_j
+//
+// A block of 256 threads owns 64 query rows (dk, dv: 64 key rows) and goes over the other side in
+// tiles of 64, with the running maximum and sum of the softmax; scores are never stored. Every thread
+// forms 4 x 4 scores, and 4 rows x DP / 16 columns of the results in registers. Bound by FMA issue:
+// two 64 x 64 x D products a tile forward, five backward (in two kernels, which form the scores and
+// do . v twice; in return no result is added to by two blocks, so the bits never change).
+#include "attn.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int R = 64;       // rows of a tile
+constexpr int PS = R + 4;   // row length of the scores in shared memory
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float* d, float v) { *d = v; }
+__device__ __forceinline__ void from_f(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
+
+// Rows [row0, row0 + live) of one head (base points at its first channel of row 0) as fp32, times f,
+// zeros past the last row and channel.
+template <typename T, int DP>
+__device__ __forceinline__ void load_tile(float* dst, const void* base, int64_t ld, int64_t row0, int live, int D, float f) {
+  const T* src = static_cast<const T*>(base) + row0 * ld;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < R * DP; i += kThreads) {
+    const int r = i / DP, d = i % DP;
+    dst[r * (DP + 4) + d] = r < live && d < D ? f * to_f(src[(int64_t)r * ld + d]) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+
+// c[r][j] += x row (4 ty + r) . y row (tx + 16 j)
+template <int DP>
+__device__ __forceinline__ void scores(float (&c)[4][4], const float* x, const float* y, int ty, int tx) {
+  constexpr int LD = DP + 4;
+#pragma unroll 4
+  for (int d = 0; d < DP; d += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(x + (4 * ty + r) * LD + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * LD + d);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[r][j] = dot4(a[r], b[j], c[r][j]);
+  }
+}
+
+// acc[r][c] += sum_j w[4 ty + r][j] y[j][column c of this thread]: kV neighbouring columns, from
+// kV tx on, of every 16 kV.
+template <int DP>
+struct Cols {
+  static constexpr int kN = DP / 16;                    // columns of a thread
+  static constexpr int kV = kN < 4 ? kN : 4;            // neighbouring ones
+};
+template <int DP>
+__device__ __forceinline__ void accumulate(float (&acc)[4][DP / 16], const float* w, const float* y, int ty, int tx) {
+  constexpr int LD = DP + 4, kN = Cols<DP>::kN, kV = Cols<DP>::kV;
+#pragma unroll 2
+  for (int j0 = 0; j0 < R; j0 += 4) {
+    float p[4][4];  // [row][j]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 t = *reinterpret_cast<const float4*>(w + (4 * ty + i) * PS + j0);
+      p[i][0] = t.x, p[i][1] = t.y, p[i][2] = t.z, p[i][3] = t.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < kN; c += kV) {
+        float v[kV];
+        const float* src = y + (j0 + j) * LD + kV * tx + 16 * c;
+        if constexpr (kV == 4) {
+          const float4 t = *reinterpret_cast<const float4*>(src);
+          v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+        } else {
+#pragma unroll
+          for (int l = 0; l < kV; ++l) v[l] = src[l];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int l = 0; l < kV; ++l) acc[r][c + l] = fmaf(p[r][j], v[l], acc[r][c + l]);
+      }
+  }
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void store_rows(void* base, int64_t ld, int64_t row0, int live, int D, const float (&acc)[4][DP / 16],
+                                           const float (&f)[4], int ty, int tx) {
+  constexpr int kN = Cols<DP>::kN, kV = Cols<DP>::kV;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (4 * ty + r >= live) continue;
+    T* dst = static_cast<T*>(base) + (row0 + 4 * ty + r) * ld;
+#pragma unroll
+    for (int c = 0; c < kN; c += kV)
+#pragma unroll
+      for (int l = 0; l < kV; ++l) {
+        const int d = kV * tx + 16 * c + l;
+        if (d < D) from_f(dst + d, acc[r][c + l] * f[r]);
+      }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ const T* head(const void* p, int h, int D) {
+  return static_cast<const T*>(p) + (int64_t)h * D;
+}
+template <typename T>
+__device__ __forceinline__ T* head(void* p, int h, int D) {
+  return static_cast<T*>(p) + (int64_t)h * D;
+}
+
+template <int DP>
+constexpr size_t tile_floats() {
+  return (size_t)R * (DP + 4);
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a) {
+  extern __shared__ float4 smem4[];
+  float* sQ = reinterpret_cast<float*>(smem4);
+  float* sK = sQ + tile_floats<DP>();
+  float* sV = sK + tile_floats<DP>();
+  float* sP = sV + tile_floats<DP>();
+  const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, false, blockIdx.x == 0 && h == 0);
+  if (t.b < 0) return;
+  const Seq s = load_seq(a, t.b, false, false);
+  const int i0 = (t.count - 1 - t.index) * R, rows = min(R, s.n - i0);  // the longest first
+  load_tile<T, DP>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, a.scale);
+
+  float acc[4][DP / 16] = {}, top[4], sum[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) top[r] = -INFINITY, sum[r] = 0.0f;
+  const int keys = visible(a, s, i0 + rows - 1);
+  for (int j0 = 0; j0 < keys; j0 += R) {
+    __syncthreads();
+    const int live = min(R, s.m - j0);
+    load_tile<T, DP>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, live, a.D, 1.0f);
+    load_tile<T, DP>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, live, a.D, 1.0f);
+    __syncthreads();
+    float c[4][4] = {};
+    scores<DP>(c, sQ, sK, ty, tx);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int end = visible(a, s, i0 + 4 * ty + r) - j0;
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (tx + 16 * j >= end) c[r][j] = -INFINITY;
+        m = fmaxf(m, c[r][j]);
+      }
+#pragma unroll
+      for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      m = fmaxf(m, top[r]);
+      const float base = m == -INFINITY ? 0.0f : m;  // no key yet: exp(-inf - 0) = 0
+      const float keep = expf(top[r] - base);
+      float part = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = expf(c[r][j] - base);
+        sP[(4 * ty + r) * PS + tx + 16 * j] = p;
+        part += p;
+      }
+#pragma unroll
+      for (int off = 8; off; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+      sum[r] = sum[r] * keep + part;
+      top[r] = m;
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) acc[r][d] *= keep;
+    }
+    __syncwarp();  // a row's scores come from the 16 threads that use them
+    accumulate<DP>(acc, sP, sV, ty, tx);
+  }
+  float f[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f[r] = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];  // no visible key: a row of zeros
+    if (tx == 0 && 4 * ty + r < rows)
+      a.lse[(int64_t)h * a.Tq + s.q0 + i0 + 4 * ty + r] = sum[r] == 0.0f ? -INFINITY : top[r] + logf(sum[r]);
+  }
+  store_rows<T, DP>(head<T>(a.o, h, a.D), a.ld_o, s.q0 + i0, rows, a.D, acc, f, ty, tx);
+}
+
+struct RowStat {
+  float lse, delta;
+};
+
+// dq of 64 query rows of a head.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
+  extern __shared__ float4 smem4[];
+  float* sQ = reinterpret_cast<float*>(smem4);
+  float* sO = sQ + tile_floats<DP>();
+  float* sK = sO + tile_floats<DP>();
+  float* sV = sK + tile_floats<DP>();
+  float* sP = sV + tile_floats<DP>();
+  const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, true, blockIdx.x == 0 && h == 0);
+  if (t.b < 0) return;
+  const Seq s = load_seq(a, t.b, true, false);
+  const int i0 = (t.count - 1 - t.index) * R, rows = min(R, s.n - i0);
+  load_tile<T, DP>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, a.scale);
+  load_tile<T, DP>(sO, head<T>(a.d_o, h, a.D), a.ld_o, s.q0 + i0, rows, a.D, 1.0f);
+  RowStat st[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int64_t at = (int64_t)h * a.Tq + s.q0 + i0 + 4 * ty + r;
+    const bool live = 4 * ty + r < rows;
+    st[r] = RowStat{live ? a.lse[at] : 0.0f, live ? a.delta[at] : 0.0f};
+  }
+  float acc[4][DP / 16] = {};
+  const int keys = visible(a, s, i0 + rows - 1);
+  for (int j0 = 0; j0 < keys; j0 += R) {
+    __syncthreads();
+    const int live = min(R, s.m - j0);
+    load_tile<T, DP>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, live, a.D, 1.0f);
+    load_tile<T, DP>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, live, a.D, 1.0f);
+    __syncthreads();
+    float c[4][4] = {}, dp[4][4] = {};
+    scores<DP>(c, sQ, sK, ty, tx);
+    scores<DP>(dp, sO, sV, ty, tx);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int end = min(4 * ty + r < rows ? visible(a, s, i0 + 4 * ty + r) : 0, s.m) - j0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        sP[(4 * ty + r) * PS + tx + 16 * j] =
+            tx + 16 * j < end ? expf(c[r][j] - st[r].lse) * (dp[r][j] - st[r].delta) : 0.0f;
+    }
+    __syncwarp();
+    accumulate<DP>(acc, sP, sK, ty, tx);
+  }
+  const float f[4] = {a.scale, a.scale, a.scale, a.scale};
+  store_rows<T, DP>(head<T>(a.dq, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, acc, f, ty, tx);
+}
+
+// dk and dv of 64 key rows of a key head: over the query rows that see them, of every query head of
+// its group. Scores are transposed: key rows by query rows.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) simt_dkv_kernel(const AttnArgs a) {
+  extern __shared__ float4 smem4[];
+  float* sK = reinterpret_cast<float*>(smem4);
+  float* sV = sK + tile_floats<DP>();
+  float* sQ = sV + tile_floats<DP>();
+  float* sO = sQ + tile_floats<DP>();
+  float* sP = sO + tile_floats<DP>();
+  float* sS = sP + R * PS;
+  __shared__ RowStat sStat[R];
+  const int hk = blockIdx.y, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const Tile t = find_tile<kThreads, true>(a, blockIdx.x, R, true, blockIdx.x == 0 && hk == 0);
+  if (t.b < 0) return;
+  const Seq s = load_seq(a, t.b, true, false);
+  const int j0 = t.index * R, rows = min(R, s.m - j0);
+  load_tile<T, DP>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, rows, a.D, 1.0f);
+  load_tile<T, DP>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, rows, a.D, 1.0f);
+  float dk[4][DP / 16] = {}, dv[4][DP / 16] = {};
+  // the first query row that sees key j0
+  const int first = a.causal ? max(0, j0 - (s.m - s.n)) : 0;
+  for (int h = hk * a.group; h < (hk + 1) * a.group; ++h)
+    for (int i0 = first / R * R; i0 < s.n; i0 += R) {
+      __syncthreads();
+      const int live = min(R, s.n - i0);
+      load_tile<T, DP>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, live, a.D, a.scale);
+      load_tile<T, DP>(sO, head<T>(a.d_o, h, a.D), a.ld_o, s.q0 + i0, live, a.D, 1.0f);
+      if (threadIdx.x < R) {
+        const int64_t at = (int64_t)h * a.Tq + s.q0 + i0 + threadIdx.x;
+        const bool in = (int)threadIdx.x < live;
+        sStat[threadIdx.x] = RowStat{in ? a.lse[at] : 0.0f, in ? a.delta[at] : 0.0f};
+      }
+      __syncthreads();
+      float c[4][4] = {}, dp[4][4] = {};
+      scores<DP>(c, sK, sQ, ty, tx);
+      scores<DP>(dp, sV, sO, ty, tx);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = tx + 16 * j;  // the query row of the thread's column
+        const RowStat st = sStat[i];
+        const int end = i < live ? min(visible(a, s, i0 + i), s.m) - j0 : 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float p = 4 * ty + r < end ? expf(c[r][j] - st.lse) : 0.0f;
+          sP[(4 * ty + r) * PS + i] = p;
+          sS[(4 * ty + r) * PS + i] = p == 0.0f ? 0.0f : p * (dp[r][j] - st.delta);
+        }
+      }
+      __syncwarp();
+      accumulate<DP>(dv, sP, sO, ty, tx);
+      accumulate<DP>(dk, sS, sQ, ty, tx);  // q holds the scale
+    }
+  const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+  store_rows<T, DP>(head<T>(a.dk, hk, a.D), a.ld_k, s.k0 + j0, rows, a.D, dk, one, ty, tx);
+  store_rows<T, DP>(head<T>(a.dv, hk, a.D), a.ld_v, s.k0 + j0, rows, a.D, dv, one, ty, tx);
+}
+
+// delta: a warp for every query row and head. Rows in no sequence are formed too (nothing reads them).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) delta_kernel(const AttnArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int lane = threadIdx.x & 31;
+  if (i >= (int64_t)a.Tq * a.Hq) return;
+  const int64_t row = i / a.Hq;
+  const int h = (int)(i - row * a.Hq);
+  const T* o = head<T>((const void*)a.o, h, a.D) + row * a.ld_o;
+  const T* d = head<T>(a.d_o, h, a.D) + row * a.ld_o;
+  float sum = 0.0f;
+  for (int c = lane; c < a.D; c += 32) sum = fmaf(to_f(o[c]), to_f(d[c]), sum);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) a.delta[(int64_t)h * a.Tq + row] = sum;
+}
+
+template <void (*KERN)(AttnArgs)>
+cudaError_t launch_tiles(dim3 grid, size_t smem, const AttnArgs& a, cudaStream_t s) {
+  static const cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  KERN<<<grid, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int DP>
+cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
+  const size_t smem = (3 * tile_floats<DP>() + R * PS) * sizeof(float);
+  return launch_tiles<simt_forward_kernel<T, DP>>(dim3((unsigned)(a.Tq / R + a.B), a.Hq), smem, a, s);
+}
+
+template <typename T, int DP>
+cudaError_t backward(const AttnArgs& a, cudaStream_t s) {
+  const size_t smem = (4 * tile_floats<DP>() + R * PS) * sizeof(float);
+  cudaError_t e = cudaSuccess;
+  if (a.Tq > 0) e = launch_tiles<simt_dq_kernel<T, DP>>(dim3((unsigned)(a.Tq / R + a.B), a.Hq), smem, a, s);
+  if (e != cudaSuccess || a.Tk == 0) return e;
+  return launch_tiles<simt_dkv_kernel<T, DP>>(dim3((unsigned)(a.Tk / R + a.B), a.Hkv), smem + R * PS * sizeof(float), a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_delta(const AttnArgs& a, bool bf16, cudaStream_t s) {
+  const int64_t blocks = ceil_div((int64_t)a.Tq * a.Hq, kThreads / 32);
+  if (blocks == 0) return cudaSuccess;
+  if (bf16) delta_kernel<__nv_bfloat16><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  else delta_kernel<float><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_simt(const AttnArgs& a, bool bf16, cudaStream_t s) {
+  if (a.D <= 32) return bf16 ? forward<__nv_bfloat16, 32>(a, s) : forward<float, 32>(a, s);
+  if (a.D <= 64) return bf16 ? forward<__nv_bfloat16, 64>(a, s) : forward<float, 64>(a, s);
+  return bf16 ? forward<__nv_bfloat16, 128>(a, s) : forward<float, 128>(a, s);
+}
+
+cudaError_t launch_simt_backward(const AttnArgs& a, bool bf16, cudaStream_t s) {
+  const cudaError_t e = launch_delta(a, bf16, s);
+  if (e != cudaSuccess) return e;
+  if (a.D <= 32) return bf16 ? backward<__nv_bfloat16, 32>(a, s) : backward<float, 32>(a, s);
+  if (a.D <= 64) return bf16 ? backward<__nv_bfloat16, 64>(a, s) : backward<float, 64>(a, s);
+  return bf16 ? backward<__nv_bfloat16, 128>(a, s) : backward<float, 128>(a, s);
+}
+
+}  // namespace attn
+}  // namespace moe

@@ -1,6 +1,6 @@
 // Launchers of the operators on either side of the MoE layer in a training or serving step:
-// block norms (norm.cu), vocabulary head loss (head_loss.cu), token embedding (embed.cu) and
-// gradient clipping (grad_clip.cu). All stream-ordered, no host sync, no allocation.
+// block norms (norm.cu), rotary positions (rope.cu), attention (attn*.cu), vocabulary head loss
+// (head_loss.cu), token embedding (embed.cu) and gradient clipping (grad_clip.cu). All stream-ordered, no host sync, no allocation.
 #pragma once
 
 #include "moe_internal.cuh"
@@ -84,5 +84,29 @@ cudaError_t launch_head_loss(const moe_head_config_t& c, const void* x, const vo
 cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x, const void* w, const int32_t* target,
                                       const float* lse, const float* dloss, const float* mean, void* dx, void* dw,
                                       void* ws, DeviceStatus* st, cudaStream_t s);
+
+// ---- rotary positions
+constexpr int kRopeMaxD = 4096;  // a token's cosines and sines fit a block's shared memory
+cudaError_t launch_rope_table(const moe_rope_freq_t& c, uint64_t* table, cudaStream_t s);
+cudaError_t launch_rope(const moe_rope_config_t& c, const void* q, const void* k, const void* v, const int32_t* pos,
+                        const int32_t* slot, const uint64_t* table, void* q_out, void* k_out, void* v_out,
+                        DeviceStatus* st, cudaStream_t s);
+cudaError_t launch_rope_backward(const moe_rope_config_t& c, const void* dq_out, const void* dk_out, const int32_t* pos,
+                                 const uint64_t* table, void* dq, void* dk, cudaStream_t s);
+
+// ---- attention
+constexpr int kAttnMaxD = 128;
+struct AttnSeqs {  // where the sequences' rows are: k_start and k_len NULL: keys beside their queries
+  const int32_t *q_start, *k_start, *k_len;
+};
+struct AttnScratch {  // workspace offsets, after the status head
+  size_t delta, total;
+};
+AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward);
+cudaError_t launch_attn(const moe_attn_config_t& c, const void* q, const void* k, const void* v, const AttnSeqs& at,
+                        void* o, float* lse, void* ws, DeviceStatus* st, cudaStream_t s);
+cudaError_t launch_attn_backward(const moe_attn_config_t& c, const void* q, const void* k, const void* v,
+                                 const AttnSeqs& at, const void* o, const float* lse, const void* d_o, void* dq, void* dk,
+                                 void* dv, void* ws, DeviceStatus* st, cudaStream_t s);
 
 }  // namespace moe

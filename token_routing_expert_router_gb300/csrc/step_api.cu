@@ -47,6 +47,49 @@ moe_status_t validate(const moe_grad_t* g, int32_t count) {
   return MOE_OK;
 }
 
+moe_status_t validate(const moe_rope_freq_t* c) {
+  if (!c || c->rot < 0 || c->rot % 2 || c->scaling < MOE_ROPE_UNSCALED || c->scaling > MOE_ROPE_YARN)
+    return MOE_ERR_INVALID_ARG;
+  if (!(c->base > 0.0) || !isfinite(c->base)) return MOE_ERR_INVALID_ARG;
+  if (c->scaling != MOE_ROPE_UNSCALED && (!(c->factor > 0.0) || !isfinite(c->factor))) return MOE_ERR_INVALID_ARG;
+  if (c->scaling == MOE_ROPE_YARN && (!(c->trained_len > 0.0) || !isfinite(c->trained_len) || !isfinite(c->beta_slow) ||
+                                      !isfinite(c->beta_fast) || !(c->beta_fast > c->beta_slow)))
+    return MOE_ERR_INVALID_ARG;
+  return c->rot > kRopeMaxD ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// A row stride of `heads` heads of D channels: 0 (dense), or room for a row.
+bool ld_ok(int64_t ld, int64_t heads, int64_t D) { return ld == 0 || (ld >= heads * D && ld <= ((int64_t)1 << 31)); }
+
+moe_status_t validate(const moe_rope_config_t* c) {
+  if (!c || c->T < 0 || c->Hq < 0 || c->Hk < 0 || c->Hq + (int64_t)c->Hk < 1 || c->D < 1) return MOE_ERR_INVALID_ARG;
+  if (c->rot < 0 || c->rot % 2 || c->first < 0 || (int64_t)c->first + c->rot > c->D || c->slots < 0) return MOE_ERR_INVALID_ARG;
+  if ((c->layout != MOE_ROPE_HALF && c->layout != MOE_ROPE_INTERLEAVED) || !act_ok(c->act_dtype) || !isfinite(c->magnitude))
+    return MOE_ERR_INVALID_ARG;
+  if (!ld_ok(c->ld_q, c->Hq, c->D) || !ld_ok(c->ld_k, c->Hk, c->D) || !ld_ok(c->ld_v, c->Hk, c->D) ||
+      !ld_ok(c->ld_q_out, c->Hq, c->D) || !ld_ok(c->ld_k_out, c->Hk, c->D) || !ld_ok(c->ld_v_out, c->Hk, c->D))
+    return MOE_ERR_INVALID_ARG;
+  if (c->T > (1 << 30) || c->D > kRopeMaxD || c->Hq > (1 << 14) || c->Hk > (1 << 14)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t validate(const moe_attn_config_t* c) {
+  if (!c || c->Tq < 0 || c->Tk < 0 || c->B < 0 || c->Hq < 1 || c->Hkv < 1 || c->Hq % c->Hkv || c->D < 1)
+    return MOE_ERR_INVALID_ARG;
+  if ((c->causal != 0 && c->causal != 1) || c->max_q < 0 || !act_ok(c->act_dtype)) return MOE_ERR_INVALID_ARG;
+  if (!(c->scale > 0.0f) || !isfinite(c->scale)) return MOE_ERR_INVALID_ARG;
+  if (!ld_ok(c->ld_q, c->Hq, c->D) || !ld_ok(c->ld_k, c->Hkv, c->D) || !ld_ok(c->ld_v, c->Hkv, c->D) ||
+      !ld_ok(c->ld_o, c->Hq, c->D))
+    return MOE_ERR_INVALID_ARG;
+  if (c->D > kAttnMaxD || c->Hq > (1 << 14) || c->B > (1 << 20) || c->Tq > (1 << 30) || c->Tk > (1 << 30))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Rows of act elements: aligned to their elements (views of a wider row will do).
+bool rows_ok(const void* p, int32_t dtype) { return p != nullptr && ((uintptr_t)p & (dtype == MOE_DTYPE_BF16 ? 1u : 3u)) == 0; }
+bool ints_ok(const void* p) { return p != nullptr && ((uintptr_t)p & 3u) == 0; }
+
 DeviceStatus* word(void* ws) { return static_cast<DeviceStatus*>(ws); }
 
 moe_status_t clip(const moe_grad_t* grads, int32_t count, float max_norm, float* norm, void* ws, moe_stream_t stream) {
@@ -159,6 +202,90 @@ moe_status_t moe_embed_backward(const moe_embed_config_t* cfg, const int32_t* to
   if (cfg->T > 0 && (!ok16(token) || !ok16(dout) || !ok16(ws))) return MOE_ERR_INVALID_ARG;
   return status_of_launch(
       launch_embed_backward(*cfg, token, dout, dtable, accumulate, ws, word(ws), (cudaStream_t)stream));
+}
+
+moe_status_t moe_rope_table(const moe_rope_freq_t* freq, uint64_t* table, moe_stream_t stream) {
+  const moe_status_t v = validate(freq);
+  if (v != MOE_OK) return v;
+  if (freq->rot == 0) return MOE_OK;
+  if (!ok16(table)) return MOE_ERR_INVALID_ARG;
+  return status_of_launch(launch_rope_table(*freq, table, (cudaStream_t)stream));
+}
+
+moe_status_t moe_rope(const moe_rope_config_t* cfg, const void* q, const void* k, const void* v, const int32_t* pos,
+                      const int32_t* slot, const uint64_t* table, void* q_out, void* k_out, void* v_out, void* ws,
+                      moe_stream_t stream) {
+  const moe_status_t st = validate(cfg);
+  if (st != MOE_OK) return st;
+  if ((v != nullptr) != (v_out != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  const int32_t d = cfg->act_dtype;
+  if (cfg->Hq > 0 && (!rows_ok(q, d) || !rows_ok(q_out, d))) return MOE_ERR_INVALID_ARG;
+  if (cfg->Hk > 0 && (!rows_ok(k, d) || !rows_ok(k_out, d) || (v && (!rows_ok(v, d) || !rows_ok(v_out, d)))))
+    return MOE_ERR_INVALID_ARG;
+  if (!ints_ok(pos) || (slot && (!ints_ok(slot) || !ok16(ws))) || (cfg->rot > 0 && !ok16(table))) return MOE_ERR_INVALID_ARG;
+  return status_of_launch(
+      launch_rope(*cfg, q, k, v, pos, slot, table, q_out, k_out, v_out, word(ws), (cudaStream_t)stream));
+}
+
+moe_status_t moe_rope_backward(const moe_rope_config_t* cfg, const void* dq_out, const void* dk_out, const int32_t* pos,
+                               const uint64_t* table, void* dq, void* dk, moe_stream_t stream) {
+  const moe_status_t st = validate(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  const int32_t d = cfg->act_dtype;
+  if (cfg->Hq > 0 && (!rows_ok(dq_out, d) || !rows_ok(dq, d))) return MOE_ERR_INVALID_ARG;
+  if (cfg->Hk > 0 && (!rows_ok(dk_out, d) || !rows_ok(dk, d))) return MOE_ERR_INVALID_ARG;
+  if (!ints_ok(pos) || (cfg->rot > 0 && !ok16(table))) return MOE_ERR_INVALID_ARG;
+  return status_of_launch(launch_rope_backward(*cfg, dq_out, dk_out, pos, table, dq, dk, (cudaStream_t)stream));
+}
+
+moe_status_t moe_attn_workspace_size(const moe_attn_config_t* cfg, size_t* bytes) {
+  const moe_status_t v = validate(cfg);
+  if (v != MOE_OK) return v;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = attn_scratch(*cfg, false).total;
+  return MOE_OK;
+}
+
+moe_status_t moe_attn(const moe_attn_config_t* cfg, const void* q, const void* k, const void* v, const int32_t* q_start,
+                      const int32_t* k_start, const int32_t* k_len, void* o, float* lse, void* ws, moe_stream_t stream) {
+  const moe_status_t st = validate(cfg);
+  if (st != MOE_OK) return st;
+  if ((k_start != nullptr) != (k_len != nullptr) || (!k_start && cfg->Tk < cfg->Tq)) return MOE_ERR_INVALID_ARG;
+  if (cfg->Tq == 0 || cfg->B == 0) return MOE_OK;
+  const int32_t d = cfg->act_dtype;
+  if (!rows_ok(q, d) || !rows_ok(o, d) || !ints_ok(q_start) || !ints_ok(lse) || !ok16(ws)) return MOE_ERR_INVALID_ARG;
+  if (cfg->Tk > 0 && (!rows_ok(k, d) || !rows_ok(v, d))) return MOE_ERR_INVALID_ARG;
+  if (k_start && (!ints_ok(k_start) || !ints_ok(k_len))) return MOE_ERR_INVALID_ARG;
+  return status_of_launch(
+      launch_attn(*cfg, q, k, v, AttnSeqs{q_start, k_start, k_len}, o, lse, ws, word(ws), (cudaStream_t)stream));
+}
+
+moe_status_t moe_attn_backward_workspace_size(const moe_attn_config_t* cfg, size_t* bytes) {
+  const moe_status_t v = validate(cfg);
+  if (v != MOE_OK) return v;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = attn_scratch(*cfg, true).total;
+  return MOE_OK;
+}
+
+moe_status_t moe_attn_backward(const moe_attn_config_t* cfg, const void* q, const void* k, const void* v,
+                               const int32_t* q_start, const int32_t* k_start, const int32_t* k_len, const void* o,
+                               const float* lse, const void* d_o, void* dq, void* dk, void* dv, void* ws,
+                               moe_stream_t stream) {
+  const moe_status_t st = validate(cfg);
+  if (st != MOE_OK) return st;
+  if ((k_start != nullptr) != (k_len != nullptr) || (!k_start && cfg->Tk < cfg->Tq)) return MOE_ERR_INVALID_ARG;
+  if (cfg->B == 0 || (cfg->Tq == 0 && cfg->Tk == 0)) return MOE_OK;
+  const int32_t d = cfg->act_dtype;
+  if (!ints_ok(q_start) || !ok16(ws)) return MOE_ERR_INVALID_ARG;
+  if (cfg->Tq > 0 && (!rows_ok(q, d) || !rows_ok(o, d) || !rows_ok(d_o, d) || !rows_ok(dq, d) || !ints_ok(lse)))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->Tk > 0 && (!rows_ok(k, d) || !rows_ok(v, d) || !rows_ok(dk, d) || !rows_ok(dv, d))) return MOE_ERR_INVALID_ARG;
+  if (k_start && (!ints_ok(k_start) || !ints_ok(k_len))) return MOE_ERR_INVALID_ARG;
+  return status_of_launch(launch_attn_backward(*cfg, q, k, v, AttnSeqs{q_start, k_start, k_len}, o, lse, d_o, dq, dk, dv,
+                                               ws, word(ws), (cudaStream_t)stream));
 }
 
 moe_status_t moe_grad_clip_workspace_size(int32_t count, size_t* bytes) {
