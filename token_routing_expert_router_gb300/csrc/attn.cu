@@ -25,6 +25,17 @@ attn::AttnArgs args_of(const moe_attn_config_t& c, const void* q, const void* k,
 
 }  // namespace
 
+namespace attn {
+
+bool tc_rows(const AttnArgs& a, bool backward) {
+  uint64_t at = (uint64_t)a.q | (uint64_t)a.k | (uint64_t)a.v | (uint64_t)a.o;
+  if (backward) at |= (uint64_t)a.d_o | (uint64_t)a.dq | (uint64_t)a.dk | (uint64_t)a.dv;
+  at |= (uint64_t)(2 * a.D) | (uint64_t)(2 * a.ld_q) | (uint64_t)(2 * a.ld_k) | (uint64_t)(2 * a.ld_v) | (uint64_t)(2 * a.ld_o);
+  return at % 16 == 0;
+}
+
+}  // namespace attn
+
 AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward) {
   AttnScratch s{};
   size_t at = kWsHead;
@@ -40,6 +51,7 @@ cudaError_t launch_attn(const moe_attn_config_t& c, const void* q, const void* k
                         void* o, float* lse, void* ws, DeviceStatus* st, cudaStream_t s) {
   if (c.Tq == 0 || c.B == 0) return cudaSuccess;
   const attn::AttnArgs a = args_of(c, q, k, v, at, o, lse, st);
+  if (c.act_dtype == MOE_DTYPE_BF16 && attn::tc_rows(a, false)) return attn::launch_tc(a, s);
   return attn::launch_simt(a, c.act_dtype == MOE_DTYPE_BF16, s);
 }
 

@@ -1,0 +1,337 @@
+// Attention on the tensor cores (bf16, D <= 128), one pass over the keys.
+//
+// A CTA has two tiles of 128 rows of Q against one key head, and goes over its keys in tiles of 128:
+//   S = Q K^T (tensor memory) -> P = exp2(c (S - m)), bf16, over S's columns -> O += P V (tensor memory)
+// Rows of a tile are (query, head) pairs, `pack` query heads of the group side by side: a key tile is
+// loaded once for 256 of them, and few queries of many heads still fill a tile.
+// Warp 0 loads by TMA (K and V tiles through one ring), warp 1 issues the products, and each of the two
+// warpgroups 1 and 2 is one tile's softmax, a thread a row: no exchange between threads. While one
+// tile's softmax runs, the tensor cores work on the other tile's products; S is free for the next scores
+// as soon as P V has been issued behind them, since one thread's products run in their order.
+//
+// The running maximum is only followed when it grows by more than 2^8 in the exponentials (then O is
+// read, scaled and written back, by the rows' own threads); until then the old one is as good a
+// reference, since all sums are fp32 and P's rounding is relative. The keys are taken from the last to
+// the first, so that the tile with the mask comes first. Key rows behind the sequence's end belong to
+// somebody else: their scores are replaced, and their V rows are zeroed in shared memory.
+#include "attn_tc.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int BK = 128;  // keys of a tile
+constexpr int kSmem = 227 * 1024;
+
+template <int DP>
+struct Fwd {
+  static constexpr int kSlabs = DP / 64;
+  static constexpr int kTile = 128 * DP * 2;                     // bytes of a tile of Q, K or V
+  static constexpr int kUnits = (kSmem - 2048 - 2 * kTile) / kTile < 8 ? (kSmem - 2048 - 2 * kTile) / kTile : 8;
+  static constexpr size_t kBytes = 1024 + (2 + kUnits) * kTile + 256;
+};
+
+struct FwdParams {
+  AttnArgs a;
+  int pack;     // query heads in a tile
+  float c;      // scale log2(e)
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
+  using F = Fwd<DP>;
+  constexpr int kUnits = F::kUnits;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * F::kTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kUnits * F::kTile);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + kUnits;
+  uint64_t* q_full = bars + 2 * kUnits;
+  uint64_t* s_full = q_full + 1;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* drain = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * 8 + 8) * 8 + 8 <= 256);
+
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h0 = blockIdx.y * p.pack, hk = h0 / a.group;  // first query head, key head
+  const int per = 128 / p.pack;                           // queries of a tile
+  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, 2 * per, false, blockIdx.x == 0 && blockIdx.y == 0);
+  if (t.b < 0) return;
+  const Seq s = load_seq(a, t.b, false, false);
+  const int i0 = (t.count - 1 - t.index) * 2 * per;  // the longest first
+  // key tiles of the two row tiles
+  auto key_tiles = [&](int m) {
+    const int first = i0 + m * per, last = min(first + per, s.n) - 1;
+    return last < first ? 0 : (max(0, visible(a, s, last)) + BK - 1) / BK;
+  };
+  const int n0 = key_tiles(0), n1 = key_tiles(1), steps = max(n0, n1);
+  auto tiles_of = [&](int m) { return m ? n1 : n0; };
+
+  if (threadIdx.x == 0) {
+    for (int u = 0; u < kUnits; ++u) {
+      mbar_init(&full[u], 1);
+      mbar_init(&empty[u], 1);
+    }
+    mbar_init(q_full, 1);
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&s_full[m], 1);
+      mbar_init(&p_full[m], 4);
+      mbar_init(&o_full[m], 1);
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tO = tmem + 256;  // S and P of tile m at 128 m, O at DP m
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 0 && lane == 0 && steps > 0) {
+      // ===================== loads: Q; K of the last tile; then K of the next and V of this one, in turn
+      mbar_arrive_expect_tx(q_full, 2 * F::kTile);
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int d = 0; d < F::kSlabs; ++d)
+          tma_load_3d(&tmQ, sQ + m * F::kTile + d * 16384, q_full, 64 * d, h0, s.q0 + i0 + m * per);
+      int unit = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap* map, int tile) {
+        if (!ok || !(ok = mbar_wait(&empty[unit], phase ^ 1, abort, kTimeoutNs, a.status))) return;
+        mbar_arrive_expect_tx(&full[unit], F::kTile);
+#pragma unroll
+        for (int d = 0; d < F::kSlabs; ++d)
+          tma_load_3d(map, sKV + unit * F::kTile + d * 16384, &full[unit], 64 * d, hk, s.k0 + tile * BK);
+        ++issued;
+        if (++unit == kUnits) unit = 0, phase ^= 1;
+      };
+      load(&tmK, steps - 1);
+      for (int j = steps - 1; j >= 0 && ok; --j) {
+        if (j > 0) load(&tmK, j - 1);
+        load(&tmV, j);
+      }
+      // leave no copy in flight
+      mbar_wait_drain(q_full, 0, kTimeoutNs, a.status);
+      for (int i = 0; i < min(issued, kUnits); ++i) {
+        const int u = (unit - 1 - i + 2 * kUnits) % kUnits;
+        mbar_wait_drain(&full[u], unit - 1 - i < 0 ? phase ^ 1 : phase, kTimeoutNs, a.status);
+      }
+    } else if (warp == 1 && steps > 0) {
+      // ===================== products
+      const uint32_t idesc_s = idesc_make(1, 128, BK);
+      const uint32_t idesc_o = idesc_make(1, 128, DP) | (1u << 16);  // V is read MN-major
+      int unit = 0;
+      uint32_t phase = 0;
+      auto wait_unit = [&] {
+        const bool ok = mbar_wait(&full[unit], phase, abort, kTimeoutNs, a.status);
+        return __all_sync(0xffffffffu, ok);
+      };
+      auto next = [&](int& u) {
+        u = unit;
+        if (++unit == kUnits) unit = 0, phase ^= 1;
+      };
+      auto scores = [&](int m, int u) {  // S_m = Q_m K^T
+        const uint32_t qa = smem_addr(sQ + m * F::kTile), ka = smem_addr(sKV + u * F::kTile);
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
+          mma_bf16(tS + 128 * m, desc_k_sw128(qa + off), desc_k_sw128(ka + off), idesc_s, k > 0);
+        }
+        mma_commit(&s_full[m]);
+      };
+      bool ok = mbar_wait(q_full, 0, abort, kTimeoutNs, a.status);
+      ok = __all_sync(0xffffffffu, ok) && wait_unit();
+      if (ok) {
+        tc_fence_after();
+        int uk, uv;
+        next(uk);
+        if (lane == 0) {
+          for (int m = 0; m < 2; ++m)
+            if (tiles_of(m) == steps) scores(m, uk);
+          mma_commit(&empty[uk]);
+        }
+        for (int j = steps - 1; j >= 0; --j) {
+          if (j > 0) {
+            if (!(ok = wait_unit())) break;
+            next(uk);
+          }
+          if (!(ok = wait_unit())) break;
+          next(uv);
+          if ((j + 1) * BK > s.m) clear_rows(sKV + uv * F::kTile, F::kSlabs, BK, s.m - j * BK, lane);
+          tc_fence_after();
+          for (int m = 0; m < 2 && ok; ++m) {
+            const int n = tiles_of(m);
+            if (j < n) {
+              ok = mbar_wait(&p_full[m], (n - 1 - j) & 1, abort, kTimeoutNs, a.status);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+              if (lane == 0) {  // O_m += P_m V
+                const uint32_t va = smem_addr(sKV + uv * F::kTile);
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k)
+                  mma_bf16_ta(tO + DP * m, tS + 128 * m + 8 * k, desc_mn_sw128(va + 2048 * k, 16384), idesc_o,
+                              j < n - 1 || k > 0);
+                if (j == 0) mma_commit(&o_full[m]);
+              }
+            }
+            if (lane == 0 && j > 0 && j - 1 < n) scores(m, uk);
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            mma_commit(&empty[uv]);
+            if (j > 0) mma_commit(&empty[uk]);
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0) {
+        mma_commit(drain);
+        mbar_wait_drain(drain, 0, kTimeoutNs, a.status);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ===================== softmax of tile m, a thread a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int m = warp / 4 - 1, quarter = warp & 3;
+    const int row = quarter * 32 + lane, i = i0 + m * per + row / p.pack, h = h0 + row % p.pack;
+    const int n = tiles_of(m);
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t my_s = tS + 128 * m + lanes, my_o = tO + DP * m + lanes;
+    const int seen = visible(a, s, i);                               // of this row
+    const int least = visible(a, s, i0 + m * per);                   // of the tile's first row
+    float top = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;
+    const float slack = 8.0f / p.c;
+    bool ok = true;
+    for (int j = n - 1; j >= 0; --j) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[m], (n - 1 - j) & 1, abort, kTimeoutNs, a.status)))) break;
+      tc_fence_after();
+      uint32_t r[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(my_s + 32 * q, r[q]);
+      tmem_ld_wait();
+      if ((j + 1) * BK > least) {
+        const int end = seen - j * BK;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int l = 0; l < 32; ++l)
+            if (32 * q + l >= end) r[q][l] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        mx[q] = __uint_as_float(r[q][0]);
+#pragma unroll
+        for (int l = 1; l < 32; ++l) mx[q] = fmaxf(mx[q], __uint_as_float(r[q][l]));
+      }
+      const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool grow = most > top + slack;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? ex2((top - most) * p.c) : 1.0f;  // 0 for the row's first key
+        if (grow) top = most;
+        sum0 *= f, sum1 *= f;
+        if (j < n - 1) {  // O holds the products up to the last tile: these scores were issued behind them
+#pragma unroll
+          for (int q = 0; q < DP / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(my_o + 32 * q, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int l = 0; l < 32; ++l) o[l] = __float_as_uint(__uint_as_float(o[l]) * f);
+            tmem_st32(my_o + 32 * q, o);
+          }
+        }
+      }
+      const float base = top == -INFINITY ? 0.0f : -top * p.c;  // no key yet: exp2(-inf) = 0
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        uint32_t w[32];
+#pragma unroll
+        for (int l = 0; l < 64; l += 2) {
+          float x = __uint_as_float(r[q + l / 32][l % 32]), y = __uint_as_float(r[q + l / 32][l % 32 + 1]);
+          scale2(x, y, p.c, base);
+          x = ex2(x), y = ex2(y);
+          add2(sum0, sum1, x, y);
+          w[l / 2] = pack2(x, y);
+        }
+        tmem_st32(my_s + 16 * q, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[m]);
+    }
+    // ===================== O / sum and the log sum
+    const float sum = sum0 + sum1;
+    if (n > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&o_full[m], 0, abort, kTimeoutNs, a.status));
+    tc_fence_after();
+    const bool live = ok && i < s.n;
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (int64_t)(s.q0 + i) * a.ld_o + (int64_t)h * a.D;
+#pragma unroll
+    for (int q = 0; q < DP / 32; ++q) {
+      uint32_t o[32];
+      if (n > 0) {
+        tmem_ld32(my_o + 32 * q, o);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int l = 0; l < 32; l += 8) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = sum == 0.0f ? 0.0f : __uint_as_float(o[l + e]) * f;  // no key: a row of zeros
+        if (live && 32 * q + l < a.D)
+          *reinterpret_cast<uint4*>(dst + 32 * q + l) =
+              make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+      }
+    }
+    if (live)
+      a.lse[(int64_t)h * a.Tq + s.q0 + i] = sum == 0.0f ? -INFINITY : (top * p.c + log2f(sum)) * kLn2;
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int DP>
+cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
+  FwdParams p{a, heads_packed(a.group), a.scale * kLog2e};
+  CUtensorMap q, k, v;
+  if (!head_map(&q, a.q, a.Tq, a.Hq, a.D, a.ld_q, p.pack, 128 / p.pack)) return cudaErrorInvalidValue;
+  if (a.Tk > 0) {
+    if (!head_map(&k, a.k, a.Tk, a.Hkv, a.D, a.ld_k, 1, BK) || !head_map(&v, a.v, a.Tk, a.Hkv, a.D, a.ld_v, 1, BK))
+      return cudaErrorInvalidValue;
+  } else {
+    k = v = q;  // no key is loaded
+  }
+  static const cudaError_t e =
+      cudaFuncSetAttribute(attn_forward_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fwd<DP>::kBytes);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(a.Tq / (256 / p.pack) + a.B), a.Hq / p.pack);
+  attn_forward_kernel<DP><<<grid, kThreads, Fwd<DP>::kBytes, s>>>(q, k, v, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) { return a.D <= 64 ? forward<64>(a, s) : forward<128>(a, s); }
+
+}  // namespace attn
+}  // namespace moe
