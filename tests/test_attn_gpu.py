@@ -17,6 +17,11 @@ def _built(lib):
     pass
 
 
+# The exponentials and the packed fp32 operations flush results below fp32's smallest normal value,
+# 2^-126, to zero: a probability is off by that much beside its relative error, and so is a product of it.
+FTZ = 2.0 ** -126
+
+
 def within(got, want, bound):
     if got.numel():
         within_all(got, want, bound)
@@ -136,8 +141,8 @@ class Batch:
     def _o_bound(self, p, ep, el, v, want):
         half = HALF[BF] if self.dt == BF else 0.0
         mag = p @ v.abs()
-        lost = (p * (ep + half)) @ v.abs() + (el[:, None] + (2 * p.shape[1] + 64) * U) * mag
-        return lost + HALF[self.dt] * (want.abs() + lost) + 1e-38
+        lost = (p * (ep + half) + FTZ) @ v.abs() + (el[:, None] + (2 * p.shape[1] + 64) * U) * mag
+        return lost + HALF[self.dt] * (want.abs() + lost) + FTZ
 
     def check_backward(self, dq, dk, dv):
         outside = [torch.ones(self.Tq if i == 0 else self.Tk, dtype=torch.bool, device="cuda") for i in range(3)]
@@ -163,18 +168,19 @@ class Batch:
                     ed = (do.abs() * eo).sum(1, keepdim=True) + 2 * (self.D + 8) * U * (do * o).abs().sum(1, keepdim=True)
                     ds = p * (dp - delta)
                     eds = p * (edp + ed) + ds.abs() * (ep + half + 4 * U) + p * 4 * U * (dp.abs() + delta.abs())
-                    eds = eds * (1 + half)
+                    # flushed: p (times dp - delta), and ds itself
+                    eds = eds * (1 + half) + FTZ * (dp.abs() + delta.abs() + 1)
                     want = self.scale * ds @ k
                     lost = self.scale * ((eds + acc * ds.abs()) @ k.abs())
-                    within(dq[rq, h], want, lost + HALF[self.dt] * (want.abs() + lost) + 4 * U * want.abs() + 1e-38)
+                    within(dq[rq, h], want, lost + HALF[self.dt] * (want.abs() + lost) + 4 * U * want.abs() + FTZ)
                     wv += p.t() @ do
-                    bv += (p * (ep + half + acc)).t() @ do.abs()
+                    bv += (p * (ep + half + acc) + FTZ).t() @ do.abs()
                     wk += self.scale * ds.t() @ q
                     bk += self.scale * (eds + acc * ds.abs()).t() @ q.abs()
                 # fp32 scales q by the scores' scale first: one rounding more
                 bk = bk + 4 * U * (bk + wk.abs())
-                within(dk[rk, hk], wk, bk + HALF[self.dt] * (wk.abs() + bk) + 1e-38)
-                within(dv[rk, hk], wv, bv + HALF[self.dt] * (wv.abs() + bv) + 1e-38)
+                within(dk[rk, hk], wk, bk + HALF[self.dt] * (wk.abs() + bk) + FTZ)
+                within(dv[rk, hk], wv, bv + HALF[self.dt] * (wv.abs() + bv) + FTZ)
         for rows, g in zip(outside, (dq, dk, dv)):
             assert (g[rows] == 7).all()
 

@@ -62,6 +62,7 @@ cudaError_t launch_attn_backward(const moe_attn_config_t& c, const void* q, cons
   attn::AttnArgs a = args_of(c, q, k, v, at, o, const_cast<float*>(lse), st);
   a.d_o = d_o, a.dq = dq, a.dk = dk, a.dv = dv;
   a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + attn_scratch(c, true).delta);
+  if (c.act_dtype == MOE_DTYPE_BF16 && attn::tc_rows(a, true)) return attn::launch_tc_backward(a, s);
   return attn::launch_simt_backward(a, c.act_dtype == MOE_DTYPE_BF16, s);
 }
 

@@ -112,6 +112,7 @@ __device__ __forceinline__ int visible(const AttnArgs& a, const Seq& s, int i) {
 bool tc_rows(const AttnArgs& a, bool backward);  // bf16 tensors' rows are multiples of 16 bytes
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_simt(const AttnArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_tc_backward(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_simt_backward(const AttnArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_delta(const AttnArgs& a, bool bf16, cudaStream_t s);
 
