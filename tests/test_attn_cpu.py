@@ -45,7 +45,7 @@ def test_rope_table_arguments(L):
     (dict(rot=3), INVALID), (dict(rot=66), INVALID), (dict(rot=32, first=33), INVALID), (dict(first=-1, rot=2), INVALID),
     (dict(first=2 ** 31 - 1, rot=2), INVALID), (dict(layout=2), INVALID), (dict(act_dtype=moe.E4M3), INVALID),
     (dict(slots=-1), INVALID), (dict(magnitude=float("nan")), INVALID), (dict(ld_q=255), INVALID), (dict(ld_k=-1), INVALID),
-    (dict(ld_v_out=127), INVALID), (dict(ld_q=1 << 32), INVALID), (dict(D=4098), UNSUPPORTED), (dict(Hq=20000), UNSUPPORTED),
+    (dict(ld_v_out=127), INVALID), (dict(ld_q=1 << 32), INVALID), (dict(D=4098), UNSUPPORTED), (dict(Hq=20000), UNSUPPORTED), (dict(Hk=2000, D=4096), UNSUPPORTED),
     (dict(T=(1 << 30) + 1), UNSUPPORTED), (dict(T=0), OK)])
 def test_rope_config(L, kw, code):
     c = ctypes.byref(rope_cfg(**kw))

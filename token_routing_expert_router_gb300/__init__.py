@@ -315,15 +315,18 @@ def _rows(t, ld, width: int):
         raise ValueError("expected a CUDA tensor")
     if 0 in t.shape:
         return t.data_ptr()
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and shape[1] * shape[2] == width and stride[0] == (ld or width):
+        return t.data_ptr()  # the usual case, first: a decoding step makes several of these calls
     inner = 1
-    for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
-        if size != 1 and stride != inner:
+    for size, step in zip(shape[:0:-1], stride[:0:-1]):
+        if size != 1 and step != inner:
             raise ValueError("expected rows of neighbouring elements")
         inner *= size
-    if t.dim() < 2 or inner != width:
+    if len(shape) < 2 or inner != width:
         raise ValueError(f"expected rows of {width} elements")
-    if t.shape[0] > 1 and t.stride(0) != (ld or width):
-        raise ValueError(f"rows {t.stride(0)} elements apart, {ld or width} in the configuration")
+    if shape[0] > 1 and stride[0] != (ld or width):
+        raise ValueError(f"rows {stride[0]} elements apart, {ld or width} in the configuration")
     return t.data_ptr()
 
 

@@ -8,23 +8,25 @@
 // nearest quarter turn comes off in integers, what is left (an eighth of a turn at most) goes to
 // fp32 and sincospif. In fp32 the product alone would be off by 0.03 radians at position 10^6.
 //
-// Memory bound: every element is read and written once, cos and sin are formed once per token and
-// pair and shared by all heads through shared memory. An item is two pieces of up to 16 bytes: the
-// two halves of lane-wise pairs, or two neighbouring pieces. The piece is the widest power of two
-// that divides what is rotated, its place, the head, the row lengths and the addresses.
+// Memory bound: every element is read and written once. A thread has one place in the heads (two
+// pieces of up to 16 bytes: the two halves of lane-wise pairs, or two neighbouring pieces) of one token
+// and turns it in up to four heads. The block forms its tokens' cosines and sines once, in shared
+// memory, while all loads of the heads are in flight. The piece is the widest power of two that divides
+// what is rotated, its place, the head, the row lengths and the addresses.
 #include "step.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // of a block
+constexpr int kThreads = 256;  // of a block, at most
+constexpr int kHeads = 4;      // of a thread, at most
 
 struct RopeParams {
   int T, Hq, Hk, Hv, D, rot, first;
   int slots;
-  int tokens;           // of a block
-  int items_qk, items_v;  // of a head
+  int items_qk, items_v;      // places of a head
+  int groups_qk, groups_v;    // heads are dealt out to this many threads of a place
+  int tokens, chunk;          // of a block: tokens, and how many of a token's threads
   float magnitude, sign;
   const void *q, *k, *v;
   void *qo, *ko, *vo;
@@ -44,154 +46,136 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& d, float v) { d = v; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 
-// cos and sin of pos * f, both times m.
+// cos and sin of pos * f, both times m. The upper half of pos * f modulo a turn is enough (2^-32 turns);
+// the quarter turns come off, and up to an eighth of a turn, x = pi / 4 radians, is left: the sine's
+// Taylor series to x^9 leaves 1.8e-9 there, the cosine's to x^10 1.2e-10.
 __device__ __forceinline__ float2 turn(int32_t pos, uint64_t f, float m, float sign) {
-  const uint64_t phase = (uint64_t)(int64_t)pos * f;
-  const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
-  const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));  // |rest| <= 2^61: an eighth of a turn
-  float s, c;
-  sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
+  const uint32_t n = pos < 0 ? 0u - (uint32_t)pos : (uint32_t)pos;
+  if (pos < 0) sign = -sign;
+  const uint32_t phase = __umulhi(n, (uint32_t)f) + n * (uint32_t)(f >> 32);
+  const uint32_t quarter = (phase + (1u << 29)) >> 30;
+  const int32_t rest = (int32_t)(phase - (quarter << 30));  // |rest| <= 2^29
+  const float x = __int2float_rn(rest) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = x * x;
+  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+  s = fmaf(z, s, 8.3333333e-3f);
+  s = fmaf(z, s, -1.6666667e-1f);
+  s = fmaf(x * z, s, x);
+  float c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+  c = fmaf(z, c, -1.3888889e-3f);
+  c = fmaf(z, c, 4.1666667e-2f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.0f);
   const float cs = quarter & 1 ? s : c, sn = quarter & 1 ? c : s;
-  return make_float2(m * (quarter == 1 || quarter == 2 ? -cs : cs), sign * m * (quarter >= 2 ? -sn : sn));
+  const int q = quarter & 3;
+  return make_float2(m * (q == 1 || q == 2 ? -cs : cs), sign * m * (q >= 2 ? -sn : sn));
 }
 
-template <typename T, int VEC, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+// Two neighbouring elements as fp32, and back with one rounding each.
+__device__ __forceinline__ float2 load2(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* v) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(v));
+}
+__device__ __forceinline__ void store2(float* v, float a, float b) { v[0] = a, v[1] = b; }
+__device__ __forceinline__ void store2(__nv_bfloat16* v, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(v) = __floats2bfloat162_rn(a, b);
+}
+
+template <typename T, int VEC, bool INTERLEAVED, int HEADS>
+__global__ void __launch_bounds__(kThreads, HEADS == 1 ? 4 : 3) rope_kernel(const RopeParams p) {
   using P = Piece<T, VEC>;
-  extern __shared__ float2 sTurn[];  // [tokens][rot / 2]
-  __shared__ int sRow[kMaxTokens];   // the row of k_out and v_out, or -1
+  constexpr bool kInside = INTERLEAVED && VEC > 1;  // pairs lie inside a piece
+  extern __shared__ float2 sTurn[];                 // [tokens][rot / 2]
   const int half = p.rot / 2;
-  const int t0 = blockIdx.x * p.tokens, tokens = min(p.tokens, p.T - t0);
-  for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-    const int t = i / half;
-    sTurn[i] = turn(__ldg(p.pos + t0 + t), __ldg(p.table + (i - t * half)), p.magnitude, p.sign);
+  const int per_qk = p.groups_qk * p.items_qk, per_token = per_qk + p.groups_v * p.items_v;
+  const int mine = (int)threadIdx.x / p.chunk;      // the thread's token of the block
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens, t = t0 + mine;
+  int r = blockIdx.y * p.chunk + (int)threadIdx.x - mine * p.chunk;
+  const bool active = mine < p.tokens && t < p.T && r < per_token;
+  const bool value = r >= per_qk;
+  if (value) r -= per_qk;
+  const int items = value ? p.items_v : p.items_qk, step = value ? p.groups_v : p.groups_qk;
+  const int group = r / items, piece = r - group * items;
+  const int heads = !active ? 0 : value ? p.Hv : p.Hq + p.Hk;  // none: loads and stores nothing
+
+  // the two pieces' first channels (b < 0: none), and the first pair of table (-1: copied)
+  int a, b, pair = -1;
+  const int nrot = kInside ? (p.rot / VEC + 1) / 2 : half / VEC;
+  if (value) {
+    a = piece * 2 * VEC;
+    b = a + VEC < p.D ? a + VEC : -1;
+  } else if (piece < nrot) {
+    pair = piece * VEC;
+    a = p.first + (kInside ? piece * 2 * VEC : INTERLEAVED ? 2 * piece : piece * VEC);
+    b = kInside ? (a + VEC < p.first + p.rot ? a + VEC : -1) : INTERLEAVED ? a + 1 : a + half;
+  } else {
+    // the channels that stay, those behind the rotated ones counted on from those before
+    const int c = (piece - nrot) * 2 * VEC, c2 = c + VEC;
+    a = c < p.first ? c : c + p.rot;
+    b = c2 < p.D - p.rot ? (c2 < p.first ? c2 : c2 + p.rot) : -1;
   }
-  if ((int)threadIdx.x < tokens) {
-    int row = t0 + threadIdx.x;
-    if (p.slot) {
-      row = __ldg(p.slot + row);
-      if (row >= p.slots) {
-        if (blockIdx.y == 0) set_status(p.status, MOE_ERR_DEVICE_BAD_INPUT, t0 + threadIdx.x);
-        row = -1;
-      }
+  int64_t row = t;  // of k_out and v_out
+  if (p.slot && active) {
+    row = __ldg(p.slot + t);
+    if (row >= p.slots) {
+      if (r == 0) set_status(p.status, MOE_ERR_DEVICE_BAD_INPUT, (int32_t)t);
+      row = -1;
     }
-    sRow[threadIdx.x] = row;
+  }
+
+  P x[HEADS], y[HEADS];
+#pragma unroll
+  for (int j = 0; j < HEADS; ++j) {
+    const int h = group + j * step;
+    if (h < heads) {
+      const T* src = value ? static_cast<const T*>(p.v) + t * p.ld_v + (int64_t)h * p.D
+                     : h < p.Hq ? static_cast<const T*>(p.q) + t * p.ld_q + (int64_t)h * p.D
+                                : static_cast<const T*>(p.k) + t * p.ld_k + (int64_t)(h - p.Hq) * p.D;
+      x[j] = *reinterpret_cast<const P*>(src + a);
+      if (b >= 0) y[j] = *reinterpret_cast<const P*>(src + b);
+    }
+  }
+  for (int i = threadIdx.x; i < p.tokens * half; i += blockDim.x) {
+    const int u = i / half;
+    if (t0 + u < p.T) sTurn[i] = turn(__ldg(p.pos + t0 + u), __ldg(p.table + (i - u * half)), p.magnitude, p.sign);
   }
   __syncthreads();
-
-  const int n_qk = (p.Hq + p.Hk) * p.items_qk, per_token = n_qk + p.Hv * p.items_v;
-  const int total = tokens * per_token, step = kThreads * gridDim.y;
-  // the first piece that is not rotated, and where the pieces behind the rotated ones begin
-  const int nrot = INTERLEAVED && VEC > 1 ? (p.rot / VEC + 1) / 2 : half / VEC;
-
-  struct Item {
-    const T *a, *b;
-    T *oa, *ob;       // NULL: no such piece
-    const float2* cs;  // NULL: copied
-  };
-  auto locate = [&](int idx) {
-    Item it{};
-    const int t = idx / per_token;
-    int r = idx - t * per_token;
-    const T* src;
-    T* dst;
-    int piece;
-    bool plain = false;
-    const int64_t row = t0 + t;
-    if (r < n_qk) {
-      const int h = r / p.items_qk;
-      piece = r - h * p.items_qk;
-      if (h < p.Hq) {
-        src = static_cast<const T*>(p.q) + row * p.ld_q + (int64_t)h * p.D;
-        dst = static_cast<T*>(p.qo) + row * p.ld_qo + (int64_t)h * p.D;
-      } else {
-        src = static_cast<const T*>(p.k) + row * p.ld_k + (int64_t)(h - p.Hq) * p.D;
-        dst = sRow[t] < 0 ? nullptr : static_cast<T*>(p.ko) + sRow[t] * p.ld_ko + (int64_t)(h - p.Hq) * p.D;
-      }
-    } else {
-      r -= n_qk;
-      const int h = r / p.items_v;
-      piece = r - h * p.items_v;
-      plain = true;
-      src = static_cast<const T*>(p.v) + row * p.ld_v + (int64_t)h * p.D;
-      dst = sRow[t] < 0 ? nullptr : static_cast<T*>(p.vo) + sRow[t] * p.ld_vo + (int64_t)h * p.D;
-    }
-    if (!dst) return it;
-    int a, b;  // first channels of the two pieces, b < 0: none
-    if (plain) {
-      a = piece * 2 * VEC;
-      b = a + VEC < p.D ? a + VEC : -1;
-    } else if (piece < nrot) {
-      it.cs = sTurn + t * half;
-      if constexpr (INTERLEAVED) {
-        a = p.first + piece * 2 * VEC;
-        b = a + VEC < p.first + p.rot ? a + VEC : -1;
-        it.cs += piece * VEC;
-      } else {
-        a = p.first + piece * VEC;
-        b = a + half;
-        it.cs += piece * VEC;
-      }
-    } else {
-      // the channels that stay, those behind the rotated ones counted on from those before
-      const int c = (piece - nrot) * 2 * VEC, left = p.D - p.rot;
-      a = c < p.first ? c : c + p.rot;
-      const int c2 = c + VEC;
-      b = c2 < left ? (c2 < p.first ? c2 : c2 + p.rot) : -1;
-    }
-    it.a = src + a;
-    it.oa = dst + a;
-    it.b = b < 0 ? nullptr : src + b;
-    it.ob = b < 0 ? nullptr : dst + b;
-    return it;
-  };
-  auto rotate = [&](const Item& it, P& a, P& b) {
-    if (!it.cs) return;
-    if constexpr (INTERLEAVED && VEC > 1) {
+  const float2* cs = sTurn + mine * half + pair;  // of the place's pairs
 #pragma unroll
-      for (int l = 0; l < VEC; l += 2) {
-        const float2 cs = it.cs[l / 2];
-        const float x = to_f(a.v[l]), y = to_f(a.v[l + 1]);
-        from_f(a.v[l], x * cs.x - y * cs.y);
-        from_f(a.v[l + 1], y * cs.x + x * cs.y);
-      }
-      if (it.b) {
+  for (int j = 0; j < HEADS; ++j) {
+    const int h = group + j * step;
+    if (h >= heads) continue;
+    T* dst;
+    if (!value && h < p.Hq) dst = static_cast<T*>(p.qo) + t * p.ld_qo + (int64_t)h * p.D;
+    else if (row < 0) continue;
+    else if (value) dst = static_cast<T*>(p.vo) + row * p.ld_vo + (int64_t)h * p.D;
+    else dst = static_cast<T*>(p.ko) + row * p.ld_ko + (int64_t)(h - p.Hq) * p.D;
+    if (pair >= 0) {
+      if constexpr (kInside) {
+        auto rotate = [](T* v, float2 c) {
+          const float2 u = load2(v);
+          store2(v, u.x * c.x - u.y * c.y, u.y * c.x + u.x * c.y);
+        };
+#pragma unroll
+        for (int l = 0; l < VEC / 2; ++l) {
+          rotate(x[j].v + 2 * l, cs[l]);
+          if (b >= 0) rotate(y[j].v + 2 * l, cs[VEC / 2 + l]);
+        }
+      } else if constexpr (VEC > 1) {
 #pragma unroll
         for (int l = 0; l < VEC; l += 2) {
-          const float2 cs = it.cs[VEC / 2 + l / 2];
-          const float x = to_f(b.v[l]), y = to_f(b.v[l + 1]);
-          from_f(b.v[l], x * cs.x - y * cs.y);
-          from_f(b.v[l + 1], y * cs.x + x * cs.y);
+          const float2 u = load2(x[j].v + l), w = load2(y[j].v + l), c = cs[l], d = cs[l + 1];
+          store2(x[j].v + l, u.x * c.x - w.x * c.y, u.y * d.x - w.y * d.y);
+          store2(y[j].v + l, w.x * c.x + u.x * c.y, w.y * d.x + u.y * d.y);
         }
-      }
-    } else {
-#pragma unroll
-      for (int l = 0; l < VEC; ++l) {
-        const float2 cs = it.cs[l];
-        const float x = to_f(a.v[l]), y = to_f(b.v[l]);
-        from_f(a.v[l], x * cs.x - y * cs.y);
-        from_f(b.v[l], y * cs.x + x * cs.y);
+      } else {
+        const float u = to_f(x[j].v[0]), w = to_f(y[j].v[0]);
+        from_f(x[j].v[0], u * cs->x - w * cs->y);
+        from_f(y[j].v[0], w * cs->x + u * cs->y);
       }
     }
-  };
-
-  constexpr int kAhead = 4;  // items whose loads are in flight at once
-  for (int base = blockIdx.y * kThreads + threadIdx.x; base < total; base += kAhead * step) {
-    Item it[kAhead];
-    P a[kAhead], b[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      it[j] = base + j * step < total ? locate(base + j * step) : Item{};
-      if (it[j].a) a[j] = *reinterpret_cast<const P*>(it[j].a);
-      if (it[j].b) b[j] = *reinterpret_cast<const P*>(it[j].b);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (!it[j].a) continue;
-      rotate(it[j], a[j], b[j]);
-      *reinterpret_cast<P*>(it[j].oa) = a[j];
-      if (it[j].b) *reinterpret_cast<P*>(it[j].ob) = b[j];
-    }
+    *reinterpret_cast<P*>(dst + a) = x[j];
+    if (b >= 0) *reinterpret_cast<P*>(dst + b) = y[j];
   }
 }
 
@@ -213,10 +197,23 @@ __global__ void rope_table_kernel(const moe_rope_freq_t c, uint64_t* table) {
   }
 }
 
+struct Launch {
+  dim3 grid;
+  unsigned threads;
+  size_t smem;
+  int heads;
+};
+
+template <typename T, int VEC, bool INTERLEAVED>
+void launch_heads(const RopeParams& p, const Launch& l, cudaStream_t s) {
+  if (l.heads == kHeads) rope_kernel<T, VEC, INTERLEAVED, kHeads><<<l.grid, l.threads, l.smem, s>>>(p);
+  else rope_kernel<T, VEC, INTERLEAVED, 1><<<l.grid, l.threads, l.smem, s>>>(p);
+}
+
 template <typename T, int VEC>
-void launch_vec(const RopeParams& p, int layout, dim3 grid, size_t smem, cudaStream_t s) {
-  if (layout == MOE_ROPE_INTERLEAVED) rope_kernel<T, VEC, true><<<grid, kThreads, smem, s>>>(p);
-  else rope_kernel<T, VEC, false><<<grid, kThreads, smem, s>>>(p);
+void launch_vec(const RopeParams& p, int layout, const Launch& l, cudaStream_t s) {
+  if (layout == MOE_ROPE_INTERLEAVED) launch_heads<T, VEC, true>(p, l, s);
+  else launch_heads<T, VEC, false>(p, l, s);
 }
 
 cudaError_t launch(RopeParams p, int layout, bool bf16, cudaStream_t s) {
@@ -237,26 +234,33 @@ cudaError_t launch(RopeParams p, int layout, bool bf16, cudaStream_t s) {
   const int nrot = wide ? (p.rot / vec + 1) / 2 : p.rot / 2 / vec;
   p.items_qk = nrot + ((p.D - p.rot) / vec + 1) / 2;
   p.items_v = (p.D / vec + 1) / 2;
-  const int64_t per_token = (int64_t)(p.Hq + p.Hk) * p.items_qk + (int64_t)p.Hv * p.items_v;
-  // a block has about four items a thread; where the tokens are few, several blocks share them
-  const int sms = tc::num_sms();
-  p.tokens = (int)max((int64_t)1, min((int64_t)kMaxTokens, ceil_div(4 * kThreads, per_token)));
-  while (p.tokens > 1 && ceil_div(p.T, p.tokens) < 2 * sms) --p.tokens;
-  while (p.tokens > 1 && (size_t)p.tokens * (p.rot / 2) * 8 > 40 * 1024) --p.tokens;
-  const int64_t blocks = ceil_div(p.T, p.tokens);
-  const int64_t most = ceil_div(per_token * p.tokens, kThreads);
-  const int64_t split = max((int64_t)1, min(most, min((int64_t)64, 2 * (int64_t)sms / blocks)));
-  const dim3 grid((unsigned)blocks, (unsigned)split);
-  const size_t smem = (size_t)p.tokens * (p.rot / 2) * sizeof(float2);
+  // several heads a thread, where that leaves every SM its threads
+  Launch l{};
+  int per_token = 0;
+  auto deal = [&](int heads) {
+    l.heads = heads;
+    p.groups_qk = (int)ceil_div(p.Hq + p.Hk, heads);
+    p.groups_v = (int)ceil_div(p.Hv, heads);
+    per_token = p.groups_qk * p.items_qk + p.groups_v * p.items_v;
+  };
+  deal(kHeads);
+  if ((int64_t)p.T * per_token < (int64_t)tc::num_sms() * 512) deal(1);
+  // whole tokens a block, or a part of one
+  p.chunk = min(per_token, kThreads);
+  p.tokens = max(1, min(kThreads / p.chunk, 40 * 1024 / max(1, p.rot / 2 * (int)sizeof(float2))));
+  l.grid = dim3((unsigned)ceil_div(p.T, p.tokens), (unsigned)ceil_div(per_token, p.chunk));
+  l.threads = (unsigned)((p.tokens * p.chunk + 31) / 32 * 32);
+  l.smem = (size_t)p.tokens * (p.rot / 2) * sizeof(float2);
+  if (l.grid.y > 65535) return cudaErrorInvalidConfiguration;
   if (bf16) {
-    if (vec == 8) launch_vec<__nv_bfloat16, 8>(p, layout, grid, smem, s);
-    else if (vec == 4) launch_vec<__nv_bfloat16, 4>(p, layout, grid, smem, s);
-    else if (vec == 2) launch_vec<__nv_bfloat16, 2>(p, layout, grid, smem, s);
-    else launch_vec<__nv_bfloat16, 1>(p, layout, grid, smem, s);
+    if (vec == 8) launch_vec<__nv_bfloat16, 8>(p, layout, l, s);
+    else if (vec == 4) launch_vec<__nv_bfloat16, 4>(p, layout, l, s);
+    else if (vec == 2) launch_vec<__nv_bfloat16, 2>(p, layout, l, s);
+    else launch_vec<__nv_bfloat16, 1>(p, layout, l, s);
   } else {
-    if (vec == 4) launch_vec<float, 4>(p, layout, grid, smem, s);
-    else if (vec == 2) launch_vec<float, 2>(p, layout, grid, smem, s);
-    else launch_vec<float, 1>(p, layout, grid, smem, s);
+    if (vec == 4) launch_vec<float, 4>(p, layout, l, s);
+    else if (vec == 2) launch_vec<float, 2>(p, layout, l, s);
+    else launch_vec<float, 1>(p, layout, l, s);
   }
   return cudaGetLastError();
 }

@@ -86,7 +86,7 @@ cudaError_t launch_head_loss_backward(const moe_head_config_t& c, const void* x,
                                       void* ws, DeviceStatus* st, cudaStream_t s);
 
 // ---- rotary positions
-constexpr int kRopeMaxD = 4096;  // a token's cosines and sines fit a block's shared memory
+constexpr int kRopeMaxD = 4096;  // a token's cosines and sines take 16 KB of a block's shared memory
 cudaError_t launch_rope_table(const moe_rope_freq_t& c, uint64_t* table, cudaStream_t s);
 cudaError_t launch_rope(const moe_rope_config_t& c, const void* q, const void* k, const void* v, const int32_t* pos,
                         const int32_t* slot, const uint64_t* table, void* q_out, void* k_out, void* v_out,

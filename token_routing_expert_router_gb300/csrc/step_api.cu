@@ -70,7 +70,7 @@ moe_status_t validate(const moe_rope_config_t* c) {
       !ld_ok(c->ld_q_out, c->Hq, c->D) || !ld_ok(c->ld_k_out, c->Hk, c->D) || !ld_ok(c->ld_v_out, c->Hk, c->D))
     return MOE_ERR_INVALID_ARG;
   if (c->T > (1 << 30) || c->D > kRopeMaxD || c->Hq > (1 << 14) || c->Hk > (1 << 14)) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
+  return (int64_t)(c->Hq > c->Hk ? c->Hq : c->Hk) * c->D > (1 << 22) ? MOE_ERR_UNSUPPORTED : MOE_OK;  // a grid's second axis
 }
 
 moe_status_t validate(const moe_attn_config_t* c) {
