@@ -1,5 +1,8 @@
 // The attention entry points' choice of variant, and their workspaces.
 #include "attn.cuh"
+#ifndef STREAM_BELOW
+#define STREAM_BELOW 76
+#endif
 
 namespace moe {
 
@@ -34,6 +37,14 @@ bool tc_rows(const AttnArgs& a, bool backward) {
   return at % 16 == 0;
 }
 
+// Tiles of 256 rows need one for every SM, and are half empty where no sequence has more than 128.
+bool stream_rule(const AttnArgs& a) {
+  int pack = 1;
+  while (pack < 128 && a.group % (2 * pack) == 0) pack *= 2;
+  if ((int64_t)a.max_q * pack <= 128) return true;
+  return (a.Tq / (256 / pack) + a.B) * (int64_t)(a.Hq / pack) < STREAM_BELOW;
+}
+
 }  // namespace attn
 
 AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward) {
@@ -42,6 +53,11 @@ AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward) {
   if (backward) {
     s.delta = at;
     at += align_up((size_t)c.Hq * c.Tq * sizeof(float), 256);
+  } else if (c.act_dtype == MOE_DTYPE_BF16 && c.D % 8 == 0) {
+    const size_t rows = (size_t)2 * attn::kMaxStreamCtas * 128;
+    s.stat = at;
+    s.part = s.stat + rows * sizeof(float2);
+    at = s.part + rows * (c.D <= 64 ? 64 : 128) * sizeof(float);
   }
   s.total = at;
   return s;
@@ -51,7 +67,13 @@ cudaError_t launch_attn(const moe_attn_config_t& c, const void* q, const void* k
                         void* o, float* lse, void* ws, DeviceStatus* st, cudaStream_t s) {
   if (c.Tq == 0 || c.B == 0) return cudaSuccess;
   const attn::AttnArgs a = args_of(c, q, k, v, at, o, lse, st);
-  if (c.act_dtype == MOE_DTYPE_BF16 && attn::tc_rows(a, false)) return attn::launch_tc(a, s);
+  if (c.act_dtype == MOE_DTYPE_BF16 && attn::tc_rows(a, false)) {
+    if (!attn::stream_rule(a)) return attn::launch_tc(a, s);
+    char* b = static_cast<char*>(ws);
+    const AttnScratch L = attn_scratch(c, false);
+    return attn::launch_stream(a, {reinterpret_cast<uint32_t*>(b + kAttnTickets), reinterpret_cast<float2*>(b + L.stat),
+                                   reinterpret_cast<float*>(b + L.part)}, s);
+  }
   return attn::launch_simt(a, c.act_dtype == MOE_DTYPE_BF16, s);
 }
 

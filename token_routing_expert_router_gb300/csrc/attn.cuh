@@ -111,6 +111,16 @@ __device__ __forceinline__ int visible(const AttnArgs& a, const Seq& s, int i) {
 // ---- launchers of the variants
 bool tc_rows(const AttnArgs& a, bool backward);  // bf16 tensors' rows are multiples of 16 bytes
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s);
+// Few rows over many keys: one CTA an SM, each with two places for parts of lines.
+constexpr int kMaxStreamCtas = 160;
+inline int stream_ctas() { return tc::num_sms() < kMaxStreamCtas ? tc::num_sms() : kMaxStreamCtas; }
+struct StreamSpace {
+  uint32_t* tickets;  // in the workspace's head
+  float2* stat;
+  float* part;
+};
+bool stream_rule(const AttnArgs& a);
+cudaError_t launch_stream(const AttnArgs& a, const StreamSpace& w, cudaStream_t s);
 cudaError_t launch_simt(const AttnArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_tc_backward(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_simt_backward(const AttnArgs& a, bool bf16, cudaStream_t s);

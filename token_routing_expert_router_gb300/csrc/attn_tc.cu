@@ -20,18 +20,6 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int BK = 128;  // keys of a tile
-constexpr int kSmem = 227 * 1024;
-
-template <int DP>
-struct Fwd {
-  static constexpr int kSlabs = DP / 64;
-  static constexpr int kTile = 128 * DP * 2;                     // bytes of a tile of Q, K or V
-  static constexpr int kUnits = (kSmem - 2048 - 2 * kTile) / kTile < 8 ? (kSmem - 2048 - 2 * kTile) / kTile : 8;
-  static constexpr size_t kBytes = 1024 + (2 + kUnits) * kTile + 256;
-};
-
 struct FwdParams {
   AttnArgs a;
   int pack;     // query heads in a tile
@@ -215,70 +203,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t my_s = tS + 128 * m + lanes, my_o = tO + DP * m + lanes;
     const int seen = visible(a, s, i);                               // of this row
     const int least = visible(a, s, i0 + m * per);                   // of the tile's first row
-    float top = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;
-    const float slack = 8.0f / p.c;
+    Running w;
     bool ok = true;
     for (int j = n - 1; j >= 0; --j) {
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[m], (n - 1 - j) & 1, abort, kTimeoutNs, a.status)))) break;
       tc_fence_after();
-      uint32_t r[4][32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(my_s + 32 * q, r[q]);
-      tmem_ld_wait();
-      if ((j + 1) * BK > least) {
-        const int end = seen - j * BK;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int l = 0; l < 32; ++l)
-            if (32 * q + l >= end) r[q][l] = 0xff800000u;
-      }
-      float mx[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        mx[q] = __uint_as_float(r[q][0]);
-#pragma unroll
-        for (int l = 1; l < 32; ++l) mx[q] = fmaxf(mx[q], __uint_as_float(r[q][l]));
-      }
-      const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool grow = most > top + slack;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? ex2((top - most) * p.c) : 1.0f;  // 0 for the row's first key
-        if (grow) top = most;
-        sum0 *= f, sum1 *= f;
-        if (j < n - 1) {  // O holds the products up to the last tile: these scores were issued behind them
-#pragma unroll
-          for (int q = 0; q < DP / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(my_o + 32 * q, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int l = 0; l < 32; ++l) o[l] = __float_as_uint(__uint_as_float(o[l]) * f);
-            tmem_st32(my_o + 32 * q, o);
-          }
-        }
-      }
-      const float base = top == -INFINITY ? 0.0f : -top * p.c;  // no key yet: exp2(-inf) = 0
-#pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        uint32_t w[32];
-#pragma unroll
-        for (int l = 0; l < 64; l += 2) {
-          float x = __uint_as_float(r[q + l / 32][l % 32]), y = __uint_as_float(r[q + l / 32][l % 32 + 1]);
-          scale2(x, y, p.c, base);
-          x = ex2(x), y = ex2(y);
-          add2(sum0, sum1, x, y);
-          w[l / 2] = pack2(x, y);
-        }
-        tmem_st32(my_s + 16 * q, w);
-      }
-      tmem_st_wait();
+      softmax_step<DP>(my_s, my_o, p.c, (j + 1) * BK > least ? seen - j * BK : BK, j < n - 1, w);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[m]);
     }
     // ===================== O / sum and the log sum
-    const float sum = sum0 + sum1;
+    const float sum = w.sum0 + w.sum1, top = w.top;
     if (n > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&o_full[m], 0, abort, kTimeoutNs, a.status));
     tc_fence_after();
     const bool live = ok && i < s.n;

@@ -59,6 +59,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // MN-major operand: blocks of 64 MN elements, block_bytes apart, each with K rows of 128 bytes
@@ -115,6 +126,82 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int slabs, int rows, i
       *reinterpret_cast<uint4*>(tile + s * rows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// ---- forward: 128 keys a tile; K and V tiles share a ring of `kUnits` tiles
+constexpr int kThreads = 384;
+constexpr int BK = 128;
+constexpr int kSmem = 227 * 1024;
+
+template <int DP>
+struct Fwd {
+  static constexpr int kSlabs = DP / 64;
+  static constexpr int kTile = 128 * DP * 2;  // bytes of a tile of Q, K or V
+  static constexpr int kUnits = (kSmem - 2048 - 2 * kTile) / kTile < 8 ? (kSmem - 2048 - 2 * kTile) / kTile : 8;
+  static constexpr size_t kBytes = 1024 + (2 + kUnits) * kTile + 512;
+};
+
+// A row's softmax so far: sums of exp2(c (s - top)), even and odd columns.
+struct Running {
+  float top = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;
+};
+
+// One tile of scores at my_s (this thread's lane) becomes P; columns from `end` on are not seen (the
+// whole warp gives BK where every row sees every column). O at my_o is scaled, where it holds anything
+// (`begun`) and a row's maximum has grown by more than 2^8.
+template <int DP>
+__device__ __forceinline__ void softmax_step(uint32_t my_s, uint32_t my_o, float c, int end, bool begun, Running& w) {
+  uint32_t r[4][32];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) tmem_ld32(my_s + 32 * q, r[q]);
+  tmem_ld_wait();
+  if (__any_sync(0xffffffffu, end < BK)) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int l = 0; l < 32; ++l)
+        if (32 * q + l >= end) r[q][l] = 0xff800000u;
+  }
+  float mx[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    mx[q] = __uint_as_float(r[q][0]);
+#pragma unroll
+    for (int l = 1; l < 32; ++l) mx[q] = fmaxf(mx[q], __uint_as_float(r[q][l]));
+  }
+  const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  const bool grow = most > w.top + 8.0f / c;
+  if (__any_sync(0xffffffffu, grow)) {
+    const float f = grow ? ex2((w.top - most) * c) : 1.0f;  // 0 for the row's first key
+    if (grow) w.top = most;
+    w.sum0 *= f, w.sum1 *= f;
+    if (begun) {  // the products up to the last tile are in O: these scores were issued behind them
+#pragma unroll 1
+      for (int col = 0; col < DP; col += 8) {  // few at a time: the scores are in registers
+        uint32_t o[8];
+        tmem_ld8(my_o + col, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int l = 0; l < 8; ++l) o[l] = __float_as_uint(__uint_as_float(o[l]) * f);
+        tmem_st8(my_o + col, o);
+      }
+    }
+  }
+  const float base = w.top == -INFINITY ? 0.0f : -w.top * c;  // no key yet: exp2(-inf) = 0
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t v[16];
+#pragma unroll
+    for (int l = 0; l < 32; l += 2) {
+      float x = __uint_as_float(r[q][l]), y = __uint_as_float(r[q][l + 1]);
+      scale2(x, y, c, base);
+      x = ex2(x), y = ex2(y);
+      add2(w.sum0, w.sum1, x, y);
+      v[l / 2] = pack2(x, y);
+    }
+    tmem_st16(my_s + 16 * q, v);
+  }
+  tmem_st_wait();
 }
 
 // Query heads of a group that are packed into a tile's rows: row r is query r / pack, head r % pack.

@@ -19,7 +19,6 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int R = 128;  // rows of every tile
 
 template <int DP>

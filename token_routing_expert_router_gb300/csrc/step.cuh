@@ -15,6 +15,7 @@ int num_sms();  // of the current device (gemm_tc.cu)
 // each returns to what the next call expects, whatever call shared the workspace before.
 constexpr size_t kClipState = 1024;   // grad_clip.cu's ticket and scale
 constexpr size_t kHeadTicket = 1152;  // head_loss.cu's ticket
+constexpr size_t kAttnTickets = 2048; // attn_stream.cu's tickets, one for every CTA
 
 // Programmatic dependent launch inside a call: a kernel launched with launch_after may be set
 // up while the one before it in the stream still runs, and calls after_previous() before it
@@ -100,7 +101,9 @@ struct AttnSeqs {  // where the sequences' rows are: k_start and k_len NULL: key
   const int32_t *q_start, *k_start, *k_len;
 };
 struct AttnScratch {  // workspace offsets, after the status head
-  size_t delta, total;
+  size_t delta;        // backward
+  size_t stat, part;   // forward, few rows over many keys
+  size_t total;
 };
 AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward);
 cudaError_t launch_attn(const moe_attn_config_t& c, const void* q, const void* k, const void* v, const AttnSeqs& at,
