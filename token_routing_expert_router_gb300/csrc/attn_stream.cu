@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t tS = tmem, tO = tmem + 256;
 
   if (warp < 4) {
@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_s = idesc_make(1, 128, BK);
       const uint32_t idesc_o = idesc_make(1, 128, DP) | (1u << 16);  // V is read MN-major
       int unit = 0;
+      const bool one = lane == 0;
       uint32_t phase = 0, tile_phase = 0, turn = 0;  // tile_phase: a bit for each warpgroup; turn: whose tile is next
       auto all = [&](bool ok) { return (bool)__all_sync(0xffffffffu, ok); };
       auto wait = [&](uint64_t* bar, uint32_t parity) { return all(mbar_wait(bar, parity, abort, kTimeoutNs, a.status)); };
@@ -282,18 +283,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // S_m = Q K^T of the unit; the last scores of a part give its Q back
       auto scores = [&](int m, int q, int u, bool final) {
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t qa = smem_addr(sQ + q * F::kTile), ka = smem_addr(sKV + u * F::kTile);
+        const uint32_t qa = uniform(k_desc(smem_addr(sQ + q * F::kTile))), ka = uniform(k_desc(smem_addr(sKV + u * F::kTile)));
+        const uint32_t d = uniform(tS + 128 * m);
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-            mma_bf16(tS + 128 * m, desc_k_sw128(qa + off), desc_k_sw128(ka + off), idesc_s, k > 0);
-          }
-          mma_commit(&s_full[m]);
-          mma_commit(&empty[u]);
-          if (final) mma_commit(&q_empty[q]);
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t off = (k / 4) * (16384 / 16) + (k % 4) * 2;
+          mma_ss(d, qa + off, ka + off, idesc_s, k > 0, one);
         }
-        __syncwarp();
+        commit(&s_full[m], one);
+        commit(&empty[u], one);
+        if (final) commit(&q_empty[q], one);
       };
       uint32_t q_phase = 0, free_phase = 1;  // q_phase: of the two buffers of Q, a bit each
       int filled = 0;        // parts with keys so far: their Q lies in buffer filled & 1
@@ -345,17 +344,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             free_phase ^= 1;
           }
           tc_fence_after();
-          if (lane == 0) {  // O_m += P_m V
-            const uint32_t va = smem_addr(sKV + uv * F::kTile);
+          const uint32_t va = uniform(mn_desc(smem_addr(sKV + uv * F::kTile))), d = uniform(tO + DP * m), w = uniform(tS + 128 * m);
 #pragma unroll
-            for (int i = 0; i < BK / 16; ++i)
-              mma_bf16_ta(tO + DP * m, tS + 128 * m + 8 * i, desc_mn_sw128(va + 2048 * i, 16384), idesc_o, j < hi - 2 || i > 0);
-            mma_commit(&empty[uv]);
-            if (j == lo) mma_commit(o_full);
-          }
-          __syncwarp();
+          for (int i = 0; i < BK / 16; ++i)  // O_m += P_m V
+            mma_ts(d, w + 8 * i, va + (2048 / 16) * i, idesc_o, j < hi - 2 || i > 0, one);
+          commit(&empty[uv], one);
+          if (j == lo) commit(o_full, one);
         }
       }
+      __syncwarp();
       if (lane == 0) {
         mma_commit(drain);
         mbar_wait_drain(drain, 0, kTimeoutNs, a.status);

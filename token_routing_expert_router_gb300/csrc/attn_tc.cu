@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t tS = tmem, tO = tmem + 256;  // S and P of tile m at 128 m, O at DP m
 
   if (warp < 4) {
@@ -132,14 +132,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         u = unit;
         if (++unit == kUnits) unit = 0, phase ^= 1;
       };
+      const bool one = lane == 0;
       auto scores = [&](int m, int u) {  // S_m = Q_m K^T
-        const uint32_t qa = smem_addr(sQ + m * F::kTile), ka = smem_addr(sKV + u * F::kTile);
+        const uint32_t qa = uniform(k_desc(smem_addr(sQ + m * F::kTile))), ka = uniform(k_desc(smem_addr(sKV + u * F::kTile)));
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-          mma_bf16(tS + 128 * m, desc_k_sw128(qa + off), desc_k_sw128(ka + off), idesc_s, k > 0);
+          const uint32_t off = (k / 4) * (16384 / 16) + (k % 4) * 2;
+          mma_ss(tS + 128 * m, qa + off, ka + off, idesc_s, k > 0, one);
         }
-        mma_commit(&s_full[m]);
+        commit(&s_full[m], one);
       };
       bool ok = mbar_wait(q_full, 0, abort, kTimeoutNs, a.status);
       ok = __all_sync(0xffffffffu, ok) && wait_unit();
@@ -147,11 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         int uk, uv;
         next(uk);
-        if (lane == 0) {
-          for (int m = 0; m < 2; ++m)
-            if (tiles_of(m) == steps) scores(m, uk);
-          mma_commit(&empty[uk]);
-        }
+        for (int m = 0; m < 2; ++m)
+          if (tiles_of(m) == steps) scores(m, uk);
+        commit(&empty[uk], one);
         for (int j = steps - 1; j >= 0; --j) {
           if (j > 0) {
             if (!(ok = wait_unit())) break;
@@ -168,25 +167,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc_fence_after();
-              if (lane == 0) {  // O_m += P_m V
-                const uint32_t va = smem_addr(sKV + uv * F::kTile);
+              const uint32_t va = uniform(mn_desc(smem_addr(sKV + uv * F::kTile)));
 #pragma unroll
-                for (int k = 0; k < BK / 16; ++k)
-                  mma_bf16_ta(tO + DP * m, tS + 128 * m + 8 * k, desc_mn_sw128(va + 2048 * k, 16384), idesc_o,
-                              j < n - 1 || k > 0);
-                if (j == 0) mma_commit(&o_full[m]);
-              }
+              for (int k = 0; k < BK / 16; ++k)  // O_m += P_m V
+                mma_ts(tO + DP * m, tS + 128 * m + 8 * k, va + (2048 / 16) * k, idesc_o, j < n - 1 || k > 0, one);
+              if (j == 0) commit(&o_full[m], one);
             }
-            if (lane == 0 && j > 0 && j - 1 < n) scores(m, uk);
+            if (j > 0 && j - 1 < n) scores(m, uk);
           }
           if (!ok) break;
-          if (lane == 0) {
-            mma_commit(&empty[uv]);
-            if (j > 0) mma_commit(&empty[uk]);
-          }
-          __syncwarp();
+          commit(&empty[uv], one);
+          if (j > 0) commit(&empty[uk], one);
         }
       }
+      __syncwarp();
       if (lane == 0) {
         mma_commit(drain);
         mbar_wait_drain(drain, 0, kTimeoutNs, a.status);

@@ -28,14 +28,54 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* m, void* dst, uin
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] B[smem]: A is 128 lanes of K elements, two bf16 to a column.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// ---- products. A thread's worth of them, but the whole warp comes here and `one` says which lane issues:
+// in a branch of a single lane every operand would be moved to a uniform register before every
+// instruction, 140 cycles a product of 128 x 128 x 16 where the tensor core takes 64. Descriptors are
+// given by their lower word (the address, to which a step adds) and their upper one (the layout).
+constexpr uint32_t kRowsDesc = (1024u >> 4) | (1u << 14) | (2u << 29);  // upper word: 128-byte swizzle, 8 rows 1024 bytes apart
+
+// One value of the warp, for the compiler to see.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Lower word of a K-major operand: a slab of 64 K elements, rows of 128 bytes; 16 K elements are 32 bytes.
+__device__ __forceinline__ uint32_t k_desc(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+// Of an MN-major one: blocks of 64 MN elements 16384 bytes apart, rows (K) of 128 bytes; 16 rows are 2048.
+__device__ __forceinline__ uint32_t mn_desc(uint32_t saddr) { return (saddr >> 4) | ((16384u >> 4) << 16); }
+
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_desc, uint32_t b_desc, uint32_t idesc, bool accumulate,
+                                       bool one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %4};\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_desc), "r"(b_desc), "r"(idesc), "r"(kRowsDesc), "r"((uint32_t)accumulate), "r"((uint32_t)one)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] B[smem]: A is 128 lanes of K elements, two bf16 to a column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_desc, uint32_t idesc, bool accumulate,
+                                       bool one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_desc), "r"(idesc), "r"(kRowsDesc), "r"((uint32_t)accumulate), "r"((uint32_t)one)
+      : "memory");
+}
+
+// The barrier gets an arrival when everything issued before has completed.
+__device__ __forceinline__ void commit(uint64_t* bar, bool one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"((uint32_t)one)
       : "memory");
 }
 
@@ -71,17 +111,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// MN-major operand: blocks of 64 MN elements, block_bytes apart, each with K rows of 128 bytes
-// (128-byte swizzle); a step of 16 K rows is 2048 bytes.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(block_bytes >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
 
 // 2^x (the PTX instruction, relative error 2^-22).
 __device__ __forceinline__ float ex2(float x) {

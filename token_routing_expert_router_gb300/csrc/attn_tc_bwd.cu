@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t tS = tmem, tP = tmem + 128, tA1 = tmem + 256, tA2 = tmem + 256 + DP;  // S, dP, dK or dQ, dV
 
   if (warp < 4) {
@@ -172,22 +172,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_s = idesc_make(1, R, R);
       const uint32_t idesc_a = idesc_make(1, R, DP) | (1u << 16);  // the inner tile is read MN-major
       auto all = [&](bool ok) { return (bool)__all_sync(0xffffffffu, ok); };
+      const bool one = lane == 0;
       // S or dP = X Y^T
       auto scores = [&](uint32_t d, const uint8_t* x, const uint8_t* y, uint64_t* bar) {
-        const uint32_t xa = smem_addr(x), ya = smem_addr(y);
+        const uint32_t xa = uniform(k_desc(smem_addr(x))), ya = uniform(k_desc(smem_addr(y)));
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-          mma_bf16(d, desc_k_sw128(xa + off), desc_k_sw128(ya + off), idesc_s, k > 0);
+          const uint32_t off = (k / 4) * (16384 / 16) + (k % 4) * 2;
+          mma_ss(d, xa + off, ya + off, idesc_s, k > 0, one);
         }
-        mma_commit(bar);
+        commit(bar, one);
       };
       // acc += W Y, W in tensor memory: the columns' halves each at the start of their half of the scores
       auto products = [&](uint32_t d, uint32_t w, const uint8_t* y, bool begin) {
-        const uint32_t ya = smem_addr(y);
+        const uint32_t ya = uniform(mn_desc(smem_addr(y)));
 #pragma unroll
         for (int k = 0; k < R / 16; ++k)
-          mma_bf16_ta(d, w + (k / 4) * 64 + (k % 4) * 8, desc_mn_sw128(ya + 2048 * k, 16384), idesc_a, !begin || k > 0);
+          mma_ts(d, w + (k / 4) * 64 + (k % 4) * 8, ya + (2048 / 16) * k, idesc_a, !begin || k > 0, one);
       };
       // inner tile i's Y1 (Y2) has come; rows that are not the sequence's are zeroed
       auto arrived = [&](uint64_t* bar, uint8_t* y, int i) {
@@ -198,38 +199,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = all(mbar_wait(x_full, 0, abort, kTimeoutNs, a.status)) && arrived(y1_full, sY1, 0);
-      if (ok && lane == 0) scores(tS, sX, sY1, s_full);
-      __syncwarp();
+      if (ok) scores(tS, sX, sY1, s_full);
       ok = ok && arrived(y2_full, sY2, 0);
-      if (ok && lane == 0) scores(tP, sX + F::kTile, sY2, dp_full);
-      __syncwarp();
+      if (ok) scores(tP, sX + F::kTile, sY2, dp_full);
       for (int i = 0; i < steps && ok; ++i) {
         const int b = i & 1;
         if (!(ok = all(mbar_wait(p_ready, b, abort, kTimeoutNs, a.status)))) break;
         tc_fence_after();
-        if (lane == 0) {
-          if constexpr (DKV) products(tA2, tS, sY2 + b * F::kTile, i == 0);
-          mma_commit(&y2_empty[b]);
-        }
-        __syncwarp();
+        if constexpr (DKV) products(tA2, tS, sY2 + b * F::kTile, i == 0);
+        commit(&y2_empty[b], one);
         if (i + 1 < steps) {
           if (!(ok = arrived(y1_full, sY1, i + 1))) break;
-          if (lane == 0) scores(tS, sX, sY1 + (b ^ 1) * F::kTile, s_full);
-          __syncwarp();
+          scores(tS, sX, sY1 + (b ^ 1) * F::kTile, s_full);
         }
         if (!(ok = all(mbar_wait(ds_ready, b, abort, kTimeoutNs, a.status)))) break;
         tc_fence_after();
-        if (lane == 0) {
-          products(tA1, tP, sY1 + b * F::kTile, i == 0);
-          mma_commit(&y1_empty[b]);
-        }
-        __syncwarp();
+        products(tA1, tP, sY1 + b * F::kTile, i == 0);
+        commit(&y1_empty[b], one);
         if (i + 1 < steps) {
           if (!(ok = arrived(y2_full, sY2, i + 1))) break;
-          if (lane == 0) scores(tP, sX + F::kTile, sY2 + (b ^ 1) * F::kTile, dp_full);
-          __syncwarp();
+          scores(tP, sX + F::kTile, sY2 + (b ^ 1) * F::kTile, dp_full);
         }
       }
+      __syncwarp();
       if (lane == 0) {
         if (ok) mma_commit(acc_full);
         mma_commit(drain);
