@@ -1,5 +1,5 @@
 // The attention entry points' choice of variant, and their workspaces.
-#include "attn.cuh"
+#include "attn_plan.cuh"
 #ifndef STREAM_BELOW
 #define STREAM_BELOW 76
 #endif
@@ -48,16 +48,26 @@ bool stream_rule(const AttnArgs& a) {
 }  // namespace attn
 
 AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward) {
+  const attn::AttnArgs a = args_of(c, nullptr, nullptr, nullptr, AttnSeqs{}, nullptr, nullptr, nullptr);
   AttnScratch s{};
   size_t at = kWsHead;
-  if (backward) {
-    s.delta = at;
-    at += align_up((size_t)c.Hq * c.Tq * sizeof(float), 256);
-  } else if (c.act_dtype == MOE_DTYPE_BF16 && c.D % 8 == 0) {
-    const size_t rows = (size_t)2 * attn::kMaxStreamCtas * 128;
-    s.stat = at;
-    s.part = s.stat + rows * sizeof(float2);
-    at = s.part + rows * (c.D <= 64 ? 64 : 128) * sizeof(float);
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, 256);
+    return here;
+  };
+  const bool tensor_cores = c.act_dtype == MOE_DTYPE_BF16 && c.D % 8 == 0;  // where rows are aligned
+  const size_t DP = c.D <= 64 ? 64 : 128, rows = (size_t)c.Hq * c.Tq;
+  if (!tensor_cores || backward) s.delta = s.neg_delta = take(backward ? rows * sizeof(float) : 0);
+  if (tensor_cores && backward) {
+    s.neg_lse = take(rows * sizeof(float));
+    s.dq_plan = take(attn::plan_bytes(attn::dq_tiles(a)));
+    s.dkv_plan = take(attn::plan_bytes(attn::dkv_tiles(a)));
+    s.part = take((size_t)attn::kMostPieces * 2 * 128 * DP * sizeof(float));
+  } else if (tensor_cores) {
+    s.plan = take(attn::plan_bytes(attn::forward_tiles(a)));
+    s.stat = take((size_t)2 * attn::kMaxStreamCtas * 128 * sizeof(float2));
+    s.part = take((size_t)2 * attn::kMaxStreamCtas * 128 * DP * sizeof(float));
   }
   s.total = at;
   return s;
@@ -67,14 +77,12 @@ cudaError_t launch_attn(const moe_attn_config_t& c, const void* q, const void* k
                         void* o, float* lse, void* ws, DeviceStatus* st, cudaStream_t s) {
   if (c.Tq == 0 || c.B == 0) return cudaSuccess;
   const attn::AttnArgs a = args_of(c, q, k, v, at, o, lse, st);
-  if (c.act_dtype == MOE_DTYPE_BF16 && attn::tc_rows(a, false)) {
-    if (!attn::stream_rule(a)) return attn::launch_tc(a, s);
-    char* b = static_cast<char*>(ws);
-    const AttnScratch L = attn_scratch(c, false);
-    return attn::launch_stream(a, {reinterpret_cast<uint32_t*>(b + kAttnTickets), reinterpret_cast<float2*>(b + L.stat),
-                                   reinterpret_cast<float*>(b + L.part)}, s);
-  }
-  return attn::launch_simt(a, c.act_dtype == MOE_DTYPE_BF16, s);
+  if (c.act_dtype != MOE_DTYPE_BF16 || !attn::tc_rows(a, false)) return attn::launch_simt(a, c.act_dtype == MOE_DTYPE_BF16, s);
+  char* b = static_cast<char*>(ws);
+  const AttnScratch L = attn_scratch(c, false);
+  if (!attn::stream_rule(a)) return attn::launch_tc(a, reinterpret_cast<attn::TilePlan*>(b + L.plan), s);
+  return attn::launch_stream(a, {reinterpret_cast<uint32_t*>(b + kAttnTickets), reinterpret_cast<float2*>(b + L.stat),
+                                 reinterpret_cast<float*>(b + L.part)}, s);
 }
 
 cudaError_t launch_attn_backward(const moe_attn_config_t& c, const void* q, const void* k, const void* v,
@@ -83,9 +91,14 @@ cudaError_t launch_attn_backward(const moe_attn_config_t& c, const void* q, cons
   if (c.B == 0 || (c.Tq == 0 && c.Tk == 0)) return cudaSuccess;
   attn::AttnArgs a = args_of(c, q, k, v, at, o, const_cast<float*>(lse), st);
   a.d_o = d_o, a.dq = dq, a.dk = dk, a.dv = dv;
-  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + attn_scratch(c, true).delta);
-  if (c.act_dtype == MOE_DTYPE_BF16 && attn::tc_rows(a, true)) return attn::launch_tc_backward(a, s);
-  return attn::launch_simt_backward(a, c.act_dtype == MOE_DTYPE_BF16, s);
+  char* b = static_cast<char*>(ws);
+  const AttnScratch L = attn_scratch(c, true);
+  a.delta = reinterpret_cast<float*>(b + L.delta);
+  if (c.act_dtype != MOE_DTYPE_BF16 || !attn::tc_rows(a, true)) return attn::launch_simt_backward(a, c.act_dtype == MOE_DTYPE_BF16, s);
+  auto floats = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
+  return attn::launch_tc_backward(a, {reinterpret_cast<attn::TilePlan*>(b + L.dq_plan), reinterpret_cast<attn::TilePlan*>(b + L.dkv_plan),
+                                      floats(L.neg_lse), floats(L.neg_delta), floats(L.part),
+                                      reinterpret_cast<uint32_t*>(b + kAttnTickets)}, s);
 }
 
 }  // namespace moe

@@ -63,11 +63,11 @@ struct Tile {
 // The block's tile `want` of all sequences' tiles of `rows` query rows (KEYS: key rows), one after
 // the other. Every thread calls it. Each thread takes the sequences of an equal share of B, the
 // block scans the shares' tiles, and the thread whose share holds the wanted one walks it. Up to
-// 256 sequences that is one load and two exchanges; it stands in for a plan kernel in front.
+// 256 sequences that is one load and two exchanges. scratch: THREADS / 32 + 3 words of shared memory.
 template <int THREADS, bool KEYS>
-__device__ Tile find_tile(const AttnArgs& a, int64_t want, int rows, bool apart, bool report) {
-  __shared__ int sWarp[THREADS / 32];
-  __shared__ Tile sTile;
+__device__ Tile find_tile(const AttnArgs& a, int64_t want, int rows, bool apart, bool report, int* scratch) {
+  int* sWarp = scratch;
+  volatile int* sTile = scratch + THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = (a.B + THREADS - 1) / THREADS;
   const int b0 = min(a.B, tid * share), b1 = min(a.B, b0 + share);
@@ -84,7 +84,7 @@ __device__ Tile find_tile(const AttnArgs& a, int64_t want, int rows, bool apart,
     if (lane >= off) inc += o;
   }
   if (lane == 31) sWarp[warp] = inc;
-  if (tid == 0) sTile = Tile{-1, 0, 0};
+  if (tid == 0) sTile[0] = -1;
   __syncthreads();
   int before = inc - mine;
   for (int w = 0; w < warp; ++w) before += sWarp[w];
@@ -93,14 +93,14 @@ __device__ Tile find_tile(const AttnArgs& a, int64_t want, int rows, bool apart,
     for (int b = b0; b < b1; ++b) {
       const int n = tiles(b, false);
       if (left < n) {
-        sTile = Tile{b, left, n};
+        sTile[0] = b, sTile[1] = left, sTile[2] = n;
         break;
       }
       left -= n;
     }
   }
   __syncthreads();
-  return sTile;
+  return Tile{sTile[0], sTile[1], sTile[2]};
 }
 
 // Keys that query row i of a sequence sees: [0, visible).
@@ -110,7 +110,8 @@ __device__ __forceinline__ int visible(const AttnArgs& a, const Seq& s, int i) {
 
 // ---- launchers of the variants
 bool tc_rows(const AttnArgs& a, bool backward);  // bf16 tensors' rows are multiples of 16 bytes
-cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s);
+struct TilePlan;  // attn_plan.cuh
+cudaError_t launch_tc(const AttnArgs& a, TilePlan* plan, cudaStream_t s);  // plan: room for the tiles' order
 // Few rows over many keys: one CTA an SM, each with two places for parts of lines.
 constexpr int kMaxStreamCtas = 160;
 inline int stream_ctas() { return tc::num_sms() < kMaxStreamCtas ? tc::num_sms() : kMaxStreamCtas; }
@@ -122,7 +123,20 @@ struct StreamSpace {
 bool stream_rule(const AttnArgs& a);
 cudaError_t launch_stream(const AttnArgs& a, const StreamSpace& w, cudaStream_t s);
 cudaError_t launch_simt(const AttnArgs& a, bool bf16, cudaStream_t s);
-cudaError_t launch_tc_backward(const AttnArgs& a, cudaStream_t s);
+// What the backward keeps in the workspace beside the statistics.
+struct BackwardSpace {
+  TilePlan *dq_plan, *dkv_plan;
+  float *neg_lse, *neg_delta;
+  float* part;        // [kMostPieces][2][128][DP]: dk and dv of pieces of a tile
+  uint32_t* tickets;  // [kMostPieces], zero between calls
+};
+constexpr int kPieces = 228;               // wanted of all tiles of dk and dv: 1.5 for every SM
+constexpr int kMostPieces = 2 * kPieces;   // of tiles that are cut
+cudaError_t launch_tc_backward(const AttnArgs& a, const BackwardSpace& w, cudaStream_t s);
+// Entries of the plans.
+int64_t forward_tiles(const AttnArgs& a);
+int64_t dq_tiles(const AttnArgs& a);
+int64_t dkv_tiles(const AttnArgs& a);
 cudaError_t launch_simt_backward(const AttnArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_delta(const AttnArgs& a, bool bf16, cudaStream_t s);
 

@@ -1,0 +1,195 @@
+// In front of the tensor-core attention kernels on a batch of several sequences: their tiles in the
+// order of their work, the longest first (the hardware deals CTAs out in that order, so the short ones
+// fill the gaps at the end), and for the backward the rows' statistics in the order its tiles read them.
+//
+// One block sorts: a prefix of the sequences' tiles, a histogram of their work over 64 classes, a
+// scatter. Tiles of equal class come in any order; no result depends on it. Long tiles of dk and dv
+// (which run over every query of a whole group of heads) are cut into pieces, so that no CTA has more
+// than its part of a round left when the others are done.
+#include "attn_plan.cuh"
+#include "attn_tc.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+constexpr int kSort = 1024;    // threads of the sorting block
+constexpr int kClasses = 64;
+
+// Steps (inner tiles) of a tile of queries, or of a tile of keys for all packs of heads.
+__device__ __forceinline__ int tile_steps(const AttnArgs& a, const PlanJob& j, const Seq& s, int tile) {
+  if (!j.keys) {
+    const int last = min((tile + 1) * j.rows, s.n) - 1;
+    return (max(0, visible(a, s, last)) + 127) / 128;
+  }
+  const int first = a.causal ? max(0, tile * 128 - (s.m - s.n)) / j.inner : 0;
+  return max(0, (s.n + j.inner - 1) / j.inner - first) * j.packs;
+}
+
+__device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool report) {
+  __shared__ int sFirst[kPlanMaxB + 1];  // tiles of the sequences before
+  __shared__ int sWarp[32];
+  __shared__ unsigned long long sTotal;
+  __shared__ int sMost, sSlots, sClass[kClasses];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rows = j.keys ? 128 : j.rows;
+  if (tid == 0) sTotal = 0, sMost = 0, sSlots = 0;
+  if (tid < kClasses) sClass[tid] = 0;
+  int carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kSort) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < a.B) {
+      const Seq s = load_seq(a, b, apart, report);
+      n = ((j.keys ? s.m : s.n) + rows - 1) / rows;
+    }
+    int inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    __syncthreads();
+    if (lane == 31) sWarp[warp] = inc;
+    __syncthreads();
+    int before = carry + inc - n, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += sWarp[w];
+      all += sWarp[w];
+    }
+    if (b < a.B) sFirst[b] = before;
+    carry += all;
+  }
+  if (tid == 0) sFirst[a.B] = carry;
+  __syncthreads();
+  const int tiles = min(carry, j.most);  // more only where sequences share rows, which is reported
+  auto seq_of = [&](int t) {
+    int lo = 0, hi = a.B - 1;  // the last sequence that begins at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sFirst[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
+  int64_t sum = 0;
+  int most = 0;
+  for (int t = tid; t < tiles; t += kSort) {
+    const int b = seq_of(t), n = tile_steps(a, j, load_seq(a, b, apart, false), t - sFirst[b]);
+    sum += n;
+    most = max(most, n);
+  }
+  atomicAdd(&sTotal, (unsigned long long)sum);
+  atomicMax(&sMost, most);
+  __syncthreads();
+  // a piece is at most a CTA's part of 1.5 rounds
+  int limit = 0x7fffffff;
+  if (j.pieces > 0) limit = max(8, (int)min((unsigned long long)0x7fffffff, (sTotal * j.heads + j.pieces - 1) / j.pieces));
+  const int top = max(1, min(sMost, limit));
+  auto cut = [&](int n) { return n > limit ? (n + limit - 1) / limit : 1; };
+  auto cls = [&](int n) { return kClasses - 1 - min(kClasses - 1, (int)((int64_t)n * (kClasses - 1) / top)); };  // 0: the longest
+  for (int t = tid; t < tiles; t += kSort) {
+    const int b = seq_of(t), n = tile_steps(a, j, load_seq(a, b, apart, false), t - sFirst[b]), p = cut(n);
+    atomicAdd(&sClass[cls((n + p - 1) / p)], p);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int at = 0;
+    for (int c = 0; c < kClasses; ++c) {
+      const int n = sClass[c];
+      sClass[c] = at;
+      at += n;
+    }
+    j.plan->count = at;
+  }
+  __syncthreads();
+  for (int t = tid; t < tiles; t += kSort) {
+    const int b = seq_of(t);
+    const Seq s = load_seq(a, b, apart, false);
+    const int n = tile_steps(a, j, s, t - sFirst[b]), p = cut(n);
+    const int at = atomicAdd(&sClass[cls((n + p - 1) / p)], p), slot = p > 1 ? atomicAdd(&sSlots, p) : 0;
+    for (int i = 0; i < p; ++i)
+      j.plan->tile[at + i] = TileEntry{s.q0, s.n, s.k0, s.m, (t - sFirst[b]) * rows, (int)((int64_t)n * i / p),
+                                       (int)((int64_t)n * (i + 1) / p), p > 1 ? (slot << 16 | i << 8 | p) : 0};
+  }
+}
+
+// The backward's statistics: -lse log2(e) and -d_o . o of every row and head, the heads of a pack side
+// by side, as its tiles' rows are. LANES lanes a row and head, 16 bytes of o and d_o each.
+template <int LANES>
+__device__ void row_stats(const AttnArgs& a, const StatsJob& j, int64_t block, int64_t blocks) {
+  constexpr int kPer = kSort / LANES;
+  const int lane = threadIdx.x % LANES;
+  const int64_t all = (int64_t)a.Tq * a.Hq;
+  const bool in = 8 * lane < a.D;
+  constexpr int kAhead = 4;
+  for (int64_t i0 = block * kPer * kAhead + threadIdx.x / LANES; i0 < all; i0 += blocks * kPer * kAhead) {
+    uint4 x[kAhead], y[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t i = i0 + u * kPer;
+      x[u] = y[u] = make_uint4(0, 0, 0, 0);
+      if (i < all && in) {
+        const int64_t row = (uint64_t)all < (1ull << 32) ? (uint32_t)i / (uint32_t)a.Hq : i / a.Hq;
+        const int64_t at = row * a.ld_o + (i - row * a.Hq) * a.D + 8 * lane;
+        x[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + at);
+        y[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_o) + at);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t i = i0 + u * kPer;
+      const __nv_bfloat162 *xs = reinterpret_cast<const __nv_bfloat162*>(&x[u]), *ys = reinterpret_cast<const __nv_bfloat162*>(&y[u]);
+      float dot = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 xf = __bfloat1622float2(xs[e]), yf = __bfloat1622float2(ys[e]);
+        dot = fmaf(xf.x, yf.x, fmaf(xf.y, yf.y, dot));
+      }
+#pragma unroll
+      for (int off = LANES / 2; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+      if (lane == 0 && i < all) {
+        const int64_t row = (uint64_t)all < (1ull << 32) ? (uint32_t)i / (uint32_t)a.Hq : i / a.Hq;
+        const int h = (int)(i - row * a.Hq);
+        const int64_t at = (h / j.pack * (int64_t)a.Tq + row) * j.pack + h % j.pack;
+        const float l = a.lse[(int64_t)h * a.Tq + row];
+        j.neg_lse[at] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row without keys: exp2(s - inf) = 0
+        j.neg_delta[at] = -dot;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kSort) plan_kernel(const AttnArgs a, const PlanJob j0, const PlanJob j1, const StatsJob st,
+                                                     int jobs, int apart) {
+  let_next_begin();
+  if ((int)blockIdx.x < jobs) {
+    if (blockIdx.x == 0) sort_tiles(a, j0, apart, true);
+    else sort_tiles(a, j1, apart, j0.keys == j1.keys);
+    return;
+  }
+  const int64_t block = blockIdx.x - jobs, blocks = gridDim.x - jobs;
+  if (a.D <= 64) row_stats<8>(a, st, block, blocks);
+  else row_stats<16>(a, st, block, blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const AttnArgs& a, const PlanJob& j, cudaStream_t s) {
+  plan_kernel<<<1, kSort, 0, s>>>(a, j, j, StatsJob{}, 1, 0);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_plan_backward(const AttnArgs& a, const PlanJob& dq, const PlanJob& dkv, const StatsJob& st, bool plan,
+                                 cudaStream_t s) {
+  const int64_t per = (int64_t)kSort / (a.D <= 64 ? 8 : 16) * 4;
+  const int jobs = plan ? 2 : 0;
+  const int64_t blocks = ceil_div((int64_t)a.Tq * a.Hq, per) < 2 * tc::num_sms() ? ceil_div((int64_t)a.Tq * a.Hq, per)
+                                                                                 : 2 * (int64_t)tc::num_sms();
+  if (jobs + blocks == 0) return cudaSuccess;
+  plan_kernel<<<(unsigned)(jobs + blocks), kSort, 0, s>>>(a, dq, dkv, st, jobs, 1);
+  return cudaGetLastError();
+}
+
+}  // namespace attn
+}  // namespace moe

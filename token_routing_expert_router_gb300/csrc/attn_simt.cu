@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a
   float* sV = sK + tile_floats<DP>();
   float* sP = sV + tile_floats<DP>();
   const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, false, blockIdx.x == 0 && h == 0);
+  __shared__ int sFind[kThreads / 32 + 3];
+  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, false, blockIdx.x == 0 && h == 0, sFind);
   if (t.b < 0) return;
   const Seq s = load_seq(a, t.b, false, false);
   const int i0 = (t.count - 1 - t.index) * R, rows = min(R, s.n - i0);  // the longest first
@@ -211,7 +212,8 @@ __global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
   float* sV = sK + tile_floats<DP>();
   float* sP = sV + tile_floats<DP>();
   const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, true, blockIdx.x == 0 && h == 0);
+  __shared__ int sFind[kThreads / 32 + 3];
+  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, true, blockIdx.x == 0 && h == 0, sFind);
   if (t.b < 0) return;
   const Seq s = load_seq(a, t.b, true, false);
   const int i0 = (t.count - 1 - t.index) * R, rows = min(R, s.n - i0);
@@ -263,7 +265,8 @@ __global__ void __launch_bounds__(kThreads) simt_dkv_kernel(const AttnArgs a) {
   float* sS = sP + R * PS;
   __shared__ RowStat sStat[R];
   const int hk = blockIdx.y, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const Tile t = find_tile<kThreads, true>(a, blockIdx.x, R, true, blockIdx.x == 0 && hk == 0);
+  __shared__ int sFind[kThreads / 32 + 3];
+  const Tile t = find_tile<kThreads, true>(a, blockIdx.x, R, true, blockIdx.x == 0 && hk == 0, sFind);
   if (t.b < 0) return;
   const Seq s = load_seq(a, t.b, true, false);
   const int j0 = t.index * R, rows = min(R, s.m - j0);

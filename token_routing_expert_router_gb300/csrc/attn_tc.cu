@@ -14,6 +14,7 @@
 // reference, since all sums are fp32 and P's rounding is relative. The keys are taken from the last to
 // the first, so that the tile with the mask comes first. Key rows behind the sequence's end belong to
 // somebody else: their scores are replaced, and their V rows are zeroed in shared memory.
+#include "attn_plan.cuh"
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -24,6 +25,8 @@ struct FwdParams {
   AttnArgs a;
   int pack;     // query heads in a tile
   float c;      // scale log2(e)
+  int tiles, heads, chunk;  // the grid: tiles (at most), packs of heads, packs that share the L2
+  const TilePlan* plan;     // NULL: tiles in their order
 };
 
 template <int DP>
@@ -50,12 +53,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h0 = blockIdx.y * p.pack, hk = h0 / a.group;  // first query head, key head
-  const int per = 128 / p.pack;                           // queries of a tile
-  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, 2 * per, false, blockIdx.x == 0 && blockIdx.y == 0);
-  if (t.b < 0) return;
-  const Seq s = load_seq(a, t.b, false, false);
-  const int i0 = (t.count - 1 - t.index) * 2 * per;  // the longest first
+  const Place at = place_of(blockIdx.x, p.tiles, p.heads, p.chunk);
+  const int h0 = at.head * p.pack, hk = h0 / a.group;  // first query head, key head
+  const int per = 128 / p.pack;                        // queries of a tile
+  Seq s;
+  int i0;  // the first query
+  if (p.plan) {
+    after_previous();
+    if (at.rank >= p.plan->count) return;
+    const TileEntry e = p.plan->tile[at.rank];
+    s = Seq{e.q0, e.n, e.k0, e.m};
+    i0 = e.start;
+  } else {
+    __shared__ int sFind[kThreads / 32 + 3];
+    const Tile t = find_tile<kThreads, false>(a, at.rank, 2 * per, false, blockIdx.x == 0, sFind);
+    if (t.b < 0) return;
+    s = load_seq(a, t.b, false, false);
+    i0 = (t.count - 1 - t.index) * 2 * per;  // the longest first
+  }
   // key tiles of the two row tiles
   auto key_tiles = [&](int m) {
     const int first = i0 + m * per, last = min(first + per, s.n) - 1;
@@ -241,8 +256,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DP>
-cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
+cudaError_t forward(const AttnArgs& a, TilePlan* plan, cudaStream_t s) {
   FwdParams p{a, heads_packed(a.group), a.scale * kLog2e};
+  p.tiles = (int)forward_tiles(a);
+  p.heads = a.Hq / p.pack;
+  p.chunk = head_chunk((int64_t)a.Tk * a.D * 4, a.Hkv) * (a.group / p.pack);
+  if ((int64_t)p.tiles * p.heads >= (1ll << 31)) return cudaErrorInvalidConfiguration;
   CUtensorMap q, k, v;
   if (!head_map(&q, a.q, a.Tq, a.Hq, a.D, a.ld_q, p.pack, 128 / p.pack)) return cudaErrorInvalidValue;
   if (a.Tk > 0) {
@@ -254,14 +273,25 @@ cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
   static const cudaError_t e =
       cudaFuncSetAttribute(attn_forward_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fwd<DP>::kBytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.Tq / (256 / p.pack) + a.B), a.Hq / p.pack);
+  const unsigned grid = (unsigned)p.tiles * p.heads;
+  // one sequence's tiles are in the order of their work as they are
+  if (a.B > 1 && a.B <= kPlanMaxB) {
+    p.plan = plan;
+    const cudaError_t l = launch_plan(a, PlanJob{0, 256 / p.pack, 0, 0, p.heads, 0, p.tiles, plan}, s);
+    if (l != cudaSuccess) return l;
+    return launch_after_smem(attn_forward_kernel<DP>, grid, kThreads, Fwd<DP>::kBytes, s, q, k, v, p);
+  }
   attn_forward_kernel<DP><<<grid, kThreads, Fwd<DP>::kBytes, s>>>(q, k, v, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) { return a.D <= 64 ? forward<64>(a, s) : forward<128>(a, s); }
+int64_t forward_tiles(const AttnArgs& a) { return a.Tq / (256 / heads_packed(a.group)) + a.B; }
+
+cudaError_t launch_tc(const AttnArgs& a, TilePlan* plan, cudaStream_t s) {
+  return a.D <= 64 ? forward<64>(a, plan, s) : forward<128>(a, plan, s);
+}
 
 }  // namespace attn
 }  // namespace moe

@@ -8,11 +8,15 @@
 // are. Sums over the query heads of a group and over all queries stay in one accumulator: no atomics,
 // and the bits never change. In return S and dP are formed twice: seven products instead of five.
 //
+// A tile of keys that meets very many queries is cut into pieces (attn_plan.cu): each leaves its sums in
+// the workspace, and the CTA that comes last (a ticket; it waits for nobody) adds them in their order.
+//
 // Warp 0 loads by TMA, warp 1 issues the products, warp 2 brings lse and delta of the inner rows (dk, dv),
 // warpgroups 1 and 2 form P and dS, each of one half of the columns. The products of one inner tile
 // take the tensor cores twice as long as P and dS take the warps, and they interleave without a second
 // set of accumulators (there is no room for one: S, dP, dK and dV fill tensor memory): while dS(t) is
 // formed, dV(t) and S(t+1) run, while P(t+1) is formed, dK(t) and dP(t+1).
+#include "attn_plan.cuh"
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -25,16 +29,25 @@ template <int DP>
 struct Bwd {
   static constexpr int kSlabs = DP / 64;
   static constexpr int kTile = R * DP * 2;
+  // Stages of Y1, which is read from S to the end of a step, and of Y2. A load takes about a step.
+  static constexpr int kN1 = DP == 64 ? 4 : 3, kN2 = DP == 64 ? 4 : 2;
   static constexpr int kStats = 2 * R * 2 * 4;  // two stages of -lse2 and -delta
-  static constexpr size_t kUsed = 1024 + 6 * kTile + kStats + 256;
-  // a CTA takes all of tensor memory: no second one on its SM
-  static constexpr size_t kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  static constexpr int kTiles = 2 + kN1 + kN2;
+  // All of it is dynamic, and begins on a boundary of 1024 bytes. A CTA takes all of tensor memory: the
+  // size leaves no second one on its SM.
+  static constexpr size_t kBytes = kTiles * kTile + kStats + 256;
+  static_assert(kBytes > 116 * 1024 && kBytes <= 227 * 1024);
 };
 
 struct BwdParams {
   AttnArgs a;
-  int pack;  // query heads in a tile
-  float c;   // scale log2(e)
+  int pack;   // query heads in a tile
+  float c;    // scale log2(e)
+  int tiles, heads, chunk;  // the grid: tiles (at most), packs of heads or key heads, those that share the L2
+  const TilePlan* plan;     // NULL: tiles in their order
+  const float *neg_lse, *neg_delta;
+  float* part;
+  uint32_t* tickets;
 };
 
 // (a, b) -> (a, b) * f + (c, d)
@@ -65,63 +78,89 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                          const BwdParams p) {
   using F = Bwd<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kN1 = F::kN1, kN2 = F::kN2;
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sX = smem;                   // X1, X2
-  uint8_t* sY1 = smem + 2 * F::kTile;   // two stages each
-  uint8_t* sY2 = smem + 4 * F::kTile;
-  float* sStat = reinterpret_cast<float*>(smem + 6 * F::kTile);  // [stage][-lse2, -delta][R]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 6 * F::kTile + F::kStats);
+  uint8_t* sY1 = smem + 2 * F::kTile;
+  uint8_t* sY2 = sY1 + kN1 * F::kTile;
+  float* sStat = reinterpret_cast<float*>(smem + F::kTiles * F::kTile);  // [stage][-lse2, -delta][R]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F::kTiles * F::kTile + F::kStats);
   uint64_t* x_full = bars;
-  uint64_t* y1_full = bars + 1;
-  uint64_t* y2_full = bars + 3;
-  uint64_t* y1_empty = bars + 5;
-  uint64_t* y2_empty = bars + 7;
-  uint64_t* stat_full = bars + 9;
-  uint64_t* stat_empty = bars + 11;
-  uint64_t* s_full = bars + 13;
-  uint64_t* dp_full = bars + 14;
-  uint64_t* p_ready = bars + 15;
-  uint64_t* ds_ready = bars + 16;
-  uint64_t* acc_full = bars + 17;
-  uint64_t* drain = bars + 18;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  uint64_t* y1_full = x_full + 1;
+  uint64_t* y1_empty = y1_full + kN1;
+  uint64_t* y2_full = y1_empty + kN1;
+  uint64_t* y2_empty = y2_full + kN2;
+  uint64_t* stat_full = y2_empty + kN2;
+  uint64_t* stat_empty = stat_full + 2;
+  uint64_t* s_full = stat_empty + 2;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* p_ready = s_full + 2;
+  uint64_t* ds_ready = s_full + 3;
+  uint64_t* acc_full = s_full + 4;
+  uint64_t* both = s_full + 5;
+  uint64_t* drain = s_full + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_one = abort + 1;
+  static_assert((1 + 2 * kN1 + 2 * kN2 + 4 + 7) * 8 + 12 <= 256);
 
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = R / p.pack;  // queries of a tile
-  const int hk = DKV ? (int)blockIdx.y : (int)blockIdx.y * p.pack / a.group;
-  const int h0 = DKV ? hk * a.group : (int)blockIdx.y * p.pack;  // first query head
-  const Tile t = find_tile<kThreads, DKV>(a, blockIdx.x, DKV ? R : per, true, blockIdx.x == 0 && blockIdx.y == 0);
-  if (t.b < 0) return;
-  const Seq s = load_seq(a, t.b, true, false);
-  // the outer tile's first row (key, or query: the longest first), and how many inner tiles it meets
-  const int o0 = DKV ? t.index * R : (t.count - 1 - t.index) * per;
-  int first = 0, tiles;  // DKV: of every pack of heads
-  if constexpr (DKV) {
-    first = a.causal ? max(0, o0 - (s.m - s.n)) / per : 0;  // the first queries that see key o0
-    tiles = max(0, (s.n + per - 1) / per - first);
-  } else {
-    tiles = (max(0, visible(a, s, min(o0 + per, s.n) - 1)) + R - 1) / R;
+  if (smem_addr(smem) & 1023) {  // the tiles' swizzle counts on it
+    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_TIMEOUT, -1);
+    return;
   }
-  const int steps = DKV ? tiles * (a.group / p.pack) : tiles;
-  // inner tile i: DKV: first query and head; else first key
-  auto inner_row = [&](int i) { return DKV ? (first + i % tiles) * per : i * R; };
-  auto inner_head = [&](int i) { return h0 + i / tiles * p.pack; };
+  const int per = R / p.pack;  // queries of a tile
+  const Place at = place_of(blockIdx.x, p.tiles, p.heads, p.chunk);
+  const int hk = DKV ? at.head : at.head * p.pack / a.group;
+  const int h0 = DKV ? hk * a.group : at.head * p.pack;  // first query head
+  let_next_begin();
+  after_previous();
+  TileEntry e;
+  if (p.plan) {
+    if (at.rank >= p.plan->count) return;
+    e = p.plan->tile[at.rank];
+  } else {
+    const Tile t = find_tile<kThreads, DKV>(a, at.rank, DKV ? R : per, true, blockIdx.x == 0, reinterpret_cast<int*>(smem));
+    if (t.b < 0) return;
+    const Seq q = load_seq(a, t.b, true, false);
+    e = TileEntry{q.q0, q.n, q.k0, q.m, DKV ? t.index * R : (t.count - 1 - t.index) * per, 0, 0, 0};
+  }
+  const Seq s{e.q0, e.n, e.k0, e.m};
+  const int o0 = e.start;  // the outer tile's first key or query
+  // inner tiles: of queries, from the first one that sees key o0, for one pack of heads after the other;
+  // or of keys
+  const int first = DKV && a.causal ? max(0, o0 - (s.m - s.n)) / per : 0;
+  const int tiles = DKV ? max(0, (s.n + per - 1) / per - first)
+                        : (max(0, visible(a, s, min(o0 + per, s.n) - 1)) + R - 1) / R;
+  const int from = p.plan ? e.lo : 0, steps = p.plan ? e.hi - e.lo : DKV ? tiles * (a.group / p.pack) : tiles;
+  struct Inner {  // walks over them
+    int tile, head;
+  };
+  auto begin = [&] { return DKV && steps > 0 ? Inner{from % tiles, h0 + from / tiles * p.pack} : Inner{from, h0}; };
+  auto advance = [&](Inner& i) {
+    ++i.tile;
+    if (DKV && i.tile == tiles) i.tile = 0, i.head += p.pack;
+  };
+  auto row_of = [&](const Inner& i) { return DKV ? (first + i.tile) * per : i.tile * R; };  // in the sequence
   // rows of it that are the sequence's
-  auto inner_live = [&](int i) { return DKV ? min(R, (s.n - inner_row(i)) * p.pack) : min(R, s.m - inner_row(i)); };
+  auto live_of = [&](const Inner& i) { return DKV ? min(R, (s.n - row_of(i)) * p.pack) : min(R, s.m - row_of(i)); };
 
   if (threadIdx.x == 0) {
     mbar_init(x_full, 1);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kN1; ++b) {
       mbar_init(&y1_full[b], 1);
-      mbar_init(&y2_full[b], 1);
       mbar_init(&y1_empty[b], 1);
+    }
+    for (int b = 0; b < kN2; ++b) {
+      mbar_init(&y2_full[b], 1);
       mbar_init(&y2_empty[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&stat_full[b], 32);
       mbar_init(&stat_empty[b], 8);
     }
+    mbar_init(both, 8);
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(p_ready, 8);
@@ -150,23 +189,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       load(DKV ? &tmK : &tmQ, sX, x_full, DKV ? hk : h0, DKV ? s.k0 + o0 : s.q0 + o0);
       load(DKV ? &tmV : &tmO, sX + F::kTile, x_full, DKV ? hk : h0, DKV ? s.k0 + o0 : s.q0 + o0);
       bool ok = true;
-      int n1 = 0, n2 = 0;
-      for (int i = 0; i < steps && ok; ++i) {
-        const int b = i & 1, head = DKV ? inner_head(i) : hk, row = (DKV ? s.q0 : s.k0) + inner_row(i);
-        const uint32_t parity = (i >> 1 & 1) ^ 1;
-        if (!(ok = mbar_wait(&y1_empty[b], parity, abort, kTimeoutNs, a.status))) break;
-        mbar_arrive_expect_tx(&y1_full[b], F::kTile);
-        load(DKV ? &tmQ : &tmK, sY1 + b * F::kTile, &y1_full[b], head, row);
+      int u1 = 0, u2 = 0, n1 = 0, n2 = 0;  // stages, loads
+      uint32_t ph1 = 0, ph2 = 0;
+      Inner in = begin();
+      for (int i = 0; i < steps && ok; ++i, advance(in)) {
+        const int head = DKV ? in.head : hk, row = (DKV ? s.q0 : s.k0) + row_of(in);
+        if (!(ok = mbar_wait(&y1_empty[u1], ph1 ^ 1, abort, kTimeoutNs, a.status))) break;
+        mbar_arrive_expect_tx(&y1_full[u1], F::kTile);
+        load(DKV ? &tmQ : &tmK, sY1 + u1 * F::kTile, &y1_full[u1], head, row);
         ++n1;
-        if (!(ok = mbar_wait(&y2_empty[b], parity, abort, kTimeoutNs, a.status))) break;
-        mbar_arrive_expect_tx(&y2_full[b], F::kTile);
-        load(DKV ? &tmO : &tmV, sY2 + b * F::kTile, &y2_full[b], head, row);
+        if (++u1 == kN1) u1 = 0, ph1 ^= 1;
+        if (!(ok = mbar_wait(&y2_empty[u2], ph2 ^ 1, abort, kTimeoutNs, a.status))) break;
+        mbar_arrive_expect_tx(&y2_full[u2], F::kTile);
+        load(DKV ? &tmO : &tmV, sY2 + u2 * F::kTile, &y2_full[u2], head, row);
         ++n2;
+        if (++u2 == kN2) u2 = 0, ph2 ^= 1;
       }
       // leave no copy in flight
       mbar_wait_drain(x_full, 0, kTimeoutNs, a.status);
-      for (int i = max(0, n1 - 2); i < n1; ++i) mbar_wait_drain(&y1_full[i & 1], i >> 1 & 1, kTimeoutNs, a.status);
-      for (int i = max(0, n2 - 2); i < n2; ++i) mbar_wait_drain(&y2_full[i & 1], i >> 1 & 1, kTimeoutNs, a.status);
+      for (int i = max(0, n1 - kN1); i < n1; ++i) mbar_wait_drain(&y1_full[i % kN1], i / kN1 & 1, kTimeoutNs, a.status);
+      for (int i = max(0, n2 - kN2); i < n2; ++i) mbar_wait_drain(&y2_full[i % kN2], i / kN2 & 1, kTimeoutNs, a.status);
     } else if (warp == 1 && steps > 0) {
       // ===================== products
       const uint32_t idesc_s = idesc_make(1, R, R);
@@ -190,36 +232,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < R / 16; ++k)
           mma_ts(d, w + (k / 4) * 64 + (k % 4) * 8, ya + (2048 / 16) * k, idesc_a, !begin || k > 0, one);
       };
-      // inner tile i's Y1 (Y2) has come; rows that are not the sequence's are zeroed
-      auto arrived = [&](uint64_t* bar, uint8_t* y, int i) {
-        if (!all(mbar_wait(&bar[i & 1], i >> 1 & 1, abort, kTimeoutNs, a.status))) return false;
-        const int live = inner_live(i);
-        if (live < R) clear_rows(y + (i & 1) * F::kTile, F::kSlabs, R, live, lane);
+      // the next inner tile's Y1 (Y2) has come; rows that are not the sequence's are zeroed
+      auto arrived = [&](uint64_t* bar, uint32_t parity, uint8_t* y, const Inner& in) {
+        if (!all(mbar_wait(bar, parity, abort, kTimeoutNs, a.status))) return false;
+        const int live = live_of(in);
+        if (live < R) clear_rows(y, F::kSlabs, R, live, lane);
         tc_fence_after();
         return true;
       };
-      bool ok = all(mbar_wait(x_full, 0, abort, kTimeoutNs, a.status)) && arrived(y1_full, sY1, 0);
+      int u1 = 0, u2 = 0;  // stages of the step
+      uint32_t ph1 = 0, ph2 = 0;
+      Inner in = begin();
+      bool ok = all(mbar_wait(x_full, 0, abort, kTimeoutNs, a.status)) && arrived(y1_full, 0, sY1, in);
       if (ok) scores(tS, sX, sY1, s_full);
-      ok = ok && arrived(y2_full, sY2, 0);
+      ok = ok && arrived(y2_full, 0, sY2, in);
       if (ok) scores(tP, sX + F::kTile, sY2, dp_full);
       for (int i = 0; i < steps && ok; ++i) {
-        const int b = i & 1;
-        if (!(ok = all(mbar_wait(p_ready, b, abort, kTimeoutNs, a.status)))) break;
+        const uint32_t parity = i & 1;
+        const int v1 = u1 + 1 == kN1 ? 0 : u1 + 1, v2 = u2 + 1 == kN2 ? 0 : u2 + 1;  // of the next step
+        if (v1 == 0) ph1 ^= 1;
+        if (v2 == 0) ph2 ^= 1;
+        advance(in);
+        if (!(ok = all(mbar_wait(p_ready, parity, abort, kTimeoutNs, a.status)))) break;
         tc_fence_after();
-        if constexpr (DKV) products(tA2, tS, sY2 + b * F::kTile, i == 0);
-        commit(&y2_empty[b], one);
+        if constexpr (DKV) products(tA2, tS, sY2 + u2 * F::kTile, i == 0);
+        commit(&y2_empty[u2], one);
         if (i + 1 < steps) {
-          if (!(ok = arrived(y1_full, sY1, i + 1))) break;
-          scores(tS, sX, sY1 + (b ^ 1) * F::kTile, s_full);
+          if (!(ok = arrived(&y1_full[v1], ph1, sY1 + v1 * F::kTile, in))) break;
+          scores(tS, sX, sY1 + v1 * F::kTile, s_full);
         }
-        if (!(ok = all(mbar_wait(ds_ready, b, abort, kTimeoutNs, a.status)))) break;
+        if (!(ok = all(mbar_wait(ds_ready, parity, abort, kTimeoutNs, a.status)))) break;
         tc_fence_after();
-        products(tA1, tP, sY1 + b * F::kTile, i == 0);
-        commit(&y1_empty[b], one);
+        products(tA1, tP, sY1 + u1 * F::kTile, i == 0);
+        commit(&y1_empty[u1], one);
         if (i + 1 < steps) {
-          if (!(ok = arrived(y2_full, sY2, i + 1))) break;
-          scores(tP, sX + F::kTile, sY2 + (b ^ 1) * F::kTile, dp_full);
+          if (!(ok = arrived(&y2_full[v2], ph2, sY2 + v2 * F::kTile, in))) break;
+          scores(tP, sX + F::kTile, sY2 + v2 * F::kTile, dp_full);
         }
+        u1 = v1, u2 = v2;
       }
       __syncwarp();
       if (lane == 0) {
@@ -229,26 +279,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (DKV && warp == 2) {
-      // ===================== -lse2 and -delta of the inner rows; a row that is not there, or sees no key,
-      // gets p = exp2(s - inf) = 0
-      for (int i = 0; i < steps; ++i) {
-        const int b = i & 1, row0 = inner_row(i), head = inner_head(i), live = inner_live(i);
-        float v[8];
+      // ===================== -lse2 and -delta of the inner rows, a step ahead of their use; a row that is
+      // not there gets p = exp2(s - inf) = 0
+      Inner in = begin();
+      float v[8];
+      auto fetch = [&] {
+        const int64_t base = (int64_t)(in.head / p.pack) * a.Tq * p.pack + (int64_t)(s.q0 + row_of(in)) * p.pack;
+        const int live = live_of(in);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int r = 32 * q + lane;
-          v[q] = -INFINITY, v[4 + q] = 0.0f;
-          if (r < live) {
-            const int64_t at = (int64_t)(head + r % p.pack) * a.Tq + s.q0 + row0 + r / p.pack;
-            const float l = __ldg(a.lse + at);
-            if (l != -INFINITY) v[q] = -l * kLog2e;
-            v[4 + q] = -__ldg(a.delta + at);
-          }
+          v[q] = r < live ? __ldg(p.neg_lse + base + r) : -INFINITY;
+          v[4 + q] = r < live ? __ldg(p.neg_delta + base + r) : 0.0f;
         }
+      };
+      if (steps > 0) fetch();
+      for (int i = 0; i < steps; ++i) {
+        const int b = i & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&stat_empty[b], (i >> 1 & 1) ^ 1, abort, kTimeoutNs, a.status))) break;
 #pragma unroll
         for (int q = 0; q < 8; ++q) sStat[b * 2 * R + q / 4 * R + 32 * (q % 4) + lane] = v[q];
         mbar_arrive(&stat_full[b]);
+        advance(in);
+        if (i + 1 < steps) fetch();
       }
     }
   } else {
@@ -262,15 +315,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     float neg_lse = -INFINITY, neg_delta = 0.0f;
     int seen = 0;
     if (!DKV && i_q < s.n) {
-      const int64_t at = (int64_t)h * a.Tq + s.q0 + i_q;
-      const float l = __ldg(a.lse + at);
-      if (l != -INFINITY) neg_lse = -l * kLog2e;
-      neg_delta = -__ldg(a.delta + at);
+      const int64_t x = ((int64_t)at.head * a.Tq + s.q0 + i_q) * p.pack + row % p.pack;
+      neg_lse = __ldg(p.neg_lse + x);
+      neg_delta = __ldg(p.neg_delta + x);
       seen = visible(a, s, i_q);
     }
+    Inner in = begin();
     bool ok = true;
-    for (int i = 0; i < steps; ++i) {
-      const int b = i & 1, row0 = inner_row(i);
+    for (int i = 0; i < steps; ++i, advance(in)) {
+      const int b = i & 1, row0 = row_of(in);
       const float4* stat = reinterpret_cast<const float4*>(sStat + b * 2 * R + 64 * half);
       if (DKV && !(ok = __all_sync(0xffffffffu, mbar_wait(&stat_full[b], i >> 1 & 1, abort, kTimeoutNs, a.status)))) break;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, b, abort, kTimeoutNs, a.status)))) break;
@@ -313,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready);
-      } else if ((i + 1) * R > visible(a, s, o0)) {
+      } else if (row0 + R > visible(a, s, o0)) {
         const int end = seen - row0 - 64 * half;
 #pragma unroll
         for (int l = 0; l < 64; ++l)
@@ -374,7 +427,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    if constexpr (DKV) {
+    if (DKV && e.cut) {
+      // a piece: its sums into the workspace, added up by whoever comes last
+      const int slot = e.cut >> 16, number = e.cut >> 8 & 255, pieces = e.cut & 255;
+      auto place = [&](int i) { return (int64_t)((slot + i) * p.heads + hk) * 2 * R * DP; };
+      float* mine = p.part + place(number) + row * DP + kCols * half;
+#pragma unroll 1
+      for (int q = 0; q < 2 * kCols; q += 16) {
+        const int which = q >= kCols, col = q - which * kCols;
+        uint32_t o[16] = {};
+        if (steps > 0) {
+          tmem_ld16((which ? tA2 : tA1) + lanes + kCols * half + col, o);
+          tmem_ld_wait();
+        }
+        if (live)
+#pragma unroll
+          for (int l = 0; l < 16; l += 4)
+            *reinterpret_cast<uint4*>(mine + which * R * DP + col + l) = make_uint4(o[l], o[l + 1], o[l + 2], o[l + 3]);
+      }
+      __threadfence();
+      uint32_t turn = 0;
+      auto both_sync = [&] {  // of both warpgroups; false: given up
+        __syncwarp();
+        if (lane == 0) mbar_arrive(both);
+        const bool come = __all_sync(0xffffffffu, mbar_wait(both, turn, abort, kTimeoutNs, a.status));
+        turn ^= 1;
+        return come;
+      };
+      if (ok && both_sync()) {
+        uint32_t* ticket = p.tickets + slot * p.heads + hk;
+        if (half == 0 && row == 0) {
+          const bool last = atomicAdd(ticket, 1u) == (uint32_t)pieces - 1;
+          if (last) *ticket = 0;
+          *last_one = last;
+        }
+        if (both_sync() && *last_one) {
+          __threadfence();
+          const int rows = min(R, s.m - o0);
+          for (int x = half * 128 + row; x < 2 * rows * (DP / 4); x += 256) {
+            const int which = x >= rows * (DP / 4), y = x - which * rows * (DP / 4), r = y / (DP / 4), d = y % (DP / 4) * 4;
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int i = 0; i < pieces; ++i) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + place(i) + which * R * DP + r * DP + d));
+              sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
+            const float f = which ? 1.0f : a.scale;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? a.dv : a.dk) +
+                                 (int64_t)(s.k0 + o0 + r) * (which ? a.ld_v : a.ld_k) + (int64_t)hk * a.D + d;
+            if (d < a.D) *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(sum.x * f, sum.y * f), pack2(sum.z * f, sum.w * f));
+          }
+        }
+      }
+    } else if constexpr (DKV) {
       store(tA1, a.dk, (int64_t)(s.k0 + o0 + row) * a.ld_k + (int64_t)hk * a.D, a.scale);
       store(tA2, a.dv, (int64_t)(s.k0 + o0 + row) * a.ld_v + (int64_t)hk * a.D, 1.0f);
     } else {
@@ -388,17 +492,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DP, bool DKV>
-cudaError_t launch(dim3 grid, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
-                   const BwdParams& p, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o, const BwdParams& p,
+                   cudaStream_t s) {
   static const cudaError_t e = cudaFuncSetAttribute(attn_backward_kernel<DP, DKV>,
                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Bwd<DP>::kBytes);
   if (e != cudaSuccess) return e;
-  attn_backward_kernel<DP, DKV><<<grid, kThreads, Bwd<DP>::kBytes, s>>>(q, k, v, o, p);
-  return cudaGetLastError();
+  if ((int64_t)p.tiles * p.heads >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  return launch_after_smem(attn_backward_kernel<DP, DKV>, (unsigned)p.tiles * p.heads, kThreads, Bwd<DP>::kBytes, s, q, k, v, o, p);
 }
 
 template <int DP>
-cudaError_t backward(const AttnArgs& a, cudaStream_t s) {
+cudaError_t backward(const AttnArgs& a, const BackwardSpace& w, cudaStream_t s) {
   BwdParams p{a, heads_packed(a.group), a.scale * kLog2e};
   CUtensorMap q, k, v, o;
   if (a.Tq > 0 && (!head_map(&q, a.q, a.Tq, a.Hq, a.D, a.ld_q, p.pack, R / p.pack) ||
@@ -409,18 +513,35 @@ cudaError_t backward(const AttnArgs& a, cudaStream_t s) {
   // without queries or keys nothing of them is loaded
   if (a.Tq == 0) q = o = k;
   if (a.Tk == 0) k = v = q;
-  cudaError_t e = cudaSuccess;
-  if (a.Tq > 0) e = launch<DP, false>(dim3((unsigned)(a.Tq / (R / p.pack) + a.B), a.Hq / p.pack), q, k, v, o, p, s);
-  if (e != cudaSuccess || a.Tk == 0) return e;
-  return launch<DP, true>(dim3((unsigned)(a.Tk / R + a.B), a.Hkv), q, k, v, o, p, s);
+  const bool plan = a.B <= kPlanMaxB;
+  const int packs = a.group / p.pack, per = R / p.pack;
+  const PlanJob dq{0, per, 0, 0, a.Hq / p.pack, 0, (int)dq_tiles(a), w.dq_plan};
+  const PlanJob dkv{1, 0, per, packs, a.Hkv, kPieces, (int)(a.Tk / R + a.B), w.dkv_plan};
+  cudaError_t e = launch_plan_backward(a, dq, dkv, StatsJob{p.pack, w.neg_lse, w.neg_delta}, plan, s);
+  if (e != cudaSuccess) return e;
+  p.neg_lse = w.neg_lse, p.neg_delta = w.neg_delta, p.part = w.part, p.tickets = w.tickets;
+  if (a.Tq > 0) {
+    p.tiles = (int)dq_tiles(a);
+    p.heads = a.Hq / p.pack;
+    p.chunk = head_chunk((int64_t)a.Tk * a.D * 4, a.Hkv) * packs;
+    p.plan = plan ? w.dq_plan : nullptr;
+    if ((e = launch<DP, false>(q, k, v, o, p, s)) != cudaSuccess) return e;
+  }
+  if (a.Tk == 0) return cudaSuccess;
+  p.tiles = (int)(plan ? dkv_tiles(a) : a.Tk / R + a.B);
+  p.heads = a.Hkv;
+  p.chunk = head_chunk((int64_t)a.Tq * a.group * a.D * 4, a.Hkv);
+  p.plan = plan ? w.dkv_plan : nullptr;
+  return launch<DP, true>(q, k, v, o, p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_tc_backward(const AttnArgs& a, cudaStream_t s) {
-  const cudaError_t e = launch_delta(a, true, s);
-  if (e != cudaSuccess) return e;
-  return a.D <= 64 ? backward<64>(a, s) : backward<128>(a, s);
+int64_t dq_tiles(const AttnArgs& a) { return a.Tq / (R / heads_packed(a.group)) + a.B; }
+int64_t dkv_tiles(const AttnArgs& a) { return a.Tk / R + a.B + kMostPieces / a.Hkv; }
+
+cudaError_t launch_tc_backward(const AttnArgs& a, const BackwardSpace& w, cudaStream_t s) {
+  return a.D <= 64 ? backward<64>(a, w, s) : backward<128>(a, w, s);
 }
 
 }  // namespace attn

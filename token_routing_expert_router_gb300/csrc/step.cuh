@@ -15,7 +15,7 @@ int num_sms();  // of the current device (gemm_tc.cu)
 // each returns to what the next call expects, whatever call shared the workspace before.
 constexpr size_t kClipState = 1024;   // grad_clip.cu's ticket and scale
 constexpr size_t kHeadTicket = 1152;  // head_loss.cu's ticket
-constexpr size_t kAttnTickets = 2048; // attn_stream.cu's tickets, one for every CTA
+constexpr size_t kAttnTickets = 2048; // attention's tickets, up to 512
 
 // Programmatic dependent launch inside a call: a kernel launched with launch_after may be set
 // up while the one before it in the stream still runs, and calls after_previous() before it
@@ -25,10 +25,11 @@ __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+cudaError_t launch_after_smem(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -37,6 +38,10 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+  return launch_after_smem(kern, grid, block, 0, s, args...);
 }
 
 // ---- block norms
@@ -101,8 +106,11 @@ struct AttnSeqs {  // where the sequences' rows are: k_start and k_len NULL: key
   const int32_t *q_start, *k_start, *k_len;
 };
 struct AttnScratch {  // workspace offsets, after the status head
-  size_t delta;        // backward
-  size_t stat, part;   // forward, few rows over many keys
+  size_t delta;                            // backward, on the FMA units
+  size_t neg_lse, neg_delta, dq_plan, dkv_plan;  // backward, on the tensor cores
+  size_t plan;                             // forward, tiles
+  size_t stat;                             // forward, few rows over many keys
+  size_t part;                             // parts of either
   size_t total;
 };
 AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward);
