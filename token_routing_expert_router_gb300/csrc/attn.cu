@@ -63,9 +63,11 @@ AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward) {
     s.neg_lse = take(rows * sizeof(float));
     s.dq_plan = take(attn::plan_bytes(attn::dq_tiles(a)));
     s.dkv_plan = take(attn::plan_bytes(attn::dkv_tiles(a)));
+    s.first = take((size_t)2 * (c.B + 1) * sizeof(int));
     s.part = take((size_t)attn::kMostPieces * 2 * 128 * DP * sizeof(float));
   } else if (tensor_cores) {
     s.plan = take(attn::plan_bytes(attn::forward_tiles(a)));
+    s.first = take((size_t)(c.B + 1) * sizeof(int));
     s.stat = take((size_t)2 * attn::kMaxStreamCtas * 128 * sizeof(float2));
     s.part = take((size_t)2 * attn::kMaxStreamCtas * 128 * DP * sizeof(float));
   }
@@ -80,7 +82,8 @@ cudaError_t launch_attn(const moe_attn_config_t& c, const void* q, const void* k
   if (c.act_dtype != MOE_DTYPE_BF16 || !attn::tc_rows(a, false)) return attn::launch_simt(a, c.act_dtype == MOE_DTYPE_BF16, s);
   char* b = static_cast<char*>(ws);
   const AttnScratch L = attn_scratch(c, false);
-  if (!attn::stream_rule(a)) return attn::launch_tc(a, reinterpret_cast<attn::TilePlan*>(b + L.plan), s);
+  if (!attn::stream_rule(a)) return attn::launch_tc(a, reinterpret_cast<attn::TilePlan*>(b + L.plan),
+                                                     reinterpret_cast<int*>(b + L.first), reinterpret_cast<int*>(b + kAttnQueue), s);
   return attn::launch_stream(a, {reinterpret_cast<uint32_t*>(b + kAttnTickets), reinterpret_cast<float2*>(b + L.stat),
                                  reinterpret_cast<float*>(b + L.part)}, s);
 }
@@ -97,6 +100,7 @@ cudaError_t launch_attn_backward(const moe_attn_config_t& c, const void* q, cons
   if (c.act_dtype != MOE_DTYPE_BF16 || !attn::tc_rows(a, true)) return attn::launch_simt_backward(a, c.act_dtype == MOE_DTYPE_BF16, s);
   auto floats = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
   return attn::launch_tc_backward(a, {reinterpret_cast<attn::TilePlan*>(b + L.dq_plan), reinterpret_cast<attn::TilePlan*>(b + L.dkv_plan),
+                                      reinterpret_cast<int*>(b + L.first),
                                       floats(L.neg_lse), floats(L.neg_delta), floats(L.part),
                                       reinterpret_cast<uint32_t*>(b + kAttnTickets)}, s);
 }

@@ -111,7 +111,8 @@ __device__ __forceinline__ int visible(const AttnArgs& a, const Seq& s, int i) {
 // ---- launchers of the variants
 bool tc_rows(const AttnArgs& a, bool backward);  // bf16 tensors' rows are multiples of 16 bytes
 struct TilePlan;  // attn_plan.cuh
-cudaError_t launch_tc(const AttnArgs& a, TilePlan* plan, cudaStream_t s);  // plan: room for the tiles' order
+// plan: room for the tiles' order; first: for B + 1 words; queue: two words of the workspace's head
+cudaError_t launch_tc(const AttnArgs& a, TilePlan* plan, int* first, int* queue, cudaStream_t s);
 // Few rows over many keys: one CTA an SM, each with two places for parts of lines.
 constexpr int kMaxStreamCtas = 160;
 inline int stream_ctas() { return tc::num_sms() < kMaxStreamCtas ? tc::num_sms() : kMaxStreamCtas; }
@@ -126,6 +127,7 @@ cudaError_t launch_simt(const AttnArgs& a, bool bf16, cudaStream_t s);
 // What the backward keeps in the workspace beside the statistics.
 struct BackwardSpace {
   TilePlan *dq_plan, *dkv_plan;
+  int* first;         // [2][B + 1]
   float *neg_lse, *neg_delta;
   float* part;        // [kMostPieces][2][128][DP]: dk and dv of pieces of a tile
   uint32_t* tickets;  // [kMostPieces], zero between calls

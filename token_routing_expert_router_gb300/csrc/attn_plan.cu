@@ -13,8 +13,10 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kSort = 1024;    // threads of the sorting block
+constexpr int kSort = 256;     // threads of a block
+constexpr int kFirst = 1024;   // sequences whose prefix is kept in shared memory
 constexpr int kClasses = 64;
+constexpr int kAhead = 4;      // rows and heads whose loads a thread has in flight
 
 // Steps (inner tiles) of a tile of queries, or of a tile of keys for all packs of heads.
 __device__ __forceinline__ int tile_steps(const AttnArgs& a, const PlanJob& j, const Seq& s, int tile) {
@@ -27,12 +29,13 @@ __device__ __forceinline__ int tile_steps(const AttnArgs& a, const PlanJob& j, c
 }
 
 __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool report) {
-  __shared__ int sFirst[kPlanMaxB + 1];  // tiles of the sequences before
-  __shared__ int sWarp[32];
+  __shared__ int sKept[kFirst + 1];
+  __shared__ int sWarp[kSort / 32];
   __shared__ unsigned long long sTotal;
   __shared__ int sMost, sSlots, sClass[kClasses];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = j.keys ? 128 : j.rows;
+  int* sFirst = a.B <= kFirst ? sKept : j.first;
   if (tid == 0) sTotal = 0, sMost = 0, sSlots = 0;
   if (tid < kClasses) sClass[tid] = 0;
   int carry = 0;
@@ -53,7 +56,7 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
     if (lane == 31) sWarp[warp] = inc;
     __syncthreads();
     int before = carry + inc - n, all = 0;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < kSort / 32; ++w) {
       if (w < warp) before += sWarp[w];
       all += sWarp[w];
     }
@@ -122,7 +125,6 @@ __device__ void row_stats(const AttnArgs& a, const StatsJob& j, int64_t block, i
   const int lane = threadIdx.x % LANES;
   const int64_t all = (int64_t)a.Tq * a.Hq;
   const bool in = 8 * lane < a.D;
-  constexpr int kAhead = 4;
   for (int64_t i0 = block * kPer * kAhead + threadIdx.x / LANES; i0 < all; i0 += blocks * kPer * kAhead) {
     uint4 x[kAhead], y[kAhead];
 #pragma unroll
@@ -180,14 +182,9 @@ cudaError_t launch_plan(const AttnArgs& a, const PlanJob& j, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_plan_backward(const AttnArgs& a, const PlanJob& dq, const PlanJob& dkv, const StatsJob& st, bool plan,
-                                 cudaStream_t s) {
-  const int64_t per = (int64_t)kSort / (a.D <= 64 ? 8 : 16) * 4;
-  const int jobs = plan ? 2 : 0;
-  const int64_t blocks = ceil_div((int64_t)a.Tq * a.Hq, per) < 2 * tc::num_sms() ? ceil_div((int64_t)a.Tq * a.Hq, per)
-                                                                                 : 2 * (int64_t)tc::num_sms();
-  if (jobs + blocks == 0) return cudaSuccess;
-  plan_kernel<<<(unsigned)(jobs + blocks), kSort, 0, s>>>(a, dq, dkv, st, jobs, 1);
+cudaError_t launch_plan_backward(const AttnArgs& a, const PlanJob& dq, const PlanJob& dkv, const StatsJob& st, cudaStream_t s) {
+  const int64_t blocks = ceil_div((int64_t)a.Tq * a.Hq, (int64_t)kSort / (a.D <= 64 ? 8 : 16) * kAhead), most = 8 * (int64_t)tc::num_sms();
+  plan_kernel<<<(unsigned)(2 + (blocks < most ? blocks : most)), kSort, 0, s>>>(a, dq, dkv, st, 2, 1);
   return cudaGetLastError();
 }
 

@@ -6,8 +6,6 @@
 namespace moe {
 namespace attn {
 
-constexpr int kPlanMaxB = 4096;  // sequences that a plan is made for; with more, tiles go in their order
-
 struct TileEntry {
   int q0, n, k0, m;  // the sequence's rows
   int start;         // the tile's first query or key
@@ -28,15 +26,14 @@ struct PlanJob {
   int pieces;        // 0, or cut tiles so that about this many pieces come of all heads' tiles
   int most;          // entries that there is room for, without the cuts
   TilePlan* plan;
+  int* first;        // [B + 1]: tiles of the sequences before
 };
 struct StatsJob {
   int pack;
   float *neg_lse, *neg_delta;  // [Hq / pack][Tq][pack]
 };
 cudaError_t launch_plan(const AttnArgs& a, const PlanJob& j, cudaStream_t s);
-// plan: sort too (else the statistics alone)
-cudaError_t launch_plan_backward(const AttnArgs& a, const PlanJob& dq, const PlanJob& dkv, const StatsJob& st, bool plan,
-                                 cudaStream_t s);
+cudaError_t launch_plan_backward(const AttnArgs& a, const PlanJob& dq, const PlanJob& dkv, const StatsJob& st, cudaStream_t s);
 
 // Block id -> the tile's place in the order and the head: chunks of heads whose operands stay in L2 one
 // behind the other, in a chunk every head's longest tile, then every head's next.

@@ -1,6 +1,7 @@
 // Attention on the tensor cores (bf16, D <= 128), one pass over the keys.
 //
-// A CTA has two tiles of 128 rows of Q against one key head, and goes over its keys in tiles of 128:
+// A CTA takes one item after the other, two tiles of 128 rows of Q against one key head, and goes over
+// its keys in tiles of 128:
 //   S = Q K^T (tensor memory) -> P = exp2(c (S - m)), bf16, over S's columns -> O += P V (tensor memory)
 // Rows of a tile are (query, head) pairs, `pack` query heads of the group side by side: a key tile is
 // loaded once for 256 of them, and few queries of many heads still fill a tile.
@@ -14,6 +15,12 @@
 // reference, since all sums are fp32 and P's rounding is relative. The keys are taken from the last to
 // the first, so that the tile with the mask comes first. Key rows behind the sequence's end belong to
 // somebody else: their scores are replaced, and their V rows are zeroed in shared memory.
+//
+// Items come in the order of their work, the longest first, and a CTA takes the next one when its loads
+// are nearly through with the last (shares fixed beforehand cost 15 % with two items a CTA: SMs are not
+// equally far from memory). The loads and the first scores of an item run while the last one's O is
+// written: a short sequence's tile is little more than such ends (40 prompts of 225 tokens: 51 us with a
+// CTA for every item).
 #include "attn_plan.cuh"
 #include "attn_tc.cuh"
 
@@ -21,12 +28,15 @@ namespace moe {
 namespace attn {
 namespace {
 
+constexpr int kIds = 2;  // items whose number is known at once
+
 struct FwdParams {
   AttnArgs a;
   int pack;     // query heads in a tile
   float c;      // scale log2(e)
-  int tiles, heads, chunk;  // the grid: tiles (at most), packs of heads, packs that share the L2
-  const TilePlan* plan;     // NULL: tiles in their order
+  int tiles, heads, chunk;  // tiles (at most), packs of heads, packs that share the L2
+  const TilePlan* plan;     // NULL: one sequence
+  int* queue;               // [2]: items taken beyond the CTAs' first ones, CTAs that are through; zero between calls
 };
 
 template <int DP>
@@ -43,41 +53,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = bars;
   uint64_t* empty = bars + kUnits;
   uint64_t* q_full = bars + 2 * kUnits;
-  uint64_t* s_full = q_full + 1;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
-  uint64_t* drain = o_full + 2;
+  uint64_t* o_free = o_full + 2;
+  uint64_t* id_full = o_free + 2;
+  uint64_t* id_empty = id_full + kIds;
+  uint64_t* drain = id_empty + kIds;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * 8 + 8) * 8 + 8 <= 256);
+  volatile int* ids = abort + 1;  // of the items, -1 behind the last
+  static_assert((2 * 8 + 11 + 2 * kIds) * 8 + 8 + 4 * kIds <= 512);
 
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Place at = place_of(blockIdx.x, p.tiles, p.heads, p.chunk);
-  const int h0 = at.head * p.pack, hk = h0 / a.group;  // first query head, key head
-  const int per = 128 / p.pack;                        // queries of a tile
-  Seq s;
-  int i0;  // the first query
-  if (p.plan) {
-    after_previous();
-    if (at.rank >= p.plan->count) return;
-    const TileEntry e = p.plan->tile[at.rank];
-    s = Seq{e.q0, e.n, e.k0, e.m};
-    i0 = e.start;
-  } else {
-    __shared__ int sFind[kThreads / 32 + 3];
-    const Tile t = find_tile<kThreads, false>(a, at.rank, 2 * per, false, blockIdx.x == 0, sFind);
-    if (t.b < 0) return;
-    s = load_seq(a, t.b, false, false);
-    i0 = (t.count - 1 - t.index) * 2 * per;  // the longest first
-  }
-  // key tiles of the two row tiles
-  auto key_tiles = [&](int m) {
-    const int first = i0 + m * per, last = min(first + per, s.n) - 1;
-    return last < first ? 0 : (max(0, visible(a, s, last)) + BK - 1) / BK;
-  };
-  const int n0 = key_tiles(0), n1 = key_tiles(1), steps = max(n0, n1);
-  auto tiles_of = [&](int m) { return m ? n1 : n0; };
+  const int per = 128 / p.pack;  // queries of a tile
 
   if (threadIdx.x == 0) {
     for (int u = 0; u < kUnits; ++u) {
@@ -85,10 +76,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[u], 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int m = 0; m < 2; ++m) {
       mbar_init(&s_full[m], 1);
       mbar_init(&p_full[m], 4);
       mbar_init(&o_full[m], 1);
+      mbar_init(&o_free[m], 4);
+    }
+    for (int i = 0; i < kIds; ++i) {
+      mbar_init(&id_full[i], 1);
+      mbar_init(&id_empty[i], 9);  // the issuing warp, the softmax warps
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -101,53 +98,118 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t tS = tmem, tO = tmem + 256;  // S and P of tile m at 128 m, O at DP m
 
+  after_previous();
+  Seq only{};
+  if (!p.plan) only = load_seq(a, 0, false, blockIdx.x == 0 && threadIdx.x == 0);
+  const int tiles = p.plan ? p.plan->count : (only.n + 2 * per - 1) / (2 * per), items = tiles * p.heads;
+  struct Item {
+    Seq s;
+    int i0, h0;     // first query, first query head
+    int n0, n1;     // key tiles of the two row tiles
+    __device__ int steps() const { return max(n0, n1); }
+    __device__ int of(int m) const { return m ? n1 : n0; }
+  };
+  auto item = [&](int id, Item& it) {
+    const Place at = place_of(id, tiles, p.heads, p.chunk);
+    it.h0 = at.head * p.pack;
+    if (p.plan) {
+      const TileEntry* e = p.plan->tile + at.rank;
+      it.s = Seq{e->q0, e->n, e->k0, e->m};
+      it.i0 = e->start;
+    } else {
+      it.s = only;
+      it.i0 = (tiles - 1 - at.rank) * 2 * per;
+    }
+    auto key_tiles = [&](int first) {
+      const int last = min(first + per, it.s.n) - 1;
+      return last < first ? 0 : (max(0, visible(a, it.s, last)) + BK - 1) / BK;
+    };
+    it.n0 = key_tiles(it.i0), it.n1 = key_tiles(it.i0 + per);
+  };
+  // a warp's view of the CTA's k-th item; false: there is none (or given up)
+  auto taken = [&](int k, Item& it) {
+    const bool come = mbar_wait(&id_full[k % kIds], k / kIds & 1, abort, kTimeoutNs, a.status);
+    if (!__all_sync(0xffffffffu, come)) return false;
+    const int id = ids[k % kIds];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&id_empty[k % kIds]);
+    if (id < 0) return false;
+    item(id, it);
+    return true;
+  };
+
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 0 && lane == 0 && steps > 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0 && lane == 0) {
       // ===================== loads: Q; K of the last tile; then K of the next and V of this one, in turn
-      mbar_arrive_expect_tx(q_full, 2 * F::kTile);
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int d = 0; d < F::kSlabs; ++d)
-          tma_load_3d(&tmQ, sQ + m * F::kTile + d * 16384, q_full, 64 * d, h0, s.q0 + i0 + m * per);
-      int unit = 0, issued = 0;
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      int unit = 0, issued = 0, queries = 0;
       uint32_t phase = 0;
       bool ok = true;
-      auto load = [&](const CUtensorMap* map, int tile) {
-        if (!ok || !(ok = mbar_wait(&empty[unit], phase ^ 1, abort, kTimeoutNs, a.status))) return;
-        mbar_arrive_expect_tx(&full[unit], F::kTile);
+      auto take = [&] { return (int)gridDim.x + atomicAdd(p.queue, 1); };
+      Item it;
+      for (int k = 0, id = blockIdx.x; ok; ++k) {
+        if (!(ok = mbar_wait(&id_empty[k % kIds], (k / kIds & 1) ^ 1, abort, kTimeoutNs, a.status))) break;
+        ids[k % kIds] = id < items ? id : -1;
+        mbar_arrive(&id_full[k % kIds]);
+        if (id >= items) break;
+        item(id, it);
+        const int steps = it.steps(), hk = it.h0 / a.group;
+        if (steps == 0) {
+          id = take();
+          continue;
+        }
+        if (!(ok = mbar_wait(q_empty, (queries & 1) ^ 1, abort, kTimeoutNs, a.status))) break;
+        ++queries;
+        mbar_arrive_expect_tx(q_full, 2 * F::kTile);
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int d = 0; d < F::kSlabs; ++d)
-          tma_load_3d(map, sKV + unit * F::kTile + d * 16384, &full[unit], 64 * d, hk, s.k0 + tile * BK);
-        ++issued;
-        if (++unit == kUnits) unit = 0, phase ^= 1;
-      };
-      load(&tmK, steps - 1);
-      for (int j = steps - 1; j >= 0 && ok; --j) {
-        if (j > 0) load(&tmK, j - 1);
-        load(&tmV, j);
+          for (int d = 0; d < F::kSlabs; ++d)
+            tma_load_3d(&tmQ, sQ + m * F::kTile + d * 16384, q_full, 64 * d, it.h0, it.s.q0 + it.i0 + m * per);
+        auto load = [&](const CUtensorMap* map, int tile) {
+          if (!ok || !(ok = mbar_wait(&empty[unit], phase ^ 1, abort, kTimeoutNs, a.status))) return;
+          mbar_arrive_expect_tx(&full[unit], F::kTile);
+#pragma unroll
+          for (int d = 0; d < F::kSlabs; ++d)
+            tma_load_3d(map, sKV + unit * F::kTile + d * 16384, &full[unit], 64 * d, hk, it.s.k0 + tile * BK);
+          ++issued;
+          if (++unit == kUnits) unit = 0, phase ^= 1;
+        };
+        load(&tmK, steps - 1);
+        for (int j = steps - 1; j >= 0 && ok; --j) {
+          if (j == min(steps - 1, 1)) id = take();
+          if (j > 0) load(&tmK, j - 1);
+          load(&tmV, j);
+        }
       }
+      // the last CTA leaves the queue as it was
+      __threadfence();
+      if (ok && atomicAdd(p.queue + 1, 1) == (int)gridDim.x - 1) p.queue[0] = p.queue[1] = 0;
       // leave no copy in flight
-      mbar_wait_drain(q_full, 0, kTimeoutNs, a.status);
+      if (queries > 0) mbar_wait_drain(q_full, (queries - 1) & 1, kTimeoutNs, a.status);
       for (int i = 0; i < min(issued, kUnits); ++i) {
         const int u = (unit - 1 - i + 2 * kUnits) % kUnits;
         mbar_wait_drain(&full[u], unit - 1 - i < 0 ? phase ^ 1 : phase, kTimeoutNs, a.status);
       }
-    } else if (warp == 1 && steps > 0) {
+    } else if (warp == 1) {
       // ===================== products
       const uint32_t idesc_s = idesc_make(1, 128, BK);
       const uint32_t idesc_o = idesc_make(1, 128, DP) | (1u << 16);  // V is read MN-major
       int unit = 0;
-      uint32_t phase = 0;
-      auto wait_unit = [&] {
-        const bool ok = mbar_wait(&full[unit], phase, abort, kTimeoutNs, a.status);
-        return __all_sync(0xffffffffu, ok);
+      uint32_t phase = 0, q_phase = 0, p_phase = 0, o_phase = 0;  // the latter two a bit for each row tile
+      const bool one = lane == 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = mbar_wait(bar, parity, abort, kTimeoutNs, a.status);
+        return (bool)__all_sync(0xffffffffu, ok);
       };
       auto next = [&](int& u) {
+        if (!wait(&full[unit], phase)) return false;
         u = unit;
         if (++unit == kUnits) unit = 0, phase ^= 1;
+        return true;
       };
-      const bool one = lane == 0;
       auto scores = [&](int m, int u) {  // S_m = Q_m K^T
         const uint32_t qa = uniform(k_desc(smem_addr(sQ + m * F::kTile))), ka = uniform(k_desc(smem_addr(sKV + u * F::kTile)));
 #pragma unroll
@@ -157,35 +219,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit(&s_full[m], one);
       };
-      bool ok = mbar_wait(q_full, 0, abort, kTimeoutNs, a.status);
-      ok = __all_sync(0xffffffffu, ok) && wait_unit();
-      if (ok) {
-        tc_fence_after();
+      bool ok = true;
+      Item it;
+      for (int k = 0; ok && taken(k, it); ++k) {
+        const int steps = it.steps(), keys = it.s.m;
+        if (steps == 0) continue;
         int uk, uv;
-        next(uk);
+        if (!(ok = wait(q_full, q_phase) && next(uk))) break;
+        q_phase ^= 1;
+        tc_fence_after();
         for (int m = 0; m < 2; ++m)
-          if (tiles_of(m) == steps) scores(m, uk);
+          if (it.of(m) == steps) scores(m, uk);
         commit(&empty[uk], one);
+        if (steps == 1) commit(q_empty, one);
         for (int j = steps - 1; j >= 0; --j) {
-          if (j > 0) {
-            if (!(ok = wait_unit())) break;
-            next(uk);
-          }
-          if (!(ok = wait_unit())) break;
-          next(uv);
-          if ((j + 1) * BK > s.m) clear_rows(sKV + uv * F::kTile, F::kSlabs, BK, s.m - j * BK, lane);
+          if (j > 0 && !(ok = next(uk))) break;
+          if (!(ok = next(uv))) break;
+          if ((j + 1) * BK > keys) clear_rows(sKV + uv * F::kTile, F::kSlabs, BK, keys - j * BK, lane);
           tc_fence_after();
           for (int m = 0; m < 2 && ok; ++m) {
-            const int n = tiles_of(m);
+            const int n = it.of(m);
             if (j < n) {
-              ok = mbar_wait(&p_full[m], (n - 1 - j) & 1, abort, kTimeoutNs, a.status);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
+              if (!(ok = wait(&p_full[m], p_phase >> m & 1))) break;
+              p_phase ^= 1u << m;
+              if (j == n - 1) {  // O of the item before has been read
+                if (!(ok = wait(&o_free[m], (o_phase >> m & 1) ^ 1))) break;
+                o_phase ^= 1u << m;
+              }
               tc_fence_after();
               const uint32_t va = uniform(mn_desc(smem_addr(sKV + uv * F::kTile)));
 #pragma unroll
-              for (int k = 0; k < BK / 16; ++k)  // O_m += P_m V
-                mma_ts(tO + DP * m, tS + 128 * m + 8 * k, va + (2048 / 16) * k, idesc_o, j < n - 1 || k > 0, one);
+              for (int q = 0; q < BK / 16; ++q)  // O_m += P_m V
+                mma_ts(tO + DP * m, tS + 128 * m + 8 * q, va + (2048 / 16) * q, idesc_o, j < n - 1 || q > 0, one);
               if (j == 0) commit(&o_full[m], one);
             }
             if (j > 0 && j - 1 < n) scores(m, uk);
@@ -193,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           commit(&empty[uv], one);
           if (j > 0) commit(&empty[uk], one);
+          if (j == 1) commit(q_empty, one);
         }
       }
       __syncwarp();
@@ -203,51 +269,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    // ===================== softmax of tile m, a thread a row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int m = warp / 4 - 1, quarter = warp & 3;
-    const int row = quarter * 32 + lane, i = i0 + m * per + row / p.pack, h = h0 + row % p.pack;
-    const int n = tiles_of(m);
+    // ===================== softmax of row tile m, a thread a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int m = warp / 4 - 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t my_s = tS + 128 * m + lanes, my_o = tO + DP * m + lanes;
-    const int seen = visible(a, s, i);                               // of this row
-    const int least = visible(a, s, i0 + m * per);                   // of the tile's first row
-    Running w;
-    bool ok = true;
-    for (int j = n - 1; j >= 0; --j) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[m], (n - 1 - j) & 1, abort, kTimeoutNs, a.status)))) break;
-      tc_fence_after();
-      softmax_step<DP>(my_s, my_o, p.c, (j + 1) * BK > least ? seen - j * BK : BK, j < n - 1, w);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[m]);
-    }
-    // ===================== O / sum and the log sum
-    const float sum = w.sum0 + w.sum1, top = w.top;
-    if (n > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(&o_full[m], 0, abort, kTimeoutNs, a.status));
-    tc_fence_after();
-    const bool live = ok && i < s.n;
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (int64_t)(s.q0 + i) * a.ld_o + (int64_t)h * a.D;
-#pragma unroll
-    for (int q = 0; q < DP / 32; ++q) {
-      uint32_t o[32];
+    uint32_t s_phase = 0, o_phase = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool ok = mbar_wait(bar, parity, abort, kTimeoutNs, a.status);
+      return (bool)__all_sync(0xffffffffu, ok);
+    };
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+      int n, seen, least, q_row, h;  // key tiles; keys that this row and that the tile's first row see; the row (-1: none)
+      {
+        Item it;
+        if (!taken(k, it)) break;
+        const int i = it.i0 + m * per + row / p.pack;
+        n = it.of(m);
+        seen = visible(a, it.s, i);
+        least = visible(a, it.s, it.i0 + m * per);
+        q_row = i < it.s.n ? it.s.q0 + i : -1;
+        h = it.h0 + row % p.pack;
+      }
+      Running w;
+      bool ok = true;
+#pragma unroll 1
+      for (int j = n - 1; j >= 0; --j) {
+        if (!(ok = wait(&s_full[m], s_phase))) break;
+        s_phase ^= 1;
+        tc_fence_after();
+        softmax_step<DP>(my_s, my_o, p.c, (j + 1) * BK > least ? seen - j * BK : BK, j < n - 1, w);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[m]);
+      }
+      // ===================== O / sum and the log sum
+      const float sum = w.sum0 + w.sum1, top = w.top;
       if (n > 0) {
-        tmem_ld32(my_o + 32 * q, o);
-        tmem_ld_wait();
+        if (!ok || !wait(&o_full[m], o_phase)) break;
+        o_phase ^= 1;
+        tc_fence_after();
       }
+      const bool live = q_row >= 0;
+      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (int64_t)q_row * a.ld_o + (int64_t)h * a.D;
 #pragma unroll
-      for (int l = 0; l < 32; l += 8) {
-        float v[8];
+      for (int q = 0; q < DP / 32; ++q) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(my_o + 32 * q, o);
+          tmem_ld_wait();
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = sum == 0.0f ? 0.0f : __uint_as_float(o[l + e]) * f;  // no key: a row of zeros
-        if (live && 32 * q + l < a.D)
-          *reinterpret_cast<uint4*>(dst + 32 * q + l) =
-              make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+        for (int l = 0; l < 32; l += 8) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = sum == 0.0f ? 0.0f : __uint_as_float(o[l + e]) * f;  // no key: a row of zeros
+          if (live && 32 * q + l < a.D)
+            *reinterpret_cast<uint4*>(dst + 32 * q + l) =
+                make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+        }
       }
+      if (n > 0) {  // O may be written again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[m]);
+      }
+      if (live)
+        a.lse[(int64_t)h * a.Tq + q_row] = sum == 0.0f ? -INFINITY : (top * p.c + log2f(sum)) * kLn2;
     }
-    if (live)
-      a.lse[(int64_t)h * a.Tq + s.q0 + i] = sum == 0.0f ? -INFINITY : (top * p.c + log2f(sum)) * kLn2;
     tc_fence_before();
   }
   __syncthreads();
@@ -256,8 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DP>
-cudaError_t forward(const AttnArgs& a, TilePlan* plan, cudaStream_t s) {
+cudaError_t forward(const AttnArgs& a, TilePlan* plan, int* first, int* queue, cudaStream_t s) {
   FwdParams p{a, heads_packed(a.group), a.scale * kLog2e};
+  p.queue = queue;
   p.tiles = (int)forward_tiles(a);
   p.heads = a.Hq / p.pack;
   p.chunk = head_chunk((int64_t)a.Tk * a.D * 4, a.Hkv) * (a.group / p.pack);
@@ -273,11 +365,11 @@ cudaError_t forward(const AttnArgs& a, TilePlan* plan, cudaStream_t s) {
   static const cudaError_t e =
       cudaFuncSetAttribute(attn_forward_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fwd<DP>::kBytes);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)p.tiles * p.heads;
+  const unsigned grid = (unsigned)min((int64_t)tc::num_sms(), (int64_t)p.tiles * p.heads);
   // one sequence's tiles are in the order of their work as they are
-  if (a.B > 1 && a.B <= kPlanMaxB) {
+  if (a.B > 1) {
     p.plan = plan;
-    const cudaError_t l = launch_plan(a, PlanJob{0, 256 / p.pack, 0, 0, p.heads, 0, p.tiles, plan}, s);
+    const cudaError_t l = launch_plan(a, PlanJob{0, 256 / p.pack, 0, 0, p.heads, 0, p.tiles, plan, first}, s);
     if (l != cudaSuccess) return l;
     return launch_after_smem(attn_forward_kernel<DP>, grid, kThreads, Fwd<DP>::kBytes, s, q, k, v, p);
   }
@@ -289,8 +381,8 @@ cudaError_t forward(const AttnArgs& a, TilePlan* plan, cudaStream_t s) {
 
 int64_t forward_tiles(const AttnArgs& a) { return a.Tq / (256 / heads_packed(a.group)) + a.B; }
 
-cudaError_t launch_tc(const AttnArgs& a, TilePlan* plan, cudaStream_t s) {
-  return a.D <= 64 ? forward<64>(a, plan, s) : forward<128>(a, plan, s);
+cudaError_t launch_tc(const AttnArgs& a, TilePlan* plan, int* first, int* queue, cudaStream_t s) {
+  return a.D <= 64 ? forward<64>(a, plan, first, queue, s) : forward<128>(a, plan, first, queue, s);
 }
 
 }  // namespace attn

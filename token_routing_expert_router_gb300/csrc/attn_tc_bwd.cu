@@ -44,7 +44,7 @@ struct BwdParams {
   int pack;   // query heads in a tile
   float c;    // scale log2(e)
   int tiles, heads, chunk;  // the grid: tiles (at most), packs of heads or key heads, those that share the L2
-  const TilePlan* plan;     // NULL: tiles in their order
+  const TilePlan* plan;
   const float *neg_lse, *neg_delta;
   float* part;
   uint32_t* tickets;
@@ -116,24 +116,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int h0 = DKV ? hk * a.group : at.head * p.pack;  // first query head
   let_next_begin();
   after_previous();
-  TileEntry e;
-  if (p.plan) {
-    if (at.rank >= p.plan->count) return;
-    e = p.plan->tile[at.rank];
-  } else {
-    const Tile t = find_tile<kThreads, DKV>(a, at.rank, DKV ? R : per, true, blockIdx.x == 0, reinterpret_cast<int*>(smem));
-    if (t.b < 0) return;
-    const Seq q = load_seq(a, t.b, true, false);
-    e = TileEntry{q.q0, q.n, q.k0, q.m, DKV ? t.index * R : (t.count - 1 - t.index) * per, 0, 0, 0};
-  }
+  if (at.rank >= p.plan->count) return;
+  const TileEntry e = p.plan->tile[at.rank];
   const Seq s{e.q0, e.n, e.k0, e.m};
   const int o0 = e.start;  // the outer tile's first key or query
   // inner tiles: of queries, from the first one that sees key o0, for one pack of heads after the other;
   // or of keys
   const int first = DKV && a.causal ? max(0, o0 - (s.m - s.n)) / per : 0;
-  const int tiles = DKV ? max(0, (s.n + per - 1) / per - first)
-                        : (max(0, visible(a, s, min(o0 + per, s.n) - 1)) + R - 1) / R;
-  const int from = p.plan ? e.lo : 0, steps = p.plan ? e.hi - e.lo : DKV ? tiles * (a.group / p.pack) : tiles;
+  const int tiles = max(0, (s.n + per - 1) / per - first);
+  const int from = e.lo, steps = e.hi - e.lo;
   struct Inner {  // walks over them
     int tile, head;
   };
@@ -513,25 +504,24 @@ cudaError_t backward(const AttnArgs& a, const BackwardSpace& w, cudaStream_t s) 
   // without queries or keys nothing of them is loaded
   if (a.Tq == 0) q = o = k;
   if (a.Tk == 0) k = v = q;
-  const bool plan = a.B <= kPlanMaxB;
   const int packs = a.group / p.pack, per = R / p.pack;
-  const PlanJob dq{0, per, 0, 0, a.Hq / p.pack, 0, (int)dq_tiles(a), w.dq_plan};
-  const PlanJob dkv{1, 0, per, packs, a.Hkv, kPieces, (int)(a.Tk / R + a.B), w.dkv_plan};
-  cudaError_t e = launch_plan_backward(a, dq, dkv, StatsJob{p.pack, w.neg_lse, w.neg_delta}, plan, s);
+  const PlanJob dq{0, per, 0, 0, a.Hq / p.pack, 0, (int)dq_tiles(a), w.dq_plan, w.first};
+  const PlanJob dkv{1, 0, per, packs, a.Hkv, kPieces, (int)(a.Tk / R + a.B), w.dkv_plan, w.first + a.B + 1};
+  cudaError_t e = launch_plan_backward(a, dq, dkv, StatsJob{p.pack, w.neg_lse, w.neg_delta}, s);
   if (e != cudaSuccess) return e;
   p.neg_lse = w.neg_lse, p.neg_delta = w.neg_delta, p.part = w.part, p.tickets = w.tickets;
   if (a.Tq > 0) {
     p.tiles = (int)dq_tiles(a);
     p.heads = a.Hq / p.pack;
     p.chunk = head_chunk((int64_t)a.Tk * a.D * 4, a.Hkv) * packs;
-    p.plan = plan ? w.dq_plan : nullptr;
+    p.plan = w.dq_plan;
     if ((e = launch<DP, false>(q, k, v, o, p, s)) != cudaSuccess) return e;
   }
   if (a.Tk == 0) return cudaSuccess;
-  p.tiles = (int)(plan ? dkv_tiles(a) : a.Tk / R + a.B);
+  p.tiles = (int)dkv_tiles(a);
   p.heads = a.Hkv;
   p.chunk = head_chunk((int64_t)a.Tq * a.group * a.D * 4, a.Hkv);
-  p.plan = plan ? w.dkv_plan : nullptr;
+  p.plan = w.dkv_plan;
   return launch<DP, true>(q, k, v, o, p, s);
 }
 

@@ -15,7 +15,8 @@ int num_sms();  // of the current device (gemm_tc.cu)
 // each returns to what the next call expects, whatever call shared the workspace before.
 constexpr size_t kClipState = 1024;   // grad_clip.cu's ticket and scale
 constexpr size_t kHeadTicket = 1152;  // head_loss.cu's ticket
-constexpr size_t kAttnTickets = 2048; // attention's tickets, up to 512
+constexpr size_t kAttnTickets = 2048; // attention's tickets, up to 456
+constexpr size_t kAttnQueue = 3968;   // attn_tc.cu's queue
 
 // Programmatic dependent launch inside a call: a kernel launched with launch_after may be set
 // up while the one before it in the stream still runs, and calls after_previous() before it
@@ -109,6 +110,7 @@ struct AttnScratch {  // workspace offsets, after the status head
   size_t delta;                            // backward, on the FMA units
   size_t neg_lse, neg_delta, dq_plan, dkv_plan;  // backward, on the tensor cores
   size_t plan;                             // forward, tiles
+  size_t first;                            // of either plan
   size_t stat;                             // forward, few rows over many keys
   size_t part;                             // parts of either
   size_t total;
