@@ -132,7 +132,7 @@ struct BackwardSpace {
   float* part;        // [kMostPieces][2][128][DP]: dk and dv of pieces of a tile
   uint32_t* tickets;  // [kMostPieces], zero between calls
 };
-constexpr int kPieces = 228;               // wanted of all tiles of dk and dv: 1.5 for every SM
+constexpr int kPieces = 228;               // a cut tile of dk and dv has at most this share of all their work
 constexpr int kMostPieces = 2 * kPieces;   // of tiles that are cut
 cudaError_t launch_tc_backward(const AttnArgs& a, const BackwardSpace& w, cudaStream_t s);
 // Entries of the plans.

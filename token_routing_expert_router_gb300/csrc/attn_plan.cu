@@ -85,9 +85,9 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
   atomicAdd(&sTotal, (unsigned long long)sum);
   atomicMax(&sMost, most);
   __syncthreads();
-  // a piece is at most a CTA's part of 1.5 rounds
+  // a piece is at most what a CTA has of all the work, and worth its ends
   int limit = 0x7fffffff;
-  if (j.pieces > 0) limit = max(8, (int)min((unsigned long long)0x7fffffff, (sTotal * j.heads + j.pieces - 1) / j.pieces));
+  if (j.pieces > 0) limit = max(16, (int)min((unsigned long long)0x7fffffff, (sTotal * j.heads + j.pieces - 1) / j.pieces));
   const int top = max(1, min(sMost, limit));
   auto cut = [&](int n) { return n > limit ? (n + limit - 1) / limit : 1; };
   auto cls = [&](int n) { return kClasses - 1 - min(kClasses - 1, (int)((int64_t)n * (kClasses - 1) / top)); };  // 0: the longest
@@ -122,25 +122,36 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
 template <int LANES>
 __device__ void row_stats(const AttnArgs& a, const StatsJob& j, int64_t block, int64_t blocks) {
   constexpr int kPer = kSort / LANES;
-  const int lane = threadIdx.x % LANES;
-  const int64_t all = (int64_t)a.Tq * a.Hq;
+  const int lane = threadIdx.x % LANES, shift = __ffs(j.pack) - 1;
   const bool in = 8 * lane < a.D;
-  for (int64_t i0 = block * kPer * kAhead + threadIdx.x / LANES; i0 < all; i0 += blocks * kPer * kAhead) {
+  // pairs (row, head) of this thread: `by` apart, from the first one on
+  const int64_t first = block * kPer + threadIdx.x / LANES, by = blocks * kPer;
+  const int by_rows = (int)(by / a.Hq), by_heads = (int)(by % a.Hq);
+  int64_t row = first / a.Hq;
+  int h = (int)(first % a.Hq);
+  while (__any_sync(0xffffffffu, row < a.Tq)) {  // a warp has several rows, and its lanes stay together
     uint4 x[kAhead], y[kAhead];
+    float l[kAhead];
+    int64_t rows[kAhead];
+    int heads[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int64_t i = i0 + u * kPer;
+      rows[u] = row, heads[u] = h;
       x[u] = y[u] = make_uint4(0, 0, 0, 0);
-      if (i < all && in) {
-        const int64_t row = (uint64_t)all < (1ull << 32) ? (uint32_t)i / (uint32_t)a.Hq : i / a.Hq;
-        const int64_t at = row * a.ld_o + (i - row * a.Hq) * a.D + 8 * lane;
-        x[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + at);
-        y[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_o) + at);
+      l[u] = 0.0f;
+      if (row < a.Tq) {
+        if (in) {
+          const int64_t at = row * a.ld_o + (int64_t)h * a.D + 8 * lane;
+          x[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + at);
+          y[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.d_o) + at);
+        }
+        if (lane == 0) l[u] = a.lse[(int64_t)h * a.Tq + row];
       }
+      row += by_rows, h += by_heads;
+      if (h >= a.Hq) h -= a.Hq, ++row;
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int64_t i = i0 + u * kPer;
       const __nv_bfloat162 *xs = reinterpret_cast<const __nv_bfloat162*>(&x[u]), *ys = reinterpret_cast<const __nv_bfloat162*>(&y[u]);
       float dot = 0.0f;
 #pragma unroll
@@ -150,12 +161,9 @@ __device__ void row_stats(const AttnArgs& a, const StatsJob& j, int64_t block, i
       }
 #pragma unroll
       for (int off = LANES / 2; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-      if (lane == 0 && i < all) {
-        const int64_t row = (uint64_t)all < (1ull << 32) ? (uint32_t)i / (uint32_t)a.Hq : i / a.Hq;
-        const int h = (int)(i - row * a.Hq);
-        const int64_t at = (h / j.pack * (int64_t)a.Tq + row) * j.pack + h % j.pack;
-        const float l = a.lse[(int64_t)h * a.Tq + row];
-        j.neg_lse[at] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row without keys: exp2(s - inf) = 0
+      if (lane == 0 && rows[u] < a.Tq) {
+        const int64_t at = (((int64_t)(heads[u] >> shift) * a.Tq + rows[u]) << shift) + (heads[u] & (j.pack - 1));
+        j.neg_lse[at] = l[u] == -INFINITY ? -INFINITY : -l[u] * kLog2e;  // a row without keys: exp2(s - inf) = 0
         j.neg_delta[at] = -dot;
       }
     }
