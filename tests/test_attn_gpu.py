@@ -167,11 +167,17 @@ class Batch:
                     edp = 2 * (self.D + 8) * U * (do.abs() @ v.abs().t())
                     ed = (do.abs() * eo).sum(1, keepdim=True) + 2 * (self.D + 8) * U * (do * o).abs().sum(1, keepdim=True)
                     ds = p * (dp - delta)
+                    first = ed
+                    if self.dt == BF:
+                        # the first delta is put right by the sum of a row's ds: what remains is the error of
+                        # the sum of p dp, and nothing of o's rounding
+                        ed = (p * (ep * dp.abs() + edp)).sum(1, keepdim=True) + acc * (p * dp.abs()).sum(1, keepdim=True)
                     eds = p * (edp + ed) + ds.abs() * (ep + half + 4 * U) + p * 4 * U * (dp.abs() + delta.abs())
                     # flushed: p (times dp - delta), and ds itself
                     eds = eds * (1 + half) + FTZ * (dp.abs() + delta.abs() + 1)
                     want = self.scale * ds @ k
-                    lost = self.scale * ((eds + acc * ds.abs()) @ k.abs())
+                    # dq's own ds have the first delta, and are rounded with it; so is the mean key that takes it back
+                    lost = self.scale * ((eds + acc * ds.abs() + 2 * (half + acc) * p * first) @ k.abs())
                     within(dq[rq, h], want, lost + HALF[self.dt] * (want.abs() + lost) + 4 * U * want.abs() + FTZ)
                     wv += p.t() @ do
                     bv += (p * (ep + half + acc) + FTZ).t() @ do.abs()

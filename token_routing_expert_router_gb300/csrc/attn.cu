@@ -58,7 +58,7 @@ AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward) {
   };
   const bool tensor_cores = c.act_dtype == MOE_DTYPE_BF16 && c.D % 8 == 0;  // where rows are aligned
   const size_t DP = c.D <= 64 ? 64 : 128, rows = (size_t)c.Hq * c.Tq;
-  if (!tensor_cores || backward) s.delta = s.neg_delta = take(backward ? rows * sizeof(float) : 0);
+  if (backward) s.delta = s.neg_delta = take(rows * sizeof(float));
   if (tensor_cores && backward) {
     s.neg_lse = take(rows * sizeof(float));
     s.dq_plan = take(attn::plan_bytes(attn::dq_tiles(a)));
@@ -70,6 +70,9 @@ AttnScratch attn_scratch(const moe_attn_config_t& c, bool backward) {
     s.first = take((size_t)(c.B + 1) * sizeof(int));
     s.stat = take((size_t)2 * attn::kMaxStreamCtas * 128 * sizeof(float2));
     s.part = take((size_t)2 * attn::kMaxStreamCtas * 128 * DP * sizeof(float));
+  } else if (!backward && c.act_dtype == MOE_DTYPE_F32) {
+    s.stat = take((size_t)attn::kMostFewParts * 16 * sizeof(float2));
+    s.part = take((size_t)attn::kMostFewParts * 16 * c.D * sizeof(float));
   }
   s.total = at;
   return s;
@@ -79,9 +82,11 @@ cudaError_t launch_attn(const moe_attn_config_t& c, const void* q, const void* k
                         void* o, float* lse, void* ws, DeviceStatus* st, cudaStream_t s) {
   if (c.Tq == 0 || c.B == 0) return cudaSuccess;
   const attn::AttnArgs a = args_of(c, q, k, v, at, o, lse, st);
-  if (c.act_dtype != MOE_DTYPE_BF16 || !attn::tc_rows(a, false)) return attn::launch_simt(a, c.act_dtype == MOE_DTYPE_BF16, s);
   char* b = static_cast<char*>(ws);
   const AttnScratch L = attn_scratch(c, false);
+  if (c.act_dtype == MOE_DTYPE_F32 && attn::few_rule(a))
+    return attn::launch_few(a, reinterpret_cast<float2*>(b + L.stat), reinterpret_cast<float*>(b + L.part), s);
+  if (c.act_dtype != MOE_DTYPE_BF16 || !attn::tc_rows(a, false)) return attn::launch_simt(a, c.act_dtype == MOE_DTYPE_BF16, s);
   if (!attn::stream_rule(a)) return attn::launch_tc(a, reinterpret_cast<attn::TilePlan*>(b + L.plan),
                                                      reinterpret_cast<int*>(b + L.first), reinterpret_cast<int*>(b + kAttnQueue), s);
   return attn::launch_stream(a, {reinterpret_cast<uint32_t*>(b + kAttnTickets), reinterpret_cast<float2*>(b + L.stat),

@@ -123,6 +123,11 @@ struct StreamSpace {
 };
 bool stream_rule(const AttnArgs& a);
 cudaError_t launch_stream(const AttnArgs& a, const StreamSpace& w, cudaStream_t s);
+// Few rows over many keys, fp32: parts of lines, a line being 16 rows of a sequence and key head.
+constexpr int kFewParts = 304, kMostSplits = 64;  // parts wanted of all lines, two for every SM; of one, at most
+constexpr int kMostFewParts = 2 * kFewParts;      // where lines are cut at all
+bool few_rule(const AttnArgs& a);
+cudaError_t launch_few(const AttnArgs& a, float2* stat, float* part, cudaStream_t s);
 cudaError_t launch_simt(const AttnArgs& a, bool bf16, cudaStream_t s);
 // What the backward keeps in the workspace beside the statistics.
 struct BackwardSpace {

@@ -8,8 +8,10 @@
 // A block of 256 threads owns 64 query rows (dk, dv: 64 key rows) and goes over the other side in
 // tiles of 64, with the running maximum and sum of the softmax; scores are never stored. Every thread
 // forms 4 x 4 scores, and 4 rows x DP / 16 columns of the results in registers. Bound by FMA issue:
-// two 64 x 64 x D products a tile forward, five backward (in two kernels, which form the scores and
-// do . v twice; in return no result is added to by two blocks, so the bits never change).
+// two 64 x 64 x D products a tile forward, seven backward (in two kernels, which form the scores and
+// do . v twice; in return no result is added to by two blocks, so the bits never change). From bf16
+// tensors delta carries the rounding of o: their dq forms the mean key too and puts both right, as in
+// attn_tc_bwd.cu.
 #include "attn.cuh"
 
 namespace moe {
@@ -186,7 +188,13 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a
       for (int d = 0; d < DP / 16; ++d) acc[r][d] *= keep;
     }
     __syncwarp();  // a row's scores come from the 16 threads that use them
-    accumulate<DP>(acc, sP, sV, ty, tx);
+    // the tile's sums apart, so that a long row's do not lose more with every tile
+    float fresh[4][DP / 16] = {};
+    accumulate<DP>(fresh, sP, sV, ty, tx);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) acc[r][d] += fresh[r][d];
   }
   float f[4];
 #pragma unroll
@@ -211,6 +219,8 @@ __global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
   float* sK = sO + tile_floats<DP>();
   float* sV = sK + tile_floats<DP>();
   float* sP = sV + tile_floats<DP>();
+  float* sM = sP + R * PS;  // kRounded: P, for the mean key
+  constexpr bool kRounded = sizeof(T) == 2;
   const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   __shared__ int sFind[kThreads / 32 + 3];
   const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, true, blockIdx.x == 0 && h == 0, sFind);
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
     const bool live = 4 * ty + r < rows;
     st[r] = RowStat{live ? a.lse[at] : 0.0f, live ? a.delta[at] : 0.0f};
   }
-  float acc[4][DP / 16] = {};
+  float acc[4][DP / 16] = {}, mean[kRounded ? 4 : 1][DP / 16] = {}, lack[4] = {};
   const int keys = visible(a, s, i0 + rows - 1);
   for (int j0 = 0; j0 < keys; j0 += R) {
     __syncthreads();
@@ -241,12 +251,27 @@ __global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
     for (int r = 0; r < 4; ++r) {
       const int end = min(4 * ty + r < rows ? visible(a, s, i0 + 4 * ty + r) : 0, s.m) - j0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        sP[(4 * ty + r) * PS + tx + 16 * j] =
-            tx + 16 * j < end ? expf(c[r][j] - st[r].lse) * (dp[r][j] - st[r].delta) : 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        const float p = tx + 16 * j < end ? expf(c[r][j] - st[r].lse) : 0.0f;
+        const float ds = p == 0.0f ? 0.0f : p * (dp[r][j] - st[r].delta);
+        sP[(4 * ty + r) * PS + tx + 16 * j] = ds;
+        if constexpr (kRounded) sM[(4 * ty + r) * PS + tx + 16 * j] = p;
+        lack[r] += ds;
+      }
     }
     __syncwarp();
     accumulate<DP>(acc, sP, sK, ty, tx);
+    if constexpr (kRounded) accumulate<DP>(mean, sM, sK, ty, tx);
+  }
+  if constexpr (kRounded) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int off = 8; off; off >>= 1) lack[r] += __shfl_xor_sync(0xffffffffu, lack[r], off);
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) acc[r][d] = fmaf(-lack[r], mean[r][d], acc[r][d]);
+      if (tx == 0 && 4 * ty + r < rows) a.delta[(int64_t)h * a.Tq + s.q0 + i0 + 4 * ty + r] = st[r].delta + lack[r];
+    }
   }
   const float f[4] = {a.scale, a.scale, a.scale, a.scale};
   store_rows<T, DP>(head<T>(a.dq, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, acc, f, ty, tx);
@@ -346,7 +371,9 @@ template <typename T, int DP>
 cudaError_t backward(const AttnArgs& a, cudaStream_t s) {
   const size_t smem = (4 * tile_floats<DP>() + R * PS) * sizeof(float);
   cudaError_t e = cudaSuccess;
-  if (a.Tq > 0) e = launch_tiles<simt_dq_kernel<T, DP>>(dim3((unsigned)(a.Tq / R + a.B), a.Hq), smem, a, s);
+  if (a.Tq > 0)
+    e = launch_tiles<simt_dq_kernel<T, DP>>(dim3((unsigned)(a.Tq / R + a.B), a.Hq),
+                                            smem + (sizeof(T) == 2 ? R * PS * sizeof(float) : 0), a, s);
   if (e != cudaSuccess || a.Tk == 0) return e;
   return launch_tiles<simt_dkv_kernel<T, DP>>(dim3((unsigned)(a.Tk / R + a.B), a.Hkv), smem + R * PS * sizeof(float), a, s);
 }

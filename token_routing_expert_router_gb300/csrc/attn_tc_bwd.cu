@@ -3,10 +3,15 @@
 // memory (X1, X2 = K, V or Q, dO), inner tiles of 128 rows go by (Y1, Y2 = Q, dO or K, V), and
 //   S = X1 Y1^T,  dP = X2 Y2^T   (tensor memory)
 //   P = exp2(c S - lse2),  dS = P (dP - delta)   (bf16, over the columns of S and dP)
-//   [dV += P Y2]   dK or dQ += dS Y1
+//   dV += P Y2, dK += dS Y1;   M += P Y1, dQ += dS Y1
 // with rows of the outer tile as lanes of tensor memory, so that P and dS are first operands where they
 // are. Sums over the query heads of a group and over all queries stay in one accumulator: no atomics,
-// and the bits never change. In return S and dP are formed twice: seven products instead of five.
+// and the bits never change. In return S and dP are formed twice.
+//
+// M serves delta. It is the sum over the keys of P dP, and formed as d_o . o it carries the rounding of o
+// to bf16 and of P in the forward: where a row looks at few keys, dP - delta is small against both, and
+// gradients were off by up to 0.4 % for that alone (their own rounding: 0.17 %). The sum e of a row's dS
+// is what delta lacks, as the sum of P is 1: dq takes e M back, M the mean key, and leaves delta + e for dk.
 //
 // A tile of keys that meets very many queries is cut into pieces (attn_plan.cu): each leaves its sums in
 // the workspace, and the CTA that comes last (a ticket; it waits for nobody) adds them in their order.
@@ -45,7 +50,8 @@ struct BwdParams {
   float c;    // scale log2(e)
   int tiles, heads, chunk;  // the grid: tiles (at most), packs of heads or key heads, those that share the L2
   const TilePlan* plan;
-  const float *neg_lse, *neg_delta;
+  const float* neg_lse;
+  float* neg_delta;   // dq leaves it exact for dk
   float* part;
   uint32_t* tickets;
 };
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         advance(in);
         if (!(ok = all(mbar_wait(p_ready, parity, abort, kTimeoutNs, a.status)))) break;
         tc_fence_after();
-        if constexpr (DKV) products(tA2, tS, sY2 + u2 * F::kTile, i == 0);
+        products(tA2, tS, DKV ? sY2 + u2 * F::kTile : sY1 + u1 * F::kTile, i == 0);
         commit(&y2_empty[u2], one);
         if (i + 1 < steps) {
           if (!(ok = arrived(&y1_full[v1], ph1, sY1 + v1 * F::kTile, in))) break;
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 4; ++q) {
           const int r = 32 * q + lane;
           v[q] = r < live ? __ldg(p.neg_lse + base + r) : -INFINITY;
-          v[4 + q] = r < live ? __ldg(p.neg_delta + base + r) : 0.0f;
+          v[4 + q] = r < live ? p.neg_delta[base + r] : 0.0f;
         }
       };
       if (steps > 0) fetch();
@@ -303,12 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t my_s = tS + lanes + 64 * half, my_p = tP + lanes + 64 * half;
     // DKV: the row's key is o0 + row; else its query and head
     const int i_q = DKV ? 0 : o0 + row / p.pack, h = DKV ? 0 : h0 + row % p.pack;
-    float neg_lse = -INFINITY, neg_delta = 0.0f;
+    float neg_lse = -INFINITY, neg_delta = 0.0f, lack0 = 0.0f, lack1 = 0.0f;  // lack: what delta lacks, of this half
     int seen = 0;
+    const int64_t stat_at = ((int64_t)at.head * a.Tq + s.q0 + i_q) * p.pack + row % p.pack;
     if (!DKV && i_q < s.n) {
-      const int64_t x = ((int64_t)at.head * a.Tq + s.q0 + i_q) * p.pack + row % p.pack;
-      neg_lse = __ldg(p.neg_lse + x);
-      neg_delta = __ldg(p.neg_delta + x);
+      neg_lse = p.neg_lse[stat_at];
+      neg_delta = p.neg_delta[stat_at];
       seen = visible(a, s, i_q);
     }
     Inner in = begin();
@@ -323,11 +329,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(my_s, r[0]);
       tmem_ld32(my_s + 32, r[1]);
       tmem_ld_wait();
-      if constexpr (!DKV) {  // S may be formed again
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready);
-      }
       float pr[64];
 #pragma unroll
       for (int l = 0; l < 64; l += 4) {
@@ -349,20 +350,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int l = 0; l < 64; ++l)
             if (l < from) pr[l] = 0.0f;
         }
-        uint32_t w[32];
-#pragma unroll
-        for (int l = 0; l < 32; ++l) w[l] = pack2(pr[2 * l], pr[2 * l + 1]);
-        tmem_st32(my_s, w);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready);
       } else if (row0 + R > visible(a, s, o0)) {
         const int end = seen - row0 - 64 * half;
 #pragma unroll
         for (int l = 0; l < 64; ++l)
           if (l >= end) pr[l] = 0.0f;
       }
+      {
+        uint32_t w[32];
+#pragma unroll
+        for (int l = 0; l < 32; ++l) w[l] = pack2(pr[2 * l], pr[2 * l + 1]);
+        tmem_st32(my_s, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready);
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, b, abort, kTimeoutNs, a.status)))) break;
       tc_fence_after();
       tmem_ld32(my_p, r[0]);
@@ -383,6 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mul2(d[2], d[3], pr[l + 2], pr[l + 3]);
         w[l / 2] = pack2(d[0], d[1]);
         w[l / 2 + 1] = pack2(d[2], d[3]);
+        if constexpr (!DKV) {
+          add2(lack0, lack1, d[0], d[1]);
+          add2(lack0, lack1, d[2], d[3]);
+        }
       }
       tmem_st32(my_p, w);
       tmem_st_wait();
@@ -398,6 +405,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const bool live = ok && (DKV ? o0 + row < s.m : i_q < s.n);
     constexpr int kCols = DP / 2;
+    uint32_t turn = 0;
+    auto both_sync = [&] {  // of both warpgroups; false: given up
+      __syncwarp();
+      if (lane == 0) mbar_arrive(both);
+      const bool come = __all_sync(0xffffffffu, mbar_wait(both, turn, abort, kTimeoutNs, a.status));
+      turn ^= 1;
+      return come;
+    };
     auto store = [&](uint32_t from, void* base, int64_t at, float f) {
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(base) + at + kCols * half;
 #pragma unroll
@@ -437,14 +452,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(mine + which * R * DP + col + l) = make_uint4(o[l], o[l + 1], o[l + 2], o[l + 3]);
       }
       __threadfence();
-      uint32_t turn = 0;
-      auto both_sync = [&] {  // of both warpgroups; false: given up
-        __syncwarp();
-        if (lane == 0) mbar_arrive(both);
-        const bool come = __all_sync(0xffffffffu, mbar_wait(both, turn, abort, kTimeoutNs, a.status));
-        turn ^= 1;
-        return come;
-      };
       if (ok && both_sync()) {
         uint32_t* ticket = p.tickets + slot * p.heads + hk;
         if (half == 0 && row == 0) {
@@ -473,7 +480,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       store(tA1, a.dk, (int64_t)(s.k0 + o0 + row) * a.ld_k + (int64_t)hk * a.D, a.scale);
       store(tA2, a.dv, (int64_t)(s.k0 + o0 + row) * a.ld_v + (int64_t)hk * a.D, 1.0f);
     } else {
-      store(tA1, a.dq, (int64_t)(s.q0 + i_q) * a.ld_q + (int64_t)h * a.D, a.scale);
+      sStat[half * R + row] = lack0 + lack1;
+      ok = ok && both_sync();
+      const float lack = sStat[row] + sStat[R + row];
+      if (ok && half == 0 && i_q < s.n) p.neg_delta[stat_at] = neg_delta - lack;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + (int64_t)(s.q0 + i_q) * a.ld_q + (int64_t)h * a.D;
+#pragma unroll 1
+      for (int col = kCols * half; col < kCols * (half + 1); col += 16) {
+        uint32_t x[16] = {}, y[16] = {};
+        if (steps > 0) {
+          tmem_ld16(tA1 + lanes + col, x);
+          tmem_ld16(tA2 + lanes + col, y);
+          tmem_ld_wait();
+        }
+        float v[16];
+#pragma unroll
+        for (int l = 0; l < 16; ++l) v[l] = a.scale * fmaf(-lack, __uint_as_float(y[l]), __uint_as_float(x[l]));
+#pragma unroll
+        for (int l = 0; l < 16; l += 8)
+          if (live && ok && col + l < a.D)
+            *reinterpret_cast<uint4*>(dst + col + l) =
+                make_uint4(pack2(v[l], v[l + 1]), pack2(v[l + 2], v[l + 3]), pack2(v[l + 4], v[l + 5]), pack2(v[l + 6], v[l + 7]));
+      }
     }
     tc_fence_before();
   }
