@@ -7,7 +7,13 @@ supplies memory and the plain SGD update.
     y  = moe(n0)                             r  = x + gate * norm(y),  n1 = norm(r)   (one pass)
     loss = cross entropy(n1, table)          (the table is shared with the embedding)
 
-    python examples/train_step.py [steps]
+With query heads the layer stands behind an attention block: rotary positions, causal attention over
+packed documents and their backward are the library's, the two projections PyTorch's matrix products:
+
+    q, k, v = norm(x) w_qkv,  q, k = rope(q, k)
+    x <- x + attention(q, k, v) w_o          (in the pass that forms n0)
+
+    python examples/train_step.py [steps [heads]]
 """
 import os
 import sys
@@ -19,9 +25,10 @@ import token_routing_expert_router_gb300 as moe  # noqa: E402
 
 
 class Model:
-    """bf16 parameters, fp32 gradients, one workspace per operator; T tokens a step."""
+    """bf16 parameters, fp32 gradients, one workspace per operator; T tokens a step. heads: query
+    heads of an attention block in front of the layer, two to a key head (0: none)."""
 
-    def __init__(self, T=512, H=256, E=8, k=2, F=512, V=2000, seed=0):
+    def __init__(self, T=512, H=256, E=8, k=2, F=512, V=2000, seed=0, heads=0, D=64):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         bf, f32 = dict(device="cuda", dtype=torch.bfloat16), dict(device="cuda", dtype=torch.float32)
@@ -39,6 +46,23 @@ class Model:
         self.vectors = {"w_in": torch.ones(H, **f32), "w_post": torch.ones(H, **f32), "w_out": torch.ones(H, **f32),
                         "gate": torch.ones(H, **f32)}
 
+        self.heads, self.D = heads, D
+        if heads:
+            self.kv, self.width = max(1, heads // 2), (heads + 2 * max(1, heads // 2)) * D
+            self.proj = {"w_qkv": normal(self.width, H, std=0.05), "w_o": normal(H, heads * D, std=0.05)}
+            self.vectors["w_attn"] = torch.ones(H, **f32)
+            # documents of different lengths, one behind the other; positions count in each
+            self.starts = sorted({0, T // 2 + 1, T // 2 + T // 3, T - 1, T})
+            self.q_start = torch.tensor(self.starts, device="cuda", dtype=torch.int32)
+            self.pos = torch.cat([torch.arange(b - a, device="cuda", dtype=torch.int32)
+                                  for a, b in zip(self.starts, self.starts[1:])])
+            row = dict(ld_q=self.width, ld_k=self.width, ld_v=self.width)
+            self.attn = moe.MoEAttnConfig.make(Tq=T, Tk=T, B=len(self.starts) - 1, Hq=heads, Hkv=self.kv, D=D, **row)
+            self.rope = moe.MoERopeConfig.make(T=T, Hq=heads, Hk=self.kv, D=D, ld_q=self.width, ld_k=self.width,
+                                               ld_q_out=self.width, ld_k_out=self.width)
+            self.turns = torch.empty(D // 2, device="cuda", dtype=torch.int64)
+            moe.moe_rope_table(moe.MoERopeFreq.make(rot=D), self.turns)
+
         self.d_table = torch.empty(V, H, **f32)
         self.d_experts = {"dw_gate": torch.empty(E, F, H, **f32), "dw_up": torch.empty(E, F, H, **f32),
                           "dw_down": torch.empty(E, H, F, **f32), "dw_router": torch.empty(E, H, **f32),
@@ -47,6 +71,10 @@ class Model:
         grads = [self.d_table, *(v for v in self.d_experts.values() if torch.is_tensor(v)), *self.d_vectors.values()]
         params = [self.table, self.experts["w_gate"], self.experts["w_up"], self.experts["w_down"],
                   self.experts["w_router"], *self.vectors.values()]
+        if heads:
+            self.d_proj = {n: torch.empty(w.shape, **f32) for n, w in self.proj.items()}
+            grads += self.d_proj.values()
+            params += self.proj.values()
         self.updates = list(zip(params, grads))
         self.grads = moe.MoEGradList.from_tensors(grads)  # clipped in place
 
@@ -56,6 +84,12 @@ class Model:
         self.gu, self.dtopk = torch.empty(T * k, 2 * F, **bf), torch.empty(T, k, **f32)
         self.loss, self.lse, self.mean = torch.empty(T, **f32), torch.empty(T, **f32), torch.empty(2, **f32)
         self.aux, self.grad_norm = torch.empty(1, **f32), torch.empty(1, **f32)
+
+        if heads:
+            self.na, self.y0, self.x1, self.dx1, self.dy0, self.dna = (rows() for _ in range(6))
+            self.qkv, self.dqkv = torch.empty(T, heads + 2 * self.kv, D, **bf), torch.empty(T, heads + 2 * self.kv, D, **bf)
+            self.o, self.do = torch.empty(T, heads, D, **bf), torch.empty(T, heads, D, **bf)
+            self.attn_lse = torch.empty(heads, T, **f32)
 
         def workspace(size):
             ws = torch.empty(size, device="cuda", dtype=torch.uint8)
@@ -68,16 +102,56 @@ class Model:
         self.ws_embed = workspace(moe.moe_embed_workspace_size(self.embed))
         self.ws_head = workspace(moe.moe_head_workspace_size(self.head))
         self.ws_clip = workspace(moe.moe_grad_clip_workspace_size(self.grads))
+        self.spaces = [self.ws_layer, self.ws_back, self.ws_norm, self.ws_embed, self.ws_head, self.ws_clip]
+        if heads:
+            self.ws_attn = workspace(max(moe.moe_attn_workspace_size(self.attn), moe.moe_attn_backward_workspace_size(self.attn)))
+            self.spaces.append(self.ws_attn)
+
+    def split(self, qkv):
+        return qkv[:, :self.heads], qkv[:, self.heads:self.heads + self.kv], qkv[:, self.heads + self.kv:]
+
+    def attention(self):
+        """x -> x1 = x + attention, and n0 = norm(x1)."""
+        v = self.vectors
+        q, k, val = self.split(self.qkv)
+        moe.moe_block_norm(self.norm, self.x, None, None, v["w_attn"], None, self.na)
+        torch.mm(self.na, self.proj["w_qkv"].t(), out=self.qkv.view(len(self.na), -1))
+        moe.moe_rope(self.rope, q, k, None, self.pos, None, self.turns, q, k, None)
+        moe.moe_attn(self.attn, q, k, val, self.q_start, None, None, self.o, self.attn_lse, self.ws_attn)
+        torch.mm(self.o.view(len(self.o), -1), self.proj["w_o"].t(), out=self.y0)
+        moe.moe_block_norm(self.norm, self.x, self.y0, None, v["w_in"], self.x1, self.n0)
+
+    def attention_backward(self):
+        """dr (of x1) and dn0 -> dx (of x), and the block's own gradients."""
+        v, dv = self.vectors, self.d_vectors
+        T = len(self.x)
+        moe.moe_block_norm_backward(self.norm, self.x1, self.y0, None, v["w_in"], self.dr, self.dn0, self.dx1, self.dy0,
+                                    {"dw_next": dv["w_in"]}, self.ws_norm)
+        torch.mm(self.dy0, self.proj["w_o"], out=self.do.view(T, -1))
+        torch.mm(self.dy0.t().float(), self.o.view(T, -1).float(), out=self.d_proj["w_o"])
+        (q, k, val), (dq, dk, dval) = self.split(self.qkv), self.split(self.dqkv)
+        moe.moe_attn_backward(self.attn, q, k, val, self.q_start, None, None, self.o, self.attn_lse, self.do, dq, dk, dval,
+                              self.ws_attn)
+        moe.moe_rope_backward(self.rope, dq, dk, self.pos, self.turns, dq, dk)
+        dqkv = self.dqkv.view(T, -1)
+        torch.mm(dqkv.t().float(), self.na.float(), out=self.d_proj["w_qkv"])
+        torch.mm(dqkv, self.proj["w_qkv"], out=self.dna)
+        moe.moe_block_norm_backward(self.norm, self.x, None, None, v["w_attn"], self.dx1, self.dna, self.dx, None,
+                                    {"dw_next": dv["w_attn"]}, self.ws_norm)
 
     def step(self, tokens, targets, lr=0.3, max_norm=1.0):
         """One training step, stream-ordered; self.mean[0] is the loss, self.grad_norm the norm."""
         v, dv = self.vectors, self.d_vectors
         # forward
         moe.moe_embed(self.embed, self.table, tokens, self.x, self.ws_embed)
-        moe.moe_block_norm(self.norm, self.x, None, None, v["w_in"], None, self.n0)
+        if self.heads:
+            self.attention()
+        else:
+            moe.moe_block_norm(self.norm, self.x, None, None, v["w_in"], None, self.n0)
+        x = self.x1 if self.heads else self.x
         moe.moe_forward_train(self.layer, self.n0, self.experts, self.y, self.ws_layer, self.gu, aux_alpha=0.01,
                               aux_loss=self.aux)
-        moe.moe_block_norm(self.norm, self.x, self.y, v["w_post"], v["w_out"], self.r, self.n1, gate=v["gate"])
+        moe.moe_block_norm(self.norm, x, self.y, v["w_post"], v["w_out"], self.r, self.n1, gate=v["gate"])
         moe.moe_head_loss(self.head, self.n1, self.table, targets, self.loss, self.lse, self.mean, self.ws_head)
         # backward
         moe.moe_head_loss_backward(self.head, self.n1, self.table, targets, self.lse, self.dn1, self.d_table,
@@ -87,8 +161,11 @@ class Model:
                                     self.ws_norm, gate=v["gate"])
         moe.moe_backward_kept(self.layer, self.n0, self.experts, self.dy, self.ws_layer, self.gu, self.dn0, self.dtopk,
                               self.d_experts, self.ws_back)
-        moe.moe_block_norm_backward(self.norm, self.x, None, None, v["w_in"], self.dr, self.dn0, self.dx, None,
-                                    {"dw_next": dv["w_in"]}, self.ws_norm)
+        if self.heads:
+            self.attention_backward()
+        else:
+            moe.moe_block_norm_backward(self.norm, self.x, None, None, v["w_in"], self.dr, self.dn0, self.dx, None,
+                                        {"dw_next": dv["w_in"]}, self.ws_norm)
         # the table's second share joins the head's
         moe.moe_embed_backward(self.embed, tokens, self.dx, self.d_table, self.ws_embed, accumulate=True)
         moe.moe_grad_clip(self.grads, max_norm, self.grad_norm, self.ws_clip)
@@ -96,7 +173,7 @@ class Model:
             param.add_(grad, alpha=-lr)
 
     def check(self):
-        for ws in (self.ws_layer, self.ws_back, self.ws_norm, self.ws_embed, self.ws_head, self.ws_clip):
+        for ws in self.spaces:
             status = moe.moe_read_status(ws)
             if status != moe.MOE_OK:
                 raise moe.MoEError(status, "train_step")
@@ -115,8 +192,8 @@ def text(T, V, seed):
     return tokens.to(torch.int32), targets.to(torch.int32)
 
 
-def main(steps=200):
-    model = Model()
+def main(steps=200, heads=0):
+    model = Model(heads=heads)
     losses = []
     for i in range(steps):
         tokens, targets = text(model.layer.T, model.head.V, seed=100 + i)
@@ -130,4 +207,4 @@ def main(steps=200):
 
 if __name__ == "__main__":
     moe.build()
-    main(int(sys.argv[1]) if len(sys.argv) > 1 else 200)
+    main(*(int(v) for v in sys.argv[1:3]))

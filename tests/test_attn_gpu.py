@@ -335,3 +335,150 @@ def test_gradients_by_differences():
         inside = torch.where(grads[i] == 7, 0.0, grads[i].double())
         # differences lose h^2 times a third derivative of order 10; fp32 gradients 1e-5 of some dozens
         assert abs(slope - (inside * d).sum()) < 1e-3
+
+
+def test_positions_cache_and_attention_together():
+    """A prompt and ten tokens behind it, as a server runs them: rotated into a cache of pages that are
+    slots, one token a step - against the attention over the whole packed text at once."""
+    n, new, Hq, Hkv, D = 70, 10, 8, 2, 64
+    T, g = n + new, gen(21)
+    row = normal(g, T, Hq + 2 * Hkv, D, dtype=BF)
+    q, k, v = row[:, :Hq], row[:, Hq:Hq + Hkv], row[:, Hq + Hkv:]
+    table = torch.empty(D // 2, dtype=torch.int64, device="cuda")
+    moe.moe_rope_table(moe.MoERopeFreq.make(rot=D), table)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    ld = (Hq + 2 * Hkv) * D
+
+    def turn(lo, hi, k_out, v_out, slot, slots, ws):
+        cfg = moe.MoERopeConfig.make(T=hi - lo, Hq=Hq, Hk=Hkv, D=D, slots=slots, ld_q=ld, ld_k=ld, ld_v=ld)
+        out = torch.empty(hi - lo, Hq, D, device="cuda", dtype=BF)
+        moe.moe_rope(cfg, q[lo:hi], k[lo:hi], v[lo:hi], pos[lo:hi].clone(), slot, table, out, k_out, v_out, ws)
+        return out
+
+    # at once
+    kk, vv = torch.empty(T, Hkv, D, device="cuda", dtype=BF), torch.empty(T, Hkv, D, device="cuda", dtype=BF)
+    qq = turn(0, T, kk, vv, None, 0, None)
+    cfg = moe.MoEAttnConfig.make(Tq=T, Tk=T, B=1, Hq=Hq, Hkv=Hkv, D=D)
+    ws = workspace(moe.moe_attn_workspace_size(cfg))
+    start = torch.tensor([0, T], device="cuda", dtype=torch.int32)
+    o, lse = torch.empty_like(qq), torch.empty(Hq, T, device="cuda")
+    moe.moe_attn(cfg, qq, kk, vv, start, None, None, o, lse, ws)
+    # step by step: the text is the second of two slots regions
+    slots = 200
+    kc, vc = (poisoned(slots, Hkv, D, dtype=BF) for _ in range(2))
+    first = 100
+    for lo, hi in [(0, n)] + [(i, i + 1) for i in range(n, T)]:
+        slot = (torch.arange(lo, hi, device="cuda") + first).to(torch.int32)
+        qs = turn(lo, hi, kc, vc, slot, slots, ws)
+        c = moe.MoEAttnConfig.make(Tq=hi - lo, Tk=slots, B=1, Hq=Hq, Hkv=Hkv, D=D, max_q=hi - lo)
+        assert moe.moe_attn_workspace_size(c) <= ws.numel()
+        os_, ls = torch.empty_like(qs), torch.empty(Hq, hi - lo, device="cuda")
+        moe.moe_attn(c, qs, kc, vc, torch.tensor([0, hi - lo], device="cuda", dtype=torch.int32),
+                     torch.tensor([first], device="cuda", dtype=torch.int32),
+                     torch.tensor([hi], device="cuda", dtype=torch.int32), os_, ls, ws)
+        assert torch.equal(qs, qq[lo:hi])
+        # the same products and sums in another order: p rounded against another maximum, 2^-8 each
+        within(os_, o[lo:hi].double(), 2 * HALF[BF] * o[lo:hi].double().abs() + 2 * HALF[BF] * vv[:hi].double().abs().max())
+        within(ls, lse[:, lo:hi].double(), 2.0 ** -18 * (1 + lse[:, lo:hi].double().abs()))
+    assert torch.equal(kc[first:first + T], kk) and torch.equal(vc[first:first + T], vv)
+    assert moe.moe_read_status(ws) == moe.MOE_OK
+
+
+RUNS = [([(300, 300), (77, 77), (129, 129)], "self", 8, 2, 64, BF), ([(1, 500), (1, 900), (1, 3)], "cache", 8, 2, 128, BF),
+        ([(300, 300), (20, 20)], "self", 4, 2, 64, FP), ([(1, 500), (1, 900)], "cache", 8, 2, 128, FP)]
+
+
+@pytest.mark.parametrize("lens,place,Hq,Hkv,D,dt", RUNS)
+def test_captured_graphs_that_share_a_workspace(lens, place, Hq, Hkv, D, dt):
+    """Two graphs over the same workspace, replayed in turn on another stream, give the bits of direct calls."""
+    a, b = (Batch(lens, Hq, Hkv, D, dt, place=place, seed=s) for s in (1, 2))
+    b.ws, b.bws = a.ws, a.bws
+    want = [(x.forward(), x.backward(*x.forward())) for x in (a, b)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(side):
+        for x in (a, b):
+            graph = torch.cuda.CUDAGraph()
+            o, lse = torch.empty_like(want[0][0][0]), torch.empty_like(want[0][0][1])
+            grads = x.grads()
+            side.synchronize()
+            with torch.cuda.graph(graph, stream=side):
+                moe.moe_attn(x.cfg, x.q, x.k, x.v, x.q_start, x.k_start, x.k_len, o, lse, x.ws)
+                x.backward(o, lse, grads)
+            graphs.append(graph)
+            outs.append((o, lse, grads))
+        for _ in range(3):
+            for (o, lse, grads), graph in zip(outs, graphs):
+                o.fill_(7.0), lse.fill_(7.0)
+                for t in grads:
+                    t.fill_(7.0)
+                graph.replay()
+    torch.cuda.synchronize()
+    for (fwd, bwd), (o, lse, grads) in zip(want, outs):
+        assert torch.equal(o, fwd[0]) and torch.equal(lse, fwd[1])
+        assert all(torch.equal(x, y) for x, y in zip(grads, bwd))
+    a.check_status()
+
+
+@pytest.mark.parametrize("lens,place,Hq,Hkv,D,dt", RUNS)
+def test_calls_at_once_on_two_streams(lens, place, Hq, Hkv, D, dt):
+    """Calls that overlap, each with a stream and a workspace of its own."""
+    parts = [Batch(lens, Hq, Hkv, D, dt, place=place, seed=s) for s in (1, 2, 3)]
+    want = [(x.forward(), x.backward(*x.forward())) for x in parts]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in parts]
+    got = [None] * len(parts)
+    for _ in range(5):
+        for i, (x, s) in enumerate(zip(parts, streams)):
+            with torch.cuda.stream(s):
+                o, lse = x.forward()
+                got[i] = (o, lse, x.backward(o, lse))
+    torch.cuda.synchronize()
+    for (fwd, bwd), (o, lse, grads) in zip(want, got):
+        assert torch.equal(o, fwd[0]) and torch.equal(lse, fwd[1])
+        assert all(torch.equal(x, y) for x, y in zip(grads, bwd))
+
+
+@pytest.mark.parametrize("D,dt", [(64, BF), (128, BF), (128, FP)])
+def test_long_offsets(D, dt):
+    """Keys at the far end of a cache of more than 2^31 elements: the bits of the same keys in a small one."""
+    Hkv, m = 2, 700
+    rows = (1 << 31) // (Hkv * D) + 5000
+    size = rows * Hkv * D * (2 if dt == BF else 4)
+    if torch.cuda.mem_get_info()[0] < 3 * size:
+        pytest.skip("needs 3 times the cache")
+    b = Batch([(1, m), (3, m - 9)], 4, Hkv, D, dt, place="cache", seed=5)
+    o, lse = b.forward()
+    far = [torch.empty(rows, Hkv, D, device="cuda", dtype=dt) for _ in range(2)]
+    at = rows - b.Tk
+    far[0][at:], far[1][at:] = b.k, b.v
+    cfg = moe.MoEAttnConfig.make(**{**b.cfg.as_dict(), "Tk": rows})
+    o2, lse2 = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+    moe.moe_attn(cfg, b.q, far[0], far[1], b.q_start, b.k_start + at, b.k_len, o2, lse2, b.ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    b.check_status()
+
+
+def test_many_sequences():
+    """More sequences than threads, empty ones among them."""
+    lens = [(i % 3, i % 3) for i in range(3000)] + [(200, 200)]
+    for dt in (BF, FP):
+        b = Batch(lens, 2, 1, 16, dt, place="self", seed=9)
+        o, lse = b.forward()
+        grads = b.backward(o, lse)
+        b.check_status()
+        # the last sequence by the formulas, the sequences of one row: one key, its value
+        alone = Batch([(200, 200)], 2, 1, 16, dt, place="self", seed=9)
+        at = slice(b.used - 200, b.used)
+        for name in ("q", "k", "v", "do"):
+            getattr(alone, name)[:200] = getattr(b, name)[at]
+        o1, lse1 = torch.full((alone.Tq, 2, 16), 7.0, dtype=dt, device="cuda"), torch.full((2, alone.Tq), 7.0, device="cuda")
+        o1[:200], lse1[:, :200] = o[at], lse[:, at]
+        alone.check_forward(o1, lse1)
+        mine = alone.grads()
+        for x, y in zip(mine, grads):
+            x[:200] = y[at]
+        alone.check_backward(*mine)
+        ones = torch.tensor([b.q_at[i] for i, (n, _) in enumerate(lens) if n == 1], device="cuda")
+        assert torch.equal(o[ones], b.v[ones].expand(-1, 2, 16))
