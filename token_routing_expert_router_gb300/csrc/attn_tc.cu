@@ -210,8 +210,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++unit == kUnits) unit = 0, phase ^= 1;
         return true;
       };
-      auto scores = [&](int m, int u) {  // S_m = Q_m K^T
-        const uint32_t qa = uniform(k_desc(smem_addr(sQ + m * F::kTile))), ka = uniform(k_desc(smem_addr(sKV + u * F::kTile)));
+      const uint32_t q_desc = uniform(k_desc(smem_addr(sQ)));
+      auto scores = [&](int m, uint32_t ka) {  // S_m = Q_m K^T
+        const uint32_t qa = q_desc + m * (F::kTile / 16);
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint32_t off = (k / 4) * (16384 / 16) + (k % 4) * 2;
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_phase ^= 1;
         tc_fence_after();
         for (int m = 0; m < 2; ++m)
-          if (it.of(m) == steps) scores(m, uk);
+          if (it.of(m) == steps) scores(m, uniform(k_desc(smem_addr(sKV + uk * F::kTile))));
         commit(&empty[uk], one);
         if (steps == 1) commit(q_empty, one);
         for (int j = steps - 1; j >= 0; --j) {
@@ -237,7 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = next(uv))) break;
           if ((j + 1) * BK > keys) clear_rows(sKV + uv * F::kTile, F::kSlabs, BK, keys - j * BK, lane);
           tc_fence_after();
-          for (int m = 0; m < 2 && ok; ++m) {
+          // all that the products need is at hand before their P is waited for
+          const uint32_t va = uniform(mn_desc(smem_addr(sKV + uv * F::kTile))), ka = uniform(k_desc(smem_addr(sKV + uk * F::kTile)));
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (!ok) break;
             const int n = it.of(m);
             if (j < n) {
               if (!(ok = wait(&p_full[m], p_phase >> m & 1))) break;
@@ -247,13 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o_phase ^= 1u << m;
               }
               tc_fence_after();
-              const uint32_t va = uniform(mn_desc(smem_addr(sKV + uv * F::kTile)));
 #pragma unroll
               for (int q = 0; q < BK / 16; ++q)  // O_m += P_m V
                 mma_ts(tO + DP * m, tS + 128 * m + 8 * q, va + (2048 / 16) * q, idesc_o, j < n - 1 || q > 0, one);
               if (j == 0) commit(&o_full[m], one);
             }
-            if (j > 0 && j - 1 < n) scores(m, uk);
+            if (j > 0 && j - 1 < n) scores(m, ka);
           }
           if (!ok) break;
           commit(&empty[uv], one);

@@ -213,8 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto all = [&](bool ok) { return (bool)__all_sync(0xffffffffu, ok); };
       const bool one = lane == 0;
       // S or dP = X Y^T
-      auto scores = [&](uint32_t d, const uint8_t* x, const uint8_t* y, uint64_t* bar) {
-        const uint32_t xa = uniform(k_desc(smem_addr(x))), ya = uniform(k_desc(smem_addr(y)));
+      auto scores = [&](uint32_t d, uint32_t xa, uint32_t ya, uint64_t* bar) {
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint32_t off = (k / 4) * (16384 / 16) + (k % 4) * 2;
@@ -223,8 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(bar, one);
       };
       // acc += W Y, W in tensor memory: the columns' halves each at the start of their half of the scores
-      auto products = [&](uint32_t d, uint32_t w, const uint8_t* y, bool begin) {
-        const uint32_t ya = uniform(mn_desc(smem_addr(y)));
+      auto products = [&](uint32_t d, uint32_t w, uint32_t ya, bool begin) {
 #pragma unroll
         for (int k = 0; k < R / 16; ++k)
           mma_ts(d, w + (k / 4) * 64 + (k % 4) * 8, ya + (2048 / 16) * k, idesc_a, !begin || k > 0, one);
@@ -237,34 +235,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return true;
       };
+      const uint32_t x1 = uniform(k_desc(smem_addr(sX))), x2 = uniform(k_desc(smem_addr(sX + F::kTile)));
       int u1 = 0, u2 = 0;  // stages of the step
       uint32_t ph1 = 0, ph2 = 0;
       Inner in = begin();
       bool ok = all(mbar_wait(x_full, 0, abort, kTimeoutNs, a.status)) && arrived(y1_full, 0, sY1, in);
-      if (ok) scores(tS, sX, sY1, s_full);
+      if (ok) scores(tS, x1, uniform(k_desc(smem_addr(sY1))), s_full);
       ok = ok && arrived(y2_full, 0, sY2, in);
-      if (ok) scores(tP, sX + F::kTile, sY2, dp_full);
+      if (ok) scores(tP, x2, uniform(k_desc(smem_addr(sY2))), dp_full);
       for (int i = 0; i < steps && ok; ++i) {
         const uint32_t parity = i & 1;
         const int v1 = u1 + 1 == kN1 ? 0 : u1 + 1, v2 = u2 + 1 == kN2 ? 0 : u2 + 1;  // of the next step
         if (v1 == 0) ph1 ^= 1;
         if (v2 == 0) ph2 ^= 1;
         advance(in);
+        // all that the products need is at hand before what they wait for
+        const uint32_t y1 = uniform(mn_desc(smem_addr(sY1 + u1 * F::kTile))), y2 = uniform(mn_desc(smem_addr(sY2 + u2 * F::kTile)));
+        const uint32_t z1 = uniform(k_desc(smem_addr(sY1 + v1 * F::kTile))), z2 = uniform(k_desc(smem_addr(sY2 + v2 * F::kTile)));
         if (!(ok = all(mbar_wait(p_ready, parity, abort, kTimeoutNs, a.status)))) break;
         tc_fence_after();
-        products(tA2, tS, DKV ? sY2 + u2 * F::kTile : sY1 + u1 * F::kTile, i == 0);
+        products(tA2, tS, DKV ? y2 : y1, i == 0);
         commit(&y2_empty[u2], one);
         if (i + 1 < steps) {
           if (!(ok = arrived(&y1_full[v1], ph1, sY1 + v1 * F::kTile, in))) break;
-          scores(tS, sX, sY1 + v1 * F::kTile, s_full);
+          scores(tS, x1, z1, s_full);
         }
         if (!(ok = all(mbar_wait(ds_ready, parity, abort, kTimeoutNs, a.status)))) break;
         tc_fence_after();
-        products(tA1, tP, sY1 + u1 * F::kTile, i == 0);
+        products(tA1, tP, y1, i == 0);
         commit(&y1_empty[u1], one);
         if (i + 1 < steps) {
           if (!(ok = arrived(&y2_full[v2], ph2, sY2 + v2 * F::kTile, in))) break;
-          scores(tP, sX + F::kTile, sY2 + v2 * F::kTile, dp_full);
+          scores(tP, x2, z2, dp_full);
         }
         u1 = v1, u2 = v2;
       }
