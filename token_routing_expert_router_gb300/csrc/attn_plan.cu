@@ -75,15 +75,34 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
     }
     return lo;
   };
+  struct Found {
+    Seq s;
+    int index, steps;
+  };
+  auto find = [&](int t) {
+    const int b = seq_of(t);
+    Found f{load_seq(a, b, apart, false), t - sFirst[b], 0};
+    f.steps = tile_steps(a, j, f.s, f.index);
+    return f;
+  };
+  const Found own = tid < tiles ? find(tid) : Found{};  // the thread's first tile, for all three passes
+  auto tile = [&](int t) { return t == tid ? own : find(t); };
   int64_t sum = 0;
   int most = 0;
   for (int t = tid; t < tiles; t += kSort) {
-    const int b = seq_of(t), n = tile_steps(a, j, load_seq(a, b, apart, false), t - sFirst[b]);
+    const int n = tile(t).steps;
     sum += n;
     most = max(most, n);
   }
-  atomicAdd(&sTotal, (unsigned long long)sum);
-  atomicMax(&sMost, most);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+  }
+  if (lane == 0) {
+    atomicAdd(&sTotal, (unsigned long long)sum);
+    atomicMax(&sMost, most);
+  }
   __syncthreads();
   // a piece is at most what a CTA has of all the work, and worth its ends
   int limit = 0x7fffffff;
@@ -92,27 +111,31 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
   auto cut = [&](int n) { return n > limit ? (n + limit - 1) / limit : 1; };
   auto cls = [&](int n) { return kClasses - 1 - min(kClasses - 1, (int)((int64_t)n * (kClasses - 1) / top)); };  // 0: the longest
   for (int t = tid; t < tiles; t += kSort) {
-    const int b = seq_of(t), n = tile_steps(a, j, load_seq(a, b, apart, false), t - sFirst[b]), p = cut(n);
+    const int n = tile(t).steps, p = cut(n);
     atomicAdd(&sClass[cls((n + p - 1) / p)], p);
   }
   __syncthreads();
-  if (tid == 0) {
-    int at = 0;
-    for (int c = 0; c < kClasses; ++c) {
-      const int n = sClass[c];
-      sClass[c] = at;
-      at += n;
+  if (warp == 0) {  // where the classes begin: two to a lane
+    static_assert(kClasses == 64);
+    const int x = sClass[2 * lane], y = sClass[2 * lane + 1];
+    int inc = x + y;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
     }
-    j.plan->count = at;
+    sClass[2 * lane] = inc - x - y;
+    sClass[2 * lane + 1] = inc - y;
+    if (lane == 31) j.plan->count = inc;
   }
   __syncthreads();
   for (int t = tid; t < tiles; t += kSort) {
-    const int b = seq_of(t);
-    const Seq s = load_seq(a, b, apart, false);
-    const int n = tile_steps(a, j, s, t - sFirst[b]), p = cut(n);
+    const Found f = tile(t);
+    const Seq& s = f.s;
+    const int n = f.steps, p = cut(n);
     const int at = atomicAdd(&sClass[cls((n + p - 1) / p)], p), slot = p > 1 ? atomicAdd(&sSlots, p) : 0;
     for (int i = 0; i < p; ++i)
-      j.plan->tile[at + i] = TileEntry{s.q0, s.n, s.k0, s.m, (t - sFirst[b]) * rows, (int)((int64_t)n * i / p),
+      j.plan->tile[at + i] = TileEntry{s.q0, s.n, s.k0, s.m, f.index * rows, (int)((int64_t)n * i / p),
                                        (int)((int64_t)n * (i + 1) / p), p > 1 ? (slot << 16 | i << 8 | p) : 0};
   }
 }

@@ -48,13 +48,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + 2 * F::kTile;
+  uint8_t* sKV = smem + 2 * F::kQ * F::kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kUnits * F::kTile);
   uint64_t* full = bars;
   uint64_t* empty = bars + kUnits;
   uint64_t* q_full = bars + 2 * kUnits;
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_full + 2;
+  uint64_t* q_empty = q_full + F::kQ;
+  uint64_t* s_full = q_empty + F::kQ;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* o_free = o_full + 2;
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* ids = abort + 1;  // of the items, -1 behind the last
-  static_assert((2 * 8 + 11 + 2 * kIds) * 8 + 8 + 4 * kIds <= 512);
+  static_assert((2 * 8 + 13 + 2 * kIds) * 8 + 8 + 4 * kIds <= 512);
 
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -75,8 +75,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[u], 1);
       mbar_init(&empty[u], 1);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    for (int b = 0; b < F::kQ; ++b) {
+      mbar_init(&q_full[b], 1);
+      mbar_init(&q_empty[b], 1);
+    }
     for (int m = 0; m < 2; ++m) {
       mbar_init(&s_full[m], 1);
       mbar_init(&p_full[m], 4);
@@ -161,13 +163,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           id = take();
           continue;
         }
-        if (!(ok = mbar_wait(q_empty, (queries & 1) ^ 1, abort, kTimeoutNs, a.status))) break;
+        const int b = queries % F::kQ;
+        if (!(ok = mbar_wait(&q_empty[b], (queries / F::kQ & 1) ^ 1, abort, kTimeoutNs, a.status))) break;
         ++queries;
-        mbar_arrive_expect_tx(q_full, 2 * F::kTile);
+        mbar_arrive_expect_tx(&q_full[b], 2 * F::kTile);
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int d = 0; d < F::kSlabs; ++d)
-            tma_load_3d(&tmQ, sQ + m * F::kTile + d * 16384, q_full, 64 * d, it.h0, it.s.q0 + it.i0 + m * per);
+            tma_load_3d(&tmQ, sQ + (2 * b + m) * F::kTile + d * 16384, &q_full[b], 64 * d, it.h0, it.s.q0 + it.i0 + m * per);
         auto load = [&](const CUtensorMap* map, int tile) {
           if (!ok || !(ok = mbar_wait(&empty[unit], phase ^ 1, abort, kTimeoutNs, a.status))) return;
           mbar_arrive_expect_tx(&full[unit], F::kTile);
@@ -188,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __threadfence();
       if (ok && atomicAdd(p.queue + 1, 1) == (int)gridDim.x - 1) p.queue[0] = p.queue[1] = 0;
       // leave no copy in flight
-      if (queries > 0) mbar_wait_drain(q_full, (queries - 1) & 1, kTimeoutNs, a.status);
+      for (int i = max(0, queries - F::kQ); i < queries; ++i)
+        mbar_wait_drain(&q_full[i % F::kQ], i / F::kQ & 1, kTimeoutNs, a.status);
       for (int i = 0; i < min(issued, kUnits); ++i) {
         const int u = (unit - 1 - i + 2 * kUnits) % kUnits;
         mbar_wait_drain(&full[u], unit - 1 - i < 0 ? phase ^ 1 : phase, kTimeoutNs, a.status);
@@ -198,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_s = idesc_make(1, 128, BK);
       const uint32_t idesc_o = idesc_make(1, 128, DP) | (1u << 16);  // V is read MN-major
       int unit = 0;
-      uint32_t phase = 0, q_phase = 0, p_phase = 0, o_phase = 0;  // the latter two a bit for each row tile
+      uint32_t phase = 0, p_phase = 0, o_phase = 0;  // the latter two a bit for each row tile
+      int queries = 0;
       const bool one = lane == 0;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         const bool ok = mbar_wait(bar, parity, abort, kTimeoutNs, a.status);
@@ -210,8 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++unit == kUnits) unit = 0, phase ^= 1;
         return true;
       };
-      const uint32_t q_desc = uniform(k_desc(smem_addr(sQ)));
-      auto scores = [&](int m, uint32_t ka) {  // S_m = Q_m K^T
+      auto scores = [&](int m, uint32_t q_desc, uint32_t ka) {  // S_m = Q_m K^T
         const uint32_t qa = q_desc + m * (F::kTile / 16);
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
@@ -226,13 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int steps = it.steps(), keys = it.s.m;
         if (steps == 0) continue;
         int uk, uv;
-        if (!(ok = wait(q_full, q_phase) && next(uk))) break;
-        q_phase ^= 1;
+        const int b = queries % F::kQ;
+        if (!(ok = wait(&q_full[b], queries / F::kQ & 1) && next(uk))) break;
+        ++queries;
+        const uint32_t q_desc = uniform(k_desc(smem_addr(sQ + 2 * b * F::kTile)));
         tc_fence_after();
         for (int m = 0; m < 2; ++m)
-          if (it.of(m) == steps) scores(m, uniform(k_desc(smem_addr(sKV + uk * F::kTile))));
+          if (it.of(m) == steps) scores(m, q_desc, uniform(k_desc(smem_addr(sKV + uk * F::kTile))));
         commit(&empty[uk], one);
-        if (steps == 1) commit(q_empty, one);
+        if (steps == 1) commit(&q_empty[b], one);
         for (int j = steps - 1; j >= 0; --j) {
           if (j > 0 && !(ok = next(uk))) break;
           if (!(ok = next(uv))) break;
@@ -257,12 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_ts(tO + DP * m, tS + 128 * m + 8 * q, va + (2048 / 16) * q, idesc_o, j < n - 1 || q > 0, one);
               if (j == 0) commit(&o_full[m], one);
             }
-            if (j > 0 && j - 1 < n) scores(m, ka);
+            if (j > 0 && j - 1 < n) scores(m, q_desc, ka);
           }
           if (!ok) break;
           commit(&empty[uv], one);
           if (j > 0) commit(&empty[uk], one);
-          if (j == 1) commit(q_empty, one);
+          if (j == 1) commit(&q_empty[b], one);
         }
       }
       __syncwarp();

@@ -166,8 +166,10 @@ template <int DP>
 struct Fwd {
   static constexpr int kSlabs = DP / 64;
   static constexpr int kTile = 128 * DP * 2;  // bytes of a tile of Q, K or V
-  static constexpr int kUnits = (kSmem - 2048 - 2 * kTile) / kTile < 8 ? (kSmem - 2048 - 2 * kTile) / kTile : 8;
-  static constexpr size_t kBytes = 1024 + (2 + kUnits) * kTile + 512;
+  static constexpr int kQ = DP == 64 ? 2 : 1;   // buffers of an item's Q: the next one's where there is room
+  static constexpr int kUnits = DP == 64 ? 8 : 5;
+  static constexpr size_t kBytes = 1024 + (2 * kQ + kUnits) * kTile + 512;
+  static_assert(kBytes + 1024 <= kSmem);
 };
 
 // A row's softmax so far: sums of exp2(c (s - top)), even and odd columns.
