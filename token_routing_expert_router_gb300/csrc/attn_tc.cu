@@ -5,7 +5,8 @@
 //   S = Q K^T (tensor memory) -> P = exp2(c (S - m)), bf16, over S's columns -> O += P V (tensor memory)
 // Rows of a tile are (query, head) pairs, `pack` query heads of the group side by side: a key tile is
 // loaded once for 256 of them, and few queries of many heads still fill a tile.
-// Warp 0 loads by TMA (K and V tiles through one ring), warp 1 issues the products, and each of the two
+// Warps 0 and 3 load by TMA (K two tiles ahead, V three, each on its own: through one ring of five a tile of
+// V had no more than a step to come), warp 1 issues the products, and each of the two
 // warpgroups 1 and 2 is one tile's softmax, a thread a row: no exchange between threads. While one
 // tile's softmax runs, the tensor cores work on the other tile's products; S is free for the next scores
 // as soon as P V has been issued behind them, since one thread's products run in their order.
@@ -44,15 +45,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
   using F = Fwd<DP>;
-  constexpr int kUnits = F::kUnits;
+  constexpr int kNK = F::kNK, kNV = F::kNV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + 2 * F::kQ * F::kTile;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kUnits * F::kTile);
-  uint64_t* full = bars;
-  uint64_t* empty = bars + kUnits;
-  uint64_t* q_full = bars + 2 * kUnits;
+  uint8_t* sK = smem + 2 * F::kQ * F::kTile;
+  uint8_t* sV = sK + kNK * F::kTile;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sV + kNV * F::kTile);
+  uint64_t* k_empty = k_full + kNK;
+  uint64_t* v_full = k_empty + kNK;
+  uint64_t* v_empty = v_full + kNV;
+  uint64_t* q_full = v_empty + kNV;
   uint64_t* q_empty = q_full + F::kQ;
   uint64_t* s_full = q_empty + F::kQ;
   uint64_t* p_full = s_full + 2;
@@ -71,9 +74,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = 128 / p.pack;  // queries of a tile
 
   if (threadIdx.x == 0) {
-    for (int u = 0; u < kUnits; ++u) {
-      mbar_init(&full[u], 1);
-      mbar_init(&empty[u], 1);
+    for (int u = 0; u < kNK; ++u) {
+      mbar_init(&k_full[u], 1);
+      mbar_init(&k_empty[u], 1);
+    }
+    for (int u = 0; u < kNV; ++u) {
+      mbar_init(&v_full[u], 1);
+      mbar_init(&v_empty[u], 1);
     }
     for (int b = 0; b < F::kQ; ++b) {
       mbar_init(&q_full[b], 1);
@@ -87,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kIds; ++i) {
       mbar_init(&id_full[i], 1);
-      mbar_init(&id_empty[i], 9);  // the issuing warp, the softmax warps
+      mbar_init(&id_empty[i], 10);  // the warp that loads V, the issuing warp, the softmax warps
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -140,13 +147,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  auto load_tile = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int head, int row) {
+    mbar_arrive_expect_tx(bar, F::kTile);
+#pragma unroll
+    for (int d = 0; d < F::kSlabs; ++d) tma_load_3d(map, dst + d * 16384, bar, 64 * d, head, row);
+  };
+
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 0 && lane == 0) {
-      // ===================== loads: Q; K of the last tile; then K of the next and V of this one, in turn
+      // ===================== loads of Q and K, from the last tile on, and the queue
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
       int unit = 0, issued = 0, queries = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -171,20 +183,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int d = 0; d < F::kSlabs; ++d)
             tma_load_3d(&tmQ, sQ + (2 * b + m) * F::kTile + d * 16384, &q_full[b], 64 * d, it.h0, it.s.q0 + it.i0 + m * per);
-        auto load = [&](const CUtensorMap* map, int tile) {
-          if (!ok || !(ok = mbar_wait(&empty[unit], phase ^ 1, abort, kTimeoutNs, a.status))) return;
-          mbar_arrive_expect_tx(&full[unit], F::kTile);
-#pragma unroll
-          for (int d = 0; d < F::kSlabs; ++d)
-            tma_load_3d(map, sKV + unit * F::kTile + d * 16384, &full[unit], 64 * d, hk, it.s.k0 + tile * BK);
+        for (int j = steps - 1; j >= 0; --j) {
+          if (j == min(steps - 1, 2)) id = take();
+          if (!(ok = mbar_wait(&k_empty[unit], phase ^ 1, abort, kTimeoutNs, a.status))) break;
+          load_tile(&tmK, sK + unit * F::kTile, &k_full[unit], hk, it.s.k0 + j * BK);
           ++issued;
-          if (++unit == kUnits) unit = 0, phase ^= 1;
-        };
-        load(&tmK, steps - 1);
-        for (int j = steps - 1; j >= 0 && ok; --j) {
-          if (j == min(steps - 1, 1)) id = take();
-          if (j > 0) load(&tmK, j - 1);
-          load(&tmV, j);
+          if (++unit == kNK) unit = 0, phase ^= 1;
         }
       }
       // the last CTA leaves the queue as it was
@@ -193,27 +197,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       // leave no copy in flight
       for (int i = max(0, queries - F::kQ); i < queries; ++i)
         mbar_wait_drain(&q_full[i % F::kQ], i / F::kQ & 1, kTimeoutNs, a.status);
-      for (int i = 0; i < min(issued, kUnits); ++i) {
-        const int u = (unit - 1 - i + 2 * kUnits) % kUnits;
-        mbar_wait_drain(&full[u], unit - 1 - i < 0 ? phase ^ 1 : phase, kTimeoutNs, a.status);
+      for (int i = max(0, issued - kNK); i < issued; ++i) mbar_wait_drain(&k_full[i % kNK], i / kNK & 1, kTimeoutNs, a.status);
+    } else if (warp == 3) {
+      // ===================== loads of V
+      if (lane == 0) tma_prefetch_desc(&tmV);
+      int unit = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      Item it;
+      for (int k = 0; ok && taken(k, it); ++k) {
+        const int hk = it.h0 / a.group;
+        for (int j = it.steps() - 1; j >= 0; --j) {
+          ok = mbar_wait(&v_empty[unit], phase ^ 1, abort, kTimeoutNs, a.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) load_tile(&tmV, sV + unit * F::kTile, &v_full[unit], hk, it.s.k0 + j * BK);
+          __syncwarp();
+          ++issued;
+          if (++unit == kNV) unit = 0, phase ^= 1;
+        }
       }
+      for (int i = max(0, issued - kNV); i < issued; ++i) mbar_wait_drain(&v_full[i % kNV], i / kNV & 1, kTimeoutNs, a.status);
     } else if (warp == 1) {
       // ===================== products
       const uint32_t idesc_s = idesc_make(1, 128, BK);
       const uint32_t idesc_o = idesc_make(1, 128, DP) | (1u << 16);  // V is read MN-major
-      int unit = 0;
-      uint32_t phase = 0, p_phase = 0, o_phase = 0;  // the latter two a bit for each row tile
+      int uk = 0, uv = 0;  // tiles of K and V that are next
+      uint32_t k_phase = 0, v_phase = 0, p_phase = 0, o_phase = 0;  // the latter two a bit for each row tile
       int queries = 0;
       const bool one = lane == 0;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         const bool ok = mbar_wait(bar, parity, abort, kTimeoutNs, a.status);
         return (bool)__all_sync(0xffffffffu, ok);
-      };
-      auto next = [&](int& u) {
-        if (!wait(&full[unit], phase)) return false;
-        u = unit;
-        if (++unit == kUnits) unit = 0, phase ^= 1;
-        return true;
       };
       auto scores = [&](int m, uint32_t q_desc, uint32_t ka) {  // S_m = Q_m K^T
         const uint32_t qa = q_desc + m * (F::kTile / 16);
@@ -229,23 +243,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok && taken(k, it); ++k) {
         const int steps = it.steps(), keys = it.s.m;
         if (steps == 0) continue;
-        int uk, uv;
         const int b = queries % F::kQ;
-        if (!(ok = wait(&q_full[b], queries / F::kQ & 1) && next(uk))) break;
+        if (!(ok = wait(&q_full[b], queries / F::kQ & 1) && wait(&k_full[uk], k_phase))) break;
         ++queries;
         const uint32_t q_desc = uniform(k_desc(smem_addr(sQ + 2 * b * F::kTile)));
         tc_fence_after();
+        auto next_k = [&] {
+          if (++uk == kNK) uk = 0, k_phase ^= 1;
+        };
         for (int m = 0; m < 2; ++m)
-          if (it.of(m) == steps) scores(m, q_desc, uniform(k_desc(smem_addr(sKV + uk * F::kTile))));
-        commit(&empty[uk], one);
+          if (it.of(m) == steps) scores(m, q_desc, uniform(k_desc(smem_addr(sK + uk * F::kTile))));
+        commit(&k_empty[uk], one);
+        next_k();
         if (steps == 1) commit(&q_empty[b], one);
         for (int j = steps - 1; j >= 0; --j) {
-          if (j > 0 && !(ok = next(uk))) break;
-          if (!(ok = next(uv))) break;
-          if ((j + 1) * BK > keys) clear_rows(sKV + uv * F::kTile, F::kSlabs, BK, keys - j * BK, lane);
+          if (j > 0 && !(ok = wait(&k_full[uk], k_phase))) break;
+          if (!(ok = wait(&v_full[uv], v_phase))) break;
+          if ((j + 1) * BK > keys) clear_rows(sV + uv * F::kTile, F::kSlabs, BK, keys - j * BK, lane);
           tc_fence_after();
           // all that the products need is at hand before their P is waited for
-          const uint32_t va = uniform(mn_desc(smem_addr(sKV + uv * F::kTile))), ka = uniform(k_desc(smem_addr(sKV + uk * F::kTile)));
+          const uint32_t va = uniform(mn_desc(smem_addr(sV + uv * F::kTile))), ka = uniform(k_desc(smem_addr(sK + uk * F::kTile)));
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (!ok) break;
@@ -263,11 +280,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_ts(tO + DP * m, tS + 128 * m + 8 * q, va + (2048 / 16) * q, idesc_o, j < n - 1 || q > 0, one);
               if (j == 0) commit(&o_full[m], one);
             }
+            if (m == 1) commit(&v_empty[uv], one);  // ahead of the last scores
             if (j > 0 && j - 1 < n) scores(m, q_desc, ka);
           }
           if (!ok) break;
-          commit(&empty[uv], one);
-          if (j > 0) commit(&empty[uk], one);
+          if (++uv == kNV) uv = 0, v_phase ^= 1;
+          if (j > 0) {
+            commit(&k_empty[uk], one);
+            next_k();
+          }
           if (j == 1) commit(&q_empty[b], one);
         }
       }
@@ -280,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ===================== softmax of row tile m, a thread a row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int m = warp / 4 - 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t my_s = tS + 128 * m + lanes, my_o = tO + DP * m + lanes;

@@ -157,7 +157,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int slabs, int rows, i
   __syncwarp();
 }
 
-// ---- forward: 128 keys a tile; K and V tiles share a ring of `kUnits` tiles
+// ---- forward: 128 keys a tile
 constexpr int kThreads = 384;
 constexpr int BK = 128;
 constexpr int kSmem = 227 * 1024;
@@ -167,8 +167,8 @@ struct Fwd {
   static constexpr int kSlabs = DP / 64;
   static constexpr int kTile = 128 * DP * 2;  // bytes of a tile of Q, K or V
   static constexpr int kQ = DP == 64 ? 2 : 1;   // buffers of an item's Q: the next one's where there is room
-  static constexpr int kUnits = DP == 64 ? 8 : 5;
-  static constexpr size_t kBytes = 1024 + (2 * kQ + kUnits) * kTile + 512;
+  static constexpr int kNK = DP == 64 ? 4 : 2, kNV = DP == 64 ? 4 : 3;  // tiles of K and of V
+  static constexpr size_t kBytes = 1024 + (2 * kQ + kNK + kNV) * kTile + 512;
   static_assert(kBytes + 1024 <= kSmem);
 };
 
