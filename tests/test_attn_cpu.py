@@ -79,7 +79,7 @@ def test_rope_arguments(L):
     (dict(act_dtype=moe.MXE4M3), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID), (dict(ld_q=255), INVALID),
     (dict(ld_k=127), INVALID), (dict(ld_v=-128), INVALID), (dict(ld_o=100), INVALID), (dict(D=129), UNSUPPORTED),
-    (dict(Hq=32768), UNSUPPORTED), (dict(B=(1 << 20) + 1), UNSUPPORTED), (dict(Tk=(1 << 30) + 1), UNSUPPORTED),
+    (dict(Hq=32768), UNSUPPORTED), (dict(B=(1 << 16) + 1), UNSUPPORTED), (dict(Tk=(1 << 30) + 1), UNSUPPORTED),
     (dict(D=128), OK), (dict(D=1), OK), (dict(Tq=0), OK), (dict(B=0), OK)])
 def test_attn_config(L, kw, code):
     c, n = ctypes.byref(attn_cfg(**kw)), ctypes.c_size_t()

@@ -1,8 +1,5 @@
 // The attention entry points' choice of variant, and their workspaces.
 #include "attn_plan.cuh"
-#ifndef STREAM_BELOW
-#define STREAM_BELOW 76
-#endif
 
 namespace moe {
 
@@ -37,12 +34,21 @@ bool tc_rows(const AttnArgs& a, bool backward) {
   return at % 16 == 0;
 }
 
-// Tiles of 256 rows need one for every SM, and are half empty where no sequence has more than 128.
+// Equal shares of all key tiles instead of tiles of 256 rows. Rows: (query, head) pairs of a sequence and pack
+// of heads. Measured with 32 query and 8 key heads of 128 (tiles, shares):
+//   few rows: 64 requests of 1 query over 2048 keys 107 and 94 us, 1 over 8192 89 and 18, 1 over 128 7 and 9;
+//   128 rows: 1 request over 8192 89 and 35, 8 over 8192 96 and 89, 64 over 2048 114 and 121;
+//   16 tiles: 64 queries over 8192 121 and 36, over 300 14 and 12;
+//   72 tiles: 512 queries over 8192 121 and 97, over 512 16 and 39. The lengths are on the device: shares
+//   only where a request may have very many keys.
 bool stream_rule(const AttnArgs& a) {
   int pack = 1;
   while (pack < 128 && a.group % (2 * pack) == 0) pack *= 2;
-  if ((int64_t)a.max_q * pack <= 128) return true;
-  return (a.Tq / (256 / pack) + a.B) * (int64_t)(a.Hq / pack) < STREAM_BELOW;
+  const int64_t rows = (int64_t)a.max_q * pack;
+  const int64_t tiles = (a.Tq / (256 / pack) + a.B) * (int64_t)(a.Hq / pack);
+  if (rows <= 64) return true;
+  if (rows <= 128) return tiles < 304;
+  return tiles <= 24 || (tiles < 76 && a.k_start && a.Tk / 8192 >= a.B);
 }
 
 }  // namespace attn

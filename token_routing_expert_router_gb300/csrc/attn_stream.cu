@@ -61,36 +61,49 @@ __device__ __forceinline__ int line_tiles(const AttnArgs& a, const Seq& s, int t
   return (max(0, visible(a, s, last)) + BK - 1) / BK;
 }
 
-// A line without keys still takes a turn: its rows are zeros.
-__device__ __forceinline__ int64_t seq_turns(const AttnArgs& a, const Seq& s, int per, int packs) {
+// A line without keys still takes a turn: its rows are zeros. longest: raised to the longest line's tiles.
+__device__ __forceinline__ int64_t seq_turns(const AttnArgs& a, const Seq& s, int per, int packs, int& longest) {
   int64_t n = 0;
-  for (int t = 0; t * per < s.n; ++t) n += max(1, line_tiles(a, s, t, per));
+  for (int t = 0; t * per < s.n; ++t) {
+    const int len = max(1, line_tiles(a, s, t, per));
+    n += len;
+    longest = max(longest, len);
+  }
   return n * packs;
 }
 
 __device__ void find_share(const StreamParams& p, int per, Share* out) {
   __shared__ int64_t sWarp[kThreads / 32];
+  __shared__ int sLongest[kThreads / 32];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * each), b1 = min(a.B, b0 + each);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_turns(a, load_seq(a, b, false, blockIdx.x == 0), per, p.packs);
+  int longest = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_turns(a, load_seq(a, b, false, blockIdx.x == 0), per, p.packs, longest);
   int64_t inc = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
     if (lane >= off) inc += o;
   }
-  if (lane == 31) sWarp[warp] = inc;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, off));
+  if (lane == 31) sWarp[warp] = inc, sLongest[warp] = longest;
   __syncthreads();
   int64_t all = 0, before = inc - mine;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sWarp[w];
     all += sWarp[w];
+    longest = max(longest, sLongest[w]);
   }
   int64_t share = (int64_t)(all * p.inv_ctas);
   while (share * gridDim.x < all) ++share;
+  // What a CTA takes at least: lines of up to 6 tiles whole (1 query over 300 keys: 10.9 us, 14.6 with a tile
+  // a CTA; over 700 14.1 and 16.8), longer ones two tiles (4 tiles: 1 query over 2048 keys 18.2 us, 14.8 with
+  // two; 64 queries over 2048 40 and 29).
+  share = max(share, (int64_t)(longest <= 6 ? longest : 2));
   const int64_t u = min(all, share * blockIdx.x);
   if (tid == 0) {
     out->each = share;
@@ -101,7 +114,7 @@ __device__ void find_share(const StreamParams& p, int per, Share* out) {
     int64_t at = before;
     for (int b = b0; b < b1; ++b) {
       const Seq s = load_seq(a, b, false, false);
-      const int64_t turns = seq_turns(a, s, per, p.packs);
+      const int64_t turns = seq_turns(a, s, per, p.packs, longest);
       if (u < at + turns) {
         int t = 0;
         int64_t len;
@@ -462,30 +475,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           __threadfence();
           // the line's first part is its CTA's last (place 1), the others are their CTAs' first (place 0)
           auto place = [&](int g) { return (int64_t)(2 * (c0 + g) + (g == 0)) * 128; };
-          const int rows = min(128, (it.n - it.i0) * p.pack);
+          const int rows = min(per, it.n - it.i0) * p.pack, h_first = it.h0, i_first = it.i0;
+          float2* sRow = sStat[k & 1][0];  // maximum and 1 / sum of every row; its last readers are past two meetings
+          if (m == 0 && (int)row < rows) {
+            float most = -INFINITY, total = 0.0f;
+#pragma unroll 8
+            for (int g = 0; g < parts; ++g) most = fmaxf(most, __ldcg(&p.stat[place(g) + row].x));
+#pragma unroll 8
+            for (int g = 0; g < parts; ++g) {
+              const float2 st = __ldcg(&p.stat[place(g) + row]);
+              if (st.y != 0.0f) total = fmaf(ex2((st.x - most) * p.c), st.y, total);
+            }
+            sRow[row] = make_float2(most, total == 0.0f ? 0.0f : 1.0f / total);
+            a.lse[(int64_t)(h_first + row % p.pack) * a.Tq + q0 + i_first + row / p.pack] =
+                total == 0.0f ? -INFINITY : (most * p.c + log2f(total)) * kLn2;
+          }
+          if (!both_sync()) break;
           for (int e = m * 128 + row; e < rows * (DP / 4); e += 256) {
             const int r = e / (DP / 4), d = e % (DP / 4) * 4;
-            float most = -INFINITY, total = 0.0f;
-            for (int g = 0; g < parts; ++g) most = fmaxf(most, __ldcg(&p.stat[place(g) + r].x));
+            const float2 whole = sRow[r];
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (most != -INFINITY)
+            if (whole.y != 0.0f)
+#pragma unroll 8
               for (int g = 0; g < parts; ++g) {
-                const float2 st = __ldcg(&p.stat[place(g) + r]);
+                const float x = __ldcg(&p.stat[place(g) + r].x);
                 const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part + (place(g) + r) * DP + d));
-                const float weight = ex2((st.x - most) * p.c);
-                total = fmaf(weight, st.y, total);
+                const float weight = ex2((x - whole.x) * p.c);
                 acc.x = fmaf(weight, o.x, acc.x);
                 acc.y = fmaf(weight, o.y, acc.y);
                 acc.z = fmaf(weight, o.z, acc.z);
                 acc.w = fmaf(weight, o.w, acc.w);
               }
-            const float g = total == 0.0f ? 0.0f : 1.0f / total;
-            const int iq = it.i0 + r / p.pack, hq = it.h0 + r % p.pack;
             if (d < a.D)
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (int64_t)(q0 + iq) * a.ld_o + (int64_t)hq * a.D + d) =
-                  make_uint2(pack2(acc.x * g, acc.y * g), pack2(acc.z * g, acc.w * g));
-            if (d == 0)
-              a.lse[(int64_t)hq * a.Tq + q0 + iq] = total == 0.0f ? -INFINITY : (most * p.c + log2f(total)) * kLn2;
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (int64_t)(q0 + i_first + r / p.pack) * a.ld_o +
+                                        (int64_t)(h_first + r % p.pack) * a.D + d) =
+                  make_uint2(pack2(acc.x * whole.y, acc.y * whole.y), pack2(acc.z * whole.y, acc.w * whole.y));
           }
         }
       }

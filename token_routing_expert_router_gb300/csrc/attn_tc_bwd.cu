@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto row_of = [&](const Inner& i) { return DKV ? (first + i.tile) * per : i.tile * R; };  // in the sequence
   // rows of it that are the sequence's
-  auto live_of = [&](const Inner& i) { return DKV ? min(R, (s.n - row_of(i)) * p.pack) : min(R, s.m - row_of(i)); };
+  auto live_of = [&](const Inner& i) { return DKV ? min(per, s.n - row_of(i)) * p.pack : min(R, s.m - row_of(i)); };
 
   if (threadIdx.x == 0) {
     mbar_init(x_full, 1);
@@ -282,14 +282,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // not there gets p = exp2(s - inf) = 0
       Inner in = begin();
       float v[8];
-      auto fetch = [&] {
+      auto fetch = [&] {  // from L2: dq, whose CTAs may have been on this SM until now, has written delta
         const int64_t base = (int64_t)(in.head / p.pack) * a.Tq * p.pack + (int64_t)(s.q0 + row_of(in)) * p.pack;
         const int live = live_of(in);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int r = 32 * q + lane;
-          v[q] = r < live ? __ldg(p.neg_lse + base + r) : -INFINITY;
-          v[4 + q] = r < live ? p.neg_delta[base + r] : 0.0f;
+          v[q] = r < live ? __ldcg(p.neg_lse + base + r) : -INFINITY;
+          v[4 + q] = r < live ? __ldcg(p.neg_delta + base + r) : 0.0f;
         }
       };
       if (steps > 0) fetch();

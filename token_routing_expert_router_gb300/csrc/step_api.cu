@@ -81,7 +81,7 @@ moe_status_t validate(const moe_attn_config_t* c) {
   if (!ld_ok(c->ld_q, c->Hq, c->D) || !ld_ok(c->ld_k, c->Hkv, c->D) || !ld_ok(c->ld_v, c->Hkv, c->D) ||
       !ld_ok(c->ld_o, c->Hq, c->D))
     return MOE_ERR_INVALID_ARG;
-  if (c->D > kAttnMaxD || c->Hq > (1 << 14) || c->B > (1 << 20) || c->Tq > (1 << 30) || c->Tk > (1 << 30))
+  if (c->D > kAttnMaxD || c->Hq > (1 << 14) || c->B > (1 << 16) || c->Tq > (1 << 30) || c->Tk > (1 << 30))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
