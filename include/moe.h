@@ -549,7 +549,7 @@ typedef struct {
  * position are dropped), so that an angle is exact modulo a turn at any position. Made once. */
 moe_status_t moe_rope_table(const moe_rope_freq_t* freq, uint64_t* table, moe_stream_t stream);
 
-/* T tokens of Hq query and Hk key heads (either may be 0) of D <= 4096 channels. */
+/* T tokens of Hq query and Hk key heads (either may be 0) of D <= 4096 channels, 2^22 of either in all. */
 enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 };
 typedef struct {
   int32_t T, Hq, Hk, D;
@@ -584,7 +584,7 @@ moe_status_t moe_rope_backward(const moe_rope_config_t* cfg, const void* dq_out,
 /* Attention of B sequences. */
 typedef struct {
   int32_t Tq, Tk;    /* rows of q and o; rows of k and v */
-  int32_t B;         /* sequences */
+  int32_t B;         /* sequences, at most 65536 */
   int32_t Hq, Hkv;   /* query and key heads: query head h reads key head h / (Hq / Hkv) */
   int32_t D;         /* channels of a head, 1 .. 128 */
   int32_t causal;    /* 1: query i of n sees the keys j <= i + m - n of m; 0: all m */
@@ -605,10 +605,12 @@ typedef struct {
  * hold anything; a value that is not finite inside a sequence's keys may reach all of its outputs.
  * Sequences out of range (rows outside q, or more than max_q; keys outside k) set
  * MOE_ERR_DEVICE_BAD_INPUT and have no rows, or no keys. lse [Hq, Tq] fp32. Scores, sums and
- * outputs are held in fp32; with bf16 tensors exp(s - max) is rounded to bf16, the operand type of
- * its product with v. Rows may be strided views, aligned to their elements; bf16 rows of multiples
+ * outputs are held in fp32 (exponentials below 2^-126 are zero); with bf16 tensors exp(s - max) is
+ * rounded to bf16, the operand type of its product with v. Rows may be strided views, aligned to their elements; bf16 rows of multiples
  * of 16 bytes (address, stride, D % 8 = 0) go to the tensor cores. o must not overlap an input.
- * ws: moe_attn_workspace_size bytes. Deterministic. */
+ * ws: moe_attn_workspace_size bytes; after a MOE_ERR_TIMEOUT (here or in the backward) it has to be
+ * initialised again. Deterministic: the same call gives the same bits (another batch around a
+ * sequence, or another max_q, may cut its keys at other places). */
 moe_status_t moe_attn_workspace_size(const moe_attn_config_t* cfg, size_t* bytes);
 moe_status_t moe_attn(const moe_attn_config_t* cfg, const void* q, const void* k, const void* v, const int32_t* q_start,
                       const int32_t* k_start, const int32_t* k_len, void* o, float* lse, void* ws, moe_stream_t stream);
@@ -620,7 +622,8 @@ moe_status_t moe_attn(const moe_attn_config_t* cfg, const void* q, const void* k
  * of q, k and v; rows in a sequence are written (zeros for keys that nothing sees), others not
  * touched. The keys of the sequences must lie one behind the other: a sequence whose keys begin
  * before those of the one in front end sets MOE_ERR_DEVICE_BAD_INPUT and has no keys. With bf16
- * tensors p and ds are rounded to bf16 for their products. Outputs must not overlap inputs or each
+ * tensors p and ds are rounded to bf16 for their products; d_o . o, which carries o's rounding, is put right by
+ * the sum of a row's ds. Outputs must not overlap inputs or each
  * other. ws: moe_attn_backward_workspace_size bytes. No atomics on sums: the same bits on every run. */
 moe_status_t moe_attn_backward_workspace_size(const moe_attn_config_t* cfg, size_t* bytes);
 moe_status_t moe_attn_backward(const moe_attn_config_t* cfg, const void* q, const void* k, const void* v,

@@ -1,5 +1,5 @@
-// What the attention kernels share (attn_simt.cu, attn_tc.cu, attn_decode.cu): the arguments as the
-// device sees them, a sequence's rows, and the map from a block to the tile of a ragged batch.
+// What the attention kernels share (attn_*.cu): the arguments as the device sees them, a sequence's rows,
+// and the map from a block to the tile of a ragged batch.
 #pragma once
 
 #include "step.cuh"

@@ -14,6 +14,9 @@
 // tiles in turn, with a maximum, sum and O of their own: scores -> P -> O of one tile is a chain of some
 // 3500 cycles, longer than its keys take from memory, and two of them overlap. At a part's end both
 // put the two together, a half of the channels each.
+//
+// Bound by reading the keys: 64 requests of 1200 to 10700 of them (32 query and 8 key heads of 128, 1.75 GB):
+// 276 us, 6.3 TB/s, 93 % of the measured copy rate. One request over 8192: 18 us, most of it latencies.
 #include "attn_tc.cuh"
 
 namespace moe {

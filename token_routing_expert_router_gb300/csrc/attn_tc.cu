@@ -22,6 +22,10 @@
 // equally far from memory). The loads and the first scores of an item run while the last one's O is
 // written: a short sequence's tile is little more than such ends (40 prompts of 225 tokens: 51 us with a
 // CTA for every item).
+//
+// Bound by the tensor cores and what feeds them: scores read 128 bytes of shared memory a cycle, all there
+// is, and the next keys are written beside. 16384 tokens, 32 query and 8 key heads of 128, causal: 1.65 ms,
+// 1.33 PFLOP/s (69 % of the measured peak).
 #include "attn_plan.cuh"
 #include "attn_tc.cuh"
 

@@ -6,13 +6,14 @@
 // that pos * f modulo a turn is one integer product, exact at any position; what is lost is the
 // frequency's own rounding in fp64, 2^-54 of it, times the position (1e-10 turns at 10^6). The
 // nearest quarter turn comes off in integers, what is left (an eighth of a turn at most) goes to
-// fp32 and sincospif. In fp32 the product alone would be off by 0.03 radians at position 10^6.
+// fp32 and two Taylor series. In fp32 the product alone would be off by 0.03 radians at position 10^6.
 //
 // Memory bound: every element is read and written once. A thread has one place in the heads (two
 // pieces of up to 16 bytes: the two halves of lane-wise pairs, or two neighbouring pieces) of one token
 // and turns it in up to four heads. The block forms its tokens' cosines and sines once, in shared
 // memory, while all loads of the heads are in flight. The piece is the widest power of two that divides
-// what is rotated, its place, the head, the row lengths and the addresses.
+// what is rotated, its place, the head, the row lengths and the addresses. 8192 tokens of 32 + 8 heads of
+// 128 with their values: 38 us, 5.3 TB/s; 4095 tokens of 129 heads of 192: 69 us, 5.9 TB/s.
 #include "step.cuh"
 
 namespace moe {
