@@ -482,3 +482,89 @@ def test_many_sequences():
         alone.check_backward(*mine)
         ones = torch.tensor([b.q_at[i] for i, (n, _) in enumerate(lens) if n == 1], device="cuda")
         assert torch.equal(o[ones], b.v[ones].expand(-1, 2, 16))
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_no_keys_at_all_and_no_queries(dt, n):
+    """Tk = 0: zeros, -inf and zero gradients; Tq = 0: zero gradients of the keys."""
+    Hq, Hkv, D = 4, 2, 64
+    code, i32 = CODE[dt], dict(device="cuda", dtype=torch.int32)
+    q, none = normal(gen(1), n, Hq, D, dtype=dt), torch.empty(0, Hkv, D, device="cuda", dtype=dt)
+    cfg = moe.MoEAttnConfig.make(Tq=n, Tk=0, B=1, Hq=Hq, Hkv=Hkv, D=D, act_dtype=code, max_q=n)
+    ws = workspace(max(moe.moe_attn_workspace_size(cfg), moe.moe_attn_backward_workspace_size(cfg)))
+    start, zero = torch.tensor([0, n], **i32), torch.zeros(1, **i32)
+    o, lse, dq = poisoned(n, Hq, D, dtype=dt), poisoned(Hq, n, dtype=FP), poisoned(n, Hq, D, dtype=dt)
+    moe.moe_attn(cfg, q, none, none, start, zero, zero, o, lse, ws)
+    assert not o.any() and (lse == -math.inf).all()
+    moe.moe_attn_backward(cfg, q, none, none, start, zero, zero, o, lse, q, dq, none, none, ws)
+    assert not dq.any() and moe.moe_read_status(ws) == moe.MOE_OK
+    # keys, but no queries
+    k = normal(gen(2), n, Hkv, D, dtype=dt)
+    nq = torch.empty(0, Hq, D, device="cuda", dtype=dt)
+    cfg = moe.MoEAttnConfig.make(Tq=0, Tk=n, B=1, Hq=Hq, Hkv=Hkv, D=D, act_dtype=code)
+    ws = workspace(max(moe.moe_attn_workspace_size(cfg), moe.moe_attn_backward_workspace_size(cfg)))
+    dk, dv = poisoned(n, Hkv, D, dtype=dt), poisoned(n, Hkv, D, dtype=dt)
+    nl, start = torch.empty(Hq, 0, device="cuda"), torch.zeros(2, **i32)
+    length = torch.tensor([n], **i32)
+    moe.moe_attn(cfg, nq, k, k, start, zero, length, nq, nl, ws)
+    moe.moe_attn_backward(cfg, nq, k, k, start, zero, length, nq, nl, nq, nq, dk, dv, ws)
+    assert not dk.any() and not dv.any() and moe.moe_read_status(ws) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("dt,D", [(BF, 64), (FP, 32)])
+def test_on_the_stream_that_is_given(dt, D):
+    """stream= another than the current one: ordered on it, with tensors made on the current one."""
+    b = Batch([(200, 200), (1, 1), (90, 90)], 4, 2, D, dt, seed=6)
+    o, lse = b.forward()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o2, lse2 = b.forward(stream=side)  # the outputs are filled on the current stream first
+    side.synchronize()
+    torch.cuda.synchronize()
+    moe.moe_attn(b.cfg, b.q, b.k, b.v, b.q_start, b.k_start, b.k_len, o2, lse2, b.ws, stream=side)
+    side.synchronize()
+    assert torch.equal(o[:b.used], o2[:b.used]) and torch.equal(lse[:, :b.used], lse2[:, :b.used])
+
+
+def test_rows_of_two_shapes():
+    """[T, heads, D] and [T, heads * D] name the same rows."""
+    b = Batch([(130, 130)], 4, 2, 64, BF, seed=8)
+    o, lse = b.forward()
+    flat = lambda t: t.reshape(len(t), -1)  # noqa: E731
+    o2, lse2 = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+    moe.moe_attn(b.cfg, flat(b.q), flat(b.k), flat(b.v), b.q_start, None, None, flat(o2), lse2, b.ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_a_sequence_does_not_see_its_neighbours():
+    """NaN in one sequence's rows stays there: the others' bits are those without it."""
+    for dt, D in ((BF, 128), (BF, 64), (BF, 36), (FP, 64)):
+        b = Batch([(100, 100), (70, 70), (300, 300)], 4, 2, D, dt, seed=4)
+        o, lse = b.forward()
+        grads = b.backward(o, lse)
+        for t in (b.q, b.k, b.v, b.do):
+            t[100:170] = float("nan")
+        o2, lse2 = b.forward()
+        grads2 = b.backward(o2, lse2)
+        for lo, hi in ((0, 100), (170, 470)):
+            assert torch.equal(o[lo:hi], o2[lo:hi]) and torch.equal(lse[:, lo:hi], lse2[:, lo:hi])
+            assert all(torch.equal(x[lo:hi], y[lo:hi]) for x, y in zip(grads, grads2))
+
+
+@pytest.mark.parametrize("dt,D,n,m", [(BF, 128, 300, 300), (BF, 64, 1, 5000), (BF, 36, 70, 70), (FP, 64, 100, 100), (FP, 32, 1, 40),
+                                      (FP, 32, 1, 5000)])
+def test_nan_stays_visible(dt, D, n, m):
+    """NaN in a query is NaN in its own outputs alone; NaN in a key that all see is NaN in all of its head's."""
+    Hq, Hkv = 4, 2
+    b = Batch([(n, m)], Hq, Hkv, D, dt, place="cache", seed=5)
+    o, lse = b.forward()
+    b.q[n - 1, 1] = float("nan")
+    o2, lse2 = b.forward()
+    assert o2[n - 1, 1].isnan().all() and lse2[1, n - 1].isnan()
+    same = torch.ones(n, Hq, dtype=torch.bool, device="cuda")
+    same[n - 1, 1] = False
+    assert torch.equal(o[:n][same], o2[:n][same]) and torch.equal(lse.T[:n][same], lse2.T[:n][same])
+    b.k[b.k_at[0], 1] = float("nan")
+    o3, lse3 = b.forward()
+    assert o3[:n, 2:].isnan().all() and lse3[2:, :n].isnan().all()

@@ -192,12 +192,12 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p, int ro
     if (r >= rows) continue;
     float most = -INFINITY, total = 0.0f, o = 0.0f;
     for (int w = 0; w < kWarps; ++w) most = fmaxf(most, sStat[w * R + x].x);
-    if (most != -INFINITY)
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = expf(sStat[w * R + x].x - most);
-        total = fmaf(f, sStat[w * R + x].y, total);
-        o = fmaf(f, sO[(w * R + x) * DP + d], o);
-      }
+    for (int w = 0; w < kWarps; ++w) {
+      // left out without a visible key only: where all scores are NaN the maximum is -inf, the sum NaN
+      const float f = sStat[w * R + x].y == 0.0f ? 0.0f : expf(sStat[w * R + x].x - most);
+      total = fmaf(f, sStat[w * R + x].y, total);
+      o = fmaf(f, sO[(w * R + x) * DP + d], o);
+    }
     if (p.splits > 1) {
       const int64_t at = ((int64_t)blockIdx.x * p.splits + blockIdx.y) * R + r;
       if (d < a.D) p.part[at * a.D + d] = o;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) few_join_kernel(const FewParams p, i
     float most = -INFINITY, total = 0.0f;
     for (int i = 0; i < p.splits; ++i) most = fmaxf(most, sStat[r][i].x);
     for (int i = 0; i < p.splits; ++i) {
-      const float f = most == -INFINITY ? 0.0f : expf(sStat[r][i].x - most);
+      const float f = sStat[r][i].y == 0.0f ? 0.0f : expf(sStat[r][i].x - most);
       total = fmaf(f, sStat[r][i].y, total);
       sStat[r][i].x = f;
     }
