@@ -583,14 +583,14 @@ moe_status_t moe_rope_backward(const moe_rope_config_t* cfg, const void* dq_out,
 
 /* Attention of B sequences. */
 typedef struct {
-  int32_t Tq, Tk;    /* rows of q and o; rows of k and v */
+  int32_t Tq, Tk;    /* rows of q and o; rows of k and v: at most 2^30 */
   int32_t B;         /* sequences, at most 65536 */
-  int32_t Hq, Hkv;   /* query and key heads: query head h reads key head h / (Hq / Hkv) */
+  int32_t Hq, Hkv;   /* query and key heads, Hq <= 16384: query head h reads key head h / (Hq / Hkv) */
   int32_t D;         /* channels of a head, 1 .. 128 */
   int32_t causal;    /* 1: query i of n sees the keys j <= i + m - n of m; 0: all m */
   int32_t max_q;     /* no sequence has more query rows than this (0: Tq); lets short ones be served as such */
   int32_t act_dtype; /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 */
-  float scale;       /* > 0, of the scores */
+  float scale;       /* of the scores: 2^-100 .. 2^100 */
   int64_t ld_q, ld_k, ld_v, ld_o; /* row strides in elements; 0: dense */
 } moe_attn_config_t;
 
@@ -620,7 +620,7 @@ moe_status_t moe_attn(const moe_attn_config_t* cfg, const void* q, const void* k
  *     dv_j = sum_i p_ij d_o_i;  dk_j = scale sum_i ds_ij q_i;  dq_i = scale sum_j ds_ij k_j
  * (dk and dv over every query head of their group). d_o has o's rows and stride, dq, dk and dv those
  * of q, k and v; rows in a sequence are written (zeros for keys that nothing sees), others not
- * touched. The keys of the sequences must lie one behind the other: a sequence whose keys begin
+ * touched. lse is fp32: p is off by up to 2^-22 |s| of itself, and means nothing beyond |s| = 2^22. The keys of the sequences must lie one behind the other: a sequence whose keys begin
  * before those of the one in front end sets MOE_ERR_DEVICE_BAD_INPUT and has no keys. With bf16
  * tensors p and ds are rounded to bf16 for their products; d_o . o, which carries o's rounding, is put right by
  * the sum of a row's ds. Outputs must not overlap inputs or each

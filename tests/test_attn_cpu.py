@@ -77,7 +77,8 @@ def test_rope_arguments(L):
     (dict(Tq=-1), INVALID), (dict(Tk=-1), INVALID), (dict(B=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID),
     (dict(Hq=5), INVALID), (dict(D=0, scale=1.0), INVALID), (dict(causal=2), INVALID), (dict(max_q=-1), INVALID),
     (dict(act_dtype=moe.MXE4M3), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
-    (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID), (dict(ld_q=255), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(scale=2.0 ** 101), INVALID), (dict(scale=2.0 ** -101), INVALID),
+    (dict(scale=2.0 ** 100), OK), (dict(scale=2.0 ** -100), OK), (dict(scale=float("nan")), INVALID), (dict(ld_q=255), INVALID),
     (dict(ld_k=127), INVALID), (dict(ld_v=-128), INVALID), (dict(ld_o=100), INVALID), (dict(D=129), UNSUPPORTED),
     (dict(Hq=32768), UNSUPPORTED), (dict(B=(1 << 16) + 1), UNSUPPORTED), (dict(Tk=(1 << 30) + 1), UNSUPPORTED),
     (dict(D=128), OK), (dict(D=1), OK), (dict(Tq=0), OK), (dict(B=0), OK)])

@@ -568,3 +568,25 @@ def test_nan_stays_visible(dt, D, n, m):
     b.k[b.k_at[0], 1] = float("nan")
     o3, lse3 = b.forward()
     assert o3[:n, 2:].isnan().all() and lse3[2:, :n].isnan().all()
+
+
+@pytest.mark.parametrize("dt,D,n,m", [(BF, 64, 1, 700), (BF, 64, 300, 700), (BF, 36, 70, 90), (FP, 32, 1, 700), (FP, 32, 100, 200)])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** 100])
+def test_the_smallest_and_largest_scale(dt, D, n, m, scale):
+    """2^-100: all scores round to 0 against 1, o is the mean of v and lse the logarithm of the count.
+    2^100: the largest score has the weight 1."""
+    b = Batch([(n, m)], 2, 1, D, dt, causal=0, place="cache", scale=scale, seed=9)
+    o, lse = b.forward()
+    at = b.k_at[0]
+    k, v = b.k[at:at + m, 0].double(), b.v[at:at + m, 0].double()
+    for h in range(2):
+        s = b.q[:n, h].double() @ k.T
+        if scale < 1:
+            want, want_lse = v.mean(0).expand(n, D), torch.full((n,), math.log(m), device="cuda", dtype=torch.float64)
+        else:
+            top, best = s.max(1)
+            want, want_lse = v[best], top * scale
+        # o: one rounding of its type, fp32 sums of m terms below 6 (2^-24 m of them at most); lse: as many roundings
+        eps = torch.finfo(dt).eps / 2
+        assert ((o[:n, h].double() - want).abs() <= eps * want.abs() + 2.0 ** -24 * m * 6).all()
+        assert ((lse[h, :n].double() - want_lse).abs() <= 2.0 ** -24 * m * want_lse.abs()).all()

@@ -175,6 +175,7 @@ struct Fwd {
 // A row's softmax so far: sums of exp2(c (s - top)), even and odd columns.
 struct Running {
   float top = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;
+  bool far = false;  // some row of the warp has a maximum beyond 2^24 (base 2)
 };
 
 // One tile of scores at my_s (this thread's lane) becomes P; columns from `end` on are not seen (the
@@ -205,6 +206,7 @@ __device__ __forceinline__ void softmax_step(uint32_t my_s, uint32_t my_o, float
   if (__any_sync(0xffffffffu, grow)) {
     const float f = grow ? ex2((w.top - most) * c) : 1.0f;  // 0 for the row's first key
     if (grow) w.top = most;
+    w.far = __any_sync(0xffffffffu, w.top != -INFINITY && fabsf(w.top * c) > 0x1p24f);
     w.sum0 *= f, w.sum1 *= f;
     if (begun) {  // the products up to the last tile are in O: these scores were issued behind them
 #pragma unroll 1
@@ -219,6 +221,27 @@ __device__ __forceinline__ void softmax_step(uint32_t my_s, uint32_t my_o, float
     }
   }
   const float base = w.top == -INFINITY ? 0.0f : -w.top * c;  // no key yet: exp2(-inf) = 0
+  // base's rounding is a factor of all the row's exponentials, too large a one where scores are: there the
+  // difference is formed first, from the scores as they lie in tensor memory (P goes over those that are read)
+  if (w.far) {
+    const float least = w.top == -INFINITY ? 0.0f : w.top;
+#pragma unroll 1
+    for (int col = 0; col < BK; col += 16) {
+      uint32_t s[16], v[8];
+      tmem_ld16(my_s + col, s);
+      tmem_ld_wait();
+#pragma unroll
+      for (int l = 0; l < 16; l += 2) {
+        const float x = col + l < end ? ex2((__uint_as_float(s[l]) - least) * c) : 0.0f;
+        const float y = col + l + 1 < end ? ex2((__uint_as_float(s[l + 1]) - least) * c) : 0.0f;
+        w.sum0 += x, w.sum1 += y;
+        v[l / 2] = pack2(x, y);
+      }
+      tmem_st8(my_s + col / 2, v);
+    }
+    tmem_st_wait();
+    return;
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     uint32_t v[16];

@@ -77,7 +77,8 @@ moe_status_t validate(const moe_attn_config_t* c) {
   if (!c || c->Tq < 0 || c->Tk < 0 || c->B < 0 || c->Hq < 1 || c->Hkv < 1 || c->Hq % c->Hkv || c->D < 1)
     return MOE_ERR_INVALID_ARG;
   if ((c->causal != 0 && c->causal != 1) || c->max_q < 0 || !act_ok(c->act_dtype)) return MOE_ERR_INVALID_ARG;
-  if (!(c->scale > 0.0f) || !isfinite(c->scale)) return MOE_ERR_INVALID_ARG;
+  // 2^-100 .. 2^100: 8 / scale, and scale in base 2, are finite in fp32
+  if (!(c->scale >= 0x1p-100f && c->scale <= 0x1p100f)) return MOE_ERR_INVALID_ARG;
   if (!ld_ok(c->ld_q, c->Hq, c->D) || !ld_ok(c->ld_k, c->Hkv, c->D) || !ld_ok(c->ld_v, c->Hkv, c->D) ||
       !ld_ok(c->ld_o, c->Hq, c->D))
     return MOE_ERR_INVALID_ARG;
