@@ -5,9 +5,9 @@
 //   delta_i = do_i . o_i;  ds_ij = p_ij (do_i . v_j - delta_i) scale
 //   dv_j = sum_i p_ij do_i;  dk_j = sum_i ds_ij q_i;  dq_i = sum_j ds_ij k_j
 //
-// A block of 256 threads owns 64 query rows (dk, dv: 64 key rows) and goes over the other side in
-// tiles of 64, with the running maximum and sum of the softmax; scores are never stored. Every thread
-// forms 4 x 4 scores, and 4 rows x DP / 16 columns of the results in registers. Bound by FMA issue
+// A block of 256 threads owns 64 query rows (dk, dv: 64 key rows), or 16 of a small batch, and goes over the
+// other side in tiles of 64, with the running maximum and sum of the softmax; scores are never stored. Every
+// thread forms 4 x 4 (1 x 4) scores, and 4 rows (1) x DP / 16 columns of the results in registers. Bound by FMA issue
 // (16384 tokens, 32 heads of 128, causal: 82 ms, 27 TFLOP/s): two 64 x 64 x D products a tile forward,
 // five backward (in two kernels, which form the scores and do . v once more each; in return no result is
 // added to by two blocks, so the bits never change). From bf16 tensors delta carries the rounding of o:
@@ -29,11 +29,23 @@ __device__ __forceinline__ void from_f(__nv_bfloat16* d, float v) { *d = __float
 
 // Rows [row0, row0 + live) of one head (base points at its first channel of row 0) as fp32, times f,
 // zeros past the last row and channel.
-template <typename T, int DP>
+template <typename T, int DP, int ROWS>
 __device__ __forceinline__ void load_tile(float* dst, const void* base, int64_t ld, int64_t row0, int live, int D, float f) {
   const T* src = static_cast<const T*>(base) + row0 * ld;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < R * DP; i += kThreads) {
+  if constexpr (sizeof(T) == 4) {
+    if ((((uint64_t)src | (uint64_t)(4 * ld) | (uint64_t)(4 * D)) & 15) == 0) {
+#pragma unroll 8
+      for (int i = threadIdx.x; i < ROWS * (DP / 4); i += kThreads) {
+        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < live && d < D) v = *reinterpret_cast<const float4*>(src + (int64_t)r * ld + d);
+        *reinterpret_cast<float4*>(dst + r * (DP + 4) + d) = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+      }
+      return;
+    }
+  }
+#pragma unroll 8
+  for (int i = threadIdx.x; i < ROWS * DP; i += kThreads) {
     const int r = i / DP, d = i % DP;
     dst[r * (DP + 4) + d] = r < live && d < D ? f * to_f(src[(int64_t)r * ld + d]) : 0.0f;
   }
@@ -43,40 +55,40 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
 }
 
-// c[r][j] += x row (4 ty + r) . y row (tx + 16 j)
-template <int DP>
-__device__ __forceinline__ void scores(float (&c)[4][4], const float* x, const float* y, int ty, int tx) {
+// c[r][j] += x row (N ty + r) . y row (tx + 16 j)
+template <int DP, int N>
+__device__ __forceinline__ void scores(float (&c)[N][4], const float* x, const float* y, int ty, int tx) {
   constexpr int LD = DP + 4;
 #pragma unroll 4
   for (int d = 0; d < DP; d += 4) {
-    float4 a[4], b[4];
+    float4 a[N], b[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(x + (4 * ty + r) * LD + d);
+    for (int r = 0; r < N; ++r) a[r] = *reinterpret_cast<const float4*>(x + (N * ty + r) * LD + d);
 #pragma unroll
     for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * LD + d);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < N; ++r)
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[r][j] = dot4(a[r], b[j], c[r][j]);
   }
 }
 
-// acc[r][c] += sum_j w[4 ty + r][j] y[j][column c of this thread]: kV neighbouring columns, from
+// acc[r][c] += sum_j w[N ty + r][j] y[j][column c of this thread]: kV neighbouring columns, from
 // kV tx on, of every 16 kV.
 template <int DP>
 struct Cols {
   static constexpr int kN = DP / 16;                    // columns of a thread
   static constexpr int kV = kN < 4 ? kN : 4;            // neighbouring ones
 };
-template <int DP>
-__device__ __forceinline__ void accumulate(float (&acc)[4][DP / 16], const float* w, const float* y, int ty, int tx) {
+template <int DP, int N>
+__device__ __forceinline__ void accumulate(float (&acc)[N][DP / 16], const float* w, const float* y, int ty, int tx) {
   constexpr int LD = DP + 4, kN = Cols<DP>::kN, kV = Cols<DP>::kV;
 #pragma unroll 2
   for (int j0 = 0; j0 < R; j0 += 4) {
-    float p[4][4];  // [row][j]
+    float p[N][4];  // [row][j]
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 t = *reinterpret_cast<const float4*>(w + (4 * ty + i) * PS + j0);
+    for (int i = 0; i < N; ++i) {
+      const float4 t = *reinterpret_cast<const float4*>(w + (N * ty + i) * PS + j0);
       p[i][0] = t.x, p[i][1] = t.y, p[i][2] = t.z, p[i][3] = t.w;
     }
 #pragma unroll
@@ -93,21 +105,21 @@ __device__ __forceinline__ void accumulate(float (&acc)[4][DP / 16], const float
           for (int l = 0; l < kV; ++l) v[l] = src[l];
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < N; ++r)
 #pragma unroll
           for (int l = 0; l < kV; ++l) acc[r][c + l] = fmaf(p[r][j], v[l], acc[r][c + l]);
       }
   }
 }
 
-template <typename T, int DP>
-__device__ __forceinline__ void store_rows(void* base, int64_t ld, int64_t row0, int live, int D, const float (&acc)[4][DP / 16],
-                                           const float (&f)[4], int ty, int tx) {
+template <typename T, int DP, int N>
+__device__ __forceinline__ void store_rows(void* base, int64_t ld, int64_t row0, int live, int D, const float (&acc)[N][DP / 16],
+                                           const float (&f)[N], int ty, int tx) {
   constexpr int kN = Cols<DP>::kN, kV = Cols<DP>::kV;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    if (4 * ty + r >= live) continue;
-    T* dst = static_cast<T*>(base) + (row0 + 4 * ty + r) * ld;
+  for (int r = 0; r < N; ++r) {
+    if (N * ty + r >= live) continue;
+    T* dst = static_cast<T*>(base) + (row0 + N * ty + r) * ld;
 #pragma unroll
     for (int c = 0; c < kN; c += kV)
 #pragma unroll
@@ -128,40 +140,41 @@ __device__ __forceinline__ T* head(void* p, int h, int D) {
 }
 
 template <int DP>
-constexpr size_t tile_floats() {
-  return (size_t)R * (DP + 4);
+__host__ __device__ constexpr size_t tile_floats(int rows) {
+  return (size_t)rows * (DP + 4);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int N>
 __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a) {
+  constexpr int O = 16 * N;  // rows of the block
   extern __shared__ float4 smem4[];
   float* sQ = reinterpret_cast<float*>(smem4);
-  float* sK = sQ + tile_floats<DP>();
-  float* sV = sK + tile_floats<DP>();
-  float* sP = sV + tile_floats<DP>();
+  float* sK = sQ + tile_floats<DP>(O);
+  float* sV = sK + tile_floats<DP>(R);
+  float* sP = sV + tile_floats<DP>(R);
   const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   __shared__ int sFind[kThreads / 32 + 3];
-  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, false, blockIdx.x == 0 && h == 0, sFind);
+  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, O, false, blockIdx.x == 0 && h == 0, sFind);
   if (t.b < 0) return;
   const Seq s = load_seq(a, t.b, false, false);
-  const int i0 = (t.count - 1 - t.index) * R, rows = min(R, s.n - i0);  // the longest first
-  load_tile<T, DP>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, a.scale);
+  const int i0 = (t.count - 1 - t.index) * O, rows = min(O, s.n - i0);  // the longest first
+  load_tile<T, DP, O>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, a.scale);
 
-  float acc[4][DP / 16] = {}, top[4], sum[4];
+  float acc[N][DP / 16] = {}, top[N], sum[N];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) top[r] = -INFINITY, sum[r] = 0.0f;
+  for (int r = 0; r < N; ++r) top[r] = -INFINITY, sum[r] = 0.0f;
   const int keys = visible(a, s, i0 + rows - 1);
   for (int j0 = 0; j0 < keys; j0 += R) {
     __syncthreads();
     const int live = min(R, s.m - j0);
-    load_tile<T, DP>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, live, a.D, 1.0f);
-    load_tile<T, DP>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, live, a.D, 1.0f);
+    load_tile<T, DP, R>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, live, a.D, 1.0f);
+    load_tile<T, DP, R>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, live, a.D, 1.0f);
     __syncthreads();
-    float c[4][4] = {};
-    scores<DP>(c, sQ, sK, ty, tx);
+    float c[N][4] = {};
+    scores<DP, N>(c, sQ, sK, ty, tx);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int end = visible(a, s, i0 + 4 * ty + r) - j0;
+    for (int r = 0; r < N; ++r) {
+      const int end = visible(a, s, i0 + N * ty + r) - j0;
       float m = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -177,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float p = expf(c[r][j] - base);
-        sP[(4 * ty + r) * PS + tx + 16 * j] = p;
+        sP[(N * ty + r) * PS + tx + 16 * j] = p;
         part += p;
       }
 #pragma unroll
@@ -189,21 +202,21 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a
     }
     __syncwarp();  // a row's scores come from the 16 threads that use them
     // the tile's sums apart, so that a long row's do not lose more with every tile
-    float fresh[4][DP / 16] = {};
-    accumulate<DP>(fresh, sP, sV, ty, tx);
+    float fresh[N][DP / 16] = {};
+    accumulate<DP, N>(fresh, sP, sV, ty, tx);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < N; ++r)
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d) acc[r][d] += fresh[r][d];
   }
-  float f[4];
+  float f[N];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < N; ++r) {
     f[r] = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];  // no visible key: a row of zeros
-    if (tx == 0 && 4 * ty + r < rows)
-      a.lse[(int64_t)h * a.Tq + s.q0 + i0 + 4 * ty + r] = sum[r] == 0.0f ? -INFINITY : top[r] + logf(sum[r]);
+    if (tx == 0 && N * ty + r < rows)
+      a.lse[(int64_t)h * a.Tq + s.q0 + i0 + N * ty + r] = sum[r] == 0.0f ? -INFINITY : top[r] + logf(sum[r]);
   }
-  store_rows<T, DP>(head<T>(a.o, h, a.D), a.ld_o, s.q0 + i0, rows, a.D, acc, f, ty, tx);
+  store_rows<T, DP, N>(head<T>(a.o, h, a.D), a.ld_o, s.q0 + i0, rows, a.D, acc, f, ty, tx);
 }
 
 struct RowStat {
@@ -211,129 +224,135 @@ struct RowStat {
 };
 
 // dq of 64 query rows of a head.
-template <typename T, int DP>
+template <typename T, int DP, int N>
 __global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
+  constexpr int O = 16 * N;  // rows of the block
   extern __shared__ float4 smem4[];
   float* sQ = reinterpret_cast<float*>(smem4);
-  float* sO = sQ + tile_floats<DP>();
-  float* sK = sO + tile_floats<DP>();
-  float* sV = sK + tile_floats<DP>();
-  float* sP = sV + tile_floats<DP>();
-  float* sM = sP + R * PS;  // kRounded: P, for the mean key
+  float* sO = sQ + tile_floats<DP>(O);
+  float* sK = sO + tile_floats<DP>(O);
+  float* sV = sK + tile_floats<DP>(R);
+  float* sP = sV + tile_floats<DP>(R);
+  float* sM = sP + O * PS;  // kRounded: P, for the mean key
   constexpr bool kRounded = sizeof(T) == 2;
   const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   __shared__ int sFind[kThreads / 32 + 3];
-  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, R, true, blockIdx.x == 0 && h == 0, sFind);
+  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, O, true, blockIdx.x == 0 && h == 0, sFind);
   if (t.b < 0) return;
   const Seq s = load_seq(a, t.b, true, false);
-  const int i0 = (t.count - 1 - t.index) * R, rows = min(R, s.n - i0);
-  load_tile<T, DP>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, a.scale);
-  load_tile<T, DP>(sO, head<T>(a.d_o, h, a.D), a.ld_o, s.q0 + i0, rows, a.D, 1.0f);
-  RowStat st[4];
+  const int i0 = (t.count - 1 - t.index) * O, rows = min(O, s.n - i0);
+  load_tile<T, DP, O>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, a.scale);
+  load_tile<T, DP, O>(sO, head<T>(a.d_o, h, a.D), a.ld_o, s.q0 + i0, rows, a.D, 1.0f);
+  RowStat st[N];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t at = (int64_t)h * a.Tq + s.q0 + i0 + 4 * ty + r;
-    const bool live = 4 * ty + r < rows;
+  for (int r = 0; r < N; ++r) {
+    const int64_t at = (int64_t)h * a.Tq + s.q0 + i0 + N * ty + r;
+    const bool live = N * ty + r < rows;
     st[r] = RowStat{live ? a.lse[at] : 0.0f, live ? a.delta[at] : 0.0f};
   }
-  float acc[4][DP / 16] = {}, mean[kRounded ? 4 : 1][DP / 16] = {}, lack[4] = {};
+  float acc[N][DP / 16] = {}, mean[kRounded ? N : 1][DP / 16] = {}, lack[N] = {};
   const int keys = visible(a, s, i0 + rows - 1);
   for (int j0 = 0; j0 < keys; j0 += R) {
     __syncthreads();
     const int live = min(R, s.m - j0);
-    load_tile<T, DP>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, live, a.D, 1.0f);
-    load_tile<T, DP>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, live, a.D, 1.0f);
+    load_tile<T, DP, R>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, live, a.D, 1.0f);
+    load_tile<T, DP, R>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, live, a.D, 1.0f);
     __syncthreads();
-    float c[4][4] = {}, dp[4][4] = {};
-    scores<DP>(c, sQ, sK, ty, tx);
-    scores<DP>(dp, sO, sV, ty, tx);
+    float c[N][4] = {}, dp[N][4] = {};
+    scores<DP, N>(c, sQ, sK, ty, tx);
+    scores<DP, N>(dp, sO, sV, ty, tx);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int end = min(4 * ty + r < rows ? visible(a, s, i0 + 4 * ty + r) : 0, s.m) - j0;
+    for (int r = 0; r < N; ++r) {
+      const int end = min(N * ty + r < rows ? visible(a, s, i0 + N * ty + r) : 0, s.m) - j0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float p = tx + 16 * j < end ? expf(c[r][j] - st[r].lse) : 0.0f;
         const float ds = p == 0.0f ? 0.0f : p * (dp[r][j] - st[r].delta);
-        sP[(4 * ty + r) * PS + tx + 16 * j] = ds;
-        if constexpr (kRounded) sM[(4 * ty + r) * PS + tx + 16 * j] = p;
+        sP[(N * ty + r) * PS + tx + 16 * j] = ds;
+        if constexpr (kRounded) sM[(N * ty + r) * PS + tx + 16 * j] = p;
         lack[r] += ds;
       }
     }
     __syncwarp();
-    accumulate<DP>(acc, sP, sK, ty, tx);
-    if constexpr (kRounded) accumulate<DP>(mean, sM, sK, ty, tx);
+    accumulate<DP, N>(acc, sP, sK, ty, tx);
+    if constexpr (kRounded) accumulate<DP, N>(mean, sM, sK, ty, tx);
   }
   if constexpr (kRounded) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < N; ++r) {
 #pragma unroll
       for (int off = 8; off; off >>= 1) lack[r] += __shfl_xor_sync(0xffffffffu, lack[r], off);
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d) acc[r][d] = fmaf(-lack[r], mean[r][d], acc[r][d]);
-      if (tx == 0 && 4 * ty + r < rows) a.delta[(int64_t)h * a.Tq + s.q0 + i0 + 4 * ty + r] = st[r].delta + lack[r];
+      if (tx == 0 && N * ty + r < rows) a.delta[(int64_t)h * a.Tq + s.q0 + i0 + N * ty + r] = st[r].delta + lack[r];
     }
   }
-  const float f[4] = {a.scale, a.scale, a.scale, a.scale};
-  store_rows<T, DP>(head<T>(a.dq, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, acc, f, ty, tx);
+  float f[N];
+#pragma unroll
+  for (int r = 0; r < N; ++r) f[r] = a.scale;
+  store_rows<T, DP, N>(head<T>(a.dq, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, acc, f, ty, tx);
 }
 
 // dk and dv of 64 key rows of a key head: over the query rows that see them, of every query head of
 // its group. Scores are transposed: key rows by query rows.
-template <typename T, int DP>
+template <typename T, int DP, int N>
 __global__ void __launch_bounds__(kThreads) simt_dkv_kernel(const AttnArgs a) {
+  constexpr int O = 16 * N;  // rows of the block
   extern __shared__ float4 smem4[];
   float* sK = reinterpret_cast<float*>(smem4);
-  float* sV = sK + tile_floats<DP>();
-  float* sQ = sV + tile_floats<DP>();
-  float* sO = sQ + tile_floats<DP>();
-  float* sP = sO + tile_floats<DP>();
-  float* sS = sP + R * PS;
+  float* sV = sK + tile_floats<DP>(O);
+  float* sQ = sV + tile_floats<DP>(O);
+  float* sO = sQ + tile_floats<DP>(R);
+  float* sP = sO + tile_floats<DP>(R);
+  float* sS = sP + O * PS;
   __shared__ RowStat sStat[R];
   const int hk = blockIdx.y, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   __shared__ int sFind[kThreads / 32 + 3];
-  const Tile t = find_tile<kThreads, true>(a, blockIdx.x, R, true, blockIdx.x == 0 && hk == 0, sFind);
+  const Tile t = find_tile<kThreads, true>(a, blockIdx.x, O, true, blockIdx.x == 0 && hk == 0, sFind);
   if (t.b < 0) return;
   const Seq s = load_seq(a, t.b, true, false);
-  const int j0 = t.index * R, rows = min(R, s.m - j0);
-  load_tile<T, DP>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, rows, a.D, 1.0f);
-  load_tile<T, DP>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, rows, a.D, 1.0f);
-  float dk[4][DP / 16] = {}, dv[4][DP / 16] = {};
+  const int j0 = t.index * O, rows = min(O, s.m - j0);
+  load_tile<T, DP, O>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, rows, a.D, 1.0f);
+  load_tile<T, DP, O>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, rows, a.D, 1.0f);
+  float dk[N][DP / 16] = {}, dv[N][DP / 16] = {};
   // the first query row that sees key j0
   const int first = a.causal ? max(0, j0 - (s.m - s.n)) : 0;
   for (int h = hk * a.group; h < (hk + 1) * a.group; ++h)
     for (int i0 = first / R * R; i0 < s.n; i0 += R) {
       __syncthreads();
       const int live = min(R, s.n - i0);
-      load_tile<T, DP>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, live, a.D, a.scale);
-      load_tile<T, DP>(sO, head<T>(a.d_o, h, a.D), a.ld_o, s.q0 + i0, live, a.D, 1.0f);
+      load_tile<T, DP, R>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, live, a.D, a.scale);
+      load_tile<T, DP, R>(sO, head<T>(a.d_o, h, a.D), a.ld_o, s.q0 + i0, live, a.D, 1.0f);
       if (threadIdx.x < R) {
         const int64_t at = (int64_t)h * a.Tq + s.q0 + i0 + threadIdx.x;
         const bool in = (int)threadIdx.x < live;
         sStat[threadIdx.x] = RowStat{in ? a.lse[at] : 0.0f, in ? a.delta[at] : 0.0f};
       }
       __syncthreads();
-      float c[4][4] = {}, dp[4][4] = {};
-      scores<DP>(c, sK, sQ, ty, tx);
-      scores<DP>(dp, sV, sO, ty, tx);
+      float c[N][4] = {}, dp[N][4] = {};
+      scores<DP, N>(c, sK, sQ, ty, tx);
+      scores<DP, N>(dp, sV, sO, ty, tx);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = tx + 16 * j;  // the query row of the thread's column
         const RowStat st = sStat[i];
         const int end = i < live ? min(visible(a, s, i0 + i), s.m) - j0 : 0;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float p = 4 * ty + r < end ? expf(c[r][j] - st.lse) : 0.0f;
-          sP[(4 * ty + r) * PS + i] = p;
-          sS[(4 * ty + r) * PS + i] = p == 0.0f ? 0.0f : p * (dp[r][j] - st.delta);
+        for (int r = 0; r < N; ++r) {
+          const float p = N * ty + r < end ? expf(c[r][j] - st.lse) : 0.0f;
+          sP[(N * ty + r) * PS + i] = p;
+          sS[(N * ty + r) * PS + i] = p == 0.0f ? 0.0f : p * (dp[r][j] - st.delta);
         }
       }
       __syncwarp();
-      accumulate<DP>(dv, sP, sO, ty, tx);
-      accumulate<DP>(dk, sS, sQ, ty, tx);  // q holds the scale
+      accumulate<DP, N>(dv, sP, sO, ty, tx);
+      accumulate<DP, N>(dk, sS, sQ, ty, tx);  // q holds the scale
     }
-  const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-  store_rows<T, DP>(head<T>(a.dk, hk, a.D), a.ld_k, s.k0 + j0, rows, a.D, dk, one, ty, tx);
-  store_rows<T, DP>(head<T>(a.dv, hk, a.D), a.ld_v, s.k0 + j0, rows, a.D, dv, one, ty, tx);
+  float one[N];
+#pragma unroll
+  for (int r = 0; r < N; ++r) one[r] = 1.0f;
+  store_rows<T, DP, N>(head<T>(a.dk, hk, a.D), a.ld_k, s.k0 + j0, rows, a.D, dk, one, ty, tx);
+  store_rows<T, DP, N>(head<T>(a.dv, hk, a.D), a.ld_v, s.k0 + j0, rows, a.D, dv, one, ty, tx);
 }
 
 // delta: a warp for every query row and head. Rows in no sequence are formed too (nothing reads them).
@@ -361,21 +380,40 @@ cudaError_t launch_tiles(dim3 grid, size_t smem, const AttnArgs& a, cudaStream_t
   return cudaGetLastError();
 }
 
-template <typename T, int DP>
-cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
-  const size_t smem = (3 * tile_floats<DP>() + R * PS) * sizeof(float);
-  return launch_tiles<simt_forward_kernel<T, DP>>(dim3((unsigned)(a.Tq / R + a.B), a.Hq), smem, a, s);
+// Blocks of `rows` rows of the batch's tiles and heads, at most.
+int64_t blocks_of(int total, int B, int heads, int rows) { return ((int64_t)total / rows + B) * heads; }
+// Tiles of 16 rows where those of 64 would leave SMs without one.
+bool small(int total, int B, int heads) { return blocks_of(total, B, heads, R) <= tc::num_sms() / 2; }
+
+template <typename T, int DP, int N>
+cudaError_t forward_n(const AttnArgs& a, cudaStream_t s) {
+  constexpr int O = 16 * N;
+  const size_t smem = (tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + O * PS) * sizeof(float);
+  return launch_tiles<simt_forward_kernel<T, DP, N>>(dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
+}
+template <typename T, int DP, int N>
+cudaError_t dq_n(const AttnArgs& a, cudaStream_t s) {
+  constexpr int O = 16 * N;
+  const size_t smem = (2 * tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + (sizeof(T) == 2 ? 2 : 1) * O * PS) * sizeof(float);
+  return launch_tiles<simt_dq_kernel<T, DP, N>>(dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
+}
+template <typename T, int DP, int N>
+cudaError_t dkv_n(const AttnArgs& a, cudaStream_t s) {
+  constexpr int O = 16 * N;
+  const size_t smem = (2 * tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + 2 * O * PS) * sizeof(float);
+  return launch_tiles<simt_dkv_kernel<T, DP, N>>(dim3((unsigned)(a.Tk / O + a.B), a.Hkv), smem, a, s);
 }
 
 template <typename T, int DP>
+cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
+  return small(a.Tq, a.B, a.Hq) ? forward_n<T, DP, 1>(a, s) : forward_n<T, DP, 4>(a, s);
+}
+template <typename T, int DP>
 cudaError_t backward(const AttnArgs& a, cudaStream_t s) {
-  const size_t smem = (4 * tile_floats<DP>() + R * PS) * sizeof(float);
   cudaError_t e = cudaSuccess;
-  if (a.Tq > 0)
-    e = launch_tiles<simt_dq_kernel<T, DP>>(dim3((unsigned)(a.Tq / R + a.B), a.Hq),
-                                            smem + (sizeof(T) == 2 ? R * PS * sizeof(float) : 0), a, s);
+  if (a.Tq > 0) e = small(a.Tq, a.B, a.Hq) ? dq_n<T, DP, 1>(a, s) : dq_n<T, DP, 4>(a, s);
   if (e != cudaSuccess || a.Tk == 0) return e;
-  return launch_tiles<simt_dkv_kernel<T, DP>>(dim3((unsigned)(a.Tk / R + a.B), a.Hkv), smem + R * PS * sizeof(float), a, s);
+  return small(a.Tk, a.B, a.Hkv) ? dkv_n<T, DP, 1>(a, s) : dkv_n<T, DP, 4>(a, s);
 }
 
 }  // namespace
