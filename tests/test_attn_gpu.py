@@ -590,3 +590,16 @@ def test_the_smallest_and_largest_scale(dt, D, n, m, scale):
         eps = torch.finfo(dt).eps / 2
         assert ((o[:n, h].double() - want).abs() <= eps * want.abs() + 2.0 ** -24 * m * 6).all()
         assert ((lse[h, :n].double() - want_lse).abs() <= 2.0 ** -24 * m * want_lse.abs()).all()
+
+
+@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("dt,D,packed", [(FP, 20, False), (FP, 64, True), (FP, 98, False), (FP, 128, False), (BF, 20, True), (BF, 50, False),
+                                         (BF, 100, False)])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (6, 1)])
+def test_fma_units_with_many_and_few_heads(dt, D, packed, Hq, Hkv, causal):
+    """Tiles of 64 rows (8 heads, both ways) and of 16 (one key head) over every edge."""
+    b = Batch(same(EDGES), Hq, Hkv, D, dt, causal=causal, packed=packed, seed=D)
+    o, lse = b.forward()
+    b.check_forward(o, lse)
+    b.check_backward(*b.backward(o, lse))
+    b.check_status()

@@ -8,7 +8,7 @@
 // A block of 256 threads owns 64 query rows (dk, dv: 64 key rows), or 16 of a small batch, and goes over the
 // other side in tiles of 64, with the running maximum and sum of the softmax; scores are never stored. Every
 // thread forms 4 x 4 (1 x 4) scores, and 4 rows (1) x DP / 16 columns of the results in registers. Bound by FMA issue
-// (16384 tokens, 32 heads of 128, causal: 82 ms, 27 TFLOP/s): two 64 x 64 x D products a tile forward,
+// (16384 tokens, 8 query and 2 key heads of 128, causal: 14.6 ms, 38 TFLOP/s): two 64 x 64 x D products a tile forward,
 // five backward (in two kernels, which form the scores and do . v once more each; in return no result is
 // added to by two blocks, so the bits never change). From bf16 tensors delta carries the rounding of o:
 // their dq forms the mean key too and puts both right, as in attn_tc_bwd.cu.
@@ -382,8 +382,10 @@ cudaError_t launch_tiles(dim3 grid, size_t smem, const AttnArgs& a, cudaStream_t
 
 // Blocks of `rows` rows of the batch's tiles and heads, at most.
 int64_t blocks_of(int total, int B, int heads, int rows) { return ((int64_t)total / rows + B) * heads; }
-// Tiles of 16 rows where those of 64 would leave SMs without one.
-bool small(int total, int B, int heads) { return blocks_of(total, B, heads, R) <= tc::num_sms() / 2; }
+// Tiles of 16 rows where those of 64 would leave most SMs without one. Forward and backward together with tiles
+// of 64 and of 16, causal, by the forward's blocks of 64: 24 (256 tokens, heads of 32) 53 and 37 us, 40 (512,
+// heads of 64) 148 and 103, 72 (1024, heads of 128) 302 and 364, 136 (1024, heads of 32) 250 and 296.
+bool small(int total, int B, int heads) { return blocks_of(total, B, heads, R) <= tc::num_sms() * 2 / 5; }
 
 template <typename T, int DP, int N>
 cudaError_t forward_n(const AttnArgs& a, cudaStream_t s) {
