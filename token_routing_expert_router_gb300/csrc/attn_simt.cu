@@ -83,7 +83,7 @@ struct Cols {
 template <int DP, int N>
 __device__ __forceinline__ void accumulate(float (&acc)[N][DP / 16], const float* w, const float* y, int ty, int tx) {
   constexpr int LD = DP + 4, kN = Cols<DP>::kN, kV = Cols<DP>::kV;
-#pragma unroll 2
+#pragma unroll(N == 1 ? 4 : 2)  // a row a thread is little work between loads
   for (int j0 = 0; j0 < R; j0 += 4) {
     float p[N][4];  // [row][j]
 #pragma unroll
@@ -223,9 +223,9 @@ struct RowStat {
   float lse, delta;
 };
 
-// dq of 64 query rows of a head.
+// dq of 16 N query rows of a head.
 template <typename T, int DP, int N>
-__global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
+__device__ __forceinline__ void dq_rows(const AttnArgs& a, int block, int h) {
   constexpr int O = 16 * N;  // rows of the block
   extern __shared__ float4 smem4[];
   float* sQ = reinterpret_cast<float*>(smem4);
@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
   float* sP = sV + tile_floats<DP>(R);
   float* sM = sP + O * PS;  // kRounded: P, for the mean key
   constexpr bool kRounded = sizeof(T) == 2;
-  const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   __shared__ int sFind[kThreads / 32 + 3];
-  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, O, true, blockIdx.x == 0 && h == 0, sFind);
+  const Tile t = find_tile<kThreads, false>(a, block, O, true, block == 0 && h == 0, sFind);
   if (t.b < 0) return;
   const Seq s = load_seq(a, t.b, true, false);
   const int i0 = (t.count - 1 - t.index) * O, rows = min(O, s.n - i0);
@@ -293,10 +293,10 @@ __global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
   store_rows<T, DP, N>(head<T>(a.dq, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, acc, f, ty, tx);
 }
 
-// dk and dv of 64 key rows of a key head: over the query rows that see them, of every query head of
+// dk and dv of 16 N key rows of a key head: over the query rows that see them, of every query head of
 // its group. Scores are transposed: key rows by query rows.
 template <typename T, int DP, int N>
-__global__ void __launch_bounds__(kThreads) simt_dkv_kernel(const AttnArgs a) {
+__device__ __forceinline__ void dkv_rows(const AttnArgs& a, int block, int hk) {
   constexpr int O = 16 * N;  // rows of the block
   extern __shared__ float4 smem4[];
   float* sK = reinterpret_cast<float*>(smem4);
@@ -306,9 +306,9 @@ __global__ void __launch_bounds__(kThreads) simt_dkv_kernel(const AttnArgs a) {
   float* sP = sO + tile_floats<DP>(R);
   float* sS = sP + O * PS;
   __shared__ RowStat sStat[R];
-  const int hk = blockIdx.y, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   __shared__ int sFind[kThreads / 32 + 3];
-  const Tile t = find_tile<kThreads, true>(a, blockIdx.x, O, true, blockIdx.x == 0 && hk == 0, sFind);
+  const Tile t = find_tile<kThreads, true>(a, block, O, true, block == 0 && hk == 0, sFind);
   if (t.b < 0) return;
   const Seq s = load_seq(a, t.b, true, false);
   const int j0 = t.index * O, rows = min(O, s.m - j0);
@@ -355,9 +355,29 @@ __global__ void __launch_bounds__(kThreads) simt_dkv_kernel(const AttnArgs a) {
   store_rows<T, DP, N>(head<T>(a.dv, hk, a.D), a.ld_v, s.k0 + j0, rows, a.D, dv, one, ty, tx);
 }
 
+template <typename T, int DP, int N>
+__global__ void __launch_bounds__(kThreads) simt_dq_kernel(const AttnArgs a) {
+  dq_rows<T, DP, N>(a, blockIdx.x, blockIdx.y);
+}
+template <typename T, int DP, int N>
+__global__ void __launch_bounds__(kThreads) simt_dkv_kernel(const AttnArgs a) {
+  dkv_rows<T, DP, N>(a, blockIdx.x, blockIdx.y);
+}
+// Both of a small batch, the key tiles first (they take longer): with fp32 tensors dq leaves delta alone. Set up
+// beside delta, and one launch less: 30 -> 23 us (256 tokens). Larger ones are launched one after the other: blocks
+// that are set up early crowd the SMs that are free first (1024 tokens of 8 heads: 187 -> 263 us).
+template <int DP>
+__global__ void __launch_bounds__(kThreads) simt_both_kernel(const AttnArgs a, int key_tiles, int query_tiles) {
+  after_previous();
+  const int i = blockIdx.x - key_tiles * a.Hkv;
+  if (i < 0) dkv_rows<float, DP, 1>(a, blockIdx.x % key_tiles, blockIdx.x / key_tiles);
+  else dq_rows<float, DP, 1>(a, i % query_tiles, i / query_tiles);
+}
+
 // delta: a warp for every query row and head. Rows in no sequence are formed too (nothing reads them).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) delta_kernel(const AttnArgs a) {
+  let_next_begin();
   const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (i >= (int64_t)a.Tq * a.Hq) return;
@@ -372,12 +392,14 @@ __global__ void __launch_bounds__(kThreads) delta_kernel(const AttnArgs a) {
   if (lane == 0) a.delta[(int64_t)h * a.Tq + row] = sum;
 }
 
-template <void (*KERN)(AttnArgs)>
-cudaError_t launch_tiles(dim3 grid, size_t smem, const AttnArgs& a, cudaStream_t s) {
-  static const cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  KERN<<<grid, kThreads, smem, s>>>(a);
+cudaError_t launch_tiles(void (*kern)(AttnArgs), cudaError_t attribute, dim3 grid, size_t smem, const AttnArgs& a, cudaStream_t s) {
+  if (attribute != cudaSuccess) return attribute;
+  kern<<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
+}
+template <typename K>
+cudaError_t allow(K* kern, size_t smem) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
 // Blocks of `rows` rows of the batch's tiles and heads, at most.
@@ -390,20 +412,34 @@ bool small(int total, int B, int heads) { return blocks_of(total, B, heads, R) <
 template <typename T, int DP, int N>
 cudaError_t forward_n(const AttnArgs& a, cudaStream_t s) {
   constexpr int O = 16 * N;
-  const size_t smem = (tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + O * PS) * sizeof(float);
-  return launch_tiles<simt_forward_kernel<T, DP, N>>(dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
+  constexpr size_t smem = (tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + O * PS) * sizeof(float);
+  static const cudaError_t e = allow(simt_forward_kernel<T, DP, N>, smem);
+  return launch_tiles(simt_forward_kernel<T, DP, N>, e, dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
 }
 template <typename T, int DP, int N>
 cudaError_t dq_n(const AttnArgs& a, cudaStream_t s) {
   constexpr int O = 16 * N;
-  const size_t smem = (2 * tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + (sizeof(T) == 2 ? 2 : 1) * O * PS) * sizeof(float);
-  return launch_tiles<simt_dq_kernel<T, DP, N>>(dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
+  constexpr size_t smem = (2 * tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + (sizeof(T) == 2 ? 2 : 1) * O * PS) * sizeof(float);
+  static const cudaError_t e = allow(simt_dq_kernel<T, DP, N>, smem);
+  return launch_tiles(simt_dq_kernel<T, DP, N>, e, dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
+}
+template <int DP>
+constexpr size_t dkv_bytes(int O) {
+  return (2 * tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + 2 * O * PS) * sizeof(float);
 }
 template <typename T, int DP, int N>
 cudaError_t dkv_n(const AttnArgs& a, cudaStream_t s) {
   constexpr int O = 16 * N;
-  const size_t smem = (2 * tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + 2 * O * PS) * sizeof(float);
-  return launch_tiles<simt_dkv_kernel<T, DP, N>>(dim3((unsigned)(a.Tk / O + a.B), a.Hkv), smem, a, s);
+  static const cudaError_t e = allow(simt_dkv_kernel<T, DP, N>, dkv_bytes<DP>(O));
+  return launch_tiles(simt_dkv_kernel<T, DP, N>, e, dim3((unsigned)(a.Tk / O + a.B), a.Hkv), dkv_bytes<DP>(O), a, s);
+}
+template <int DP>
+cudaError_t both(const AttnArgs& a, cudaStream_t s) {
+  static const cudaError_t e = allow(simt_both_kernel<DP>, dkv_bytes<DP>(16));  // more than dq's
+  if (e != cudaSuccess) return e;
+  const int key_tiles = a.Tk / 16 + a.B, query_tiles = a.Tq / 16 + a.B;
+  return launch_after_smem(simt_both_kernel<DP>, dim3((unsigned)(key_tiles * a.Hkv + query_tiles * a.Hq)), kThreads, dkv_bytes<DP>(16),
+                           s, a, key_tiles, query_tiles);
 }
 
 template <typename T, int DP>
@@ -412,10 +448,14 @@ cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
 }
 template <typename T, int DP>
 cudaError_t backward(const AttnArgs& a, cudaStream_t s) {
+  const bool few_queries = small(a.Tq, a.B, a.Hq), few_keys = small(a.Tk, a.B, a.Hkv);
+  // an SM for each: 204 blocks (512 tokens) took 87 us in one launch and 84 in two
+  const bool together = blocks_of(a.Tq, a.B, a.Hq, 16) + blocks_of(a.Tk, a.B, a.Hkv, 16) <= tc::num_sms();
+  if (sizeof(T) == 4 && together && few_queries && few_keys && a.Tq > 0 && a.Tk > 0) return both<DP>(a, s);
   cudaError_t e = cudaSuccess;
-  if (a.Tq > 0) e = small(a.Tq, a.B, a.Hq) ? dq_n<T, DP, 1>(a, s) : dq_n<T, DP, 4>(a, s);
+  if (a.Tq > 0) e = few_queries ? dq_n<T, DP, 1>(a, s) : dq_n<T, DP, 4>(a, s);
   if (e != cudaSuccess || a.Tk == 0) return e;
-  return small(a.Tk, a.B, a.Hkv) ? dkv_n<T, DP, 1>(a, s) : dkv_n<T, DP, 4>(a, s);
+  return few_keys ? dkv_n<T, DP, 1>(a, s) : dkv_n<T, DP, 4>(a, s);
 }
 
 }  // namespace
