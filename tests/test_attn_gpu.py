@@ -603,3 +603,24 @@ def test_fma_units_with_many_and_few_heads(dt, D, packed, Hq, Hkv, causal):
     b.check_forward(o, lse)
     b.check_backward(*b.backward(o, lse))
     b.check_status()
+
+
+@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("D", [1, 32, 60, 128])
+@pytest.mark.parametrize("lens,place", [(same([1, 0, 63, 64, 2, 17, 16]), "self"), ([(5, 40), (0, 9), (17, 3), (33, 0), (16, 129)], "cache")])
+def test_small_fp32_batches(lens, place, D, causal):
+    """dq beside dk and dv in one launch, captured and replayed behind other work too."""
+    b = Batch(lens, 2, 1, D, FP, causal=causal, place=place, seed=D)
+    o, lse = b.forward()
+    b.check_forward(o, lse)
+    grads = b.backward(o, lse)
+    b.check_backward(*grads)
+    b.check_status()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, lse2 = b.forward()
+        grads2 = b.backward(o2, lse2)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(x, y) for x, y in zip(grads, grads2))
