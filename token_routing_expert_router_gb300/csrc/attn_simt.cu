@@ -59,7 +59,7 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
 template <int DP, int N>
 __device__ __forceinline__ void scores(float (&c)[N][4], const float* x, const float* y, int ty, int tx) {
   constexpr int LD = DP + 4;
-#pragma unroll 4
+#pragma unroll(N == 1 ? 8 : 4)
   for (int d = 0; d < DP; d += 4) {
     float4 a[N], b[4];
 #pragma unroll
@@ -83,7 +83,7 @@ struct Cols {
 template <int DP, int N>
 __device__ __forceinline__ void accumulate(float (&acc)[N][DP / 16], const float* w, const float* y, int ty, int tx) {
   constexpr int LD = DP + 4, kN = Cols<DP>::kN, kV = Cols<DP>::kV;
-#pragma unroll(N == 1 ? 4 : 2)  // a row a thread is little work between loads
+#pragma unroll(N == 1 ? 8 : 2)  // a row a thread is little work between loads
   for (int j0 = 0; j0 < R; j0 += 4) {
     float p[N][4];  // [row][j]
 #pragma unroll
@@ -101,8 +101,9 @@ __device__ __forceinline__ void accumulate(float (&acc)[N][DP / 16], const float
           const float4 t = *reinterpret_cast<const float4*>(src);
           v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
         } else {
-#pragma unroll
-          for (int l = 0; l < kV; ++l) v[l] = src[l];
+          static_assert(kV == 2);
+          const float2 t = *reinterpret_cast<const float2*>(src);
+          v[0] = t.x, v[1] = t.y;
         }
 #pragma unroll
         for (int r = 0; r < N; ++r)
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) simt_dkv_kernel(const AttnArgs a) {
   dkv_rows<T, DP, N>(a, blockIdx.x, blockIdx.y);
 }
 // Both of a small batch, the key tiles first (they take longer): with fp32 tensors dq leaves delta alone. Set up
-// beside delta, and one launch less: 30 -> 23 us (256 tokens). Larger ones are launched one after the other: blocks
+// beside delta, and one launch less: 30 -> 22 us (256 tokens). Larger ones are launched one after the other: blocks
 // that are set up early crowd the SMs that are free first (1024 tokens of 8 heads: 187 -> 263 us).
 template <int DP>
 __global__ void __launch_bounds__(kThreads) simt_both_kernel(const AttnArgs a, int key_tiles, int query_tiles) {
