@@ -620,11 +620,12 @@ moe_status_t moe_attn(const moe_attn_config_t* cfg, const void* q, const void* k
  *     dv_j = sum_i p_ij d_o_i;  dk_j = scale sum_i ds_ij q_i;  dq_i = scale sum_j ds_ij k_j
  * (dk and dv over every query head of their group). d_o has o's rows and stride, dq, dk and dv those
  * of q, k and v; rows in a sequence are written (zeros for keys that nothing sees), others not
- * touched. lse is fp32: p is off by up to 2^-22 |s| of itself, and means nothing beyond |s| = 2^22. The keys of the sequences must lie one behind the other: a sequence whose keys begin
- * before those of the one in front end sets MOE_ERR_DEVICE_BAD_INPUT and has no keys. With bf16
- * tensors p and ds are rounded to bf16 for their products; d_o . o, which carries o's rounding, is put right by
- * the sum of a row's ds. Outputs must not overlap inputs or each
- * other. ws: moe_attn_backward_workspace_size bytes. No atomics on sums: the same bits on every run. */
+ * touched. lse is fp32: p is off by up to 2^-22 |s| of itself, and means nothing beyond |s| = 2^22.
+ * The keys of the sequences must lie one behind the other: of the sequences in range, one with keys
+ * that begin before those of any other in front of it end sets MOE_ERR_DEVICE_BAD_INPUT and has no
+ * keys. With bf16 tensors p and ds are rounded to bf16 for their products; d_o . o, which carries o's
+ * rounding, is put right by the sum of a row's ds. Outputs must not overlap inputs or each other.
+ * ws: moe_attn_backward_workspace_size bytes. No atomics on sums: the same bits on every run. */
 moe_status_t moe_attn_backward_workspace_size(const moe_attn_config_t* cfg, size_t* bytes);
 moe_status_t moe_attn_backward(const moe_attn_config_t* cfg, const void* q, const void* k, const void* v,
                                const int32_t* q_start, const int32_t* k_start, const int32_t* k_len, const void* o,

@@ -1,0 +1,106 @@
+"""Attention of batches with empty, refused and overlapping sequences."""
+import pytest
+import torch
+
+import token_routing_expert_router_gb300 as moe
+from test_attn_gpu import Batch
+from test_step_gpu import BF, FP, gen, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _built(lib):
+    pass
+
+
+# Hq, Hkv, D, dtype: the tensor cores, the FMA units with bf16, and with fp32 by tiles of 64 rows and of 16
+KERNELS = [(4, 2, 64, BF), (4, 1, 128, BF), (2, 1, 36, BF), (32, 32, 32, FP), (2, 1, 64, FP)]
+
+
+@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("Hq,Hkv,D,dt", KERNELS)
+def test_backward_with_empty_places(Hq, Hkv, D, dt, causal):
+    """Places of a batch without keys, with and without queries, whose start is any row: nothing to report, and
+    the sequences around them have their gradients."""
+    b = Batch([(70, 90), (0, 0), (130, 200), (5, 0), (33, 40), (0, 0), (64, 64)], Hq, Hkv, D, dt, causal=causal, place="cache",
+              seed=D)
+    for at, row in ((1, 0), (3, b.Tk), (5, 7)):
+        b.k_start[at] = row
+    o, lse = b.forward()
+    b.check_forward(o, lse)
+    b.check_status()
+    grads = b.backward(o, lse)
+    assert moe.moe_read_status(b.bws) == moe.MOE_OK
+    b.check_backward(*grads)
+
+
+@pytest.mark.parametrize("name,value", [("k_len", "Tk"), ("k_start", "Tk"), ("k_start", -3), ("k_len", -1)])
+@pytest.mark.parametrize("Hq,Hkv,D,dt", KERNELS)
+def test_backward_behind_keys_out_of_range(Hq, Hkv, D, dt, name, value):
+    """A sequence whose keys are not there takes none from the ones behind it."""
+    lens = [(20, 40), (30, 50), (60, 80)]
+    b = Batch(lens, Hq, Hkv, D, dt, place="cache", seed=D)
+    o, lse = b.forward()
+    want = b.backward(o, lse)
+    getattr(b, name)[1] = b.Tk if value == "Tk" else value
+    got = b.backward(o, lse)
+    assert moe.moe_read_status(b.bws) == moe.MOE_ERR_DEVICE_BAD_INPUT
+    for i in (0, 2):
+        q, k = slice(b.q_at[i], b.q_at[i] + lens[i][0]), slice(b.k_at[i], b.k_at[i] + lens[i][1])
+        for x, y, rows in zip(got, want, (q, k, k)):
+            assert torch.equal(x[rows], y[rows])
+    assert not got[0][20:50].any()
+    assert all((x[b.k_at[1]:b.k_at[1] + 50] == 7).all() for x in got[1:])
+
+
+def _keys_apart(start, length, Tk):
+    """Which sequences keep their keys in the backward: those in range that do not begin before one in front
+    of them, in range too, ends."""
+    end, keep = 0, []
+    for k0, m in zip(start, length):
+        inside = 0 <= k0 <= Tk and 0 <= m <= Tk - k0
+        keep.append(inside and (m == 0 or k0 >= end))
+        if inside and m:
+            end = max(end, k0 + m)
+    return keep
+
+
+OVERLAPS = [[(0, 100), (0, 50), (60, 40)], [(0, 100), (0, 50), (60, 40), (100, 30)], [(50, 30), (0, 60), (10, 20), (80, 0), (80, 40)],
+            [(0, 90), (40, 400), (60, 20), (90, 30)], [(10, 5)] * 4]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dt", KERNELS)
+@pytest.mark.parametrize("keys", OVERLAPS + ["many"])
+def test_backward_of_overlapping_keys(keys, Hq, Hkv, D, dt):
+    """Every key's gradient is written by one sequence: the others have no keys, and are reported."""
+    if keys == "many":  # several sequences to a thread
+        g = torch.Generator()
+        g.manual_seed(3)
+        keys, at = [], 0
+        for i in range(700):
+            m = int(torch.randint(0, 6, (1,), generator=g))
+            back = int(torch.randint(0, 4, (1,), generator=g)) if i % 5 == 4 else 0
+            keys.append((max(0, at - back), m))
+            at = max(at, keys[-1][0] + m)
+        Hq, Hkv = Hq // Hkv, 1
+    Tk = max(k0 + m for k0, m in keys) + 3
+    n = 2 if len(keys) > 100 else 40
+    b = Batch([(n, 1)] * len(keys), Hq, Hkv, D, dt, place="cache", seed=7)
+    b.cfg = moe.MoEAttnConfig.make(**{**b.cfg.as_dict(), "Tk": Tk})
+    b.Tk = Tk
+    b.k, b.v = normal(gen(1), Tk, Hkv, D, dtype=dt), normal(gen(2), Tk, Hkv, D, dtype=dt)
+    b.k_start.copy_(torch.tensor([k for k, _ in keys], dtype=torch.int32))
+    b.k_len.copy_(torch.tensor([m for _, m in keys], dtype=torch.int32))
+    b.bws = torch.empty(moe.moe_attn_backward_workspace_size(b.cfg), dtype=torch.uint8, device="cuda")
+    moe.moe_workspace_init(b.bws)
+    keep = _keys_apart([k for k, _ in keys], [m for _, m in keys], Tk)
+    assert not all(keep)
+    o, lse = b.forward()
+    got = b.backward(o, lse)
+    assert moe.moe_read_status(b.bws) == moe.MOE_ERR_DEVICE_BAD_INPUT
+    b.lens = [(n, m if ok else 0) for (_, m), ok in zip(keys, keep)]
+    b.k_at = [k for k, _ in keys]
+    b.check_backward(*got)
+    for x, y in zip(got, b.backward(o, lse)):
+        assert torch.equal(x, y)

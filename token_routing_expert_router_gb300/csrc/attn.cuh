@@ -29,10 +29,8 @@ struct Seq {
 };
 
 // Sequence b, with what is out of range left out: no rows for query rows that are not inside q or
-// more than max_q, no keys for key rows that are not inside k. With `apart` a sequence whose keys
-// begin before the ones of the sequence in front of it end has no keys either (the backward writes
-// every key's gradient once).
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, bool apart, bool report) {
+// more than max_q, no keys for key rows that are not inside k.
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, bool report) {
   Seq s;
   s.q0 = __ldg(a.q_start + b);
   const int q1 = __ldg(a.q_start + b + 1);
@@ -41,9 +39,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, bool apart, bo
   if (a.k_start) {
     s.k0 = __ldg(a.k_start + b);
     s.m = __ldg(a.k_len + b);
-    bool bad_k = s.k0 < 0 || s.m < 0 || s.k0 > a.Tk || s.m > a.Tk - s.k0;
-    if (apart && b > 0 && !bad_k)
-      bad_k = (int64_t)__ldg(a.k_start + b - 1) + __ldg(a.k_len + b - 1) > s.k0;
+    const bool bad_k = s.k0 < 0 || s.m < 0 || s.k0 > a.Tk || s.m > a.Tk - s.k0;
     if (bad_k) s.k0 = s.m = 0;
     bad |= bad_k;
   } else {
@@ -54,29 +50,75 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, bool apart, bo
   return s;
 }
 
+// The backward writes every key's gradient once: of the sequences in range, one whose keys begin before
+// those of another in front of it end has none. end: of those in front, then of s too. True: s has lost its keys.
+__device__ __forceinline__ int keys_end(const Seq& s) { return s.m > 0 ? s.k0 + s.m : 0; }
+__device__ __forceinline__ bool hold_apart(Seq& s, int& end) {
+  const bool lost = s.m > 0 && s.k0 < end;
+  end = max(end, keys_end(s));
+  if (lost) s.k0 = s.m = 0;
+  return lost;
+}
+
+// The largest v (>= 0) of the threads in front of this one, and of all. Every thread calls it.
+// scratch: THREADS / 32 words of shared memory, read until the next barrier.
+struct Largest {
+  int before, all;
+};
+template <int THREADS>
+__device__ __forceinline__ Largest largest_before(int v, int* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v = max(v, o);
+  }
+  if (lane == 31) scratch[warp] = v;
+  Largest l{__shfl_up_sync(0xffffffffu, v, 1), 0};
+  if (lane == 0) l.before = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) l.before = max(l.before, scratch[w]);
+    l.all = max(l.all, scratch[w]);
+  }
+  return l;
+}
+
 struct Tile {
   int b;      // sequence, or -1: no such tile
   int index;  // of its tiles, from 0
   int count;  // of the sequence's tiles
+  Seq s;
 };
 
 // The block's tile `want` of all sequences' tiles of `rows` query rows (KEYS: key rows), one after
 // the other. Every thread calls it. Each thread takes the sequences of an equal share of B, the
-// block scans the shares' tiles, and the thread whose share holds the wanted one walks it. Up to
-// 256 sequences that is one load and two exchanges. scratch: THREADS / 32 + 3 words of shared memory.
-template <int THREADS, bool KEYS>
-__device__ Tile find_tile(const AttnArgs& a, int64_t want, int rows, bool apart, bool report, int* scratch) {
+// block scans the shares' tiles (APART: after the ends of their keys), and the thread whose share holds
+// the wanted one walks it. Up to 256 sequences that is one load and two exchanges, and one more.
+template <int THREADS>
+constexpr int kFindWords = 2 * (THREADS / 32) + 4;
+template <int THREADS, bool KEYS, bool APART>
+__device__ Tile find_tile(const AttnArgs& a, int64_t want, int rows, bool report, int (&scratch)[kFindWords<THREADS>]) {
   int* sWarp = scratch;
-  volatile int* sTile = scratch + THREADS / 32;
+  volatile int* sTile = scratch + 2 * (THREADS / 32);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = (a.B + THREADS - 1) / THREADS;
   const int b0 = min(a.B, tid * share), b1 = min(a.B, b0 + share);
-  auto tiles = [&](int b, bool tell) {
-    const Seq s = load_seq(a, b, apart, tell);
+  int front = 0;  // where the keys in front of the share end
+  if constexpr (APART) {
+    int end = 0;
+    for (int b = b0; b < b1; ++b) end = max(end, keys_end(load_seq(a, b, false)));
+    front = largest_before<THREADS>(end, scratch + THREADS / 32).before;
+  }
+  auto tiles = [&](int b, int& end, bool& lost, bool tell) {
+    Seq s = load_seq(a, b, tell);
+    if (APART && (lost = hold_apart(s, end)) && tell) set_status(a.status, MOE_ERR_DEVICE_BAD_INPUT, b);
     return ((KEYS ? s.m : s.n) + rows - 1) / rows;
   };
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles(b, report);
+  int mine = 0, end = front;
+  bool lost = false;
+  for (int b = b0; b < b1; ++b) mine += tiles(b, end, lost, report);
   int inc = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -90,17 +132,23 @@ __device__ Tile find_tile(const AttnArgs& a, int64_t want, int rows, bool apart,
   for (int w = 0; w < warp; ++w) before += sWarp[w];
   if (want >= before && want < before + mine) {
     int left = (int)want - before;
+    end = front;
     for (int b = b0; b < b1; ++b) {
-      const int n = tiles(b, false);
+      const int n = tiles(b, end, lost, false);
       if (left < n) {
-        sTile[0] = b, sTile[1] = left, sTile[2] = n;
+        sTile[0] = b, sTile[1] = left, sTile[2] = n, sTile[3] = lost;
         break;
       }
       left -= n;
     }
   }
   __syncthreads();
-  return Tile{sTile[0], sTile[1], sTile[2]};
+  Tile t{sTile[0], sTile[1], sTile[2]};
+  if (t.b >= 0) {
+    t.s = load_seq(a, t.b, false);
+    if (APART && sTile[3]) t.s.k0 = t.s.m = 0;
+  }
+  return t;
 }
 
 // Keys that query row i of a sequence sees: [0, visible).

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p, int ro
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Line line = line_of(a, blockIdx.x, row_tiles);
-  const Seq s = load_seq(a, line.b, false, line.hk == 0 && line.r0 == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  const Seq s = load_seq(a, line.b, line.hk == 0 && line.r0 == 0 && blockIdx.y == 0 && threadIdx.x == 0);
   const int rows = min(R, s.n * a.group - line.r0);
   if (rows <= 0) return;
   // row r: query (r0 + r) / group of the sequence, head (r0 + r) % group of the key head's
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) few_join_kernel(const FewParams p, i
   after_previous();
   const AttnArgs& a = p.a;
   const Line line = line_of(a, blockIdx.x, row_tiles);
-  const Seq s = load_seq(a, line.b, false, false);
+  const Seq s = load_seq(a, line.b, false);
   const int rows = min(R, s.n * a.group - line.r0);
   const int64_t at = (int64_t)blockIdx.x * p.splits * R;
   for (int e = threadIdx.x; e < p.splits * R; e += kThreads) sStat[e % R][e / R] = e % R < rows ? p.stat[at + e] : float2{};

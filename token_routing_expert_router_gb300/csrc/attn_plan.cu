@@ -16,6 +16,7 @@ namespace {
 constexpr int kSort = 256;     // threads of a block
 constexpr int kFirst = 1024;   // sequences whose prefix is kept in shared memory
 constexpr int kClasses = 64;
+constexpr int kLost = (int)0x80000000;  // of a sequence's entry in the prefix: its keys are not its own
 constexpr int kAhead = 4;      // rows and heads whose loads a thread has in flight
 
 // Steps (inner tiles) of a tile of queries, or of a tile of keys for all packs of heads.
@@ -30,7 +31,7 @@ __device__ __forceinline__ int tile_steps(const AttnArgs& a, const PlanJob& j, c
 
 __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool report) {
   __shared__ int sKept[kFirst + 1];
-  __shared__ int sWarp[kSort / 32];
+  __shared__ int sWarp[kSort / 32], sEnd[kSort / 32];
   __shared__ unsigned long long sTotal;
   __shared__ int sMost, sSlots, sClass[kClasses];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -38,14 +39,20 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
   int* sFirst = a.B <= kFirst ? sKept : j.first;
   if (tid == 0) sTotal = 0, sMost = 0, sSlots = 0;
   if (tid < kClasses) sClass[tid] = 0;
-  int carry = 0;
+  int carry = 0, front = 0;  // tiles of the sequences before; where their keys end
   for (int b0 = 0; b0 < a.B; b0 += kSort) {
     const int b = b0 + tid;
-    int n = 0;
-    if (b < a.B) {
-      const Seq s = load_seq(a, b, apart, report);
-      n = ((j.keys ? s.m : s.n) + rows - 1) / rows;
+    Seq s{};
+    if (b < a.B) s = load_seq(a, b, report);
+    bool lost = false;
+    if (apart) {
+      const Largest l = largest_before<kSort>(keys_end(s), sEnd);
+      int end = max(front, l.before);
+      lost = hold_apart(s, end);
+      if (lost && report) set_status(a.status, MOE_ERR_DEVICE_BAD_INPUT, b);
+      front = max(front, l.all);
     }
+    const int n = ((j.keys ? s.m : s.n) + rows - 1) / rows;
     int inc = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -60,7 +67,7 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
       if (w < warp) before += sWarp[w];
       all += sWarp[w];
     }
-    if (b < a.B) sFirst[b] = before;
+    if (b < a.B) sFirst[b] = lost ? before | kLost : before;
     carry += all;
   }
   if (tid == 0) sFirst[a.B] = carry;
@@ -70,7 +77,7 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
     int lo = 0, hi = a.B - 1;  // the last sequence that begins at or before t
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (sFirst[mid] <= t) lo = mid;
+      if ((sFirst[mid] & ~kLost) <= t) lo = mid;
       else hi = mid - 1;
     }
     return lo;
@@ -80,8 +87,9 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
     int index, steps;
   };
   auto find = [&](int t) {
-    const int b = seq_of(t);
-    Found f{load_seq(a, b, apart, false), t - sFirst[b], 0};
+    const int b = seq_of(t), first = sFirst[b];
+    Found f{load_seq(a, b, false), t - (first & ~kLost), 0};
+    if (first & kLost) f.s.k0 = f.s.m = 0;
     f.steps = tile_steps(a, j, f.s, f.index);
     return f;
   };

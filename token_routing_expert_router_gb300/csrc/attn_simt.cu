@@ -154,10 +154,10 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a
   float* sV = sK + tile_floats<DP>(R);
   float* sP = sV + tile_floats<DP>(R);
   const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  __shared__ int sFind[kThreads / 32 + 3];
-  const Tile t = find_tile<kThreads, false>(a, blockIdx.x, O, false, blockIdx.x == 0 && h == 0, sFind);
+  __shared__ int sFind[kFindWords<kThreads>];
+  const Tile t = find_tile<kThreads, false, false>(a, blockIdx.x, O, blockIdx.x == 0 && h == 0, sFind);
   if (t.b < 0) return;
-  const Seq s = load_seq(a, t.b, false, false);
+  const Seq s = t.s;
   const int i0 = (t.count - 1 - t.index) * O, rows = min(O, s.n - i0);  // the longest first
   load_tile<T, DP, O>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, a.scale);
 
@@ -237,10 +237,10 @@ __device__ __forceinline__ void dq_rows(const AttnArgs& a, int block, int h) {
   float* sM = sP + O * PS;  // kRounded: P, for the mean key
   constexpr bool kRounded = sizeof(T) == 2;
   const int hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  __shared__ int sFind[kThreads / 32 + 3];
-  const Tile t = find_tile<kThreads, false>(a, block, O, true, block == 0 && h == 0, sFind);
+  __shared__ int sFind[kFindWords<kThreads>];
+  const Tile t = find_tile<kThreads, false, true>(a, block, O, block == 0 && h == 0, sFind);
   if (t.b < 0) return;
-  const Seq s = load_seq(a, t.b, true, false);
+  const Seq s = t.s;
   const int i0 = (t.count - 1 - t.index) * O, rows = min(O, s.n - i0);
   load_tile<T, DP, O>(sQ, head<T>(a.q, h, a.D), a.ld_q, s.q0 + i0, rows, a.D, a.scale);
   load_tile<T, DP, O>(sO, head<T>(a.d_o, h, a.D), a.ld_o, s.q0 + i0, rows, a.D, 1.0f);
@@ -308,10 +308,10 @@ __device__ __forceinline__ void dkv_rows(const AttnArgs& a, int block, int hk) {
   float* sS = sP + O * PS;
   __shared__ RowStat sStat[R];
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  __shared__ int sFind[kThreads / 32 + 3];
-  const Tile t = find_tile<kThreads, true>(a, block, O, true, block == 0 && hk == 0, sFind);
+  __shared__ int sFind[kFindWords<kThreads>];
+  const Tile t = find_tile<kThreads, true, true>(a, block, O, block == 0 && hk == 0, sFind);
   if (t.b < 0) return;
-  const Seq s = load_seq(a, t.b, true, false);
+  const Seq s = t.s;
   const int j0 = t.index * O, rows = min(O, s.m - j0);
   load_tile<T, DP, O>(sK, head<T>(a.k, hk, a.D), a.ld_k, s.k0 + j0, rows, a.D, 1.0f);
   load_tile<T, DP, O>(sV, head<T>(a.v, hk, a.D), a.ld_v, s.k0 + j0, rows, a.D, 1.0f);

@@ -84,7 +84,7 @@ __device__ void find_share(const StreamParams& p, int per, Share* out) {
   const int b0 = min(a.B, tid * each), b1 = min(a.B, b0 + each);
   int64_t mine = 0;
   int longest = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_turns(a, load_seq(a, b, false, blockIdx.x == 0), per, p.packs, longest);
+  for (int b = b0; b < b1; ++b) mine += seq_turns(a, load_seq(a, b, blockIdx.x == 0), per, p.packs, longest);
   int64_t inc = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -116,7 +116,7 @@ __device__ void find_share(const StreamParams& p, int per, Share* out) {
   if (u >= before && u < before + mine) {
     int64_t at = before;
     for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(a, b, false, false);
+      const Seq s = load_seq(a, b, false);
       const int64_t turns = seq_turns(a, s, per, p.packs, longest);
       if (u < at + turns) {
         int t = 0;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ===================== the share's parts
       int b = share.b, tile = share.tile, pack = share.pack;
       int64_t u = share.u, line = share.line;
-      Seq s = load_seq(a, b, false, false);
+      Seq s = load_seq(a, b, false);
       bool ok = true;
       for (int k = 0, end = 0; ok && !end; ++k) {
         Item it{};
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               pack = 0;
               if (++tile * per >= s.n && u < share.end) {
                 tile = 0;
-                do s = load_seq(a, ++b, false, false);
+                do s = load_seq(a, ++b, false);
                 while (s.n == 0);
               }
             }

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   after_previous();
   Seq only{};
-  if (!p.plan) only = load_seq(a, 0, false, blockIdx.x == 0 && threadIdx.x == 0);
+  if (!p.plan) only = load_seq(a, 0, blockIdx.x == 0 && threadIdx.x == 0);
   const int tiles = p.plan ? p.plan->count : (only.n + 2 * per - 1) / (2 * per), items = tiles * p.heads;
   struct Item {
     Seq s;
