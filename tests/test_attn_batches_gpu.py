@@ -1,10 +1,11 @@
-"""Attention of batches with empty, refused and overlapping sequences."""
+"""Attention of batches with empty, refused and overlapping sequences, and of
+long sums in fp32."""
 import pytest
 import torch
 
 import token_routing_expert_router_gb300 as moe
 from test_attn_gpu import Batch
-from test_step_gpu import BF, FP, gen, normal
+from test_step_gpu import BF, FP, U, gen, normal, within
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,62 @@ def test_backward_of_overlapping_keys(keys, Hq, Hkv, D, dt):
     b.check_backward(*got)
     for x, y in zip(got, b.backward(o, lse)):
         assert torch.equal(x, y)
+
+
+def _uniform(n, m, Hq, Hkv, D, seed):
+    """A batch whose scores are all 0 (every probability 1 / m) and whose rows are all alike."""
+    b = Batch([(n, m)], Hq, Hkv, D, FP, causal=0, place="cache", seed=seed)
+    g = gen(seed + 1)
+    row = torch.rand(2, Hq, D, generator=g, device="cuda") + 1.0
+    b.q[:n], b.do[:n] = row[0], row[1]
+    return b
+
+
+@pytest.mark.parametrize("D", [16, 128])
+@pytest.mark.parametrize("Hkv", [1, 32])
+def test_long_sums_of_key_gradients_in_fp32(Hkv, D):
+    """dk and dv over 32768 equal terms: an accumulator that takes them one after the other rounds every one
+    the same way."""
+    n, m, G = 8192, 64, 4
+    b = _uniform(n, m, Hkv * G, Hkv, D, 5)
+    at = slice(b.k_at[0], b.k_at[0] + m)
+    b.k[at] = 0
+    o, lse = b.forward()
+    _, dk, dv = b.backward(o, lse)
+    q, do = b.q[0].double().view(Hkv, G, D), b.do[0].double().view(Hkv, G, D)
+    v = b.v[at].double().transpose(0, 1)                       # [Hkv, m, D]
+    # sums of 64 terms each, and of their n G / 64 results; beside them p: lse's rounding and logf's (2 U each of
+    # 4.2), expf's 4 U; the scale on q, the products, the result: 32 U cover all of them
+    rel = (64 + n * G / 64 + 32) * U
+    want = (n / m * do.sum(1))[:, None].expand(Hkv, m, D)
+    within(dv[at].transpose(0, 1), want, rel * want.abs())
+    dp = torch.einsum("hgd,hmd->hgm", do, v)
+    mean = dp.mean(2, keepdim=True)
+    size = torch.einsum("hgd,hmd->hgm", do.abs(), v.abs())
+    # dp and delta: D products each; o: 64 terms, a division, its rounding
+    lost = (D + 8) * U * size + ((D + 8) + 64 + 32) * U * size.mean(2, keepdim=True)
+    ds = (dp - mean) / m
+    want = n * b.scale * torch.einsum("hgm,hgd->hmd", ds, q)
+    bound = n * b.scale * torch.einsum("hgm,hgd->hmd", lost / m + rel * ds.abs(), q)
+    within(dk[at].transpose(0, 1), want, bound)
+
+
+@pytest.mark.parametrize("D", [16, 128])
+@pytest.mark.parametrize("Hq", [1, 64])
+def test_long_sums_of_query_gradients_in_fp32(Hq, D):
+    """dq over 32768 equal terms."""
+    n, m = 64, 32768
+    b = _uniform(n, m, Hq, 1, D, 6)
+    b.q[:n] = 0
+    at = slice(b.k_at[0], b.k_at[0] + m)
+    row = torch.rand(2, D, generator=gen(9), device="cuda") + 1.0
+    sign = 1.0 - 2.0 * (torch.arange(m, device="cuda") % 2)
+    b.k[at], b.v[at] = (sign[:, None] * row[0])[:, None], (sign[:, None] * row[1])[:, None]
+    o, lse = b.forward()
+    dq, _, _ = b.backward(o, lse)
+    x = b.do[0].double() @ row[1].double()                    # [Hq]: do . v of the even keys; o and delta are 0
+    want = b.scale * x[:, None] * row[0].double()
+    # sums of 64 terms, and of their m / 64 results; p: 2 U each of lse's 10.4 twice, expf 4 U; x: D + 8 roundings;
+    # the scale, the products and the result; what o is not quite 0 by falls out, as the keys' signs do
+    rel = (64 + m / 64 + 64 + D + 8) * U
+    within(dq[:n], want.expand(n, Hq, D), rel * want.abs())

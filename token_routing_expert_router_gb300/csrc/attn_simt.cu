@@ -113,6 +113,18 @@ __device__ __forceinline__ void accumulate(float (&acc)[N][DP / 16], const float
   }
 }
 
+// The same with the tile's sums formed apart: a chain of 64 terms and one of the tiles, where rows over many tiles
+// would otherwise lose with every term (32768 equal terms: up to 4e-4 of the sum).
+template <int DP, int N>
+__device__ __forceinline__ void add_tile(float (&acc)[N][DP / 16], const float* w, const float* y, int ty, int tx) {
+  float fresh[N][DP / 16] = {};
+  accumulate<DP, N>(fresh, w, y, ty, tx);
+#pragma unroll
+  for (int r = 0; r < N; ++r)
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d) acc[r][d] += fresh[r][d];
+}
+
 template <typename T, int DP, int N>
 __device__ __forceinline__ void store_rows(void* base, int64_t ld, int64_t row0, int live, int D, const float (&acc)[N][DP / 16],
                                            const float (&f)[N], int ty, int tx) {
@@ -202,13 +214,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a
       for (int d = 0; d < DP / 16; ++d) acc[r][d] *= keep;
     }
     __syncwarp();  // a row's scores come from the 16 threads that use them
-    // the tile's sums apart, so that a long row's do not lose more with every tile
-    float fresh[N][DP / 16] = {};
-    accumulate<DP, N>(fresh, sP, sV, ty, tx);
-#pragma unroll
-    for (int r = 0; r < N; ++r)
-#pragma unroll
-      for (int d = 0; d < DP / 16; ++d) acc[r][d] += fresh[r][d];
+    add_tile<DP, N>(acc, sP, sV, ty, tx);
   }
   float f[N];
 #pragma unroll
@@ -275,8 +281,8 @@ __device__ __forceinline__ void dq_rows(const AttnArgs& a, int block, int h) {
       }
     }
     __syncwarp();
-    accumulate<DP, N>(acc, sP, sK, ty, tx);
-    if constexpr (kRounded) accumulate<DP, N>(mean, sM, sK, ty, tx);
+    add_tile<DP, N>(acc, sP, sK, ty, tx);
+    if constexpr (kRounded) add_tile<DP, N>(mean, sM, sK, ty, tx);
   }
   if constexpr (kRounded) {
 #pragma unroll
@@ -346,8 +352,8 @@ __device__ __forceinline__ void dkv_rows(const AttnArgs& a, int block, int hk) {
         }
       }
       __syncwarp();
-      accumulate<DP, N>(dv, sP, sO, ty, tx);
-      accumulate<DP, N>(dk, sS, sQ, ty, tx);  // q holds the scale
+      add_tile<DP, N>(dv, sP, sO, ty, tx);
+      add_tile<DP, N>(dk, sS, sQ, ty, tx);  // q holds the scale
     }
   float one[N];
 #pragma unroll
