@@ -604,13 +604,15 @@ typedef struct {
  * Rows of o and lse that are in no sequence are not touched, and key rows outside the sequences may
  * hold anything; a value that is not finite inside a sequence's keys may reach all of its outputs.
  * Sequences out of range (rows outside q, or more than max_q; keys outside k) set
- * MOE_ERR_DEVICE_BAD_INPUT and have no rows, or no keys. lse [Hq, Tq] fp32. Scores, sums and
- * outputs are held in fp32 (exponentials below 2^-126 are zero); with bf16 tensors exp(s - max) is
- * rounded to bf16, the operand type of its product with v. Rows may be strided views, aligned to their elements; bf16 rows of multiples
- * of 16 bytes (address, stride, D % 8 = 0) go to the tensor cores. o must not overlap an input.
- * ws: moe_attn_workspace_size bytes; after a MOE_ERR_TIMEOUT (here or in the backward) it has to be
- * initialised again. Deterministic: the same call gives the same bits (another batch around a
- * sequence, or another max_q, may cut its keys at other places). */
+ * MOE_ERR_DEVICE_BAD_INPUT and have no rows, or no keys. q_start must not decrease: where it does,
+ * which is reported too, and later sequences come back to rows of earlier ones, such rows may hold
+ * either's results, and rows may be left as they were. lse [Hq, Tq] fp32. Scores, sums and outputs
+ * are held in fp32 (exponentials below 2^-126 are zero); with bf16 tensors exp(s - max) is rounded to
+ * bf16, the operand type of its product with v. Rows may be strided views, aligned to their elements;
+ * bf16 rows of multiples of 16 bytes (address, stride, D % 8 = 0) go to the tensor cores. o must not
+ * overlap an input. ws: moe_attn_workspace_size bytes; after a MOE_ERR_TIMEOUT (here or in the
+ * backward) it has to be initialised again. Deterministic: the same call gives the same bits (another
+ * batch around a sequence, or another max_q, may cut its keys at other places). */
 moe_status_t moe_attn_workspace_size(const moe_attn_config_t* cfg, size_t* bytes);
 moe_status_t moe_attn(const moe_attn_config_t* cfg, const void* q, const void* k, const void* v, const int32_t* q_start,
                       const int32_t* k_start, const int32_t* k_len, void* o, float* lse, void* ws, moe_stream_t stream);

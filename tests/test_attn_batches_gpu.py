@@ -107,6 +107,34 @@ def test_backward_of_overlapping_keys(keys, Hq, Hkv, D, dt):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("rows,Hq,D,dt", [(140000, 128, 8, BF), (4300001, 1, 1, FP)])
+def test_rows_that_come_back_65536_times(rows, Hq, D, dt):
+    """A q_start that goes back to 0 for every second sequence: reported, also where the sequences' tiles
+    together are more than 32 bits count, and nothing outside the rows is written."""
+    B, code = 65536, moe.BF16 if dt == BF else moe.F32
+    q, o = (torch.zeros(rows + 2, Hq, D, device="cuda", dtype=dt) for _ in range(2))
+    o[0], o[-1] = 7, 7
+    lse = torch.full((Hq + 2, rows), 7.0, device="cuda")
+    q_start = torch.zeros(B + 1, device="cuda", dtype=torch.int32)
+    q_start[1::2] = rows
+    k, v = torch.ones(1, 1, D, device="cuda", dtype=dt), torch.full((1, 1, D), 3.0, device="cuda", dtype=dt)
+    k_start, k_len = torch.zeros(B, device="cuda", dtype=torch.int32), torch.ones(B, device="cuda", dtype=torch.int32)
+    cfg = moe.MoEAttnConfig.make(Tq=rows, Tk=1, B=B, Hq=Hq, Hkv=1, D=D, causal=0, act_dtype=code)
+    ws = torch.empty(max(moe.moe_attn_workspace_size(cfg), moe.moe_attn_backward_workspace_size(cfg)), dtype=torch.uint8, device="cuda")
+    moe.moe_workspace_init(ws)
+    moe.moe_attn(cfg, q[1:-1], k, v, q_start, k_start, k_len, o[1:-1], lse[1:-1], ws)
+    assert moe.moe_read_status(ws) == moe.MOE_ERR_DEVICE_BAD_INPUT
+    # every row's only key has the score 0
+    assert ((o[1:-1] == 3) | (o[1:-1] == 0)).all() and ((lse[1:-1] == 0) | (lse[1:-1] == 7)).all()
+    assert (o[0] == 7).all() and (o[-1] == 7).all() and (lse[0] == 7).all() and (lse[-1] == 7).all()
+    dq, dkv = torch.zeros_like(q), torch.zeros(2, 3, 1, D, device="cuda", dtype=dt)
+    dq[0], dq[-1] = 7, 7
+    moe.moe_attn_backward(cfg, q[1:-1], k, v, q_start, k_start, k_len, o[1:-1], lse[1:-1], q[1:-1], dq[1:-1], dkv[0, 1:2], dkv[1, 1:2], ws)
+    assert moe.moe_read_status(ws) == moe.MOE_ERR_DEVICE_BAD_INPUT
+    assert not dq[1:-1].any() and (dq[0] == 7).all() and (dq[-1] == 7).all()
+    assert not dkv[:, 0].any() and not dkv[:, 2].any()
+
+
 def _uniform(n, m, Hq, Hkv, D, seed):
     """A batch whose scores are all 0 (every probability 1 / m) and whose rows are all alike."""
     b = Batch([(n, m)], Hq, Hkv, D, FP, causal=0, place="cache", seed=seed)

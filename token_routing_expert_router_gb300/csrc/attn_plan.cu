@@ -31,7 +31,8 @@ __device__ __forceinline__ int tile_steps(const AttnArgs& a, const PlanJob& j, c
 
 __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool report) {
   __shared__ int sKept[kFirst + 1];
-  __shared__ int sWarp[kSort / 32], sEnd[kSort / 32];
+  __shared__ int64_t sWarp[kSort / 32];
+  __shared__ int sEnd[kSort / 32];
   __shared__ unsigned long long sTotal;
   __shared__ int sMost, sSlots, sClass[kClasses];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -39,7 +40,8 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
   int* sFirst = a.B <= kFirst ? sKept : j.first;
   if (tid == 0) sTotal = 0, sMost = 0, sSlots = 0;
   if (tid < kClasses) sClass[tid] = 0;
-  int carry = 0, front = 0;  // tiles of the sequences before; where their keys end
+  int64_t carry = 0;  // tiles of the sequences before: with rows that overlap more than 32 bits count
+  int front = 0;      // where their keys end
   for (int b0 = 0; b0 < a.B; b0 += kSort) {
     const int b = b0 + tid;
     Seq s{};
@@ -53,26 +55,25 @@ __device__ void sort_tiles(const AttnArgs& a, const PlanJob& j, bool apart, bool
       front = max(front, l.all);
     }
     const int n = ((j.keys ? s.m : s.n) + rows - 1) / rows;
-    int inc = n;
+    int64_t inc = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, off);
+      const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
       if (lane >= off) inc += o;
     }
     __syncthreads();
     if (lane == 31) sWarp[warp] = inc;
     __syncthreads();
-    int before = carry + inc - n, all = 0;
+    int64_t before = carry + inc - n, all = 0;
     for (int w = 0; w < kSort / 32; ++w) {
       if (w < warp) before += sWarp[w];
       all += sWarp[w];
     }
-    if (b < a.B) sFirst[b] = lost ? before | kLost : before;
+    if (b < a.B) sFirst[b] = (int)min(before, (int64_t)j.most) | (lost ? kLost : 0);
     carry += all;
   }
-  if (tid == 0) sFirst[a.B] = carry;
   __syncthreads();
-  const int tiles = min(carry, j.most);  // more only where sequences share rows, which is reported
+  const int tiles = (int)min(carry, (int64_t)j.most);  // more only where sequences share rows, which is reported
   auto seq_of = [&](int t) {
     int lo = 0, hi = a.B - 1;  // the last sequence that begins at or before t
     while (lo < hi) {

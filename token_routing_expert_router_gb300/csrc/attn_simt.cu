@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const AttnArgs a
   float* sV = sK + tile_floats<DP>(R);
   float* sP = sV + tile_floats<DP>(R);
   const int h = blockIdx.y, hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  __shared__ int sFind[kFindWords<kThreads>];
+  __shared__ alignas(8) int sFind[kFindWords<kThreads>];
   const Tile t = find_tile<kThreads, false, false>(a, blockIdx.x, O, blockIdx.x == 0 && h == 0, sFind);
   if (t.b < 0) return;
   const Seq s = t.s;
@@ -243,7 +243,7 @@ __device__ __forceinline__ void dq_rows(const AttnArgs& a, int block, int h) {
   float* sM = sP + O * PS;  // kRounded: P, for the mean key
   constexpr bool kRounded = sizeof(T) == 2;
   const int hk = h / a.group, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  __shared__ int sFind[kFindWords<kThreads>];
+  __shared__ alignas(8) int sFind[kFindWords<kThreads>];
   const Tile t = find_tile<kThreads, false, true>(a, block, O, block == 0 && h == 0, sFind);
   if (t.b < 0) return;
   const Seq s = t.s;
@@ -314,7 +314,7 @@ __device__ __forceinline__ void dkv_rows(const AttnArgs& a, int block, int hk) {
   float* sS = sP + O * PS;
   __shared__ RowStat sStat[R];
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  __shared__ int sFind[kFindWords<kThreads>];
+  __shared__ alignas(8) int sFind[kFindWords<kThreads>];
   const Tile t = find_tile<kThreads, true, true>(a, block, O, block == 0 && hk == 0, sFind);
   if (t.b < 0) return;
   const Seq s = t.s;
