@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kThreads) few_join_kernel(const FewParams p, i
 template <int DP, bool WIDE>
 cudaError_t few(const FewParams& p, int row_tiles, cudaStream_t s) {
   constexpr size_t smem = ((R + 4 * K) * (DP + 4) + kWarps * kMine * R) * sizeof(float);
-  static const cudaError_t e = cudaFuncSetAttribute(few_kernel<DP, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static Once once;
+  const cudaError_t e = allow_smem(once, few_kernel<DP, WIDE>, smem);
   if (e != cudaSuccess) return e;
   few_kernel<DP, WIDE><<<dim3((unsigned)p.lines, (unsigned)p.splits), kThreads, smem, s>>>(p, row_tiles);
   return cudaGetLastError();

@@ -399,14 +399,11 @@ __global__ void __launch_bounds__(kThreads) delta_kernel(const AttnArgs a) {
   if (lane == 0) a.delta[(int64_t)h * a.Tq + row] = sum;
 }
 
-cudaError_t launch_tiles(void (*kern)(AttnArgs), cudaError_t attribute, dim3 grid, size_t smem, const AttnArgs& a, cudaStream_t s) {
-  if (attribute != cudaSuccess) return attribute;
+cudaError_t launch_tiles(Once& once, void (*kern)(AttnArgs), dim3 grid, size_t smem, const AttnArgs& a, cudaStream_t s) {
+  const cudaError_t e = allow_smem(once, kern, smem);
+  if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
-}
-template <typename K>
-cudaError_t allow(K* kern, size_t smem) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
 // Blocks of `rows` rows of the batch's tiles and heads, at most.
@@ -420,15 +417,15 @@ template <typename T, int DP, int N>
 cudaError_t forward_n(const AttnArgs& a, cudaStream_t s) {
   constexpr int O = 16 * N;
   constexpr size_t smem = (tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + O * PS) * sizeof(float);
-  static const cudaError_t e = allow(simt_forward_kernel<T, DP, N>, smem);
-  return launch_tiles(simt_forward_kernel<T, DP, N>, e, dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
+  static Once once;
+  return launch_tiles(once, simt_forward_kernel<T, DP, N>, dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
 }
 template <typename T, int DP, int N>
 cudaError_t dq_n(const AttnArgs& a, cudaStream_t s) {
   constexpr int O = 16 * N;
   constexpr size_t smem = (2 * tile_floats<DP>(O) + 2 * tile_floats<DP>(R) + (sizeof(T) == 2 ? 2 : 1) * O * PS) * sizeof(float);
-  static const cudaError_t e = allow(simt_dq_kernel<T, DP, N>, smem);
-  return launch_tiles(simt_dq_kernel<T, DP, N>, e, dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
+  static Once once;
+  return launch_tiles(once, simt_dq_kernel<T, DP, N>, dim3((unsigned)(a.Tq / O + a.B), a.Hq), smem, a, s);
 }
 template <int DP>
 constexpr size_t dkv_bytes(int O) {
@@ -437,12 +434,13 @@ constexpr size_t dkv_bytes(int O) {
 template <typename T, int DP, int N>
 cudaError_t dkv_n(const AttnArgs& a, cudaStream_t s) {
   constexpr int O = 16 * N;
-  static const cudaError_t e = allow(simt_dkv_kernel<T, DP, N>, dkv_bytes<DP>(O));
-  return launch_tiles(simt_dkv_kernel<T, DP, N>, e, dim3((unsigned)(a.Tk / O + a.B), a.Hkv), dkv_bytes<DP>(O), a, s);
+  static Once once;
+  return launch_tiles(once, simt_dkv_kernel<T, DP, N>, dim3((unsigned)(a.Tk / O + a.B), a.Hkv), dkv_bytes<DP>(O), a, s);
 }
 template <int DP>
 cudaError_t both(const AttnArgs& a, cudaStream_t s) {
-  static const cudaError_t e = allow(simt_both_kernel<DP>, dkv_bytes<DP>(16));  // more than dq's
+  static Once once;
+  const cudaError_t e = allow_smem(once, simt_both_kernel<DP>, dkv_bytes<DP>(16));  // more than dq's
   if (e != cudaSuccess) return e;
   const int key_tiles = a.Tk / 16 + a.B, query_tiles = a.Tq / 16 + a.B;
   return launch_after_smem(simt_both_kernel<DP>, dim3((unsigned)(key_tiles * a.Hkv + query_tiles * a.Hq)), kThreads, dkv_bytes<DP>(16),

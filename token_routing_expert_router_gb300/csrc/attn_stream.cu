@@ -538,8 +538,8 @@ cudaError_t forward(const AttnArgs& a, const StreamSpace& w, cudaStream_t s) {
   } else {
     k = v = q;  // no key is loaded
   }
-  static const cudaError_t e =
-      cudaFuncSetAttribute(attn_stream_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<DP>::kBytes);
+  static Once once;
+  const cudaError_t e = allow_smem(once, attn_stream_kernel<DP>, Ring<DP>::kBytes);
   if (e != cudaSuccess) return e;
   attn_stream_kernel<DP><<<stream_ctas(), kThreads, Ring<DP>::kBytes, s>>>(q, k, v, p);
   return cudaGetLastError();

@@ -397,8 +397,8 @@ cudaError_t forward(const AttnArgs& a, TilePlan* plan, int* first, int* queue, c
   } else {
     k = v = q;  // no key is loaded
   }
-  static const cudaError_t e =
-      cudaFuncSetAttribute(attn_forward_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fwd<DP>::kBytes);
+  static Once once;
+  const cudaError_t e = allow_smem(once, attn_forward_kernel<DP>, Fwd<DP>::kBytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)min((int64_t)tc::num_sms(), (int64_t)p.tiles * p.heads);
   // one sequence's tiles are in the order of their work as they are

@@ -518,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int DP, bool DKV>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o, const BwdParams& p,
                    cudaStream_t s) {
-  static const cudaError_t e = cudaFuncSetAttribute(attn_backward_kernel<DP, DKV>,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Bwd<DP>::kBytes);
+  static Once once;
+  const cudaError_t e = allow_smem(once, attn_backward_kernel<DP, DKV>, Bwd<DP>::kBytes);
   if (e != cudaSuccess) return e;
   if ((int64_t)p.tiles * p.heads >= (1ll << 31)) return cudaErrorInvalidConfiguration;
   return launch_after_smem(attn_backward_kernel<DP, DKV>, (unsigned)p.tiles * p.heads, kThreads, Bwd<DP>::kBytes, s, q, k, v, o, p);

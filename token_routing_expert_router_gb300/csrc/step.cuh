@@ -4,6 +4,7 @@
 #pragma once
 
 #include "moe_internal.cuh"
+#include "once.h"
 
 namespace moe {
 
@@ -43,6 +44,16 @@ cudaError_t launch_after_smem(void (*kern)(P...), dim3 grid, dim3 block, size_t 
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
   return launch_after_smem(kern, grid, block, 0, s, args...);
+}
+
+// A kernel's limit of dynamic shared memory, raised before its first launch.
+template <typename K>
+cudaError_t allow_smem(Once& once, K* kern, size_t smem) {
+  return once([&] {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) cudaGetLastError();  // told here, not by the next launch's check as well
+    return e;
+  });
 }
 
 // ---- block norms
