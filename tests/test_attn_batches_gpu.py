@@ -1,5 +1,5 @@
-"""Attention of batches with empty, refused and overlapping sequences, and of
-long sums in fp32."""
+"""Attention of batches with empty, refused and overlapping sequences, of very many sequences, of long
+sums in fp32, and of every call on the stream that it is given."""
 import pytest
 import torch
 
@@ -192,3 +192,15 @@ def test_long_sums_of_query_gradients_in_fp32(Hq, D):
     # the scale, the products and the result; what o is not quite 0 by falls out, as the keys' signs do
     rel = (64 + m / 64 + 64 + D + 8) * U
     within(dq[:n], want.expand(n, Hq, D), rel * want.abs())
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D", [(385, 4, 2, 64), (1000, 8, 4, 32), (3000, 2, 2, 128)])
+def test_single_tokens_of_very_many_requests(B, Hq, Hkv, D):
+    """More requests than a block has threads: several to a thread, those without keys or queries among them."""
+    lens = [(0 if i % 11 == 5 else 1, 0 if i % 7 == 3 else (37 * i) % 190 + (400 if i % 97 == 0 else 0)) for i in range(B)]
+    b = Batch(lens, Hq, Hkv, D, BF, place="cache", max_q=1, seed=B)
+    o, lse = b.forward()
+    b.check_forward(o, lse)
+    b.check_status()
+    o2, lse2 = b.forward()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
