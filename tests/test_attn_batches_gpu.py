@@ -204,3 +204,15 @@ def test_single_tokens_of_very_many_requests(B, Hq, Hkv, D):
     b.check_status()
     o2, lse2 = b.forward()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([(1, 900), (0, 4), (1, 33), (1, 0), (1, 2000)], 64, 1), ([(4, 500), (1, 70)], 32, 2),
+                                         ([(1, 700)], 49, 1)])
+def test_fp32_groups_beyond_tiles_of_few_rows(lens, Hq, Hkv, causal):
+    """More than 48 rows of a key head over a cache."""
+    b = Batch(lens, Hq, Hkv, 64, FP, causal=causal, place="cache", seed=Hq)
+    o, lse = b.forward()
+    b.check_forward(o, lse)
+    b.check_status()
+    b.check_backward(*b.backward(o, lse))
