@@ -216,3 +216,52 @@ def test_fp32_groups_beyond_tiles_of_few_rows(lens, Hq, Hkv, causal):
     b.check_forward(o, lse)
     b.check_status()
     b.check_backward(*b.backward(o, lse))
+
+
+@pytest.mark.parametrize("dt,D", [(BF, 64), (FP, 32)])
+def test_calls_run_on_the_stream_that_is_given(dt, D):
+    """Every call's input is made by work on a side stream that is still running when the call is given that
+    stream: on any other it would read what was there before."""
+    Hq, Hkv, T = 4, 2, 200
+    b = Batch([(T, T)], Hq, Hkv, D, dt, seed=6, tail=0)
+    o, lse = b.forward()
+    grads = b.backward(o, lse)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    rope = moe.MoERopeConfig.make(T=T, Hq=Hq, Hk=Hkv, D=D, act_dtype=moe.BF16 if dt == BF else moe.F32)
+    table = torch.empty(D // 2, dtype=torch.int64, device="cuda")
+    moe.moe_rope_table(moe.MoERopeFreq.make(rot=D), table)
+    turned, back = ([torch.empty_like(x) for x in (b.q, b.k)] for _ in range(2))
+    moe.moe_rope(rope, b.q, b.k, None, pos, None, table, *turned[:1], turned[1], None)
+    moe.moe_rope_backward(rope, b.q, b.k, pos, table, *back)
+    q, do = b.q.clone(), b.do.clone()
+    big = torch.randn(4096, 4096, device="cuda").to(BF)
+    sink = torch.empty_like(big)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.mm(big, big, out=sink)  # the library's first call on a stream is slow
+
+    def behind(target, value, call):
+        """call, with `target` turned into `value` by the side stream after some milliseconds of other work."""
+        target.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(150):
+                torch.mm(big, big, out=sink)
+            target.copy_(value)
+        assert not side.query()  # still at it
+        call()
+        side.synchronize()
+        torch.cuda.synchronize()
+
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    behind(b.q, q, lambda: moe.moe_attn(b.cfg, b.q, b.k, b.v, b.q_start, None, None, o2, lse2, b.ws, stream=side))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    got = [torch.empty_like(x) for x in grads]
+    behind(b.do, do, lambda: moe.moe_attn_backward(b.cfg, b.q, b.k, b.v, b.q_start, None, None, o, lse, b.do, *got, b.bws, stream=side))
+    assert all(torch.equal(x, y) for x, y in zip(grads, got))
+    got = [torch.empty_like(x) for x in turned]
+    behind(b.q, q, lambda: moe.moe_rope(rope, b.q, b.k, None, pos, None, table, *got, None, stream=side))
+    assert all(torch.equal(x, y) for x, y in zip(turned, got))
+    got = [torch.empty_like(x) for x in back]
+    behind(b.q, q, lambda: moe.moe_rope_backward(rope, b.q, b.k, pos, table, *got, stream=side))
+    assert all(torch.equal(x, y) for x, y in zip(back, got))
