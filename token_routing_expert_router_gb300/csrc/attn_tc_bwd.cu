@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (smem_addr(smem) & 1023) {  // the tiles' swizzle counts on it
-    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_TIMEOUT, -1);
+  if (smem_addr(smem) & 1023) {  // the tiles' swizzle counts on it; a launch without static shared memory has it so
+    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_CUDA, -1);
     return;
   }
   const int per = R / p.pack;  // queries of a tile
