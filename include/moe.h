@@ -534,7 +534,12 @@ moe_status_t moe_block_norm_backward(const moe_norm_config_t* cfg, const void* r
  * f_i = base^(-2 i / rot), i = 0 .. rot / 2 - 1, and for a context longer than the trained one
  *   MOE_ROPE_LINEAR: f_i / factor;
  *   MOE_ROPE_YARN: f_i k_i + f_i / factor (1 - k_i), k_i = (r_i - beta_slow) / (beta_fast - beta_slow)
- *     held to [0, 1], r_i = trained_len f_i / (2 pi) the whole turns within the trained length. */
+ *     held to [0, 1], r_i = trained_len f_i / (2 pi) the whole turns within the trained length.
+ * That is the paper's equation, linear in r. Model code often mixes linearly in the pair's index i
+ * instead, between the indices at which r is beta_fast (rounded down) and beta_slow (rounded up), and
+ * checkpoints trained with it need its frequencies: between the two indices they are others (rot 64,
+ * factor 40, trained_len 4096: 1.1 to 4.3 times). For these, as for any that are not listed here, the
+ * caller fills the table. */
 enum { MOE_ROPE_UNSCALED = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_YARN = 2 };
 typedef struct {
   int32_t rot;        /* rotated channels of a head: even */
@@ -546,7 +551,8 @@ typedef struct {
 } moe_rope_freq_t;
 
 /* table [rot / 2]: turns per position, in 64-bit fixed point (2^64 is one turn; whole turns per
- * position are dropped), so that an angle is exact modulo a turn at any position. Made once. */
+ * position are dropped), so that an angle is exact modulo a turn at any position. Made once; entries
+ * of the caller's own frequencies are 2^64 (f_i / (2 pi) mod 1), rounded. */
 moe_status_t moe_rope_table(const moe_rope_freq_t* freq, uint64_t* table, moe_stream_t stream);
 
 /* T tokens of Hq query and Hk key heads (either may be 0) of D <= 4096 channels, 2^22 of either in all. */

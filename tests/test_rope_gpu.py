@@ -190,3 +190,32 @@ def test_rope_by_differences():
         slope = up - (out.double() * g.double()).sum((1, 2))
         # linear: differences are exact but for the roundings of 2 x 10 products of size up to ~4 each
         assert (slope - dx[:, 0, c].double()).abs().max() < 40 * 8 * U * 4
+
+
+@pytest.mark.parametrize("rot,D,layout,dt", [(64, 192, moe.ROPE_INTERLEAVED, BF), (128, 128, moe.ROPE_HALF, FP)])
+def test_frequencies_of_the_callers_own(rot, D, layout, dt):
+    """A table that the caller fills: YaRN mixed linearly in the pair's index, which is not moe_rope_table's."""
+    base, L, factor, fast, slow = 10000.0, 4096, 40.0, 32.0, 1.0
+
+    def at(turns):
+        return rot * math.log(L / (2 * math.pi * turns)) / (2 * math.log(base))
+
+    lo, hi = max(0, math.floor(at(fast))), min(rot // 2 - 1, math.ceil(at(slow)))
+    ramp = [min(1.0, max(0.0, (i - lo) / (hi - lo))) for i in range(rot // 2)]
+    plain = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    f = [v * (1 - r) + v / factor * r for v, r in zip(plain, ramp)]
+    entries = [round(v / (2 * math.pi) % 1 * 2.0 ** 64) % 2 ** 64 for v in f]
+    table = torch.tensor([e - 2 ** 64 if e >= 2 ** 63 else e for e in entries], dtype=torch.int64, device="cuda")
+    freq = torch.tensor(f, dtype=torch.float64, device="cuda")
+    ratio = freq / frequencies(rot, **YARN)
+    assert ratio.max() > 4 and (ratio > 1.05).sum() > rot // 8  # other frequencies than the listed scaling's
+    T, m = 300, 0.1 * math.log(factor) + 1
+    q, k, v, ld = inputs(T, 4, 2, D, dt, True)
+    pos = (torch.arange(T, device="cuda") * 541).to(torch.int32)
+    cfg = moe.MoERopeConfig.make(T=T, Hq=4, Hk=2, D=D, rot=rot, first=D - rot, layout=layout, act_dtype=CODE[dt], magnitude=m,
+                                 ld_q=ld, ld_k=ld, ld_v=ld)
+    qo, ko = poisoned(T, 4, D, dtype=dt), poisoned(T, 2, D, dtype=dt)
+    moe.moe_rope(cfg, q, k, None, pos, None, table, qo, ko, None)
+    for got, x in ((qo, q), (ko, k)):
+        want, bound = turned(x, pos, freq, D - rot, layout, m, 1.0)
+        within(got, want, bound)

@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, HEADS == 4 ? 7 : HEADS == 3 ? 8 : 12
 
 // Turns per position of every pair. YaRN (Peng et al. 2023): with r = trained_len f / 2 pi whole
 // turns within the trained length, f is kept from r = beta_fast on, divided by the factor up to
-// r = beta_slow, and mixed linearly between.
+// r = beta_slow, and mixed linearly in r between (much model code mixes linearly in the pair's index
+// instead: its callers fill the table).
 __global__ void rope_table_kernel(const moe_rope_freq_t c, uint64_t* table) {
   for (int i = threadIdx.x; i < c.rot / 2; i += blockDim.x) {
     const double turns = pow(c.base, -2.0 * i / c.rot) / 6.283185307179586476925;
