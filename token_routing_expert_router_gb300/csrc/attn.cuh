@@ -176,7 +176,7 @@ struct StreamSpace {
 bool stream_rule(const AttnArgs& a);
 cudaError_t launch_stream(const AttnArgs& a, const StreamSpace& w, cudaStream_t s);
 // Few rows over many keys, fp32: parts of lines, a line being 16 rows of a sequence and key head.
-constexpr int kFewParts = 304, kMostSplits = 64;  // parts wanted of all lines, two for every SM; of one, at most
+constexpr int kFewParts = 304, kMostSplits = 64;  // parts wanted of all lines, two for every SM (in turn, at 128 channels); of one, at most
 constexpr int kMostFewParts = 2 * kFewParts;      // where lines are cut at all
 bool few_rule(const AttnArgs& a);
 cudaError_t launch_few(const AttnArgs& a, float2* stat, float* part, cudaStream_t s);

@@ -1,14 +1,14 @@
 // Attention of few query rows over many keys in fp32: 16 (query, head) rows of a key head at a time, so
-// that a cache is read once for all heads of a group, and the keys of a line cut into as many parts as
-// give every SM two.
+// that a cache is read once for all heads of a group, and the keys of a line cut into some 300 parts in all, two
+// for every SM: side by side up to 64 channels, one after the other at 128 (148 KB of shared memory a block).
 //
 // A block of 8 warps takes tiles of 64 keys, which come by asynchronous copies into two buffers while the
 // tile before is used. Of a tile a warp has 8 keys, and its own running maximum, sum and output for all 16
 // rows: a lane forms the scores of 4 rows and one key, then adds DP / 32 channels of all rows. Warps meet
 // only at the copies and at the end, where their results, and later the parts', are put together in
-// order. 16 requests of 4096 keys (32 query and 8 key heads of 128, 537 MB): 248 us, 2.2 TB/s. A tile of
-// 64 KB has 2100 cycles of FMA issue and would come in 2800; with 8 warps of 170 registers on an SM, what it
-// takes are their latencies.
+// order. 16 requests of 4096 keys (32 query and 8 key heads of 128, 537 MB): 249 us, 2.2 TB/s. Not memory (a third of
+// its rate), but what 8 warps of 170 registers on an SM can do: shared memory's pipe is at 58 %, issue at 51 %,
+// FMA at 34 %, and the warps wait for shared memory most of all (counted); 384 blocks are 2.5 rounds.
 #include "attn.cuh"
 #include "tc_common.cuh"
 
@@ -260,7 +260,9 @@ cudaError_t few(const FewParams& p, int row_tiles, cudaStream_t s) {
 
 }  // namespace
 
-// Rows of a sequence and key head that are worth tiles of 16: beyond them tiles of 64 use a key tile four times as long.
+// Rows of a sequence and key head that are taken 16 at a time, the keys read once for each 16; beyond them attn_simt.cu's
+// tiles of a head's rows, which suit prompts. The edge is for these: single tokens of a group beyond 48 lose
+// by it (one query of 64 heads over 4096 keys, a key head of 128: 543 us, of 32 heads 77).
 bool few_rule(const AttnArgs& a) {
   return (int64_t)a.max_q * a.group <= 3 * R && (int64_t)a.B * a.Hkv * 3 < (1ll << 31);
 }

@@ -7,10 +7,12 @@
 //
 // A block of 256 threads owns 64 query rows (dk, dv: 64 key rows), or 16 of a small batch, and goes over the
 // other side in tiles of 64, with the running maximum and sum of the softmax; scores are never stored. Every
-// thread forms 4 x 4 (1 x 4) scores, and 4 rows (1) x DP / 16 columns of the results in registers. Bound by FMA issue
-// (16384 tokens, 8 query and 2 key heads of 128, causal: 14.6 ms, 38 TFLOP/s): two 64 x 64 x D products a tile forward,
-// five backward (in two kernels, which form the scores and do . v once more each; in return no result is
-// added to by two blocks, so the bits never change). From bf16 tensors delta carries the rounding of o:
+// thread forms 4 x 4 (1 x 4) scores, and 4 rows (1) x DP / 16 columns of the results in registers. Two 64 x 64 x D products a
+// tile forward; backward three for dq and four for dk and dv (both kernels form the scores and do . v; in return no
+// result is added to by two blocks, so the bits never change). What bounds it: operands from shared memory, read at 68 to
+// 75 % of that pipe's rate beside FMA units busy 50 to 55 % of the time, with one block of 8 warps an SM to hide the
+// latencies of both (counted at 4096 tokens of 8 / 2 heads of 128). 16384 such tokens, causal: forward 14.8 ms,
+// 37 TFLOP/s, backward 50.0 ms, 38 TFLOP/s of its seven products. From bf16 tensors delta carries the rounding of o:
 // their dq forms the mean key too and puts both right, as in attn_tc_bwd.cu.
 #include "attn.cuh"
 

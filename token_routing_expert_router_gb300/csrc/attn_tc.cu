@@ -11,7 +11,8 @@
 // tile's softmax runs, the tensor cores work on the other tile's products; S is free for the next scores
 // as soon as P V has been issued behind them, since one thread's products run in their order.
 //
-// The running maximum is only followed when it grows by more than 2^8 in the exponentials (then O is
+// The online softmax is Milakov and Gimelshein's (2018); following the maximum past a threshold only is a
+// published refinement of it. The running maximum is only followed when it grows by more than 2^8 in the exponentials (then O is
 // read, scaled and written back, by the rows' own threads); until then the old one is as good a
 // reference, since all sums are fp32 and P's rounding is relative. The keys are taken from the last to
 // the first, so that the tile with the mask comes first. Key rows behind the sequence's end belong to
@@ -23,9 +24,10 @@
 // written: a short sequence's tile is little more than such ends (40 prompts of 225 tokens: 51 us with a
 // CTA for every item).
 //
-// Bound by the tensor cores and what feeds them: scores read 128 bytes of shared memory a cycle, all there
-// is, and the next keys are written beside. 16384 tokens, 32 query and 8 key heads of 128, causal: 1.65 ms,
-// 1.33 PFLOP/s (69 % of the measured peak).
+// Bound by the tensor cores and what feeds them. A step's products read shared memory in 1536 wavefronts of 128 bytes
+// (counted), 1024 of them in the scores' products, which take as many cycles: all there is meanwhile, and the
+// next keys are written beside. The rest of a step is the chain from scores to P. 16384 tokens, 32 query
+// and 8 key heads of 128, causal: 1.66 ms, 1.32 PFLOP/s (69 % of the measured peak).
 #include "attn_plan.cuh"
 #include "attn_tc.cuh"
 

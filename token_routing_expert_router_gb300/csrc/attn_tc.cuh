@@ -178,7 +178,9 @@ struct Running {
   bool far = false;  // some row of the warp has a maximum beyond 2^24 (base 2)
 };
 
-// One tile of scores at my_s (this thread's lane) becomes P; columns from `end` on are not seen (the
+// One tile of scores at my_s (this thread's lane) becomes P. P is rounded to bf16 (2^-8 of it at most): the tensor
+// cores take both operands of a product in one type, and V is bf16; the sums are of the exponentials before it. By norm
+// o is off by 0.19 to 0.24 %, where its own rounding alone makes 0.17. Columns from `end` on are not seen (the
 // whole warp gives BK where every row sees every column). O at my_o is scaled, where it holds anything
 // (`begun`) and a row's maximum has grown by more than 2^8.
 template <int DP>

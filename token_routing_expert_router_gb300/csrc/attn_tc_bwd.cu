@@ -8,6 +8,10 @@
 // are. Sums over the query heads of a group and over all queries stay in one accumulator: no atomics,
 // and the bits never change. In return S and dP are formed twice.
 //
+// P and dS are rounded to bf16 (2^-8 of each at most): the tensor cores take both operands of a product in one
+// type. The sums of dS are of the unrounded ones. By norm gradients are off by 0.24 %, where their own rounding
+// alone makes 0.17.
+//
 // M serves delta. It is the sum over the keys of P dP, and formed as d_o . o it carries the rounding of o
 // to bf16 and of P in the forward: where a row looks at few keys, dP - delta is small against both, and
 // gradients were off by up to 0.4 % for that alone (their own rounding: 0.17 %). The sum e of a row's dS
